@@ -74,6 +74,7 @@ extern "C" {
 #define KDA_ERR_CUDA (-4)
 #define KDA_ERR_TIMEOUT (-5)
 #define KDA_ERR_SCRATCH (-6)
+#define KDA_ERR_SLOTS (-7) /* the free list has no slot left (kda_slot_plan) */
 
 #define KDA_STATE_F32 0
 #define KDA_STATE_BF16 1
@@ -81,6 +82,7 @@ extern "C" {
 #define KDA_HEAD_DIM 128
 #define KDA_MAX_WINDOW 8
 #define KDA_MAX_LAYERS 64
+#define KDA_PROMPT_MAX_HEADS 1024 /* heads of the prompt operators */
 
 typedef uint16_t kda_bf16;
 
@@ -461,6 +463,156 @@ int kda_layer_step_noalloc(const kda_bf16 *x, const kda_bf16 *conv_weight,
                            const float *norm_weight, float eps, kda_bf16 *out,
                            int B, int H, int Q, int null_slot, int32_t *status,
                            void *stream);
+
+/* ------------------------------------------------------------------------
+ * Prompts and plain decoding.  The calls above verify windows of at most 8
+ * draft tokens from a checkpoint; the calls below bring a prompt of any
+ * length into that checkpoint, decode from it without speculation, and make
+ * the slot maps of both from the requests' lengths:
+ *
+ *   kda_slot_plan -> kda_prefill_conv -> kda_prefill -> the verify calls, or
+ *   kda_recurrent.
+ *
+ * Conventions that the four share, beside those at the top of this file:
+ *  - Request b's tokens are query_start_loc[b] .. query_start_loc[b + 1] - 1
+ *    of the packed activations (b*Q .. b*Q + Q - 1 when query_start_loc is
+ *    NULL), their number n_b <= Q; Q is any size from 1 on.  query_start_loc
+ *    does not decrease.  A window outside 0 .. n_tokens or longer than Q is
+ *    reported as KDA_ERR_ARG in the status word and nothing of that request
+ *    is read or written.  Rows of the activations that belong to no request
+ *    are not touched.
+ *  - sources[b] is the slot that request b's state is read from, a fresh
+ *    start (zeros) when <= null_slot; destinations[b] the slot that its
+ *    state is left in.  A request whose destination is <= null_slot is
+ *    inert: zeros go to its rows of `out`, and nothing else is written.  A
+ *    request with no tokens is not read or written at all.  null_slot >= -1.
+ *  - boundaries and boundary_lens ([B] int32, or both NULL) are kda_commit's:
+ *    with m = min(boundary_lens[b], n_b) > 0 and boundaries[b] > null_slot,
+ *    the state after m tokens is left in slot boundaries[b] as well.
+ *  - Destinations and boundary slots of the live requests are pairwise
+ *    distinct.  A source may be shared by any number of requests as long as
+ *    none of them writes it; a request may write its own source, as its
+ *    destination (in place) or as its boundary slot.
+ *  - A source, destination or boundary slot >= n_slots is reported as
+ *    KDA_ERR_ARG and its request left out.
+ *  - 1 <= H <= KDA_PROMPT_MAX_HEADS, and n_tokens * H and B * H fit 31 bits
+ *    (KDA_ERR_ARG otherwise); -10 <= lower_bound <= 0, q_scale finite: the
+ *    decays of a long prompt multiply, and must not exceed 1
+ *    (KDA_ERR_UNSUPPORTED otherwise).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kda_slot_plan -- the align mode's bookkeeping on the device: offsets of
+ * the packed activations, block table entries and slot maps, from the
+ * requests' lengths.  State blocks hold block_size tokens, and the state
+ * after p > 0 tokens of request b is held in slot
+ * block_table[b][(p - 1) / block_size]; at a block's last token that state
+ * stays, as the prefix that other requests can go on from.  With
+ * c = computed_lens[b] tokens behind it, n = new_lens[b] > 0 to come,
+ * e = c + n, cur = (c - 1) / block_size (none when c == 0) and
+ * last = (e - 1) / block_size, per request in order:
+ *   sources[b]      = c > 0 ? block_table[b][cur] : null_slot;
+ *   m               = last * block_size - c: tokens up to the last block
+ *                     boundary before the end;
+ *   m > 0:  if last - 1 != cur, block_table[b][last - 1] takes the next slot
+ *           of the free list; boundaries[b] = block_table[b][last - 1],
+ *           boundary_lens[b] = m; entries cur + 1 .. last - 2, whose states
+ *           nothing will hold, become null_slot;
+ *   m <= 0: boundaries[b] = null_slot, boundary_lens[b] = 0;
+ *   if last != cur, block_table[b][last] takes the next slot of the free
+ *   list; destinations[b] = block_table[b][last].
+ * query_start_loc[b] = sum of max(new_lens[0 .. b - 1], 0), [B + 1].
+ * free_slots [n_free] int32 is a list of slots, the first *free_head of them
+ * taken; *free_next becomes the number taken after this call (the two may be
+ * one word).  The maps are what kda_prefill, kda_prefill_conv and
+ * kda_recurrent take, and kda_commit (new_lens then being the accepted
+ * counts).
+ * A request with n == 0 gets null slots and length 0, and its row is left
+ * alone.  So does one that is reported: negative lengths, e beyond
+ * max_blocks * block_size or 31 bits, or a block_table[b][cur] <= null_slot
+ * (KDA_ERR_ARG); or no free slot left for it (KDA_ERR_SLOTS; the requests
+ * behind it that need a slot are left out too, and nothing is taken for
+ * them).  Its tokens still count in query_start_loc, so that the packed
+ * activations keep their places.  A *free_head outside 0 .. n_free
+ * (KDA_ERR_ARG) leaves no slot to any request.  A total beyond 31 bits is
+ * reported (KDA_ERR_ARG) and cut off there.
+ *   computed_lens, new_lens [B] int32; block_table [B, max_blocks] int32,
+ *   rows table_row_stride >= max_blocks elements apart; sources,
+ *   destinations, boundaries, boundary_lens [B], query_start_loc [B + 1]
+ *   int32 outputs.  B == 0 writes query_start_loc[0] and *free_next.
+ */
+int kda_slot_plan(const int32_t *computed_lens, const int32_t *new_lens, int32_t *block_table,
+                  int64_t table_row_stride, int max_blocks, const int32_t *free_slots,
+                  int n_free, const int32_t *free_head, int32_t *free_next,
+                  int32_t *query_start_loc, int32_t *sources, int32_t *destinations,
+                  int32_t *boundaries, int32_t *boundary_lens, int B, int block_size,
+                  int null_slot, int32_t *status, void *stream);
+
+/*
+ * kda_prefill_conv -- kda_layer_prologue's convolution and SiLU over prompts:
+ *   s = [W_0, W_1, W_2, x_0 .. x_{n-1}] per channel ch, W = conv_state[
+ *       sources[b], ch] (zeros for a fresh start);
+ *   out_t = BF16(silu(bias[ch] + sum_{i<4} conv_weight[part, i, h*128 + c] *
+ *           s[t + i])) to q / k / v;
+ *   the last three entries of s become entries 0 .. 2 of the destination's
+ *   window (its other entries are kept), and the last three after m tokens
+ *   those of the boundary slot's.
+ * The window is the one kda_layer_prologue and kda_layer_step go on from
+ * when no replay is pending.  Inert requests are skipped (nothing read or
+ * written).
+ *   x [n_tokens, 3*D], conv_weight [3, 4, D], conv_bias [3*D] or NULL BF16;
+ *   conv_state [n_slots, 3*D, conv_width] BF16, 3 <= conv_width <= 10
+ *   (rq + 2 of the layer calls), slot stride a multiple of 8 elements;
+ *   q, k, v [n_tokens, H, 128] BF16.  16-byte aligned.
+ */
+int kda_prefill_conv(const kda_bf16 *x, const kda_bf16 *conv_weight, const kda_bf16 *conv_bias,
+                     kda_bf16 *conv_state, int64_t conv_slot_stride, int conv_width,
+                     int n_slots, const int32_t *sources, const int32_t *destinations,
+                     const int32_t *boundaries, const int32_t *boundary_lens,
+                     const int32_t *query_start_loc, int n_tokens, kda_bf16 *q, kda_bf16 *k,
+                     kda_bf16 *v, int B, int H, int Q, int null_slot, int32_t *status,
+                     void *stream);
+
+/*
+ * kda_prefill -- the gated delta rule over prompts, in chunks.  Per (request
+ * b, head h), from S = the source's state, for t < n_b, in exact arithmetic:
+ *   S <- S diag(d_t); u_t = sigmoid(raw_beta_t) (v_t - S kn_t);
+ *   S <- S + u_t kn_t^T; out_t = BF16(S qn_t)
+ * with d_t, kn_t and qn_t as in kda_verify; the state after the last token
+ * goes to the destination (rounded once to the pool's type).
+ *   q, k, v, raw_g, out [n_tokens, H, 128], raw_beta [n_tokens, H] BF16;
+ *   A_log [H], dt_bias [H, 128] FP32; state_pool [n_slots, H, 128, 128] of
+ *   state_dtype, slot stride `slot_stride` elements (>= H*128*128).
+ *   workspace  device, 16-byte aligned, at least kda_prefill_workspace_bytes(
+ *              n_tokens, B, H) bytes, owned by the caller and not used by
+ *              other work at the same time; may be NULL when that is 0.
+ *              Nothing in it outlives the call's kernels.
+ * All pointers but raw_beta, A_log and the index arrays 16-byte aligned.
+ */
+int64_t kda_prefill_workspace_bytes(int n_tokens, int B, int H);
+int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const kda_bf16 *raw_g,
+                const kda_bf16 *raw_beta, const float *A_log, const float *dt_bias,
+                float lower_bound, float q_scale, void *state_pool, int state_dtype,
+                int64_t slot_stride, int n_slots, const int32_t *sources,
+                const int32_t *destinations, const int32_t *boundaries,
+                const int32_t *boundary_lens, const int32_t *query_start_loc, int n_tokens,
+                kda_bf16 *out, void *workspace, int64_t workspace_bytes, int B, int H, int Q,
+                int null_slot, int32_t *status, void *stream);
+
+/*
+ * kda_recurrent -- the same rule token by token, for decoding (one token per
+ * request, or a few): the state is read once, advanced over the window in
+ * registers, and written once.  Arguments and results as kda_prefill's,
+ * without a workspace.
+ */
+int kda_recurrent(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const kda_bf16 *raw_g,
+                  const kda_bf16 *raw_beta, const float *A_log, const float *dt_bias,
+                  float lower_bound, float q_scale, void *state_pool, int state_dtype,
+                  int64_t slot_stride, int n_slots, const int32_t *sources,
+                  const int32_t *destinations, const int32_t *boundaries,
+                  const int32_t *boundary_lens, const int32_t *query_start_loc, int n_tokens,
+                  kda_bf16 *out, int B, int H, int Q, int null_slot, int32_t *status,
+                  void *stream);
 
 #ifdef __cplusplus
 }

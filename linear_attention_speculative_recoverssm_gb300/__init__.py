@@ -13,6 +13,7 @@ from ._lib import (  # noqa: F401
     KDA_ERR_ARG,
     KDA_ERR_CUDA,
     KDA_ERR_SCRATCH,
+    KDA_ERR_SLOTS,
     KDA_ERR_TIMEOUT,
     KDA_ERR_UNSUPPORTED,
     KDA_LAYER_STEP_NOALLOC_MAX_BYTES,
@@ -29,9 +30,14 @@ from ._lib import (  # noqa: F401
     kda_layer_step,
     kda_layer_step_noalloc,
     kda_layer_step_workspace_bytes,
+    kda_prefill,
+    kda_prefill_conv,
+    kda_prefill_workspace_bytes,
+    kda_recurrent,
     kda_replay_verify,
     kda_replay_verify_layers,
     kda_selftest_wait_timeout,
+    kda_slot_plan,
     kda_verify,
     layer_tables,
     load,

@@ -22,6 +22,7 @@ KDA_ERR_UNSUPPORTED = -3
 KDA_ERR_CUDA = -4
 KDA_ERR_TIMEOUT = -5
 KDA_ERR_SCRATCH = -6
+KDA_ERR_SLOTS = -7
 KDA_LAYER_STEP_NOALLOC_MAX_BYTES = 16 * 1024 * 1024
 KDA_STATE_F32 = 0
 KDA_STATE_BF16 = 1
@@ -30,7 +31,8 @@ EXPORTS = ("kda_abi_version", "kda_error_string", "kda_check_status", "kda_verif
            "kda_replay_verify", "kda_replay_verify_layers",
            "kda_commit", "kda_defer_commit", "kda_flush_plan", "kda_selftest_wait_timeout",
            "kda_layer_prologue", "kda_layer_epilogue", "kda_layer_step_workspace_bytes",
-           "kda_layer_step", "kda_layer_step_noalloc")
+           "kda_layer_step", "kda_layer_step_noalloc", "kda_slot_plan", "kda_prefill_conv",
+           "kda_prefill_workspace_bytes", "kda_prefill", "kda_recurrent")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -62,6 +64,14 @@ _SIGS = {
     "kda_layer_step": ([_P] * 4 + [_I64] + [_P] * 5 + [_F, _F, _P, _I64, _I, _P, _P, _P, _P, _P,
                                                    _I64, _I64, _I, _I, _P, _P, _F, _P, _P, _I64,
                                                    _I, _I, _I, _I, _P, _P], _I),
+    "kda_slot_plan": ([_P] * 3 + [_I64, _I, _P, _I] + [_P] * 7 + [_I, _I, _I, _P, _P], _I),
+    "kda_prefill_conv": ([_P] * 4 + [_I64, _I, _I] + [_P] * 5 + [_I] + [_P] * 3
+                         + [_I, _I, _I, _I, _P, _P], _I),
+    "kda_prefill_workspace_bytes": ([_I, _I, _I], _I64),
+    "kda_prefill": ([_P] * 7 + [_F, _F, _P, _I, _I64, _I] + [_P] * 5 + [_I, _P, _P, _I64]
+                    + [_I, _I, _I, _I, _P, _P], _I),
+    "kda_recurrent": ([_P] * 7 + [_F, _F, _P, _I, _I64, _I] + [_P] * 5 + [_I, _P]
+                      + [_I, _I, _I, _I, _P, _P], _I),
 }
 
 _lib = None
@@ -391,3 +401,232 @@ def kda_layer_step_noalloc(x, conv_weight, conv_bias, conv_state, f_a, f_b, raw_
         key_gate.stride(0), corr.shape[0], rq, _ptr(gate), _ptr(norm_weight), eps, _ptr(out),
         B, H, Q, null_slot, _ptr(status), _stream(stream))
     return _check("kda_layer_step_noalloc", rc, raise_on_error)
+
+
+# ---------------------------------------------------------------------------
+# prompts and plain decoding
+# ---------------------------------------------------------------------------
+
+def _expect_tensors(device, *specs):
+    """The prompt operators' tensors, (name, tensor or None, type, shape) each:
+    their types, shapes and layouts (contiguous), and that all are on
+    `device`, a GPU."""
+    for name, t, dtype, shape in specs:
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, got {device}")
+    for name, t, _, _ in specs:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _expect_rows(device, name, t, dtype, inner):
+    """A pool or table: rows of shape `inner` (None: any size), each
+    contiguous, any stride from one to the next."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(inner) + 1 or any(w is not None and w != n
+                                        for w, n in zip(inner, t.shape[1:])):
+        raise ValueError(f"{name} must have shape {('any', *inner)}, got {tuple(t.shape)}")
+    want = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != want:
+            raise ValueError(f"{name} must be contiguous but for the stride of its rows")
+        want *= n
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+class _on:
+    """A call's stream, with the device of its tensors the current one: the
+    caller's own when that is so already."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = None
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.given = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.given)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _row_stride(t, minimum):
+    """Elements from one slot to the next (the pool of a single slot may have
+    any stride there: nothing uses it)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), minimum)
+
+
+def kda_slot_plan(computed_lens, new_lens, block_table, free_slots, free_head, free_next,
+                  query_start_loc, sources, destinations, boundaries, boundary_lens, *,
+                  block_size, null_slot=0, status=None, stream=None, raise_on_error=True):
+    """Packed offsets, block table entries and slot maps from the requests'
+    lengths (the rules are in include/kda_recoverssm.h).  In: computed_lens,
+    new_lens [B], block_table [B, max_blocks] (rows of any stride; extended in
+    place), free_slots [n], free_head [1].  Out: free_next [1] (may be
+    free_head), query_start_loc [B + 1], sources, destinations, boundaries,
+    boundary_lens [B].  All int32."""
+    import torch
+    i32, dev = torch.int32, computed_lens.device
+    B = computed_lens.shape[0]
+    one, per = (1,), (B,)
+    _expect_tensors(dev, ("computed_lens", computed_lens, i32, per), ("new_lens", new_lens, i32, per),
+                    ("free_slots", free_slots, i32, (free_slots.numel(),)),
+                    ("free_head", free_head, i32, one), ("free_next", free_next, i32, one),
+                    ("query_start_loc", query_start_loc, i32, (B + 1,)),
+                    ("sources", sources, i32, per), ("destinations", destinations, i32, per),
+                    ("boundaries", boundaries, i32, per),
+                    ("boundary_lens", boundary_lens, i32, per), ("status", status, i32, one))
+    _expect_rows(dev, "block_table", block_table, i32, (None,))
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
+    with _on(dev, stream) as st:
+        rc = load().kda_slot_plan(
+            computed_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+            _row_stride(block_table, block_table.shape[1]), block_table.shape[1],
+            free_slots.data_ptr(), free_slots.shape[0], free_head.data_ptr(),
+            free_next.data_ptr(), query_start_loc.data_ptr(), sources.data_ptr(),
+            destinations.data_ptr(), boundaries.data_ptr(), boundary_lens.data_ptr(), B,
+            block_size, null_slot, _address(status), st)
+    return _check("kda_slot_plan", rc, raise_on_error)
+
+
+def kda_prefill_conv(x, conv_weight, conv_bias, conv_state, sources, destinations,
+                     query_start_loc, q, k, v, *, Q, boundaries=None, boundary_lens=None,
+                     null_slot=0, status=None, stream=None, raise_on_error=True):
+    """The layer's convolution + SiLU over ragged prompts: x [T, 3*H*128] to
+    q, k, v [T, H, 128], the windows of conv_state [slots, 3*H*128, width]
+    read at ``sources`` and left at ``destinations`` (and after boundary_lens
+    tokens at ``boundaries``).  Q: at least the longest window;
+    query_start_loc None: windows of Q tokens."""
+    import torch
+    bf, i32, dev = torch.bfloat16, torch.int32, x.device
+    T, H, _ = q.shape
+    D, B = H * 128, sources.shape[0]
+    per, heads = (B,), (T, H, 128)
+    _expect_tensors(dev, ("x", x, bf, (T, 3 * D)), ("conv_weight", conv_weight, bf, (3, 4, D)),
+                    ("conv_bias", conv_bias, bf, (3 * D,)), ("q", q, bf, heads),
+                    ("k", k, bf, heads), ("v", v, bf, heads), ("sources", sources, i32, per),
+                    ("destinations", destinations, i32, per),
+                    ("boundaries", boundaries, i32, per),
+                    ("boundary_lens", boundary_lens, i32, per),
+                    ("query_start_loc", query_start_loc, i32, (B + 1,)),
+                    ("status", status, i32, (1,)))
+    _expect_rows(dev, "conv_state", conv_state, bf, (3 * D, None))
+    with _on(dev, stream) as st:
+        rc = load().kda_prefill_conv(
+            x.data_ptr(), conv_weight.data_ptr(), _address(conv_bias), conv_state.data_ptr(),
+            _row_stride(conv_state, 3 * D * conv_state.shape[2]), conv_state.shape[2],
+            conv_state.shape[0], sources.data_ptr(), destinations.data_ptr(),
+            _address(boundaries), _address(boundary_lens), _address(query_start_loc), T,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, Q, null_slot, _address(status), st)
+    return _check("kda_prefill_conv", rc, raise_on_error)
+
+
+def _rule_args(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources, destinations,
+               query_start_loc, out, boundaries, boundary_lens, status):
+    """Checks of kda_prefill's and kda_recurrent's tensors; the pool's type
+    and stride."""
+    import torch
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, q.device
+    T, H, _ = q.shape
+    B = sources.shape[0]
+    per, heads = (B,), (T, H, 128)
+    if state_pool.dtype != f32 and state_pool.dtype != bf:
+        raise TypeError("state_pool must be float32 or bfloat16")
+    _expect_tensors(dev, ("q", q, bf, heads), ("k", k, bf, heads), ("v", v, bf, heads),
+                    ("raw_g", raw_g, bf, heads), ("out", out, bf, heads),
+                    ("raw_beta", raw_beta, bf, (T, H)), ("A_log", A_log, f32, (H,)),
+                    ("dt_bias", dt_bias, f32, (H, 128)), ("sources", sources, i32, per),
+                    ("destinations", destinations, i32, per),
+                    ("boundaries", boundaries, i32, per),
+                    ("boundary_lens", boundary_lens, i32, per),
+                    ("query_start_loc", query_start_loc, i32, (B + 1,)),
+                    ("status", status, i32, (1,)))
+    _expect_rows(dev, "state_pool", state_pool, state_pool.dtype, (H, 128, 128))
+    return (KDA_STATE_F32 if state_pool.dtype == f32 else KDA_STATE_BF16,
+            _row_stride(state_pool, H * 128 * 128))
+
+
+def kda_prefill_workspace_bytes(n_tokens, B, H):
+    """Bytes of workspace kda_prefill needs for n_tokens packed tokens of B
+    requests."""
+    return load().kda_prefill_workspace_bytes(n_tokens, B, H)
+
+
+def kda_prefill(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources, destinations,
+                query_start_loc, out, *, Q, lower_bound, q_scale, boundaries=None,
+                boundary_lens=None, workspace=None, null_slot=0, status=None, stream=None,
+                raise_on_error=True):
+    """The gated delta rule over ragged prompts, in chunks: q, k, v, raw_g,
+    out [T, H, 128], raw_beta [T, H] BF16; the states of state_pool
+    [slots, H, 128, 128] (float32 or bfloat16) read at ``sources`` (a fresh
+    start at null_slot) and left at ``destinations`` (and after boundary_lens
+    tokens at ``boundaries``).  Q: at least the longest window;
+    query_start_loc None: windows of Q tokens.  ``workspace``: a device
+    tensor of kda_prefill_workspace_bytes(T, B, H) bytes that nothing else
+    uses meanwhile; None takes it from torch's allocator for this call."""
+    import torch
+    dtype, slot_stride = _rule_args(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources,
+                                    destinations, query_start_loc, out, boundaries,
+                                    boundary_lens, status)
+    T, H, _ = q.shape
+    B = sources.shape[0]
+    if workspace is not None and (not workspace.is_contiguous() or workspace.device != q.device):
+        raise ValueError("workspace must be a contiguous tensor on the operands' device")
+    with _on(q.device, stream) as st:
+        if workspace is None:
+            need = max(0, kda_prefill_workspace_bytes(T, B, H))
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            else:
+                # of the call's own stream: the allocator hands it on there
+                with torch.cuda.stream(torch.cuda.ExternalStream(st.value or 0)):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        nbytes = workspace.numel() * workspace.element_size()
+        rc = load().kda_prefill(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), raw_g.data_ptr(), raw_beta.data_ptr(),
+            A_log.data_ptr(), dt_bias.data_ptr(), lower_bound, q_scale, state_pool.data_ptr(),
+            dtype, slot_stride, state_pool.shape[0], sources.data_ptr(), destinations.data_ptr(),
+            _address(boundaries), _address(boundary_lens), _address(query_start_loc), T,
+            out.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes, B, H, Q, null_slot,
+            _address(status), st)
+    return _check("kda_prefill", rc, raise_on_error)
+
+
+def kda_recurrent(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources, destinations,
+                  out, *, Q, lower_bound, q_scale, query_start_loc=None, boundaries=None,
+                  boundary_lens=None, null_slot=0, status=None, stream=None,
+                  raise_on_error=True):
+    """The gated delta rule token by token, for decoding: arguments as
+    kda_prefill's; query_start_loc None: windows of Q tokens."""
+    dtype, slot_stride = _rule_args(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources,
+                                    destinations, query_start_loc, out, boundaries,
+                                    boundary_lens, status)
+    T, H, _ = q.shape
+    with _on(q.device, stream) as st:
+        rc = load().kda_recurrent(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), raw_g.data_ptr(), raw_beta.data_ptr(),
+            A_log.data_ptr(), dt_bias.data_ptr(), lower_bound, q_scale, state_pool.data_ptr(),
+            dtype, slot_stride, state_pool.shape[0], sources.data_ptr(), destinations.data_ptr(),
+            _address(boundaries), _address(boundary_lens), _address(query_start_loc), T,
+            out.data_ptr(), sources.shape[0], H, Q, null_slot, _address(status), st)
+    return _check("kda_recurrent", rc, raise_on_error)

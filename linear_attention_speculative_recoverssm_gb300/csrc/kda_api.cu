@@ -210,6 +210,7 @@ const char *kda_error_string(int status) {
     case KDA_ERR_CUDA: return "CUDA launch failed";
     case KDA_ERR_TIMEOUT: return "device wait timed out";
     case KDA_ERR_SCRATCH: return "call larger than the library's fixed scratch memory";
+    case KDA_ERR_SLOTS: return "no free state slot left";
     default: return "unknown status";
   }
 }
