@@ -1,16 +1,143 @@
-// kda_prefill: the gated delta rule over ragged prompts.
+// kda_prefill: the gated delta rule over ragged prompts, in chunks of 64
+// tokens (kda_prefill.cuh).  Four kernels: the list of chunks, what each
+// needs of itself (the preparation, all chunks at once), the chain of each
+// (request, head) through its chunks, and token by token what is too short
+// for a chunk, or inert.
 #include <cuda_runtime.h>
 
 #include "../../include/kda_recoverssm.h"
 #include "kda_launch.h"
-#include "kda_prompt.cuh"
-#include "kda_recurrent.cuh"
+#include "kda_prefill.cuh"
+
+namespace kda {
+namespace {
+
+// Windows of at most this many tokens go through the token-by-token kernel.
+constexpr int kShortLen = 8;
+constexpr int kListThreads = 1024;
+
+struct Workspace {
+  int64_t chunks, requests, order, images, bytes;  // offsets
+  int64_t max_chunks;
+};
+
+// Chunks end at a request's boundary and at its end, so a request of n
+// tokens has at most n / 64 + 2, and one with any has more than kShortLen.
+Workspace workspace_layout(int64_t n_tokens, int64_t B, int64_t H) {
+  const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  const int64_t most = n_tokens / (kShortLen + 1);
+  Workspace w;
+  w.max_chunks = n_tokens / kChunk + 2 * (B < most ? B : most);
+  w.chunks = 256;
+  w.requests = up(w.chunks + w.max_chunks * (int64_t)sizeof(PrefillChunk));
+  w.order = up(w.requests + B * (int64_t)sizeof(PrefillRequest));
+  w.images = up(w.order + B * 4);
+  w.bytes = w.images + w.max_chunks * H * (int64_t)kImgBytes;
+  return w;
+}
+
+__device__ __forceinline__ int chunks_of(int n) { return (n + kChunk - 1) / kChunk; }
+
+// One CTA: the chunks of every request, packed in order of the requests, and
+// the requests by falling number of chunks (a counting sort: the chain's
+// longest items start first).
+__global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const PrefillParams p) {
+  __shared__ int warp_sums[kListThreads / 32];
+  __shared__ int bins[kListThreads];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = p.r.maps.B;
+  bins[tid] = 0;
+  __syncthreads();
+  int base = 0;
+  for (int b0 = 0; b0 < B; b0 += kListThreads) {
+    const int b = b0 + tid;
+    int first = 0, rest = 0, t0 = 0, m = 0, n = 0;
+    if (b < B) {
+      const PromptRequest r = prompt_request(p.r.maps, b);
+      if (r.error != KDA_OK) report(p.r.maps.status, r.error);
+      if (r.n > p.short_len && r.dst >= 0) {
+        t0 = r.t0;
+        n = r.n;
+        m = r.m;
+        first = chunks_of(m);
+        rest = chunks_of(n - m);
+      }
+    }
+    int inc = first + rest;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, s, 31);
+    const int before = warp > 0 ? __shfl_sync(0xffffffffu, s, warp - 1) : 0;
+    int at = base + before + inc - (first + rest);
+    base += total;
+    // (windows that overlap can ask for more chunks than there is room for)
+    if (first + rest > 0 && (long long)at + first + rest > p.max_chunks) {
+      report(p.r.maps.status, KDA_ERR_ARG);
+      first = rest = 0;
+    }
+    if (b < B) {
+      p.requests[b] = PrefillRequest{at, first + rest, first};
+      atomicAdd(&bins[min(first + rest, kListThreads - 1)], 1);
+    }
+    // a warp writes the chunks of its 32 requests one after the other
+    uint32_t some = __ballot_sync(0xffffffffu, first + rest > 0);
+    while (some != 0) {
+      const int l = __ffs(some) - 1;
+      some &= some - 1;
+      const int f = __shfl_sync(0xffffffffu, first, l), c = f + __shfl_sync(0xffffffffu, rest, l);
+      const int w = __shfl_sync(0xffffffffu, at, l), t = __shfl_sync(0xffffffffu, t0, l);
+      const int mm = __shfl_sync(0xffffffffu, m, l), nn = __shfl_sync(0xffffffffu, n, l);
+      for (int j = lane; j < c; j += 32) {
+        const int from = j < f ? j * kChunk : mm + (j - f) * kChunk;
+        const int end = j < f ? mm : nn;
+        p.chunks[w + j] = PrefillChunk{t + from, min(kChunk, end - from)};
+      }
+    }
+    __syncthreads();
+  }
+  if (tid == 0) *p.n_chunks = base < p.max_chunks ? base : p.max_chunks;
+  // bins, longest first -> where each begins
+  const int bin = kListThreads - 1 - tid;
+  const int mine = bins[bin];
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int s = warp_sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  bins[bin] = inc - mine + (warp > 0 ? __shfl_sync(0xffffffffu, s, warp - 1) : 0);
+  __syncthreads();
+  for (int b = tid; b < B; b += kListThreads)
+    p.order[atomicAdd(&bins[min(p.requests[b].chunks, kListThreads - 1)], 1)] = b;
+}
+
+}  // namespace
+}  // namespace kda
 
 extern "C" {
 
 int64_t kda_prefill_workspace_bytes(int n_tokens, int B, int H) {
   if (n_tokens < 0 || B < 0 || H < 1 || H > KDA_PROMPT_MAX_HEADS) return -1;
-  return 0;
+  return kda::workspace_layout(n_tokens, B, H).bytes;
 }
 
 int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const kda_bf16 *raw_g,
@@ -21,13 +148,44 @@ int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const k
                 const int32_t *boundary_lens, const int32_t *query_start_loc, int n_tokens,
                 kda_bf16 *out, void *workspace, int64_t workspace_bytes, int B, int H, int Q,
                 int null_slot, int32_t *status, void *stream) {
-  const int64_t need = kda_prefill_workspace_bytes(n_tokens, B, H);
-  if (need < 0) return KDA_ERR_ARG;
-  if (B > 0 && n_tokens > 0 && workspace_bytes < need) return KDA_ERR_ARG;
-  return kda_recurrent(q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale, state_pool,
-                       state_dtype, slot_stride, n_slots, sources, destinations, boundaries,
-                       boundary_lens, query_start_loc, n_tokens, out, B, H, Q, null_slot, status,
-                       stream);
+  if (state_dtype != KDA_STATE_F32 && state_dtype != KDA_STATE_BF16) return KDA_ERR_UNSUPPORTED;
+  if (!kda::prompt_gate_ok(lower_bound)) return KDA_ERR_UNSUPPORTED;
+  int rc = kda::check_prompt_maps(sources, destinations, boundaries, boundary_lens,
+                                  query_start_loc, n_tokens, n_slots, B, H, Q, null_slot);
+  if (rc != KDA_OK) return rc;
+  if (B == 0 || n_tokens == 0) return KDA_OK;
+  rc = kda::check_rule(q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale, state_pool,
+                       state_dtype, slot_stride, H, out);
+  if (rc != KDA_OK) return rc;
+  const kda::Workspace w = kda::workspace_layout(n_tokens, B, H);
+  if (!workspace || workspace_bytes < w.bytes) return KDA_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return KDA_ERR_ALIGN;
+  if (w.max_chunks * H > 0x7fffffffLL) return KDA_ERR_ARG;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  kda::PrefillParams p;
+  p.r = kda::RecurrentParams{q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale,
+                             state_pool, slot_stride, out, H, kda::kShortLen,
+                             kda::make_prompt_maps(sources, destinations, boundaries,
+                                                   boundary_lens, query_start_loc, n_tokens,
+                                                   n_slots, B, Q, null_slot, status)};
+  p.short_len = kda::kShortLen;
+  p.max_chunks = (int)w.max_chunks;
+  p.n_chunks = reinterpret_cast<int *>(ws);
+  p.chunks = reinterpret_cast<kda::PrefillChunk *>(ws + w.chunks);
+  p.requests = reinterpret_cast<kda::PrefillRequest *>(ws + w.requests);
+  p.order = reinterpret_cast<int *>(ws + w.order);
+  p.images = ws + w.images;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf16 = state_dtype == KDA_STATE_BF16;
+  if (Q > kda::kShortLen && p.max_chunks > 0) {
+    kda::kda_prefill_list_kernel<<<1, kda::kListThreads, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    rc = kda::launch_prefill_prep(p, st);
+    if (rc != KDA_OK) return rc;
+    rc = kda::launch_prefill_chain(p, bf16, st);
+    if (rc != KDA_OK) return rc;
+  }
+  return kda::launch_recurrent(p.r, bf16, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,70 @@
+// The chunked gated delta rule: what its three kernels share.
+//
+// A chunk is 64 consecutive tokens of a request (fewer at its end and at its
+// boundary).  With G_t the sum of the log decays from the chunk's first
+// token to t (per key channel), the tokens of a chunk and the state S before
+// it give
+//   L_ts = beta_t sum_c kn_tc kn_sc e^{G_tc - G_sc}  (s < t),
+//   T = (I + L)^-1 diag(beta),
+//   A_ts = sum_c qn_tc kn_sc e^{G_tc - G_sc}         (s <= t),
+//   R = V - Kd S^T, Kd_t = kn_t e^{G_t};  U = T R;
+//   O = Qd S^T + A U, Qd_t = qn_t e^{G_t};
+//   S <- S diag(e^{G_end}) + U^T Ke, Ke_t = kn_t e^{G_end - G_t}.
+// The preparation kernel (kda_prefill_prep.cu) makes T, A, Kd, Qd, Ke of
+// every (chunk, head) at once, as shared-memory images in the layouts that
+// the matrix instructions read; the chain kernel (kda_prefill_chain.cu) takes
+// each (request, head) through its chunks.
+//
+// Every entry of the images is at most 1 in size (unit keys and queries,
+// decays <= 1, and T_ts is minus beta_t k_t applied to what is left of a
+// state beta_s k_s after contractions).  They are held as FP16 times 1024;
+// "hi" and "lo" are x rounded to FP16 and the rest rounded again, 22 bits
+// together.  hi.hi + hi.lo + lo.hi leaves 2^-22 of a product.
+#pragma once
+
+#include "kda_recurrent.cuh"
+
+namespace kda {
+
+constexpr int kChunk = 64;
+constexpr float kImgScale = 1024.f;
+
+// Image of one (chunk, head): byte offsets of its parts.  Rows of 128 bytes
+// (64 FP16), the 16-byte pieces of row r at position piece ^ (r & 7); K = 128
+// operands are two such blocks of 64 rows, channels 0 .. 63 and 64 .. 127.
+constexpr uint32_t kImgBlock = kChunk * 128;             // 8 KB
+constexpr uint32_t kImgKdHi = 0;                         // [t][channel]
+constexpr uint32_t kImgKdLo = kImgKdHi + 2 * kImgBlock;
+constexpr uint32_t kImgQd = kImgKdLo + 2 * kImgBlock;    // [t][channel], hi only
+constexpr uint32_t kImgTHi = kImgQd + 2 * kImgBlock;     // [t][s]
+constexpr uint32_t kImgTLo = kImgTHi + kImgBlock;
+constexpr uint32_t kImgKeHi = kImgTLo + kImgBlock;       // [s][channel]
+constexpr uint32_t kImgKeLo = kImgKeHi + 2 * kImgBlock;
+constexpr uint32_t kImgA = kImgKeLo + 2 * kImgBlock;     // [t][s], hi only
+constexpr uint32_t kImgDecay = kImgA + kImgBlock;        // e^{G_end}, 128 FP32
+constexpr uint32_t kImgBytes = kImgDecay + 128 * 4;
+
+struct PrefillChunk {
+  int t0, count;  // tokens t0 .. t0 + count - 1 of the packed activations
+};
+
+struct PrefillRequest {
+  int base, chunks;  // its chunks are base .. base + chunks - 1
+  int bnd_chunks;    // chunks up to its boundary; 0: none
+};
+
+struct PrefillParams {
+  RecurrentParams r;
+  int short_len;  // requests of at most so many tokens go token by token
+  int max_chunks;
+  int *n_chunks;            // [1]
+  PrefillChunk *chunks;     // [max_chunks]
+  PrefillRequest *requests; // [B]
+  int *order;               // [B], requests by falling number of chunks
+  uint8_t *images;          // [max_chunks, H, kImgBytes]
+};
+
+int launch_prefill_prep(const PrefillParams &p, cudaStream_t stream);
+int launch_prefill_chain(const PrefillParams &p, bool bf16, cudaStream_t stream);
+
+}  // namespace kda

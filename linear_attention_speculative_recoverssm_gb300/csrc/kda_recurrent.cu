@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(256, 2) kda_recurrent_kernel(const RecurrentPa
   const PromptRequest r = prompt_request(p.maps, b);
   if (r.error != KDA_OK && h == 0 && row0 == 0 && lane == 0) report(p.maps.status, r.error);
   if (r.n == 0) return;
+  if (r.n > p.max_len && r.dst >= 0) return;
   if (r.dst < 0) {  // inert: zero outputs
     for (int t = 0; t < r.n; ++t)
       if (lane < kRecRows)
@@ -199,7 +200,7 @@ extern "C" int kda_recurrent(
                        state_dtype, slot_stride, H, out);
   if (rc != KDA_OK) return rc;
   const kda::RecurrentParams p{q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale,
-                               state_pool, slot_stride, out, H,
+                               state_pool, slot_stride, out, H, 0x7fffffff,
                                kda::make_prompt_maps(sources, destinations, boundaries,
                                                      boundary_lens, query_start_loc, n_tokens,
                                                      n_slots, B, Q, null_slot, status)};

@@ -16,6 +16,7 @@ struct RecurrentParams {
   long long slot_stride;
   uint16_t *out;  // [n_tokens, H, 128]
   int H;
+  int max_len;  // requests of more tokens are someone else's (inert ones are not)
   PromptMaps maps;
 };
 

@@ -41,10 +41,13 @@ def _slots(b, n, sources, destinations, boundaries, boundary_lens, n_slots, null
 
 def rule(*, q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale, state, sources,
          destinations, out, Q, query_start_loc=None, boundaries=None, boundary_lens=None,
-         null_slot=0, out_f64=None):
+         null_slot=0, out_f64=None, sizes=None):
     """In place on ``state`` [slots, H, V, K] (FP32 or BF16 bits) and ``out``
     [T, H, V] (BF16 bits).  Returns the number of requests left out.
-    ``out_f64`` [T, H, V], when given, takes the outputs before rounding."""
+    ``out_f64`` [T, H, V], when given, takes the outputs before rounding.
+    ``sizes`` [T, H, V], when given, takes the size of what the outputs are
+    sums of: with q_scale and unit queries, the largest norm of the state row
+    over the last 64 tokens plus twice the sum of |u| over them."""
     T, H, V = v.shape
     B = len(sources)
     a = np.exp(A_log.astype(np.float64))[:, None]
@@ -70,6 +73,7 @@ def rule(*, q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale, stat
                 out_f64[t0:t0 + n] = 0
             continue
         S = np.zeros(state.shape[1:]) if src is None else state_to_f64(old[src])
+        norms, us = [np.sqrt((S * S).sum(-1))], []
         for t in range(t0, t0 + n):
             d = np.exp(lower_bound * sigmoid(a * (bf16_to_f64(raw_g[t]) + dt)))
             kn, qn = l2norm(bf16_to_f64(k[t])), l2norm(bf16_to_f64(q[t])) * q_scale
@@ -78,6 +82,9 @@ def rule(*, q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale, stat
             u = beta * (bf16_to_f64(v[t]) - np.einsum("hvk,hk->hv", S, kn))
             S = S + u[:, :, None] * kn[:, None, :]
             o = np.einsum("hvk,hk->hv", S, qn)
+            if sizes is not None:
+                norms, us = norms[-64:] + [np.sqrt((S * S).sum(-1))], us[-63:] + [np.abs(u)]
+                sizes[t] = abs(q_scale) * (np.max(norms, axis=0) + 2 * np.sum(us, axis=0))
             out[t] = f64_to_bf16(o)
             if out_f64 is not None:
                 out_f64[t] = o
