@@ -1,19 +1,25 @@
 // The preparation of the chunked delta rule: the images of every (chunk,
 // head) (kda_prefill.cuh).  One CTA of 8 warps each; warps 2 i and 2 i + 1
-// own the 16 tokens of block i, half the channels each, in the layout of an
-// m16n8k8 operand: lane 4 g + j holds tokens g and g + 8 and eight
-// consecutive channels of every 32.
+// own the 16 tokens of block i.
 //
 // The products need e^{G_t - G_s} per channel, whose two factors must stay
 // representable.  Within a block of 16 they are taken from its middle,
 // 2^(G_t - mid) and 2^(mid - G_s), at most 2^116 with the steepest gate, and
 // the 16 x 16 products run in TF32 (8 exponent bits) straight from the
-// registers that hold the factors.  Between blocks a border lies between s
-// and t, and both factors, from t back to it and from it back to s, are at
-// most 1: blocks 0-1 | 2-3 with the border at token 32, blocks 0 | 1 and
-// 2 | 3 with theirs at 16 and 48, in FP16 parts through shared memory.  The
-// key products take hi.hi + hi.lo + lo.hi (their errors reach the state);
-// the query products hi alone, 2^-12 of values whose result rounds to BF16.
+// registers that hold the factors: lane 4 g + j of a warp holds tokens g and
+// g + 8 and eight consecutive channels of every 32, half of the channels in
+// each of the two warps.  Between blocks a border lies between s and t, and
+// both factors, from t back to it and from it back to s, are at most 1:
+// blocks 0-1 | 2-3 with the border at token 32, blocks 0 | 1 and 2 | 3 with
+// theirs at 16 and 48, in FP16 parts through shared memory.  The key products
+// take hi.hi + hi.lo + lo.hi (their errors reach the state); the query
+// products round q alone to 11 bits, whose result rounds to BF16's 8.
+//
+// The references are powers of two: with B_i the sum of the log2 decays
+// before block i rounded to an integer, a row operand is R_t = kn_t
+// 2^(G_t - B_i) and a column operand C_s = kn_s 2^(B_{i+1} - G_s), split into
+// FP16 parts once; from another block's border, or the chunk's start, they
+// are the same parts times an exact 2^n.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -27,10 +33,10 @@ namespace kda {
 namespace {
 
 constexpr int kPrepThreads = 256;
-constexpr uint32_t kXPitch = 272;  // bytes of a 128-channel FP16 row, padded
+constexpr uint32_t kXPitch = 256;  // bytes of a 128-channel FP16 row
 constexpr uint32_t kXBytes = kChunk * kXPitch;
 constexpr uint32_t kYBytes = 32 * kXPitch;
-constexpr int kLPitch = 68;  // floats
+constexpr int kLPitch = 68, kYPitch = 72, kLtPitch = 20;  // floats
 constexpr int kDPitch = 17;
 
 // Shared memory, by phases: the FP16 operands of the products between
@@ -38,24 +44,40 @@ constexpr int kDPitch = 17;
 struct PrepSmem {
   union {
     struct {
+      // (before they hold operands, x16_hi and x16_lo hold the log2 decay
+      // sums: of a 16-byte piece's eight channels the first and last four)
       uint8_t x16_hi[kXBytes], x16_lo[kXBytes], x32_hi[kXBytes], x32_lo[kXBytes];
       uint8_t y16[kYBytes], y32[kYBytes];
     } x;
     struct {
-      float L[kChunk * kLPitch], X[kChunk * kLPitch], Y[32 * kLPitch];
+      float L[kChunk * kLPitch], X[kChunk * kLPitch], Y[32 * kYPitch];
+      float Lt[4][16 * kLtPitch];  // the diagonal blocks of L, transposed
     } s;
   } u;
-  float fac[4][4][128];        // [kind][block][channel], times 1024
-  float tot[2][4][128];        // log2 decays of a block's two halves
+  float fac[3][4][128];   // [R, C, Ke][block][channel], times 1024
+  uint16_t pow[2][4][128];  // FP16 2^n: of Kd and Qd; of the operands at 32
+  float tot[2][4][128];   // log2 decays of a block's two halves
   float part[4][2][16 * kDPitch];  // a block's products over channels 64 .. 127
-  float norm[2][kChunk][2];    // sums of squares per channel half
+  float norm[2][kChunk][2];        // sums of squares per channel half
   float beta[kChunk];
 };
 
+// Rows r of 256 bytes: 16-byte pieces, each 128-byte half permuted so that
+// one piece of eight consecutive rows, and four pieces of two, meet every
+// bank once.
+__device__ __forceinline__ uint32_t x_at(int r, int piece) {
+  const int f = ((r & 1) << 2) | ((r >> 1) & 3);
+  return (uint32_t)r * kXPitch + (uint32_t)(piece >> 3) * 128u +
+         (uint32_t)(((piece & 7) ^ f) << 4);
+}
+
+// The leading 11 bits of x (truncated), and x rounded to them as the tensor
+// cores, which drop the rest, then see it.
 __device__ __forceinline__ float tf32_hi(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return __uint_as_float(r);
+  return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+}
+__device__ __forceinline__ float tf32_round(float x) {
+  return __uint_as_float(__float_as_uint(x) + 0x1000u);
 }
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], float b0, float b1) {
@@ -83,45 +105,81 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// Eight values as FP16 (hi), and what that leaves (lo).
-__device__ __forceinline__ uint4 half8(const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) {
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ void split8(const float (&x)[8], uint4 &hi, uint4 &lo) {
+// Eight values (four pairs) as FP16, and what that leaves.
+__device__ __forceinline__ uint4 half8(const float2 (&x)[4]) {
+  return make_uint4(h2_bits(__float22half2_rn(x[0])), h2_bits(__float22half2_rn(x[1])),
+                    h2_bits(__float22half2_rn(x[2])), h2_bits(__float22half2_rn(x[3])));
+}
+
+__device__ __forceinline__ void split8(const float2 (&x)[4], uint4 &hi, uint4 &lo) {
   uint32_t w[4], v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-    const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(x[2 * i] - f.x, x[2 * i + 1] - f.y);
-    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    v[i] = *reinterpret_cast<const uint32_t *>(&l);
+    const __half2 h = __float22half2_rn(x[i]);
+    w[i] = h2_bits(h);
+    v[i] = h2_bits(__float22half2_rn(ffma2(__half22float2(h), make_float2(-1.f, -1.f), x[i])));
   }
   hi = make_uint4(w[0], w[1], w[2], w[3]);
   lo = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-__device__ __forceinline__ void unpack8f(uint4 b, float (&f)[8]) {
-  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// Eight FP16 values times powers of two.
+__device__ __forceinline__ uint4 scale8(uint4 x, uint4 f) {
+  uint4 r;
+  const auto mul = [](uint32_t a, uint32_t b) {
+    return h2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&a),
+                           *reinterpret_cast<const __half2 *>(&b)));
+  };
+  r.x = mul(x.x, f.x);
+  r.y = mul(x.y, f.y);
+  r.z = mul(x.z, f.z);
+  r.w = mul(x.w, f.w);
+  return r;
 }
 
-__device__ __forceinline__ void scaled8(const float (&x)[8], const float *fac, float (&out)[8]) {
-  const float4 a = lds4(fac), b = lds4(fac + 4);
-  const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ float2 bf16x2_f32(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+__device__ __forceinline__ void unpack4x2(uint4 b, float2 (&f)[4]) {
+  f[0] = bf16x2_f32(b.x);
+  f[1] = bf16x2_f32(b.y);
+  f[2] = bf16x2_f32(b.z);
+  f[3] = bf16x2_f32(b.w);
+}
+
+__device__ __forceinline__ void load4x2(const float *p, float2 (&f)[4]) {
+  const float4 a = lds4(p), b = lds4(p + 4);
+  f[0] = make_float2(a.x, a.y);
+  f[1] = make_float2(a.z, a.w);
+  f[2] = make_float2(b.x, b.y);
+  f[3] = make_float2(b.z, b.w);
+}
+
+// C[16 x 8] (+)= A[16 x 8 steps] B[8 steps x 8], FP32 operands in shared
+// memory as TF32 parts, from step `first` on.
+__device__ __forceinline__ void tile_mm(float (&c)[4], const float *A, int lda, const float *B,
+                                        int ldb, int first, int steps, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  for (int ks = first; ks < steps; ++ks) {
+    const float a[4] = {A[g * lda + 8 * ks + t], A[(g + 8) * lda + 8 * ks + t],
+                        A[g * lda + 8 * ks + t + 4], A[(g + 8) * lda + 8 * ks + t + 4]};
+    const float b0 = B[(8 * ks + t) * ldb + g], b1 = B[(8 * ks + t + 4) * ldb + g];
+    float h[4], l[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = x[i] * f[i];
+    for (int i = 0; i < 4; ++i) {
+      h[i] = tf32_hi(a[i]);
+      l[i] = a[i] - h[i];
+    }
+    const float h0 = tf32_hi(b0), h1 = tf32_hi(b1);
+    mma_tf32(c, l, h0, h1);
+    mma_tf32(c, h, b0 - h0, b1 - h1);
+    mma_tf32(c, h, h0, h1);
+  }
 }
 
 // Where the 16-byte piece of channels c .. c + 7 (or columns) of row t lies.
@@ -142,24 +200,30 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
   const int row[2] = {16 * blk + g, 16 * blk + g + 8};
   const int ch0 = hf * 64 + tig * 8;  // slices add 0 and 32
 
-  // -- loads; log2 decays and their sums over the block's tokens ------------
   uint4 kraw[2][2], qraw[2][2];  // [slice][token]
-  float d[2][2][8];              // log2 decay sums around the block's middle
-  {
-    uint4 graw[2][2];
 #pragma unroll
-    for (int sl = 0; sl < 2; ++sl)
+  for (int sl = 0; sl < 2; ++sl)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        kraw[sl][r] = qraw[sl][r] = graw[sl][r] = make_uint4(0, 0, 0, 0);
-        if (row[r] < ck.count) {
-          const long long at =
-              ((long long)(ck.t0 + row[r]) * p.r.H + h) * kDim + ch0 + 32 * sl;
-          kraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(p.r.k + at));
-          graw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(p.r.g + at));
-          qraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(p.r.q + at));
-        }
+    for (int r = 0; r < 2; ++r) {
+      kraw[sl][r] = qraw[sl][r] = make_uint4(0, 0, 0, 0);
+      if (row[r] < ck.count) {
+        const long long at = ((long long)(ck.t0 + row[r]) * p.r.H + h) * kDim + ch0 + 32 * sl;
+        kraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(p.r.k + at));
+        qraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(p.r.q + at));
       }
+    }
+  // -- log2 decays and their sums around the block's middle: a thread takes
+  //    two channels and the block's 16 tokens in turn -------------------------
+  {
+    const int pr = threadIdx.x & 63, c = 2 * pr;
+    uint32_t graw[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      graw[t] = 0;
+      if (16 * blk + t < ck.count)
+        graw[t] = __ldg(reinterpret_cast<const uint32_t *>(
+            p.r.g + ((long long)(ck.t0 + 16 * blk + t) * p.r.H + h) * kDim + c));
+    }
     if (threadIdx.x < kChunk) {
       float b = 0.f;
       if ((int)threadIdx.x < ck.count)
@@ -168,103 +232,97 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
       sm.beta[threadIdx.x] = b;
     }
     const float al = expf(p.r.A_log[h]) * kLog2e, lb2 = p.r.lower_bound * kLog2e;
+    const float2 dt = *reinterpret_cast<const float2 *>(p.r.dt_bias + h * kDim + c);
+    const float2 off = make_float2(-al * dt.x, -al * dt.y), nal = make_float2(-al, -al);
+    float2 x[16], sum = make_float2(0.f, 0.f), mid = sum;
 #pragma unroll
-    for (int sl = 0; sl < 2; ++sl) {
-      const float4 da = *reinterpret_cast<const float4 *>(p.r.dt_bias + h * kDim + ch0 + 32 * sl);
-      const float4 db =
-          *reinterpret_cast<const float4 *>(p.r.dt_bias + h * kDim + ch0 + 32 * sl + 4);
-      const float dt[8] = {da.x, da.y, da.z, da.w, db.x, db.y, db.z, db.w};
-      float ta[8], tb[8];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float raw[8];
-        unpack8f(graw[sl][r], raw);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float x = lb2 * __fdividef(1.f, 1.f + exp2f_fast(fmaf(-al, raw[e], -al * dt[e])));
-          if (row[r] >= ck.count) x = 0.f;
-          // inclusive sum over the 8 tokens of this half
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, x, 4 * o);
-            if (g >= o) x += y;
-          }
-          const float t = __shfl_sync(0xffffffffu, x, 28 + tig);
-          d[sl][r][e] = r == 0 ? x - t : x;
-          if (r == 0) ta[e] = t;
-          else tb[e] = t;
-        }
+    for (int t = 0; t < 16; ++t) {
+      const float2 z = ffma2(nal, bf16x2_f32(graw[t]), off);
+      if (16 * blk + t < ck.count) {
+        sum.x += lb2 * __fdividef(1.f, 1.f + exp2f_fast(z.x));
+        sum.y += lb2 * __fdividef(1.f, 1.f + exp2f_fast(z.y));
       }
-      if (g == 0) {
-        float *pa = &sm.tot[0][blk][ch0 + 32 * sl], *pb = &sm.tot[1][blk][ch0 + 32 * sl];
-        sts4(pa, make_float4(ta[0], ta[1], ta[2], ta[3]));
-        sts4(pa + 4, make_float4(ta[4], ta[5], ta[6], ta[7]));
-        sts4(pb, make_float4(tb[0], tb[1], tb[2], tb[3]));
-        sts4(pb + 4, make_float4(tb[4], tb[5], tb[6], tb[7]));
+      x[t] = sum;
+      if (t == 7) {
+        mid = sum;
+        sum = make_float2(0.f, 0.f);
       }
     }
+    // (the halves are summed apart: tokens 8 .. 15 start from the middle)
+    uint8_t *to = ((pr & 2) ? sm.u.x.x16_lo : sm.u.x.x16_hi) + (pr & 1) * 8;
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+      *reinterpret_cast<float2 *>(to + x_at(16 * blk + t, pr >> 2)) =
+          t < 8 ? make_float2(x[t].x - mid.x, x[t].y - mid.y) : x[t];
+    *reinterpret_cast<float2 *>(&sm.tot[0][blk][c]) = mid;
+    *reinterpret_cast<float2 *>(&sm.tot[1][blk][c]) = sum;
   }
   // -- norms: sums of squares over this warp's channels ----------------------
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    float ks = 0.f, qs = 0.f;
+    float2 ks = make_float2(0.f, 0.f), qs = ks;
 #pragma unroll
     for (int sl = 0; sl < 2; ++sl) {
-      float f[8];
-      unpack8f(kraw[sl][r], f);
+      float2 f[4];
+      unpack4x2(kraw[sl][r], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ks = fmaf(f[e], f[e], ks);
-      unpack8f(qraw[sl][r], f);
+      for (int e = 0; e < 4; ++e) ks = ffma2(f[e], f[e], ks);
+      unpack4x2(qraw[sl][r], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) qs = fmaf(f[e], f[e], qs);
+      for (int e = 0; e < 4; ++e) qs = ffma2(f[e], f[e], qs);
     }
-    ks += __shfl_xor_sync(0xffffffffu, ks, 1);
-    qs += __shfl_xor_sync(0xffffffffu, qs, 1);
-    ks += __shfl_xor_sync(0xffffffffu, ks, 2);
-    qs += __shfl_xor_sync(0xffffffffu, qs, 2);
+    float kk = ks.x + ks.y, qq = qs.x + qs.y;
+    kk += __shfl_xor_sync(0xffffffffu, kk, 1);
+    qq += __shfl_xor_sync(0xffffffffu, qq, 1);
+    kk += __shfl_xor_sync(0xffffffffu, kk, 2);
+    qq += __shfl_xor_sync(0xffffffffu, qq, 2);
     if (tig == 0) {
-      sm.norm[hf][row[r]][0] = ks;
-      sm.norm[hf][row[r]][1] = qs;
+      sm.norm[hf][row[r]][0] = kk;
+      sm.norm[hf][row[r]][1] = qq;
     }
   }
   __syncthreads();
 
-  // -- per (block, channel) factors, times the images' scale -----------------
-  // kind 0: from a token to the chunk's start (on 2^(G_t - mid))
-  //      1: from the chunk's end back to a token (on 2^(mid - G_s))
-  //      2, 3: to the border at 16 / 48, and at 32 (even and first blocks
-  //            hold the columns s, odd and last ones the rows t)
+  // -- per (block, channel) factors -------------------------------------------
+  // With ph_i what the rounding of B_i leaves, summed block by block so that a
+  // block's own size, not the sum's, sets the error:
+  //   R = kn 2^(G - mid) fac[0], fac[0] = 2^(mid - before + ph_i)
+  //   C = kn 2^(mid - G) fac[1], fac[1] = 2^(after - mid - ph_{i+1})
+  //   Ke = kn 2^(mid - G) fac[2], from the chunk's end
   {
     const int c = threadIdx.x & 127;
-    float ta[4], tb[4];
+    float ta[4], tb[4], ph[5], B[5];
+    ph[0] = B[0] = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       ta[j] = sm.tot[0][j][c];
       tb[j] = sm.tot[1][j][c];
+      const float x = ph[j] + (ta[j] + tb[j]), n = rintf(x);
+      ph[j + 1] = x - n;
+      B[j + 1] = B[j] + n;
     }
-    const float t0 = ta[0] + tb[0], t1 = ta[1] + tb[1], t2 = ta[2] + tb[2], t3 = ta[3] + tb[3];
-    const auto put = [&](int kind, int j, float x) {
-      sm.fac[kind][j][c] = kImgScale * exp2f_fast(x);
+    // 2^n, n <= 0 an integer (FP16 has it down to 2^-24)
+    const auto power = [](float n) {
+      return __half_as_ushort(__float2half_rn(exp2f_fast(fmaxf(n, -60.f))));
     };
     if (threadIdx.x < 128) {
-      put(0, 0, ta[0]);
-      put(0, 1, t0 + ta[1]);
-      put(1, 0, tb[0] + t1 + t2 + t3);
-      put(1, 1, tb[1] + t2 + t3);
-      put(2, 0, tb[0]);
-      put(2, 1, ta[1]);
-      put(3, 0, tb[0] + t1);
-      put(3, 1, tb[1]);
-      reinterpret_cast<float *>(img + kImgDecay)[c] = exp2f_fast(t0 + t1 + t2 + t3);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sm.fac[0][j][c] = kImgScale * exp2f_fast(ta[j] + ph[j]);
+        sm.pow[0][j][c] = power(B[j]);
+      }
+      reinterpret_cast<float *>(img + kImgDecay)[c] =
+          exp2f_fast((ta[0] + tb[0]) + (ta[1] + tb[1]) + (ta[2] + tb[2]) + (ta[3] + tb[3]));
     } else {
-      put(0, 2, t0 + t1 + ta[2]);
-      put(0, 3, t0 + t1 + t2 + ta[3]);
-      put(1, 2, tb[2] + t3);
-      put(1, 3, tb[3]);
-      put(2, 2, tb[2]);
-      put(2, 3, ta[3]);
-      put(3, 2, ta[2]);
-      put(3, 3, t2 + ta[3]);
+      float rest = 0.f;
+#pragma unroll
+      for (int j = 3; j >= 0; --j) {
+        sm.fac[1][j][c] = kImgScale * exp2f_fast(tb[j] - ph[j + 1]);
+        sm.fac[2][j][c] = kImgScale * exp2f_fast(tb[j] + rest);
+        rest += ta[j] + tb[j];
+      }
+      sm.pow[1][0][c] = power(B[2] - B[1]);
+      sm.pow[1][3][c] = power(B[3] - B[2]);
     }
   }
   float rk[2], rq[2];
@@ -283,78 +341,98 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
     for (int i = 0; i < 4; ++i) dk[n][i] = dq[n][i] = 0.f;
 #pragma unroll
   for (int sl = 0; sl < 2; ++sl) {
-    const int c = ch0 + 32 * sl;
-    float kf[2][8], kg[2][8], qf[2][8];  // kn 2^(G - mid), kn 2^(mid - G), qn 2^(G - mid)
+    const int c = ch0 + 32 * sl, piece = c >> 3;
+    float2 kf[2][4], kg[2][4], qf[2][4];  // kn 2^(G - mid), kn 2^(mid - G), qn 2^(G - mid)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float k[8], q[8];
-      unpack8f(kraw[sl][r], k);
-      unpack8f(qraw[sl][r], q);
+      float2 k[4], q[4];
+      unpack4x2(kraw[sl][r], k);
+      unpack4x2(qraw[sl][r], q);
+      const float4 d0 = *reinterpret_cast<const float4 *>(sm.u.x.x16_hi + x_at(row[r], piece));
+      const float4 d1 = *reinterpret_cast<const float4 *>(sm.u.x.x16_lo + x_at(row[r], piece));
+      const float2 d[4] = {make_float2(d0.x, d0.y), make_float2(d0.z, d0.w),
+                           make_float2(d1.x, d1.y), make_float2(d1.z, d1.w)};
+      const float2 rk2 = make_float2(rk[r], rk[r]), rq2 = make_float2(rq[r], rq[r]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f = exp2f_fast(d[sl][r][e]), b = exp2f_fast(-d[sl][r][e]);
-        const float kn = k[e] * rk[r];
-        kf[r][e] = kn * f;
-        kg[r][e] = kn * b;
-        qf[r][e] = q[e] * rq[r] * f;
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = make_float2(exp2f_fast(d[e].x), exp2f_fast(d[e].y));
+        const float2 b = make_float2(exp2f_fast(-d[e].x), exp2f_fast(-d[e].y));
+        const float2 kn = fmul2(k[e], rk2);
+        kf[r][e] = fmul2(kn, f);
+        kg[r][e] = fmul2(kn, b);
+        qf[r][e] = fmul2(fmul2(q[e], rq2), f);
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      // columns tig and tig + 4 of the operand are channels e and e + 1
-      float a[4] = {kf[0][e], kf[1][e], kf[0][e + 1], kf[1][e + 1]};
-      float ah[4], alo[4], aq[4] = {qf[0][e], qf[1][e], qf[0][e + 1], qf[1][e + 1]};
+    for (int e = 0; e < 4; ++e) {
+      // columns tig and tig + 4 of the operand are channels 2 e and 2 e + 1
+      const float a[4] = {kf[0][e].x, kf[1][e].x, kf[0][e].y, kf[1][e].y};
+      const float aq[4] = {tf32_round(qf[0][e].x), tf32_round(qf[1][e].x),
+                           tf32_round(qf[0][e].y), tf32_round(qf[1][e].y)};
+      float ah[4], al[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         ah[i] = tf32_hi(a[i]);
-        alo[i] = a[i] - ah[i];
-        aq[i] = tf32_hi(aq[i]);
+        al[i] = a[i] - ah[i];
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        const float b0 = tf32_hi(kg[n][e]), b1 = tf32_hi(kg[n][e + 1]);
-        mma_tf32(dk[n], alo, b0, b1);
-        mma_tf32(dk[n], ah, kg[n][e] - b0, kg[n][e + 1] - b1);
-        mma_tf32(dk[n], ah, b0, b1);
-        mma_tf32(dq[n], aq, b0, b1);
+        const float h0 = tf32_hi(kg[n][e].x), h1 = tf32_hi(kg[n][e].y);
+        const float l0 = kg[n][e].x - h0, l1 = kg[n][e].y - h1;
+        mma_tf32(dk[n], al, h0, h1);
+        mma_tf32(dk[n], ah, l0, l1);
+        mma_tf32(dk[n], ah, h0, h1);
+        mma_tf32(dq[n], aq, l0, l1);
+        mma_tf32(dq[n], aq, h0, h1);
       }
     }
+    float2 facR[4], facC[4], facE[4];
+    load4x2(&sm.fac[0][blk][c], facR);
+    load4x2(&sm.fac[1][blk][c], facC);
+    load4x2(&sm.fac[2][blk][c], facE);
+    const uint4 pow0 = *reinterpret_cast<const uint4 *>(&sm.pow[0][blk][c]);
+    const uint4 pow32 = *reinterpret_cast<const uint4 *>(&sm.pow[1][blk][c]);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float x[8];
-      uint4 hi, lo;
-      const uint32_t at = img_at(row[r], c);
-      scaled8(kf[r], &sm.fac[0][blk][c], x);
-      split8(x, hi, lo);
-      *reinterpret_cast<uint4 *>(img + kImgKdHi + at) = hi;
-      *reinterpret_cast<uint4 *>(img + kImgKdLo + at) = lo;
-      scaled8(qf[r], &sm.fac[0][blk][c], x);
-      *reinterpret_cast<uint4 *>(img + kImgQd + at) = half8(x);
-      scaled8(kg[r], &sm.fac[1][blk][c], x);
+      float2 x[4];
+      uint4 rh, rl, hi, lo;
+      const uint32_t at = img_at(row[r], c), xat = x_at(row[r], piece);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = fmul2(kg[r][e], facE[e]);
       split8(x, hi, lo);
       *reinterpret_cast<uint4 *>(img + kImgKeHi + at) = hi;
       *reinterpret_cast<uint4 *>(img + kImgKeLo + at) = lo;
-      const uint32_t xat = (uint32_t)row[r] * kXPitch + (uint32_t)c * 2;
-      scaled8((blk & 1) ? kf[r] : kg[r], &sm.fac[2][blk][c], x);
-      split8(x, hi, lo);
-      *reinterpret_cast<uint4 *>(sm.u.x.x16_hi + xat) = hi;
-      *reinterpret_cast<uint4 *>(sm.u.x.x16_lo + xat) = lo;
-      scaled8(blk >= 2 ? kf[r] : kg[r], &sm.fac[3][blk][c], x);
-      split8(x, hi, lo);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = fmul2(kf[r][e], facR[e]);
+      split8(x, rh, rl);
+      *reinterpret_cast<uint4 *>(img + kImgKdHi + at) = blk == 0 ? rh : scale8(rh, pow0);
+      *reinterpret_cast<uint4 *>(img + kImgKdLo + at) = blk == 0 ? rl : scale8(rl, pow0);
+      if (blk < 3) {  // (block 3 is no column)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = fmul2(kg[r][e], facC[e]);
+        split8(x, hi, lo);
+      }
+      *reinterpret_cast<uint4 *>(sm.u.x.x16_hi + xat) = (blk & 1) ? rh : hi;
+      *reinterpret_cast<uint4 *>(sm.u.x.x16_lo + xat) = (blk & 1) ? rl : lo;
+      if (blk >= 2) {
+        hi = rh;
+        lo = rl;
+      }
+      if (blk == 0 || blk == 3) {
+        hi = scale8(hi, pow32);
+        lo = scale8(lo, pow32);
+      }
       *reinterpret_cast<uint4 *>(sm.u.x.x32_hi + xat) = hi;
       *reinterpret_cast<uint4 *>(sm.u.x.x32_lo + xat) = lo;
-      if (blk & 1) {
-        scaled8(qf[r], &sm.fac[2][blk][c], x);
-        *reinterpret_cast<uint4 *>(sm.u.x.y16 +
-                                   (uint32_t)((blk >> 1) * 16 + g + 8 * r) * kXPitch + c * 2) =
-            half8(x);
-      }
-      if (blk >= 2) {
-        scaled8(qf[r], &sm.fac[3][blk][c], x);
-        *reinterpret_cast<uint4 *>(sm.u.x.y32 +
-                                   (uint32_t)((blk - 2) * 16 + g + 8 * r) * kXPitch + c * 2) =
-            half8(x);
-      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = fmul2(qf[r][e], facR[e]);
+      hi = half8(x);
+      *reinterpret_cast<uint4 *>(img + kImgQd + at) = blk == 0 ? hi : scale8(hi, pow0);
+      if (blk & 1)
+        *reinterpret_cast<uint4 *>(sm.u.x.y16 + x_at((blk >> 1) * 16 + g + 8 * r, piece)) = hi;
+      if (blk >= 2)
+        *reinterpret_cast<uint4 *>(sm.u.x.y32 + x_at((blk - 2) * 16 + g + 8 * r, piece)) =
+            blk == 2 ? hi : scale8(hi, pow32);
     }
   }
   if (hf == 1) {
@@ -392,22 +470,18 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
       xl = sm.u.x.x16_lo;
       y = sm.u.x.y16;
     }
-    const uint32_t arow = (uint32_t)(lane & 15) * kXPitch + (uint32_t)(lane >> 4) * 16;
-    const uint32_t brow = (uint32_t)((lane & 7) + ((lane >> 4) << 3)) * kXPitch +
-                          (uint32_t)((lane >> 3) & 1) * 16;
-    const uint32_t ah0 = smem_u32(xh) + r0 * kXPitch + arow;
-    const uint32_t al0 = smem_u32(xl) + r0 * kXPitch + arow;
-    const uint32_t aq0 = smem_u32(y) + y0 * kXPitch + arow;
-    const uint32_t bh0 = smem_u32(xh) + c0 * kXPitch + brow;
-    const uint32_t bl0 = smem_u32(xl) + c0 * kXPitch + brow;
+    const int ar = lane & 15, br = (lane & 7) + ((lane >> 4) << 3);
+    const uint32_t ah0 = smem_u32(xh), al0 = smem_u32(xl), aq0 = smem_u32(y);
 #pragma unroll 2
     for (int ks = 0; ks < 8; ++ks) {
       uint32_t ah[4], al[4], aq[4], bh[4], bl[4];
-      ldmatrix4(ah, ah0 + ks * 32);
-      ldmatrix4(al, al0 + ks * 32);
-      ldmatrix4(aq, aq0 + ks * 32);
-      ldmatrix4(bh, bh0 + ks * 32);
-      ldmatrix4(bl, bl0 + ks * 32);
+      const uint32_t at = x_at(r0 + ar, 2 * ks + (lane >> 4));
+      const uint32_t bt = x_at(c0 + br, 2 * ks + ((lane >> 3) & 1));
+      ldmatrix4(ah, ah0 + at);
+      ldmatrix4(al, al0 + at);
+      ldmatrix4(aq, aq0 + x_at(y0 + ar, 2 * ks + (lane >> 4)));
+      ldmatrix4(bh, ah0 + bt);
+      ldmatrix4(bl, al0 + bt);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         mma_f16(ok[n], al, bh[2 * n], bh[2 * n + 1]);
@@ -450,8 +524,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
         for (int e = 0; e < 2; ++e) {
           // (above the diagonal the factors may have overflowed: dropped, not
           // multiplied by zero)
-          L[t * kLPitch + 16 * blk + s0 + e] =
-              s0 + e < tl ? sm.beta[t] * (dk[n][i + e] + pk[e]) : 0.f;
+          const float l = s0 + e < tl ? sm.beta[t] * (dk[n][i + e] + pk[e]) : 0.f;
+          sm.u.s.Lt[blk][(s0 + e) * kLtPitch + tl] = l;
           a[e] = s0 + e <= tl ? (dq[n][i + e] + pq[e]) * kImgScale : 0.f;
         }
         put_a(t, 16 * blk + s0, a[0], a[1]);
@@ -471,57 +545,57 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
     float x[16];
 #pragma unroll
     for (int t = 0; t < 16; ++t) x[t] = t == j ? 1.f : 0.f;
-    const float *Lb = L + (16 * warp) * kLPitch + 16 * warp;
+    const float *Lb = sm.u.s.Lt[warp];
 #pragma unroll
-    for (int t = 0; t < 15; ++t)
+    for (int t = 0; t < 15; ++t) {
 #pragma unroll
-      for (int u = t + 1; u < 16; ++u) x[u] = fmaf(-Lb[u * kLPitch + t], x[t], x[u]);
+      for (int u = (t + 1) & ~3; u < 16; u += 4) {
+        // (entries up to the diagonal are zeros)
+        const float4 l = lds4(Lb + t * kLtPitch + u);
+        if (u + 0 > t) x[u] = fmaf(-l.x, x[t], x[u]);
+        if (u + 1 > t) x[u + 1] = fmaf(-l.y, x[t], x[u + 1]);
+        if (u + 2 > t) x[u + 2] = fmaf(-l.z, x[t], x[u + 2]);
+        if (u + 3 > t) x[u + 3] = fmaf(-l.w, x[t], x[u + 3]);
+      }
+    }
     if (lane < 16) {
 #pragma unroll
       for (int t = 0; t < 16; ++t) X[(16 * warp + t) * kLPitch + 16 * warp + j] = x[t];
     }
   }
   __syncthreads();
+  const auto put = [&](float *to, int ld, const float (&c)[4], float sign) {
+    *reinterpret_cast<float2 *>(to + g * ld + 2 * tig) = make_float2(sign * c[0], sign * c[1]);
+    *reinterpret_cast<float2 *>(to + (g + 8) * ld + 2 * tig) =
+        make_float2(sign * c[2], sign * c[3]);
+  };
   {
-    // X10 = -X11 (L10 X00) and X32 = -X33 (L32 X22), 16 x 16 each
-    const int pr = threadIdx.x >> 7, r = (threadIdx.x & 127) >> 3, c = (threadIdx.x & 7) * 2;
-    const int lo = 32 * pr, hi = lo + 16;
-    float y0 = 0.f, y1 = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float l = L[(hi + r) * kLPitch + lo + k];
-      const float2 x = *reinterpret_cast<const float2 *>(&X[(lo + k) * kLPitch + lo + c]);
-      y0 = fmaf(l, x.x, y0);
-      y1 = fmaf(l, x.y, y1);
+    // X10 = -X11 (L10 X00) and X32 = -X33 (L32 X22), 16 x 8 a warp
+    const int lo = 32 * (warp >> 1), hi = lo + 16, n = 8 * (warp & 1);
+    if (warp < 4) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      tile_mm(c, &L[hi * kLPitch + lo], kLPitch, &X[lo * kLPitch + lo + n], kLPitch, n / 8, 2,
+              lane);
+      put(&Y[lo / 2 * kYPitch + n], kYPitch, c, 1.f);
     }
-    *reinterpret_cast<float2 *>(&Y[r * kLPitch + 32 * pr + c]) = make_float2(y0, y1);
     __syncthreads();
-    float z0 = 0.f, z1 = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float l = X[(hi + r) * kLPitch + hi + k];
-      const float2 x = *reinterpret_cast<const float2 *>(&Y[k * kLPitch + 32 * pr + c]);
-      z0 = fmaf(l, x.x, z0);
-      z1 = fmaf(l, x.y, z1);
+    if (warp < 4) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      tile_mm(c, &X[hi * kLPitch + hi], kLPitch, &Y[lo / 2 * kYPitch + n], kYPitch, 0, 2, lane);
+      put(&X[hi * kLPitch + lo + n], kLPitch, c, -1.f);
     }
-    *reinterpret_cast<float2 *>(&X[(hi + r) * kLPitch + lo + c]) = make_float2(-z0, -z1);
-    // above the diagonal of the two halves
-    *reinterpret_cast<float2 *>(&X[(lo + r) * kLPitch + hi + c]) = make_float2(0.f, 0.f);
     __syncthreads();
   }
   {
     // the lower left 32 x 32: -X[32.., 32..] (L[32.., ..32] X[..32, ..32])
-    const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) y = ffma4s(L[(32 + r) * kLPitch + k], lds4(&X[k * kLPitch + c]), y);
-    sts4(&Y[r * kLPitch + c], y);
+    const int m = 16 * (warp >> 2), n = 8 * (warp & 3);
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    tile_mm(c, &L[(32 + m) * kLPitch], kLPitch, &X[n], kLPitch, n / 8, 4, lane);
+    put(&Y[m * kYPitch + n], kYPitch, c, 1.f);
     __syncthreads();
-    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k)
-      z = ffma4s(-X[(32 + r) * kLPitch + 32 + k], lds4(&Y[k * kLPitch + c]), z);
-    sts4(&X[(32 + r) * kLPitch + c], z);
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+    tile_mm(z, &X[(32 + m) * kLPitch + 32], kLPitch, &Y[n], kYPitch, 0, m / 8 + 2, lane);
+    put(&X[(32 + m) * kLPitch + n], kLPitch, z, -1.f);
     __syncthreads();
   }
   // -- T = X diag(beta) ------------------------------------------------------
@@ -530,10 +604,15 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int s0 = (threadIdx.x & 3) * 16 + 8 * e;
-      float x[8];
+      float2 x[4], b[4];
+      load4x2(&X[t * kLPitch + s0], x);
+      load4x2(&sm.beta[s0], b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        x[i] = s0 + i <= t ? X[t * kLPitch + s0 + i] * (sm.beta[s0 + i] * kImgScale) : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = fmul2(x[i], fmul2(b[i], make_float2(kImgScale, kImgScale)));
+        // (what lies above the diagonal was never written)
+        x[i] = make_float2(s0 + 2 * i <= t ? v.x : 0.f, s0 + 2 * i + 1 <= t ? v.y : 0.f);
+      }
       uint4 hi, lo;
       split8(x, hi, lo);
       const uint32_t at = img_at(t, s0);
