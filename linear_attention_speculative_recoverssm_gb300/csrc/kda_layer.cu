@@ -17,6 +17,7 @@
 #include "kda_device.cuh"
 #include "kda_launch.h"
 #include "kda_tcgen05.cuh"
+#include "kda_tensor_map.h"
 
 namespace kda {
 namespace {
@@ -516,24 +517,10 @@ __global__ void __launch_bounds__(256) kda_layer_epilogue(const uint16_t *__rest
   if (valid) *reinterpret_cast<uint4 *>(out + base) = make_uint4(res[0], res[1], res[2], res[3]);
 }
 
-// cuTensorMapEncodeTiled from the driver, looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 gate_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
 // f_a [n_tokens, 128] and f_b [H*128, 128] (BF16, 256-byte rows) with a (64,
 // 128) box in the 128-byte swizzle; rows past the tensor arrive as zeros.
 int encode_gate_maps(const LayerParams &p, int n_tokens, GateMaps &maps) {
-  const auto encode = gate_map_encoder();
+  const auto encode = tensor_map_encoder();
   if (encode == nullptr) return KDA_ERR_CUDA;
   const cuuint64_t strides[1] = {(cuuint64_t)kDim * 2};
   const cuuint32_t box[2] = {(cuuint32_t)kGateKBlock, (cuuint32_t)kGateTile};

@@ -1,7 +1,7 @@
 // The chain of the chunked delta rule: one CTA takes a (request, head)
 // through its chunks, its state on the chip throughout.  Everything is
 // transposed so that a value channel v is a row: S^T [v][key channel],
-// W = (S Kd^T), U, O [v][token].  Rows never meet, a thread owns half of one,
+// W = (S Kd^T), U, O [v][token].  Rows never meet, a thread owns a quarter of one,
 // and per chunk (kda_prefill.cuh for the operands)
 //   E0  S <- S e^{G_end} + dS of the chunk before; S as FP16 parts to TMEM
 //   M1  W = S Kd^T, O = S Qd^T
@@ -10,17 +10,23 @@
 //   E2  U as FP16 parts to TMEM (over R)
 //   M3  dS = U Ke;  M4  O += U A^T
 // with M on the tensor cores (M = 128 rows, the first operand in TMEM, the
-// second the image in shared memory) and E on warps 0-7: warp w holds lanes
-// (rows) 32 (w & 3) .. and half w >> 2 of the columns.  O leaves while the
-// next chunk's M1 runs.  Warp 8 issues the MMAs, warp 9 the copies.
+// second the image in shared memory) and E on warps 0-15: warp w holds lanes
+// (rows) 32 (w & 3) .. and quarter w >> 2 of the columns.  O leaves while the
+// next chunk's M1 runs.  Warp 16 issues the MMAs, warp 17 the copies.
 //
-// FP16 parts of a row are taken times a power of two that brings the largest
-// of |S| and |v| over the row to 2^8 .. 2^9.  R is then below 12.4 2^9, and
+// FP16 parts of a row are taken times a power of two that brings M, a bound
+// of |S| and |v| over the row, to 2^8 .. 2^9.  R is then below 12.4 2^9, and
 // U below 76 2^9 < 65504 (a row of the state grows by at most beta |v| a
 // token), so one factor a chunk serves S, R, U and O, and their accumulators
-// share it.  The state itself stays in FP32, in registers: an accumulator
-// that is added to over and over loses up to a unit of its last place each
-// time, so dS is summed apart, smallest parts first.
+// share it.  M is known before dS is: the largest |S| before the chunk plus
+// 64 times the largest |U| in it (unit keys), or the largest |v| to come.
+// Where that is a few bits too much, the parts have them to spare (2^-25 of
+// values up to 2^9).  So the rows' quarters exchange their peaks while M3
+// runs, and nothing waits between dS and S but the arithmetic; M3 and M1 go
+// by halves of the key channels, E0 of the one under the other's MMAs.
+// The state itself stays in FP32, in registers: an accumulator that is added
+// to over and over loses up to a unit of its last place each time, so dS is
+// summed apart, smallest parts first.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -30,11 +36,14 @@
 #include "kda_launch.h"
 #include "kda_prefill.cuh"
 #include "kda_tcgen05.cuh"
+#include "kda_tensor_map.h"
 
 namespace kda {
 namespace {
 
-constexpr int kChainThreads = 320;  // E warps 0-7, MMA warp 8, copy warp 9
+constexpr int kRowWarps = 16;
+constexpr int kChainThreads = 32 * (kRowWarps + 2);  // and the MMA and copy warps
+constexpr int kKeys = kDim / 4, kToks = kChunk / 4;  // columns of a thread
 constexpr uint32_t kPartA = kImgTHi;                  // Kd, Qd: 48 KB
 constexpr uint32_t kPartB = kImgKeHi - kImgTHi;       // T: 16 KB
 constexpr uint32_t kPartC = kImgDecay - kImgKeHi;     // Ke, A: 40 KB
@@ -59,9 +68,9 @@ struct ChainSmem {
   uint8_t a[kPartA], b[kPartB], c[kPartC];  // each a multiple of 1024 bytes
   uint8_t v[2][kVBytes];
   float decay[2][kDim];
-  float peak[2][2][128];  // [chunk parity][column half][row]
+  float4 peak[2][4][128];  // [chunk parity][column quarter][row]: |S|, |U|, next |v|
   uint64_t a_full, a_free, b_full, b_free, c_full, c_free, v_full[2], v_free[2], d_full[2];
-  uint64_t s_ready, r_ready, u_ready, w_full, u_full, ds_full, o_full, drained;
+  uint64_t s_ready[2], r_ready, u_ready, w_full, u_full, ds_full[2], o_full, drained;
   uint32_t tmem;
 };
 static_assert(kPartA % 1024 == 0 && kPartB % 1024 == 0 && kPartC % 1024 == 0, "swizzle atoms");
@@ -73,24 +82,51 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// D[tmem] (+)= A[tmem, 128 x 16] . B[N x 16]^T
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                        bool accumulate) {
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p;
+}
+
+// D[tmem] (+)= A[tmem, 128 x 16] . B[N x 16]^T, issued by the lane with
+// `lead` while the whole warp runs along: what is the same in every lane then
+// lives in uniform registers, which the instruction takes its operands from.
+// (In a branch of one lane each operand is moved there first, some 50 cycles
+// an issue against the 32 that N = 64 takes to execute.)
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                        bool accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
+// 16 FP32 columns of this warp's lanes; waits for the load.
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 
@@ -109,21 +145,29 @@ __device__ __forceinline__ float pow2_inverse(float s) {
   return __uint_as_float((254u << 23) - __float_as_uint(s));
 }
 
-// Two values as FP16 and what that leaves.
-__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+// Two values as FP16 and what that leaves; `peak` the largest |hi| so far.
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo, __half2 &peak) {
   const __half2 h = __float22half2_rn(x);
+  peak = __hmax2(peak, __habs2(h));
   const float2 f = __half22float2(h);
   const __half2 l = __float22half2_rn(ffma2(f, make_float2(-1.f, -1.f), x));
   hi = *reinterpret_cast<const uint32_t *>(&h);
   lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
+__device__ __forceinline__ float max_of(__half2 x) {
+  const float2 f = __half22float2(x);
+  return fmaxf(f.x, f.y);
+}
+
+// A quarter row of a state page (32 key channels from 32 quarter).
 template <bool BF16>
-__device__ __forceinline__ void load_state(const void *page, int row, int half, float2 (&s)[32]) {
+__device__ __forceinline__ void load_state(const void *page, int row, int quarter,
+                                           float2 (&s)[kKeys / 2]) {
   if constexpr (BF16) {
-    const uint4 *g = reinterpret_cast<const uint4 *>(page) + row * (kDim / 8) + half * 8;
+    const uint4 *g = reinterpret_cast<const uint4 *>(page) + row * (kDim / 8) + quarter * 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const uint4 x = __ldcs(g + i);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -132,9 +176,9 @@ __device__ __forceinline__ void load_state(const void *page, int row, int half, 
                                    __uint_as_float(w[j] & 0xffff0000u));
     }
   } else {
-    const float4 *g = reinterpret_cast<const float4 *>(page) + row * (kDim / 4) + half * 16;
+    const float4 *g = reinterpret_cast<const float4 *>(page) + row * (kDim / 4) + quarter * 8;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const float4 x = __ldcs(g + i);
       s[2 * i] = make_float2(x.x, x.y);
       s[2 * i + 1] = make_float2(x.z, x.w);
@@ -143,51 +187,72 @@ __device__ __forceinline__ void load_state(const void *page, int row, int half, 
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store_state(void *page, int row, int half,
-                                            const float2 (&s)[32]) {
+__device__ __forceinline__ void store_state(void *page, int row, int quarter,
+                                            const float2 (&s)[kKeys / 2]) {
   if constexpr (BF16) {
-    uint4 *g = reinterpret_cast<uint4 *>(page) + row * (kDim / 8) + half * 8;
+    uint4 *g = reinterpret_cast<uint4 *>(page) + row * (kDim / 8) + quarter * 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
       g[i] = make_uint4(pack_bf16x2(s[4 * i].x, s[4 * i].y),
                         pack_bf16x2(s[4 * i + 1].x, s[4 * i + 1].y),
                         pack_bf16x2(s[4 * i + 2].x, s[4 * i + 2].y),
                         pack_bf16x2(s[4 * i + 3].x, s[4 * i + 3].y));
   } else {
-    float4 *g = reinterpret_cast<float4 *>(page) + row * (kDim / 4) + half * 16;
+    float4 *g = reinterpret_cast<float4 *>(page) + row * (kDim / 4) + quarter * 8;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       g[i] = make_float4(s[2 * i].x, s[2 * i].y, s[2 * i + 1].x, s[2 * i + 1].y);
   }
 }
 
-// The MMAs of one product: hi and lo parts, `steps` K = 16 steps each,
-// smallest first.  `bstep(ks)`: byte offset of step ks in an operand part.
-template <typename BDesc>
-__device__ __forceinline__ void mma_split(uint32_t d, uint32_t a_hi, uint32_t a_lo, int steps,
-                                          uint32_t idesc, BDesc hi, BDesc lo) {
-  for (int ks = 0; ks < steps; ++ks) umma_ts(d, a_lo + 8 * ks, hi(ks), idesc, ks > 0);
-  for (int ks = 0; ks < steps; ++ks) umma_ts(d, a_hi + 8 * ks, lo(ks), idesc, true);
-  for (int ks = 0; ks < steps; ++ks) umma_ts(d, a_hi + 8 * ks, hi(ks), idesc, true);
+// The MMAs of one product: hi and lo parts, STEPS K = 16 steps each, smallest
+// first.
+template <int STEPS, typename BDesc>
+__device__ __forceinline__ void mma_part(uint32_t d, uint32_t a, BDesc b, uint32_t idesc,
+                                         bool accumulate, uint32_t lead) {
+#pragma unroll
+  for (int ks = 0; ks < STEPS; ++ks)
+    umma_ts(d, a + 8 * ks, b(ks), idesc, accumulate || ks > 0, lead);
+}
+template <int STEPS, typename BDesc>
+__device__ __forceinline__ void mma_split(uint32_t d, uint32_t a_hi, uint32_t a_lo, BDesc hi,
+                                          BDesc lo, uint32_t idesc, bool accumulate,
+                                          uint32_t lead) {
+  mma_part<STEPS>(d, a_lo, hi, idesc, accumulate, lead);
+  mma_part<STEPS>(d, a_hi, lo, idesc, true, lead);
+  mma_part<STEPS>(d, a_hi, hi, idesc, true, lead);
 }
 
 // K-major parts: a K step is 32 bytes of a 128-byte row, 4 to a block.
 struct KMajor {
-  uint32_t base;
+  uint64_t desc;
+  __device__ __forceinline__ explicit KMajor(uint32_t at) : desc(umma_desc_sw128(at)) {}
   __device__ __forceinline__ uint64_t operator()(int ks) const {
-    return umma_desc_sw128(base + (uint32_t)(ks >> 2) * kImgBlock + (uint32_t)(ks & 3) * 32u);
+    return desc + (uint64_t)(((uint32_t)(ks >> 2) * kImgBlock + (uint32_t)(ks & 3) * 32u) >> 4);
+  }
+  __device__ __forceinline__ KMajor block(int i) const {  // K steps from 4 i on
+    KMajor b = *this;
+    b.desc += (uint64_t)((uint32_t)i * kImgBlock >> 4);
+    return b;
   }
 };
 // MN-major parts: a K step is 16 rows of 128 bytes.
 struct MnMajor {
-  uint32_t base;
+  uint64_t desc;
+  __device__ __forceinline__ explicit MnMajor(uint32_t at) : desc(umma_desc_mn_sw128(at)) {}
   __device__ __forceinline__ uint64_t operator()(int ks) const {
-    return umma_desc_mn_sw128(base + (uint32_t)ks * 2048u);
+    return desc + (uint64_t)((uint32_t)ks * 2048u >> 4);
+  }
+  __device__ __forceinline__ MnMajor block(int i) const {  // N from 64 i on
+    MnMajor b = *this;
+    b.desc += (uint64_t)((uint32_t)i * kImgBlock >> 4);
+    return b;
   }
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(const PrefillParams p) {
+__global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(const PrefillParams p,
+                                                                             const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ uint8_t chain_raw[];
   const int H = p.r.H;
   const int b = p.order[blockIdx.x / H], h = blockIdx.x % H;
@@ -207,15 +272,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
     mbar_init(&sm.c_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_free[i], 8);
+      mbar_init(&sm.v_free[i], kRowWarps);
       mbar_init(&sm.d_full[i], 1);
+      mbar_init(&sm.s_ready[i], kRowWarps / 2);
+      mbar_init(&sm.ds_full[i], 1);
     }
-    mbar_init(&sm.s_ready, 8);
-    mbar_init(&sm.r_ready, 8);
-    mbar_init(&sm.u_ready, 8);
+    mbar_init(&sm.r_ready, kRowWarps);
+    mbar_init(&sm.u_ready, kRowWarps);
     mbar_init(&sm.w_full, 1);
     mbar_init(&sm.u_full, 1);
-    mbar_init(&sm.ds_full, 1);
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.drained, 1);
     mbar_init_fence();
@@ -228,265 +293,311 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
   const uint8_t *images = p.images + ((long long)req.base * H + h) * kImgBytes;
   const long long img_step = (long long)H * kImgBytes;
 
-  if (warp == 9) {
+  if (warp == kRowWarps + 1) {
     // -- copies ---------------------------------------------------------------
     bool ok = true;
+    int n_v = 0, n_a = 0, n_b = 0, n_c = 0;  // copies issued of each kind
     const auto load_v = [&](int i) {
-      const PrefillChunk ck = p.chunks[req.base + i];
       uint64_t *bar = &sm.v_full[i & 1];
       if (i >= 2) ok = ok && mbar_wait_bounded(&sm.v_free[i & 1], (uint32_t)((i >> 1) - 1) & 1u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
-      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)ck.count * kDim * 2);
-      __syncwarp();
-      for (int t = lane; t < ck.count; t += 32)
-        bulk_g2s(sm.v[i & 1] + t * kDim * 2,
-                 p.r.v + ((long long)(ck.t0 + t) * H + h) * kDim, kDim * 2, bar);
+      n_v = i + 1;
+      if (lane != 0) return;
+      // 64 rows whatever the count: one copy (a copy a row took the warp some
+      // 75 cycles each); what is past it, rows of others or the zeros past the
+      // activations, is not used
+      mbar_arrive_expect_tx(bar, kVBytes);
+      tma_load_3d(sm.v[i & 1], &v_map, 0, h, p.chunks[req.base + i].t0, bar);
     };
     const auto load_part = [&](int i, uint64_t *full, uint64_t *free, uint8_t *dst, uint32_t at,
-                               uint32_t bytes) {
+                               uint32_t bytes, int &issued) {
       if (i >= 1) ok = ok && mbar_wait_bounded(free, (uint32_t)(i - 1) & 1u);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok || lane != 0) return;
+      if (!ok) return;
+      issued = i + 1;
+      if (lane != 0) return;
       mbar_arrive_expect_tx(full, bytes);
       bulk_g2s(dst, images + i * img_step + at, bytes, full);
     };
     load_v(0);
-    int issued = 0;  // parts A, B, C and the decays of chunks 0 .. issued - 1
-    int part = 0;    // and so many parts of the next one
     for (int i = 0; i < n && ok; ++i) {
-      part = 0;
-      load_part(i, &sm.a_full, &sm.a_free, sm.a, 0, kPartA);
-      if (!ok) break;
-      if (lane == 0) {
+      load_part(i, &sm.a_full, &sm.a_free, sm.a, 0, kPartA, n_a);
+      if (ok && lane == 0) {
         mbar_arrive_expect_tx(&sm.d_full[i & 1], kDim * 4);
         bulk_g2s(sm.decay[i & 1], images + i * img_step + kImgDecay, kDim * 4, &sm.d_full[i & 1]);
       }
-      part = 1;
-      load_part(i, &sm.b_full, &sm.b_free, sm.b, kPartA, kPartB);
-      if (!ok) break;
-      part = 2;
-      load_part(i, &sm.c_full, &sm.c_free, sm.c, kPartA + kPartB, kPartC);
-      if (!ok) break;
-      issued = i + 1;
-      part = 0;
-      if (i + 1 < n) load_v(i + 1);
+      if (ok && i + 1 < n) load_v(i + 1);
+      if (ok) load_part(i, &sm.b_full, &sm.b_free, sm.b, kPartA, kPartB, n_b);
+      if (ok) load_part(i, &sm.c_full, &sm.c_free, sm.c, kPartA + kPartB, kPartC, n_c);
     }
     if (!ok) {
-      // every copy issued lands before the CTA can exit: each barrier's last
-      // phase in use
+      // every copy issued lands before the CTA can exit: the last phase in
+      // use of each barrier
       if (lane == 0) report(status, KDA_ERR_TIMEOUT);
       const auto settle = [&](uint64_t *bar, int uses) {
         if (uses > 0) mbar_wait_bounded(bar, (uint32_t)(uses - 1) & 1u);
       };
-      const int a = issued + (part >= 1), bb = issued + (part >= 2);
-      settle(&sm.a_full, a);
-      settle(&sm.b_full, bb);
-      settle(&sm.c_full, issued);
-      settle(&sm.d_full[0], (a + 1) / 2);
-      settle(&sm.d_full[1], a / 2);
-      const int v = issued + 1 < n ? issued + 1 : n;  // (at most so many: a wait may run out)
-      settle(&sm.v_full[0], (v + 1) / 2);
-      settle(&sm.v_full[1], v / 2);
+      settle(&sm.a_full, n_a);
+      settle(&sm.b_full, n_b);
+      settle(&sm.c_full, n_c);
+      settle(&sm.d_full[0], (n_a + 1) / 2);
+      settle(&sm.d_full[1], n_a / 2);
+      settle(&sm.v_full[0], (n_v + 1) / 2);
+      settle(&sm.v_full[1], n_v / 2);
     }
-  } else if (warp == 8) {
-    // -- tensor cores ---------------------------------------------------------
-    if (lane == 0) {
-      bool ok = true;
-      const uint32_t a = smem_u32(sm.a), bt = smem_u32(sm.b), c = smem_u32(sm.c);
-      for (int i = 0; i < n; ++i) {
-        const uint32_t ph = (uint32_t)i & 1u;
-        const uint32_t o = tmem + kColO + 64u * ph;
-        ok = mbar_wait_bounded(&sm.a_full, ph) && mbar_wait_bounded(&sm.s_ready, ph);
+  } else if (warp == kRowWarps) {
+    // -- tensor cores: the whole warp, converged ------------------------------
+    const uint32_t lead = elect_one();
+    const auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t tm = uniform(tmem);
+    const uint32_t sa = uniform(smem_u32(sm.a)), sb = uniform(smem_u32(sm.b));
+    const uint32_t sc = uniform(smem_u32(sm.c));
+    const KMajor kd_hi(sa + kImgKdHi), kd_lo(sa + kImgKdLo), qd(sa + kImgQd);
+    const KMajor am(sc + 4 * kImgBlock), t_hi(sb), t_lo(sb + kImgBlock);
+    const MnMajor ke_hi(sc), ke_lo(sc + 2 * kImgBlock);
+    constexpr uint32_t k64 = idesc_f16(64, false), k64mn = idesc_f16(64, true);
+    const uint32_t w = tm + kColW, s_hi = tm + kColSHi, s_lo = tm + kColSLo;
+    const uint32_t r_hi = tm + kColRHi, r_lo = tm + kColRLo;
+    const auto commit = [&](uint64_t *bar) {
+      if (lead) umma_commit(bar);
+      __syncwarp();
+    };
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t ph = (uint32_t)i & 1u;
+      const uint32_t o = tm + kColO + 64u * ph;
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.a_full, ph));
+      for (int half = 0; half < 2 && ok; ++half) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.s_ready[half], ph));
         if (!ok) break;
         tc_fence_after();
-        mma_split(tmem + kColW, tmem + kColSHi, tmem + kColSLo, 8, idesc_f16(64, false),
-                  KMajor{a + kImgKdHi}, KMajor{a + kImgKdLo});
-        umma_commit(&sm.w_full);
-        for (int ks = 0; ks < 8; ++ks)
-          umma_ts(o, tmem + kColSHi + 8 * ks, KMajor{a + kImgQd}(ks), idesc_f16(64, false),
-                  ks > 0);
-        umma_commit(&sm.a_free);
-        ok = mbar_wait_bounded(&sm.b_full, ph) && mbar_wait_bounded(&sm.r_ready, ph);
-        if (!ok) break;
-        tc_fence_after();
-        mma_split(tmem + kColW, tmem + kColRHi, tmem + kColRLo, 4, idesc_f16(64, false),
-                  KMajor{bt}, KMajor{bt + kImgBlock});
-        umma_commit(&sm.u_full);
-        umma_commit(&sm.b_free);
-        ok = mbar_wait_bounded(&sm.c_full, ph) && mbar_wait_bounded(&sm.u_ready, ph);
-        if (!ok) break;
-        tc_fence_after();
-        mma_split(tmem + kColDs, tmem + kColRHi, tmem + kColRLo, 4, idesc_f16(128, true),
-                  MnMajor{c}, MnMajor{c + 2 * kImgBlock});
-        umma_commit(&sm.ds_full);
-        for (int ks = 0; ks < 4; ++ks)
-          umma_ts(o, tmem + kColRHi + 8 * ks, KMajor{c + 4 * kImgBlock}(ks),
-                  idesc_f16(64, false), true);
-        umma_commit(&sm.o_full);
-        umma_commit(&sm.c_free);
+        const uint32_t at = 32u * half;  // four K steps of TMEM columns
+        mma_split<4>(w, s_hi + at, s_lo + at, kd_hi.block(half), kd_lo.block(half), k64, half > 0,
+                     lead);
       }
-      if (!ok) report(status, KDA_ERR_TIMEOUT);
-      // nothing of this CTA's is in flight when its columns are released
-      umma_commit(&sm.drained);
-      mbar_wait_bounded(&sm.drained, 0u);
+      if (!ok) break;
+      commit(&sm.w_full);
+      mma_part<8>(o, s_hi, qd, k64, false, lead);
+      commit(&sm.a_free);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.b_full, ph) &&
+                                       mbar_wait_bounded(&sm.r_ready, ph));
+      if (!ok) break;
+      tc_fence_after();
+      mma_split<4>(w, r_hi, r_lo, t_hi, t_lo, k64, false, lead);
+      commit(&sm.u_full);
+      commit(&sm.b_free);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.c_full, ph) &&
+                                       mbar_wait_bounded(&sm.u_ready, ph));
+      if (!ok) break;
+      tc_fence_after();
+      for (int half = 0; half < 2; ++half) {
+        mma_split<4>(tm + kColDs + 64u * half, r_hi, r_lo, ke_hi.block(half), ke_lo.block(half),
+                     k64mn, false, lead);
+        commit(&sm.ds_full[half]);
+      }
+      mma_part<4>(o, r_hi, am, k64, true, lead);
+      commit(&sm.o_full);
+      commit(&sm.c_free);
     }
+    if (!ok && lead) report(status, KDA_ERR_TIMEOUT);
+    // nothing of this CTA's is in flight when its columns are released
+    commit(&sm.drained);
+    mbar_wait_bounded(&sm.drained, 0u);
   } else {
     // -- rows -------------------------------------------------------------------
-    const int row = 32 * (warp & 3) + lane, hf = warp >> 2;
+    const int row = 32 * (warp & 3) + lane, qt = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const long long elem = BF16 ? 2 : 4;
     char *pool = reinterpret_cast<char *>(p.r.state) + (long long)h * kDim * kDim * elem;
     const long long slot_bytes = p.r.slot_stride * elem;
     const PromptRequest rq = prompt_request(p.r.maps, b);
-    float2 s[32];  // this row's key channels 64 hf .. 64 hf + 63
+    float2 s[kKeys / 2];  // this row's key channels 32 qt .. 32 qt + 31
     if (rq.src >= 0) {
-      load_state<BF16>(pool + rq.src * slot_bytes, row, hf, s);
+      load_state<BF16>(pool + rq.src * slot_bytes, row, qt, s);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < kKeys / 2; ++i) s[i] = make_float2(0.f, 0.f);
     }
     constexpr float kDown = 1.f / kImgScale;
-    float inv = 0.f;  // 1 / the chunk before's row scale
-    int t0 = 0, count = 0;
+    const auto f2 = [](uint32_t x, uint32_t y) {
+      return make_float2(__uint_as_float(x), __uint_as_float(y));
+    };
+    const auto both = [](float x) { return make_float2(x, x); };
+    const int half = qt >> 1;
     bool bad = false;
-    // S <- S e^{G_end} + dS of chunk i
+    const auto wait = [&](uint64_t *bar, uint32_t parity) {
+      bad = __any_sync(0xffffffffu, bad || !mbar_wait_bounded(bar, parity));
+      return !bad;
+    };
+    // v of chunk i: this row's tokens 16 qt .. 16 qt + 15, and their peak
+    uint32_t v2[kToks / 2];
+    const auto load_v = [&](int i, int count) {
+      if (!wait(&sm.v_full[i & 1], (uint32_t)(i >> 1) & 1u)) return 0.f;
+      const uint16_t *v = reinterpret_cast<const uint16_t *>(sm.v[i & 1]) + kToks * qt * kDim + row;
+      const int left = count - kToks * qt;
+      if (left >= kToks) {
+#pragma unroll
+        for (int j = 0; j < kToks / 2; ++j)
+          v2[j] = (uint32_t)v[2 * j * kDim] | ((uint32_t)v[(2 * j + 1) * kDim] << 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kToks / 2; ++j) {
+          const uint32_t x = 2 * j < left ? v[2 * j * kDim] : 0u;
+          v2[j] = x | (2 * j + 1 < left ? (uint32_t)v[(2 * j + 1) * kDim] << 16 : 0u);
+        }
+      }
+      __nv_bfloat162 peak = __float2bfloat162_rn(0.f);
+#pragma unroll
+      for (int j = 0; j < kToks / 2; ++j)
+        peak = __hmax2(peak, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v2[j])));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_free[i & 1]);
+      return fmaxf(__low2float(peak), __high2float(peak));
+    };
+    // this row's scale from its quarters' peaks
+    const auto scale_of = [&](int i) {
+      float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 x = sm.peak[i & 1][j][row];
+        m = make_float4(fmaxf(m.x, x.x), fmaxf(m.y, x.y), fmaxf(m.z, x.z), 0.f);
+      }
+      return row_scale(fmaxf(fmaf(64.f, m.y, m.x), m.z));
+    };
+    // chunk i, i + 1 and i + 2: loaded two chunks ahead
+    PrefillChunk ck = p.chunks[req.base], next = p.chunks[req.base + min(1, n - 1)];
+    float peak_s = 0.f;  // largest |S| of this quarter row
+#pragma unroll
+    for (int e = 0; e < kKeys / 2; ++e)
+      peak_s = fmaxf(peak_s, fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
+    sm.peak[1][qt][row] = make_float4(peak_s, 0.f, load_v(0, ck.count), 0.f);
+    bad = named_bar_or(1, 32 * kRowWarps, bad);
+    float scale = scale_of(1), inv = pow2_inverse(scale);
+    // S <- S e^{G_end} + dS of chunk i, whose scale is 1 / inv
     const auto advance = [&](int i) {
-      bad = bad || !mbar_wait_bounded(&sm.d_full[i & 1], (uint32_t)(i >> 1) & 1u) ||
-            !mbar_wait_bounded(&sm.ds_full, (uint32_t)i & 1u);
-      bad = __any_sync(0xffffffffu, bad);
-      if (bad) return;
+      if (!wait(&sm.d_full[i & 1], (uint32_t)(i >> 1) & 1u) ||
+          !wait(&sm.ds_full[half], (uint32_t)i & 1u))
+        return;
       tc_fence_after();
-      const float2 f = make_float2(inv * kDown, inv * kDown);
-      const float *dec = sm.decay[i & 1] + 64 * hf;
+      const float2 f = both(inv * kDown);
+      const float *dec = sm.decay[i & 1] + kKeys * qt;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        uint32_t d[32];
-        tmem_load32(lanes + kColDs + 64u * hf + 32u * j, d);
+        uint32_t d[16];
+        tmem_load16(lanes + kColDs + (uint32_t)(kKeys * qt + 16 * j), d);
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float4 g = lds4(dec + 32 * j + 2 * e);
-          float2 &x = s[16 * j + e], &y = s[16 * j + e + 1];
-          x = ffma2(x, make_float2(g.x, g.y),
-                    fmul2(f, make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]))));
-          y = ffma2(y, make_float2(g.z, g.w),
-                    fmul2(f, make_float2(__uint_as_float(d[2 * e + 2]),
-                                         __uint_as_float(d[2 * e + 3]))));
+        for (int e = 0; e < 8; e += 2) {
+          const float4 g = lds4(dec + 16 * j + 2 * e);
+          float2 &x = s[8 * j + e], &y = s[8 * j + e + 1];
+          x = ffma2(x, make_float2(g.x, g.y), fmul2(f, f2(d[2 * e], d[2 * e + 1])));
+          y = ffma2(y, make_float2(g.z, g.w), fmul2(f, f2(d[2 * e + 2], d[2 * e + 3])));
         }
       }
     };
-    // the outputs of chunk i (at t0, count: still that chunk's)
-    const auto emit = [&](int i, int t0, int count) {
-      bad = bad || !mbar_wait_bounded(&sm.o_full, (uint32_t)i & 1u);
-      bad = __any_sync(0xffffffffu, bad);
-      if (bad) return;
+    // the outputs of chunk i (tokens t0 .. t0 + count - 1)
+    const auto emit = [&](int i, int t0, int count, float inv) {
+      if (!wait(&sm.o_full, (uint32_t)i & 1u)) return;
       tc_fence_after();
-      uint32_t d[32];
-      tmem_load32(lanes + kColO + 64u * (i & 1) + 32u * hf, d);
+      uint32_t d[16];
+      tmem_load16(lanes + kColO + 64u * (i & 1) + (uint32_t)(kToks * qt), d);
       const float f = p.r.q_scale * kDown * inv;
-      uint16_t *o = p.r.out + ((long long)(t0 + 32 * hf) * H + h) * kDim + row;
-      const int left = count - 32 * hf;
+      const uint32_t step = (uint32_t)H * kDim;
+      uint16_t *o = p.r.out + (long long)(t0 + kToks * qt) * step + h * kDim + row;
+      const int left = count - kToks * qt;
+      if (left >= kToks) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < left) o[(long long)j * H * kDim] = f32_to_bf16_bits(__uint_as_float(d[j]) * f);
-    };
-    for (int i = 0; i < n; ++i) {
-      const PrefillChunk ck = p.chunks[req.base + i];
-      // v of the chunk: this row's tokens 32 hf .. 32 hf + 31
-      uint32_t v2[16];
-      float peak = 0.f;
-      bad = bad || !mbar_wait_bounded(&sm.v_full[i & 1], (uint32_t)(i >> 1) & 1u);
-      {
-        const uint16_t *v = reinterpret_cast<const uint16_t *>(sm.v[i & 1]) + 32 * hf * kDim + row;
-        const int left = ck.count - 32 * hf;
+        for (int j = 0; j < kToks; ++j)
+          o[j * step] = f32_to_bf16_bits(__uint_as_float(d[j]) * f);
+      } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t x = 2 * j < left ? v[2 * j * kDim] : 0u;
-          const uint32_t y = 2 * j + 1 < left ? v[(2 * j + 1) * kDim] : 0u;
-          v2[j] = x | (y << 16);
-          peak = fmaxf(peak, fmaxf(fabsf(__uint_as_float(x << 16)),
-                                   fabsf(__uint_as_float(y << 16))));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_free[i & 1]);
+        for (int j = 0; j < kToks; ++j)
+          if (j < left) o[j * step] = f32_to_bf16_bits(__uint_as_float(d[j]) * f);
       }
+    };
+    int t0 = 0, count = 0;  // the chunk before's
+    float inv_before = 0.f;
+    for (int i = 0; i < n; ++i) {
+      const PrefillChunk later = p.chunks[req.base + min(i + 2, n - 1)];
       if (i > 0) {
         advance(i - 1);
-        if (i == req.bnd_chunks && !bad)
-          store_state<BF16>(pool + rq.bnd * slot_bytes, row, hf, s);
+        if (bad) break;
+        if (i == req.bnd_chunks) store_state<BF16>(pool + rq.bnd * slot_bytes, row, qt, s);
+        inv_before = inv;
+        inv = pow2_inverse(scale);  // chunk i's, from the peaks of chunk i - 1
       }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) peak = fmaxf(peak, fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
-      sm.peak[i & 1][hf][row] = peak;
-      bad = named_bar_or(1, 256, bad);
-      if (bad) break;
-      const float scale = row_scale(fmaxf(peak, sm.peak[i & 1][hf ^ 1][row]));
+      // S as parts
       {
-        const float2 f = make_float2(scale, scale);
+        const float2 f = both(scale);
+        __half2 peak = __float2half2_rn(0.f);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint32_t hi[16], lo[16];
+          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) split2(fmul2(s[16 * j + e], f), hi[e], lo[e]);
-          tmem_store16(lanes + kColSHi + 32u * hf + 16u * j, hi);
-          tmem_store16(lanes + kColSLo + 32u * hf + 16u * j, lo);
+          for (int e = 0; e < 8; ++e) split2(fmul2(s[8 * j + e], f), hi[e], lo[e], peak);
+          tmem_store8(lanes + kColSHi + 16u * qt + 8u * j, hi);
+          tmem_store8(lanes + kColSLo + 16u * qt + 8u * j, lo);
         }
+        peak_s = max_of(peak) * inv;
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.s_ready);
+        if (lane == 0) mbar_arrive(&sm.s_ready[half]);
       }
-      if (i > 0) emit(i - 1, t0, count);
-      inv = pow2_inverse(scale);
+      if (i > 0) emit(i - 1, t0, count, inv_before);
       t0 = ck.t0;
       count = ck.count;
       // R = V - W
-      bad = bad || !mbar_wait_bounded(&sm.w_full, (uint32_t)i & 1u);
-      bad = __any_sync(0xffffffffu, bad);
-      if (!bad) {
-        tc_fence_after();
-        uint32_t d[32], hi[16], lo[16];
-        tmem_load32(lanes + kColW + 32u * hf, d);
+      if (!wait(&sm.w_full, (uint32_t)i & 1u)) break;
+      tc_fence_after();
+      {
+        uint32_t d[16], hi[8], lo[8];
+        __half2 unused = __float2half2_rn(0.f);
+        tmem_load16(lanes + kColW + (uint32_t)(kToks * qt), d);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 w = make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
+        for (int j = 0; j < 8; ++j) {
           const float2 v = make_float2(__uint_as_float(v2[j] << 16),
                                        __uint_as_float(v2[j] & 0xffff0000u));
-          split2(ffma2(w, make_float2(-kDown, -kDown), fmul2(v, make_float2(scale, scale))),
-                 hi[j], lo[j]);
+          split2(ffma2(f2(d[2 * j], d[2 * j + 1]), both(-kDown), fmul2(v, both(scale))), hi[j],
+                 lo[j], unused);
         }
-        tmem_store16(lanes + kColRHi + 16u * hf, hi);
-        tmem_store16(lanes + kColRLo + 16u * hf, lo);
+        tmem_store8(lanes + kColRHi + 8u * qt, hi);
+        tmem_store8(lanes + kColRLo + 8u * qt, lo);
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.r_ready);
-        bad = !mbar_wait_bounded(&sm.u_full, (uint32_t)i & 1u);
       }
+      ck = next;
+      next = later;
+      const float peak_v = i + 1 < n ? load_v(i + 1, ck.count) : 0.f;
       // U
-      bad = __any_sync(0xffffffffu, bad);
-      if (!bad) {
-        tc_fence_after();
-        uint32_t d[32], hi[16], lo[16];
-        tmem_load32(lanes + kColW + 32u * hf, d);
+      if (!wait(&sm.u_full, (uint32_t)i & 1u)) break;
+      tc_fence_after();
+      {
+        uint32_t d[16], hi[8], lo[8];
+        tmem_load16(lanes + kColW + (uint32_t)(kToks * qt), d);
+        __half2 peak = __float2half2_rn(0.f);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          split2(fmul2(make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])),
-                       make_float2(kDown, kDown)),
-                 hi[j], lo[j]);
-        tmem_store16(lanes + kColRHi + 16u * hf, hi);
-        tmem_store16(lanes + kColRLo + 16u * hf, lo);
+        for (int j = 0; j < 8; ++j)
+          split2(fmul2(f2(d[2 * j], d[2 * j + 1]), both(kDown)), hi[j], lo[j], peak);
+        tmem_store8(lanes + kColRHi + 8u * qt, hi);
+        tmem_store8(lanes + kColRLo + 8u * qt, lo);
+        sm.peak[i & 1][qt][row] = make_float4(peak_s, max_of(peak) * inv, peak_v, 0.f);
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.u_ready);
       }
+      // (every row's peaks are there once all warps have arrived)
+      if (!wait(&sm.u_ready, (uint32_t)i & 1u)) break;
+      scale = scale_of(i);
     }
     if (!bad) advance(n - 1);
     if (!bad) {
-      if (n == req.bnd_chunks) store_state<BF16>(pool + rq.bnd * slot_bytes, row, hf, s);
-      store_state<BF16>(pool + rq.dst * slot_bytes, row, hf, s);
-      emit(n - 1, t0, count);
+      if (n == req.bnd_chunks) store_state<BF16>(pool + rq.bnd * slot_bytes, row, qt, s);
+      store_state<BF16>(pool + rq.dst * slot_bytes, row, qt, s);
+      emit(n - 1, t0, count, inv);
     }
     if (bad && lane == 0) report(status, KDA_ERR_TIMEOUT);
   }
@@ -518,9 +629,23 @@ int launch_prefill_chain(const PrefillParams &p, bool bf16, cudaStream_t stream)
       return KDA_ERR_CUDA;
     configured.fetch_or(bit);
   }
+  // v [n_tokens, H, 128] as a 3-D tensor, a chunk's rows of one head a copy
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return KDA_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)kDim, (cuuint64_t)p.r.H,
+                              (cuuint64_t)p.r.maps.n_tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)kDim * 2, (cuuint64_t)p.r.H * kDim * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)kDim, 1, (cuuint32_t)kChunk};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  CUtensorMap v_map;
+  if (encode(&v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(p.r.v), dims,
+             strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+      CUDA_SUCCESS)
+    return KDA_ERR_CUDA;
   const unsigned grid = (unsigned)(p.r.maps.B * p.r.H);
-  if (bf16) kda_prefill_chain_kernel<true><<<grid, kChainThreads, kSmem, stream>>>(p);
-  else kda_prefill_chain_kernel<false><<<grid, kChainThreads, kSmem, stream>>>(p);
+  if (bf16) kda_prefill_chain_kernel<true><<<grid, kChainThreads, kSmem, stream>>>(p, v_map);
+  else kda_prefill_chain_kernel<false><<<grid, kChainThreads, kSmem, stream>>>(p, v_map);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -12,22 +12,9 @@
 #include "kda_step.cuh"
 #include "kda_step_cluster.cuh"
 #include "kda_step_ws.cuh"
+#include "kda_tensor_map.h"
 
 namespace kda {
-
-// cuTensorMapEncodeTiled from the driver, looked up once.
-inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
 
 // The four token-major inputs [n_tokens, H, 128] (BF16) as 3-D tensors (128,
 // H, n_tokens) with a (128, 1, Q) box: one item's window rows per copy (rows
