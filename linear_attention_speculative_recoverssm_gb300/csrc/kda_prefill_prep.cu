@@ -45,7 +45,8 @@ struct PrepSmem {
   union {
     struct {
       // (before they hold operands, x16_hi and x16_lo hold the log2 decay
-      // sums: of a 16-byte piece's eight channels the first and last four)
+      // sums of each half block: of a 16-byte piece's eight channels the first
+      // and last four)
       uint8_t x16_hi[kXBytes], x16_lo[kXBytes], x32_hi[kXBytes], x32_lo[kXBytes];
       uint8_t y16[kYBytes], y32[kYBytes];
     } x;
@@ -96,6 +97,10 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -191,39 +196,49 @@ __device__ __forceinline__ uint32_t img_at(int t, int c) {
 __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const PrefillParams p) {
   extern __shared__ __align__(16) uint8_t prep_raw[];
   PrepSmem &sm = *reinterpret_cast<PrepSmem *>(prep_raw);
-  const int chunk = blockIdx.x / p.r.H, h = blockIdx.x - chunk * p.r.H;
-  if (chunk >= *p.n_chunks) return;
-  const PrefillChunk ck = p.chunks[chunk];
-  uint8_t *img = p.images + ((long long)chunk * p.r.H + h) * kImgBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_items = *p.n_chunks * p.r.H;
+  // CTAs stay, two to an SM, and fetch the next item's rows into L2 while
+  // they work on this one: without that the loads took a fifth of an item.
+  int chunk = blockIdx.x / p.r.H;
+  PrefillChunk next = p.chunks[chunk < p.max_chunks ? chunk : 0];
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+  const PrefillChunk ck = next;
+  const int h = item - chunk * p.r.H;
+  uint8_t *img = p.images + (long long)item * kImgBytes;
+  const int next_item = item + gridDim.x;
+  chunk = next_item / p.r.H;
+  if (next_item < n_items) next = p.chunks[chunk];
   const int blk = warp >> 1, hf = warp & 1, g = lane >> 2, tig = lane & 3;
   const int row[2] = {16 * blk + g, 16 * blk + g + 8};
   const int ch0 = hf * 64 + tig * 8;  // slices add 0 and 32
 
+  // Rows past the chunk's tokens take its last token's inputs (their own may
+  // be another request's) and get no weight: decay 1, kn = qn = 0, beta = 0.
+  const int last = ck.count - 1;
+  const uint32_t row_step = (uint32_t)p.r.H * kDim;
+  const long long head0 = ((long long)ck.t0 * p.r.H + h) * kDim;
   uint4 kraw[2][2], qraw[2][2];  // [slice][token]
 #pragma unroll
-  for (int sl = 0; sl < 2; ++sl)
+  for (int r = 0; r < 2; ++r) {
+    const uint32_t at = (uint32_t)min(row[r], last) * row_step + (uint32_t)ch0;
+    const uint16_t *k = p.r.k + head0 + at, *q = p.r.q + head0 + at;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      kraw[sl][r] = qraw[sl][r] = make_uint4(0, 0, 0, 0);
-      if (row[r] < ck.count) {
-        const long long at = ((long long)(ck.t0 + row[r]) * p.r.H + h) * kDim + ch0 + 32 * sl;
-        kraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(p.r.k + at));
-        qraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(p.r.q + at));
-      }
+    for (int sl = 0; sl < 2; ++sl) {
+      kraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(k + 32 * sl));
+      qraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(q + 32 * sl));
     }
+  }
   // -- log2 decays and their sums around the block's middle: a thread takes
   //    two channels and the block's 16 tokens in turn -------------------------
   {
     const int pr = threadIdx.x & 63, c = 2 * pr;
     uint32_t graw[16];
+    const uint16_t *gp = p.r.g + head0 + c;
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      graw[t] = 0;
-      if (16 * blk + t < ck.count)
-        graw[t] = __ldg(reinterpret_cast<const uint32_t *>(
-            p.r.g + ((long long)(ck.t0 + 16 * blk + t) * p.r.H + h) * kDim + c));
-    }
+    for (int t = 0; t < 16; ++t)
+      graw[t] = __ldg(reinterpret_cast<const uint32_t *>(
+          gp + (uint32_t)min(16 * blk + t, last) * row_step));
     if (threadIdx.x < kChunk) {
       float b = 0.f;
       if ((int)threadIdx.x < ck.count)
@@ -234,28 +249,23 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
     const float al = expf(p.r.A_log[h]) * kLog2e, lb2 = p.r.lower_bound * kLog2e;
     const float2 dt = *reinterpret_cast<const float2 *>(p.r.dt_bias + h * kDim + c);
     const float2 off = make_float2(-al * dt.x, -al * dt.y), nal = make_float2(-al, -al);
-    float2 x[16], sum = make_float2(0.f, 0.f), mid = sum;
+    // each half of the block is summed from its own start
+    uint8_t *to = ((pr & 2) ? sm.u.x.x16_lo : sm.u.x.x16_hi) + (pr & 1) * 8 + 16 * blk * kXPitch;
+    const uint32_t at = x_at(0, pr >> 2);
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      const float2 z = ffma2(nal, bf16x2_f32(graw[t]), off);
-      if (16 * blk + t < ck.count) {
-        sum.x += lb2 * __fdividef(1.f, 1.f + exp2f_fast(z.x));
-        sum.y += lb2 * __fdividef(1.f, 1.f + exp2f_fast(z.y));
+    for (int r = 0; r < 2; ++r) {
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = 8 * r + i;
+        const float2 z = ffma2(nal, bf16x2_f32(graw[t]), off);
+        const float w = 16 * blk + t < ck.count ? lb2 : 0.f;
+        sum.x += __fdividef(w, 1.f + exp2f_fast(z.x));
+        sum.y += __fdividef(w, 1.f + exp2f_fast(z.y));
+        *reinterpret_cast<float2 *>(to + (at ^ x_at(i, 0) ^ (i * kXPitch)) + t * kXPitch) = sum;
       }
-      x[t] = sum;
-      if (t == 7) {
-        mid = sum;
-        sum = make_float2(0.f, 0.f);
-      }
+      *reinterpret_cast<float2 *>(&sm.tot[r][blk][c]) = sum;
     }
-    // (the halves are summed apart: tokens 8 .. 15 start from the middle)
-    uint8_t *to = ((pr & 2) ? sm.u.x.x16_lo : sm.u.x.x16_hi) + (pr & 1) * 8;
-#pragma unroll
-    for (int t = 0; t < 16; ++t)
-      *reinterpret_cast<float2 *>(to + x_at(16 * blk + t, pr >> 2)) =
-          t < 8 ? make_float2(x[t].x - mid.x, x[t].y - mid.y) : x[t];
-    *reinterpret_cast<float2 *>(&sm.tot[0][blk][c]) = mid;
-    *reinterpret_cast<float2 *>(&sm.tot[1][blk][c]) = sum;
   }
   // -- norms: sums of squares over this warp's channels ----------------------
 #pragma unroll
@@ -330,28 +340,53 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
   for (int r = 0; r < 2; ++r) {
     rk[r] = rsqrtf(sm.norm[0][row[r]][0] + sm.norm[1][row[r]][0] + kNormEps);
     rq[r] = rsqrtf(sm.norm[0][row[r]][1] + sm.norm[1][row[r]][1] + kNormEps);
+    if (row[r] > last) rk[r] = rq[r] = 0.f;
   }
   __syncthreads();
 
+  if (next_item < n_items) {
+    // 64 rows of 256 bytes of q, k and raw_g: two lines each
+    const long long at = ((long long)next.t0 * p.r.H + (next_item - chunk * p.r.H)) * kDim;
+    const int t = threadIdx.x >> 1;
+    if (t < next.count) {
+      const long long line = at + (long long)t * row_step + (threadIdx.x & 1) * 64;
+      prefetch_l2(p.r.k + line);
+      prefetch_l2(p.r.q + line);
+      prefetch_l2(p.r.g + line);
+    }
+  }
   // -- the block's own products, and the operands of everything else ---------
   float dk[2][4], dq[2][4];  // [n-tile] 16 x 8 of kn kn^T and qn kn^T
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) dk[n][i] = dq[n][i] = 0.f;
+  // Token g's places; token g + 8 lies 8 rows further, and slice 1 four pieces
+  // on, which flips bit 6 of the permuted place.
+  const uint32_t img0 = img_at(row[0], ch0), x0 = x_at(row[0], ch0 >> 3);
+  const uint32_t y16_0 = x_at((blk >> 1) * 16 + g, ch0 >> 3);
+  const uint32_t y32_0 = x_at((blk & 1) * 16 + g, ch0 >> 3);
 #pragma unroll
   for (int sl = 0; sl < 2; ++sl) {
-    const int c = ch0 + 32 * sl, piece = c >> 3;
+    const int c = ch0 + 32 * sl;
+    uint8_t *const im = img + (img0 ^ (64u * sl));
+    const uint32_t xs = x0 ^ (64u * sl);
     float2 kf[2][4], kg[2][4], qf[2][4];  // kn 2^(G - mid), kn 2^(mid - G), qn 2^(G - mid)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float2 k[4], q[4];
       unpack4x2(kraw[sl][r], k);
       unpack4x2(qraw[sl][r], q);
-      const float4 d0 = *reinterpret_cast<const float4 *>(sm.u.x.x16_hi + x_at(row[r], piece));
-      const float4 d1 = *reinterpret_cast<const float4 *>(sm.u.x.x16_lo + x_at(row[r], piece));
-      const float2 d[4] = {make_float2(d0.x, d0.y), make_float2(d0.z, d0.w),
-                           make_float2(d1.x, d1.y), make_float2(d1.z, d1.w)};
+      const float4 d0 = *reinterpret_cast<const float4 *>(sm.u.x.x16_hi + xs + 8 * r * kXPitch);
+      const float4 d1 = *reinterpret_cast<const float4 *>(sm.u.x.x16_lo + xs + 8 * r * kXPitch);
+      float2 d[4] = {make_float2(d0.x, d0.y), make_float2(d0.z, d0.w), make_float2(d1.x, d1.y),
+                     make_float2(d1.z, d1.w)};
+      if (r == 0) {
+        float2 mid[4];
+        load4x2(&sm.tot[0][blk][c], mid);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = make_float2(d[e].x - mid[e].x, d[e].y - mid[e].y);
+      }
       const float2 rk2 = make_float2(rk[r], rk[r]), rq2 = make_float2(rq[r], rq[r]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -386,53 +421,71 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
         mma_tf32(dq[n], aq, h0, h1);
       }
     }
-    float2 facR[4], facC[4], facE[4];
-    load4x2(&sm.fac[0][blk][c], facR);
-    load4x2(&sm.fac[1][blk][c], facC);
-    load4x2(&sm.fac[2][blk][c], facE);
-    const uint4 pow0 = *reinterpret_cast<const uint4 *>(&sm.pow[0][blk][c]);
     const uint4 pow32 = *reinterpret_cast<const uint4 *>(&sm.pow[1][blk][c]);
+    const auto times = [](const float2 (&x)[4], const float2 (&f)[4], float2 (&y)[4]) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float2 x[4];
-      uint4 rh, rl, hi, lo;
-      const uint32_t at = img_at(row[r], c), xat = x_at(row[r], piece);
+      for (int e = 0; e < 4; ++e) y[e] = fmul2(x[e], f[e]);
+    };
+    const auto put = [](uint8_t *at, uint4 x) { *reinterpret_cast<uint4 *>(at) = x; };
+    {
+      float2 fac[4], x[4];
+      uint4 hi, lo;
+      load4x2(&sm.fac[2][blk][c], fac);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = fmul2(kg[r][e], facE[e]);
-      split8(x, hi, lo);
-      *reinterpret_cast<uint4 *>(img + kImgKeHi + at) = hi;
-      *reinterpret_cast<uint4 *>(img + kImgKeLo + at) = lo;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = fmul2(kf[r][e], facR[e]);
-      split8(x, rh, rl);
-      *reinterpret_cast<uint4 *>(img + kImgKdHi + at) = blk == 0 ? rh : scale8(rh, pow0);
-      *reinterpret_cast<uint4 *>(img + kImgKdLo + at) = blk == 0 ? rl : scale8(rl, pow0);
-      if (blk < 3) {  // (block 3 is no column)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = fmul2(kg[r][e], facC[e]);
+      for (int r = 0; r < 2; ++r) {
+        times(kg[r], fac, x);
         split8(x, hi, lo);
+        put(im + 1024 * r + kImgKeHi, hi);
+        put(im + 1024 * r + kImgKeLo, lo);
       }
-      *reinterpret_cast<uint4 *>(sm.u.x.x16_hi + xat) = (blk & 1) ? rh : hi;
-      *reinterpret_cast<uint4 *>(sm.u.x.x16_lo + xat) = (blk & 1) ? rl : lo;
-      if (blk >= 2) {
-        hi = rh;
-        lo = rl;
-      }
-      if (blk == 0 || blk == 3) {
-        hi = scale8(hi, pow32);
-        lo = scale8(lo, pow32);
-      }
-      *reinterpret_cast<uint4 *>(sm.u.x.x32_hi + xat) = hi;
-      *reinterpret_cast<uint4 *>(sm.u.x.x32_lo + xat) = lo;
+    }
+    if (blk < 3) {  // columns: of the border at 16 / 48 (even blocks), at 32 (0 and 1)
+      float2 fac[4], x[4];
+      uint4 hi, lo;
+      load4x2(&sm.fac[1][blk][c], fac);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = fmul2(qf[r][e], facR[e]);
-      hi = half8(x);
-      *reinterpret_cast<uint4 *>(img + kImgQd + at) = blk == 0 ? hi : scale8(hi, pow0);
-      if (blk & 1)
-        *reinterpret_cast<uint4 *>(sm.u.x.y16 + x_at((blk >> 1) * 16 + g + 8 * r, piece)) = hi;
-      if (blk >= 2)
-        *reinterpret_cast<uint4 *>(sm.u.x.y32 + x_at((blk - 2) * 16 + g + 8 * r, piece)) =
-            blk == 2 ? hi : scale8(hi, pow32);
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t xat = xs + 8 * r * kXPitch;
+        times(kg[r], fac, x);
+        split8(x, hi, lo);
+        if (!(blk & 1)) {
+          put(sm.u.x.x16_hi + xat, hi);
+          put(sm.u.x.x16_lo + xat, lo);
+        }
+        if (blk < 2) {
+          put(sm.u.x.x32_hi + xat, blk == 0 ? scale8(hi, pow32) : hi);
+          put(sm.u.x.x32_lo + xat, blk == 0 ? scale8(lo, pow32) : lo);
+        }
+      }
+    }
+    {  // rows: of the chunk's start, of 16 / 48 (odd blocks), of 32 (2 and 3)
+      float2 fac[4], x[4];
+      uint4 hi, lo;
+      load4x2(&sm.fac[0][blk][c], fac);
+      const uint4 pow0 = *reinterpret_cast<const uint4 *>(&sm.pow[0][blk][c]);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t xat = xs + 8 * r * kXPitch;
+        times(kf[r], fac, x);
+        split8(x, hi, lo);
+        put(im + 1024 * r + kImgKdHi, blk == 0 ? hi : scale8(hi, pow0));
+        put(im + 1024 * r + kImgKdLo, blk == 0 ? lo : scale8(lo, pow0));
+        if (blk & 1) {
+          put(sm.u.x.x16_hi + xat, hi);
+          put(sm.u.x.x16_lo + xat, lo);
+        }
+        if (blk >= 2) {
+          put(sm.u.x.x32_hi + xat, blk == 3 ? scale8(hi, pow32) : hi);
+          put(sm.u.x.x32_lo + xat, blk == 3 ? scale8(lo, pow32) : lo);
+        }
+        times(qf[r], fac, x);
+        hi = half8(x);
+        put(im + 1024 * r + kImgQd, blk == 0 ? hi : scale8(hi, pow0));
+        if (blk & 1) put(sm.u.x.y16 + (y16_0 ^ (64u * sl)) + 8 * r * kXPitch, hi);
+        if (blk >= 2)
+          put(sm.u.x.y32 + (y32_0 ^ (64u * sl)) + 8 * r * kXPitch,
+              blk == 3 ? scale8(hi, pow32) : hi);
+      }
     }
   }
   if (hf == 1) {
@@ -472,16 +525,19 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
     }
     const int ar = lane & 15, br = (lane & 7) + ((lane >> 4) << 3);
     const uint32_t ah0 = smem_u32(xh), al0 = smem_u32(xl), aq0 = smem_u32(y);
-#pragma unroll 2
+    // (K step ks: pieces 2 ks and 2 ks + 1 of the rows, bits 5 and 6 of the
+    // permuted place within a half)
+    const uint32_t a0 = x_at(r0 + ar, lane >> 4), b0 = x_at(c0 + br, (lane >> 3) & 1);
+    const uint32_t q0 = x_at(y0 + ar, lane >> 4);
+#pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       uint32_t ah[4], al[4], aq[4], bh[4], bl[4];
-      const uint32_t at = x_at(r0 + ar, 2 * ks + (lane >> 4));
-      const uint32_t bt = x_at(c0 + br, 2 * ks + ((lane >> 3) & 1));
-      ldmatrix4(ah, ah0 + at);
-      ldmatrix4(al, al0 + at);
-      ldmatrix4(aq, aq0 + x_at(y0 + ar, 2 * ks + (lane >> 4)));
-      ldmatrix4(bh, ah0 + bt);
-      ldmatrix4(bl, al0 + bt);
+      const uint32_t flip = 32u * (ks & 3), half = 128u * (ks >> 2);
+      ldmatrix4(ah, ah0 + (a0 ^ flip) + half);
+      ldmatrix4(al, al0 + (a0 ^ flip) + half);
+      ldmatrix4(aq, aq0 + (q0 ^ flip) + half);
+      ldmatrix4(bh, ah0 + (b0 ^ flip) + half);
+      ldmatrix4(bl, al0 + (b0 ^ flip) + half);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         mma_f16(ok[n], al, bh[2 * n], bh[2 * n + 1]);
@@ -506,8 +562,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
       for (int i = 0; i < 4; i += 2) {
         const int t = r0 + g + 4 * i, s = c0 + 8 * n + 2 * tig;
         const float b = sm.beta[t] * kUnit;
-        L[t * kLPitch + s] = b * ok[n][i];
-        L[t * kLPitch + s + 1] = b * ok[n][i + 1];
+        *reinterpret_cast<float2 *>(&L[t * kLPitch + s]) =
+            make_float2(b * ok[n][i], b * ok[n][i + 1]);
         put_a(t, s, oq[n][i] * (kImgScale * kUnit), oq[n][i + 1] * (kImgScale * kUnit));
       }
   }
@@ -600,10 +656,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
   }
   // -- T = X diag(beta) ------------------------------------------------------
   {
-    const int t = threadIdx.x >> 2;
+    const int t = threadIdx.x & 63;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int s0 = (threadIdx.x & 3) * 16 + 8 * e;
+      const int s0 = (threadIdx.x >> 6) * 16 + 8 * e;
       float2 x[4], b[4];
       load4x2(&X[t * kLPitch + s0], x);
       load4x2(&sm.beta[s0], b);
@@ -619,6 +675,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
       *reinterpret_cast<uint4 *>(img + kImgTHi + at) = hi;
       *reinterpret_cast<uint4 *>(img + kImgTLo + at) = lo;
     }
+  }
+  __syncthreads();  // the next item's operands take the place of X
   }
 }
 
@@ -636,8 +694,10 @@ int launch_prefill_prep(const PrefillParams &p, cudaStream_t stream) {
     configured.fetch_or(bit);
   }
   static_assert(2 * (sizeof(PrepSmem) + 1024) <= 228 * 1024, "two CTAs per SM");
-  kda_prefill_prep_kernel<<<(unsigned)(p.max_chunks * p.r.H), kPrepThreads, sizeof(PrepSmem),
-                            stream>>>(p);
+  const long long items = (long long)p.max_chunks * p.r.H;
+  const long long room = 2LL * device_sm_count(dev);
+  kda_prefill_prep_kernel<<<(unsigned)(items < room ? items : room), kPrepThreads,
+                            sizeof(PrepSmem), stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
