@@ -28,6 +28,7 @@
 #include "../../include/kda_recoverssm.h"
 #include "kda_launch.h"
 #include "kda_prefill.cuh"
+#include "kda_tensor_map.h"
 
 namespace kda {
 namespace {
@@ -36,11 +37,14 @@ constexpr int kPrepThreads = 256;
 constexpr uint32_t kXPitch = 256;  // bytes of a 128-channel FP16 row
 constexpr uint32_t kXBytes = kChunk * kXPitch;
 constexpr uint32_t kYBytes = 32 * kXPitch;
-constexpr int kLPitch = 68, kYPitch = 72, kLtPitch = 20;  // floats
+// Pitches (floats): rows four or eight banks apart, as their readers want.
+constexpr int kLPitch = 36, kL16Pitch = 20, kXPitchF = 68, kYPitch = 40, kLtPitch = 20;
 constexpr int kDPitch = 17;
+constexpr uint32_t kRowsBytes = kChunk * kDim * 2;  // a chunk's rows of an input
 
-// Shared memory, by phases: the FP16 operands of the products between
-// blocks, then (in their place) L, its inverse and a scratch matrix.
+// Shared memory, by phases: the FP16 operands of the products between blocks;
+// then, in their place, L between blocks, X = (I + L)^-1 and a scratch matrix,
+// and behind those the next item's q, k and raw_g as they arrive.
 struct PrepSmem {
   union {
     struct {
@@ -51,16 +55,33 @@ struct PrepSmem {
       uint8_t y16[kYBytes], y32[kYBytes];
     } x;
     struct {
-      float L[kChunk * kLPitch], X[kChunk * kLPitch], Y[32 * kYPitch];
-      float Lt[4][16 * kLtPitch];  // the diagonal blocks of L, transposed
+      float L[32 * kLPitch];          // rows 32 .. 63 by columns 0 .. 31
+      float L16[2][16 * kL16Pitch];   // blocks 1 by 0, 3 by 2
+      float X[kChunk * kXPitchF], Y[32 * kYPitch];
     } s;
+    struct {
+      uint8_t before[2 * kXBytes];    // (the decay sums are made from g)
+      uint8_t g[kRowsBytes], q[kRowsBytes], k[kRowsBytes];
+    } in;
   } u;
-  float fac[3][4][128];   // [R, C, Ke][block][channel], times 1024
+  union {
+    float fac[3][4][128];          // [R, C, Ke][block][channel], times 1024
+    float Lt[4][16 * kLtPitch];    // then the diagonal blocks of L, transposed
+  };
   uint16_t pow[2][4][128];  // FP16 2^n: of Kd and Qd; of the operands at 32
   float tot[2][4][128];   // log2 decays of a block's two halves
-  float part[4][2][16 * kDPitch];  // a block's products over channels 64 .. 127
+  // a block's products kn kn^T and qn kn^T, over either half of the channels
+  float part[4][2][2][16 * kDPitch];
   float norm[2][kChunk][2];        // sums of squares per channel half
   float beta[kChunk];
+  uint64_t landed;  // the item's q, k and raw_g are there
+};
+static_assert(sizeof(PrepSmem::u.s) <= sizeof(PrepSmem::u.in.before), "inputs behind X");
+
+// q, k and raw_g [n_tokens, H, 128] as 3-D tensors, a chunk's rows of one head
+// a copy.
+struct PrepMaps {
+  CUtensorMap g, q, k;
 };
 
 // Rows r of 256 bytes: 16-byte pieces, each 128-byte half permuted so that
@@ -97,10 +118,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void prefetch_l2(const void *p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -165,11 +182,14 @@ __device__ __forceinline__ void load4x2(const float *p, float2 (&f)[4]) {
   f[3] = make_float2(b.z, b.w);
 }
 
-// C[16 x 8] (+)= A[16 x 8 steps] B[8 steps x 8], FP32 operands in shared
-// memory as TF32 parts, from step `first` on.
+// C[16 x 8] = A[16 x 8 steps] B[8 steps x 8], FP32 operands in shared memory
+// as TF32 parts, from step `first` on.
 __device__ __forceinline__ void tile_mm(float (&c)[4], const float *A, int lda, const float *B,
                                         int ldb, int first, int steps, int lane) {
   const int g = lane >> 2, t = lane & 3;
+  float c1[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = 0.f;
   for (int ks = first; ks < steps; ++ks) {
     const float a[4] = {A[g * lda + 8 * ks + t], A[(g + 8) * lda + 8 * ks + t],
                         A[g * lda + 8 * ks + t + 4], A[(g + 8) * lda + 8 * ks + t + 4]};
@@ -181,10 +201,12 @@ __device__ __forceinline__ void tile_mm(float (&c)[4], const float *A, int lda, 
       l[i] = a[i] - h[i];
     }
     const float h0 = tf32_hi(b0), h1 = tf32_hi(b1);
-    mma_tf32(c, l, h0, h1);
-    mma_tf32(c, h, b0 - h0, b1 - h1);
+    mma_tf32(c1, l, h0, h1);
+    mma_tf32(c2, h, b0 - h0, b1 - h1);
     mma_tf32(c, h, h0, h1);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] += c1[i] + c2[i];
 }
 
 // Where the 16-byte piece of channels c .. c + 7 (or columns) of row t lies.
@@ -193,73 +215,104 @@ __device__ __forceinline__ uint32_t img_at(int t, int c) {
          (uint32_t)((((c & 63) >> 3) ^ (t & 7)) << 4);
 }
 
-__global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const PrefillParams p) {
-  extern __shared__ __align__(16) uint8_t prep_raw[];
+__global__ void __launch_bounds__(kPrepThreads, 2)
+    kda_prefill_prep_kernel(const PrefillParams p, const __grid_constant__ PrepMaps maps) {
+  extern __shared__ __align__(1024) uint8_t prep_raw[];
   PrepSmem &sm = *reinterpret_cast<PrepSmem *>(prep_raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_items = *p.n_chunks * p.r.H;
-  // CTAs stay, two to an SM, and fetch the next item's rows into L2 while
-  // they work on this one: without that the loads took a fifth of an item.
-  int chunk = blockIdx.x / p.r.H;
-  PrefillChunk next = p.chunks[chunk < p.max_chunks ? chunk : 0];
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-  const PrefillChunk ck = next;
-  const int h = item - chunk * p.r.H;
-  uint8_t *img = p.images + (long long)item * kImgBytes;
-  const int next_item = item + gridDim.x;
-  chunk = next_item / p.r.H;
-  if (next_item < n_items) next = p.chunks[chunk];
+  const int H = p.r.H;
+  const int n_items = *p.n_chunks * H;
+  if ((int)blockIdx.x >= n_items) return;
+  // CTAs stay, two to an SM.  An item's rows arrive (one copy each) while the
+  // one before it takes its last steps, which need little of the shared memory.
+  const auto fetch = [&](const PrefillChunk &ck, int h) {
+    mbar_arrive_expect_tx(&sm.landed, 3 * kRowsBytes);
+    tma_load_3d(sm.u.in.g, &maps.g, 0, h, ck.t0, &sm.landed);
+    tma_load_3d(sm.u.in.q, &maps.q, 0, h, ck.t0, &sm.landed);
+    tma_load_3d(sm.u.in.k, &maps.k, 0, h, ck.t0, &sm.landed);
+  };
+  uint16_t braw = 0;
+  float a_log = 0.f;
+  float2 dt = make_float2(0.f, 0.f);
+  const auto load_head = [&](int tid, const PrefillChunk &ck, int h) {
+    braw = __ldg(p.r.beta + (long long)(ck.t0 + min(tid & 63, ck.count - 1)) * H + h);
+    a_log = __ldg(p.r.A_log + h);
+    dt = __ldg(reinterpret_cast<const float2 *>(p.r.dt_bias + h * kDim) + (tid & 63));
+  };
+  int chunk = blockIdx.x / H, h = blockIdx.x - chunk * H;
+  const int chunk_step = gridDim.x / H, h_step = gridDim.x - chunk_step * H;
+  PrefillChunk ck = p.chunks[chunk];
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.landed, 1);
+    mbar_init_fence();
+    fetch(ck, h);
+  }
+  load_head(threadIdx.x, ck, h);
+  __syncthreads();
+  uint32_t phase = 0;
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x, phase ^= 1u) {
+  // (a value that the compiler takes for new each time: the many addresses
+  // that follow from it are then made again, not kept through the loop in
+  // registers that the steps need)
+  int tid = threadIdx.x;
+  asm volatile("" : "+r"(tid));
+  const int warp = tid >> 5, lane = tid & 31;
   const int blk = warp >> 1, hf = warp & 1, g = lane >> 2, tig = lane & 3;
   const int row[2] = {16 * blk + g, 16 * blk + g + 8};
   const int ch0 = hf * 64 + tig * 8;  // slices add 0 and 32
+  const int pr = tid & 63;            // a pair of channels, for the decays
+  const int last = ck.count - 1;
+  uint8_t *img = p.images + (long long)item * kImgBytes;
+  // the next item
+  chunk += chunk_step;
+  h += h_step;
+  if (h >= H) {
+    h -= H;
+    ++chunk;
+  }
+  const bool more = item + (int)gridDim.x < n_items;
+  const PrefillChunk next = p.chunks[more ? chunk : 0];
 
+  const bool here = mbar_wait_bounded(&sm.landed, phase);
+  if (__syncthreads_or(!here)) {  // (nothing else can run out in this kernel)
+    if (tid == 0) {
+      report(p.r.maps.status, KDA_ERR_TIMEOUT);
+      mbar_wait_bounded(&sm.landed, phase);  // (once more for the copies in flight)
+    }
+    break;
+  }
   // Rows past the chunk's tokens take its last token's inputs (their own may
   // be another request's) and get no weight: decay 1, kn = qn = 0, beta = 0.
-  const int last = ck.count - 1;
-  const uint32_t row_step = (uint32_t)p.r.H * kDim;
-  const long long head0 = ((long long)ck.t0 * p.r.H + h) * kDim;
   uint4 kraw[2][2], qraw[2][2];  // [slice][token]
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    const uint32_t at = (uint32_t)min(row[r], last) * row_step + (uint32_t)ch0;
-    const uint16_t *k = p.r.k + head0 + at, *q = p.r.q + head0 + at;
+    const uint32_t at = (uint32_t)min(row[r], last) * (kDim * 2) + (uint32_t)ch0 * 2;
 #pragma unroll
     for (int sl = 0; sl < 2; ++sl) {
-      kraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(k + 32 * sl));
-      qraw[sl][r] = __ldg(reinterpret_cast<const uint4 *>(q + 32 * sl));
+      kraw[sl][r] = *reinterpret_cast<const uint4 *>(sm.u.in.k + at + 64 * sl);
+      qraw[sl][r] = *reinterpret_cast<const uint4 *>(sm.u.in.q + at + 64 * sl);
     }
   }
-  // -- log2 decays and their sums around the block's middle: a thread takes
+  // -- log2 decays and their sums over each half of the block: a thread takes
   //    two channels and the block's 16 tokens in turn -------------------------
   {
-    const int pr = threadIdx.x & 63, c = 2 * pr;
-    uint32_t graw[16];
-    const uint16_t *gp = p.r.g + head0 + c;
-#pragma unroll
-    for (int t = 0; t < 16; ++t)
-      graw[t] = __ldg(reinterpret_cast<const uint32_t *>(
-          gp + (uint32_t)min(16 * blk + t, last) * row_step));
-    if (threadIdx.x < kChunk) {
-      float b = 0.f;
-      if ((int)threadIdx.x < ck.count)
-        b = 1.f / (1.f + __expf(-bf16_bits_to_f32(
-                             p.r.beta[(long long)(ck.t0 + threadIdx.x) * p.r.H + h])));
-      sm.beta[threadIdx.x] = b;
-    }
-    const float al = expf(p.r.A_log[h]) * kLog2e, lb2 = p.r.lower_bound * kLog2e;
-    const float2 dt = *reinterpret_cast<const float2 *>(p.r.dt_bias + h * kDim + c);
+    const int c = 2 * pr;
+    if (tid < kChunk)
+      sm.beta[tid] = tid <= last ? 1.f / (1.f + __expf(-bf16_bits_to_f32(braw))) : 0.f;
+    const float al = expf(a_log) * kLog2e, lb2 = p.r.lower_bound * kLog2e;
     const float2 off = make_float2(-al * dt.x, -al * dt.y), nal = make_float2(-al, -al);
-    // each half of the block is summed from its own start
     uint8_t *to = ((pr & 2) ? sm.u.x.x16_lo : sm.u.x.x16_hi) + (pr & 1) * 8 + 16 * blk * kXPitch;
     const uint32_t at = x_at(0, pr >> 2);
+    const uint8_t *from = sm.u.in.g + 4 * pr;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int t = 8 * r + i;
-        const float2 z = ffma2(nal, bf16x2_f32(graw[t]), off);
-        const float w = 16 * blk + t < ck.count ? lb2 : 0.f;
+        const uint32_t raw = *reinterpret_cast<const uint32_t *>(
+            from + (uint32_t)min(16 * blk + t, last) * (kDim * 2));
+        const float2 z = ffma2(nal, bf16x2_f32(raw), off);
+        const float w = 16 * blk + t <= last ? lb2 : 0.f;
         sum.x += __fdividef(w, 1.f + exp2f_fast(z.x));
         sum.y += __fdividef(w, 1.f + exp2f_fast(z.y));
         *reinterpret_cast<float2 *>(to + (at ^ x_at(i, 0) ^ (i * kXPitch)) + t * kXPitch) = sum;
@@ -300,7 +353,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
   //   C = kn 2^(mid - G) fac[1], fac[1] = 2^(after - mid - ph_{i+1})
   //   Ke = kn 2^(mid - G) fac[2], from the chunk's end
   {
-    const int c = threadIdx.x & 127;
+    const int c = tid & 127;
     float ta[4], tb[4], ph[5], B[5];
     ph[0] = B[0] = 0.f;
 #pragma unroll
@@ -315,7 +368,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
     const auto power = [](float n) {
       return __half_as_ushort(__float2half_rn(exp2f_fast(fmaxf(n, -60.f))));
     };
-    if (threadIdx.x < 128) {
+    if (tid < 128) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         sm.fac[0][j][c] = kImgScale * exp2f_fast(ta[j] + ph[j]);
@@ -344,17 +397,6 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
   }
   __syncthreads();
 
-  if (next_item < n_items) {
-    // 64 rows of 256 bytes of q, k and raw_g: two lines each
-    const long long at = ((long long)next.t0 * p.r.H + (next_item - chunk * p.r.H)) * kDim;
-    const int t = threadIdx.x >> 1;
-    if (t < next.count) {
-      const long long line = at + (long long)t * row_step + (threadIdx.x & 1) * 64;
-      prefetch_l2(p.r.k + line);
-      prefetch_l2(p.r.q + line);
-      prefetch_l2(p.r.g + line);
-    }
-  }
   // -- the block's own products, and the operands of everything else ---------
   float dk[2][4], dq[2][4];  // [n-tile] 16 x 8 of kn kn^T and qn kn^T
 #pragma unroll
@@ -488,25 +530,29 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
       }
     }
   }
-  if (hf == 1) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+  for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = (g + 8 * (i >> 1)) * kDPitch + 8 * n + 2 * tig + (i & 1);
-        sm.part[blk][0][at] = dk[n][i];
-        sm.part[blk][1][at] = dq[n][i];
-      }
-  }
+    for (int i = 0; i < 4; ++i) {
+      const int at = (g + 8 * (i >> 1)) * kDPitch + 8 * n + 2 * tig + (i & 1);
+      sm.part[blk][0][hf][at] = dk[n][i];
+      sm.part[blk][1][hf][at] = dq[n][i];
+    }
   __syncthreads();
 
   // -- products between blocks: warps 0-3 the quarters of rows 32 .. 63 by
-  //    columns 0 .. 31, warps 4 and 5 blocks 1 by 0 and 3 by 2 ---------------
-  float ok[2][4], oq[2][4];
+  //    columns 0 .. 31, warps 4 and 5 blocks 1 by 0 and 3 by 2.  Warps 6 and 7
+  //    meanwhile invert the diagonal blocks of I + L, two each, a lane a
+  //    column -----------------------------------------------------------------
+  // (all start from zero in every warp: what one branch leaves unset would
+  // hold its registers around the loop)
+  float ok[2][4], oq[2][4], x[16];
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) ok[n][i] = oq[n][i] = 0.f;
+#pragma unroll
+  for (int t = 0; t < 16; ++t) x[t] = 0.f;
   int r0 = 0, c0 = 0;
   if (warp < 6) {
     const uint8_t *xh = sm.u.x.x32_hi, *xl = sm.u.x.x32_lo, *y = sm.u.x.y32;
@@ -546,67 +592,25 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
         mma_f16(oq[n], aq, bh[2 * n], bh[2 * n + 1]);
       }
     }
-  }
-  __syncthreads();  // the operands have been read: L and X take their place
-
-  float *L = sm.u.s.L, *X = sm.u.s.X, *Y = sm.u.s.Y;
-  const auto put_a = [&](int t, int s, float x0, float x1) {  // s even
-    const __half2 a = __floats2half2_rn(x0, x1);
-    *reinterpret_cast<__half2 *>(img + kImgA + img_at(t, s & ~7) + (s & 7) * 2) = a;
-  };
-  if (warp < 6) {
-    constexpr float kUnit = 1.f / (kImgScale * kImgScale);
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const int t = r0 + g + 4 * i, s = c0 + 8 * n + 2 * tig;
-        const float b = sm.beta[t] * kUnit;
-        *reinterpret_cast<float2 *>(&L[t * kLPitch + s]) =
-            make_float2(b * ok[n][i], b * ok[n][i + 1]);
-        put_a(t, s, oq[n][i] * (kImgScale * kUnit), oq[n][i + 1] * (kImgScale * kUnit));
-      }
-  }
-  if (hf == 0) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const int tl = g + 4 * i, s0 = 8 * n + 2 * tig, t = 16 * blk + tl;
-        const float *pk = &sm.part[blk][0][tl * kDPitch + s0];
-        const float *pq = &sm.part[blk][1][tl * kDPitch + s0];
-        float a[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // (above the diagonal the factors may have overflowed: dropped, not
-          // multiplied by zero)
-          const float l = s0 + e < tl ? sm.beta[t] * (dk[n][i + e] + pk[e]) : 0.f;
-          sm.u.s.Lt[blk][(s0 + e) * kLtPitch + tl] = l;
-          a[e] = s0 + e <= tl ? (dq[n][i + e] + pq[e]) * kImgScale : 0.f;
-        }
-        put_a(t, 16 * blk + s0, a[0], a[1]);
-      }
   } else {
-    // A above its diagonal blocks: zeros
-    for (int i = lane; i < 16 * (6 - 2 * blk); i += 32) {
-      const int t = 16 * blk + (i & 15), piece = 2 * (blk + 1) + (i >> 4);
-      *reinterpret_cast<uint4 *>(img + kImgA + img_at(t, 8 * piece)) = make_uint4(0, 0, 0, 0);
+    r0 = 16 * (2 * (warp - 6) + (lane >> 4));  // the block's first token
+    const int bi = r0 >> 4, j = lane & 15;
+    float *Lb = sm.Lt[bi];
+    const float b = sm.beta[r0 + j];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const int at = j * kDPitch + c;
+      // (above the diagonal the factors may have overflowed: dropped, not
+      // multiplied by zero)
+      Lb[c * kLtPitch + j] = c < j ? b * (sm.part[bi][0][0][at] + sm.part[bi][0][1][at]) : 0.f;
     }
-  }
-  __syncthreads();
-
-  // -- X = (I + L)^-1: its diagonal blocks by columns, then the rest ---------
-  if (warp < 4) {
-    const int j = lane & 15;
-    float x[16];
+    __syncwarp();
 #pragma unroll
     for (int t = 0; t < 16; ++t) x[t] = t == j ? 1.f : 0.f;
-    const float *Lb = sm.u.s.Lt[warp];
 #pragma unroll
     for (int t = 0; t < 15; ++t) {
 #pragma unroll
       for (int u = (t + 1) & ~3; u < 16; u += 4) {
-        // (entries up to the diagonal are zeros)
         const float4 l = lds4(Lb + t * kLtPitch + u);
         if (u + 0 > t) x[u] = fmaf(-l.x, x[t], x[u]);
         if (u + 1 > t) x[u + 1] = fmaf(-l.y, x[t], x[u + 1]);
@@ -614,69 +618,128 @@ __global__ void __launch_bounds__(kPrepThreads, 2) kda_prefill_prep_kernel(const
         if (u + 3 > t) x[u + 3] = fmaf(-l.w, x[t], x[u + 3]);
       }
     }
-    if (lane < 16) {
+  }
+  __syncthreads();  // the operands have been read: L and X take their place
+
+  if (more && tid == 0) {
+    fence_proxy_async_smem();
+    fetch(next, h);
+  }
+  float *L = sm.u.s.L, *X = sm.u.s.X, *Y = sm.u.s.Y;
+  constexpr float kUnit = 1.f / (kImgScale * kImgScale);
+  if (warp < 6) {
 #pragma unroll
-      for (int t = 0; t < 16; ++t) X[(16 * warp + t) * kLPitch + 16 * warp + j] = x[t];
-    }
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const int t = g + 4 * i, s = 8 * n + 2 * tig;
+        const float b = sm.beta[r0 + t] * kUnit;
+        float *to = warp < 4 ? &L[(r0 - 32 + t) * kLPitch + c0 + s]
+                             : &sm.u.s.L16[warp - 4][t * kL16Pitch + s];
+        *reinterpret_cast<float2 *>(to) = make_float2(b * ok[n][i], b * ok[n][i + 1]);
+      }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 16; ++t) X[(r0 + t) * kXPitchF + r0 + (lane & 15)] = x[t];
   }
   __syncthreads();
-  const auto put = [&](float *to, int ld, const float (&c)[4], float sign) {
+
+  // -- the rest of X = (I + L)^-1, block by block; what each step leaves ready
+  //    for the images is written under the next ------------------------------
+  const auto put_f = [&](float *to, int ld, const float (&c)[4], float sign) {
     *reinterpret_cast<float2 *>(to + g * ld + 2 * tig) = make_float2(sign * c[0], sign * c[1]);
     *reinterpret_cast<float2 *>(to + (g + 8) * ld + 2 * tig) =
         make_float2(sign * c[2], sign * c[3]);
   };
-  {
-    // X10 = -X11 (L10 X00) and X32 = -X33 (L32 X22), 16 x 8 a warp
-    const int lo = 32 * (warp >> 1), hi = lo + 16, n = 8 * (warp & 1);
-    if (warp < 4) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
-      tile_mm(c, &L[hi * kLPitch + lo], kLPitch, &X[lo * kLPitch + lo + n], kLPitch, n / 8, 2,
-              lane);
-      put(&Y[lo / 2 * kYPitch + n], kYPitch, c, 1.f);
-    }
-    __syncthreads();
-    if (warp < 4) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
-      tile_mm(c, &X[hi * kLPitch + hi], kLPitch, &Y[lo / 2 * kYPitch + n], kYPitch, 0, 2, lane);
-      put(&X[hi * kLPitch + lo + n], kLPitch, c, -1.f);
-    }
-    __syncthreads();
+  const auto put_a = [&](int t, int s, float x0, float x1) {  // s even
+    *reinterpret_cast<uint32_t *>(img + kImgA + img_at(t, s & ~7) + (s & 7) * 2) =
+        h2_bits(__floats2half2_rn(x0, x1));
+  };
+  // X10 = -X11 (L10 X00) and X32 = -X33 (L32 X22), 16 x 8 a warp
+  const int lo = 32 * ((warp >> 1) & 1), hi = lo + 16, n16 = 8 * (warp & 1);
+  float c[4] = {0.f, 0.f, 0.f, 0.f};
+  if (warp < 4) {
+    tile_mm(c, sm.u.s.L16[lo / 32], kL16Pitch, &X[lo * kXPitchF + lo + n16], kXPitchF, n16 / 8, 2,
+            lane);
+    put_f(&Y[lo / 2 * kYPitch + n16], kYPitch, c, 1.f);
   }
-  {
-    // the lower left 32 x 32: -X[32.., 32..] (L[32.., ..32] X[..32, ..32])
-    const int m = 16 * (warp >> 2), n = 8 * (warp & 3);
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
-    tile_mm(c, &L[(32 + m) * kLPitch], kLPitch, &X[n], kLPitch, n / 8, 4, lane);
-    put(&Y[m * kYPitch + n], kYPitch, c, 1.f);
-    __syncthreads();
-    float z[4] = {0.f, 0.f, 0.f, 0.f};
-    tile_mm(z, &X[(32 + m) * kLPitch + 32], kLPitch, &Y[n], kYPitch, 0, m / 8 + 2, lane);
-    put(&X[(32 + m) * kLPitch + n], kLPitch, z, -1.f);
-    __syncthreads();
+  __syncthreads();
+  if (warp < 4) {
+    tile_mm(c, &X[hi * kXPitchF + hi], kXPitchF, &Y[lo / 2 * kYPitch + n16], kYPitch, 0, 2, lane);
+    put_f(&X[hi * kXPitchF + lo + n16], kXPitchF, c, -1.f);
   }
-  // -- T = X diag(beta) ------------------------------------------------------
+  if (warp < 6) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2)
+        put_a(r0 + g + 4 * i, c0 + 8 * n + 2 * tig, oq[n][i] * (kImgScale * kUnit),
+              oq[n][i + 1] * (kImgScale * kUnit));
+  }
+  __syncthreads();
+  load_head(tid, next, more ? h : 0);
+  // the lower left 32 x 32: -X[32.., 32..] (L[32.., ..32] X[..32, ..32])
+  const int m32 = 16 * (warp >> 2), n32 = 8 * (warp & 3);
+  tile_mm(c, &L[m32 * kLPitch], kLPitch, &X[n32], kXPitchF, n32 / 8, 4, lane);
+  put_f(&Y[m32 * kYPitch + n32], kYPitch, c, 1.f);
   {
-    const int t = threadIdx.x & 63;
+    // A: its diagonal blocks, and above them zeros
+    const int t = tid & 63, tl = t & 15, bt = t >> 4;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int s0 = (threadIdx.x >> 6) * 16 + 8 * e;
-      float2 x[4], b[4];
-      load4x2(&X[t * kLPitch + s0], x);
-      load4x2(&sm.beta[s0], b);
+      const int piece = 2 * (tid >> 6) + e, s0 = 8 * (piece & 1);
+      if ((piece >> 1) < bt) continue;  // (below: by the products' own warps)
+      float2 v[4];
+      const float *pq = &sm.part[bt][1][0][tl * kDPitch + s0];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 v = fmul2(x[i], fmul2(b[i], make_float2(kImgScale, kImgScale)));
-        // (what lies above the diagonal was never written)
-        x[i] = make_float2(s0 + 2 * i <= t ? v.x : 0.f, s0 + 2 * i + 1 <= t ? v.y : 0.f);
+        const float a0 = pq[2 * i] + pq[16 * kDPitch + 2 * i];
+        const float a1 = pq[2 * i + 1] + pq[16 * kDPitch + 2 * i + 1];
+        const int s = 8 * piece + 2 * i;
+        v[i] = make_float2(s <= t ? a0 * kImgScale : 0.f, s + 1 <= t ? a1 * kImgScale : 0.f);
       }
-      uint4 hi, lo;
-      split8(x, hi, lo);
-      const uint32_t at = img_at(t, s0);
-      *reinterpret_cast<uint4 *>(img + kImgTHi + at) = hi;
-      *reinterpret_cast<uint4 *>(img + kImgTLo + at) = lo;
+      *reinterpret_cast<uint4 *>(img + kImgA + img_at(t, 8 * piece)) = half8(v);
     }
   }
-  __syncthreads();  // the next item's operands take the place of X
+  __syncthreads();
+  tile_mm(c, &X[(32 + m32) * kXPitchF + 32], kXPitchF, &Y[n32], kYPitch, 0, m32 / 8 + 2, lane);
+  // -- T = X diag(beta): the lower left quarter from registers, the two on the
+  //    diagonal from X, zeros above ------------------------------------------
+  {
+    const float b0 = sm.beta[n32 + 2 * tig] * -kImgScale;
+    const float b1 = sm.beta[n32 + 2 * tig + 1] * -kImgScale;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const float2 v = make_float2(c[i] * b0, c[i + 1] * b1);
+      const __half2 h = __float22half2_rn(v);
+      const uint32_t at = img_at(32 + m32 + g + 4 * i, n32) + 4u * tig;
+      *reinterpret_cast<uint32_t *>(img + kImgTHi + at) = h2_bits(h);
+      *reinterpret_cast<uint32_t *>(img + kImgTLo + at) =
+          h2_bits(__float22half2_rn(ffma2(__half22float2(h), make_float2(-1.f, -1.f), v)));
+    }
+  }
+  {
+    const int t = tid & 63, s0 = (t & 32) + 8 * (tid >> 6);
+    float2 v[4], b[4];
+    load4x2(&X[t * kXPitchF + s0], v);
+    load4x2(&sm.beta[s0], b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = fmul2(v[i], fmul2(b[i], make_float2(kImgScale, kImgScale)));
+      // (what lies above the diagonal was not all written)
+      v[i] = make_float2(s0 + 2 * i <= t ? y.x : 0.f, s0 + 2 * i + 1 <= t ? y.y : 0.f);
+    }
+    uint4 th, tl;
+    split8(v, th, tl);
+    const uint32_t at = img_at(t, s0);
+    *reinterpret_cast<uint4 *>(img + kImgTHi + at) = th;
+    *reinterpret_cast<uint4 *>(img + kImgTLo + at) = tl;
+    const uint32_t above = img_at(tid & 31, 32 + 8 * ((tid >> 5) & 3));
+    *reinterpret_cast<uint4 *>(img + (tid < 128 ? kImgTHi : kImgTLo) + above) =
+        make_uint4(0, 0, 0, 0);
+  }
+  ck = next;
+  __syncthreads();  // the next item's decay sums take the place of X
   }
 }
 
@@ -694,10 +757,26 @@ int launch_prefill_prep(const PrefillParams &p, cudaStream_t stream) {
     configured.fetch_or(bit);
   }
   static_assert(2 * (sizeof(PrepSmem) + 1024) <= 228 * 1024, "two CTAs per SM");
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return KDA_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)kDim, (cuuint64_t)p.r.H,
+                              (cuuint64_t)p.r.maps.n_tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)kDim * 2, (cuuint64_t)p.r.H * kDim * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)kDim, 1, (cuuint32_t)kChunk};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  PrepMaps maps;
+  CUtensorMap *const map[3] = {&maps.g, &maps.q, &maps.k};
+  const uint16_t *const src[3] = {p.r.g, p.r.q, p.r.k};
+  for (int i = 0; i < 3; ++i)
+    if (encode(map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(src[i]), dims,
+               strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+        CUDA_SUCCESS)
+      return KDA_ERR_CUDA;
   const long long items = (long long)p.max_chunks * p.r.H;
   const long long room = 2LL * device_sm_count(dev);
   kda_prefill_prep_kernel<<<(unsigned)(items < room ? items : room), kPrepThreads,
-                            sizeof(PrepSmem), stream>>>(p);
+                            sizeof(PrepSmem), stream>>>(p, maps);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
