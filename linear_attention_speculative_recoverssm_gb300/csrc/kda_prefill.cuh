@@ -17,9 +17,10 @@
 //
 // Every entry of the images is at most 1 in size (unit keys and queries,
 // decays <= 1, and T_ts is minus beta_t k_t applied to what is left of a
-// state beta_s k_s after contractions).  They are held as FP16 times 1024;
-// "hi" and "lo" are x rounded to FP16 and the rest rounded again, 22 bits
-// together.  hi.hi + hi.lo + lo.hi leaves 2^-22 of a product.
+// state beta_s k_s after contractions).  Kd, Ke and A are held as FP16 times
+// 1024, T and Qd as they are (kda_prefill_chain.cu says why).  "hi" and "lo"
+// are x rounded to FP16 and the rest rounded again, 22 bits together (to 2^-25
+// of 1 for T).  hi.hi + hi.lo + lo.hi leaves 2^-22 of a product.
 #pragma once
 
 #include "kda_recurrent.cuh"

@@ -14,16 +14,19 @@
 // (rows) 32 (w & 3) .. and quarter w >> 2 of the columns.  O leaves while the
 // next chunk's M1 runs.  Warp 16 issues the MMAs, warp 17 the copies.
 //
-// FP16 parts of a row are taken times a power of two that brings M, a bound
-// of |S| and |v| over the row, to 2^8 .. 2^9.  R is then below 12.4 2^9, and
-// U below 76 2^9 < 65504 (a row of the state grows by at most beta |v| a
-// token), so one factor a chunk serves S, R, U and O, and their accumulators
-// share it.  M is known before dS is: the largest |S| before the chunk plus
-// 64 times the largest |U| in it (unit keys), or the largest |v| to come.
-// Where that is a few bits too much, the parts have them to spare (2^-25 of
-// values up to 2^9).  So the rows' quarters exchange their peaks while M3
-// runs, and nothing waits between dS and S but the arithmetic; M3 and M1 go
-// by halves of the key channels, E0 of the one under the other's MMAs.
+// FP16 parts of a row are taken times powers of two.  With M a bound of |S|
+// and |v| over the row, S goes times 1024 f and R and U times f, f M between 2
+// and 2^5 (f is kept while that holds): then S is below 2^15, R below 12.4 2^5
+// and U below 76 2^5 (a row of the state grows by at most beta |v| a token),
+// and with the images' own scales every accumulator comes out where it is
+// needed: dS in the state's units, U in those of its parts, both terms of O
+// alike, nothing to multiply.  M is known before dS is: the largest |S| before
+// the chunk plus 64 times the largest |U| in it (unit keys), or the largest
+// |v| to come.  Where that is too much by bits, the parts have them to spare
+// (2^-25 of values up to 2^15 and 2^5).  So the rows' quarters exchange their
+// peaks while M3 runs, and nothing waits between dS and S but the arithmetic;
+// M3 and M1 go by halves of the key channels, E0 of the one under the other's
+// MMAs.
 // The state itself stays in FP32, in registers: an accumulator that is added
 // to over and over loses up to a unit of its last place each time, so dS is
 // summed apart, smallest parts first.
@@ -134,10 +137,13 @@ __device__ __forceinline__ void tmem_store_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// 2^(8 - e) for m in [2^e, 2^(e+1)), at most 2^100 (zero rows)
-__device__ __forceinline__ float row_scale(float m) {
+// The row factor f for a bound M: kept while f M stays in 2 .. 2^5, else the
+// power of two with f M in 2^3 .. 2^4 (at most 2^100: zero rows).
+__device__ __forceinline__ float row_factor(float f, float m) {
+  const float fm = f * m;
+  if (fm >= 2.f && fm <= 32.f) return f;
   const int e = (int)((__float_as_uint(m) >> 23) & 255u);
-  const int s = 127 + 8 + 127 - e;
+  const int s = 127 + 3 + 127 - e;
   return __uint_as_float((uint32_t)(s > 227 ? 227 : s) << 23);
 }
 
@@ -455,15 +461,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       if (lane == 0) mbar_arrive(&sm.v_free[i & 1]);
       return fmaxf(__low2float(peak), __high2float(peak));
     };
-    // this row's scale from its quarters' peaks
-    const auto scale_of = [&](int i) {
+    // this row's bound M from its quarters' peaks
+    const auto bound_of = [&](int i) {
       float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float4 x = sm.peak[i & 1][j][row];
         m = make_float4(fmaxf(m.x, x.x), fmaxf(m.y, x.y), fmaxf(m.z, x.z), 0.f);
       }
-      return row_scale(fmaxf(fmaf(64.f, m.y, m.x), m.z));
+      return fmaxf(fmaf(64.f, m.y, m.x), m.z);
     };
     // chunk i, i + 1 and i + 2: loaded two chunks ahead
     PrefillChunk ck = p.chunks[req.base], next = p.chunks[req.base + min(1, n - 1)];
@@ -473,14 +479,14 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       peak_s = fmaxf(peak_s, fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
     sm.peak[1][qt][row] = make_float4(peak_s, 0.f, load_v(0, ck.count), 0.f);
     bad = named_bar_or(1, 32 * kRowWarps, bad);
-    float scale = scale_of(1), inv = pow2_inverse(scale);
-    // S <- S e^{G_end} + dS of chunk i, whose scale is 1 / inv
+    // s holds the state times 1024 f from here on; inv = 1 / f
+    float f = row_factor(0.f, bound_of(1)), inv = pow2_inverse(f);
+#pragma unroll
+    for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(s[e], both(f * kImgScale));
+    // S <- S e^{G_end} + dS of chunk i
     const auto advance = [&](int i) {
-      if (!wait(&sm.d_full[i & 1], (uint32_t)(i >> 1) & 1u) ||
-          !wait(&sm.ds_full[half], (uint32_t)i & 1u))
-        return;
+      if (!wait(&sm.ds_full[half], (uint32_t)i & 1u)) return;
       tc_fence_after();
-      const float2 f = both(inv * kDown);
       const float *dec = sm.decay[i & 1] + kKeys * qt;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -490,8 +496,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
         for (int e = 0; e < 8; e += 2) {
           const float4 g = lds4(dec + 16 * j + 2 * e);
           float2 &x = s[8 * j + e], &y = s[8 * j + e + 1];
-          x = ffma2(x, make_float2(g.x, g.y), fmul2(f, f2(d[2 * e], d[2 * e + 1])));
-          y = ffma2(y, make_float2(g.z, g.w), fmul2(f, f2(d[2 * e + 2], d[2 * e + 3])));
+          x = ffma2(x, make_float2(g.x, g.y), f2(d[2 * e], d[2 * e + 1]));
+          y = ffma2(y, make_float2(g.z, g.w), f2(d[2 * e + 2], d[2 * e + 3]));
         }
       }
     };
@@ -515,34 +521,47 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
           if (j < left) o[j * step] = f32_to_bf16_bits(__uint_as_float(d[j]) * f);
       }
     };
+    // the state to a page
+    const auto store = [&](int slot) {
+      float2 x[kKeys / 2];
+#pragma unroll
+      for (int e = 0; e < kKeys / 2; ++e) x[e] = fmul2(s[e], both(inv * kDown));
+      store_state<BF16>(pool + slot * slot_bytes, row, qt, x);
+    };
     int t0 = 0, count = 0;  // the chunk before's
-    float inv_before = 0.f;
+    float f_next = f;       // the next chunk's factor
+    bool changes = false;   // for any row of the warp
     for (int i = 0; i < n; ++i) {
       const PrefillChunk later = p.chunks[req.base + min(i + 2, n - 1)];
+      float inv_before = inv;
       if (i > 0) {
         advance(i - 1);
         if (bad) break;
-        if (i == req.bnd_chunks) store_state<BF16>(pool + rq.bnd * slot_bytes, row, qt, s);
-        inv_before = inv;
-        inv = pow2_inverse(scale);  // chunk i's, from the peaks of chunk i - 1
+        if (i == req.bnd_chunks) store(rq.bnd);
+        if (changes) {
+          const float2 by = both(f_next * inv);
+#pragma unroll
+          for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(s[e], by);
+          f = f_next;
+          inv = pow2_inverse(f);
+        }
       }
       // S as parts
       {
-        const float2 f = both(scale);
         __half2 peak = __float2half2_rn(0.f);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) split2(fmul2(s[8 * j + e], f), hi[e], lo[e], peak);
+          for (int e = 0; e < 8; ++e) split2(s[8 * j + e], hi[e], lo[e], peak);
           tmem_store8(lanes + kColSHi + 16u * qt + 8u * j, hi);
           tmem_store8(lanes + kColSLo + 16u * qt + 8u * j, lo);
         }
-        peak_s = max_of(peak) * inv;
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.s_ready[half]);
+        peak_s = max_of(peak) * (kDown * inv);
       }
       if (i > 0) emit(i - 1, t0, count, inv_before);
       t0 = ck.t0;
@@ -558,8 +577,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
         for (int j = 0; j < 8; ++j) {
           const float2 v = make_float2(__uint_as_float(v2[j] << 16),
                                        __uint_as_float(v2[j] & 0xffff0000u));
-          split2(ffma2(f2(d[2 * j], d[2 * j + 1]), both(-kDown), fmul2(v, both(scale))), hi[j],
-                 lo[j], unused);
+          split2(ffma2(f2(d[2 * j], d[2 * j + 1]), both(-kDown * kDown), fmul2(v, both(f))),
+                 hi[j], lo[j], unused);
         }
         tmem_store8(lanes + kColRHi + 8u * qt, hi);
         tmem_store8(lanes + kColRLo + 8u * qt, lo);
@@ -579,8 +598,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
         tmem_load16(lanes + kColW + (uint32_t)(kToks * qt), d);
         __half2 peak = __float2half2_rn(0.f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          split2(fmul2(f2(d[2 * j], d[2 * j + 1]), both(kDown)), hi[j], lo[j], peak);
+        for (int j = 0; j < 8; ++j) split2(f2(d[2 * j], d[2 * j + 1]), hi[j], lo[j], peak);
         tmem_store8(lanes + kColRHi + 8u * qt, hi);
         tmem_store8(lanes + kColRLo + 8u * qt, lo);
         sm.peak[i & 1][qt][row] = make_float4(peak_s, max_of(peak) * inv, peak_v, 0.f);
@@ -589,14 +607,18 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.u_ready);
       }
-      // (every row's peaks are there once all warps have arrived)
-      if (!wait(&sm.u_ready, (uint32_t)i & 1u)) break;
-      scale = scale_of(i);
+      // under M3: every row's peaks are there once all warps have arrived, and
+      // the chunk's decays have long been
+      if (!wait(&sm.u_ready, (uint32_t)i & 1u) ||
+          !wait(&sm.d_full[i & 1], (uint32_t)(i >> 1) & 1u))
+        break;
+      f_next = row_factor(f, bound_of(i));
+      changes = __any_sync(0xffffffffu, f_next != f);
     }
     if (!bad) advance(n - 1);
     if (!bad) {
-      if (n == req.bnd_chunks) store_state<BF16>(pool + rq.bnd * slot_bytes, row, qt, s);
-      store_state<BF16>(pool + rq.dst * slot_bytes, row, qt, s);
+      if (n == req.bnd_chunks) store(rq.bnd);
+      store(rq.dst);
       emit(n - 1, t0, count, inv);
     }
     if (bad && lane == 0) report(status, KDA_ERR_TIMEOUT);

@@ -522,7 +522,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
         }
         times(qf[r], fac, x);
         hi = half8(x);
-        put(im + 1024 * r + kImgQd, blk == 0 ? hi : scale8(hi, pow0));
+        constexpr uint32_t kDown = 0x14001400u;  // FP16 2^-10, twice: Qd has no scale
+        put(im + 1024 * r + kImgQd,
+            scale8(blk == 0 ? hi : scale8(hi, pow0), make_uint4(kDown, kDown, kDown, kDown)));
         if (blk & 1) put(sm.u.x.y16 + (y16_0 ^ (64u * sl)) + 8 * r * kXPitch, hi);
         if (blk >= 2)
           put(sm.u.x.y32 + (y32_0 ^ (64u * sl)) + 8 * r * kXPitch,
@@ -706,8 +708,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   // -- T = X diag(beta): the lower left quarter from registers, the two on the
   //    diagonal from X, zeros above ------------------------------------------
   {
-    const float b0 = sm.beta[n32 + 2 * tig] * -kImgScale;
-    const float b1 = sm.beta[n32 + 2 * tig + 1] * -kImgScale;
+    const float b0 = -sm.beta[n32 + 2 * tig], b1 = -sm.beta[n32 + 2 * tig + 1];
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
       const float2 v = make_float2(c[i] * b0, c[i + 1] * b1);
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
     load4x2(&sm.beta[s0], b);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 y = fmul2(v[i], fmul2(b[i], make_float2(kImgScale, kImgScale)));
+      const float2 y = fmul2(v[i], b[i]);
       // (what lies above the diagonal was not all written)
       v[i] = make_float2(s0 + 2 * i <= t ? y.x : 0.f, s0 + 2 * i + 1 <= t ? y.y : 0.f);
     }
