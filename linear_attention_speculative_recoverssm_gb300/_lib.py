@@ -411,20 +411,21 @@ def _expect_tensors(device, *specs):
     """The prompt operators' tensors, (name, tensor or None, type, shape) each:
     their types, shapes and layouts (contiguous), and that all are on
     `device`, a GPU."""
+    index = device.index
     for name, t, dtype, shape in specs:
-        if t is None:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                         and t.get_device() == index):
             continue
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+        if device.type == "cuda":
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, got {device}")
-    for name, t, _, _ in specs:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
 def _expect_rows(device, name, t, dtype, inner):
@@ -444,25 +445,20 @@ def _expect_rows(device, name, t, dtype, inner):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-class _on:
-    """A call's stream, with the device of its tensors the current one: the
-    caller's own when that is so already."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.guard = None
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.given = stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.given)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call_on(device, stream, call):
+    """call(stream's address) with the device of the call's tensors the
+    current one; the device's current stream where none is given."""
+    import torch
+    if stream is None:
+        # (torch.cuda.current_stream builds a Stream object: 3 us of a call
+        # that takes 12)
+        address = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        address = stream if isinstance(stream, int) else stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        return call(address)
+    with torch.cuda.device(device):
+        return call(address)
 
 
 def _address(t):
@@ -498,14 +494,13 @@ def kda_slot_plan(computed_lens, new_lens, block_table, free_slots, free_head, f
     _expect_rows(dev, "block_table", block_table, i32, (None,))
     if block_table.shape[0] != B:
         raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
-    with _on(dev, stream) as st:
-        rc = load().kda_slot_plan(
+    rc = _call_on(dev, stream, lambda st: load().kda_slot_plan(
             computed_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
             _row_stride(block_table, block_table.shape[1]), block_table.shape[1],
             free_slots.data_ptr(), free_slots.shape[0], free_head.data_ptr(),
             free_next.data_ptr(), query_start_loc.data_ptr(), sources.data_ptr(),
             destinations.data_ptr(), boundaries.data_ptr(), boundary_lens.data_ptr(), B,
-            block_size, null_slot, _address(status), st)
+            block_size, null_slot, _address(status), st))
     return _check("kda_slot_plan", rc, raise_on_error)
 
 
@@ -531,13 +526,12 @@ def kda_prefill_conv(x, conv_weight, conv_bias, conv_state, sources, destination
                     ("query_start_loc", query_start_loc, i32, (B + 1,)),
                     ("status", status, i32, (1,)))
     _expect_rows(dev, "conv_state", conv_state, bf, (3 * D, None))
-    with _on(dev, stream) as st:
-        rc = load().kda_prefill_conv(
+    rc = _call_on(dev, stream, lambda st: load().kda_prefill_conv(
             x.data_ptr(), conv_weight.data_ptr(), _address(conv_bias), conv_state.data_ptr(),
             _row_stride(conv_state, 3 * D * conv_state.shape[2]), conv_state.shape[2],
             conv_state.shape[0], sources.data_ptr(), destinations.data_ptr(),
             _address(boundaries), _address(boundary_lens), _address(query_start_loc), T,
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, Q, null_slot, _address(status), st)
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, Q, null_slot, _address(status), st))
     return _check("kda_prefill_conv", rc, raise_on_error)
 
 
@@ -592,23 +586,28 @@ def kda_prefill(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources, d
     B = sources.shape[0]
     if workspace is not None and (not workspace.is_contiguous() or workspace.device != q.device):
         raise ValueError("workspace must be a contiguous tensor on the operands' device")
-    with _on(q.device, stream) as st:
-        if workspace is None:
-            need = max(0, kda_prefill_workspace_bytes(T, B, H))
+    lib = load()
+
+    def call(st):
+        ws = workspace
+        if ws is None:
+            need = max(0, lib.kda_prefill_workspace_bytes(T, B, H))
             if stream is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
             else:
                 # of the call's own stream: the allocator hands it on there
-                with torch.cuda.stream(torch.cuda.ExternalStream(st.value or 0)):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        nbytes = workspace.numel() * workspace.element_size()
-        rc = load().kda_prefill(
+                with torch.cuda.stream(torch.cuda.ExternalStream(st)):
+                    ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        nbytes = ws.numel() * ws.element_size()
+        return lib.kda_prefill(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), raw_g.data_ptr(), raw_beta.data_ptr(),
             A_log.data_ptr(), dt_bias.data_ptr(), lower_bound, q_scale, state_pool.data_ptr(),
             dtype, slot_stride, state_pool.shape[0], sources.data_ptr(), destinations.data_ptr(),
             _address(boundaries), _address(boundary_lens), _address(query_start_loc), T,
-            out.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes, B, H, Q, null_slot,
+            out.data_ptr(), ws.data_ptr() if nbytes else None, nbytes, B, H, Q, null_slot,
             _address(status), st)
+
+    rc = _call_on(q.device, stream, call)
     return _check("kda_prefill", rc, raise_on_error)
 
 
@@ -622,11 +621,10 @@ def kda_recurrent(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources,
                                     destinations, query_start_loc, out, boundaries,
                                     boundary_lens, status)
     T, H, _ = q.shape
-    with _on(q.device, stream) as st:
-        rc = load().kda_recurrent(
+    rc = _call_on(q.device, stream, lambda st: load().kda_recurrent(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), raw_g.data_ptr(), raw_beta.data_ptr(),
             A_log.data_ptr(), dt_bias.data_ptr(), lower_bound, q_scale, state_pool.data_ptr(),
             dtype, slot_stride, state_pool.shape[0], sources.data_ptr(), destinations.data_ptr(),
             _address(boundaries), _address(boundary_lens), _address(query_start_loc), T,
-            out.data_ptr(), sources.shape[0], H, Q, null_slot, _address(status), st)
+            out.data_ptr(), sources.shape[0], H, Q, null_slot, _address(status), st))
     return _check("kda_recurrent", rc, raise_on_error)

@@ -16,8 +16,15 @@ namespace {
 constexpr int kShortLen = 8;
 constexpr int kListThreads = 1024;
 
+// Segments: where a call has too few (request, head) items to fill half the
+// SMs, the chain of a long prompt leaves the others idle, and the preparation
+// of the next segment runs there meanwhile.  One prompt of 16384 tokens, 32
+// heads: 1000 us in one segment, 892 us in eight.  With more items the chain fills the GPU by itself, and a
+// segment only costs its launches and the state's way through memory.
+constexpr int kSegItems = 76, kSegChunks = 32, kMaxSegments = 16;
+
 struct Workspace {
-  int64_t chunks, requests, order, images, bytes;  // offsets
+  int64_t chunks, bases, order, carry, images, bytes;  // offsets
   int64_t max_chunks;
 };
 
@@ -27,86 +34,98 @@ Workspace workspace_layout(int64_t n_tokens, int64_t B, int64_t H) {
   const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   const int64_t most = n_tokens / (kShortLen + 1);
   Workspace w;
-  w.max_chunks = n_tokens / kChunk + 2 * (B < most ? B : most);
+  w.max_chunks = n_tokens / kChunk + 2 * (B == 1 || B < most ? B : most);
   w.chunks = 256;
-  w.requests = up(w.chunks + w.max_chunks * (int64_t)sizeof(PrefillChunk));
-  w.order = up(w.requests + B * (int64_t)sizeof(PrefillRequest));
-  w.images = up(w.order + B * 4);
+  const bool segments = B * H <= kSegItems;
+  w.bases = up(w.chunks + w.max_chunks * (int64_t)sizeof(PrefillChunk));
+  w.order = up(w.bases + B * 4 * (segments ? kMaxSegments : 1));
+  w.carry = up(w.order + B * (int64_t)sizeof(PrefillRequest));
+  w.images = up(w.carry + (segments ? B * H * kDim * kDim * 4 : 0));
   w.bytes = w.images + w.max_chunks * H * (int64_t)kImgBytes;
   return w;
 }
 
 __device__ __forceinline__ int chunks_of(int n) { return (n + kChunk - 1) / kChunk; }
 
-// One CTA: the chunks of every request, packed in order of the requests, and
-// the requests by falling number of chunks (a counting sort: the chain's
-// longest items start first).
+// One CTA: the chunks of every request, by segment and then in order of the
+// requests, and the requests by falling number of chunks (a counting sort: the
+// chain's longest items start first).
 __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const PrefillParams p) {
-  __shared__ int warp_sums[kListThreads / 32];
+  __shared__ long long warp_sums[kListThreads / 32];  // (windows may overlap: no bound on a sum)
   __shared__ int bins[kListThreads];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = p.r.maps.B;
+  grid_launch_dependents();
   bins[tid] = 0;
   __syncthreads();
-  int base = 0;
-  for (int b0 = 0; b0 < B; b0 += kListThreads) {
-    const int b = b0 + tid;
-    int first = 0, rest = 0, t0 = 0, m = 0, n = 0;
-    if (b < B) {
-      const PromptRequest r = prompt_request(p.r.maps, b);
-      if (r.error != KDA_OK) report(p.r.maps.status, r.error);
-      if (r.n > p.short_len && r.dst >= 0) {
-        t0 = r.t0;
-        n = r.n;
-        m = r.m;
-        first = chunks_of(m);
-        rest = chunks_of(n - m);
+  long long base = 0;
+  for (int seg = 0; seg < p.segments; ++seg) {
+    if (tid == 0) p.seg_first[seg] = (int)min(base, (long long)p.max_chunks);
+    for (int b0 = 0; b0 < B; b0 += kListThreads) {
+      const int b = b0 + tid;
+      int first = 0, rest = 0, t0 = 0, m = 0, n = 0;
+      if (b < B) {
+        const PromptRequest r = prompt_request(p.r.maps, b);
+        if (seg == 0 && r.error != KDA_OK) report(p.r.maps.status, r.error);
+        if (r.n > p.short_len && r.dst >= 0) {
+          t0 = r.t0;
+          n = r.n;
+          m = r.m;
+          first = chunks_of(m);
+          rest = chunks_of(n - m);
+        }
       }
-    }
-    int inc = first + rest;
+      // (the last segment takes what is left: there is nothing where Q is kept)
+      const int done = seg * p.seg_chunks, all = first + rest;
+      int mine = min(max(all - done, 0), p.seg_chunks);
+      long long inc = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) warp_sums[warp] = inc;
-    __syncthreads();
-    int s = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    const int total = __shfl_sync(0xffffffffu, s, 31);
-    const int before = warp > 0 ? __shfl_sync(0xffffffffu, s, warp - 1) : 0;
-    int at = base + before + inc - (first + rest);
-    base += total;
-    // (windows that overlap can ask for more chunks than there is room for)
-    if (first + rest > 0 && (long long)at + first + rest > p.max_chunks) {
-      report(p.r.maps.status, KDA_ERR_ARG);
-      first = rest = 0;
-    }
-    if (b < B) {
-      p.requests[b] = PrefillRequest{at, first + rest, first};
-      atomicAdd(&bins[min(first + rest, kListThreads - 1)], 1);
-    }
-    // a warp writes the chunks of its 32 requests one after the other
-    uint32_t some = __ballot_sync(0xffffffffu, first + rest > 0);
-    while (some != 0) {
-      const int l = __ffs(some) - 1;
-      some &= some - 1;
-      const int f = __shfl_sync(0xffffffffu, first, l), c = f + __shfl_sync(0xffffffffu, rest, l);
-      const int w = __shfl_sync(0xffffffffu, at, l), t = __shfl_sync(0xffffffffu, t0, l);
-      const int mm = __shfl_sync(0xffffffffu, m, l), nn = __shfl_sync(0xffffffffu, n, l);
-      for (int j = lane; j < c; j += 32) {
-        const int from = j < f ? j * kChunk : mm + (j - f) * kChunk;
-        const int end = j < f ? mm : nn;
-        p.chunks[w + j] = PrefillChunk{t + from, min(kChunk, end - from)};
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
       }
+      if (lane == 31) warp_sums[warp] = inc;
+      __syncthreads();
+      long long s = warp_sums[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+      }
+      const long long total = __shfl_sync(0xffffffffu, s, 31);
+      const long long before = warp > 0 ? __shfl_sync(0xffffffffu, s, warp - 1) : 0;
+      const long long at = base + before + inc - mine;
+      base += total;
+      // (windows that overlap can ask for more chunks than there is room for:
+      // such a request is cut off, and reported)
+      const bool fits = at + mine <= p.max_chunks;
+      if (!fits) {
+        report(p.r.maps.status, KDA_ERR_ARG);
+        mine = 0;
+      }
+      if (b < B) {
+        p.bases[seg * B + b] = fits ? (int)at : -1;
+        if (seg == 0) atomicAdd(&bins[min(all, kListThreads - 1)], 1);
+      }
+      // a warp writes the chunks of its 32 requests one after the other
+      uint32_t some = __ballot_sync(0xffffffffu, mine > 0);
+      while (some != 0) {
+        const int l = __ffs(some) - 1;
+        some &= some - 1;
+        const int f = __shfl_sync(0xffffffffu, first, l), c = __shfl_sync(0xffffffffu, mine, l);
+        const int w = __shfl_sync(0xffffffffu, (int)at, l), t = __shfl_sync(0xffffffffu, t0, l);
+        const int mm = __shfl_sync(0xffffffffu, m, l), nn = __shfl_sync(0xffffffffu, n, l);
+        for (int j = lane; j < c; j += 32) {
+          const int k = done + j;  // the request's chunk
+          const int from = k < f ? k * kChunk : mm + (k - f) * kChunk;
+          const int end = k < f ? mm : nn;
+          p.chunks[w + j] = PrefillChunk{t + from, min(kChunk, end - from)};
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
-  if (tid == 0) *p.n_chunks = base < p.max_chunks ? base : p.max_chunks;
+  if (tid == 0) p.seg_first[p.segments] = (int)min(base, (long long)p.max_chunks);
   // bins, longest first -> where each begins
   const int bin = kListThreads - 1 - tid;
   const int mine = bins[bin];
@@ -118,7 +137,7 @@ __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const Pr
   }
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  int s = warp_sums[lane];
+  int s = (int)warp_sums[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, s, o);
@@ -126,8 +145,19 @@ __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const Pr
   }
   bins[bin] = inc - mine + (warp > 0 ? __shfl_sync(0xffffffffu, s, warp - 1) : 0);
   __syncthreads();
-  for (int b = tid; b < B; b += kListThreads)
-    p.order[atomicAdd(&bins[min(p.requests[b].chunks, kListThreads - 1)], 1)] = b;
+  for (int b = tid; b < B; b += kListThreads) {
+    const PromptRequest r = prompt_request(p.r.maps, b);
+    PrefillRequest q{b, 0, 0, p.bases[b]};
+    if (r.n > p.short_len && r.dst >= 0) {
+      q.bnd_chunks = chunks_of(r.m);
+      q.chunks = q.bnd_chunks + chunks_of(r.n - r.m);
+    }
+    const int at = atomicAdd(&bins[min(q.chunks, kListThreads - 1)], 1);
+    // (cut off where there was no room)
+    for (int seg = 0; seg < p.segments; ++seg)
+      if (p.bases[seg * B + b] < 0) q.chunks = min(q.chunks, seg * p.seg_chunks);
+    p.order[at] = q;
+  }
 }
 
 }  // namespace
@@ -164,27 +194,43 @@ int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const k
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   kda::PrefillParams p;
   p.r = kda::RecurrentParams{q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale,
-                             state_pool, slot_stride, out, H, kda::kShortLen,
+                             state_pool, slot_stride, out, H, kda::kShortLen, false,
                              kda::make_prompt_maps(sources, destinations, boundaries,
                                                    boundary_lens, query_start_loc, n_tokens,
                                                    n_slots, B, Q, null_slot, status)};
-  p.short_len = kda::kShortLen;
+  // a single request of any length is one launch less by chunks alone
+  p.short_len = B == 1 ? 0 : kda::kShortLen;
   p.max_chunks = (int)w.max_chunks;
-  p.n_chunks = reinterpret_cast<int *>(ws);
+  // the longest request's chunks: its own and one more where its boundary
+  // cuts one in two
+  const int most = (Q - 1) / kda::kChunk + 1 + (boundaries != nullptr ? 1 : 0);
+  p.segments = 1;
+  if ((long long)B * H <= kda::kSegItems && most >= 2 * kda::kSegChunks) {
+    p.segments = (most + kda::kSegChunks / 2) / kda::kSegChunks;
+    if (p.segments > kda::kMaxSegments) p.segments = kda::kMaxSegments;
+  }
+  p.seg_chunks = (most + p.segments - 1) / p.segments;
+  p.seg_first = reinterpret_cast<int *>(ws);
+  p.bases = reinterpret_cast<int *>(ws + w.bases);
+  p.carry = reinterpret_cast<float *>(ws + w.carry);
   p.chunks = reinterpret_cast<kda::PrefillChunk *>(ws + w.chunks);
-  p.requests = reinterpret_cast<kda::PrefillRequest *>(ws + w.requests);
-  p.order = reinterpret_cast<int *>(ws + w.order);
+  p.order = reinterpret_cast<kda::PrefillRequest *>(ws + w.order);
   p.images = ws + w.images;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf16 = state_dtype == KDA_STATE_BF16;
-  if (Q > kda::kShortLen && p.max_chunks > 0) {
-    kda::kda_prefill_list_kernel<<<1, kda::kListThreads, 0, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
-    rc = kda::launch_prefill_prep(p, st);
+  if (Q <= kda::kShortLen) return kda::launch_recurrent(p.r, bf16, st);
+  kda::kda_prefill_list_kernel<<<1, kda::kListThreads, 0, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+  // From here on each kernel is launched as the one before it starts, and
+  // waits, where it needs to, for that one to end.
+  for (int seg = 0; seg < p.segments; ++seg) {
+    rc = kda::launch_prefill_prep(p, seg, st);
     if (rc != KDA_OK) return rc;
-    rc = kda::launch_prefill_chain(p, bf16, st);
+    rc = kda::launch_prefill_chain(p, seg, bf16, st);
     if (rc != KDA_OK) return rc;
   }
+  if (p.short_len == 0) return KDA_OK;
+  p.r.beside = true;
   return kda::launch_recurrent(p.r, bf16, st);
 }
 

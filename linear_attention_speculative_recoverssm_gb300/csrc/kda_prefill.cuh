@@ -49,23 +49,32 @@ struct PrefillChunk {
   int t0, count;  // tokens t0 .. t0 + count - 1 of the packed activations
 };
 
-struct PrefillRequest {
-  int base, chunks;  // its chunks are base .. base + chunks - 1
-  int bnd_chunks;    // chunks up to its boundary; 0: none
+struct __align__(16) PrefillRequest {
+  int b;
+  int chunks;      // all of its chunks
+  int bnd_chunks;  // chunks up to its boundary; 0: none
+  int base;        // its first chunk of segment 0
 };
 
+// The chunks go by segments of every request, seg_chunks of each at a time:
+// the preparation of one and then its chain, whose CTAs leave the state to the
+// next segment's in FP32.  The next preparation runs beside the chain.
 struct PrefillParams {
   RecurrentParams r;
   int short_len;  // requests of at most so many tokens go token by token
   int max_chunks;
-  int *n_chunks;            // [1]
-  PrefillChunk *chunks;     // [max_chunks]
-  PrefillRequest *requests; // [B]
-  int *order;               // [B], requests by falling number of chunks
+  int segments, seg_chunks;
+  int *seg_first;           // [segments + 1], the segments' first chunks
+  PrefillChunk *chunks;     // [max_chunks], by segment, then request
+  int *bases;               // [segments, B], a request's first chunk of each
+  PrefillRequest *order;    // [B], by falling number of chunks
+  float *carry;             // [B, H, 128, 128] (segments > 1)
   uint8_t *images;          // [max_chunks, H, kImgBytes]
 };
 
-int launch_prefill_prep(const PrefillParams &p, cudaStream_t stream);
-int launch_prefill_chain(const PrefillParams &p, bool bf16, cudaStream_t stream);
+// One segment.  A preparation that is not the first may start as soon as the
+// chain before it has, and ends after it.
+int launch_prefill_prep(const PrefillParams &p, int segment, cudaStream_t stream);
+int launch_prefill_chain(const PrefillParams &p, int segment, bool bf16, cudaStream_t stream);
 
 }  // namespace kda

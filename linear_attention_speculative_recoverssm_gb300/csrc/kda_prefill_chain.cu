@@ -46,7 +46,8 @@ namespace {
 
 constexpr int kRowWarps = 16;
 constexpr int kChainThreads = 32 * (kRowWarps + 2);  // and the MMA and copy warps
-constexpr int kKeys = kDim / 4, kToks = kChunk / 4;  // columns of a thread
+constexpr int kParts = kRowWarps / 4;  // threads of a row
+constexpr int kKeys = kDim / kParts, kToks = kChunk / kParts;  // their columns
 constexpr uint32_t kPartA = kImgTHi;                  // Kd, Qd: 48 KB
 constexpr uint32_t kPartB = kImgKeHi - kImgTHi;       // T: 16 KB
 constexpr uint32_t kPartC = kImgDecay - kImgKeHi;     // Ke, A: 40 KB
@@ -71,7 +72,8 @@ struct ChainSmem {
   uint8_t a[kPartA], b[kPartB], c[kPartC];  // each a multiple of 1024 bytes
   uint8_t v[2][kVBytes];
   float decay[2][kDim];
-  float4 peak[2][4][128];  // [chunk parity][column quarter][row]: |S|, |U|, next |v|
+  PrefillChunk chunk[4];  // chunk i at i & 3, there when its v is
+  float4 peak[2][kParts][128];  // [chunk parity][part][row]: |S|, |U|, next |v|
   uint64_t a_full, a_free, b_full, b_free, c_full, c_free, v_full[2], v_free[2], d_full[2];
   uint64_t s_ready[2], r_ready, u_ready, w_full, u_full, ds_full[2], o_full, drained;
   uint32_t tmem;
@@ -166,14 +168,14 @@ __device__ __forceinline__ float max_of(__half2 x) {
   return fmaxf(f.x, f.y);
 }
 
-// A quarter row of a state page (32 key channels from 32 quarter).
+// A part of a state page's row (kKeys key channels).
 template <bool BF16>
-__device__ __forceinline__ void load_state(const void *page, int row, int quarter,
+__device__ __forceinline__ void load_state(const void *page, int row, int part,
                                            float2 (&s)[kKeys / 2]) {
   if constexpr (BF16) {
-    const uint4 *g = reinterpret_cast<const uint4 *>(page) + row * (kDim / 8) + quarter * 4;
+    const uint4 *g = reinterpret_cast<const uint4 *>(page) + row * (kDim / 8) + part * (kKeys / 8);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kKeys / 8; ++i) {
       const uint4 x = __ldcs(g + i);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -182,9 +184,10 @@ __device__ __forceinline__ void load_state(const void *page, int row, int quarte
                                    __uint_as_float(w[j] & 0xffff0000u));
     }
   } else {
-    const float4 *g = reinterpret_cast<const float4 *>(page) + row * (kDim / 4) + quarter * 8;
+    const float4 *g =
+        reinterpret_cast<const float4 *>(page) + row * (kDim / 4) + part * (kKeys / 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kKeys / 4; ++i) {
       const float4 x = __ldcs(g + i);
       s[2 * i] = make_float2(x.x, x.y);
       s[2 * i + 1] = make_float2(x.z, x.w);
@@ -192,22 +195,30 @@ __device__ __forceinline__ void load_state(const void *page, int row, int quarte
   }
 }
 
+// The same to memory, times `f`.
 template <bool BF16>
-__device__ __forceinline__ void store_state(void *page, int row, int quarter,
-                                            const float2 (&s)[kKeys / 2]) {
+__device__ __forceinline__ void store_state(void *page, int row, int part,
+                                            const float2 (&s)[kKeys / 2], float f) {
+  const float2 ff = make_float2(f, f);
   if constexpr (BF16) {
-    uint4 *g = reinterpret_cast<uint4 *>(page) + row * (kDim / 8) + quarter * 4;
+    uint4 *g = reinterpret_cast<uint4 *>(page) + row * (kDim / 8) + part * (kKeys / 8);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      g[i] = make_uint4(pack_bf16x2(s[4 * i].x, s[4 * i].y),
-                        pack_bf16x2(s[4 * i + 1].x, s[4 * i + 1].y),
-                        pack_bf16x2(s[4 * i + 2].x, s[4 * i + 2].y),
-                        pack_bf16x2(s[4 * i + 3].x, s[4 * i + 3].y));
+    for (int i = 0; i < kKeys / 8; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = fmul2(s[4 * i + j], ff);
+        w[j] = pack_bf16x2(x.x, x.y);
+      }
+      g[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   } else {
-    float4 *g = reinterpret_cast<float4 *>(page) + row * (kDim / 4) + quarter * 8;
+    float4 *g = reinterpret_cast<float4 *>(page) + row * (kDim / 4) + part * (kKeys / 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      g[i] = make_float4(s[2 * i].x, s[2 * i].y, s[2 * i + 1].x, s[2 * i + 1].y);
+    for (int i = 0; i < kKeys / 4; ++i) {
+      const float2 x = fmul2(s[2 * i], ff), y = fmul2(s[2 * i + 1], ff);
+      g[i] = make_float4(x.x, x.y, y.x, y.y);
+    }
   }
 }
 
@@ -256,19 +267,27 @@ struct MnMajor {
   }
 };
 
+// Zeros to the outputs of an inert request's head.
+__device__ __forceinline__ void zero_inert(const PrefillParams &p, int b, int h) {
+  const PromptRequest rq = prompt_request(p.r.maps, b);
+  if (rq.dst >= 0) return;
+  for (int i = threadIdx.x; i < rq.n * (kDim / 8); i += kChainThreads)
+    *reinterpret_cast<uint4 *>(p.r.out +
+                               ((long long)(rq.t0 + i / (kDim / 8)) * p.r.H + h) * kDim +
+                               i % (kDim / 8) * 8) = make_uint4(0, 0, 0, 0);
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(const PrefillParams p,
-                                                                             const __grid_constant__ CUtensorMap v_map) {
-  extern __shared__ uint8_t chain_raw[];
+                                                                             const __grid_constant__ CUtensorMap v_map,
+                                                                             int segment) {
+  // (the swizzle atoms want 1024 bytes; there is no other shared memory)
+  extern __shared__ __align__(1024) uint8_t chain_raw[];
   const int H = p.r.H;
-  const int b = p.order[blockIdx.x / H], h = blockIdx.x % H;
-  const PrefillRequest req = p.requests[b];
-  const int n = req.chunks;
-  if (n == 0) return;
-  ChainSmem &sm = *reinterpret_cast<ChainSmem *>(
-      chain_raw + ((1024u - (smem_u32(chain_raw) & 1023u)) & 1023u));
+  ChainSmem &sm = *reinterpret_cast<ChainSmem *>(chain_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t *status = p.r.maps.status;
+  // what does not need the preparation, while its last CTAs may still run
   if (threadIdx.x == 0) {
     mbar_init(&sm.a_full, 1);
     mbar_init(&sm.a_free, 1);
@@ -292,17 +311,32 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
+  grid_dependency_wait();
+  // (only now: the next kernel may count on what this one has waited for)
+  grid_launch_dependents();
+  const PrefillRequest req = p.order[blockIdx.x / H];
+  const int b = req.b, h = blockIdx.x % H;
+  // this segment's chunks: done, done + 1 .. done + n - 1 of the request's
+  const int done = segment * p.seg_chunks;
+  const int n = max(min(req.chunks - done, p.seg_chunks), 0);
+  const bool ends = done + n == req.chunks;
+  const int bnd_at = req.bnd_chunks > 0 ? req.bnd_chunks - done : -1;  // in its chunks
+  const int base = segment == 0 ? req.base : p.bases[segment * p.r.maps.B + b];
+  const int src = prompt_request(p.r.maps, b).src;  // (of segment 0)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const uint8_t *images = p.images + ((long long)req.base * H + h) * kImgBytes;
+  const uint8_t *images = p.images + ((long long)base * H + h) * kImgBytes;
   const long long img_step = (long long)H * kImgBytes;
 
-  if (warp == kRowWarps + 1) {
+  if (n == 0) {
+    if (segment == 0 && p.short_len == 0) zero_inert(p, b, h);
+  } else if (warp == kRowWarps + 1) {
     // -- copies ---------------------------------------------------------------
     bool ok = true;
     int n_v = 0, n_a = 0, n_b = 0, n_c = 0;  // copies issued of each kind
+    PrefillChunk coming = p.chunks[base];    // the next chunk whose v is copied
     const auto load_v = [&](int i) {
       uint64_t *bar = &sm.v_full[i & 1];
       if (i >= 2) ok = ok && mbar_wait_bounded(&sm.v_free[i & 1], (uint32_t)((i >> 1) - 1) & 1u);
@@ -313,8 +347,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       // 64 rows whatever the count: one copy (a copy a row took the warp some
       // 75 cycles each); what is past it, rows of others or the zeros past the
       // activations, is not used
+      const PrefillChunk ck = coming;
+      coming = p.chunks[base + min(i + 1, n - 1)];
+      sm.chunk[i & 3] = ck;  // (its place was chunk i - 4's: long emitted)
       mbar_arrive_expect_tx(bar, kVBytes);
-      tma_load_3d(sm.v[i & 1], &v_map, 0, h, p.chunks[req.base + i].t0, bar);
+      tma_load_3d(sm.v[i & 1], &v_map, 0, h, ck.t0, bar);
     };
     const auto load_part = [&](int i, uint64_t *full, uint64_t *free, uint8_t *dst, uint32_t at,
                                uint32_t bytes, int &issued) {
@@ -414,32 +451,52 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
     // -- rows -------------------------------------------------------------------
     const int row = 32 * (warp & 3) + lane, qt = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const long long elem = BF16 ? 2 : 4;
-    char *pool = reinterpret_cast<char *>(p.r.state) + (long long)h * kDim * kDim * elem;
-    const long long slot_bytes = p.r.slot_stride * elem;
-    const PromptRequest rq = prompt_request(p.r.maps, b);
-    float2 s[kKeys / 2];  // this row's key channels 32 qt .. 32 qt + 31
-    if (rq.src >= 0) {
-      load_state<BF16>(pool + rq.src * slot_bytes, row, qt, s);
+    // The pages' addresses are made where they are used, from values that the
+    // compiler takes for new each time: kept through the loop they would take
+    // registers that it has not got.
+    const auto page = [&](int slot) {
+      long long at = h;
+      asm volatile("" : "+l"(at));
+      return reinterpret_cast<char *>(p.r.state) +
+             ((long long)slot * p.r.slot_stride + at * kDim * kDim) * (BF16 ? 2 : 4);
+    };
+    const auto carry = [&] {
+      long long at = (long long)b * H + h;
+      asm volatile("" : "+l"(at));
+      return p.carry + at * kDim * kDim;
+    };
+    const auto request = [&] {
+      int at = b;
+      asm volatile("" : "+r"(at));
+      return prompt_request(p.r.maps, at);
+    };
+    float2 s[kKeys / 2];  // this row's key channels from kKeys qt on
+    if (segment > 0) {
+      load_state<false>(carry(), row, qt, s);
     } else {
+      if (src >= 0) {
+        load_state<BF16>(page(src), row, qt, s);
+      } else {
 #pragma unroll
-      for (int i = 0; i < kKeys / 2; ++i) s[i] = make_float2(0.f, 0.f);
+        for (int i = 0; i < kKeys / 2; ++i) s[i] = make_float2(0.f, 0.f);
+      }
     }
     constexpr float kDown = 1.f / kImgScale;
     const auto f2 = [](uint32_t x, uint32_t y) {
       return make_float2(__uint_as_float(x), __uint_as_float(y));
     };
     const auto both = [](float x) { return make_float2(x, x); };
-    const int half = qt >> 1;
+    const int half = 2 * qt / kParts;  // of the key channels
     bool bad = false;
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
       bad = __any_sync(0xffffffffu, bad || !mbar_wait_bounded(bar, parity));
       return !bad;
     };
-    // v of chunk i: this row's tokens 16 qt .. 16 qt + 15, and their peak
+    // v of chunk i: this row's tokens from kToks qt on, and their peak
     uint32_t v2[kToks / 2];
-    const auto load_v = [&](int i, int count) {
+    const auto load_v = [&](int i) {
       if (!wait(&sm.v_full[i & 1], (uint32_t)(i >> 1) & 1u)) return 0.f;
+      const int count = sm.chunk[i & 3].count;
       const uint16_t *v = reinterpret_cast<const uint16_t *>(sm.v[i & 1]) + kToks * qt * kDim + row;
       const int left = count - kToks * qt;
       if (left >= kToks) {
@@ -461,23 +518,21 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       if (lane == 0) mbar_arrive(&sm.v_free[i & 1]);
       return fmaxf(__low2float(peak), __high2float(peak));
     };
-    // this row's bound M from its quarters' peaks
+    // this row's bound M from its parts' peaks
     const auto bound_of = [&](int i) {
       float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kParts; ++j) {
         const float4 x = sm.peak[i & 1][j][row];
         m = make_float4(fmaxf(m.x, x.x), fmaxf(m.y, x.y), fmaxf(m.z, x.z), 0.f);
       }
       return fmaxf(fmaf(64.f, m.y, m.x), m.z);
     };
-    // chunk i, i + 1 and i + 2: loaded two chunks ahead
-    PrefillChunk ck = p.chunks[req.base], next = p.chunks[req.base + min(1, n - 1)];
-    float peak_s = 0.f;  // largest |S| of this quarter row
+    float peak_s = 0.f;  // largest |S| of this part
 #pragma unroll
     for (int e = 0; e < kKeys / 2; ++e)
       peak_s = fmaxf(peak_s, fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
-    sm.peak[1][qt][row] = make_float4(peak_s, 0.f, load_v(0, ck.count), 0.f);
+    sm.peak[1][qt][row] = make_float4(peak_s, 0.f, load_v(0), 0.f);
     bad = named_bar_or(1, 32 * kRowWarps, bad);
     // s holds the state times 1024 f from here on; inv = 1 / f
     float f = row_factor(0.f, bound_of(1)), inv = pow2_inverse(f);
@@ -489,7 +544,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       tc_fence_after();
       const float *dec = sm.decay[i & 1] + kKeys * qt;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kKeys / 16; ++j) {
         uint32_t d[16];
         tmem_load16(lanes + kColDs + (uint32_t)(kKeys * qt + 16 * j), d);
 #pragma unroll
@@ -501,43 +556,44 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
         }
       }
     };
-    // the outputs of chunk i (tokens t0 .. t0 + count - 1)
-    const auto emit = [&](int i, int t0, int count, float inv) {
+    // the outputs of chunk i
+    const auto emit = [&](int i, float inv) {
       if (!wait(&sm.o_full, (uint32_t)i & 1u)) return;
       tc_fence_after();
-      uint32_t d[16];
-      tmem_load16(lanes + kColO + 64u * (i & 1) + (uint32_t)(kToks * qt), d);
       const float f = p.r.q_scale * kDown * inv;
       const uint32_t step = (uint32_t)H * kDim;
-      uint16_t *o = p.r.out + (long long)(t0 + kToks * qt) * step + h * kDim + row;
-      const int left = count - kToks * qt;
-      if (left >= kToks) {
+      const PrefillChunk ck = sm.chunk[i & 3];
 #pragma unroll
-        for (int j = 0; j < kToks; ++j)
-          o[j * step] = f32_to_bf16_bits(__uint_as_float(d[j]) * f);
-      } else {
+      for (int k = 0; k < kToks / 16; ++k) {
+        const int t = kToks * qt + 16 * k;
+        uint32_t d[16];
+        tmem_load16(lanes + kColO + 64u * (i & 1) + (uint32_t)t, d);
+        uint16_t *o = p.r.out + (long long)(ck.t0 + t) * step + h * kDim + row;
+        const int left = ck.count - t;
+        if (left >= 16) {
 #pragma unroll
-        for (int j = 0; j < kToks; ++j)
-          if (j < left) o[j * step] = f32_to_bf16_bits(__uint_as_float(d[j]) * f);
+          for (int j = 0; j < 16; ++j)
+            o[j * step] = f32_to_bf16_bits(__uint_as_float(d[j]) * f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < left) o[j * step] = f32_to_bf16_bits(__uint_as_float(d[j]) * f);
+        }
       }
     };
-    // the state to a page
+    // the state to a page; to the next segment (slot < 0)
     const auto store = [&](int slot) {
-      float2 x[kKeys / 2];
-#pragma unroll
-      for (int e = 0; e < kKeys / 2; ++e) x[e] = fmul2(s[e], both(inv * kDown));
-      store_state<BF16>(pool + slot * slot_bytes, row, qt, x);
+      if (slot < 0) store_state<false>(carry(), row, qt, s, inv * kDown);
+      else store_state<BF16>(page(slot), row, qt, s, inv * kDown);
     };
-    int t0 = 0, count = 0;  // the chunk before's
     float f_next = f;       // the next chunk's factor
     bool changes = false;   // for any row of the warp
     for (int i = 0; i < n; ++i) {
-      const PrefillChunk later = p.chunks[req.base + min(i + 2, n - 1)];
       float inv_before = inv;
       if (i > 0) {
         advance(i - 1);
         if (bad) break;
-        if (i == req.bnd_chunks) store(rq.bnd);
+        if (i == bnd_at) store(request().bnd);
         if (changes) {
           const float2 by = both(f_next * inv);
 #pragma unroll
@@ -550,12 +606,12 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       {
         __half2 peak = __float2half2_rn(0.f);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kKeys / 16; ++j) {
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) split2(s[8 * j + e], hi[e], lo[e], peak);
-          tmem_store8(lanes + kColSHi + 16u * qt + 8u * j, hi);
-          tmem_store8(lanes + kColSLo + 16u * qt + 8u * j, lo);
+          tmem_store8(lanes + kColSHi + (uint32_t)(kKeys / 2 * qt + 8 * j), hi);
+          tmem_store8(lanes + kColSLo + (uint32_t)(kKeys / 2 * qt + 8 * j), lo);
         }
         tmem_store_wait();
         tc_fence_before();
@@ -563,44 +619,47 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
         if (lane == 0) mbar_arrive(&sm.s_ready[half]);
         peak_s = max_of(peak) * (kDown * inv);
       }
-      if (i > 0) emit(i - 1, t0, count, inv_before);
-      t0 = ck.t0;
-      count = ck.count;
+      if (i > 0) emit(i - 1, inv_before);
       // R = V - W
       if (!wait(&sm.w_full, (uint32_t)i & 1u)) break;
       tc_fence_after();
       {
-        uint32_t d[16], hi[8], lo[8];
         __half2 unused = __float2half2_rn(0.f);
-        tmem_load16(lanes + kColW + (uint32_t)(kToks * qt), d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 v = make_float2(__uint_as_float(v2[j] << 16),
-                                       __uint_as_float(v2[j] & 0xffff0000u));
-          split2(ffma2(f2(d[2 * j], d[2 * j + 1]), both(-kDown * kDown), fmul2(v, both(f))),
-                 hi[j], lo[j], unused);
+        for (int k = 0; k < kToks / 16; ++k) {
+          uint32_t d[16], hi[8], lo[8];
+          tmem_load16(lanes + kColW + (uint32_t)(kToks * qt + 16 * k), d);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t vv = v2[8 * k + j];
+            const float2 v = make_float2(__uint_as_float(vv << 16),
+                                         __uint_as_float(vv & 0xffff0000u));
+            split2(ffma2(f2(d[2 * j], d[2 * j + 1]), both(-kDown * kDown), fmul2(v, both(f))),
+                   hi[j], lo[j], unused);
+          }
+          tmem_store8(lanes + kColRHi + (uint32_t)(kToks / 2 * qt + 8 * k), hi);
+          tmem_store8(lanes + kColRLo + (uint32_t)(kToks / 2 * qt + 8 * k), lo);
         }
-        tmem_store8(lanes + kColRHi + 8u * qt, hi);
-        tmem_store8(lanes + kColRLo + 8u * qt, lo);
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.r_ready);
       }
-      ck = next;
-      next = later;
-      const float peak_v = i + 1 < n ? load_v(i + 1, ck.count) : 0.f;
+      const float peak_v = i + 1 < n ? load_v(i + 1) : 0.f;
       // U
       if (!wait(&sm.u_full, (uint32_t)i & 1u)) break;
       tc_fence_after();
       {
-        uint32_t d[16], hi[8], lo[8];
-        tmem_load16(lanes + kColW + (uint32_t)(kToks * qt), d);
         __half2 peak = __float2half2_rn(0.f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split2(f2(d[2 * j], d[2 * j + 1]), hi[j], lo[j], peak);
-        tmem_store8(lanes + kColRHi + 8u * qt, hi);
-        tmem_store8(lanes + kColRLo + 8u * qt, lo);
+        for (int k = 0; k < kToks / 16; ++k) {
+          uint32_t d[16], hi[8], lo[8];
+          tmem_load16(lanes + kColW + (uint32_t)(kToks * qt + 16 * k), d);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) split2(f2(d[2 * j], d[2 * j + 1]), hi[j], lo[j], peak);
+          tmem_store8(lanes + kColRHi + (uint32_t)(kToks / 2 * qt + 8 * k), hi);
+          tmem_store8(lanes + kColRLo + (uint32_t)(kToks / 2 * qt + 8 * k), lo);
+        }
         sm.peak[i & 1][qt][row] = make_float4(peak_s, max_of(peak) * inv, peak_v, 0.f);
         tmem_store_wait();
         tc_fence_before();
@@ -617,9 +676,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
     }
     if (!bad) advance(n - 1);
     if (!bad) {
-      if (n == req.bnd_chunks) store(rq.bnd);
-      store(rq.dst);
-      emit(n - 1, t0, count, inv);
+      if (n == bnd_at) store(request().bnd);
+      store(ends ? request().dst : -1);
+      emit(n - 1, inv);
     }
     if (bad && lane == 0) report(status, KDA_ERR_TIMEOUT);
   }
@@ -633,9 +692,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
 
 }  // namespace
 
-int launch_prefill_chain(const PrefillParams &p, bool bf16, cudaStream_t stream) {
+int launch_prefill_chain(const PrefillParams &p, int segment, bool bf16, cudaStream_t stream) {
   static std::atomic<uint64_t> configured{0};
-  constexpr uint32_t kSmem = sizeof(ChainSmem) + 1024;
+  constexpr uint32_t kSmem = sizeof(ChainSmem);
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(2 * kSmem > 228 * 1024, "one CTA per SM: its TMEM allocation never waits");
   int dev = 0;
@@ -665,9 +724,18 @@ int launch_prefill_chain(const PrefillParams &p, bool bf16, cudaStream_t stream)
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
       CUDA_SUCCESS)
     return KDA_ERR_CUDA;
-  const unsigned grid = (unsigned)(p.r.maps.B * p.r.H);
-  if (bf16) kda_prefill_chain_kernel<true><<<grid, kChainThreads, kSmem, stream>>>(p, v_map);
-  else kda_prefill_chain_kernel<false><<<grid, kChainThreads, kSmem, stream>>>(p, v_map);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.r.maps.B * p.r.H));
+  cfg.blockDim = dim3(kChainThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const auto kernel = bf16 ? kda_prefill_chain_kernel<true> : kda_prefill_chain_kernel<false>;
+  if (cudaLaunchKernelEx(&cfg, kernel, p, v_map, segment) != cudaSuccess) return KDA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -216,12 +216,21 @@ __device__ __forceinline__ uint32_t img_at(int t, int c) {
 }
 
 __global__ void __launch_bounds__(kPrepThreads, 2)
-    kda_prefill_prep_kernel(const PrefillParams p, const __grid_constant__ PrepMaps maps) {
+    kda_prefill_prep_kernel(const PrefillParams p, const __grid_constant__ PrepMaps maps,
+                            int segment) {
   extern __shared__ __align__(1024) uint8_t prep_raw[];
   PrepSmem &sm = *reinterpret_cast<PrepSmem *>(prep_raw);
   const int H = p.r.H;
-  const int n_items = *p.n_chunks * H;
-  if ((int)blockIdx.x >= n_items) return;
+  // The first segment waits for the list; the others start once the chain
+  // before them has seen the preparation before it, and so the list, complete.
+  if (segment == 0) grid_dependency_wait();
+  grid_launch_dependents();
+  const int first = p.seg_first[segment];
+  const int n_items = (p.seg_first[segment + 1] - first) * H;
+  if ((int)blockIdx.x >= n_items) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) grid_dependency_wait();
+    return;
+  }
   // CTAs stay, two to an SM.  An item's rows arrive (one copy each) while the
   // one before it takes its last steps, which need little of the shared memory.
   const auto fetch = [&](const PrefillChunk &ck, int h) {
@@ -240,7 +249,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   };
   int chunk = blockIdx.x / H, h = blockIdx.x - chunk * H;
   const int chunk_step = gridDim.x / H, h_step = gridDim.x - chunk_step * H;
-  PrefillChunk ck = p.chunks[chunk];
+  const PrefillChunk *const chunks = p.chunks + first;
+  uint8_t *const images = p.images + (long long)first * H * kImgBytes;
+  PrefillChunk ck = chunks[chunk];
   if (threadIdx.x == 0) {
     mbar_init(&sm.landed, 1);
     mbar_init_fence();
@@ -261,7 +272,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   const int ch0 = hf * 64 + tig * 8;  // slices add 0 and 32
   const int pr = tid & 63;            // a pair of channels, for the decays
   const int last = ck.count - 1;
-  uint8_t *img = p.images + (long long)item * kImgBytes;
+  uint8_t *img = images + (long long)item * kImgBytes;
   // the next item
   chunk += chunk_step;
   h += h_step;
@@ -270,7 +281,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
     ++chunk;
   }
   const bool more = item + (int)gridDim.x < n_items;
-  const PrefillChunk next = p.chunks[more ? chunk : 0];
+  const PrefillChunk next = chunks[more ? chunk : 0];
 
   const bool here = mbar_wait_bounded(&sm.landed, phase);
   if (__syncthreads_or(!here)) {  // (nothing else can run out in this kernel)
@@ -742,11 +753,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   ck = next;
   __syncthreads();  // the next item's decay sums take the place of X
   }
+  // beside a chain, this grid completes after it
+  if (blockIdx.x == 0 && threadIdx.x == 0) grid_dependency_wait();
 }
 
 }  // namespace
 
-int launch_prefill_prep(const PrefillParams &p, cudaStream_t stream) {
+int launch_prefill_prep(const PrefillParams &p, int segment, cudaStream_t stream) {
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
@@ -774,10 +787,24 @@ int launch_prefill_prep(const PrefillParams &p, cudaStream_t stream) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
         CUDA_SUCCESS)
       return KDA_ERR_CUDA;
-  const long long items = (long long)p.max_chunks * p.r.H;
-  const long long room = 2LL * device_sm_count(dev);
-  kda_prefill_prep_kernel<<<(unsigned)(items < room ? items : room), kPrepThreads,
-                            sizeof(PrepSmem), stream>>>(p, maps);
+  long long items = (long long)p.max_chunks * p.r.H;
+  const long long most = (long long)p.r.maps.B * p.seg_chunks * p.r.H;
+  if (p.segments > 1 && most < items) items = most;
+  // (beside a chain: what its CTAs, one to an SM, leave)
+  const int sms = device_sm_count(dev), chain = p.r.maps.B * p.r.H;
+  const long long room = 2LL * (segment > 0 && chain < sms ? sms - chain : sms);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items < room ? items : room));
+  cfg.blockDim = dim3(kPrepThreads);
+  cfg.dynamicSmemBytes = sizeof(PrepSmem);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kda_prefill_prep_kernel, p, maps, segment) != cudaSuccess)
+    return KDA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(256, 2) kda_recurrent_kernel(const RecurrentPa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
   const int row0 = (blockIdx.y * (blockDim.x >> 5) + warp) * kRecRows;
+  // launched behind a chain, this grid needs nothing of it but ends after it
+  if (p.beside && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) grid_dependency_wait();
   const PromptRequest r = prompt_request(p.maps, b);
   if (r.error != KDA_OK && h == 0 && row0 == 0 && lane == 0) report(p.maps.status, r.error);
   if (r.n == 0) return;
@@ -175,9 +177,17 @@ int check_rule(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const kd
 int launch_recurrent(const RecurrentParams &p, bool bf16, cudaStream_t stream) {
   const int items = p.maps.B * p.H;
   const int warps = 8;
-  const dim3 grid(items, kDim / kRecRows / warps), block(32 * warps);
-  if (bf16) kda_recurrent_kernel<true><<<grid, block, 0, stream>>>(p);
-  else kda_recurrent_kernel<false><<<grid, block, 0, stream>>>(p);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = p.beside ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(items, kDim / kRecRows / warps);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const auto kernel = bf16 ? kda_recurrent_kernel<true> : kda_recurrent_kernel<false>;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return KDA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -200,7 +210,7 @@ extern "C" int kda_recurrent(
                        state_dtype, slot_stride, H, out);
   if (rc != KDA_OK) return rc;
   const kda::RecurrentParams p{q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale,
-                               state_pool, slot_stride, out, H, 0x7fffffff,
+                               state_pool, slot_stride, out, H, 0x7fffffff, false,
                                kda::make_prompt_maps(sources, destinations, boundaries,
                                                      boundary_lens, query_start_loc, n_tokens,
                                                      n_slots, B, Q, null_slot, status)};

@@ -17,6 +17,7 @@ struct RecurrentParams {
   uint16_t *out;  // [n_tokens, H, 128]
   int H;
   int max_len;  // requests of more tokens are someone else's (inert ones are not)
+  bool beside;  // may start beside the kernel before it in the stream
   PromptMaps maps;
 };
 
