@@ -2,15 +2,27 @@
 // and left in slots of the pool.  Per (request, head) item and token
 //   S <- S diag(d); u = beta (v - S kn); S <- S + u kn^T; o = S qn,
 // d, kn, qn, beta as in the verify kernels.  The rows of S (value channels)
-// never meet, so a warp owns 16 rows for the whole window, in registers:
-// lane l holds key channels 4 l .. 4 l + 3 of each.  With S_d = S diag(d),
-//   w = S_d kn, y = S_d qn, u = beta (v - w), o = y + u (kn . qn),
-// so one pass over the rows gives both products, the 32 partial sums of a
-// token (w and y of 16 rows) go through one reduce-scatter (31 shuffles)
-// that leaves row r's w in lane r and its y in lane 16 + r, and the update
-// needs u of each row from its lane (16 shuffles).  State traffic is one
-// read and one write of the page whatever the window; at one token that is
-// all there is to do, and the kernel streams pages.
+// never meet, so a warp owns 16 rows for the whole window, in registers, and
+// the page moves once each way whatever the window.  With S_d = S diag(d),
+//   w = S_d kn, y = S_d qn, u = beta (v - w), o = y + u (kn . qn):
+// one pass over the rows gives both products.
+//
+// Two kernels, by the window that the caller allows:
+//  - one token (kda_recurrent_one): moving the pages is all there is to do.  A
+//    warp's load covers a whole FP32 row (512 bytes; lane l holds channels
+//    4 l .. 4 l + 3 of each row), every warp makes the token's operands for
+//    itself, and none waits for another.  The token is asked for before the
+//    page, so that its operands are made while the rows arrive (behind the
+//    rows: 654 us).  512 requests of 64 heads, FP32: 616 us, 6.97 TB/s (a
+//    copy measures 6.77); the other kernel 662.
+//  - more (kda_recurrent_group): lane 8 g + j holds 16 channels of rows g,
+//    g + 4, g + 8, g + 12, so that the eight partial sums of a lane go through
+//    one reduce-scatter over eight lanes (7 shuffles, where a row to a warp
+//    takes 31) and u comes back by 4 instead of 16; a token's operands are
+//    made once for the CTA, a token a warp, eight tokens at a time.  100
+//    requests of 32 heads, 3 tokens, BF16: 65 us (3.4 TB/s: the arithmetic
+//    of a warp's tokens is a chain of sums and shuffles, and 16 warps an SM is
+//    what the rows' registers leave room for); the other kernel 82.
 #include <cuda_runtime.h>
 
 #include "../../include/kda_recoverssm.h"
@@ -22,138 +34,297 @@ namespace kda {
 namespace {
 
 constexpr int kRecRows = 16;  // state rows of a warp
+constexpr int kGroup = 8;     // tokens whose operands are made at a time
 
-__device__ __forceinline__ float4 bf16x4_to_f32(uint2 b) {
-  return make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
-                     __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+__device__ __forceinline__ float4 bf16x4_to_f32(uint32_t lo, uint32_t hi) {
+  return make_float4(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u),
+                     __uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
 }
 
-// The 16 rows of a page from `row0`, to and from registers.
-template <bool BF16>
-__device__ __forceinline__ void load_rows(const void *page, int row0, int lane,
-                                          float4 (&s)[kRecRows]) {
-  if constexpr (BF16) {
-    const uint2 *g = reinterpret_cast<const uint2 *>(page) + row0 * (kDim / 4) + lane;
-    uint2 raw[kRecRows];
-#pragma unroll
-    for (int r = 0; r < kRecRows; ++r) raw[r] = __ldcs(g + r * (kDim / 4));
-#pragma unroll
-    for (int r = 0; r < kRecRows; ++r) s[r] = bf16x4_to_f32(raw[r]);
-  } else {
-    const float4 *g = reinterpret_cast<const float4 *>(page) + row0 * (kDim / 4) + lane;
-#pragma unroll
-    for (int r = 0; r < kRecRows; ++r) s[r] = __ldcs(g + r * (kDim / 4));
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store_rows(void *page, int row0, int lane,
-                                           const float4 (&s)[kRecRows]) {
-  if constexpr (BF16) {
-    // the page's own type: rounded once, here
-    uint2 *g = reinterpret_cast<uint2 *>(page) + row0 * (kDim / 4) + lane;
-#pragma unroll
-    for (int r = 0; r < kRecRows; ++r)
-      __stcs(g + r * (kDim / 4),
-             make_uint2(pack_bf16x2(s[r].x, s[r].y), pack_bf16x2(s[r].z, s[r].w)));
-  } else {
-    float4 *g = reinterpret_cast<float4 *>(page) + row0 * (kDim / 4) + lane;
-#pragma unroll
-    for (int r = 0; r < kRecRows; ++r) __stcs(g + r * (kDim / 4), s[r]);
-  }
-}
-
-// One token's operands of a head as loaded: 4 key channels per lane, and the
-// value of row `lane & 15` of the warp.
+// One token's operands as loaded, four channels to a lane.
 struct RawToken {
-  uint2 q, k, g;
-  uint16_t v, beta;
+  uint2 q, k, g, v;
+  uint16_t beta;
 };
 
-__device__ __forceinline__ RawToken load_token(const RecurrentParams &p, long long row, int lane,
-                                               int vrow) {
-  RawToken t;
+// Row `row` of the activations.
+__device__ __forceinline__ RawToken load_token(const RecurrentParams &p, long long row, int lane) {
   const long long base = row * kDim;
+  RawToken t;
   t.q = __ldg(reinterpret_cast<const uint2 *>(p.q + base) + lane);
   t.k = __ldg(reinterpret_cast<const uint2 *>(p.k + base) + lane);
   t.g = __ldg(reinterpret_cast<const uint2 *>(p.g + base) + lane);
-  t.v = __ldg(p.v + base + vrow);
+  t.v = __ldg(reinterpret_cast<const uint2 *>(p.v + base) + lane);
   t.beta = __ldg(p.beta + row);
   return t;
 }
 
+// The same, worked out: the lane's channels of d, kn and qn, and kn . qn (with
+// q_scale) and beta.
+struct Token {
+  float4 d, k, q;
+  float kq, beta;
+};
+
+// `a` is exp(A_log) of the head, `dt` the lane's channels' bias.
+__device__ __forceinline__ Token make_token(const RecurrentParams &p, const RawToken &r, float a,
+                                            float4 dt) {
+  Token t;
+  const float4 q = bf16x4_to_f32(r.q.x, r.q.y), k = bf16x4_to_f32(r.k.x, r.k.y);
+  const float4 g = bf16x4_to_f32(r.g.x, r.g.y);
+  float qq = q.x * q.x + q.y * q.y + q.z * q.z + q.w * q.w;
+  float kk = k.x * k.x + k.y * k.y + k.z * k.z + k.w * k.w;
+  float kq = k.x * q.x + k.y * q.y + k.z * q.z + k.w * q.w;
+  qq = warp_sum(qq);
+  kk = warp_sum(kk);
+  kq = warp_sum(kq);
+  const float qs = rsqrtf(qq + kNormEps) * p.q_scale, ks = rsqrtf(kk + kNormEps);
+  t.d = make_float4(gate_decay(a, g.x, dt.x, p.lower_bound), gate_decay(a, g.y, dt.y, p.lower_bound),
+                    gate_decay(a, g.z, dt.z, p.lower_bound),
+                    gate_decay(a, g.w, dt.w, p.lower_bound));
+  t.k = make_float4(k.x * ks, k.y * ks, k.z * ks, k.w * ks);
+  t.q = make_float4(q.x * qs, q.y * qs, q.z * qs, q.w * qs);
+  t.kq = kq * qs * ks;
+  t.beta = 1.f / (1.f + __expf(-bf16_bits_to_f32(r.beta)));
+  return t;
+}
+
+// What both kernels do first: this item's request, reported if it is wrong,
+// its outputs zeroed if it is inert.  False: nothing is left to do.
+__device__ __forceinline__ bool begin_item(const RecurrentParams &p, int b, int h, int row0,
+                                           int lane, PromptRequest &r) {
+  // launched behind a chain, this grid needs nothing of it but ends after it
+  if (p.beside && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) grid_dependency_wait();
+  r = prompt_request(p.maps, b);
+  if (r.error != KDA_OK && h == 0 && row0 == 0 && lane == 0) report(p.maps.status, r.error);
+  if (r.n == 0) return false;
+  if (r.dst < 0) {
+    for (int t = lane >> 4; t < r.n; t += 2)
+      p.out[((long long)(r.t0 + t) * p.H + h) * kDim + row0 + (lane & 15)] = 0;
+    return false;
+  }
+  return r.n <= p.max_len;
+}
+
+// -- one token ---------------------------------------------------------------
+
 template <bool BF16>
-__global__ void __launch_bounds__(256, 2) kda_recurrent_kernel(const RecurrentParams p) {
+__device__ __forceinline__ void store_whole(void *page, int row0, int lane,
+                                            const float4 (&s)[kRecRows]) {
+#pragma unroll
+  for (int i = 0; i < kRecRows; ++i) {
+    if constexpr (BF16)  // the page's own type: rounded once, here
+      __stcs(reinterpret_cast<uint2 *>(page) + (row0 + i) * (kDim / 4) + lane,
+             make_uint2(pack_bf16x2(s[i].x, s[i].y), pack_bf16x2(s[i].z, s[i].w)));
+    else
+      __stcs(reinterpret_cast<float4 *>(page) + (row0 + i) * (kDim / 4) + lane, s[i]);
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256, 2) kda_recurrent_one(const RecurrentParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
   const int row0 = (blockIdx.y * (blockDim.x >> 5) + warp) * kRecRows;
-  // launched behind a chain, this grid needs nothing of it but ends after it
-  if (p.beside && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) grid_dependency_wait();
-  const PromptRequest r = prompt_request(p.maps, b);
-  if (r.error != KDA_OK && h == 0 && row0 == 0 && lane == 0) report(p.maps.status, r.error);
-  if (r.n == 0) return;
-  if (r.n > p.max_len && r.dst >= 0) return;
-  if (r.dst < 0) {  // inert: zero outputs
-    for (int t = 0; t < r.n; ++t)
-      if (lane < kRecRows)
-        p.out[((long long)(r.t0 + t) * p.H + h) * kDim + row0 + lane] = 0;
-    return;
-  }
-  const long long head = (long long)h * kDim * kDim * (BF16 ? 2 : 4);
-  const long long slot_bytes = p.slot_stride * (BF16 ? 2 : 4);
-  char *pool = reinterpret_cast<char *>(p.state) + head;
+  PromptRequest r;
+  if (!begin_item(p, b, h, row0, lane, r)) return;
+  const long long elem = BF16 ? 2 : 4;
+  char *pool = reinterpret_cast<char *>(p.state) + (long long)h * kDim * kDim * elem;
+  const long long slot_bytes = p.slot_stride * elem;
+  const float a = expf(p.A_log[h]);
+  const float4 dt = *reinterpret_cast<const float4 *>(p.dt_bias + h * kDim + 4 * lane);
+  const long long at = (long long)r.t0 * p.H + h;
+  const int row = row0 + (lane & (kRecRows - 1));
+  const float v = bf16_bits_to_f32(__ldg(p.v + at * kDim + row));
+  const RawToken raw = load_token(p, at, lane);
   float4 s[kRecRows];
-  if (r.src >= 0) {
-    load_rows<BF16>(pool + r.src * slot_bytes, row0, lane, s);
-  } else {
+  if (r.src < 0) {
 #pragma unroll
     for (int i = 0; i < kRecRows; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  } else if constexpr (BF16) {
+    const uint2 *g = reinterpret_cast<const uint2 *>(pool + r.src * slot_bytes) +
+                     row0 * (kDim / 4) + lane;
+    uint2 x[kRecRows];
+#pragma unroll
+    for (int i = 0; i < kRecRows; ++i) x[i] = __ldcs(g + i * (kDim / 4));
+#pragma unroll
+    for (int i = 0; i < kRecRows; ++i) s[i] = bf16x4_to_f32(x[i].x, x[i].y);
+  } else {
+    const float4 *g = reinterpret_cast<const float4 *>(pool + r.src * slot_bytes) +
+                      row0 * (kDim / 4) + lane;
+#pragma unroll
+    for (int i = 0; i < kRecRows; ++i) s[i] = __ldcs(g + i * (kDim / 4));
+  }
+  const Token t = make_token(p, raw, a, dt);
+  float part[2 * kRecRows];
+#pragma unroll
+  for (int i = 0; i < kRecRows; ++i) {
+    s[i] = fmul4(s[i], t.d);
+    const float2 z = make_float2(0.f, 0.f);
+    const float2 w = dot4_acc(s[i], t.k, z), y = dot4_acc(s[i], t.q, z);
+    part[i] = w.x + w.y;
+    part[kRecRows + i] = y.x + y.y;
+  }
+  reduce_scatter<2 * kRecRows, 32>(part, lane);
+  // lane i < 16: w of row i; lane 16 + i: y of row i
+  const float w = __shfl_sync(0xffffffffu, part[0], lane & (kRecRows - 1));
+  const float u = t.beta * (v - w);  // of row lane & 15
+  if (lane >= kRecRows) p.out[at * kDim + row] = f32_to_bf16_bits(fmaf(u, t.kq, part[0]));
+#pragma unroll
+  for (int i = 0; i < kRecRows; ++i) s[i] = ffma4s(__shfl_sync(0xffffffffu, u, i), t.k, s[i]);
+  if (r.m > 0) store_whole<BF16>(pool + r.bnd * slot_bytes, row0, lane, s);
+  store_whole<BF16>(pool + r.dst * slot_bytes, row0, lane, s);
+}
+
+// -- more --------------------------------------------------------------------
+
+// The key channels of lane part j, as the m-th four: 16-byte pieces of a page's
+// row, eight lanes side by side (BF16: two fours to a piece).
+template <bool BF16>
+__device__ __forceinline__ constexpr int key_of(int j, int m) {
+  return BF16 ? 64 * (m >> 1) + 8 * j + 4 * (m & 1) : 32 * m + 4 * j;
+}
+
+// Rows `row`, row + 4, row + 8 and row + 12, to and from registers.
+template <bool BF16>
+__device__ __forceinline__ void load_rows(const void *page, int row, int j, float4 (&s)[4][4]) {
+  if constexpr (BF16) {
+    uint4 raw[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        raw[i][m] = __ldcs(reinterpret_cast<const uint4 *>(page) +
+                           (row + 4 * i) * (kDim / 8) + 8 * m + j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        s[i][2 * m] = bf16x4_to_f32(raw[i][m].x, raw[i][m].y);
+        s[i][2 * m + 1] = bf16x4_to_f32(raw[i][m].z, raw[i][m].w);
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        s[i][m] = __ldcs(reinterpret_cast<const float4 *>(page) +
+                         (row + 4 * i) * (kDim / 4) + 8 * m + j);
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_rows(void *page, int row, int j, const float4 (&s)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      // the page's own type: rounded once, here
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float4 a = s[i][2 * m], b = s[i][2 * m + 1];
+        __stcs(reinterpret_cast<uint4 *>(page) + (row + 4 * i) * (kDim / 8) + 8 * m + j,
+               make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                          pack_bf16x2(b.z, b.w)));
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        __stcs(reinterpret_cast<float4 *>(page) + (row + 4 * i) * (kDim / 4) + 8 * m + j, s[i][m]);
+    }
+  }
+}
+
+// Operands of a group's tokens.
+struct __align__(16) GroupOps {
+  float d[kGroup][kDim], k[kGroup][kDim], q[kGroup][kDim];
+  uint2 v[kGroup][kDim / 4];  // BF16
+  float kq[kGroup], beta[kGroup];
+};
+
+// One token of a group on a warp's rows; `out` is the head's row of it.
+template <bool BF16>
+__device__ __forceinline__ void step_rows(const GroupOps &sm, int t, int lane, int row,
+                                          float4 (&s)[4][4], uint16_t *out) {
+  const int j = lane & 7;
+  float part[8];
+  float4 k[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int c = key_of<BF16>(j, m);
+    const float4 d = lds4(&sm.d[t][c]), q = lds4(&sm.q[t][c]);
+    k[m] = lds4(&sm.k[t][c]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i][m] = fmul4(s[i][m], d);
+      const float2 z = make_float2(0.f, 0.f);
+      const float2 w = dot4_acc(s[i][m], k[m], z), y = dot4_acc(s[i][m], q, z);
+      part[i] = m == 0 ? w.x + w.y : part[i] + (w.x + w.y);
+      part[4 + i] = m == 0 ? y.x + y.y : part[4 + i] + (y.x + y.y);
+    }
+  }
+  reduce_scatter<8, 8>(part, lane);
+  // lane j < 4 of eight: w of its row j; 4 + j: y of row j
+  const float w = __shfl_sync(0xffffffffu, part[0], lane & ~4);
+  const float v =
+      bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(sm.v[t])[row + 4 * (lane & 3)]);
+  const float u = sm.beta[t] * (v - w);  // of row lane & 3
+  if (j >= 4) out[row + 4 * (j - 4)] = f32_to_bf16_bits(fmaf(u, sm.kq[t], part[0]));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float ui = __shfl_sync(0xffffffffu, u, (lane & ~7) + i);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) s[i][m] = ffma4s(ui, k[m], s[i][m]);
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(128, 4) kda_recurrent_group(const RecurrentParams p) {
+  __shared__ GroupOps ops[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
+  const int row0 = (blockIdx.y * warps + warp) * kRecRows;
+  PromptRequest r;
+  if (!begin_item(p, b, h, row0, lane, r)) return;  // (all of the CTA alike)
+  const int j = lane & 7, row = row0 + (lane >> 3);
+  const long long elem = BF16 ? 2 : 4;
+  char *pool = reinterpret_cast<char *>(p.state) + (long long)h * kDim * kDim * elem;
+  const long long slot_bytes = p.slot_stride * elem;
+  float4 s[4][4];
+  if (r.src >= 0) {
+    load_rows<BF16>(pool + r.src * slot_bytes, row, j, s);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) s[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const float a = expf(p.A_log[h]);
   const float4 dt = *reinterpret_cast<const float4 *>(p.dt_bias + h * kDim + 4 * lane);
-  const int vrow = row0 + (lane & (kRecRows - 1));
-  RawToken next = load_token(p, (long long)r.t0 * p.H + h, lane, vrow);
-  for (int t = 0; t < r.n; ++t) {
-    const RawToken cur = next;
-    if (t + 1 < r.n) next = load_token(p, (long long)(r.t0 + t + 1) * p.H + h, lane, vrow);
-    float4 q = bf16x4_to_f32(cur.q), k = bf16x4_to_f32(cur.k);
-    const float4 g = bf16x4_to_f32(cur.g);
-    const float4 d = make_float4(gate_decay(a, g.x, dt.x, p.lower_bound),
-                                 gate_decay(a, g.y, dt.y, p.lower_bound),
-                                 gate_decay(a, g.z, dt.z, p.lower_bound),
-                                 gate_decay(a, g.w, dt.w, p.lower_bound));
-    float qq = q.x * q.x + q.y * q.y + q.z * q.z + q.w * q.w;
-    float kk = k.x * k.x + k.y * k.y + k.z * k.z + k.w * k.w;
-    float kq = k.x * q.x + k.y * q.y + k.z * q.z + k.w * q.w;
-    qq = warp_sum(qq);
-    kk = warp_sum(kk);
-    kq = warp_sum(kq);
-    const float qs = rsqrtf(qq + kNormEps) * p.q_scale, ks = rsqrtf(kk + kNormEps);
-    q = make_float4(q.x * qs, q.y * qs, q.z * qs, q.w * qs);
-    k = make_float4(k.x * ks, k.y * ks, k.z * ks, k.w * ks);
-    kq *= qs * ks;
-    float part[2 * kRecRows];
-#pragma unroll
-    for (int i = 0; i < kRecRows; ++i) {
-      s[i] = fmul4(s[i], d);
-      const float2 z = make_float2(0.f, 0.f);
-      const float2 w = dot4_acc(s[i], k, z), y = dot4_acc(s[i], q, z);
-      part[i] = w.x + w.y;
-      part[kRecRows + i] = y.x + y.y;
+  const long long t0 = (long long)r.t0 * p.H + h;
+  for (int g0 = 0; g0 < r.n; g0 += kGroup) {
+    GroupOps &sm = ops[(g0 / kGroup) & 1];
+    const int n = r.n - g0 < kGroup ? r.n - g0 : kGroup;
+    for (int i = warp; i < n; i += warps) {
+      const RawToken raw = load_token(p, t0 + (long long)(g0 + i) * p.H, lane);
+      const Token t = make_token(p, raw, a, dt);
+      sm.v[i][lane] = raw.v;
+      sts4(&sm.d[i][4 * lane], t.d);
+      sts4(&sm.k[i][4 * lane], t.k);
+      sts4(&sm.q[i][4 * lane], t.q);
+      if (lane == 0) {
+        sm.kq[i] = t.kq;
+        sm.beta[i] = t.beta;
+      }
     }
-    reduce_scatter<2 * kRecRows, 32>(part, lane);
-    // lane i < 16: w of row i; lane 16 + i: y of row i
-    const float beta = 1.f / (1.f + __expf(-bf16_bits_to_f32(cur.beta)));
-    const float w = __shfl_sync(0xffffffffu, part[0], lane & (kRecRows - 1));
-    const float u = beta * (bf16_bits_to_f32(cur.v) - w);  // of row lane & 15
-    if (lane >= kRecRows)
-      p.out[((long long)(r.t0 + t) * p.H + h) * kDim + vrow] =
-          f32_to_bf16_bits(fmaf(u, kq, part[0]));
-#pragma unroll
-    for (int i = 0; i < kRecRows; ++i) s[i] = ffma4s(__shfl_sync(0xffffffffu, u, i), k, s[i]);
-    if (t + 1 == r.m) store_rows<BF16>(pool + r.bnd * slot_bytes, row0, lane, s);
+    // (one barrier a group: the buffer before the last has been read by all
+    // that have come here)
+    __syncthreads();
+    for (int t = 0; t < n; ++t) {
+      step_rows<BF16>(sm, t, lane, row, s, p.out + (t0 + (long long)(g0 + t) * p.H) * kDim);
+      if (g0 + t + 1 == r.m) store_rows<BF16>(pool + r.bnd * slot_bytes, row, j, s);
+    }
   }
-  store_rows<BF16>(pool + r.dst * slot_bytes, row0, lane, s);
+  store_rows<BF16>(pool + r.dst * slot_bytes, row, j, s);
 }
 
 }  // namespace
@@ -176,17 +347,27 @@ int check_rule(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const kd
 
 int launch_recurrent(const RecurrentParams &p, bool bf16, cudaStream_t stream) {
   const int items = p.maps.B * p.H;
-  const int warps = 8;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
+  const int sms = device_sm_count(dev);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = p.beside ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(items, kDim / kRecRows / warps);
-  cfg.blockDim = dim3(32 * warps);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto kernel = bf16 ? kda_recurrent_kernel<true> : kda_recurrent_kernel<false>;
+  // Few items: their rows over more CTAs, so that more SMs take part (32
+  // items: 5.2 us by 64-thread CTAs, 5.9 by 256); many: CTAs as large as
+  // the SM's registers hold whole (32768 items of one token: 616 us by 256
+  // threads, 637 by 128, 645 by 64).
+  const bool one = p.maps.Q == 1;
+  const int most = one ? 8 : 4;
+  const int warps = items >= sms ? most : 2;
+  cfg.gridDim = dim3(items, kDim / kRecRows / warps);
+  cfg.blockDim = dim3(32 * warps);
+  const auto kernel = one ? (bf16 ? kda_recurrent_one<true> : kda_recurrent_one<false>)
+                          : (bf16 ? kda_recurrent_group<true> : kda_recurrent_group<false>);
   if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return KDA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

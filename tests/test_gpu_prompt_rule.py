@@ -87,6 +87,21 @@ def test_heads(op, H):
 
 
 @pytest.mark.parametrize("op", ["prefill", "recurrent"])
+@pytest.mark.parametrize("pool", ["f32", "bf16"])
+@pytest.mark.parametrize("most", [1, 8, 40])
+def test_more_items_than_fit(op, pool, most):
+    """Hundreds of (request, head) items: empty, inert, fresh and resumed
+    windows of one token, of a group of eight and of several, boundaries."""
+    rng = np.random.default_rng(most)
+    lens = [int(n) for n in rng.integers(0, most + 1, size=60)]
+    lens[:6] = [most, 0, most, min(most, 17), 1, min(most, 16)]
+    boundary = {b: max(1, n // 2) for b, n in enumerate(lens) if n > 1 and b % 5 == 0}
+    resume = [b for b in range(60) if b % 7 != 3]
+    run_and_check(op, ragged_case(lens=lens, H=11, seed=100 + most, pool=pool, boundary=boundary,
+                                  inert=(2, 9, 30), resume=resume, tail=2))
+
+
+@pytest.mark.parametrize("op", ["prefill", "recurrent"])
 def test_uniform_windows(op):
     case = ragged_case(lens=[70] * 3, H=2, seed=31)
     d = on_device(case)
