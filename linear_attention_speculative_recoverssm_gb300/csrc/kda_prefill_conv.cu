@@ -3,11 +3,15 @@
 //   out_t = BF16(silu(bias + sum_{i<4} w_i s_{t+i})),
 //   s = [3 window entries (zeros without a source), x_0 .. x_{n-1}],
 // and the last three entries of s after n (and after m) tokens become the
-// destination's (the boundary's) window.  Nothing but bandwidth: 6 D bytes
-// read and 6 D written per token.  A thread takes 8 channels (16-byte
-// accesses) and a run of kTokens consecutive tokens, keeping the three
-// entries before the current one in registers, so x is read once but for the
-// three entries before each run.
+// destination's (the boundary's) window.  6 D bytes read and 6 D written per
+// token and nothing used twice: bandwidth, if enough is in flight and the
+// arithmetic (4 FMA, 2 functions of the special unit per element) stays under
+// it.  A thread takes 4 channels and a run of consecutive tokens, keeping the
+// three entries before the current one in registers, so x is read once but for
+// the three entries before each run; 8 tokens are asked for at a time.  4
+// channels a thread and not 8: 80 registers, 24 warps an SM (8 channels: 127,
+// 16 warps).  16384 tokens, 32 heads: 138 us, 5.8 TB/s (of 6.77 measured for a
+// copy); 8 channels and runs of 16 tokens: 215.
 #include <cuda_runtime.h>
 
 #include "../../include/kda_recoverssm.h"
@@ -18,13 +22,14 @@ namespace kda {
 namespace {
 
 constexpr int kPcThreads = 128;
-constexpr int kPcTokens = 16;  // tokens of a CTA
+constexpr int kAhead = 8;      // tokens whose loads are in flight at a time
 
 struct ConvParams {
   const uint16_t *x, *w, *bias;  // [n_tokens, 3 D], [3, 4, D], [3 D] or nullptr
   uint16_t *window;              // [n_slots, 3 D, width]
   long long slot_stride;
   int width, H;
+  int run;  // tokens of a CTA
   uint16_t *q, *k, *v;  // [n_tokens, H, 128]
   PromptMaps maps;
 };
@@ -47,29 +52,35 @@ __device__ __forceinline__ int find_request(const int32_t *qsl, int B, int t, in
   return lo;
 }
 
-__device__ __forceinline__ float silu_f32(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+// z / (1 + 2^(-z log2 e)), the two functions of the special unit once each
+// (their plain forms' care for subnormals has no use here: 1 + e stays normal,
+// or overflows to a reciprocal of zero)
+__device__ __forceinline__ float2 silu2(float2 z) {
+  const float2 t = fmul2(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = __fadd2_rn(e, make_float2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return fmul2(z, r);
+}
 
-struct Eight {
-  float f[8];
+struct Four {
+  float2 a, b;
 };
 
-__device__ __forceinline__ Eight unpack8(uint4 b) {
-  Eight e;
-  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    e.f[2 * i] = __uint_as_float(w[i] << 16);
-    e.f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-  return e;
+__device__ __forceinline__ Four unpack4(uint2 x) {
+  return Four{make_float2(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u)),
+              make_float2(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u))};
 }
 
-__device__ __forceinline__ uint4 pack8(const uint16_t (&e)[8]) {
-  return make_uint4(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16),
-                    e[4] | ((uint32_t)e[5] << 16), e[6] | ((uint32_t)e[7] << 16));
+__device__ __forceinline__ uint32_t silu_pair(float2 z) {
+  const __nv_bfloat162 r = __float22bfloat162_rn(silu2(z));
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-__global__ void __launch_bounds__(kPcThreads) kda_prefill_conv_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kPcThreads, 6) kda_prefill_conv_kernel(const ConvParams p) {
   const PromptMaps &mp = p.maps;
   const int lane = threadIdx.x & 31;
   // every window is looked at once, by the first channel CTAs
@@ -83,19 +94,20 @@ __global__ void __launch_bounds__(kPcThreads) kda_prefill_conv_kernel(const Conv
   }
   const int D = p.H * kDim;
   const int group = blockIdx.y * kPcThreads + threadIdx.x;
-  const bool active = group < 3 * D / 8;
-  const int ch = active ? 8 * group : 0, part = ch / D, hc = ch - part * D;
-  const int first = blockIdx.x * kPcTokens;
-  const int past = first + kPcTokens < mp.n_tokens ? first + kPcTokens : mp.n_tokens;
-  Eight w[4], bias;
+  const bool active = group < 3 * D / 4;
+  const int ch = active ? 4 * group : 0, part = ch / D, hc = ch - part * D;
+  const int first = blockIdx.x * p.run;
+  const int past = mp.n_tokens - first > p.run ? first + p.run : mp.n_tokens;
+  Four w[4], bias;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = unpack8(__ldg(reinterpret_cast<const uint4 *>(p.w + (long long)(part * 4 + i) * D + hc)));
-  bias = p.bias != nullptr ? unpack8(__ldg(reinterpret_cast<const uint4 *>(p.bias + ch)))
-                           : unpack8(make_uint4(0, 0, 0, 0));
-  uint16_t *out = part == 0 ? p.q : (part == 1 ? p.k : p.v);
+    w[i] = unpack4(__ldg(reinterpret_cast<const uint2 *>(p.w + (long long)(part * 4 + i) * D + hc)));
+  bias = unpack4(p.bias != nullptr ? __ldg(reinterpret_cast<const uint2 *>(p.bias + ch))
+                                   : make_uint2(0, 0));
+  uint16_t *out = (part == 0 ? p.q : (part == 1 ? p.k : p.v)) + hc;
+  const uint16_t *x = p.x + ch;
   const auto input = [&](int t) {
-    return __ldg(reinterpret_cast<const uint4 *>(p.x + (long long)t * (3 * D) + ch));
+    return __ldg(reinterpret_cast<const uint2 *>(x + (long long)t * (3 * D)));
   };
   int b = mp.qsl != nullptr ? find_request(mp.qsl, mp.B, first, lane) : first / mp.Q;
   for (; b < mp.B; ++b) {  // the requests that reach into this run
@@ -112,32 +124,39 @@ __global__ void __launch_bounds__(kPcThreads) kda_prefill_conv_kernel(const Conv
     if (end > r.t0 + r.n) end = r.t0 + r.n;
     // an inert request is skipped: the step over its tokens writes zeros
     if (!active || r.dst < 0 || t >= end) continue;
-    uint4 h0, h1, h2;  // the three entries before token t
+    uint2 h0, h1, h2;  // the three entries before token t
     if (starts) {
-      uint16_t e[3][8];
-      const uint16_t *win = p.window + (long long)(r.src < 0 ? 0 : r.src) * p.slot_stride +
-                            (long long)ch * p.width;
+      h0 = h1 = h2 = make_uint2(0, 0);
+      if (r.src >= 0) {
+        const uint16_t *win = p.window + r.src * p.slot_stride + (long long)ch * p.width;
+        uint32_t e[3][4];
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) e[i][c] = r.src >= 0 ? win[c * p.width + i] : (uint16_t)0;
-      h0 = pack8(e[0]);
-      h1 = pack8(e[1]);
-      h2 = pack8(e[2]);
+          for (int i = 0; i < 3; ++i) e[i][c] = win[c * p.width + i];
+        h0 = make_uint2(e[0][0] | e[0][1] << 16, e[0][2] | e[0][3] << 16);
+        h1 = make_uint2(e[1][0] | e[1][1] << 16, e[1][2] | e[1][3] << 16);
+        h2 = make_uint2(e[2][0] | e[2][1] << 16, e[2][2] | e[2][3] << 16);
+      }
       // entries n - 3 .. n - 1 are what the request leaves, m - 3 .. m - 1
       // its boundary's
 #pragma unroll 1
       for (int which = 0; which < 2; ++which) {
         const int slot = which == 0 ? r.bnd : r.dst, at = which == 0 ? r.m : r.n;
         if (slot < 0) continue;
-        uint16_t *to = p.window + (long long)slot * p.slot_stride + (long long)ch * p.width;
-#pragma unroll 1
+        uint16_t *to = p.window + slot * p.slot_stride + (long long)ch * p.width;
+        uint2 v[3];
+#pragma unroll
         for (int i = 0; i < 3; ++i) {
           const int j = at - 3 + i;  // >= -2: at >= 1
-          const uint4 v = j >= 0 ? input(r.t0 + j) : (j == -1 ? h2 : h1);
-          const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+          v[i] = j >= 0 ? input(r.t0 + j) : (j == -1 ? h2 : h1);
+        }
 #pragma unroll
-          for (int c = 0; c < 8; ++c) to[c * p.width + i] = (uint16_t)(vw[c / 2] >> (16 * (c & 1)));
+        for (int i = 0; i < 3; ++i) {
+          to[i] = (uint16_t)v[i].x;
+          to[p.width + i] = (uint16_t)(v[i].x >> 16);
+          to[2 * p.width + i] = (uint16_t)v[i].y;
+          to[3 * p.width + i] = (uint16_t)(v[i].y >> 16);
         }
       }
     } else {
@@ -145,31 +164,29 @@ __global__ void __launch_bounds__(kPcThreads) kda_prefill_conv_kernel(const Conv
       h1 = input(t - 2);
       h2 = input(t - 1);
     }
-    Eight s0 = unpack8(h0), s1 = unpack8(h1), s2 = unpack8(h2);
-#pragma unroll 4
-    for (; t < end; ++t) {
-      const Eight x = unpack8(input(t));
-      uint32_t res[4];
-#pragma unroll
-      for (int c = 0; c < 8; c += 2) {
-        float z[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // in tap order, as in kda_layer_prologue
-          float acc = fmaf(s0.f[c + e], w[0].f[c + e], bias.f[c + e]);
-          acc = fmaf(s1.f[c + e], w[1].f[c + e], acc);
-          acc = fmaf(s2.f[c + e], w[2].f[c + e], acc);
-          acc = fmaf(x.f[c + e], w[3].f[c + e], acc);
-          z[e] = silu_f32(acc);
-        }
-        res[c / 2] = pack_bf16x2(z[0], z[1]);
-      }
-      *reinterpret_cast<uint4 *>(out + (long long)t * D + hc) =
-          make_uint4(res[0], res[1], res[2], res[3]);
+    Four s0 = unpack4(h0), s1 = unpack4(h1), s2 = unpack4(h2);
+    const auto step = [&](uint2 raw, int at) {
+      const Four in = unpack4(raw);
+      // in tap order, as in kda_layer_prologue
+      Four z{ffma2(s0.a, w[0].a, bias.a), ffma2(s0.b, w[0].b, bias.b)};
+      z = Four{ffma2(s1.a, w[1].a, z.a), ffma2(s1.b, w[1].b, z.b)};
+      z = Four{ffma2(s2.a, w[2].a, z.a), ffma2(s2.b, w[2].b, z.b)};
+      z = Four{ffma2(in.a, w[3].a, z.a), ffma2(in.b, w[3].b, z.b)};
+      *reinterpret_cast<uint2 *>(out + (long long)at * D) =
+          make_uint2(silu_pair(z.a), silu_pair(z.b));
       s0 = s1;
       s1 = s2;
-      s2 = x;
+      s2 = in;
+    };
+    // kAhead tokens are asked for at a time
+    for (; end - t >= kAhead; t += kAhead) {
+      uint2 raw[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) raw[i] = input(t + i);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) step(raw[i], t + i);
     }
+    for (; t < end; ++t) step(input(t), t);
   }
 }
 
@@ -208,9 +225,18 @@ extern "C" int kda_prefill_conv(
   p.v = v;
   p.maps = kda::make_prompt_maps(sources, destinations, boundaries, boundary_lens,
                                  query_start_loc, n_tokens, n_slots, B, Q, null_slot, status);
-  const int groups = 3 * H * KDA_HEAD_DIM / 8;
-  const dim3 grid((n_tokens + kda::kPcTokens - 1) / kda::kPcTokens,
-                  (groups + kda::kPcThreads - 1) / kda::kPcThreads);
+  const int channels = (3 * H * KDA_HEAD_DIM / 4 + kda::kPcThreads - 1) / kda::kPcThreads;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
+  const int sms = kda::device_sm_count(dev);
+  if (sms < 1) return KDA_ERR_CUDA;
+  // Long runs where they leave every SM its fill (16384 tokens, 32 heads: 171
+  // us by runs of 16 tokens, 153 by 32, 147 by 64); a few tokens are a chain of
+  // loads, and run side by side (37 tokens: 7 us by 4, 13 by 16).
+  int run = 64;
+  while (run > 4 && (long long)((n_tokens - 1) / run + 1) * channels < 4 * sms) run /= 2;
+  p.run = run;
+  const dim3 grid((n_tokens - 1) / run + 1, channels);
   kda::kda_prefill_conv_kernel<<<grid, kda::kPcThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -187,6 +187,18 @@ def test_conv_ragged(lens, H, width):
     check_conv(case, run_conv(case))
 
 
+@pytest.mark.parametrize("H,tokens", [(16, 900), (16, 1700), (17, 3500)])
+def test_conv_longer_runs(H, tokens):
+    """Enough tokens that a thread takes runs of 16, 32 and 64 of them:
+    requests that end and begin everywhere in a run."""
+    rng = np.random.default_rng(tokens)
+    lens = [int(n) for n in rng.integers(0, 90, size=tokens // 90)] + [64, 1, 2, 63, 65, 128]
+    lens.append(max(tokens - sum(lens), 1))
+    boundary = {b: max(1, n // 3) for b, n in enumerate(lens) if n and b % 3 != 1}
+    case = conv_case(lens, H, seed=tokens, width=4, boundary=boundary, tail=5, inert=(2, 7))
+    check_conv(case, run_conv(case))
+
+
 def test_conv_in_place_and_shared():
     """Windows left in their own source (as destination or as boundary), for
     prompts of one to many runs, and one source for several requests."""
