@@ -83,6 +83,7 @@ extern "C" {
 #define KDA_MAX_WINDOW 8
 #define KDA_MAX_LAYERS 64
 #define KDA_PROMPT_MAX_HEADS 1024 /* heads of the prompt operators */
+#define KDA_PLAN_MAX_REQUESTS (1 << 24) /* requests of one kda_slot_plan */
 
 typedef uint16_t kda_bf16;
 
@@ -539,7 +540,8 @@ int kda_layer_step_noalloc(const kda_bf16 *x, const kda_bf16 *conv_weight,
  *   computed_lens, new_lens [B] int32; block_table [B, max_blocks] int32,
  *   rows table_row_stride >= max_blocks elements apart; sources,
  *   destinations, boundaries, boundary_lens [B], query_start_loc [B + 1]
- *   int32 outputs.  B == 0 writes query_start_loc[0] and *free_next.
+ *   int32 outputs.  B == 0 writes query_start_loc[0] and *free_next; B is at
+ *   most KDA_PLAN_MAX_REQUESTS.
  */
 int kda_slot_plan(const int32_t *computed_lens, const int32_t *new_lens, int32_t *block_table,
                   int64_t table_row_stride, int max_blocks, const int32_t *free_slots,

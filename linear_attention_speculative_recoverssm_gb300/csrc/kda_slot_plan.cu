@@ -1,11 +1,13 @@
 // kda_slot_plan: packed offsets, block table entries and slot maps from the
 // requests' lengths (the align mode's bookkeeping).  Integer work: per
 // request a few divisions, and two prefix sums over the requests (tokens,
-// and free slots taken).  One cluster of up to 8 CTAs: CTA c owns a
+// and free slots taken).  One cluster of up to 16 CTAs: CTA c owns a
 // contiguous part of the requests and sums it; the CTAs exchange their sums
-// through distributed shared memory; then each places its requests, 1024 at
-// a time, behind what comes before them.  Latency is all there is: a few
-// dependent loads and two barriers.
+// through distributed shared memory; then each places its requests behind
+// what comes before them.  Latency is all there is: three loads that depend
+// on one another, two barriers, the scans by shuffles.  48 requests 7 us;
+// 8192 requests 14.4 us, most of it the 4 MB of table entries that the prompts
+// pass over.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -16,8 +18,12 @@
 namespace kda {
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanMaxCtas = 8;  // the portable cluster size
+// A thread a request, and many CTAs before large ones, as every SM of the
+// cluster stores for itself: 8192 requests take 14.4 us by 16 CTAs of 512,
+// 16.7 by 8 of 1024, 23 by 16 of 256 (two requests a thread, worked out twice).
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxCtas = 16;   // the largest cluster
+constexpr int kPlanPortable = 8;   // the largest that needs no permission
 
 struct PlanParams {
   const int32_t *computed, *fresh;  // [B]
@@ -45,13 +51,18 @@ struct PlanRequest {
   int src;           // slot it goes on from, or null
 };
 
-__device__ __forceinline__ PlanRequest plan_request(const PlanParams &p, int b, bool say) {
+__device__ __forceinline__ PlanRequest no_request() {
   PlanRequest r;
-  const int c = p.computed[b], n = p.fresh[b];
-  r.tokens = n > 0 ? n : 0;
+  r.tokens = r.bnd_len = r.src = 0;
   r.live = r.crosses = r.new_last = r.new_bnd = false;
   r.cur = r.last = -1;
-  r.bnd_len = 0;
+  return r;
+}
+
+__device__ __forceinline__ PlanRequest plan_request(const PlanParams &p, int b, bool say) {
+  PlanRequest r = no_request();
+  const int c = p.computed[b], n = p.fresh[b];
+  r.tokens = n > 0 ? n : 0;
   r.src = p.null_slot;
   const long long end = (long long)c + n;
   if (c < 0 || n < 0 || end > (long long)p.max_blocks * p.block_size || end > 0x7fffffffLL) {
@@ -78,68 +89,88 @@ __device__ __forceinline__ PlanRequest plan_request(const PlanParams &p, int b, 
   return r;
 }
 
-// Sum over the CTA's threads of (tokens, slots), and this thread's exclusive
-// prefix; every thread gets both.
+// The two halves of a cluster's barrier (every thread of every CTA does both).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Tokens and free slots, counted.
 struct Pair {
   long long tokens;
   int slots;
 };
 
-__device__ __forceinline__ Pair block_scan(Pair mine, Pair *warp_sums, Pair &total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Pair inc = mine;
+// The sums over the lanes up to and with this one.
+__device__ __forceinline__ Pair warp_scan(Pair x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, inc.tokens, o);
-    const int s = __shfl_up_sync(0xffffffffu, inc.slots, o);
+    const long long t = __shfl_up_sync(0xffffffffu, x.tokens, o);
+    const int s = __shfl_up_sync(0xffffffffu, x.slots, o);
     if (lane >= o) {
-      inc.tokens += t;
-      inc.slots += s;
+      x.tokens += t;
+      x.slots += s;
     }
   }
+  return x;
+}
+
+// Sum over the CTA's threads, and over the threads before this one.
+__device__ __forceinline__ Pair block_scan(Pair mine, Pair *warp_sums, Pair &total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Pair inc = warp_scan(mine);
   __syncthreads();  // the sums of an earlier scan have been read
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  Pair before{0, 0};
-  total = Pair{0, 0};
-  const int warps = blockDim.x >> 5;
-  for (int w = 0; w < warps; ++w) {
-    if (w == warp) before = total;
-    total.tokens += warp_sums[w].tokens;
-    total.slots += warp_sums[w].slots;
-  }
-  return Pair{before.tokens + inc.tokens - mine.tokens, before.slots + inc.slots - mine.slots};
+  // each warp scans the warps' sums for itself (there are at most 32)
+  const Pair sums = warp_scan(lane < (blockDim.x >> 5) ? warp_sums[lane] : Pair{0, 0});
+  total.tokens = __shfl_sync(0xffffffffu, sums.tokens, 31);
+  total.slots = __shfl_sync(0xffffffffu, sums.slots, 31);
+  const long long t = __shfl_sync(0xffffffffu, sums.tokens, (warp + 31) & 31);
+  const int s = __shfl_sync(0xffffffffu, sums.slots, (warp + 31) & 31);
+  return Pair{(warp ? t : 0) + inc.tokens - mine.tokens, (warp ? s : 0) + inc.slots - mine.slots};
 }
 
 __global__ void __launch_bounds__(kPlanThreads) kda_slot_plan_kernel(const PlanParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ Pair warp_sums[kPlanThreads / 32];
+  __shared__ Pair warp_sums[32];
   __shared__ Pair cta_sum;
   const int ctas = gridDim.x, rank = blockIdx.x;
   const int lane = threadIdx.x & 31;
   const int b_begin = (int)((long long)p.B * rank / ctas);
   const int b_end = (int)((long long)p.B * (rank + 1) / ctas);
   const int head = *p.free_head;
-  // this CTA's requests, summed
-  Pair sum{0, 0};
+  // this CTA's requests, summed; where each thread has one at most, it is
+  // worked out here and kept
+  const bool once = b_end - b_begin <= (int)blockDim.x;
+  PlanRequest r = no_request();
+  Pair sum{0, 0}, total;
   for (int b = b_begin + threadIdx.x; b < b_end; b += blockDim.x) {
-    const PlanRequest r = plan_request(p, b, false);
+    r = plan_request(p, b, once);
     sum.tokens += r.tokens;
     sum.slots += r.new_last + r.new_bnd;
   }
-  Pair total;
-  block_scan(sum, warp_sums, total);
-  if (threadIdx.x == 0) cta_sum = total;
-  cluster.sync();  // every CTA's sum is there, and every CTA has read free_head
+  const Pair before = block_scan(sum, warp_sums, total);
   Pair base{0, 0}, all{0, 0};
-  for (int c = 0; c < ctas; ++c) {
-    const Pair s = *cluster.map_shared_rank(&cta_sum, c);
-    if (c == rank) base = all;
-    all.tokens += s.tokens;
-    all.slots += s.slots;
+  if (ctas == 1) {
+    all = total;
+    __syncthreads();  // free_head has been read: free_next may be its place
+  } else {
+    if (threadIdx.x == 0) cta_sum = total;
+    cluster.sync();  // every CTA's sum is there, and every CTA has read free_head
+    const Pair sums =
+        warp_scan(lane < ctas ? *cluster.map_shared_rank(&cta_sum, lane) : Pair{0, 0});
+    all.tokens = __shfl_sync(0xffffffffu, sums.tokens, 31);
+    all.slots = __shfl_sync(0xffffffffu, sums.slots, 31);
+    const long long t = __shfl_sync(0xffffffffu, sums.tokens, (rank + 31) & 31);
+    const int s = __shfl_sync(0xffffffffu, sums.slots, (rank + 31) & 31);
+    if (rank > 0) base = Pair{t, s};
+    cluster_arrive();  // waited for at the end: no CTA leaves while its sum is read
   }
-  cluster.sync();  // no CTA leaves while its sum is still read
   const bool head_ok = head >= 0 && head <= p.n_free;
   const int avail = head_ok ? p.n_free - head : 0;
   if (rank == ctas - 1 && threadIdx.x == 0) {
@@ -149,18 +180,20 @@ __global__ void __launch_bounds__(kPlanThreads) kda_slot_plan_kernel(const PlanP
   }
   for (int b0 = b_begin; b0 < b_end; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
-    PlanRequest r;
-    r.tokens = 0;
-    r.live = r.crosses = r.new_last = r.new_bnd = false;
-    r.cur = r.last = -1;
-    if (b < b_end) r = plan_request(p, b, true);
+    Pair at = before;
+    if (!once) {
+      r = b < b_end ? plan_request(p, b, true) : no_request();
+      Pair tile;
+      at = block_scan(Pair{r.tokens, r.new_last + r.new_bnd}, warp_sums, tile);
+      at.tokens += base.tokens;
+      at.slots += base.slots;
+      base.tokens += tile.tokens;
+      base.slots += tile.slots;
+    } else {
+      at.tokens += base.tokens;
+      at.slots += base.slots;
+    }
     const int need = r.new_last + r.new_bnd;
-    Pair tile;
-    Pair at = block_scan(Pair{r.tokens, need}, warp_sums, tile);
-    at.tokens += base.tokens;
-    at.slots += base.slots;
-    base.tokens += tile.tokens;
-    base.slots += tile.slots;
     // A request that the free list has no slots for is not served, and so
     // neither is any behind it that needs one (their places in the list lie
     // further on): the first one's place is how far the list was used.
@@ -201,6 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads) kda_slot_plan_kernel(const PlanP
       for (int j = from + lane; j < to; j += 32) row[j] = p.null_slot;
     }
   }
+  if (ctas > 1) cluster_wait();
 }
 
 }  // namespace
@@ -213,8 +247,8 @@ extern "C" int kda_slot_plan(const int32_t *computed_lens, const int32_t *new_le
                              int32_t *destinations, int32_t *boundaries, int32_t *boundary_lens,
                              int B, int block_size, int null_slot, int32_t *status,
                              void *stream) {
-  if (B < 0 || max_blocks < 1 || table_row_stride < max_blocks || n_free < 0 || block_size < 1 ||
-      null_slot < -1)
+  if (B < 0 || B > KDA_PLAN_MAX_REQUESTS || max_blocks < 1 || table_row_stride < max_blocks ||
+      n_free < 0 || block_size < 1 || null_slot < -1)
     return KDA_ERR_ARG;
   if (!free_head || !free_next || !query_start_loc) return KDA_ERR_ARG;
   if (B > 0 && (!computed_lens || !new_lens || !block_table || !sources || !destinations ||
@@ -239,9 +273,8 @@ extern "C" int kda_slot_plan(const int32_t *computed_lens, const int32_t *new_le
   p.block_size = block_size;
   p.null_slot = null_slot;
   p.status = status;
-  // one request per thread while the cluster has room for it
-  int ctas = (B + kda::kPlanThreads - 1) / kda::kPlanThreads;
-  ctas = ctas < 1 ? 1 : (ctas > kda::kPlanMaxCtas ? kda::kPlanMaxCtas : ctas);
+  int ctas = B < 1 ? 1 : (B - 1) / kda::kPlanThreads + 1;
+  if (ctas > kda::kPlanMaxCtas) ctas = kda::kPlanMaxCtas;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ctas;
@@ -249,10 +282,15 @@ extern "C" int kda_slot_plan(const int32_t *computed_lens, const int32_t *new_le
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kda::kPlanThreads);
+  cfg.blockDim = dim3(B >= kda::kPlanThreads ? kda::kPlanThreads
+                                             : (B < 1 ? 32 : (B + 31) / 32 * 32));
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (ctas > kda::kPlanPortable &&
+      cudaFuncSetAttribute(kda::kda_slot_plan_kernel,
+                           cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return KDA_ERR_CUDA;
   if (cudaLaunchKernelEx(&cfg, kda::kda_slot_plan_kernel, p) != cudaSuccess) return KDA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -81,7 +81,7 @@ def test_conv_refusals(lib, over, code):
 
 
 @pytest.mark.parametrize("over", [
-    dict(B=-1), dict(max_blocks=0), dict(stride=3), dict(n_free=-1), dict(bs=0), dict(null=-2),
+    dict(B=-1), dict(B=2 ** 24 + 1), dict(max_blocks=0), dict(stride=3), dict(n_free=-1), dict(bs=0), dict(null=-2),
     dict(head=None), dict(nxt=None), dict(qsl=None), dict(c=None), dict(n=None), dict(table=None),
     dict(free=None), dict(src=None), dict(dst=None), dict(bnd=None), dict(bl=None),
 ])
