@@ -293,3 +293,65 @@ def test_strided_pool():
         assert not bool(wide[:, 2].any())
         d["state"] = d["state"].contiguous()
         verify(op, case, d)
+
+
+def long_case(lens, H, seed, pool="f32", **kw):
+    # (what a state remembers stays under 50 tokens, as in the other cases)
+    return ragged_case(lens=lens, H=H, seed=seed, pool=pool, **kw)
+
+
+@pytest.mark.parametrize("pool", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,boundary", [
+    ([4096], {}), ([4097], {0: 1}), ([4200], {0: 4199}), ([6000], {0: 2048}), ([6000], {0: 2049}),
+    ([4500, 0, 9, 5, 130, 4096], {0: 64 * 35, 3: 2, 4: 100}), ([64 * 33, 64 * 65], {1: 64 * 32 + 1})])
+def test_long_prompts(pool, lens, boundary):
+    """Prompts of 64 chunks and more, few heads: the form that works by
+    segments, boundaries in a segment and at its edges, short and empty
+    requests beside the long ones."""
+    run_and_check("prefill", long_case(lens, 2, seed=sum(lens), pool=pool, boundary=boundary,
+                                       inert=(5,) if len(lens) > 5 and pool == "bf16" else (),
+                                       resume=(0, 3, 4), tail=3))
+
+
+def test_long_prompt_many_heads():
+    """More (request, head) items than the segments' form takes."""
+    run_and_check("prefill", long_case([4100], 77, seed=77, boundary={0: 70}))
+
+
+@pytest.mark.parametrize("n", [1, 5, 8, 9, 64])
+@pytest.mark.parametrize("most", [0, 5000])
+@pytest.mark.parametrize("inert", [(), (0,)])
+def test_one_request(n, most, inert):
+    """A single request, its window far below the longest allowed too."""
+    case = ragged_case(lens=[n], H=3, seed=n, inert=inert, boundary={0: max(1, n - 1)}, resume=(0,))
+    case["Q"] = max(n, most)
+    run_and_check("prefill", case)
+
+
+def test_graphs_share_a_workspace():
+    """Two captured calls of different shapes on one workspace, replayed in
+    turn and again, beside eager calls on it: each as if alone."""
+    import torch
+    from linear_attention_speculative_recoverssm_gb300 import kda_prefill_workspace_bytes
+    cases = [long_case([4300], 2, seed=81, boundary={0: 77}),
+             ragged_case(lens=[70, 1, 130, 20], H=5, seed=82, boundary={2: 33})]
+    need = max(kda_prefill_workspace_bytes(len(c["v"]), len(c["destinations"]), c["v"].shape[1])
+               for c in cases)
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    ds, graphs = [on_device(c) for c in cases], []
+    for c, d in zip(cases, ds):
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            call_rule(ops()["prefill"], c, d, workspace=ws)
+        graphs.append(g)
+    for i in (0, 1, 1, 0):
+        fresh = on_device(cases[i])
+        for name in fresh:
+            ds[i][name].copy_(fresh[name])
+        graphs[i].replay()
+        other = on_device(cases[1 - i])
+        call_rule(ops()["prefill"], cases[1 - i], other, workspace=ws)
+        torch.cuda.synchronize()
+        verify("prefill", cases[i], ds[i])
+        verify("prefill", cases[1 - i], other)
