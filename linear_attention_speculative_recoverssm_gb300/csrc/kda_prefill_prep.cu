@@ -39,7 +39,8 @@ constexpr uint32_t kXBytes = kChunk * kXPitch;
 constexpr uint32_t kYBytes = 32 * kXPitch;
 // Pitches (floats): rows four or eight banks apart, as their readers want.
 constexpr int kLPitch = 36, kL16Pitch = 20, kXPitchF = 68, kYPitch = 40, kLtPitch = 20;
-constexpr int kDPitch = 17;
+constexpr int kDPitch = 20;
+constexpr int kLtSize = 16 * kLtPitch + 16;  // (two blocks apart by half the banks)
 constexpr uint32_t kRowsBytes = kChunk * kDim * 2;  // a chunk's rows of an input
 
 // Shared memory, by phases: the FP16 operands of the products between blocks;
@@ -65,13 +66,22 @@ struct PrepSmem {
     } in;
   } u;
   union {
-    float fac[3][4][128];          // [R, C, Ke][block][channel], times 1024
-    float Lt[4][16 * kLtPitch];    // then the diagonal blocks of L, transposed
+    struct {
+      union {
+        float fac[3][4][128];        // [R, C, Ke][block][channel], times 1024
+        float Lt[4][kLtSize];        // then the diagonal blocks of L, transposed
+      };
+      uint16_t pow[4][128];    // FP16 2^n: of Kd and Qd
+      uint16_t pow32[2][128];  // of the operands at 32, blocks 0 and 3
+      float tot[2][4][128];    // log2 decays of a block's two halves
+    };
+    __align__(16) uint8_t a[kImgBlock];  // then the image's A
   };
-  uint16_t pow[2][4][128];  // FP16 2^n: of Kd and Qd; of the operands at 32
-  float tot[2][4][128];   // log2 decays of a block's two halves
-  // a block's products kn kn^T and qn kn^T, over either half of the channels
-  float part[4][2][2][16 * kDPitch];
+  union {
+    // a block's products kn kn^T and qn kn^T, over either half of the channels
+    __align__(16) float part[4][2][2][16 * kDPitch];
+    uint8_t t[2 * kImgBlock];  // then the image's T
+  };
   float norm[2][kChunk][2];        // sums of squares per channel half
   float beta[kChunk];
   uint64_t landed;  // the item's q, k and raw_g are there
@@ -209,10 +219,33 @@ __device__ __forceinline__ void tile_mm(float (&c)[4], const float *A, int lda, 
   for (int i = 0; i < 4; ++i) c[i] += c1[i] + c2[i];
 }
 
+// Shared memory to global memory, asynchronously (the writes were fenced and
+// waited for); both 16-byte aligned.
+__device__ __forceinline__ void bulk_store(uint8_t *to, const uint8_t *from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to),
+               "r"(smem_u32(from)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// This thread's stores but the N last have read their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void bulk_stores_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // Where the 16-byte piece of channels c .. c + 7 (or columns) of row t lies.
 __device__ __forceinline__ uint32_t img_at(int t, int c) {
   return (uint32_t)(c >> 6) * kImgBlock + (uint32_t)t * 128u +
          (uint32_t)((((c & 63) >> 3) ^ (t & 7)) << 4);
+}
+
+__device__ __forceinline__ int pair_of(int tid) {
+  return (tid & 32) | ((tid & 14) << 1) | ((tid & 16) >> 3) | (tid & 1);
 }
 
 __global__ void __launch_bounds__(kPrepThreads, 2)
@@ -245,7 +278,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   const auto load_head = [&](int tid, const PrefillChunk &ck, int h) {
     braw = __ldg(p.r.beta + (long long)(ck.t0 + min(tid & 63, ck.count - 1)) * H + h);
     a_log = __ldg(p.r.A_log + h);
-    dt = __ldg(reinterpret_cast<const float2 *>(p.r.dt_bias + h * kDim) + (tid & 63));
+    dt = __ldg(reinterpret_cast<const float2 *>(p.r.dt_bias + h * kDim) + pair_of(tid));
   };
   int chunk = blockIdx.x / H, h = blockIdx.x - chunk * H;
   const int chunk_step = gridDim.x / H, h_step = gridDim.x - chunk_step * H;
@@ -270,7 +303,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   const int blk = warp >> 1, hf = warp & 1, g = lane >> 2, tig = lane & 3;
   const int row[2] = {16 * blk + g, 16 * blk + g + 8};
   const int ch0 = hf * 64 + tig * 8;  // slices add 0 and 32
-  const int pr = tid & 63;            // a pair of channels, for the decays
+  // A pair of channels, for the decays: half a warp takes the first four
+  // channels of eight pieces, the other half the last four.
+  const int pr = pair_of(tid);
   const int last = ck.count - 1;
   uint8_t *img = images + (long long)item * kImgBytes;
   // the next item
@@ -284,6 +319,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   const PrefillChunk next = chunks[more ? chunk : 0];
 
   const bool here = mbar_wait_bounded(&sm.landed, phase);
+  if (tid == 0) bulk_stores_read<1>();  // A's place is free (T, asked for last, may not be)
   if (__syncthreads_or(!here)) {  // (nothing else can run out in this kernel)
     if (tid == 0) {
       report(p.r.maps.status, KDA_ERR_TIMEOUT);
@@ -293,15 +329,25 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   }
   // Rows past the chunk's tokens take its last token's inputs (their own may
   // be another request's) and get no weight: decay 1, kn = qn = 0, beta = 0.
+  // (rows g and g + 1 lie in the same banks: odd rows take their slices the
+  // other way round)
   uint4 kraw[2][2], qraw[2][2];  // [slice][token]
+  const bool odd = g & 1;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const uint32_t at = (uint32_t)min(row[r], last) * (kDim * 2) + (uint32_t)ch0 * 2;
-#pragma unroll
-    for (int sl = 0; sl < 2; ++sl) {
-      kraw[sl][r] = *reinterpret_cast<const uint4 *>(sm.u.in.k + at + 64 * sl);
-      qraw[sl][r] = *reinterpret_cast<const uint4 *>(sm.u.in.q + at + 64 * sl);
-    }
+    const uint32_t at0 = at + (odd ? 64u : 0u), at1 = at + (odd ? 0u : 64u);
+    const auto swap = [&](uint4 &x, uint4 &y) {
+      const uint4 u = odd ? y : x;
+      y = odd ? x : y;
+      x = u;
+    };
+    kraw[0][r] = *reinterpret_cast<const uint4 *>(sm.u.in.k + at0);
+    kraw[1][r] = *reinterpret_cast<const uint4 *>(sm.u.in.k + at1);
+    swap(kraw[0][r], kraw[1][r]);
+    qraw[0][r] = *reinterpret_cast<const uint4 *>(sm.u.in.q + at0);
+    qraw[1][r] = *reinterpret_cast<const uint4 *>(sm.u.in.q + at1);
+    swap(qraw[0][r], qraw[1][r]);
   }
   // -- log2 decays and their sums over each half of the block: a thread takes
   //    two channels and the block's 16 tokens in turn -------------------------
@@ -383,7 +429,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         sm.fac[0][j][c] = kImgScale * exp2f_fast(ta[j] + ph[j]);
-        sm.pow[0][j][c] = power(B[j]);
+        sm.pow[j][c] = power(B[j]);
       }
       reinterpret_cast<float *>(img + kImgDecay)[c] =
           exp2f_fast((ta[0] + tb[0]) + (ta[1] + tb[1]) + (ta[2] + tb[2]) + (ta[3] + tb[3]));
@@ -395,8 +441,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
         sm.fac[2][j][c] = kImgScale * exp2f_fast(tb[j] + rest);
         rest += ta[j] + tb[j];
       }
-      sm.pow[1][0][c] = power(B[2] - B[1]);
-      sm.pow[1][3][c] = power(B[3] - B[2]);
+      sm.pow32[0][c] = power(B[2] - B[1]);
+      sm.pow32[1][c] = power(B[3] - B[2]);
     }
   }
   float rk[2], rq[2];
@@ -406,6 +452,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
     rq[r] = rsqrtf(sm.norm[0][row[r]][1] + sm.norm[1][row[r]][1] + kNormEps);
     if (row[r] > last) rk[r] = rq[r] = 0.f;
   }
+  if (tid == 0) bulk_stores_read<0>();  // and T's
   __syncthreads();
 
   // -- the block's own products, and the operands of everything else ---------
@@ -474,7 +521,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
         mma_tf32(dq[n], aq, h0, h1);
       }
     }
-    const uint4 pow32 = *reinterpret_cast<const uint4 *>(&sm.pow[1][blk][c]);
+    const uint4 pow32 = *reinterpret_cast<const uint4 *>(&sm.pow32[blk >> 1][c]);
     const auto times = [](const float2 (&x)[4], const float2 (&f)[4], float2 (&y)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = fmul2(x[e], f[e]);
@@ -515,7 +562,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
       float2 fac[4], x[4];
       uint4 hi, lo;
       load4x2(&sm.fac[0][blk][c], fac);
-      const uint4 pow0 = *reinterpret_cast<const uint4 *>(&sm.pow[0][blk][c]);
+      const uint4 pow0 = *reinterpret_cast<const uint4 *>(&sm.pow[blk][c]);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const uint32_t xat = xs + 8 * r * kXPitch;
@@ -546,10 +593,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = (g + 8 * (i >> 1)) * kDPitch + 8 * n + 2 * tig + (i & 1);
-      sm.part[blk][0][hf][at] = dk[n][i];
-      sm.part[blk][1][hf][at] = dq[n][i];
+    for (int i = 0; i < 4; i += 2) {
+      const int at = (g + 4 * i) * kDPitch + 8 * n + 2 * tig;
+      *reinterpret_cast<float2 *>(&sm.part[blk][0][hf][at]) = make_float2(dk[n][i], dk[n][i + 1]);
+      *reinterpret_cast<float2 *>(&sm.part[blk][1][hf][at]) = make_float2(dq[n][i], dq[n][i + 1]);
     }
   __syncthreads();
 
@@ -611,11 +658,14 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
     float *Lb = sm.Lt[bi];
     const float b = sm.beta[r0 + j];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const int at = j * kDPitch + c;
+    for (int c = 0; c < 16; c += 4) {
+      const float4 p0 = lds4(&sm.part[bi][0][0][j * kDPitch + c]);
+      const float4 p1 = lds4(&sm.part[bi][0][1][j * kDPitch + c]);
+      const float v[4] = {p0.x + p1.x, p0.y + p1.y, p0.z + p1.z, p0.w + p1.w};
       // (above the diagonal the factors may have overflowed: dropped, not
       // multiplied by zero)
-      Lb[c * kLtPitch + j] = c < j ? b * (sm.part[bi][0][0][at] + sm.part[bi][0][1][at]) : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Lb[(c + e) * kLtPitch + j] = c + e < j ? b * v[e] : 0.f;
     }
     __syncwarp();
 #pragma unroll
@@ -665,7 +715,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
         make_float2(sign * c[2], sign * c[3]);
   };
   const auto put_a = [&](int t, int s, float x0, float x1) {  // s even
-    *reinterpret_cast<uint32_t *>(img + kImgA + img_at(t, s & ~7) + (s & 7) * 2) =
+    *reinterpret_cast<uint32_t *>(sm.a + img_at(t, s & ~7) + (s & 7) * 2) =
         h2_bits(__floats2half2_rn(x0, x1));
   };
   // X10 = -X11 (L10 X00) and X32 = -X33 (L32 X22), 16 x 8 a warp
@@ -703,18 +753,22 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
       const int piece = 2 * (tid >> 6) + e, s0 = 8 * (piece & 1);
       if ((piece >> 1) < bt) continue;  // (below: by the products' own warps)
       float2 v[4];
-      const float *pq = &sm.part[bt][1][0][tl * kDPitch + s0];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a0 = pq[2 * i] + pq[16 * kDPitch + 2 * i];
-        const float a1 = pq[2 * i + 1] + pq[16 * kDPitch + 2 * i + 1];
-        const int s = 8 * piece + 2 * i;
-        v[i] = make_float2(s <= t ? a0 * kImgScale : 0.f, s + 1 <= t ? a1 * kImgScale : 0.f);
+      for (int i = 0; i < 2; ++i) {
+        const float4 p0 = lds4(&sm.part[bt][1][0][tl * kDPitch + s0 + 4 * i]);
+        const float4 p1 = lds4(&sm.part[bt][1][1][tl * kDPitch + s0 + 4 * i]);
+        const int s = 8 * piece + 4 * i;
+        v[2 * i] = make_float2(s <= t ? (p0.x + p1.x) * kImgScale : 0.f,
+                               s + 1 <= t ? (p0.y + p1.y) * kImgScale : 0.f);
+        v[2 * i + 1] = make_float2(s + 2 <= t ? (p0.z + p1.z) * kImgScale : 0.f,
+                                   s + 3 <= t ? (p0.w + p1.w) * kImgScale : 0.f);
       }
-      *reinterpret_cast<uint4 *>(img + kImgA + img_at(t, 8 * piece)) = half8(v);
+      *reinterpret_cast<uint4 *>(sm.a + img_at(t, 8 * piece)) = half8(v);
     }
   }
+  fence_proxy_async_smem();
   __syncthreads();
+  if (tid == 0) bulk_store(img + kImgA, sm.a, kImgBlock);
   tile_mm(c, &X[(32 + m32) * kXPitchF + 32], kXPitchF, &Y[n32], kYPitch, 0, m32 / 8 + 2, lane);
   // -- T = X diag(beta): the lower left quarter from registers, the two on the
   //    diagonal from X, zeros above ------------------------------------------
@@ -725,8 +779,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
       const float2 v = make_float2(c[i] * b0, c[i + 1] * b1);
       const __half2 h = __float22half2_rn(v);
       const uint32_t at = img_at(32 + m32 + g + 4 * i, n32) + 4u * tig;
-      *reinterpret_cast<uint32_t *>(img + kImgTHi + at) = h2_bits(h);
-      *reinterpret_cast<uint32_t *>(img + kImgTLo + at) =
+      *reinterpret_cast<uint32_t *>(sm.t + at) = h2_bits(h);
+      *reinterpret_cast<uint32_t *>(sm.t + kImgBlock + at) =
           h2_bits(__float22half2_rn(ffma2(__half22float2(h), make_float2(-1.f, -1.f), v)));
     }
   }
@@ -744,15 +798,18 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
     uint4 th, tl;
     split8(v, th, tl);
     const uint32_t at = img_at(t, s0);
-    *reinterpret_cast<uint4 *>(img + kImgTHi + at) = th;
-    *reinterpret_cast<uint4 *>(img + kImgTLo + at) = tl;
+    *reinterpret_cast<uint4 *>(sm.t + at) = th;
+    *reinterpret_cast<uint4 *>(sm.t + kImgBlock + at) = tl;
     const uint32_t above = img_at(tid & 31, 32 + 8 * ((tid >> 5) & 3));
-    *reinterpret_cast<uint4 *>(img + (tid < 128 ? kImgTHi : kImgTLo) + above) =
+    *reinterpret_cast<uint4 *>(sm.t + (tid < 128 ? 0 : kImgBlock) + above) =
         make_uint4(0, 0, 0, 0);
   }
   ck = next;
+  fence_proxy_async_smem();
   __syncthreads();  // the next item's decay sums take the place of X
+  if (tid == 0) bulk_store(img + kImgTHi, sm.t, 2 * kImgBlock);
   }
+  if (threadIdx.x == 0) bulk_stores_done();
   // beside a chain, this grid completes after it
   if (blockIdx.x == 0 && threadIdx.x == 0) grid_dependency_wait();
 }
