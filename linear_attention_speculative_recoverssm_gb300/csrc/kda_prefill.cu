@@ -18,10 +18,17 @@ constexpr int kListThreads = 1024;
 
 // Segments: where a call has too few (request, head) items to fill half the
 // SMs, the chain of a long prompt leaves the others idle, and the preparation
-// of the next segment runs there meanwhile.  One prompt of 16384 tokens, 32
-// heads: 1000 us in one segment, 892 us in eight.  With more items the chain fills the GPU by itself, and a
-// segment only costs its launches and the state's way through memory.
+// of the next segment runs there meanwhile.  A chunk takes an SM of the chain
+// some 3 us, and one of the preparation 6: up to a quarter of the SMs' items,
+// the rest of the SMs prepare two chunks of each while the chain goes through
+// one, and a segment can be twice the one before it.  Then the chain starts
+// after a short first one, and there are few.  With more items the chain fills
+// the GPU by itself, and a segment only costs its launches and the state's way
+// through memory.  One prompt of 16384 tokens, us in one segment / in eight of
+// 32 chunks / in four from 18 chunks on: 8 heads -- / 867 / 811, 32 heads
+// 1000 / 929 / 856, 64 heads -- / 1273 / 1502.
 constexpr int kSegItems = 76, kSegChunks = 32, kMaxSegments = 16;
+constexpr int kSegDoubleItems = 38, kSegFirst = 16;
 
 struct Workspace {
   int64_t chunks, bases, order, carry, images, bytes;  // offsets
@@ -76,8 +83,8 @@ __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const Pr
         }
       }
       // (the last segment takes what is left: there is nothing where Q is kept)
-      const int done = seg * p.seg_chunks, all = first + rest;
-      int mine = min(max(all - done, 0), p.seg_chunks);
+      const int done = seg_from(p, seg), all = first + rest;
+      int mine = min(max(all - done, 0), seg_from(p, seg + 1) - done);
       long long inc = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -155,7 +162,7 @@ __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const Pr
     const int at = atomicAdd(&bins[min(q.chunks, kListThreads - 1)], 1);
     // (cut off where there was no room)
     for (int seg = 0; seg < p.segments; ++seg)
-      if (p.bases[seg * B + b] < 0) q.chunks = min(q.chunks, seg * p.seg_chunks);
+      if (p.bases[seg * B + b] < 0) q.chunks = min(q.chunks, seg_from(p, seg));
     p.order[at] = q;
   }
 }
@@ -205,11 +212,18 @@ int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const k
   // cuts one in two
   const int most = (Q - 1) / kda::kChunk + 1 + (boundaries != nullptr ? 1 : 0);
   p.segments = 1;
-  if ((long long)B * H <= kda::kSegItems && most >= 2 * kda::kSegChunks) {
+  p.seg_doubles = false;
+  const long long heads = (long long)B * H;
+  if (heads <= kda::kSegDoubleItems && most >= 2 * kda::kSegFirst) {
+    p.seg_doubles = true;
+    while (p.segments < kda::kMaxSegments && kda::kSegFirst * ((2LL << p.segments) - 1) <= most)
+      ++p.segments;
+  } else if (heads <= kda::kSegItems && most >= 2 * kda::kSegChunks) {
     p.segments = (most + kda::kSegChunks / 2) / kda::kSegChunks;
     if (p.segments > kda::kMaxSegments) p.segments = kda::kMaxSegments;
   }
-  p.seg_chunks = (most + p.segments - 1) / p.segments;
+  const int parts = p.seg_doubles ? (1 << p.segments) - 1 : p.segments;
+  p.seg_chunks = (most + parts - 1) / parts;
   p.seg_first = reinterpret_cast<int *>(ws);
   p.bases = reinterpret_cast<int *>(ws + w.bases);
   p.carry = reinterpret_cast<float *>(ws + w.carry);

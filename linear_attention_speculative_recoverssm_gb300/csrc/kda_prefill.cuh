@@ -56,14 +56,15 @@ struct __align__(16) PrefillRequest {
   int base;        // its first chunk of segment 0
 };
 
-// The chunks go by segments of every request, seg_chunks of each at a time:
-// the preparation of one and then its chain, whose CTAs leave the state to the
+// The chunks go by segments of every request, seg_from(s) .. seg_from(s + 1) - 1
+// of each at a time: the preparation of one and then its chain, whose CTAs leave the state to the
 // next segment's in FP32.  The next preparation runs beside the chain.
 struct PrefillParams {
   RecurrentParams r;
   int short_len;  // requests of at most so many tokens go token by token
   int max_chunks;
   int segments, seg_chunks;
+  bool seg_doubles;  // each segment twice the one before, the first seg_chunks
   int *seg_first;           // [segments + 1], the segments' first chunks
   PrefillChunk *chunks;     // [max_chunks], by segment, then request
   int *bases;               // [segments, B], a request's first chunk of each
@@ -71,6 +72,10 @@ struct PrefillParams {
   float *carry;             // [B, H, 128, 128] (segments > 1)
   uint8_t *images;          // [max_chunks, H, kImgBytes]
 };
+
+__host__ __device__ __forceinline__ int seg_from(const PrefillParams &p, int s) {
+  return p.seg_chunks * (p.seg_doubles ? (1 << s) - 1 : s);
+}
 
 // One segment.  A preparation that is not the first may start as soon as the
 // chain before it has, and ends after it.

@@ -51,6 +51,9 @@ constexpr int kKeys = kDim / kParts, kToks = kChunk / kParts;  // their columns
 constexpr uint32_t kPartA = kImgTHi;                  // Kd, Qd: 48 KB
 constexpr uint32_t kPartB = kImgKeHi - kImgTHi;       // T: 16 KB
 constexpr uint32_t kPartC = kImgDecay - kImgKeHi;     // Ke, A: 40 KB
+// Buffers of each.  C is released last, a chunk's end, and needed soonest: a
+// second one takes 2 to 3 % off the chain (of A or B: nothing).
+constexpr int kBufA = 1, kBufB = 1, kBufC = 2;
 constexpr uint32_t kVBytes = kChunk * kDim * 2;       // 16 KB
 
 // TMEM columns
@@ -69,12 +72,14 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t n, bool mn) {
 }
 
 struct ChainSmem {
-  uint8_t a[kPartA], b[kPartB], c[kPartC];  // each a multiple of 1024 bytes
+  uint8_t a[kBufA][kPartA], b[kBufB][kPartB], c[kBufC][kPartC];  // multiples of 1024 bytes
   uint8_t v[2][kVBytes];
-  float decay[2][kDim];
+  float decay[4][kDim];  // of chunk i at i & 3
   PrefillChunk chunk[4];  // chunk i at i & 3, there when its v is
   float4 peak[2][kParts][128];  // [chunk parity][part][row]: |S|, |U|, next |v|
-  uint64_t a_full, a_free, b_full, b_free, c_full, c_free, v_full[2], v_free[2], d_full[2];
+  uint64_t a_full[kBufA], a_free[kBufA], b_full[kBufB], b_free[kBufB];
+  uint64_t c_full[kBufC], c_free[kBufC];
+  uint64_t v_full[2], v_free[2], d_full[4];
   uint64_t s_ready[2], r_ready, u_ready, w_full, u_full, ds_full[2], o_full, drained;
   uint32_t tmem;
 };
@@ -278,9 +283,9 @@ __device__ __forceinline__ void zero_inert(const PrefillParams &p, int b, int h)
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(const PrefillParams p,
-                                                                             const __grid_constant__ CUtensorMap v_map,
-                                                                             int segment) {
+__global__ void __launch_bounds__(kChainThreads, 1)
+    kda_prefill_chain_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap v_map,
+                             int segment) {
   // (the swizzle atoms want 1024 bytes; there is no other shared memory)
   extern __shared__ __align__(1024) uint8_t chain_raw[];
   const int H = p.r.H;
@@ -289,16 +294,20 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
   int32_t *status = p.r.maps.status;
   // what does not need the preparation, while its last CTAs may still run
   if (threadIdx.x == 0) {
-    mbar_init(&sm.a_full, 1);
-    mbar_init(&sm.a_free, 1);
-    mbar_init(&sm.b_full, 1);
-    mbar_init(&sm.b_free, 1);
-    mbar_init(&sm.c_full, 1);
-    mbar_init(&sm.c_free, 1);
+    const auto init = [](uint64_t *full, uint64_t *free, int n) {
+      for (int i = 0; i < n; ++i) {
+        mbar_init(full + i, 1);
+        mbar_init(free + i, 1);
+      }
+    };
+    init(sm.a_full, sm.a_free, kBufA);
+    init(sm.b_full, sm.b_free, kBufB);
+    init(sm.c_full, sm.c_free, kBufC);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.v_full[i], 1);
       mbar_init(&sm.v_free[i], kRowWarps);
       mbar_init(&sm.d_full[i], 1);
+      mbar_init(&sm.d_full[i + 2], 1);
       mbar_init(&sm.s_ready[i], kRowWarps / 2);
       mbar_init(&sm.ds_full[i], 1);
     }
@@ -317,8 +326,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
   const PrefillRequest req = p.order[blockIdx.x / H];
   const int b = req.b, h = blockIdx.x % H;
   // this segment's chunks: done, done + 1 .. done + n - 1 of the request's
-  const int done = segment * p.seg_chunks;
-  const int n = max(min(req.chunks - done, p.seg_chunks), 0);
+  const int done = seg_from(p, segment);
+  const int n = max(min(req.chunks, seg_from(p, segment + 1)) - done, 0);
   const bool ends = done + n == req.chunks;
   const int bnd_at = req.bnd_chunks > 0 ? req.bnd_chunks - done : -1;  // in its chunks
   const int base = segment == 0 ? req.base : p.bases[segment * p.r.maps.B + b];
@@ -353,26 +362,29 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       mbar_arrive_expect_tx(bar, kVBytes);
       tma_load_3d(sm.v[i & 1], &v_map, 0, h, ck.t0, bar);
     };
-    const auto load_part = [&](int i, uint64_t *full, uint64_t *free, uint8_t *dst, uint32_t at,
-                               uint32_t bytes, int &issued) {
-      if (i >= 1) ok = ok && mbar_wait_bounded(free, (uint32_t)(i - 1) & 1u);
+    const auto load_part = [&](int i, int buffers, uint64_t *full, uint64_t *free, uint8_t *dst,
+                               uint32_t at, uint32_t bytes, int &issued) {
+      const int use = i / buffers, which = i - use * buffers;
+      if (use >= 1) ok = ok && mbar_wait_bounded(free + which, (uint32_t)(use - 1) & 1u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       issued = i + 1;
       if (lane != 0) return;
-      mbar_arrive_expect_tx(full, bytes);
-      bulk_g2s(dst, images + i * img_step + at, bytes, full);
+      mbar_arrive_expect_tx(full + which, bytes);
+      bulk_g2s(dst + which * bytes, images + i * img_step + at, bytes, full + which);
     };
     load_v(0);
     for (int i = 0; i < n && ok; ++i) {
-      load_part(i, &sm.a_full, &sm.a_free, sm.a, 0, kPartA, n_a);
+      load_part(i, kBufA, sm.a_full, sm.a_free, sm.a[0], 0, kPartA, n_a);
       if (ok && lane == 0) {
-        mbar_arrive_expect_tx(&sm.d_full[i & 1], kDim * 4);
-        bulk_g2s(sm.decay[i & 1], images + i * img_step + kImgDecay, kDim * 4, &sm.d_full[i & 1]);
+        // (the place of chunk i - 4's: the state has had them since before
+        // chunk i - 2 released its Kd)
+        mbar_arrive_expect_tx(&sm.d_full[i & 3], kDim * 4);
+        bulk_g2s(sm.decay[i & 3], images + i * img_step + kImgDecay, kDim * 4, &sm.d_full[i & 3]);
       }
       if (ok && i + 1 < n) load_v(i + 1);
-      if (ok) load_part(i, &sm.b_full, &sm.b_free, sm.b, kPartA, kPartB, n_b);
-      if (ok) load_part(i, &sm.c_full, &sm.c_free, sm.c, kPartA + kPartB, kPartC, n_c);
+      if (ok) load_part(i, kBufB, sm.b_full, sm.b_free, sm.b[0], kPartA, kPartB, n_b);
+      if (ok) load_part(i, kBufC, sm.c_full, sm.c_free, sm.c[0], kPartA + kPartB, kPartC, n_c);
     }
     if (!ok) {
       // every copy issued lands before the CTA can exit: the last phase in
@@ -381,11 +393,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       const auto settle = [&](uint64_t *bar, int uses) {
         if (uses > 0) mbar_wait_bounded(bar, (uint32_t)(uses - 1) & 1u);
       };
-      settle(&sm.a_full, n_a);
-      settle(&sm.b_full, n_b);
-      settle(&sm.c_full, n_c);
-      settle(&sm.d_full[0], (n_a + 1) / 2);
-      settle(&sm.d_full[1], n_a / 2);
+      const auto settle_all = [&](uint64_t *bar, int buffers, int uses) {
+        for (int j = 0; j < buffers; ++j) settle(bar + j, (uses - j + buffers - 1) / buffers);
+      };
+      settle_all(sm.a_full, kBufA, n_a);
+      settle_all(sm.b_full, kBufB, n_b);
+      settle_all(sm.c_full, kBufC, n_c);
+      settle_all(sm.d_full, 4, n_a);
       settle(&sm.v_full[0], (n_v + 1) / 2);
       settle(&sm.v_full[1], n_v / 2);
     }
@@ -394,11 +408,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
     const uint32_t lead = elect_one();
     const auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
     const uint32_t tm = uniform(tmem);
-    const uint32_t sa = uniform(smem_u32(sm.a)), sb = uniform(smem_u32(sm.b));
-    const uint32_t sc = uniform(smem_u32(sm.c));
-    const KMajor kd_hi(sa + kImgKdHi), kd_lo(sa + kImgKdLo), qd(sa + kImgQd);
-    const KMajor am(sc + 4 * kImgBlock), t_hi(sb), t_lo(sb + kImgBlock);
-    const MnMajor ke_hi(sc), ke_lo(sc + 2 * kImgBlock);
+    const uint32_t base_a = uniform(smem_u32(sm.a)), base_b = uniform(smem_u32(sm.b));
+    const uint32_t base_c = uniform(smem_u32(sm.c));
     constexpr uint32_t k64 = idesc_f16(64, false), k64mn = idesc_f16(64, true);
     const uint32_t w = tm + kColW, s_hi = tm + kColSHi, s_lo = tm + kColSLo;
     const uint32_t r_hi = tm + kColRHi, r_lo = tm + kColRLo;
@@ -410,7 +421,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
     for (int i = 0; i < n; ++i) {
       const uint32_t ph = (uint32_t)i & 1u;
       const uint32_t o = tm + kColO + 64u * ph;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.a_full, ph));
+      const uint32_t ia = (uint32_t)i % kBufA, ib = (uint32_t)i % kBufB, ic = (uint32_t)i % kBufC;
+      const uint32_t sa = base_a + ia * kPartA, sb = base_b + ib * kPartB;
+      const uint32_t sc = base_c + ic * kPartC;
+      const KMajor kd_hi(sa + kImgKdHi), kd_lo(sa + kImgKdLo), qd(sa + kImgQd);
+      const KMajor am(sc + 4 * kImgBlock), t_hi(sb), t_lo(sb + kImgBlock);
+      const MnMajor ke_hi(sc), ke_lo(sc + 2 * kImgBlock);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.a_full[ia], (uint32_t)(i / kBufA) & 1u));
       for (int half = 0; half < 2 && ok; ++half) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.s_ready[half], ph));
         if (!ok) break;
@@ -422,15 +439,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       if (!ok) break;
       commit(&sm.w_full);
       mma_part<8>(o, s_hi, qd, k64, false, lead);
-      commit(&sm.a_free);
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.b_full, ph) &&
+      commit(&sm.a_free[ia]);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.b_full[ib], (uint32_t)(i / kBufB) & 1u) &&
                                        mbar_wait_bounded(&sm.r_ready, ph));
       if (!ok) break;
       tc_fence_after();
       mma_split<4>(w, r_hi, r_lo, t_hi, t_lo, k64, false, lead);
       commit(&sm.u_full);
-      commit(&sm.b_free);
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.c_full, ph) &&
+      commit(&sm.b_free[ib]);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.c_full[ic], (uint32_t)(i / kBufC) & 1u) &&
                                        mbar_wait_bounded(&sm.u_ready, ph));
       if (!ok) break;
       tc_fence_after();
@@ -441,7 +458,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       }
       mma_part<4>(o, r_hi, am, k64, true, lead);
       commit(&sm.o_full);
-      commit(&sm.c_free);
+      commit(&sm.c_free[ic]);
     }
     if (!ok && lead) report(status, KDA_ERR_TIMEOUT);
     // nothing of this CTA's is in flight when its columns are released
@@ -542,7 +559,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
     const auto advance = [&](int i) {
       if (!wait(&sm.ds_full[half], (uint32_t)i & 1u)) return;
       tc_fence_after();
-      const float *dec = sm.decay[i & 1] + kKeys * qt;
+      const float *dec = sm.decay[i & 3] + kKeys * qt;
 #pragma unroll
       for (int j = 0; j < kKeys / 16; ++j) {
         uint32_t d[16];
@@ -669,7 +686,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_prefill_chain_kernel(con
       // under M3: every row's peaks are there once all warps have arrived, and
       // the chunk's decays have long been
       if (!wait(&sm.u_ready, (uint32_t)i & 1u) ||
-          !wait(&sm.d_full[i & 1], (uint32_t)(i >> 1) & 1u))
+          !wait(&sm.d_full[i & 3], (uint32_t)(i >> 2) & 1u))
         break;
       f_next = row_factor(f, bound_of(i));
       changes = __any_sync(0xffffffffu, f_next != f);

@@ -845,7 +845,8 @@ int launch_prefill_prep(const PrefillParams &p, int segment, cudaStream_t stream
         CUDA_SUCCESS)
       return KDA_ERR_CUDA;
   long long items = (long long)p.max_chunks * p.r.H;
-  const long long most = (long long)p.r.maps.B * p.seg_chunks * p.r.H;
+  const long long most = (long long)p.r.maps.B * p.r.H *
+                         (seg_from(p, segment + 1) - seg_from(p, segment));
   if (p.segments > 1 && most < items) items = most;
   // (beside a chain: what its CTAs, one to an SM, leave)
   const int sms = device_sm_count(dev), chain = p.r.maps.B * p.r.H;
