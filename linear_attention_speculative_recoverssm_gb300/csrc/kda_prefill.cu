@@ -13,9 +13,9 @@ namespace kda {
 namespace {
 
 // Windows of at most this many tokens go through the token-by-token kernel:
-// 32 tokens of 1 / 4 / 32 requests of 32 heads take 24 / 30 / 130 us there and
-// 23 / 31 / 190 as a chunk each, 48 tokens 35 / 43 / 194 and 23 / 32 / 193.
-constexpr int kShortLen = 32;
+// 40 tokens of 1 / 4 / 32 requests of 32 heads take 21 / 29 / 155 us there and
+// 24 / 31 / 192 as a chunk each, 48 tokens 25 / 34 / 185 and 23 / 32 / 196.
+constexpr int kShortLen = 40;
 constexpr int kListThreads = 1024;
 
 // Segments: where a call has too few (request, head) items to fill half the

@@ -19,10 +19,12 @@
 //    g + 4, g + 8, g + 12, so that the eight partial sums of a lane go through
 //    one reduce-scatter over eight lanes (7 shuffles, where a row to a warp
 //    takes 31) and u comes back by 4 instead of 16; a token's operands are
-//    made once for the CTA, a token a warp, eight tokens at a time.  100
-//    requests of 32 heads, 3 tokens, BF16: 65 us (3.4 TB/s: the arithmetic
-//    of a warp's tokens is a chain of sums and shuffles, and 16 warps an SM is
-//    what the rows' registers leave room for); the other kernel 82.
+//    made once for the CTA, a token a warp, eight tokens at a time, from rows
+//    asked for a step ahead (8 tokens of 32 heads, one request: 6.7 us, asked
+//    for when needed 8.5; 100 requests 109 and 114).  100 requests of 32 heads, 3 tokens, BF16: 62 us (3.6 TB/s:
+//    the arithmetic of a warp's tokens is a chain of sums and shuffles, and 16
+//    warps an SM is what the rows' registers leave room for); the other kernel
+//    82.
 #include <cuda_runtime.h>
 
 #include "../../include/kda_recoverssm.h"
@@ -34,7 +36,8 @@ namespace kda {
 namespace {
 
 constexpr int kRecRows = 16;  // state rows of a warp
-constexpr int kGroup = 8;     // tokens whose operands are made at a time
+constexpr int kGroup = 8;     // tokens whose operands are made at a time,
+constexpr int kGroupWarps = 4;  // by so many warps
 
 __device__ __forceinline__ float4 bf16x4_to_f32(uint32_t lo, uint32_t hi) {
   return make_float4(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u),
@@ -278,11 +281,12 @@ __device__ __forceinline__ void step_rows(const GroupOps &sm, int t, int lane, i
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(128, 4) kda_recurrent_group(const RecurrentParams p) {
+__global__ void __launch_bounds__(32 * kGroupWarps, 4)
+    kda_recurrent_group(const RecurrentParams p) {
   __shared__ GroupOps ops[2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
-  const int row0 = (blockIdx.y * warps + warp) * kRecRows;
+  const int row0 = (blockIdx.y * kGroupWarps + warp) * kRecRows;
   PromptRequest r;
   if (!begin_item(p, b, h, row0, lane, r)) return;  // (all of the CTA alike)
   const int j = lane & 7, row = row0 + (lane >> 3);
@@ -301,11 +305,18 @@ __global__ void __launch_bounds__(128, 4) kda_recurrent_group(const RecurrentPar
   const float a = expf(p.A_log[h]);
   const float4 dt = *reinterpret_cast<const float4 *>(p.dt_bias + h * kDim + 4 * lane);
   const long long t0 = (long long)r.t0 * p.H + h;
+  // A warp makes every fourth token's operands, and asks for the one after it
+  // first: across groups too, so that it arrives under the steps between.
+  const auto ask = [&](int t) {
+    return load_token(p, t0 + (long long)(t < r.n ? t : r.n - 1) * p.H, lane);
+  };
+  RawToken next = ask(warp);
   for (int g0 = 0; g0 < r.n; g0 += kGroup) {
     GroupOps &sm = ops[(g0 / kGroup) & 1];
     const int n = r.n - g0 < kGroup ? r.n - g0 : kGroup;
-    for (int i = warp; i < n; i += warps) {
-      const RawToken raw = load_token(p, t0 + (long long)(g0 + i) * p.H, lane);
+    for (int i = warp; i < n; i += kGroupWarps) {
+      const RawToken raw = next;
+      next = ask(g0 + i + kGroupWarps);
       const Token t = make_token(p, raw, a, dt);
       sm.v[i][lane] = raw.v;
       sts4(&sm.d[i][4 * lane], t.d);
@@ -357,13 +368,12 @@ int launch_recurrent(const RecurrentParams &p, bool bf16, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // Few items: their rows over more CTAs, so that more SMs take part (32
-  // items: 5.2 us by 64-thread CTAs, 5.9 by 256); many: CTAs as large as
-  // the SM's registers hold whole (32768 items of one token: 616 us by 256
-  // threads, 637 by 128, 645 by 64).
+  // One token, few items: their rows over more CTAs, so that more SMs take part
+  // (32 items: 5.2 us by 64-thread CTAs, 5.9 by 256); many: CTAs as large as
+  // the SM's registers hold whole (32768 items: 616 us by 256 threads, 637 by
+  // 128, 645 by 64).
   const bool one = p.maps.Q == 1;
-  const int most = one ? 8 : 4;
-  const int warps = items >= sms ? most : 2;
+  const int warps = !one ? kGroupWarps : (items >= sms ? 8 : 2);
   cfg.gridDim = dim3(items, kDim / kRecRows / warps);
   cfg.blockDim = dim3(32 * warps);
   const auto kernel = one ? (bf16 ? kda_recurrent_one<true> : kda_recurrent_one<false>)

@@ -318,13 +318,13 @@ def test_long_prompt_many_heads():
     run_and_check("prefill", long_case([4100], 77, seed=77, boundary={0: 70}))
 
 
-@pytest.mark.parametrize("n", [1, 5, 8, 9, 32, 33, 64])
+@pytest.mark.parametrize("n", [1, 5, 8, 9, 40, 41, 64])
 @pytest.mark.parametrize("most", [0, 5000])
 @pytest.mark.parametrize("inert", [(), (0,)])
 def test_one_request(n, most, inert):
     """A single request, its window far below the longest allowed too."""
     case = ragged_case(lens=[n], H=3, seed=n, inert=inert, boundary={0: max(1, n - 1)}, resume=(0,),
-                       tail=40 if most else 0)
+                       tail=50 if most else 0)
     case["Q"] = max(n, most)
     run_and_check("prefill", case)
 
