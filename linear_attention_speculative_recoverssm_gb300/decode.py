@@ -10,6 +10,8 @@ sequences the library's entry points in that order; every step runs in the
 library's kernels, on the given stream, with no host synchronisation, so a
 sequence of steps can be captured in a CUDA graph.
 
+* ``prefill``: prompts are taken into their requests' checkpoints before the
+  first step (in one call or in parts);
 * ``verify``: the fused replay + verify, or the stock verify (no replay) when
   the pending replays were just folded in by ``flush``;
 * ``accept``: the accepted counts become the pending replays (defer); rows
@@ -21,7 +23,7 @@ sequence of steps can be captured in a CUDA graph.
 from __future__ import annotations
 
 from ._lib import (KDA_STATE_F32, kda_commit, kda_defer_commit, kda_flush_plan,
-                   kda_replay_verify, kda_verify, layer_tables)
+                   kda_prefill, kda_replay_verify, kda_verify, layer_tables)
 
 
 class DeferredRecoverSSM:
@@ -48,6 +50,7 @@ class DeferredRecoverSSM:
         self._plan = {name: torch.zeros(self.B, dtype=torch.int32, device=dev)
                       for name in ("commit_lens", "final_slots", "boundary_slots",
                                    "boundary_lens")}
+        self._fresh = torch.full((self.B,), self.null_slot, dtype=torch.int32, device=dev)
         self.flushed = False
 
     def _commit(self, commit_lens, destinations, boundaries=None, boundary_lens=None):
@@ -58,6 +61,23 @@ class DeferredRecoverSSM:
                    boundaries=boundaries, boundary_lens=boundary_lens,
                    record_rows=self.record_rows, null_slot=self.null_slot, status=self.status,
                    stream=self.stream)
+
+    def prefill(self, q, k, v, raw_g, raw_beta, query_start_loc, out, *, Q, sources=None,
+                workspace=None):
+        """Prompts (q, k, v, raw_g BF16 [T, H, 128], raw_beta BF16 [T, H],
+        packed by query_start_loc [B + 1], windows of up to Q tokens) through
+        the rule, outputs to out: each request's state is left in its own
+        slot, from which ``verify`` goes on.  A request with an empty window is
+        left alone.  ``sources`` (int32 [B]): the slots to go on from, the null
+        slot for a fresh start (None: all fresh; ``state_slots`` for a prompt's
+        later parts).  A request whose prompt this is has no pending replay
+        (``pending`` of its record row is 0)."""
+        if sources is None:
+            sources = self._fresh
+        kda_prefill(q, k, v, raw_g, raw_beta, self.A_log, self.dt_bias, self.state_pool, sources,
+                    self.state_slots, query_start_loc, out, Q=Q, lower_bound=self.lower_bound,
+                    q_scale=self.q_scale, workspace=workspace, null_slot=self.null_slot,
+                    status=self.status, stream=self.stream)
 
     def verify(self, q, k, v, raw_g, raw_beta, out, query_start_loc=None):
         """Verify this step's window (q, k, v, raw_g BF16 [T, H, 128],

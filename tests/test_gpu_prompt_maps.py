@@ -386,3 +386,66 @@ def test_plan_feeds_the_commit():
               boundary_lens=ref["boundary_lens"])
     assert int(status[0]) == 0
     assert np.abs(to_numpy(state) - want[0]["state"]).max() <= 1e-4 * np.abs(want[0]["state"]).max()
+
+
+def test_prompts_before_speculation():
+    """DeferredRecoverSSM takes prompts in, whole and in two parts beside an
+    empty window and an inert request, then verifies and commits windows: the
+    outputs and states of kda_recurrent over the same tokens."""
+    import torch
+    from linear_attention_speculative_recoverssm_gb300 import DeferredRecoverSSM, kda_recurrent
+    H, B, Q, slots = 2, 4, 3, 9
+    lens, window = [100, 70, 0, 50], [Q] * B
+    rng = np.random.default_rng(91)
+    bits = lambda *s, std=1.0: to_torch(
+        synth.to_bf16_bits((rng.standard_normal(s) * std).astype(np.float32)), "cuda")
+    T = sum(lens)
+    dev = "cuda"
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)
+    x = [bits(T, H, 128), bits(T, H, 128), bits(T, H, 128), bits(T, H, 128, std=0.7), bits(T, H)]
+    y = [bits(B * Q, H, 128) for _ in range(3)] + [bits(B * Q, H, 128, std=0.7), bits(B * Q, H)]
+    A_log = to_torch(rng.uniform(0, 1.5, H).astype(np.float32), dev)
+    dt = to_torch((rng.standard_normal((H, 128)) - 2).astype(np.float32), dev)
+    first = torch.randn((slots, H, 128, 128), device=dev)
+    pool, own = first.clone(), i32(3, 5, 7, 0)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    loop = DeferredRecoverSSM(pool, own, i32(0, 1, 2, 3),
+                              torch.zeros(B, dtype=torch.int32, device=dev),
+                              torch.zeros((B, H, 8, 128), device=dev),
+                              torch.zeros((B, H, 8, 256), dtype=torch.bfloat16, device=dev),
+                              A_log, dt, Q=Q, lower_bound=-5.0, q_scale=128 ** -0.5,
+                              status=status)
+    out = torch.zeros((T, H, 128), dtype=torch.bfloat16, device=dev)
+    cut = i32(0, 64, 134, 134, 184)  # request 0 in two parts
+    part = [torch.cat([t[:64], t[100:]]) for t in x]
+    o = torch.zeros_like(part[2])
+    loop.prefill(*part, cut, o, Q=70)
+    rest = [t[64:100].contiguous() for t in x]
+    o2 = torch.zeros_like(rest[2])
+    loop.prefill(*rest, i32(0, 36, 36, 36, 36), o2, Q=36, sources=own)
+    out[:64], out[100:], out[64:100] = o[:64], o[64:], o2
+    ref_pool, ref = first.clone(), torch.zeros_like(out)
+    common = dict(lower_bound=-5.0, q_scale=128 ** -0.5)
+    kda_recurrent(*x, A_log, dt, ref_pool, i32(0, 0, 0, 0), own, ref, Q=100,
+                  query_start_loc=i32(0, 100, 170, 170, 220), **common)
+    # two evaluations of one rule, each output rounded once and the chunked
+    # form's query products before that (11 bits): half a step each and the
+    # operators' tolerance
+    def close(a, b):
+        a, b = a.double(), b.double()
+        assert torch.linalg.norm(a - b) <= 2.0 ** -8 * 2 * torch.linalg.norm(b)
+    close(out, ref)
+    assert torch.equal(pool[[0, 1, 2, 4, 6, 7, 8]], first[[0, 1, 2, 4, 6, 7, 8]])
+    err = (pool - ref_pool).abs().max()
+    assert err <= 1e-4 * ref_pool[[3, 5]].abs().max()
+    # a window verified and accepted whole is that window decoded
+    got, want = (torch.zeros((B * Q, H, 128), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    loop.verify(*y, got)
+    loop.accept(i32(Q, Q, Q, 0))
+    loop.flush()
+    kda_recurrent(*y, A_log, dt, ref_pool, own, own, want, Q=Q, **common)
+    close(got[:3 * Q], want[:3 * Q])
+    # (the records hold keys and gates in BF16: a step of each, 2^-8, in a state
+    # that three tokens changed)
+    assert (pool - ref_pool)[[3, 5, 7]].abs().max() <= 3 * 2.0 ** -7 * ref_pool[[3, 5, 7]].abs().max()
+    assert int(status[0]) == 0
