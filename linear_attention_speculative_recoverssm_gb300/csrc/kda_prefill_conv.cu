@@ -11,7 +11,9 @@
 // the three entries before each run; 8 tokens are asked for at a time.  4
 // channels a thread and not 8: 80 registers, 24 warps an SM (8 channels: 127,
 // 16 warps).  16384 tokens, 32 heads: 138 us, 5.8 TB/s (of 6.77 measured for a
-// copy); 8 channels and runs of 16 tokens: 215.
+// copy); 8 channels and runs of 16 tokens: 215.  Short prompts are windows above
+// all: a thread's four are neighbours, and move whole (entry by entry, 4096
+// requests of one token took 809 us in place of 281).
 #include <cuda_runtime.h>
 
 #include "../../include/kda_recoverssm.h"
@@ -28,7 +30,7 @@ struct ConvParams {
   const uint16_t *x, *w, *bias;  // [n_tokens, 3 D], [3, 4, D], [3 D] or nullptr
   uint16_t *window;              // [n_slots, 3 D, width]
   long long slot_stride;
-  int width, H;
+  int H;
   int run;  // tokens of a CTA
   uint16_t *q, *k, *v;  // [n_tokens, H, 128]
   PromptMaps maps;
@@ -75,11 +77,63 @@ __device__ __forceinline__ Four unpack4(uint2 x) {
               make_float2(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u))};
 }
 
+// The windows of a thread's four channels, W entries each, one after the other:
+// halfword c W + i.
+template <int W>
+struct Windows {
+  static constexpr int kWords = 2 * W;
+  uint32_t w[kWords];
+  // (16-byte pieces where W is even, else 8-byte ones)
+  __device__ __forceinline__ void load(const uint16_t *at) {
+    if constexpr (W % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const uint4 x = reinterpret_cast<const uint4 *>(at)[i];
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const uint2 x = reinterpret_cast<const uint2 *>(at)[i];
+        w[2 * i] = x.x, w[2 * i + 1] = x.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t *at) const {
+    if constexpr (W % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i)
+        reinterpret_cast<uint4 *>(at)[i] =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        reinterpret_cast<uint2 *>(at)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ uint32_t get(int h) const {
+    return h & 1 ? w[h / 2] >> 16 : w[h / 2] & 0xffffu;
+  }
+  __device__ __forceinline__ void set(int h, uint32_t x) {  // x's low half
+    w[h / 2] = __byte_perm(w[h / 2], x, h & 1 ? 0x5410 : 0x3254);
+  }
+  __device__ __forceinline__ uint2 entry(int i) const {  // of the four channels
+    return make_uint2(get(i) | get(W + i) << 16, get(2 * W + i) | get(3 * W + i) << 16);
+  }
+  __device__ __forceinline__ void set_entry(int i, uint2 x) {
+    set(i, x.x);
+    set(W + i, x.x >> 16);
+    set(2 * W + i, x.y);
+    set(3 * W + i, x.y >> 16);
+  }
+};
+
 __device__ __forceinline__ uint32_t silu_pair(float2 z) {
   const __nv_bfloat162 r = __float22bfloat162_rn(silu2(z));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+template <int W>
 __global__ void __launch_bounds__(kPcThreads, 6) kda_prefill_conv_kernel(const ConvParams p) {
   const PromptMaps &mp = p.maps;
   const int lane = threadIdx.x & 31;
@@ -128,15 +182,11 @@ __global__ void __launch_bounds__(kPcThreads, 6) kda_prefill_conv_kernel(const C
     if (starts) {
       h0 = h1 = h2 = make_uint2(0, 0);
       if (r.src >= 0) {
-        const uint16_t *win = p.window + r.src * p.slot_stride + (long long)ch * p.width;
-        uint32_t e[3][4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 3; ++i) e[i][c] = win[c * p.width + i];
-        h0 = make_uint2(e[0][0] | e[0][1] << 16, e[0][2] | e[0][3] << 16);
-        h1 = make_uint2(e[1][0] | e[1][1] << 16, e[1][2] | e[1][3] << 16);
-        h2 = make_uint2(e[2][0] | e[2][1] << 16, e[2][2] | e[2][3] << 16);
+        Windows<W> win;
+        win.load(p.window + r.src * p.slot_stride + (long long)ch * W);
+        h0 = win.entry(0);
+        h1 = win.entry(1);
+        h2 = win.entry(2);
       }
       // entries n - 3 .. n - 1 are what the request leaves, m - 3 .. m - 1
       // its boundary's
@@ -144,20 +194,15 @@ __global__ void __launch_bounds__(kPcThreads, 6) kda_prefill_conv_kernel(const C
       for (int which = 0; which < 2; ++which) {
         const int slot = which == 0 ? r.bnd : r.dst, at = which == 0 ? r.m : r.n;
         if (slot < 0) continue;
-        uint16_t *to = p.window + slot * p.slot_stride + (long long)ch * p.width;
-        uint2 v[3];
+        uint16_t *to = p.window + slot * p.slot_stride + (long long)ch * W;
+        Windows<W> win;
+        if (W > 3) win.load(to);  // (what the other entries hold stays)
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
           const int j = at - 3 + i;  // >= -2: at >= 1
-          v[i] = j >= 0 ? input(r.t0 + j) : (j == -1 ? h2 : h1);
+          win.set_entry(i, j >= 0 ? input(r.t0 + j) : (j == -1 ? h2 : h1));
         }
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          to[i] = (uint16_t)v[i].x;
-          to[p.width + i] = (uint16_t)(v[i].x >> 16);
-          to[2 * p.width + i] = (uint16_t)v[i].y;
-          to[3 * p.width + i] = (uint16_t)(v[i].y >> 16);
-        }
+        win.store(to);
       }
     } else {
       h0 = input(t - 3);
@@ -218,7 +263,6 @@ extern "C" int kda_prefill_conv(
   p.bias = conv_bias;
   p.window = conv_state;
   p.slot_stride = conv_slot_stride;
-  p.width = conv_width;
   p.H = H;
   p.q = q;
   p.k = k;
@@ -232,11 +276,28 @@ extern "C" int kda_prefill_conv(
   if (sms < 1) return KDA_ERR_CUDA;
   // Long runs where they leave every SM its fill (16384 tokens, 32 heads: 171
   // us by runs of 16 tokens, 153 by 32, 147 by 64); a few tokens are a chain of
-  // loads, and run side by side (37 tokens: 7 us by 4, 13 by 16).
+  // loads, and run side by side (37 tokens: 7 us by 4, 13 by 16); and so do short
+  // windows (4096 of one token: 281 us by runs of 8, 294 by 64; 512 of three: 53
+  // by 16, 60 by 64).
   int run = 64;
-  while (run > 4 && (long long)((n_tokens - 1) / run + 1) * channels < 4 * sms) run /= 2;
+  while (run > 4 && ((long long)((n_tokens - 1) / run + 1) * channels < 4 * sms ||
+                     run > 8LL * n_tokens / B))
+    run /= 2;
   p.run = run;
   const dim3 grid((n_tokens - 1) / run + 1, channels);
-  kda::kda_prefill_conv_kernel<<<grid, kda::kPcThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const auto kernel = [&] {
+    switch (conv_width) {
+      case 3: return kda::kda_prefill_conv_kernel<3>;
+      case 4: return kda::kda_prefill_conv_kernel<4>;
+      case 5: return kda::kda_prefill_conv_kernel<5>;
+      case 6: return kda::kda_prefill_conv_kernel<6>;
+      case 7: return kda::kda_prefill_conv_kernel<7>;
+      case 8: return kda::kda_prefill_conv_kernel<8>;
+      case 9: return kda::kda_prefill_conv_kernel<9>;
+      default: return kda::kda_prefill_conv_kernel<10>;
+    }
+  }();
+  static_assert(KDA_MAX_WINDOW + 2 == 10, "an instance for every width");
+  kernel<<<grid, kda::kPcThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -199,6 +199,28 @@ def test_conv_longer_runs(H, tokens):
     check_conv(case, run_conv(case))
 
 
+@pytest.mark.parametrize("width", [3, 4, 5, 6, 7, 8, 9, 10])
+def test_conv_every_width(width):
+    """Windows of every width, one-token prompts among them, some advanced in
+    place and some left as a boundary in their own source."""
+    lens = [1, 1, 2, 1, 3, 1, 4, 1, 7, 1]
+    case = conv_case(lens, 3, seed=width, width=width, resume=range(9), boundary={2: 1, 6: 3, 8: 4})
+    case["destinations"][:4] = case["sources"][:4]
+    case["boundaries"][6] = case["sources"][6]
+    check_conv(case, run_conv(case))
+
+
+@pytest.mark.parametrize("null_slot", [-1, 4])
+def test_conv_other_null_slots(null_slot):
+    """Slot 0 is a slot where the null slot is -1; slots up to it are none."""
+    case = conv_case([3, 20, 5, 1], 2, seed=60, boundary={1: 9})
+    case["destinations"][2], case["sources"][3] = 0, 0
+    case["null_slot"] = null_slot
+    d = {n: None if a is None else to_torch(a, "cuda") for n, a in case.items()
+         if n not in ("Q", "null_slot")}
+    check_conv(case, run_conv(case, d, null_slot=null_slot))
+
+
 def test_conv_in_place_and_shared():
     """Windows left in their own source (as destination or as boundary), for
     prompts of one to many runs, and one source for several requests."""

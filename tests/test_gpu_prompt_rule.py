@@ -111,6 +111,16 @@ def test_uniform_windows(op):
 
 
 @pytest.mark.parametrize("op", ["prefill", "recurrent"])
+@pytest.mark.parametrize("null_slot", [-1, 4])
+def test_other_null_slots(op, null_slot):
+    """Slot 0 is a slot where the null slot is -1; slots up to it are none."""
+    case = ragged_case(lens=[70, 3, 100, 20, 50], H=2, seed=25, boundary={2: 66}, resume=(0, 1, 3))
+    case["null_slot"] = null_slot
+    case["destinations"][1], case["sources"][4] = 0, 0
+    run_and_check(op, case)
+
+
+@pytest.mark.parametrize("op", ["prefill", "recurrent"])
 @pytest.mark.parametrize("lower_bound", [-10.0, -0.5, 0.0])
 def test_gate_bounds(op, lower_bound):
     """The steepest gates (every channel forgetting e^-10 a token), and none."""
