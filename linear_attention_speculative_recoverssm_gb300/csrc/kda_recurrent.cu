@@ -293,15 +293,6 @@ __global__ void __launch_bounds__(32 * kGroupWarps, 4)
   const long long elem = BF16 ? 2 : 4;
   char *pool = reinterpret_cast<char *>(p.state) + (long long)h * kDim * kDim * elem;
   const long long slot_bytes = p.slot_stride * elem;
-  float4 s[4][4];
-  if (r.src >= 0) {
-    load_rows<BF16>(pool + r.src * slot_bytes, row, j, s);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int m = 0; m < 4; ++m) s[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
   const float a = expf(p.A_log[h]);
   const float4 dt = *reinterpret_cast<const float4 *>(p.dt_bias + h * kDim + 4 * lane);
   const long long t0 = (long long)r.t0 * p.H + h;
@@ -311,6 +302,15 @@ __global__ void __launch_bounds__(32 * kGroupWarps, 4)
     return load_token(p, t0 + (long long)(t < r.n ? t : r.n - 1) * p.H, lane);
   };
   RawToken next = ask(warp);
+  float4 s[4][4];
+  if (r.src >= 0) {
+    load_rows<BF16>(pool + r.src * slot_bytes, row, j, s);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) s[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   for (int g0 = 0; g0 < r.n; g0 += kGroup) {
     GroupOps &sm = ops[(g0 / kGroup) & 1];
     const int n = r.n - g0 < kGroup ? r.n - g0 : kGroup;

@@ -214,7 +214,8 @@ def test_conv_every_width(width):
 def test_conv_other_null_slots(null_slot):
     """Slot 0 is a slot where the null slot is -1; slots up to it are none."""
     case = conv_case([3, 20, 5, 1], 2, seed=60, boundary={1: 9})
-    case["destinations"][2], case["sources"][3] = 0, 0
+    case["sources"][case["sources"] == 0] = null_slot  # (fresh, none reads slot 0 but its writer)
+    case["destinations"][3] = case["sources"][3] = 0
     case["null_slot"] = null_slot
     d = {n: None if a is None else to_torch(a, "cuda") for n, a in case.items()
          if n not in ("Q", "null_slot")}

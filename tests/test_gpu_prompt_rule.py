@@ -116,7 +116,8 @@ def test_other_null_slots(op, null_slot):
     """Slot 0 is a slot where the null slot is -1; slots up to it are none."""
     case = ragged_case(lens=[70, 3, 100, 20, 50], H=2, seed=25, boundary={2: 66}, resume=(0, 1, 3))
     case["null_slot"] = null_slot
-    case["destinations"][1], case["sources"][4] = 0, 0
+    case["sources"][case["sources"] == 0] = null_slot  # (fresh, none reads slot 0 but its writer)
+    case["destinations"][1] = case["sources"][1] = 0
     run_and_check(op, case)
 
 
