@@ -12,10 +12,14 @@
 namespace kda {
 namespace {
 
-// Windows of at most this many tokens go through the token-by-token kernel:
-// 40 tokens of 1 / 4 / 32 requests of 32 heads take 21 / 29 / 155 us there and
-// 24 / 31 / 192 as a chunk each, 48 tokens 25 / 34 / 185 and 23 / 32 / 196.
-constexpr int kShortLen = 40;
+// Windows of at most so many tokens go through the token-by-token kernel, where
+// a call has none longer: 40 tokens of 1 / 4 / 32 requests of 32 heads take 21 /
+// 29 / 155 us there and 24 / 31 / 192 as a chunk each, 48 tokens 25 / 34 / 185
+// and 23 / 32 / 196.  Beside longer ones fewer, since that kernel finds room
+// only as the chain ends: prompts of 63 x 24 and 2000 tokens take 307 us with
+// 24 and 317 with 16 in its place, 37 and 5 x 1600 tokens 345 with 24 and 365
+// with 40.
+constexpr int kShortLen = 40, kMixedLen = 24;
 constexpr int kListThreads = 1024;
 
 // Segments: where a call has too few (request, head) items to fill half the
@@ -38,10 +42,10 @@ struct Workspace {
 };
 
 // Chunks end at a request's boundary and at its end, so a request of n
-// tokens has at most n / 64 + 2, and one with any has more than kShortLen.
+// tokens has at most n / 64 + 2, and one with any has more than kMixedLen.
 Workspace workspace_layout(int64_t n_tokens, int64_t B, int64_t H) {
   const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  const int64_t most = n_tokens / (kShortLen + 1);
+  const int64_t most = n_tokens / (kMixedLen + 1);
   Workspace w;
   w.max_chunks = n_tokens / kChunk + 2 * (B == 1 || B < most ? B : most);
   w.chunks = 256;
@@ -266,7 +270,7 @@ int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const k
                                                    boundary_lens, query_start_loc, n_tokens,
                                                    n_slots, B, Q, null_slot, status)};
   // a single request of any length is one launch less by chunks alone
-  p.short_len = B == 1 ? 0 : kda::kShortLen;
+  p.short_len = B == 1 ? 0 : kda::kMixedLen;
   p.max_chunks = (int)w.max_chunks;
   // the longest request's chunks: its own and one more where its boundary
   // cuts one in two
@@ -309,6 +313,7 @@ int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const k
   }
   if (p.short_len == 0) return KDA_OK;
   p.r.beside = true;
+  p.r.max_len = p.short_len;
   return kda::launch_recurrent(p.r, bf16, st);
 }
 
