@@ -22,7 +22,7 @@ namespace {
 constexpr int kShortLen = 40, kMixedLen = 24;
 constexpr int kListThreads = 1024;
 
-// Segments: where a call has too few (request, head) items to fill half the
+// Segments: where a call has far fewer (request, head) items than there are
 // SMs, the chain of a long prompt leaves the others idle, and the preparation
 // of the next segment runs there meanwhile.  A chunk takes an SM of the chain
 // some 3 us, and one of the preparation 6: up to a quarter of the SMs' items,
@@ -31,9 +31,9 @@ constexpr int kListThreads = 1024;
 // after a short first one, and there are few.  With more items the chain fills
 // the GPU by itself, and a segment only costs its launches and the state's way
 // through memory.  One prompt of 16384 tokens, us in one segment / in eight of
-// 32 chunks / in four from 18 chunks on: 8 heads -- / 867 / 811, 32 heads
-// 1000 / 929 / 856, 64 heads -- / 1273 / 1502.
-constexpr int kSegItems = 76, kSegChunks = 32, kMaxSegments = 16;
+// 32 chunks / in four from 18 chunks on: 8 heads 715 / 768 / 697, 32 heads 947 /
+// 834 / 769, 48 heads 1100 / 905 / 1046, 64 heads 1268 / 1263 / 1434.
+constexpr int kSegItems = 57, kSegChunks = 32, kMaxSegments = 16;
 constexpr int kSegDoubleItems = 38, kSegFirst = 16;
 
 struct Workspace {

@@ -31,10 +31,10 @@
 // to over and over loses up to a unit of its last place each time, so dS is
 // summed apart, smallest parts first.
 //
-// What bounds it: a chunk's products and passes depend on one another, some 6 K
-// cycles (3.1 us) of which the tensor cores run 2.3 K, with 8 CTAs on the GPU
-// as with 152; 265 chunks of 32 heads in 16 prompts take 230 us, 190 of them the
-// longest prompt's 78 chunks.  TMEM and shared memory hold one item an SM.
+// What bounds it: a chunk's products and passes depend on one another, some 5.4 K
+// cycles (2.8 us) of which the tensor cores run 2.3 K, with 8 CTAs on the GPU
+// (697 us for 256 chunks) nearly as with 32; 265 chunks of 32 heads in 16 prompts
+// take 214 us, most of them the longest prompt's 78 chunks.  TMEM and shared memory hold one item an SM.
 // Eight row warps in place of 16 took longer, and so did the outputs' stores
 // between R and U (2 to 6 %): what the other warps split then waits.
 #include <cuda_fp16.h>
