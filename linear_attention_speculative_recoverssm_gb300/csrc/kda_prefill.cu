@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(32) kda_prefill_list_warp_kernel(const Prefill
     place += other > all || (other == all && l < b);
   }
   long long base = 0, start = 0;
+  int room = p.max_chunks;  // the list ends where the first request was cut off
   for (int seg = 0; seg < p.segments; ++seg) {
     const int done = seg_from(p, seg);
     int mine = min(max(all - done, 0), seg_from(p, seg + 1) - done);
@@ -114,21 +115,24 @@ __global__ void __launch_bounds__(32) kda_prefill_list_warp_kernel(const Prefill
       const long long y = __shfl_up_sync(0xffffffffu, inc, o);
       if (b >= o) inc += y;
     }
-    if (b == 0) p.seg_first[seg] = (int)min(base, (long long)p.max_chunks);
+    if (b == 0) p.seg_first[seg] = (int)min(base, (long long)room);
     const long long at = base + inc - mine;
     base += __shfl_sync(0xffffffffu, inc, 31);
     // (cut off where windows that overlap ask for more than there is room for)
-    const bool fits = at + mine <= p.max_chunks;
+    const bool fits = at + mine <= room;
     if (!fits) {
       report(p.r.maps.status, KDA_ERR_ARG);
       mine = 0;
       kept = min(kept, done);
     }
+    const uint32_t cut = __ballot_sync(0xffffffffu, !fits);
+    if (cut != 0)
+      room = (int)min((long long)room, __shfl_sync(0xffffffffu, at, __ffs(cut) - 1));
     if (seg == 0) start = fits ? at : -1;
     if (b < B) p.bases[seg * B + b] = fits ? (int)at : -1;
     write_chunks(p, (int)at, mine, done, t0, first, m, n);
   }
-  if (b == 0) p.seg_first[p.segments] = (int)min(base, (long long)p.max_chunks);
+  if (b == 0) p.seg_first[p.segments] = (int)min(base, (long long)room);
   if (b < B) p.order[place] = PrefillRequest{b, kept, first, (int)start};
 }
 
@@ -138,14 +142,16 @@ __global__ void __launch_bounds__(32) kda_prefill_list_warp_kernel(const Prefill
 __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const PrefillParams p) {
   __shared__ long long warp_sums[kListThreads / 32];  // (windows may overlap: no bound on a sum)
   __shared__ int bins[kListThreads];
+  __shared__ int room;  // the list ends where the first request was cut off
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = p.r.maps.B;
   grid_launch_dependents();
   bins[tid] = 0;
+  if (tid == 0) room = p.max_chunks;
   __syncthreads();
   long long base = 0;
   for (int seg = 0; seg < p.segments; ++seg) {
-    if (tid == 0) p.seg_first[seg] = (int)min(base, (long long)p.max_chunks);
+    if (tid == 0) p.seg_first[seg] = (int)min(base, (long long)room);
     for (int b0 = 0; b0 < B; b0 += kListThreads) {
       const int b = b0 + tid;
       int first = 0, rest = 0, t0 = 0, m = 0, n = 0;
@@ -187,6 +193,7 @@ __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const Pr
       if (!fits) {
         report(p.r.maps.status, KDA_ERR_ARG);
         mine = 0;
+        if (at < p.max_chunks) atomicMin(&room, (int)at);
       }
       if (b < B) {
         p.bases[seg * B + b] = fits ? (int)at : -1;
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const Pr
       __syncthreads();
     }
   }
-  if (tid == 0) p.seg_first[p.segments] = (int)min(base, (long long)p.max_chunks);
+  if (tid == 0) p.seg_first[p.segments] = (int)min(base, (long long)room);
   // bins, longest first -> where each begins
   const int bin = kListThreads - 1 - tid;
   const int mine = bins[bin];

@@ -367,3 +367,35 @@ def test_graphs_share_a_workspace():
         torch.cuda.synchronize()
         verify("prefill", cases[i], ds[i])
         verify("prefill", cases[1 - i], other)
+
+
+@pytest.mark.parametrize("again", [2, 40])
+@pytest.mark.parametrize("n", [640, 4200])
+def test_offsets_that_go_back(n, again):
+    """Offsets 0, n, 0, n, ..: every second window is negative, and the others
+    together ask for more chunks than the tokens have.  All that does not fit
+    is reported and left out; nothing else is touched."""
+    import torch
+    B = 2 * again + 1
+    case = ragged_case(lens=[n] + [0] * (B - 1), H=2, seed=n + again, resume=(0,), tail=3)
+    case["query_start_loc"] = np.array([0, n] * (again + 1), dtype=np.int32)
+    d = on_device(case)
+    call_rule(ops()["prefill"], case, d)
+    torch.cuda.synchronize()
+    assert int(d["status"][0]) != 0
+    state, dst = to_numpy(d["state"]), case["destinations"]
+    spared = np.ones(len(state), dtype=bool)
+    spared[dst[::2]] = False
+    np.testing.assert_array_equal(state[spared], case["state"][spared])
+    np.testing.assert_array_equal(to_numpy(d["out"])[n:], case["out"][n:])
+    if n == 640:  # one segment: the first request is served, the one too many is not
+        # (the outputs' rows are several requests', in no order)
+        one = ragged_case(lens=[n], H=2, seed=1)
+        for name in ("q", "k", "v", "raw_g", "raw_beta", "A_log", "dt_bias", "state", "out"):
+            one[name] = case[name]
+        for name in ("sources", "destinations"):
+            one[name] = case[name][:1]
+        alone = on_device(one)
+        call_rule(ops()["prefill"], one, alone)
+        np.testing.assert_array_equal(state[dst[0]], to_numpy(alone["state"])[dst[0]])
+        np.testing.assert_array_equal(state[dst[-1]], case["state"][dst[-1]])
