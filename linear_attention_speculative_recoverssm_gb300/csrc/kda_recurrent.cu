@@ -21,10 +21,10 @@
 //    takes 31) and u comes back by 4 instead of 16; a token's operands are
 //    made once for the CTA, a token a warp, eight tokens at a time, from rows
 //    asked for a step ahead (8 tokens of 32 heads, one request: 6.7 us, asked
-//    for when needed 8.5; 100 requests 109 and 114).  100 requests of 32 heads, 3 tokens, BF16: 60 us (3.7 TB/s:
-//    the arithmetic of a warp's tokens is a chain of sums and shuffles, and 16
-//    warps an SM is what the rows' registers leave room for); the other kernel
-//    82.
+//    for when needed 8.5; 100 requests 109 and 114).  100 requests of 32 heads,
+//    3 tokens, BF16: 60 us (3.7 TB/s: the arithmetic of a warp's tokens is a
+//    chain of sums and shuffles, and 16 warps an SM is what the rows' registers
+//    leave room for); the other kernel 82.
 #include <cuda_runtime.h>
 
 #include "../../include/kda_recoverssm.h"

@@ -210,6 +210,24 @@ def test_conv_every_width(width):
     check_conv(case, run_conv(case))
 
 
+def test_conv_slots_far_apart():
+    """Windows more than 2^31 elements apart: as in a pool without gaps."""
+    import torch
+    case = conv_case([5, 40], 2, seed=96, resume=(1,), boundary={1: 7})
+    case["sources"], case["destinations"] = np.array([0, 1], I32), np.array([2, 1], I32)
+    case["boundaries"], case["conv_state"] = np.array([0, 3], I32), case["conv_state"][:4]
+    d = {n: None if a is None else to_torch(a, "cuda") for n, a in case.items() if n != "Q"}
+    step, (_, D3, width) = 2 ** 31 + 512, case["conv_state"].shape
+    far = torch.empty(3 * step + D3 * width, dtype=torch.bfloat16, device="cuda")
+    far = far.as_strided((4, D3, width), (step, width, 1))
+    far.copy_(d["conv_state"])
+    d["conv_state"] = far
+    run_conv(case, d)
+    d["conv_state"] = far.contiguous()
+    del far
+    check_conv(case, d)
+
+
 @pytest.mark.parametrize("null_slot", [-1, 4])
 def test_conv_other_null_slots(null_slot):
     """Slot 0 is a slot where the null slot is -1; slots up to it are none."""

@@ -399,3 +399,30 @@ def test_offsets_that_go_back(n, again):
         call_rule(ops()["prefill"], one, alone)
         np.testing.assert_array_equal(state[dst[0]], to_numpy(alone["state"])[dst[0]])
         np.testing.assert_array_equal(state[dst[-1]], case["state"][dst[-1]])
+
+
+@pytest.mark.parametrize("op", ["prefill", "recurrent"])
+def test_slots_far_apart(op):
+    """Slots more than 2^31 elements apart: as in a pool without gaps."""
+    import torch
+    case = ragged_case(lens=[70, 30], H=2, seed=95, pool="bf16", slots=9, resume=(1,),
+                       boundary={1: 20})
+    case["sources"], case["destinations"] = np.array([0, 1], np.int32), np.array([2, 1], np.int32)
+    case["boundaries"] = np.array([0, 3], np.int32)
+    case["state"] = case["state"][:4]
+    d = on_device(case)
+    step = 2 ** 31 + 512
+    far = torch.empty(3 * step + 2 * 128 * 128, dtype=torch.bfloat16, device="cuda")
+    far = far.as_strided((4, 2, 128, 128), (step, 128 * 128, 128, 1))
+    far.copy_(d["state"])
+    near, d["state"] = d["state"], far
+    call_rule(ops()[op], case, d)
+    d["state"] = far.contiguous()
+    del far
+    verify(op, case, d)
+
+
+def test_very_long_prompt():
+    """Hundreds of chunks, many segments."""
+    run_and_check("prefill", ragged_case(lens=[33000, 700], H=1, seed=98, boundary={0: 32897},
+                                         resume=(1,), tail=1))
