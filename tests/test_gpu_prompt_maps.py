@@ -110,6 +110,63 @@ def test_plan_bad_head(head):
     assert np.all(got["destinations"][fresh] == 0)
 
 
+@pytest.mark.parametrize("B", [3, 5000])
+def test_plan_captured(B):
+    """Captured on another stream and replayed on other lengths: the plan
+    that an eager call makes."""
+    import torch
+    from linear_attention_speculative_recoverssm_gb300 import kda_slot_plan
+    cases = [plan_case(B, 16, 8, seed=s) for s in (31, 32)]
+    dev = "cuda"
+    names = ("computed_lens", "new_lens", "block_table", "free_slots", "free_head")
+    d = {n: to_torch(cases[0][n], dev) for n in names}
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device=dev)
+    out = [i32(B + 1)] + [i32(B) for _ in range(4)]
+    nxt, side = i32(1), torch.cuda.Stream()
+    call = lambda: kda_slot_plan(*d.values(), nxt, *out, block_size=16)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for case in cases:
+        for n in names:
+            d[n].copy_(to_torch(case[n], dev))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref_table = case["block_table"].copy()
+        ref, bad = po.slot_plan(computed_lens=case["computed_lens"], new_lens=case["new_lens"],
+                                block_table=ref_table, free_slots=case["free_slots"],
+                                free_head=0, block_size=16)
+        assert bad == 0
+        np.testing.assert_array_equal(to_numpy(d["block_table"]), ref_table)
+        for n, t in zip(("query_start_loc", "sources", "destinations", "boundaries",
+                         "boundary_lens"), out):
+            np.testing.assert_array_equal(to_numpy(t), ref[n])
+        assert int(nxt[0]) == int(np.asarray(ref["free_next"]).reshape(-1)[0])
+
+
+@pytest.mark.parametrize("resume", [(), (0, 1, 2)])
+def test_conv_captured(resume):
+    """The same for the convolution, whose windows are advanced in place."""
+    import torch
+    cases = [conv_case([30, 1, 70], 2, seed=s, resume=resume) for s in (33, 34)]
+    for c in cases[1:]:
+        for n in ("sources", "destinations"):
+            c[n] = cases[0][n]
+    d = {n: None if a is None else to_torch(a, "cuda") for n, a in cases[0].items() if n != "Q"}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        run_conv(cases[0], d)
+    for c in cases:
+        for n, a in c.items():
+            if n != "Q":
+                d[n].copy_(to_torch(a, "cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_conv(c, d)
+
+
 def test_plan_no_requests():
     case = plan_case(0, 16, 20, seed=7, n_free=0)
     case["free_slots"] = np.arange(1, 4, dtype=I32)
