@@ -17,10 +17,13 @@
 //
 // Every entry of the images is at most 1 in size (unit keys and queries,
 // decays <= 1, and T_ts is minus beta_t k_t applied to what is left of a
-// state beta_s k_s after contractions).  Kd, Ke and A are held as FP16 times
-// 1024, T and Qd as they are (kda_prefill_chain.cu says why).  "hi" and "lo"
-// are x rounded to FP16 and the rest rounded again, 22 bits together (to 2^-25
-// of 1 for T).  hi.hi + hi.lo + lo.hi leaves 2^-22 of a product.
+// state beta_s k_s after contractions: at most beta_s).  They are held as FP16
+// times powers of two, Kd and A 2^10, Qd 2^4, Ke 2^6 (kda_prefill_chain.cu says
+// why), and T 2^14 over p, the power of two above the chunk's largest beta: what
+// a nearly closed write gate leaves is as small as the gate.  "hi" and "lo" are
+// x rounded to FP16 and the rest rounded again, 22 bits together where neither
+// is subnormal (x above 2^-24 for Kd, 2^-20 for Ke, 2^-28 p for T) and 2^-25 of
+// the held value below.  hi.hi + hi.lo + lo.hi leaves 2^-22 of a product.
 #pragma once
 
 #include "kda_recurrent.cuh"
@@ -28,7 +31,9 @@
 namespace kda {
 
 constexpr int kChunk = 64;
-constexpr float kImgScale = 1024.f;
+constexpr float kImgScale = 1024.f;           // Kd, A
+constexpr float kImgQdScale = 16.f, kImgKeScale = 64.f;
+constexpr float kImgTScale = 16384.f;         // over the chunk's p
 
 // Image of one (chunk, head): byte offsets of its parts.  Rows of 128 bytes
 // (64 FP16), the 16-byte pieces of row r at position piece ^ (r & 7); K = 128
@@ -43,7 +48,15 @@ constexpr uint32_t kImgKeHi = kImgTLo + kImgBlock;       // [s][channel]
 constexpr uint32_t kImgKeLo = kImgKeHi + 2 * kImgBlock;
 constexpr uint32_t kImgA = kImgKeLo + 2 * kImgBlock;     // [t][s], hi only
 constexpr uint32_t kImgDecay = kImgA + kImgBlock;        // e^{G_end}, 128 FP32
-constexpr uint32_t kImgBytes = kImgDecay + 128 * 4;
+// Behind the decays, FP32, what bounds the states to come (kScal..)
+constexpr uint32_t kImgTail = (128 + 32) * 4;            // decays and scalars
+constexpr uint32_t kImgBytes = kImgDecay + kImgTail;
+// Scalars, by their place behind the decays: kEndFactor (the largest e^{G_end})^2
+// (four values, whose maximum it is); kLeftFactor (the largest decay from the
+// end of block 0 .. 2, of 16 tokens, to the chunk's)^2 (four values each); p; and
+// p + 64 p^2.
+constexpr int kScalEnd = 128, kScalLeft = 132, kScalBeta = 144, kScalValue = 145;
+constexpr float kEndFactor = 2.03f / 4096.f, kLeftFactor = 130.f;
 
 struct PrefillChunk {
   int t0, count;  // tokens t0 .. t0 + count - 1 of the packed activations

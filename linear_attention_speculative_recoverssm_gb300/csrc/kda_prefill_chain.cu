@@ -14,19 +14,27 @@
 // (rows) 32 (w & 3) .. and quarter w >> 2 of the columns.  O leaves while the
 // next chunk's M1 runs.  Warp 16 issues the MMAs, warp 17 the copies.
 //
-// FP16 parts of a row are taken times powers of two.  With M a bound of |S|
-// and |v| over the row, S goes times 1024 f and R and U times f, f M between 2
-// and 2^5 (f is kept while that holds): then S is below 2^15, R below 12.4 2^5
-// and U below 76 2^5 (a row of the state grows by at most beta |v| a token),
-// and with the images' own scales every accumulator comes out where it is
-// needed: dS in the state's units, U in those of its parts, both terms of O
-// alike, nothing to multiply.  M is known before dS is: the largest |S| before
-// the chunk plus 64 times the largest |U| in it (unit keys), or the largest
-// |v| to come.  Where that is too much by bits, the parts have them to spare
-// (2^-25 of values up to 2^15 and 2^5).  So the rows' quarters exchange their
-// peaks while M3 runs, and nothing waits between dS and S but the arithmetic;
-// M3 and M1 go by halves of the key channels, E0 of the one under the other's
-// MMAs.
+// FP16 parts of a row are taken times powers of two: S times 2^6 f, U times f,
+// R times a factor fr of its own, so that with the images' scales dS comes out
+// in the state's units and both terms of O alike.  A part ends at 2^-24, so
+// each factor is as large as what it holds allows, and follows what S, U and R
+// themselves can be: of the state a chunk began with only what its decays leave
+// counts, values behind a nearly closed write gate count for R and not for U.
+// With B a bound of |S| over the row, V the largest |v| of the chunk and p at
+// least its largest beta,
+//   |R| <= V + sqrt(128) B,  |U| <= (p + 64 p^2) V + sqrt(128) p B
+// (unit keys; a row's norm grows by at most beta |v| a token), and B itself is
+//   |S before|_2 max e^{G_end} + 8 |U'|_2,
+// U' being U times the largest decay from the end of its block of 16 tokens to
+// the chunk's (the sum of 64 of them is at most 8 times their norm); (x + y)^2
+// <= 2 x^2 + 2 y^2 makes Z = (f B)^2 of two sums of squares.  f is kept while
+// Z < 2^18 and f (p + 64 p^2) V < 2^14, which hold S and U below 2^15, and one
+// of them is not 2^10 or 2^5 below that.  All of it is known before dS is, from
+// a chunk's image and U: the rows' quarters exchange squares while M3 runs, and
+// nothing waits between dS and S but the arithmetic; M3 and M1 go by halves of
+// the key channels, E0 of the one under the other's MMAs.  For states that last
+// B is some 2^5 above |S|: U's parts keep 2^-29 of U's size, and more where
+// much is forgotten, so that a chunk may leave some 2^-14 of the sizes in it.
 // The state itself stays in FP32, in registers: an accumulator that is added
 // to over and over loses up to a unit of its last place each time, so dS is
 // summed apart, smallest parts first.
@@ -81,9 +89,10 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t n, bool mn) {
 struct ChainSmem {
   uint8_t a[kBufA][kPartA], b[kBufB][kPartB], c[kBufC][kPartC];  // multiples of 1024 bytes
   uint8_t v[2][kVBytes];
-  float decay[4][kDim];  // of chunk i at i & 3
+  float decay[4][kImgTail / 4];  // decays and scalars of chunk i at i & 3
   PrefillChunk chunk[4];  // chunk i at i & 3, there when its v is
-  float4 peak[2][kParts][128];  // [chunk parity][part][row]: |S|, |U|, next |v|
+  // [chunk parity][part][row]: squares of S and of U', in parts' units; next |v|
+  float4 peak[2][kParts][128];
   uint64_t a_full[kBufA], a_free[kBufA], b_full[kBufB], b_free[kBufB];
   uint64_t c_full[kBufC], c_free[kBufC];
   uint64_t v_full[2], v_free[2], d_full[4];
@@ -151,14 +160,23 @@ __device__ __forceinline__ void tmem_store_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// The row factor f for a bound M: kept while f M stays in 2 .. 2^5, else the
-// power of two with f M in 2^3 .. 2^4 (at most 2^100: zero rows).
-__device__ __forceinline__ float row_factor(float f, float m) {
-  const float fm = f * m;
-  if (fm >= 2.f && fm <= 32.f) return f;
-  const int e = (int)((__float_as_uint(m) >> 23) & 255u);
-  const int s = 127 + 3 + 127 - e;
-  return __uint_as_float((uint32_t)(s > 227 ? 227 : s) << 23);
+// floor(log2 |x|) (128 for infinities and NaN, -127 for zero).
+__device__ __forceinline__ int exponent(float x) {
+  return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// f for a row of zeros, and for the bounds B and V' = (p + 64 p^2) V.
+constexpr int kMostExp = 90;
+__device__ __forceinline__ float row_factor(float b, float v) {
+  return pow2(min(max(min(8 - exponent(b), 13 - exponent(v)) - 2, -109), kMostExp));
+}
+
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ float pow2_inverse(float s) {
@@ -181,18 +199,12 @@ __device__ __forceinline__ float2 less_half(float2 x, __half2 h) {
   return d;
 }
 
-// Two values as FP16 and what that leaves; `peak` the largest |hi| so far.
-__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo, __half2 &peak) {
+// Two values as FP16 and what that leaves.
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
   const __half2 h = __float22half2_rn(x);
-  peak = __hmax2(peak, __habs2(h));
   const __half2 l = __float22half2_rn(less_half(x, h));
   hi = *reinterpret_cast<const uint32_t *>(&h);
   lo = *reinterpret_cast<const uint32_t *>(&l);
-}
-
-__device__ __forceinline__ float max_of(__half2 x) {
-  const float2 f = __half22float2(x);
-  return fmaxf(f.x, f.y);
 }
 
 // A part of a state page's row (kKeys key channels).
@@ -380,7 +392,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       // activations, is not used
       const PrefillChunk ck = coming;
       coming = p.chunks[base + min(i + 1, n - 1)];
-      sm.chunk[i & 3] = ck;  // (its place was chunk i - 4's: long emitted)
+      // (the places of chunk i - 4: its outputs and state were done before any
+      // row warp released v of chunk i - 2)
+      sm.chunk[i & 3] = ck;
+      mbar_arrive_expect_tx(&sm.d_full[i & 3], kImgTail);
+      bulk_g2s(sm.decay[i & 3], images + i * img_step + kImgDecay, kImgTail, &sm.d_full[i & 3]);
       mbar_arrive_expect_tx(bar, kVBytes);
       tma_load_3d(sm.v[i & 1], &v_map, 0, h, ck.t0, bar);
     };
@@ -398,12 +414,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     load_v(0);
     for (int i = 0; i < n && ok; ++i) {
       load_part(i, kBufA, sm.a_full, sm.a_free, sm.a[0], 0, kPartA, n_a);
-      if (ok && lane == 0) {
-        // (the place of chunk i - 4's: the state has had them since before
-        // chunk i - 2 released its Kd)
-        mbar_arrive_expect_tx(&sm.d_full[i & 3], kDim * 4);
-        bulk_g2s(sm.decay[i & 3], images + i * img_step + kImgDecay, kDim * 4, &sm.d_full[i & 3]);
-      }
       if (ok && i + 1 < n) load_v(i + 1);
       if (ok) load_part(i, kBufB, sm.b_full, sm.b_free, sm.b[0], kPartA, kPartB, n_b);
       if (ok) load_part(i, kBufC, sm.c_full, sm.c_free, sm.c[0], kPartA + kPartB, kPartC, n_c);
@@ -421,7 +431,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       settle_all(sm.a_full, kBufA, n_a);
       settle_all(sm.b_full, kBufB, n_b);
       settle_all(sm.c_full, kBufC, n_c);
-      settle_all(sm.d_full, 4, n_a);
+      settle_all(sm.d_full, 4, n_v);
       settle(&sm.v_full[0], (n_v + 1) / 2);
       settle(&sm.v_full[1], n_v / 2);
     }
@@ -521,6 +531,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
     }
     constexpr float kDown = 1.f / kImgScale;
+    constexpr float kUnit = kImgKeScale, kPerUnit = 1.f / kImgKeScale;  // S's factor over f
+    static_assert(kImgKeScale * kImgQdScale == kImgScale, "both terms of O alike");
     const auto f2 = [](uint32_t x, uint32_t y) {
       return make_float2(__uint_as_float(x), __uint_as_float(y));
     };
@@ -557,26 +569,47 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       if (lane == 0) mbar_arrive(&sm.v_free[i & 1]);
       return fmaxf(__low2float(peak), __high2float(peak));
     };
-    // this row's bound M from its parts' peaks
-    const auto bound_of = [&](int i) {
-      float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+    // the sum of what this row's parts left at [i & 1], of |v| the largest
+    const auto joined = [&](int i) {
+      float4 m = sm.peak[i & 1][0][row];
 #pragma unroll
-      for (int j = 0; j < kParts; ++j) {
+      for (int j = 1; j < kParts; ++j) {
         const float4 x = sm.peak[i & 1][j][row];
-        m = make_float4(fmaxf(m.x, x.x), fmaxf(m.y, x.y), fmaxf(m.z, x.z), 0.f);
+        m = make_float4(m.x + x.x, m.y + x.y, fmaxf(m.z, x.z), 0.f);
       }
-      return fmaxf(fmaf(64.f, m.y, m.x), m.z);
+      return m;
     };
-    float peak_s = 0.f;  // largest |S| of this part
+    const auto max4 = [](const float *x) {
+      const float4 v = lds4(x);
+      return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+    };
+    float most_s = 0.f;  // largest |S| of this part
 #pragma unroll
     for (int e = 0; e < kKeys / 2; ++e)
-      peak_s = fmaxf(peak_s, fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
-    sm.peak[1][qt][row] = make_float4(peak_s, 0.f, load_v(0), 0.f);
+      most_s = fmaxf(most_s, fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
+    static_assert(kKeys == 32, "5.7 is above its root");
+    sm.peak[1][qt][row] = make_float4(5.7f * most_s, 0.f, load_v(0), 0.f);
+    wait(&sm.d_full[0], 0u);
     bad = named_bar_or(1, 32 * kRowWarps, bad);
-    // s holds the state times 1024 f from here on; inv = 1 / f
-    float f = row_factor(0.f, bound_of(1)), inv = pow2_inverse(f);
+    // s holds the state times 2^6 f from here on; inv = 1 / f
+    float f, inv;
+    int most_r;  // no |R| of the chunk reaches 2^most_r
+    {
+      const float4 m = joined(1);
+      f = row_factor(m.x, m.z * sm.decay[0][kScalValue]);
+      inv = pow2_inverse(f);
+      most_r = max(exponent(m.x) + 4, exponent(m.z)) + 2;
+    }
 #pragma unroll
-    for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(s[e], both(f * kImgScale));
+    for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(s[e], both(f * kUnit));
+    float squares = 0.f;  // of s
+    const auto square = [&] {
+      float2 ss[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int e = 0; e < kKeys / 2; ++e) ss[e & 1] = ffma2(s[e], s[e], ss[e & 1]);
+      squares = (ss[0].x + ss[0].y) + (ss[1].x + ss[1].y);
+    };
+    square();
     // S <- S e^{G_end} + dS of chunk i
     const auto advance = [&](int i) {
       if (!wait(&sm.ds_full[half], (uint32_t)i & 1u)) return;
@@ -594,6 +627,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           y = ffma2(y, make_float2(g.z, g.w), f2(d[2 * e + 2], d[2 * e + 3]));
         }
       }
+      square();
     };
     // the outputs of chunk i
     const auto emit = [&](int i, float inv) {
@@ -622,10 +656,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     };
     // the state to a page; to the next segment (slot < 0)
     const auto store = [&](int slot) {
-      if (slot < 0) store_state<false>(carry(), row, qt, s, inv * kDown);
-      else store_state<BF16>(page(slot), row, qt, s, inv * kDown);
+      if (slot < 0) store_state<false>(carry(), row, qt, s, inv * kPerUnit);
+      else store_state<BF16>(page(slot), row, qt, s, inv * kPerUnit);
     };
-    float f_next = f;       // the next chunk's factor
+    float f_next = f;
     bool changes = false;   // for any row of the warp
     for (int i = 0; i < n; ++i) {
       float inv_before = inv;
@@ -634,21 +668,22 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         if (bad) break;
         if (i == bnd_at) store(request().bnd);
         if (changes) {
-          const float2 by = both(f_next * inv);
+          // (one after the other: the factors' quotient may be out of range)
 #pragma unroll
-          for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(s[e], by);
+          for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(fmul2(s[e], both(f_next)), both(inv));
           f = f_next;
           inv = pow2_inverse(f);
+          square();
+          changes = false;
         }
       }
       // S as parts
       {
-        __half2 peak = __float2half2_rn(0.f);
 #pragma unroll
         for (int j = 0; j < kKeys / 16; ++j) {
           uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) split2(s[8 * j + e], hi[e], lo[e], peak);
+          for (int e = 0; e < 8; ++e) split2(s[8 * j + e], hi[e], lo[e]);
           tmem_store8(lanes + kColSHi + (uint32_t)(kKeys / 2 * qt + 8 * j), hi);
           tmem_store8(lanes + kColSLo + (uint32_t)(kKeys / 2 * qt + 8 * j), lo);
         }
@@ -656,14 +691,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.s_ready[half]);
-        peak_s = max_of(peak) * (kDown * inv);
       }
       if (i > 0) emit(i - 1, inv_before);
       // R = V - W
+      const float fr = pow2(min(max(15 - most_r, -113), 100));
+      const float w = -kDown * kPerUnit * fr * inv;
       if (!wait(&sm.w_full, (uint32_t)i & 1u)) break;
       tc_fence_after();
       {
-        __half2 unused = __float2half2_rn(0.f);
 #pragma unroll
         for (int k = 0; k < kToks / 16; ++k) {
           uint32_t d[16], hi[8], lo[8];
@@ -673,8 +708,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             const uint32_t vv = v2[8 * k + j];
             const float2 v = make_float2(__uint_as_float(vv << 16),
                                          __uint_as_float(vv & 0xffff0000u));
-            split2(ffma2(f2(d[2 * j], d[2 * j + 1]), both(-kDown * kDown), fmul2(v, both(f))),
-                   hi[j], lo[j], unused);
+            split2(ffma2(f2(d[2 * j], d[2 * j + 1]), both(w), fmul2(v, both(fr))), hi[j],
+                   lo[j]);
           }
           tmem_store8(lanes + kColRHi + (uint32_t)(kToks / 2 * qt + 8 * k), hi);
           tmem_store8(lanes + kColRLo + (uint32_t)(kToks / 2 * qt + 8 * k), lo);
@@ -684,34 +719,55 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.r_ready);
       }
-      const float peak_v = i + 1 < n ? load_v(i + 1) : 0.f;
-      // U
+      float peak_v = 0.f;
+      if (i + 1 < n) {
+        peak_v = load_v(i + 1);
+        if (!wait(&sm.d_full[(i + 1) & 3], (uint32_t)((i + 1) >> 2) & 1u)) break;
+      }
+      // U: T's scale and R's off, its own on (f p / fr is at most 4)
+      const float *const tail = sm.decay[i & 3];
+      const float by = f * tail[kScalBeta] * (pow2_inverse(fr) * (1.f / kImgTScale));
+      static_assert(kToks == 16, "a part's tokens are a block of the scalars'");
+      const float left = qt < kParts - 1 ? max4(tail + kScalLeft + 4 * qt) : kLeftFactor;
+      float2 uu[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       if (!wait(&sm.u_full, (uint32_t)i & 1u)) break;
       tc_fence_after();
       {
-        __half2 peak = __float2half2_rn(0.f);
 #pragma unroll
         for (int k = 0; k < kToks / 16; ++k) {
           uint32_t d[16], hi[8], lo[8];
           tmem_load16(lanes + kColW + (uint32_t)(kToks * qt + 16 * k), d);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) split2(f2(d[2 * j], d[2 * j + 1]), hi[j], lo[j], peak);
+          for (int j = 0; j < 8; ++j) {
+            const float2 u = fmul2(f2(d[2 * j], d[2 * j + 1]), both(by));
+            uu[j & 1] = ffma2(u, u, uu[j & 1]);
+            split2(u, hi[j], lo[j]);
+          }
           tmem_store8(lanes + kColRHi + (uint32_t)(kToks / 2 * qt + 8 * k), hi);
           tmem_store8(lanes + kColRLo + (uint32_t)(kToks / 2 * qt + 8 * k), lo);
         }
-        sm.peak[i & 1][qt][row] = make_float4(peak_s, max_of(peak) * inv, peak_v, 0.f);
+        sm.peak[i & 1][qt][row] =
+            make_float4(squares, left * ((uu[0].x + uu[0].y) + (uu[1].x + uu[1].y)), peak_v, 0.f);
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.u_ready);
       }
-      // under M3: every row's peaks are there once all warps have arrived, and
-      // the chunk's decays have long been
-      if (!wait(&sm.u_ready, (uint32_t)i & 1u) ||
-          !wait(&sm.d_full[i & 3], (uint32_t)(i >> 2) & 1u))
-        break;
-      f_next = row_factor(f, bound_of(i));
-      changes = __any_sync(0xffffffffu, f_next != f);
+      // under M3: every row's squares are there once all warps have arrived
+      if (!wait(&sm.u_ready, (uint32_t)i & 1u)) break;
+      if (i + 1 < n) {
+        const float4 m = joined(i);
+        const float z = fmaf(m.x, max4(tail + kScalEnd), m.y);
+        const float v = m.z * sm.decay[(i + 1) & 3][kScalValue], fv = f * v;
+        const bool keep = z < 0x1p18f && fv < 0x1p14f &&
+                          (z >= 0x1p8f || fv >= 0x1p9f || f == pow2(kMostExp));
+        if (__any_sync(0xffffffffu, !keep)) {
+          f_next = keep ? f : row_factor(sqrt_fast(z) * inv, v);
+          changes = __any_sync(0xffffffffu, f_next != f);
+        }
+        // (sqrt(128) B is below 2^4 B, and of the sum each at most half)
+        most_r = max(((exponent(z) + 1) >> 1) - exponent(f) + 4, exponent(m.z)) + 2;
+      }
     }
     if (!bad) advance(n - 1);
     if (!bad) {

@@ -76,7 +76,7 @@ struct PrepSmem {
   union {
     struct {
       union {
-        float fac[3][4][128];        // [R, C, Ke][block][channel], times 1024
+        float fac[3][4][128];        // [R, C, Ke][block][channel], times their scales
         float Lt[4][kLtSize];        // then the diagonal blocks of L, transposed
       };
       uint16_t pow[4][128];    // FP16 2^n: of Kd and Qd
@@ -109,6 +109,19 @@ __device__ __forceinline__ uint32_t x_at(int r, int piece) {
   const int f = ((r & 1) << 2) | ((r >> 1) & 3);
   return (uint32_t)r * kXPitch + (uint32_t)(piece >> 3) * 128u +
          (uint32_t)(((piece & 7) ^ f) << 4);
+}
+
+// The largest of a warp's non-negative values.
+__device__ __forceinline__ float warp_max(float x) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+}
+
+// The power of two above the chunk's largest beta, 2^-100 at least: every warp
+// for itself.
+__device__ __forceinline__ float beta_power(const float *beta, int lane) {
+  const float m = warp_max(fmaxf(beta[lane], beta[lane + 32]));
+  const int e = (int)(__float_as_uint(m) >> 23) + 1;
+  return __uint_as_float((uint32_t)min(max(e, 27), 128) << 23);
 }
 
 // The leading 11 bits of x (truncated), and x rounded to them as the tensor
@@ -439,18 +452,32 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
         sm.fac[0][j][c] = kImgScale * exp2f_fast(ta[j] + ph[j]);
         sm.pow[j][c] = power(B[j]);
       }
-      reinterpret_cast<float *>(img + kImgDecay)[c] =
+      float *const tail = reinterpret_cast<float *>(img + kImgDecay);
+      const float end =
           exp2f_fast((ta[0] + tb[0]) + (ta[1] + tb[1]) + (ta[2] + tb[2]) + (ta[3] + tb[3]));
+      tail[c] = end;
+      const float most = warp_max(end);
+      if (lane == 0) tail[kScalEnd + warp] = kEndFactor * (most * most);
     } else {
+      float *const tail = reinterpret_cast<float *>(img + kImgDecay);
       float rest = 0.f;
 #pragma unroll
       for (int j = 3; j >= 0; --j) {
         sm.fac[1][j][c] = kImgScale * exp2f_fast(tb[j] - ph[j + 1]);
-        sm.fac[2][j][c] = kImgScale * exp2f_fast(tb[j] + rest);
+        sm.fac[2][j][c] = kImgKeScale * exp2f_fast(tb[j] + rest);
+        if (j < 3) {
+          const float most = warp_max(exp2f_fast(rest));
+          if (lane == 0) tail[kScalLeft + 4 * j + warp - 4] = kLeftFactor * (most * most);
+        }
         rest += ta[j] + tb[j];
       }
       sm.pow32[0][c] = power(B[2] - B[1]);
       sm.pow32[1][c] = power(B[3] - B[2]);
+      const float p2 = beta_power(sm.beta, lane);
+      if (tid == 128) {
+        tail[kScalBeta] = p2;
+        tail[kScalValue] = p2 + 64.f * p2 * p2;
+      }
     }
   }
   float rk[2], rq[2];
@@ -588,7 +615,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
         }
         times(qf[r], fac, x);
         hi = half8(x);
-        constexpr uint32_t kDown = 0x14001400u;  // FP16 2^-10, twice: Qd has no scale
+        constexpr uint32_t kDown = 0x24002400u;  // FP16 2^-6, twice: Qd's own scale
+        static_assert(kImgQdScale == kImgScale / 64, "2^-6");
         put(im + 1024 * r + kImgQd,
             scale8(blk == 0 ? hi : scale8(hi, pow0), make_uint4(kDown, kDown, kDown, kDown)));
         if (blk & 1) put(sm.u.x.y16 + (y16_0 ^ (64u * sl)) + 8 * r * kXPitch, hi);
@@ -780,8 +808,12 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   tile_mm(c, &X[(32 + m32) * kXPitchF + 32], kXPitchF, &Y[n32], kYPitch, 0, m32 / 8 + 2, lane);
   // -- T = X diag(beta): the lower left quarter from registers, the two on the
   //    diagonal from X, zeros above ------------------------------------------
+  static_assert(kImgTScale == 16384.f, "2^14");
+  const float t_scale =
+      __uint_as_float((268u << 23) - __float_as_uint(beta_power(sm.beta, lane)));  // 2^14 / p
   {
-    const float b0 = -sm.beta[n32 + 2 * tig], b1 = -sm.beta[n32 + 2 * tig + 1];
+    const float b0 = -sm.beta[n32 + 2 * tig] * t_scale;
+    const float b1 = -sm.beta[n32 + 2 * tig + 1] * t_scale;
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
       const float2 v = make_float2(c[i] * b0, c[i + 1] * b1);
@@ -799,7 +831,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
     load4x2(&sm.beta[s0], b);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 y = fmul2(v[i], b[i]);
+      const float2 y = fmul2(v[i], fmul2(b[i], make_float2(t_scale, t_scale)));
       // (what lies above the diagonal was not all written)
       v[i] = make_float2(s0 + 2 * i <= t ? y.x : 0.f, s0 + 2 * i + 1 <= t ? y.y : 0.f);
     }
