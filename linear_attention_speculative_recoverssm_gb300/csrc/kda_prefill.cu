@@ -37,7 +37,7 @@ constexpr int kSegItems = 57, kSegChunks = 32, kMaxSegments = 16;
 constexpr int kSegDoubleItems = 38, kSegFirst = 16;
 
 struct Workspace {
-  int64_t chunks, bases, order, carry, images, bytes;  // offsets
+  int64_t chunks, bases, order, lost, redo, carry, images, bytes;  // offsets
   int64_t max_chunks;
 };
 
@@ -52,7 +52,9 @@ Workspace workspace_layout(int64_t n_tokens, int64_t B, int64_t H) {
   const bool segments = B * H <= kSegItems;
   w.bases = up(w.chunks + w.max_chunks * (int64_t)sizeof(PrefillChunk));
   w.order = up(w.bases + B * 4 * (segments ? kMaxSegments : 1));
-  w.carry = up(w.order + B * (int64_t)sizeof(PrefillRequest));
+  w.lost = up(w.order + B * (int64_t)sizeof(PrefillRequest));
+  w.redo = up(w.lost + (segments ? B * H * 4 : 0));
+  w.carry = up(w.redo + B * H * (int64_t)sizeof(PrefillRedo));
   w.images = up(w.carry + (segments ? B * H * kDim * kDim * 4 : 0));
   w.bytes = w.images + w.max_chunks * H * (int64_t)kImgBytes;
   return w;
@@ -133,6 +135,7 @@ __global__ void __launch_bounds__(32) kda_prefill_list_warp_kernel(const Prefill
     write_chunks(p, (int)at, mine, done, t0, first, m, n);
   }
   if (b == 0) p.seg_first[p.segments] = (int)min(base, (long long)room);
+  if (b == 0) *p.n_redo = 0;
   if (b < B) p.order[place] = PrefillRequest{b, kept, first, (int)start};
 }
 
@@ -204,6 +207,7 @@ __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const Pr
     }
   }
   if (tid == 0) p.seg_first[p.segments] = (int)min(base, (long long)room);
+  if (tid == 0) *p.n_redo = 0;
   // bins, longest first -> where each begins
   const int bin = kListThreads - 1 - tid;
   const int mine = bins[bin];
@@ -297,6 +301,10 @@ int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const k
   const int parts = p.seg_doubles ? (1 << p.segments) - 1 : p.segments;
   p.seg_chunks = (most + parts - 1) / parts;
   p.seg_first = reinterpret_cast<int *>(ws);
+  static_assert(4 * (kda::kMaxSegments + 1) <= 128, "n_redo behind them");
+  p.n_redo = reinterpret_cast<int *>(ws + 128);
+  p.lost = reinterpret_cast<int *>(ws + w.lost);
+  p.redo = reinterpret_cast<kda::PrefillRedo *>(ws + w.redo);
   p.bases = reinterpret_cast<int *>(ws + w.bases);
   p.carry = reinterpret_cast<float *>(ws + w.carry);
   p.chunks = reinterpret_cast<kda::PrefillChunk *>(ws + w.chunks);
@@ -318,10 +326,13 @@ int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const k
     rc = kda::launch_prefill_chain(p, seg, bf16, st);
     if (rc != KDA_OK) return rc;
   }
-  if (p.short_len == 0) return KDA_OK;
-  p.r.beside = true;
-  p.r.max_len = p.short_len;
-  return kda::launch_recurrent(p.r, bf16, st);
+  if (p.short_len != 0) {
+    p.r.beside = true;
+    p.r.max_len = p.short_len;
+    rc = kda::launch_recurrent(p.r, bf16, st);
+    if (rc != KDA_OK) return rc;
+  }
+  return kda::launch_prefill_redo(p, bf16, st);
 }
 
 }  // extern "C"

@@ -69,6 +69,12 @@ struct __align__(16) PrefillRequest {
   int base;        // its first chunk of segment 0
 };
 
+// A (request, head) of which a chain's parts lost something (LostRows): by its
+// place in the chain's grid, and which of its four groups of 32 rows.
+struct PrefillRedo {
+  int item, groups;
+};
+
 // The chunks go by segments of every request, seg_from(s) .. seg_from(s + 1) - 1
 // of each at a time: the preparation of one and then its chain, whose CTAs leave the state to the
 // next segment's in FP32.  The next preparation runs beside the chain.
@@ -83,6 +89,9 @@ struct PrefillParams {
   int *bases;               // [segments, B], a request's first chunk of each
   PrefillRequest *order;    // [B], by falling number of chunks
   float *carry;             // [B, H, 128, 128] (segments > 1)
+  int *lost;                // [B, H], the groups lost so far (segments > 1)
+  int *n_redo;
+  PrefillRedo *redo;        // [B * H], the first n_redo
   uint8_t *images;          // [max_chunks, H, kImgBytes]
 };
 
@@ -94,5 +103,7 @@ __host__ __device__ __forceinline__ int seg_from(const PrefillParams &p, int s) 
 // chain before it has, and ends after it.
 int launch_prefill_prep(const PrefillParams &p, int segment, cudaStream_t stream);
 int launch_prefill_chain(const PrefillParams &p, int segment, bool bf16, cudaStream_t stream);
+// After the last segment's chain: what `redo` lists once more, from its source.
+int launch_prefill_redo(const PrefillParams &p, bool bf16, cudaStream_t stream);
 
 }  // namespace kda

@@ -35,6 +35,13 @@
 // the key channels, E0 of the one under the other's MMAs.  For states that last
 // B is some 2^5 above |S|: U's parts keep 2^-29 of U's size, and more where
 // much is forgotten, so that a chunk may leave some 2^-14 of the sizes in it.
+// Where a chunk leaves less in all rows of a group of 32 (those of one warp), or
+// has tokens whose sizes are as far below the largest, the parts cannot hold it.
+// The chain finds that when it has the next state's norms; the group's rows then
+// go through the chunks once more, from the source, in a second kernel behind
+// it, which looks before it goes on and does such a chunk token by token
+// (CAREFUL).  Both in one kernel leave a chunk's path too few registers: 16384
+// tokens took 895 us in place of 843.
 // The state itself stays in FP32, in registers: an accumulator that is added
 // to over and over loses up to a unit of its last place each time, so dS is
 // summed apart, smallest parts first.
@@ -49,6 +56,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstddef>
 
 #include "../../include/kda_recoverssm.h"
 #include "kda_launch.h"
@@ -91,12 +99,22 @@ struct ChainSmem {
   uint8_t v[2][kVBytes];
   float decay[4][kImgTail / 4];  // decays and scalars of chunk i at i & 3
   PrefillChunk chunk[4];  // chunk i at i & 3, there when its v is
-  // [chunk parity][part][row]: squares of S and of U', in parts' units; next |v|
+  // [chunk parity][part][row]: squares of S and of U', in parts' units; next |v|;
+  // squares of U over the part's block of tokens
   float4 peak[2][kParts][128];
+  uint32_t kept[4][kParts];  // by row warps w & 3 and part: what a chunk left (CAREFUL)
+  float least[2][128];       // [chunk parity][row]: see is_lost
+  int lost;                  // the groups of rows that parts lost something of, a bit each
+  // The item: its request, head, chunks and boundary as the row warps need them
+  // (what they keep in registers costs them others in every chunk).
+  struct {
+    int b, h, n, bnd_at, ends;
+  } item;
   uint64_t a_full[kBufA], a_free[kBufA], b_full[kBufB], b_free[kBufB];
   uint64_t c_full[kBufC], c_free[kBufC];
   uint64_t v_full[2], v_free[2], d_full[4];
   uint64_t s_ready[2], r_ready, u_ready, w_full, u_full, ds_full[2], o_full, drained;
+  uint64_t advanced[4], token[4];  // of the four warps of the same rows
   uint32_t tmem;
 };
 static_assert(kPartA % 1024 == 0 && kPartB % 1024 == 0 && kPartC % 1024 == 0, "swizzle atoms");
@@ -306,6 +324,79 @@ struct MnMajor {
   }
 };
 
+// A chunk's tokens one after the other in FP32, its outputs stored and the
+// state `s` (as it is, not scaled) advanced: by the four warps of the same
+// rows, for a chunk that the parts cannot hold.  Some 0.6 us a token.  What a
+// row's parts add up goes through their places in sm.peak of the chunk before,
+// which have been read (each token's by turns in two of the four floats).
+// False: a wait ran out.
+__device__ __noinline__ bool rows_by_token(const RecurrentParams &r, ChainSmem &sm, int chunk,
+                                           int h, int row, int part, volatile float *state) {
+  float2 s[kKeys / 2];
+#pragma unroll
+  for (int e = 0; e < kKeys / 2; ++e) s[e] = make_float2(state[2 * e], state[2 * e + 1]);
+  const int lane = row & 31;
+  const PrefillChunk ck = sm.chunk[chunk & 3];
+  const float a = expf(r.A_log[h]);
+  const float4 dt = *reinterpret_cast<const float4 *>(r.dt_bias + h * kDim + 4 * lane);
+  uint64_t *const bar = &sm.token[row >> 5];
+  bool ok = true;
+  static_assert(kChunk % 2 == 0, "the barrier ends on the parity that it began with");
+#pragma unroll 1
+  for (int t = 0; t < kChunk && ok; ++t) {
+    Token tk;
+    float v = 0.f;
+    const long long at = (long long)(ck.t0 + min(t, ck.count - 1)) * r.H + h;
+    if (t < ck.count) {
+      tk = make_token(r, load_token(r, at, lane), a, dt);
+      v = bf16_bits_to_f32(r.v[at * kDim + row]);
+      // (channel c of a token is held by lane c / 4)
+      const auto of = [&](const float4 &x, int e) {
+        const int from = (kKeys / 4) * part + (e >> 1);
+        return (e & 1) ? make_float2(__shfl_sync(0xffffffffu, x.z, from),
+                                     __shfl_sync(0xffffffffu, x.w, from))
+                       : make_float2(__shfl_sync(0xffffffffu, x.x, from),
+                                     __shfl_sync(0xffffffffu, x.y, from));
+      };
+      float2 w = make_float2(0.f, 0.f), y = w;
+#pragma unroll
+      for (int e = 0; e < kKeys / 2; ++e) {
+        s[e] = fmul2(s[e], of(tk.d, e));
+        w = ffma2(s[e], of(tk.k, e), w);
+        y = ffma2(s[e], of(tk.q, e), y);
+      }
+      reinterpret_cast<float2 *>(&sm.peak[(chunk + 1) & 1][part][row])[t & 1] =
+          make_float2(w.x + w.y, y.x + y.y);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)t & 1u));
+    if (t >= ck.count || !ok) continue;
+    float w = 0.f, y = 0.f;
+#pragma unroll
+    for (int j = 0; j < kParts; ++j) {
+      const float2 x = reinterpret_cast<const float2 *>(&sm.peak[(chunk + 1) & 1][j][row])[t & 1];
+      w += x.x;
+      y += x.y;
+    }
+    const float u = tk.beta * (v - w);
+    if (part == 0) r.out[at * kDim + row] = f32_to_bf16_bits(fmaf(u, tk.kq, y));
+#pragma unroll
+    for (int e = 0; e < kKeys / 2; ++e) {
+      const int from = (kKeys / 4) * part + (e >> 1);
+      const float k0 = __shfl_sync(0xffffffffu, (e & 1) ? tk.k.z : tk.k.x, from);
+      const float k1 = __shfl_sync(0xffffffffu, (e & 1) ? tk.k.w : tk.k.y, from);
+      s[e] = ffma2(make_float2(u, u), make_float2(k0, k1), s[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kKeys / 2; ++e) {
+    state[2 * e] = s[e].x;
+    state[2 * e + 1] = s[e].y;
+  }
+  return ok;
+}
+
 // Zeros to the outputs of an inert request's head.
 __device__ __forceinline__ void zero_inert(const PrefillParams &p, int b, int h) {
   const PromptRequest rq = prompt_request(p.r.maps, b);
@@ -316,18 +407,22 @@ __device__ __forceinline__ void zero_inert(const PrefillParams &p, int b, int h)
                                i % (kDim / 8) * 8) = make_uint4(0, 0, 0, 0);
 }
 
-template <bool BF16>
+// CAREFUL: the redo list's items, all of their chunks, every segment's.
+template <bool BF16, bool CAREFUL>
 __global__ void __launch_bounds__(kChainThreads, 1)
-    kda_prefill_chain_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap v_map,
-                             int segment) {
+    kda_prefill_chain_kernel(const __grid_constant__ PrefillParams p,
+                             const __grid_constant__ CUtensorMap v_map, int segment) {
   // (the swizzle atoms want 1024 bytes; there is no other shared memory)
   extern __shared__ __align__(1024) uint8_t chain_raw[];
   const int H = p.r.H;
   ChainSmem &sm = *reinterpret_cast<ChainSmem *>(chain_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int32_t *status = p.r.maps.status;
+  const auto give_up = [&] {
+    report(p.r.maps.status, KDA_ERR_TIMEOUT);
+    if constexpr (CAREFUL) atomicOr(&sm.lost, 1);  // (goes to no other item)
+  };
   // what does not need the preparation, while its last CTAs may still run
-  if (threadIdx.x == 0) {
+  const auto init_barriers = [&] {
     const auto init = [](uint64_t *full, uint64_t *free, int n) {
       for (int i = 0; i < n; ++i) {
         mbar_init(full + i, 1);
@@ -345,6 +440,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       mbar_init(&sm.s_ready[i], kRowWarps / 2);
       mbar_init(&sm.ds_full[i], 1);
     }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.advanced[i], kParts);
+      mbar_init(&sm.token[i], kParts);
+    }
     mbar_init(&sm.r_ready, kRowWarps);
     mbar_init(&sm.u_ready, kRowWarps);
     mbar_init(&sm.w_full, 1);
@@ -352,26 +451,51 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.drained, 1);
     mbar_init_fence();
-  }
-  if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
+    sm.lost = 0;
+  };
+  if (threadIdx.x == 0) init_barriers();
+  if (!CAREFUL && warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
   grid_dependency_wait();
   // (only now: the next kernel may count on what this one has waited for)
   grid_launch_dependents();
-  const PrefillRequest req = p.order[blockIdx.x / H];
-  const int b = req.b, h = blockIdx.x % H;
+  int listed = blockIdx.x;
+  const int n_listed = CAREFUL ? __ldcg(p.n_redo) : 0;
+  if constexpr (CAREFUL) {
+    if (listed >= n_listed) return;
+    if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
+  }
+  while (!CAREFUL || listed < n_listed) {
+  PrefillRedo redo{(int)blockIdx.x, 15};
+  if constexpr (CAREFUL)
+    redo = PrefillRedo{__ldcg(&p.redo[listed].item), __ldcg(&p.redo[listed].groups)};
+  const PrefillRequest req = p.order[redo.item / H];
+  const int b = req.b, h = redo.item % H;
   // this segment's chunks: done, done + 1 .. done + n - 1 of the request's
-  const int done = seg_from(p, segment);
-  const int n = max(min(req.chunks, seg_from(p, segment + 1)) - done, 0);
+  const int done = CAREFUL ? 0 : seg_from(p, segment);
+  const int n = CAREFUL ? req.chunks : max(min(req.chunks, seg_from(p, segment + 1)) - done, 0);
+  const bool starts = CAREFUL || segment == 0;
   const bool ends = done + n == req.chunks;
   const int bnd_at = req.bnd_chunks > 0 ? req.bnd_chunks - done : -1;  // in its chunks
-  const int base = segment == 0 ? req.base : p.bases[segment * p.r.maps.B + b];
+  const int base = starts ? req.base : p.bases[segment * p.r.maps.B + b];
   const int src = prompt_request(p.r.maps, b).src;  // (of segment 0)
+  if (threadIdx.x == 0) {
+    if (!starts) sm.lost = p.lost[b * H + h];
+    sm.item.b = b, sm.item.h = h, sm.item.n = n, sm.item.bnd_at = bnd_at, sm.item.ends = ends;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const uint8_t *images = p.images + ((long long)base * H + h) * kImgBytes;
-  const long long img_step = (long long)H * kImgBytes;
+  // the list's place of chunk i, and its image
+  const auto place = [&](int i) {
+    if constexpr (!CAREFUL) return base + i;
+    int s = 0;
+    while (s + 1 < p.segments && seg_from(p, s + 1) <= i) ++s;
+    return p.bases[s * p.r.maps.B + b] + i - seg_from(p, s);
+  };
+  const auto image = [&](int i) {
+    return p.images + ((long long)place(i) * H + h) * kImgBytes;
+  };
 
   if (n == 0) {
     if (segment == 0 && p.short_len == 0) zero_inert(p, b, h);
@@ -379,7 +503,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     // -- copies ---------------------------------------------------------------
     bool ok = true;
     int n_v = 0, n_a = 0, n_b = 0, n_c = 0;  // copies issued of each kind
-    PrefillChunk coming = p.chunks[base];    // the next chunk whose v is copied
+    PrefillChunk coming = p.chunks[place(0)];  // the next chunk whose v is copied
     const auto load_v = [&](int i) {
       uint64_t *bar = &sm.v_full[i & 1];
       if (i >= 2) ok = ok && mbar_wait_bounded(&sm.v_free[i & 1], (uint32_t)((i >> 1) - 1) & 1u);
@@ -391,12 +515,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       // 75 cycles each); what is past it, rows of others or the zeros past the
       // activations, is not used
       const PrefillChunk ck = coming;
-      coming = p.chunks[base + min(i + 1, n - 1)];
+      coming = p.chunks[place(min(i + 1, n - 1))];
       // (the places of chunk i - 4: its outputs and state were done before any
       // row warp released v of chunk i - 2)
       sm.chunk[i & 3] = ck;
       mbar_arrive_expect_tx(&sm.d_full[i & 3], kImgTail);
-      bulk_g2s(sm.decay[i & 3], images + i * img_step + kImgDecay, kImgTail, &sm.d_full[i & 3]);
+      bulk_g2s(sm.decay[i & 3], image(i) + kImgDecay, kImgTail, &sm.d_full[i & 3]);
       mbar_arrive_expect_tx(bar, kVBytes);
       tma_load_3d(sm.v[i & 1], &v_map, 0, h, ck.t0, bar);
     };
@@ -409,7 +533,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       issued = i + 1;
       if (lane != 0) return;
       mbar_arrive_expect_tx(full + which, bytes);
-      bulk_g2s(dst + which * bytes, images + i * img_step + at, bytes, full + which);
+      bulk_g2s(dst + which * bytes, image(i) + at, bytes, full + which);
     };
     load_v(0);
     for (int i = 0; i < n && ok; ++i) {
@@ -421,7 +545,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     if (!ok) {
       // every copy issued lands before the CTA can exit: the last phase in
       // use of each barrier
-      if (lane == 0) report(status, KDA_ERR_TIMEOUT);
+      if (lane == 0) give_up();
       const auto settle = [&](uint64_t *bar, int uses) {
         if (uses > 0) mbar_wait_bounded(bar, (uint32_t)(uses - 1) & 1u);
       };
@@ -492,7 +616,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       commit(&sm.o_full);
       commit(&sm.c_free[ic]);
     }
-    if (!ok && lead) report(status, KDA_ERR_TIMEOUT);
+    if (!ok && lead) give_up();
     // nothing of this CTA's is in flight when its columns are released
     commit(&sm.drained);
     mbar_wait_bounded(&sm.drained, 0u);
@@ -500,30 +624,27 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     // -- rows -------------------------------------------------------------------
     const int row = 32 * (warp & 3) + lane, qt = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    // The pages' addresses are made where they are used, from values that the
-    // compiler takes for new each time: kept through the loop they would take
-    // registers that it has not got.
+    // The pages' addresses are made where they are used, from values that are
+    // read anew each time: kept through the loop they would take registers that
+    // it has not got.
+    const auto now = [](const int &x) { return *const_cast<const volatile int *>(&x); };
     const auto page = [&](int slot) {
-      long long at = h;
-      asm volatile("" : "+l"(at));
       return reinterpret_cast<char *>(p.r.state) +
-             ((long long)slot * p.r.slot_stride + at * kDim * kDim) * (BF16 ? 2 : 4);
+             ((long long)slot * p.r.slot_stride + (long long)now(sm.item.h) * kDim * kDim) *
+                 (BF16 ? 2 : 4);
     };
     const auto carry = [&] {
-      long long at = (long long)b * H + h;
-      asm volatile("" : "+l"(at));
-      return p.carry + at * kDim * kDim;
+      return p.carry + ((long long)now(sm.item.b) * H + now(sm.item.h)) * kDim * kDim;
     };
-    const auto request = [&] {
-      int at = b;
-      asm volatile("" : "+r"(at));
-      return prompt_request(p.r.maps, at);
-    };
+    const auto request = [&] { return prompt_request(p.r.maps, now(sm.item.b)); };
     float2 s[kKeys / 2];  // this row's key channels from kKeys qt on
-    if (segment > 0) {
+    const int group = warp & 3;
+    // (rows that are not to be done again run along, from zeros)
+    const bool live = !CAREFUL || ((redo.groups >> group) & 1);
+    if (!starts) {
       load_state<false>(carry(), row, qt, s);
     } else {
-      if (src >= 0) {
+      if (src >= 0 && live) {
         load_state<BF16>(page(src), row, qt, s);
       } else {
 #pragma unroll
@@ -569,13 +690,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       if (lane == 0) mbar_arrive(&sm.v_free[i & 1]);
       return fmaxf(__low2float(peak), __high2float(peak));
     };
-    // the sum of what this row's parts left at [i & 1], of |v| the largest
+    // the sum of what this row's parts left at [i & 1], of |v| the largest, of
+    // the blocks' U the smallest
     const auto joined = [&](int i) {
       float4 m = sm.peak[i & 1][0][row];
 #pragma unroll
       for (int j = 1; j < kParts; ++j) {
         const float4 x = sm.peak[i & 1][j][row];
-        m = make_float4(m.x + x.x, m.y + x.y, fmaxf(m.z, x.z), 0.f);
+        m = make_float4(m.x + x.x, m.y + x.y, fmaxf(m.z, x.z), fminf(m.w, x.w));
       }
       return m;
     };
@@ -609,10 +731,71 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       for (int e = 0; e < kKeys / 2; ++e) ss[e & 1] = ffma2(s[e], s[e], ss[e & 1]);
       squares = (ss[0].x + ss[0].y) + (ss[1].x + ss[1].y);
     };
+    const auto is_marked = [&] { return ((now(sm.lost) >> group) & 1) != 0; };
     square();
+    // The parts end a fixed way below what they could hold, 2^-24 / f, and what
+    // of that reaches the state measures some 2^-27 / f.  A chunk is lost for a
+    // group of rows that is left with norms below 2^-11 / f throughout: 2^-16 of
+    // the largest row.  So it is where a block of 16 tokens has no U above that,
+    // nor had the state before the chunk: of its outputs not enough would be left
+    // (values before an outlying one).
+    constexpr float kLeast = 0x1p-11f;
+    constexpr float kLeastSquare = kLeast * kUnit * (kLeast * kUnit);
+    // (CAREFUL) Before the next chunk: where that is so for the largest of the
+    // four parts' norms, the chunk is done again token by token, from the state
+    // before it.  Its parts are still in TMEM, and hold it to 2^-19 of its rows;
+    // where they would not, `by_token` was set before dS was there.  All four
+    // warps come to that together: one whose rows all keep more says so, and
+    // only one that cannot waits for what the others say.
+    bool by_token = false;
+    const auto check = [&](int i) {
+      uint32_t mine = 0xffffffffu;  // (every row keeps enough)
+      bool finite = true;
+      const bool doubt = !by_token && live &&
+                         !__all_sync(0xffffffffu, squares >= kLeastSquare || f == pow2(kMostExp));
+      if (doubt) {
+        // (a row that is not finite asks for nothing)
+        const float n = sqrt_fast(squares) * (inv * kPerUnit);
+        finite = n < __int_as_float(0x7f800000);
+        mine = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(n) : 0u);
+      }
+      if (lane == 0) {
+        sm.kept[group][qt] = mine;
+        mbar_arrive(&sm.advanced[group]);
+      }
+      if (!doubt || !wait(&sm.advanced[group], (uint32_t)i & 1u)) return;
+      uint32_t most = 0;
+#pragma unroll
+      for (int j = 0; j < kParts; ++j) most = max(most, sm.kept[group][j]);
+      const float floor = kLeast * __uint_as_float(__reduce_max_sync(
+                                       0xffffffffu, finite ? __float_as_uint(inv) : 0u));
+      by_token = most != 0xffffffffu && __uint_as_float(most) < floor && floor > 0x1p-100f;
+      if (by_token) {
+        uint32_t d[16];
+        tmem_load16(lanes + kColSHi + (uint32_t)(kKeys / 2 * qt), d);
+#pragma unroll
+        for (int e = 0; e < kKeys / 2; ++e)
+          s[e] = __half22float2(*reinterpret_cast<const __half2 *>(&d[e]));
+        tmem_load16(lanes + kColSLo + (uint32_t)(kKeys / 2 * qt), d);
+#pragma unroll
+        for (int e = 0; e < kKeys / 2; ++e)
+          s[e] = ffma2(both(1.f), s[e], __half22float2(*reinterpret_cast<const __half2 *>(&d[e])));
+      }
+    };
+    // The same of rows whose squares are brought together, in units of f;
+    // `least` is kLeastSquare in those units where f is not the chunk's.
+    const auto is_lost = [&](float squares, float least) {
+      const float n = sqrt_fast(squares) * (inv * kPerUnit);
+      const float floor = sqrt_fast(least) * (inv * kPerUnit);
+      const bool finite = n < __int_as_float(0x7f800000);
+      const uint32_t most = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(n) : 0u);
+      const uint32_t worst = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(floor) : 0u);
+      return most < worst && __uint_as_float(worst) > 0x1p-100f;
+    };
     // S <- S e^{G_end} + dS of chunk i
     const auto advance = [&](int i) {
       if (!wait(&sm.ds_full[half], (uint32_t)i & 1u)) return;
+      if (CAREFUL && by_token) return check(i);
       tc_fence_after();
       const float *dec = sm.decay[i & 3] + kKeys * qt;
 #pragma unroll
@@ -628,10 +811,15 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
       }
       square();
+      if constexpr (CAREFUL) check(i);
     };
     // the outputs of chunk i
     const auto emit = [&](int i, float inv) {
       if (!wait(&sm.o_full, (uint32_t)i & 1u)) return;
+      if (CAREFUL && (by_token || !live)) {
+        by_token = false;  // (they are there)
+        return;
+      }
       tc_fence_after();
       const float f = p.r.q_scale * kDown * inv;
       const uint32_t step = (uint32_t)H * kDim;
@@ -641,7 +829,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         const int t = kToks * qt + 16 * k;
         uint32_t d[16];
         tmem_load16(lanes + kColO + 64u * (i & 1) + (uint32_t)t, d);
-        uint16_t *o = p.r.out + (long long)(ck.t0 + t) * step + h * kDim + row;
+        uint16_t *o = p.r.out + (long long)(ck.t0 + t) * step + now(sm.item.h) * kDim + row;
         const int left = ck.count - t;
         if (left >= 16) {
 #pragma unroll
@@ -659,24 +847,45 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       if (slot < 0) store_state<false>(carry(), row, qt, s, inv * kPerUnit);
       else store_state<BF16>(page(slot), row, qt, s, inv * kPerUnit);
     };
+    // The state after the boundary.  The chain keeps the source as it is while
+    // it may have to go again: where the boundary's slot is the source, the
+    // destination's holds it until the end.
+    const auto store_boundary = [&] {
+      const PromptRequest r = request();
+      if (CAREFUL ? live : !is_marked()) store(!CAREFUL && r.bnd == r.src ? r.dst : r.bnd);
+    };
+    const auto settle_boundary = [&] {
+      const PromptRequest r = request();
+      if (r.bnd < 0 || r.bnd != r.src || now(sm.item.bnd_at) > now(sm.item.n)) return;  // (cut off)
+      constexpr int kPieces = kKeys * (BF16 ? 2 : 4) / 16;
+      const long long at = ((long long)row * kParts + qt) * kPieces;
+      const uint4 *const from = reinterpret_cast<const uint4 *>(page(r.dst)) + at;
+      uint4 *const to = reinterpret_cast<uint4 *>(page(r.bnd)) + at;
+#pragma unroll 1
+      for (int e = 0; e < kPieces; ++e) to[e] = from[e];
+    };
     float f_next = f;
     bool changes = false;   // for any row of the warp
-    for (int i = 0; i < n; ++i) {
-      float inv_before = inv;
-      if (i > 0) {
-        advance(i - 1);
-        if (bad) break;
-        if (i == bnd_at) store(request().bnd);
-        if (changes) {
-          // (one after the other: the factors' quotient may be out of range)
+    // What a state that is ready goes through.
+    const auto rescale = [&](int i) {
+      float least = kLeastSquare;
+      if (changes) {
+        // (one after the other: the factors' quotient may be out of range)
+        least *= f_next * inv * (f_next * inv);
 #pragma unroll
-          for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(fmul2(s[e], both(f_next)), both(inv));
-          f = f_next;
-          inv = pow2_inverse(f);
-          square();
-          changes = false;
-        }
+        for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(fmul2(s[e], both(f_next)), both(inv));
+        f = f_next;
+        inv = pow2_inverse(f);
+        square();
+        changes = false;
       }
+      if (!CAREFUL && qt == 0) sm.least[i & 1][row] = least;
+    };
+    const auto pass = [&](int i, float inv_before) {
+      // (what the factors are made of goes to memory at once: the registers are
+      // wanted)
+      float *const peak = reinterpret_cast<float *>(&sm.peak[i & 1][qt][row]);
+      peak[0] = squares;
       // S as parts
       {
 #pragma unroll
@@ -696,7 +905,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       // R = V - W
       const float fr = pow2(min(max(15 - most_r, -113), 100));
       const float w = -kDown * kPerUnit * fr * inv;
-      if (!wait(&sm.w_full, (uint32_t)i & 1u)) break;
+      if (!wait(&sm.w_full, (uint32_t)i & 1u)) return false;
       tc_fence_after();
       {
 #pragma unroll
@@ -719,10 +928,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.r_ready);
       }
-      float peak_v = 0.f;
-      if (i + 1 < n) {
-        peak_v = load_v(i + 1);
-        if (!wait(&sm.d_full[(i + 1) & 3], (uint32_t)((i + 1) >> 2) & 1u)) break;
+      peak[2] = 0.f;
+      if (i + 1 < now(sm.item.n)) {
+        peak[2] = load_v(i + 1);
+        if (!wait(&sm.d_full[(i + 1) & 3], (uint32_t)((i + 1) >> 2) & 1u)) return false;
       }
       // U: T's scale and R's off, its own on (f p / fr is at most 4)
       const float *const tail = sm.decay[i & 3];
@@ -730,7 +939,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       static_assert(kToks == 16, "a part's tokens are a block of the scalars'");
       const float left = qt < kParts - 1 ? max4(tail + kScalLeft + 4 * qt) : kLeftFactor;
       float2 uu[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      if (!wait(&sm.u_full, (uint32_t)i & 1u)) break;
+      if (!wait(&sm.u_full, (uint32_t)i & 1u)) return false;
       tc_fence_after();
       {
 #pragma unroll
@@ -746,48 +955,146 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           tmem_store8(lanes + kColRHi + (uint32_t)(kToks / 2 * qt + 8 * k), hi);
           tmem_store8(lanes + kColRLo + (uint32_t)(kToks / 2 * qt + 8 * k), lo);
         }
-        sm.peak[i & 1][qt][row] =
-            make_float4(squares, left * ((uu[0].x + uu[0].y) + (uu[1].x + uu[1].y)), peak_v, 0.f);
+        const float u2 = (uu[0].x + uu[0].y) + (uu[1].x + uu[1].y);
+        // (a block past the chunk's tokens has none)
+        peak[1] = left * u2;
+        peak[3] = kToks * qt < sm.chunk[i & 3].count ? u2 : __int_as_float(0x7f800000);
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.u_ready);
       }
       // under M3: every row's squares are there once all warps have arrived
-      if (!wait(&sm.u_ready, (uint32_t)i & 1u)) break;
-      if (i + 1 < n) {
+      if (!wait(&sm.u_ready, (uint32_t)i & 1u)) return false;
+      {  // (of the last chunk only what was lost before it counts)
         const float4 m = joined(i);
         const float z = fmaf(m.x, max4(tail + kScalEnd), m.y);
         const float v = m.z * sm.decay[(i + 1) & 3][kScalValue], fv = f * v;
         const bool keep = z < 0x1p18f && fv < 0x1p14f &&
                           (z >= 0x1p8f || fv >= 0x1p9f || f == pow2(kMostExp));
-        if (__any_sync(0xffffffffu, !keep)) {
+        // (CAREFUL: a state that its parts would not give back; a fresh one is
+        // zeros)
+        const float least = CAREFUL || i == 0 ? 0.f : sm.least[i & 1][row];
+        const bool low = CAREFUL ? m.x < 0x1p-12f && f != pow2(kMostExp) && (i > 0 || src >= 0)
+                                 : m.x < least;
+        const float some = fmaxf(m.x, kUnit * kUnit * m.w);
+        if (__any_sync(0xffffffffu, !keep || low || some < kLeastSquare)) {
+          const bool thin = is_lost(some, kLeastSquare);
+          if constexpr (CAREFUL) by_token = live && (__any_sync(0xffffffffu, low) || thin);
+          else if ((thin || is_lost(m.x, least)) && lane == 0) atomicOr(&sm.lost, 1 << group);
           f_next = keep ? f : row_factor(sqrt_fast(z) * inv, v);
           changes = __any_sync(0xffffffffu, f_next != f);
         }
         // (sqrt(128) B is below 2^4 B, and of the sum each at most half)
         most_r = max(((exponent(z) + 1) >> 1) - exponent(f) + 4, exponent(m.z)) + 2;
       }
+      return true;
+    };
+    if constexpr (!CAREFUL) {
+      for (int i = 0; i < now(sm.item.n); ++i) {
+        const float inv_before = inv;
+        if (i > 0) {
+          advance(i - 1);
+          if (bad) break;
+          if (i == now(sm.item.bnd_at)) store_boundary();
+          rescale(i);
+        }
+        if (!pass(i, inv_before)) break;
+      }
+      if (!bad) advance(now(sm.item.n) - 1);
+      if (!bad && now(sm.item.n) == now(sm.item.bnd_at)) store_boundary();
+    } else {
+      // (by token: through memory, so that what the chunks need in registers is
+      // not kept in them meanwhile)
+      volatile float held[kKeys + kToks / 2 + 3];
+      for (int i = 0;;) {
+        const float inv_before = inv;
+        if (i > 0) rescale(i);
+        if (!pass(i, inv_before)) break;
+        advance(i);
+        if (bad) break;
+        if (by_token) {
+#pragma unroll
+          for (int e = 0; e < kKeys / 2; ++e) {
+            held[2 * e] = s[e].x * (inv * kPerUnit);
+            held[2 * e + 1] = s[e].y * (inv * kPerUnit);
+          }
+#pragma unroll
+          for (int e = 0; e < kToks / 2; ++e) held[kKeys + e] = __uint_as_float(v2[e]);
+          held[kKeys + kToks / 2] = f;
+          held[kKeys + kToks / 2 + 1] = f_next;
+          held[kKeys + kToks / 2 + 2] = __int_as_float(most_r);
+          if (!rows_by_token(p.r, sm, i, now(sm.item.h), row, qt, held)) {
+            bad = true;
+            break;
+          }
+          f = held[kKeys + kToks / 2];
+          f_next = held[kKeys + kToks / 2 + 1];
+          most_r = __float_as_int(held[kKeys + kToks / 2 + 2]);
+          inv = pow2_inverse(f);
+          changes = __any_sync(0xffffffffu, f_next != f);
+#pragma unroll
+          for (int e = 0; e < kKeys / 2; ++e)
+            s[e] = fmul2(make_float2(held[2 * e], held[2 * e + 1]), both(f * kUnit));
+#pragma unroll
+          for (int e = 0; e < kToks / 2; ++e) v2[e] = __float_as_uint(held[kKeys + e]);
+          square();
+        }
+        ++i;
+        if (i == now(sm.item.bnd_at)) store_boundary();
+        if (i == now(sm.item.n)) break;
+      }
     }
-    if (!bad) advance(n - 1);
+    if constexpr (!CAREFUL) {
+      // the last chunk's, whose norms nothing else brings together
+      const int n = now(sm.item.n);
+      sm.peak[n & 1][qt][row].x = squares;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.advanced[group]);
+      if (!bad && wait(&sm.advanced[group], 0u) && is_lost(joined(n).x, kLeastSquare) && lane == 0)
+        atomicOr(&sm.lost, 1 << group);
+      __syncwarp();
+    }
     if (!bad) {
-      if (n == bnd_at) store(request().bnd);
-      store(ends ? request().dst : -1);
-      emit(n - 1, inv);
+      const bool marked = !CAREFUL && is_marked();
+      const bool ends = now(sm.item.ends) != 0;
+      if (ends && !CAREFUL && !marked) settle_boundary();
+      if (live && !(ends && marked)) store(ends ? request().dst : -1);
+      emit(now(sm.item.n) - 1, inv);
     }
-    if (bad && lane == 0) report(status, KDA_ERR_TIMEOUT);
+    if (bad && lane == 0) give_up();
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (!CAREFUL) {
+    if (n > 0 && threadIdx.x == 0) {
+      if (p.segments > 1) p.lost[b * H + h] = sm.lost;
+      if (ends && sm.lost != 0) p.redo[atomicAdd(p.n_redo, 1)] = PrefillRedo{redo.item, sm.lost};
+    }
+    break;
+  }
+  if (sm.lost != 0) break;
+  listed += gridDim.x;
+  if (listed < n_listed) {
+    // (no wait or arrival is left of the item before)
+    if (threadIdx.x == 0) {
+      constexpr int kBars = (offsetof(ChainSmem, tmem) - offsetof(ChainSmem, a_full)) / 8;
+      for (int j = 0; j < kBars; ++j) mbar_inval(sm.a_full + j);
+      init_barriers();
+    }
+    __syncthreads();
+  }
+  }
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(sm.tmem, kTmemCols);
   }
 }
 
 }  // namespace
 
-int launch_prefill_chain(const PrefillParams &p, int segment, bool bf16, cudaStream_t stream) {
+// The chain of a segment; of what the redo list holds (segment < 0).
+static int launch_chain(const PrefillParams &p, int segment, bool bf16, cudaStream_t stream) {
   static std::atomic<uint64_t> configured{0};
   constexpr uint32_t kSmem = sizeof(ChainSmem);
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -796,13 +1103,13 @@ int launch_prefill_chain(const PrefillParams &p, int segment, bool bf16, cudaStr
   if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load() & bit)) {
-    if (cudaFuncSetAttribute(kda_prefill_chain_kernel<false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(kda_prefill_chain_kernel<true>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmem) != cudaSuccess)
-      return KDA_ERR_CUDA;
+    for (const auto kernel : {kda_prefill_chain_kernel<false, false>,
+                              kda_prefill_chain_kernel<true, false>,
+                              kda_prefill_chain_kernel<false, true>,
+                              kda_prefill_chain_kernel<true, true>})
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)kSmem) != cudaSuccess)
+        return KDA_ERR_CUDA;
     configured.fetch_or(bit);
   }
   // v [n_tokens, H, 128] as a 3-D tensor, a chunk's rows of one head a copy
@@ -823,15 +1130,26 @@ int launch_prefill_chain(const PrefillParams &p, int segment, bool bf16, cudaStr
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.r.maps.B * p.r.H));
+  const int items = p.r.maps.B * p.r.H, sms = device_sm_count(dev);
+  cfg.gridDim = dim3((unsigned)(segment < 0 && sms > 0 && sms < items ? sms : items));
   cfg.blockDim = dim3(kChainThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto kernel = bf16 ? kda_prefill_chain_kernel<true> : kda_prefill_chain_kernel<false>;
+  const auto kernel =
+      segment < 0 ? (bf16 ? kda_prefill_chain_kernel<true, true> : kda_prefill_chain_kernel<false, true>)
+                  : (bf16 ? kda_prefill_chain_kernel<true, false> : kda_prefill_chain_kernel<false, false>);
   if (cudaLaunchKernelEx(&cfg, kernel, p, v_map, segment) != cudaSuccess) return KDA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int launch_prefill_chain(const PrefillParams &p, int segment, bool bf16, cudaStream_t stream) {
+  return launch_chain(p, segment, bf16, stream);
+}
+
+int launch_prefill_redo(const PrefillParams &p, bool bf16, cudaStream_t stream) {
+  return launch_chain(p, -1, bf16, stream);
 }
 
 }  // namespace kda

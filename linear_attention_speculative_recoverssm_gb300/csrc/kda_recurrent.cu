@@ -39,59 +39,6 @@ constexpr int kRecRows = 16;  // state rows of a warp
 constexpr int kGroup = 8;     // tokens whose operands are made at a time,
 constexpr int kGroupWarps = 4;  // by so many warps
 
-__device__ __forceinline__ float4 bf16x4_to_f32(uint32_t lo, uint32_t hi) {
-  return make_float4(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u),
-                     __uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
-}
-
-// One token's operands as loaded, four channels to a lane.
-struct RawToken {
-  uint2 q, k, g, v;
-  uint16_t beta;
-};
-
-// Row `row` of the activations.
-__device__ __forceinline__ RawToken load_token(const RecurrentParams &p, long long row, int lane) {
-  const long long base = row * kDim;
-  RawToken t;
-  t.q = __ldg(reinterpret_cast<const uint2 *>(p.q + base) + lane);
-  t.k = __ldg(reinterpret_cast<const uint2 *>(p.k + base) + lane);
-  t.g = __ldg(reinterpret_cast<const uint2 *>(p.g + base) + lane);
-  t.v = __ldg(reinterpret_cast<const uint2 *>(p.v + base) + lane);
-  t.beta = __ldg(p.beta + row);
-  return t;
-}
-
-// The same, worked out: the lane's channels of d, kn and qn, and kn . qn (with
-// q_scale) and beta.
-struct Token {
-  float4 d, k, q;
-  float kq, beta;
-};
-
-// `a` is exp(A_log) of the head, `dt` the lane's channels' bias.
-__device__ __forceinline__ Token make_token(const RecurrentParams &p, const RawToken &r, float a,
-                                            float4 dt) {
-  Token t;
-  const float4 q = bf16x4_to_f32(r.q.x, r.q.y), k = bf16x4_to_f32(r.k.x, r.k.y);
-  const float4 g = bf16x4_to_f32(r.g.x, r.g.y);
-  float qq = q.x * q.x + q.y * q.y + q.z * q.z + q.w * q.w;
-  float kk = k.x * k.x + k.y * k.y + k.z * k.z + k.w * k.w;
-  float kq = k.x * q.x + k.y * q.y + k.z * q.z + k.w * q.w;
-  qq = warp_sum(qq);
-  kk = warp_sum(kk);
-  kq = warp_sum(kq);
-  const float qs = rsqrtf(qq + kNormEps) * p.q_scale, ks = rsqrtf(kk + kNormEps);
-  t.d = make_float4(gate_decay(a, g.x, dt.x, p.lower_bound), gate_decay(a, g.y, dt.y, p.lower_bound),
-                    gate_decay(a, g.z, dt.z, p.lower_bound),
-                    gate_decay(a, g.w, dt.w, p.lower_bound));
-  t.k = make_float4(k.x * ks, k.y * ks, k.z * ks, k.w * ks);
-  t.q = make_float4(q.x * qs, q.y * qs, q.z * qs, q.w * qs);
-  t.kq = kq * qs * ks;
-  t.beta = 1.f / (1.f + __expf(-bf16_bits_to_f32(r.beta)));
-  return t;
-}
-
 // What both kernels do first: this item's request, reported if it is wrong,
 // its outputs zeroed if it is inert.  False: nothing is left to do.
 __device__ __forceinline__ bool begin_item(const RecurrentParams &p, int b, int h, int row0,
