@@ -36,7 +36,8 @@
 // B is some 2^5 above |S|: U's parts keep 2^-29 of U's size, and more where
 // much is forgotten, so that a chunk may leave some 2^-14 of the sizes in it.
 // Where a chunk leaves less in all rows of a group of 32 (those of one warp), or
-// has tokens whose sizes are as far below the largest, the parts cannot hold it.
+// has tokens whose sizes are as far below the largest, or something in it is not
+// finite, the parts cannot hold it.
 // The chain finds that when it has the next state's norms; the group's rows then
 // go through the chunks once more, from the source, in a second kernel behind
 // it, which looks before it goes on and does such a chunk token by token
@@ -182,6 +183,8 @@ __device__ __forceinline__ void tmem_store_wait() {
 __device__ __forceinline__ int exponent(float x) {
   return (int)((__float_as_uint(x) >> 23) & 255u) - 127;
 }
+
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -718,7 +721,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     int most_r;  // no |R| of the chunk reaches 2^most_r
     {
       const float4 m = joined(1);
-      f = row_factor(m.x, m.z * sm.decay[0][kScalValue]);
+      const float v = m.z * sm.decay[0][kScalValue];
+      f = row_factor(m.x, is_finite(v) ? v : 0.f);
       inv = pow2_inverse(f);
       most_r = max(exponent(m.x) + 4, exponent(m.z)) + 2;
     }
@@ -756,7 +760,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       if (doubt) {
         // (a row that is not finite asks for nothing)
         const float n = sqrt_fast(squares) * (inv * kPerUnit);
-        finite = n < __int_as_float(0x7f800000);
+        finite = is_finite(n);
         mine = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(n) : 0u);
       }
       if (lane == 0) {
@@ -787,7 +791,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     const auto is_lost = [&](float squares, float least) {
       const float n = sqrt_fast(squares) * (inv * kPerUnit);
       const float floor = sqrt_fast(least) * (inv * kPerUnit);
-      const bool finite = n < __int_as_float(0x7f800000);
+      const bool finite = is_finite(n);
       const uint32_t most = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(n) : 0u);
       const uint32_t worst = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(floor) : 0u);
       return most < worst && __uint_as_float(worst) > 0x1p-100f;
@@ -969,7 +973,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       {  // (of the last chunk only what was lost before it counts)
         const float4 m = joined(i);
         const float z = fmaf(m.x, max4(tail + kScalEnd), m.y);
-        const float v = m.z * sm.decay[(i + 1) & 3][kScalValue], fv = f * v;
+        // (a chunk whose V is infinite goes token by token, from this state)
+        const float v0 = m.z * sm.decay[(i + 1) & 3][kScalValue];
+        const float v = is_finite(v0) ? v0 : 0.f, fv = f * v;
         const bool keep = z < 0x1p18f && fv < 0x1p14f &&
                           (z >= 0x1p8f || fv >= 0x1p9f || f == pow2(kMostExp));
         // (CAREFUL: a state that its parts would not give back; a fresh one is
@@ -979,7 +985,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                                  : m.x < least;
         const float some = fmaxf(m.x, kUnit * kUnit * m.w);
         if (__any_sync(0xffffffffu, !keep || low || some < kLeastSquare)) {
-          const bool thin = is_lost(some, kLeastSquare);
+          // An infinity or a NaN of one token is in the U of all of its chunk's
+          // (zeros of T times it), and not of those before it by the rule.  (A
+          // state that is not finite spoils all that follows by either.)
+          const bool wild = __any_sync(0xffffffffu, !is_finite(m.y) && is_finite(m.x));
+          const bool thin = wild || is_lost(some, kLeastSquare);
           if constexpr (CAREFUL) by_token = live && (__any_sync(0xffffffffu, low) || thin);
           else if ((thin || is_lost(m.x, least)) && lane == 0) atomicOr(&sm.lost, 1 << group);
           f_next = keep ? f : row_factor(sqrt_fast(z) * inv, v);

@@ -189,3 +189,37 @@ def test_some_rows_only(op):
     out = ko.bf16_to_f64(got)
     slack = (QUERY if op == "prefill" else REL) * sizes
     assert np.all(np.abs(out - f64) <= 2.0 ** -8 * np.abs(f64) + slack), "outputs"
+
+
+def same_finite(got, want, name):
+    np.testing.assert_array_equal(np.isfinite(got), np.isfinite(want), err_msg=name)
+
+
+@pytest.mark.parametrize("at", [30, 100, 127, 128])
+@pytest.mark.parametrize("bits", [0x7FC0, 0x7F80, 0xFF80])
+@pytest.mark.parametrize("name", ["q", "k", "v", "raw_g", "raw_beta"])
+def test_not_finite(name, bits, at):
+    """A NaN or an infinity of one token: the outputs before it are those
+    without it, and from it on what the recurrence makes of it."""
+    case = ragged_case(lens=[200, 150], H=2, seed=13, resume=(1,), boundary={0: at})
+    clean = {k: x.copy() if isinstance(x, np.ndarray) else x for k, x in case.items()}
+    for t in (at, 200 + at):  # (one channel of the first head, and all of its beta)
+        case[name][(t, 0, 5) if case[name].ndim == 3 else (t, 0)] = bits
+    got, state, status = run("prefill", case)
+    want, left, _ = run("recurrent", case)
+    assert status == 0
+    got, want = ko.bf16_to_f64(got), ko.bf16_to_f64(want)
+    same_finite(got, want, "outputs")
+    same_finite(state, left, "states")
+    f64, sizes = np.zeros(case["v"].shape), np.zeros(case["v"].shape)
+    po.rule(out_f64=f64, sizes=sizes, **clean)
+    close = np.abs(got - f64) <= 2.0 ** -8 * np.abs(f64) + QUERY * sizes
+    for t0, t1, h in ((0, at, 0), (200, 200 + at, 0), (0, 350, 1)):
+        assert np.all(close[t0:t1, h]), "outputs that it does not reach"
+    s = case["boundaries"][0]
+    assert np.abs(state[s] - clean["state"][s]).max() <= REL * np.abs(clean["state"][s]).max()
+    fin = np.isfinite(want)
+    rounded = 2 * 2.0 ** -8 * np.abs(want) + 2 * QUERY * np.nanmax(np.where(fin, np.abs(want), 0))
+    assert np.all((np.abs(got[fin] - want[fin]) <= rounded[fin]))
+    fin = np.isfinite(left)
+    assert np.all(np.abs(state[fin] - left[fin]) <= 2 * REL * np.abs(left[fin]).max())
