@@ -111,6 +111,13 @@ __device__ __forceinline__ uint32_t x_at(int r, int piece) {
          (uint32_t)(((piece & 7) ^ f) << 4);
 }
 
+// 2^x, as exp2f_fast but for results below 2^-126, which are not flushed.
+__device__ __forceinline__ float exp2f_subnormal(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The largest of a warp's non-negative values.
 __device__ __forceinline__ float warp_max(float x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
@@ -464,7 +471,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
 #pragma unroll
       for (int j = 3; j >= 0; --j) {
         sm.fac[1][j][c] = kImgScale * exp2f_fast(tb[j] - ph[j + 1]);
-        sm.fac[2][j][c] = kImgKeScale * exp2f_fast(tb[j] + rest);
+        // (2^-115 and less where a half block forgets that much, times 2^115: not
+        // flushed where it is subnormal, which leaves Ke to 2^-34; 6: its scale)
+        sm.fac[2][j][c] = exp2f_subnormal(tb[j] + rest + 6.f);
+        static_assert(kImgKeScale == 64.f, "2^6");
         if (j < 3) {
           const float most = warp_max(exp2f_fast(rest));
           if (lane == 0) tail[kScalLeft + 4 * j + warp - 4] = kLeftFactor * (most * most);

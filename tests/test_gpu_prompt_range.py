@@ -191,6 +191,19 @@ def test_some_rows_only(op):
     assert np.all(np.abs(out - f64) <= 2.0 ** -8 * np.abs(f64) + slack), "outputs"
 
 
+@OPS
+@pytest.mark.parametrize("lens", [[64], [100, 64]])
+def test_steep_half_block(op, lens):
+    """Gates that forget e^-10 a token for eight tokens, then a slow decline
+    behind closed write gates: the last of the eight is what is left."""
+    case = ragged_case(lens=lens, H=2, seed=14, resume=(), lower_bound=-10.0)
+    set_decay(case, -0.27)
+    for t0 in case["query_start_loc"][:-1]:
+        case["raw_g"][t0 + 24:t0 + 32] = synth.to_bf16_bits(np.array([30.0], np.float32))
+        case["raw_beta"][t0 + 32:t0 + 64] = synth.to_bf16_bits(np.array([-30.0], np.float32))
+    check(op, case)
+
+
 def same_finite(got, want, name):
     np.testing.assert_array_equal(np.isfinite(got), np.isfinite(want), err_msg=name)
 
