@@ -585,13 +585,18 @@ int kda_prefill_conv(const kda_bf16 *x, const kda_bf16 *conv_weight, const kda_b
  *   q, k, v, raw_g, out [n_tokens, H, 128], raw_beta [n_tokens, H] BF16;
  *   A_log [H], dt_bias [H, 128] FP32; state_pool [n_slots, H, 128, 128] of
  *   state_dtype, slot stride `slot_stride` elements (>= H*128*128).
- *   workspace  device, 16-byte aligned, at least kda_prefill_workspace_bytes(
- *              n_tokens, B, H) bytes, owned by the caller and not used by
- *              other work at the same time; may be NULL when that is 0.
+ *   workspace  device, 16-byte aligned, at least
+ *              kda_prefill_workspace_bytes_for(n_tokens, B, H, Q, boundaries
+ *              != NULL) bytes, owned by the caller and not used by other work
+ *              at the same time; may be NULL when that is 0, as it is for
+ *              calls whose windows are all short (Q or n_tokens at most 40).
  *              Nothing in it outlives the call's kernels.
+ *              kda_prefill_workspace_bytes is the size that does for any Q
+ *              and boundaries.  -1: an argument is out of range.
  * All pointers but raw_beta, A_log and the index arrays 16-byte aligned.
  */
 int64_t kda_prefill_workspace_bytes(int n_tokens, int B, int H);
+int64_t kda_prefill_workspace_bytes_for(int n_tokens, int B, int H, int Q, int has_boundaries);
 int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const kda_bf16 *raw_g,
                 const kda_bf16 *raw_beta, const float *A_log, const float *dt_bias,
                 float lower_bound, float q_scale, void *state_pool, int state_dtype,

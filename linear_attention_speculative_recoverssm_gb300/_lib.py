@@ -32,7 +32,8 @@ EXPORTS = ("kda_abi_version", "kda_error_string", "kda_check_status", "kda_verif
            "kda_commit", "kda_defer_commit", "kda_flush_plan", "kda_selftest_wait_timeout",
            "kda_layer_prologue", "kda_layer_epilogue", "kda_layer_step_workspace_bytes",
            "kda_layer_step", "kda_layer_step_noalloc", "kda_slot_plan", "kda_prefill_conv",
-           "kda_prefill_workspace_bytes", "kda_prefill", "kda_recurrent")
+           "kda_prefill_workspace_bytes", "kda_prefill_workspace_bytes_for", "kda_prefill",
+           "kda_recurrent")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -68,6 +69,7 @@ _SIGS = {
     "kda_prefill_conv": ([_P] * 4 + [_I64, _I, _I] + [_P] * 5 + [_I] + [_P] * 3
                          + [_I, _I, _I, _I, _P, _P], _I),
     "kda_prefill_workspace_bytes": ([_I, _I, _I], _I64),
+    "kda_prefill_workspace_bytes_for": ([_I, _I, _I, _I, _I], _I64),
     "kda_prefill": ([_P] * 7 + [_F, _F, _P, _I, _I64, _I] + [_P] * 5 + [_I, _P, _P, _I64]
                     + [_I, _I, _I, _I, _P, _P], _I),
     "kda_recurrent": ([_P] * 7 + [_F, _F, _P, _I, _I64, _I] + [_P] * 5 + [_I, _P]
@@ -565,10 +567,13 @@ def _rule_args(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources, de
             _row_stride(state_pool, H * 128 * 128))
 
 
-def kda_prefill_workspace_bytes(n_tokens, B, H):
+def kda_prefill_workspace_bytes(n_tokens, B, H, Q=None, boundaries=True):
     """Bytes of workspace kda_prefill needs for n_tokens packed tokens of B
-    requests."""
-    return load().kda_prefill_workspace_bytes(n_tokens, B, H)
+    requests; with ``Q`` (and ``boundaries`` False where there are none) for
+    windows of up to Q tokens, which may be far less (0 for Q <= 40)."""
+    if Q is None:
+        return load().kda_prefill_workspace_bytes(n_tokens, B, H)
+    return load().kda_prefill_workspace_bytes_for(n_tokens, B, H, Q, int(boundaries))
 
 
 def kda_prefill(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources, destinations,
@@ -581,8 +586,9 @@ def kda_prefill(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources, d
     start at null_slot) and left at ``destinations`` (and after boundary_lens
     tokens at ``boundaries``).  Q: at least the longest window;
     query_start_loc None: windows of Q tokens.  ``workspace``: a device
-    tensor of kda_prefill_workspace_bytes(T, B, H) bytes that nothing else
-    uses meanwhile; None takes it from torch's allocator for this call."""
+    tensor of kda_prefill_workspace_bytes(T, B, H, Q, boundaries is not None)
+    bytes that nothing else uses meanwhile; None takes it from torch's
+    allocator for this call."""
     import torch
     dtype, slot_stride = _rule_args(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources,
                                     destinations, query_start_loc, out, boundaries,
@@ -596,7 +602,7 @@ def kda_prefill(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources, d
     def call(st):
         ws = workspace
         if ws is None:
-            need = max(0, lib.kda_prefill_workspace_bytes(T, B, H))
+            need = max(0, lib.kda_prefill_workspace_bytes_for(T, B, H, Q, boundaries is not None))
             if stream is None:
                 ws = torch.empty(need, dtype=torch.uint8, device=q.device)
             else:

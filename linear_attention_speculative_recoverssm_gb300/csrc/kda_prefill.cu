@@ -41,13 +41,19 @@ struct Workspace {
   int64_t max_chunks;
 };
 
-// Chunks end at a request's boundary and at its end, so a request of n
-// tokens has at most n / 64 + 2, and one with any has more than kMixedLen.
-Workspace workspace_layout(int64_t n_tokens, int64_t B, int64_t H) {
+// Of windows of up to Q tokens.  Chunks end at a request's boundary (if there
+// are any) and at its end, so a request of n tokens has at most n / 64 + 2 (+ 1),
+// and one with any has more than kMixedLen.  A call without windows longer than
+// kShortLen has none.
+Workspace workspace_layout(int64_t n_tokens, int64_t B, int64_t H, int64_t Q, bool boundaries) {
   const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  const int64_t most = n_tokens / (kMixedLen + 1);
-  Workspace w;
-  w.max_chunks = n_tokens / kChunk + 2 * (B == 1 || B < most ? B : most);
+  const int64_t longest = Q < n_tokens ? Q : n_tokens, cuts = boundaries ? 2 : 1;
+  Workspace w = {};
+  if (longest <= kShortLen || B < 1) return w;
+  const int64_t most = n_tokens / (kMixedLen + 1), with = B == 1 || B < most ? B : most;
+  const int64_t by_tokens = n_tokens / kChunk + cuts * with;
+  const int64_t by_windows = with * ((longest - 1) / kChunk + cuts);
+  w.max_chunks = by_windows < by_tokens ? by_windows : by_tokens;
   w.chunks = 256;
   const bool segments = B * H <= kSegItems;
   w.bases = up(w.chunks + w.max_chunks * (int64_t)sizeof(PrefillChunk));
@@ -248,8 +254,12 @@ __global__ void __launch_bounds__(kListThreads) kda_prefill_list_kernel(const Pr
 extern "C" {
 
 int64_t kda_prefill_workspace_bytes(int n_tokens, int B, int H) {
-  if (n_tokens < 0 || B < 0 || H < 1 || H > KDA_PROMPT_MAX_HEADS) return -1;
-  return kda::workspace_layout(n_tokens, B, H).bytes;
+  return kda_prefill_workspace_bytes_for(n_tokens, B, H, n_tokens > 1 ? n_tokens : 1, 1);
+}
+
+int64_t kda_prefill_workspace_bytes_for(int n_tokens, int B, int H, int Q, int has_boundaries) {
+  if (n_tokens < 0 || B < 0 || H < 1 || H > KDA_PROMPT_MAX_HEADS || Q < 1) return -1;
+  return kda::workspace_layout(n_tokens, B, H, Q, has_boundaries != 0).bytes;
 }
 
 int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const kda_bf16 *raw_g,
@@ -269,23 +279,26 @@ int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const k
   rc = kda::check_rule(q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale, state_pool,
                        state_dtype, slot_stride, H, out);
   if (rc != KDA_OK) return rc;
-  const kda::Workspace w = kda::workspace_layout(n_tokens, B, H);
-  if (!workspace || workspace_bytes < w.bytes) return KDA_ERR_ARG;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return KDA_ERR_ALIGN;
-  if (w.max_chunks * H > 0x7fffffffLL) return KDA_ERR_ARG;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf16 = state_dtype == KDA_STATE_BF16;
+  const int longest = Q < n_tokens ? Q : n_tokens;
   kda::PrefillParams p;
   p.r = kda::RecurrentParams{q, k, v, raw_g, raw_beta, A_log, dt_bias, lower_bound, q_scale,
                              state_pool, slot_stride, out, H, kda::kShortLen, false,
                              kda::make_prompt_maps(sources, destinations, boundaries,
                                                    boundary_lens, query_start_loc, n_tokens,
                                                    n_slots, B, Q, null_slot, status)};
+  if (longest <= kda::kShortLen) return kda::launch_recurrent(p.r, bf16, st);
+  const kda::Workspace w = kda::workspace_layout(n_tokens, B, H, Q, boundaries != nullptr);
+  if (!workspace || workspace_bytes < w.bytes) return KDA_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return KDA_ERR_ALIGN;
+  if (w.max_chunks * H > 0x7fffffffLL) return KDA_ERR_ARG;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
   // a single request of any length is one launch less by chunks alone
   p.short_len = B == 1 ? 0 : kda::kMixedLen;
   p.max_chunks = (int)w.max_chunks;
   // the longest request's chunks: its own and one more where its boundary
   // cuts one in two
-  const int longest = Q < n_tokens ? Q : n_tokens;
   const int most = (longest - 1) / kda::kChunk + 1 + (boundaries != nullptr ? 1 : 0);
   p.segments = 1;
   p.seg_doubles = false;
@@ -310,9 +323,6 @@ int kda_prefill(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const k
   p.chunks = reinterpret_cast<kda::PrefillChunk *>(ws + w.chunks);
   p.order = reinterpret_cast<kda::PrefillRequest *>(ws + w.order);
   p.images = ws + w.images;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool bf16 = state_dtype == KDA_STATE_BF16;
-  if (longest <= kda::kShortLen) return kda::launch_recurrent(p.r, bf16, st);
   if (B <= 32)
     kda::kda_prefill_list_warp_kernel<<<1, 32, 0, st>>>(p);
   else
