@@ -606,8 +606,11 @@ def kda_prefill(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources, d
             if stream is None:
                 ws = torch.empty(need, dtype=torch.uint8, device=q.device)
             else:
-                # of the call's own stream: the allocator hands it on there
-                with torch.cuda.stream(torch.cuda.ExternalStream(st)):
+                # of the call's own stream: the allocator hands it on there (the
+                # default one has no address: ExternalStream(0) is another)
+                own = (torch.cuda.ExternalStream(st) if st
+                       else torch.cuda.default_stream(q.device))
+                with torch.cuda.stream(own):
                     ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         nbytes = ws.numel() * ws.element_size()
         return lib.kda_prefill(

@@ -71,3 +71,32 @@ def test_too_small_is_refused():
                   workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert torch.equal(before, d["state"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", ["default", "zero", "side", "address", "none"])
+def test_workspace_belongs_to_the_call_s_stream(which, monkeypatch):
+    """What the binding allocates is of the stream that the kernels run on:
+    another stream's next allocation does not take it while they run."""
+    import torch
+    from linear_attention_speculative_recoverssm_gb300 import kda_prefill
+    from prompt_testutil import call_rule, on_device, ragged_case
+    from test_gpu_prompt_rule import verify
+    case = ragged_case(lens=[70, 100], H=2, seed=3)
+    d = on_device(case)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stream, want = {"default": (torch.cuda.default_stream(), 0), "zero": (0, 0),
+                    "side": (side, side.cuda_stream), "none": (None, other.cuda_stream),
+                    "address": (side.cuda_stream, side.cuda_stream)}[which]
+    seen, empty = [], torch.empty
+    def noted(*args, **kw):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*args, **kw)
+    with torch.cuda.stream(other):
+        monkeypatch.setattr(torch, "empty", noted)
+        call_rule(kda_prefill, case, d, stream=stream)
+        monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert seen == [want]
+    verify("prefill", case, d)
