@@ -7,8 +7,9 @@ accepted tokens into each request's checkpoint.  The deferred form (page
 after sampling: the accepted count becomes the request's pending replay, and
 the next verify replays it in the same pass over the state.  This class only
 sequences the library's entry points in that order; every step runs in the
-library's kernels, on the given stream, with no host synchronisation, so a
-sequence of steps can be captured in a CUDA graph.
+library's kernels (and what a prompt does to the pending counts in a few of
+torch's), on the given stream, with no host synchronisation, so a sequence of
+steps can be captured in a CUDA graph.
 
 * ``prefill``: prompts are taken into their requests' checkpoints before the
   first step (in one call or in parts);
@@ -51,6 +52,8 @@ class DeferredRecoverSSM:
                       for name in ("commit_lens", "final_slots", "boundary_slots",
                                    "boundary_lens")}
         self._fresh = torch.full((self.B,), self.null_slot, dtype=torch.int32, device=dev)
+        self._none = torch.zeros(self.B, dtype=torch.int32, device=dev)
+        self._no_row = torch.tensor(-1, dtype=torch.int32, device=dev)
         self.flushed = False
 
     def _commit(self, commit_lens, destinations, boundaries=None, boundary_lens=None):
@@ -62,22 +65,54 @@ class DeferredRecoverSSM:
                    record_rows=self.record_rows, null_slot=self.null_slot, status=self.status,
                    stream=self.stream)
 
+    def _on_stream(self):
+        """torch's operations on the loop's stream."""
+        import contextlib
+        import torch
+        if self.stream is None:
+            return contextlib.nullcontext()
+        stream = self.stream
+        if isinstance(stream, int):
+            dev = self.state_pool.device
+            stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
+                      else torch.cuda.default_stream(dev))
+        return torch.cuda.stream(stream)
+
     def prefill(self, q, k, v, raw_g, raw_beta, query_start_loc, out, *, Q, sources=None,
-                workspace=None):
+                boundaries=None, boundary_lens=None, workspace=None):
         """Prompts (q, k, v, raw_g BF16 [T, H, 128], raw_beta BF16 [T, H],
         packed by query_start_loc [B + 1], windows of up to Q tokens) through
         the rule, outputs to out: each request's state is left in its own
-        slot, from which ``verify`` goes on.  A request with an empty window is
-        left alone.  ``sources`` (int32 [B]): the slots to go on from, the null
-        slot for a fresh start (None: all fresh; ``state_slots`` for a prompt's
-        later parts).  A request whose prompt this is has no pending replay
-        (``pending`` of its record row is 0)."""
+        slot, from which ``verify`` goes on, and after boundary_lens tokens
+        in ``boundaries`` (int32 [B] each).  A request with an empty window is
+        left alone, its pending replay too.  ``sources`` (int32 [B]): the slots
+        to go on from, the null slot for a fresh start (None: all fresh;
+        ``state_slots`` for a prompt's later parts, or for what follows decoded
+        tokens).  A request that goes on from its own slot has its pending
+        replay folded in first; whatever was pending in the record row of a
+        request that gets a prompt is gone afterwards."""
+        import torch
+        common = dict(null_slot=self.null_slot, status=self.status, stream=self.stream)
+        with self._on_stream():
+            prompted = query_start_loc[1:] > query_start_loc[:-1]
+            rows = torch.where(prompted, self.record_rows, self._no_row)
+            resumed = None
+            if sources is not None and not self.flushed:
+                resumed = torch.where(sources == self.state_slots, rows, self._no_row)
         if sources is None:
             sources = self._fresh
+        if resumed is not None:
+            p = self._plan
+            kda_flush_plan(self.state_slots, resumed, self.pending, p["commit_lens"],
+                           p["final_slots"], p["boundary_slots"], p["boundary_lens"], Q=self.Q,
+                           **common)
+            self._commit(p["commit_lens"], p["final_slots"])
         kda_prefill(q, k, v, raw_g, raw_beta, self.A_log, self.dt_bias, self.state_pool, sources,
                     self.state_slots, query_start_loc, out, Q=Q, lower_bound=self.lower_bound,
-                    q_scale=self.q_scale, workspace=workspace, null_slot=self.null_slot,
-                    status=self.status, stream=self.stream)
+                    q_scale=self.q_scale, boundaries=boundaries, boundary_lens=boundary_lens,
+                    workspace=workspace, **common)
+        # (no accepted token is pending in those rows: the counts stay zero)
+        kda_defer_commit(self.state_slots, self._none, rows, self.pending, **common)
 
     def verify(self, q, k, v, raw_g, raw_beta, out, query_start_loc=None):
         """Verify this step's window (q, k, v, raw_g BF16 [T, H, 128],
