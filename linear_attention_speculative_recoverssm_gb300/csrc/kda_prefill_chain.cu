@@ -104,7 +104,8 @@ struct ChainSmem {
   // squares of U over the part's block of tokens
   float4 peak[2][kParts][128];
   uint32_t kept[4][kParts];  // by row warps w & 3 and part: what a chunk left (CAREFUL)
-  float least[2][128];       // [chunk parity][row]: see is_lost
+  float2 next[128];          // by row: f of the next chunk and most_r's bits
+  float least[128];          // by row: see is_lost
   int lost;                  // the groups of rows that parts lost something of, a bit each
   // The item: its request, head, chunks and boundary as the row warps need them
   // (what they keep in registers costs them others in every chunk).
@@ -115,7 +116,7 @@ struct ChainSmem {
   uint64_t c_full[kBufC], c_free[kBufC];
   uint64_t v_full[2], v_free[2], d_full[4];
   uint64_t s_ready[2], r_ready, u_ready, w_full, u_full, ds_full[2], o_full, drained;
-  uint64_t advanced[4], token[4];  // of the four warps of the same rows
+  uint64_t factors[4], advanced[4], token[4];  // of the four warps of the same rows
   uint32_t tmem;
 };
 static_assert(kPartA % 1024 == 0 && kPartB % 1024 == 0 && kPartC % 1024 == 0, "swizzle atoms");
@@ -444,6 +445,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       mbar_init(&sm.ds_full[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.factors[i], 1);
       mbar_init(&sm.advanced[i], kParts);
       mbar_init(&sm.token[i], kParts);
     }
@@ -871,11 +873,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     float f_next = f;
     bool changes = false;   // for any row of the warp
     // What a state that is ready goes through.
-    const auto rescale = [&](int i) {
-      float least = kLeastSquare;
+    const auto rescale = [&] {
       if (changes) {
+        if (!CAREFUL && qt == kParts - 1) sm.least[row] *= f_next * inv * (f_next * inv);
         // (one after the other: the factors' quotient may be out of range)
-        least *= f_next * inv * (f_next * inv);
 #pragma unroll
         for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(fmul2(s[e], both(f_next)), both(inv));
         f = f_next;
@@ -883,7 +884,15 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         square();
         changes = false;
       }
-      if (!CAREFUL && qt == 0) sm.least[i & 1][row] = least;
+    };
+    // (else) What the rows' warps go by after chunk i.
+    const auto take = [&](int i) {
+      if (!wait(&sm.factors[group], (uint32_t)i & 1u)) return false;
+      const float2 x = sm.next[row];
+      f_next = x.x;
+      most_r = __float_as_int(x.y);
+      changes = __any_sync(0xffffffffu, f_next != f);
+      return true;
     };
     const auto pass = [&](int i, float inv_before) {
       // (what the factors are made of goes to memory at once: the registers are
@@ -968,9 +977,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.u_ready);
       }
-      // under M3: every row's squares are there once all warps have arrived
-      if (!wait(&sm.u_ready, (uint32_t)i & 1u)) return false;
-      {  // (of the last chunk only what was lost before it counts)
+      // under M3: every row's squares are there once all warps have arrived.  One
+      // of a row's four warps, of those whose half of dS comes last, works out
+      // what all of them go by (an E's four warps share a scheduler: all four
+      // would take it 350 issue slots a chunk)
+      if (CAREFUL || qt == kParts - 1) {  // (of the last chunk: what was lost before it)
+        if (!wait(&sm.u_ready, (uint32_t)i & 1u)) return false;
         const float4 m = joined(i);
         const float z = fmaf(m.x, max4(tail + kScalEnd), m.y);
         // (a chunk whose V is infinite goes token by token, from this state)
@@ -980,7 +992,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                           (z >= 0x1p8f || fv >= 0x1p9f || f == pow2(kMostExp));
         // (CAREFUL: a state that its parts would not give back; a fresh one is
         // zeros)
-        const float least = CAREFUL || i == 0 ? 0.f : sm.least[i & 1][row];
+        const float least = CAREFUL || i == 0 ? 0.f : sm.least[row];
         const bool low = CAREFUL ? m.x < 0x1p-12f && f != pow2(kMostExp) && (i > 0 || src >= 0)
                                  : m.x < least;
         const float some = fmaxf(m.x, kUnit * kUnit * m.w);
@@ -993,10 +1005,16 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           if constexpr (CAREFUL) by_token = live && (__any_sync(0xffffffffu, low) || thin);
           else if ((thin || is_lost(m.x, least)) && lane == 0) atomicOr(&sm.lost, 1 << group);
           f_next = keep ? f : row_factor(sqrt_fast(z) * inv, v);
-          changes = __any_sync(0xffffffffu, f_next != f);
+          if constexpr (CAREFUL) changes = __any_sync(0xffffffffu, f_next != f);
         }
         // (sqrt(128) B is below 2^4 B, and of the sum each at most half)
         most_r = max(((exponent(z) + 1) >> 1) - exponent(f) + 4, exponent(m.z)) + 2;
+        if constexpr (!CAREFUL) {
+          sm.next[row] = make_float2(f_next, __int_as_float(most_r));
+          sm.least[row] = kLeastSquare;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.factors[group]);
+        }
       }
       return true;
     };
@@ -1006,12 +1024,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         if (i > 0) {
           advance(i - 1);
           if (bad) break;
+          if (!take(i - 1)) break;
           if (i == now(sm.item.bnd_at)) store_boundary();
-          rescale(i);
+          rescale();
         }
         if (!pass(i, inv_before)) break;
       }
       if (!bad) advance(now(sm.item.n) - 1);
+      if (!bad) take(now(sm.item.n) - 1);
       if (!bad && now(sm.item.n) == now(sm.item.bnd_at)) store_boundary();
     } else {
       // (by token: through memory, so that what the chunks need in registers is
@@ -1019,7 +1039,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       volatile float held[kKeys + kToks / 2 + 3];
       for (int i = 0;;) {
         const float inv_before = inv;
-        if (i > 0) rescale(i);
+        if (i > 0) rescale();
         if (!pass(i, inv_before)) break;
         advance(i);
         if (bad) break;
