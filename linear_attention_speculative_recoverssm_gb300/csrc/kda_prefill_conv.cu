@@ -55,8 +55,8 @@ __device__ __forceinline__ int find_request(const int32_t *qsl, int B, int t, in
 }
 
 // z / (1 + 2^(-z log2 e)), the two functions of the special unit once each
-// (their plain forms' care for subnormals has no use here: 1 + e stays normal,
-// or overflows to a reciprocal of zero)
+// (the reciprocal is flushed from 2^126 on, as in kda_layer_prologue's: below
+// z = -87.3, where silu is under 2^-119 in size, it is -0)
 __device__ __forceinline__ float2 silu2(float2 z) {
   const float2 t = fmul2(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
   float2 e, r;
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kPcThreads, 6) kda_prefill_conv_kernel(const C
   int b = mp.qsl != nullptr ? find_request(mp.qsl, mp.B, first, lane) : first / mp.Q;
   for (; b < mp.B; ++b) {  // the requests that reach into this run
     const PromptRequest r = prompt_request(mp, b);
+    if (r.t0 >= past) break;  // (a window without tokens lies somewhere too)
     if (r.n == 0) continue;
-    if (r.t0 >= past) break;
     // A request's first three tokens belong to the run of its first: that
     // run alone reads the source's window, so it may then write the
     // destination's and the boundary's, which may be the same slot.
