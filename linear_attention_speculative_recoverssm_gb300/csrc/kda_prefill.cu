@@ -1,8 +1,8 @@
 // kda_prefill: the gated delta rule over ragged prompts, in chunks of 64
-// tokens (kda_prefill.cuh).  Four kernels: the list of chunks, what each
+// tokens (kda_prefill.cuh).  Five kernels: the list of chunks, what each
 // needs of itself (the preparation, all chunks at once), the chain of each
-// (request, head) through its chunks, and token by token what is too short
-// for a chunk, or inert.
+// (request, head) through its chunks, token by token what is too short for a
+// chunk, or inert, and once more what the chain's parts did not hold.
 #include <cuda_runtime.h>
 
 #include "../../include/kda_recoverssm.h"
@@ -13,11 +13,11 @@ namespace kda {
 namespace {
 
 // Windows of at most so many tokens go through the token-by-token kernel, where
-// a call has none longer: 40 tokens of 1 / 4 / 32 requests of 32 heads take 21 /
-// 29 / 155 us there and 24 / 31 / 192 as a chunk each, 48 tokens 25 / 34 / 185
-// and 23 / 32 / 196.  Beside longer ones fewer, since that kernel finds room
-// only as the chain ends: prompts of 63 x 24 and 2000 tokens take 307 us with
-// 24 and 317 with 16 in its place, 37 and 5 x 1600 tokens 345 with 24 and 365
+// a call has none longer: 40 tokens of 1 / 4 / 32 requests of 32 heads take 30 /
+// 36 / 159 us there and 35 / 38 / 157 as a chunk each, 48 tokens 35 / 41 / 188
+// and 36 / 39 / 157.  Beside longer ones fewer, since that kernel finds room
+// only as the chain ends: prompts of 63 x 24 and 2000 tokens take 286 us with
+// 24 and 329 with 16 in its place, 37 and 5 x 1600 tokens 341 with 24 and 359
 // with 40.
 constexpr int kShortLen = 40, kMixedLen = 24;
 constexpr int kListThreads = 1024;
@@ -31,10 +31,13 @@ constexpr int kListThreads = 1024;
 // after a short first one, and there are few.  With more items the chain fills
 // the GPU by itself, and a segment only costs its launches and the state's way
 // through memory.  One prompt of 16384 tokens, us in one segment / in eight of
-// 32 chunks / in four from 18 chunks on: 8 heads 715 / 768 / 697, 32 heads 947 /
-// 834 / 769, 48 heads 1100 / 905 / 1046, 64 heads 1268 / 1263 / 1434.
-constexpr int kSegItems = 57, kSegChunks = 32, kMaxSegments = 16;
-constexpr int kSegDoubleItems = 38, kSegFirst = 16;
+// 32 chunks / in four from 18 chunks on: 8 heads 778 / 826 / 763, 32 heads 1011 /
+// 913 / 836, 48 heads 1167 / 964 / 1076, 64 heads 1334 / 1264 / 1468.  (The
+// workspace's size depends on it, so it goes by the SMs of a GB300, not of the
+// device at hand.)
+constexpr int kSms = 152;
+constexpr int kSegItems = 3 * kSms / 8, kSegChunks = 32, kMaxSegments = 16;
+constexpr int kSegDoubleItems = kSms / 4, kSegFirst = 16;
 
 struct Workspace {
   int64_t chunks, bases, order, lost, redo, carry, images, bytes;  // offsets

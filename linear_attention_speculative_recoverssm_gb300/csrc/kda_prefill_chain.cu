@@ -41,18 +41,20 @@
 // The chain finds that when it has the next state's norms; the group's rows then
 // go through the chunks once more, from the source, in a second kernel behind
 // it, which looks before it goes on and does such a chunk token by token
-// (CAREFUL).  Both in one kernel leave a chunk's path too few registers: 16384
-// tokens took 895 us in place of 843.
+// (CAREFUL): 150 us for such a chunk, 5 for the others.  Both in one kernel leave
+// every chunk's path too few registers: 16384 tokens took 895 us in place of 843.
 // The state itself stays in FP32, in registers: an accumulator that is added
 // to over and over loses up to a unit of its last place each time, so dS is
 // summed apart, smallest parts first.
 //
-// What bounds it: a chunk's products and passes depend on one another, some 5.4 K
-// cycles (2.8 us) of which the tensor cores run 2.3 K, with 8 CTAs on the GPU
-// (697 us for 256 chunks) nearly as with 32; 265 chunks of 32 heads in 16 prompts
-// take 214 us, most of them the longest prompt's 78 chunks.  TMEM and shared memory hold one item an SM.
-// Eight row warps in place of 16 took longer, and so did the outputs' stores
-// between R and U (2 to 6 %): what the other warps split then waits.
+// What bounds it: a chunk's products and passes depend on one another, some 6 K
+// cycles (3.1 us) of which the tensor cores run 2.3 K, with 8 CTAs on the GPU
+// (763 us for 256 chunks) nearly as with 32; 265 chunks of 32 heads in 16 prompts
+// take 229 us, most of them the longest prompt's 78 chunks.  TMEM and shared
+// memory hold one item an SM.  (One factor for R, S and U, from bounds that know
+// no decay, was 0.3 us a chunk less, and lost what the above keeps.)  Eight row
+// warps in place of 16 took longer, and so did the outputs' stores between R and
+// U (2 to 6 %): what the other warps split then waits.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -330,8 +332,9 @@ struct MnMajor {
 
 // A chunk's tokens one after the other in FP32, its outputs stored and the
 // state `s` (as it is, not scaled) advanced: by the four warps of the same
-// rows, for a chunk that the parts cannot hold.  Some 0.6 us a token.  What a
-// row's parts add up goes through their places in sm.peak of the chunk before,
+// rows, for a chunk that the parts cannot hold.  2.4 us a token (its operands by
+// 128 shuffles a warp), 150 a chunk, with 16 warps at it.  What a row's parts
+// add up goes through their places in sm.peak of the chunk before,
 // which have been read (each token's by turns in two of the four floats).
 // False: a wait ran out.
 __device__ __noinline__ bool rows_by_token(const RecurrentParams &r, ChainSmem &sm, int chunk,
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     mbar_init_fence();
     sm.lost = 0;
   };
-  if (threadIdx.x == 0) init_barriers();
+  if (!CAREFUL && threadIdx.x == 0) init_barriers();
   if (!CAREFUL && warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
   grid_dependency_wait();
   // (only now: the next kernel may count on what this one has waited for)
@@ -467,6 +470,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const int n_listed = CAREFUL ? __ldcg(p.n_redo) : 0;
   if constexpr (CAREFUL) {
     if (listed >= n_listed) return;
+    if (threadIdx.x == 0) init_barriers();
     if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
   }
   while (!CAREFUL || listed < n_listed) {

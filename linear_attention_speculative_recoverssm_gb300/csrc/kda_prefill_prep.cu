@@ -22,8 +22,8 @@
 // are the same parts times an exact 2^n.
 //
 // What bounds it: 265 chunks of 32 heads read 0.42 GB and write 0.89 GB, 192 us
-// at a copy's rate, and take 325.  16 warps an SM is what registers (128, no
-// fewer without spills) and shared memory leave room for; they issue every
+// at a copy's rate, and take 327.  16 warps an SM is what registers (128, with 8
+// bytes spilled) and shared memory leave room for; they issue every
 // other cycle, the operands' pass (44 % of an item's 22 K cycles) on exponents,
 // FP16 splits and their stores.  Laid out without care for banks, and with A
 // and T stored from registers, it took 342; an item to a CTA, without the next

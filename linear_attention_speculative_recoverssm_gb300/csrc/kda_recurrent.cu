@@ -22,9 +22,12 @@
 //    made once for the CTA, a token a warp, eight tokens at a time, from rows
 //    asked for a step ahead (8 tokens of 32 heads, one request: 6.7 us, asked
 //    for when needed 8.5; 100 requests 109 and 114).  100 requests of 32 heads,
-//    3 tokens, BF16: 60 us (3.7 TB/s: the arithmetic of a warp's tokens is a
-//    chain of sums and shuffles, and 16 warps an SM is what the rows' registers
-//    leave room for); the other kernel 82.
+//    3 tokens, BF16: 60 us, 3.7 TB/s; the other kernel 82.  What bounds it is
+//    its form, a token after the other: each is a chain of sums, shuffles and an
+//    update behind the one before, and the 16 warps an SM that the rows'
+//    registers leave room for do not cover it.  (The verify kernels take a whole
+//    window's products from the state as loaded, and move pages at 80 % of a
+//    copy's rate with 8 tokens each.)
 #include <cuda_runtime.h>
 
 #include "../../include/kda_recoverssm.h"
