@@ -583,18 +583,15 @@ int kda_prefill_conv(const kda_bf16 *x, const kda_bf16 *conv_weight, const kda_b
  * with d_t, kn_t and qn_t as in kda_verify; the state after the last token
  * goes to the destination (rounded once to the pool's type).
  *   What is held in fewer bits.  States, sums, norms and gates are FP32.  In
- *   windows that go by chunks the products that reach the state take their
- *   operands with 22 bits (a state is off by some 1e-7 of its largest entry, 1e-5
- *   at worst), and those that reach the outputs alone (queries, and
- *   state and updates as the queries meet them) with 11: beside its rounding to
- *   BF16 an output may be off by 2^-10 of (the largest |row of S| + 2 sum |u|)
- *   |q_scale| over the last 64 tokens, typically by a tenth of a BF16 step.
- *   Windows of up to 40 tokens (24 beside longer ones) go token by token, all in
- *   FP32, as in kda_recurrent: which way a window of 25 to 40 tokens goes
- *   depends on the longest that Q and n_tokens allow, and so do its outputs'
- *   last bits.  Chunks whose sizes or values 22 bits cannot hold go token by
- *   token too, so the rule holds for any finite inputs, and a NaN or an
- *   infinity reaches what comes after its token only.
+ *   windows that go by chunks the products take their operands with 22 bits: a
+ *   state is off by some 1e-7 of its largest entry (1e-5 at worst), an output
+ *   before its rounding to BF16 by some 1e-6 of (the largest |row of S| + 2 sum
+ *   |u|) |q_scale| over the last 64 tokens.  Windows of up to 40 tokens (24
+ *   beside longer ones) go token by token, in FP32, as in kda_recurrent; so do
+ *   chunks whose sizes or values 22 bits cannot hold: the rule holds for any
+ *   finite inputs, and a NaN or an infinity reaches what comes after its token
+ *   only.  Which way a window of 25 to 40 tokens goes depends on the longest
+ *   that Q and n_tokens allow, and so may its last bits.
  *   q, k, v, raw_g, out [n_tokens, H, 128], raw_beta [n_tokens, H] BF16;
  *   A_log [H], dt_bias [H, 128] FP32; state_pool [n_slots, H, 128, 128] of
  *   state_dtype, slot stride `slot_stride` elements (>= H*128*128).

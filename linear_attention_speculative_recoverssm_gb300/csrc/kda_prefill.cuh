@@ -26,6 +26,8 @@
 // the held value below.  hi.hi + hi.lo + lo.hi leaves 2^-22 of a product.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "kda_recurrent.cuh"
 
 namespace kda {
@@ -41,13 +43,15 @@ constexpr float kImgTScale = 16384.f;         // over the chunk's p
 constexpr uint32_t kImgBlock = kChunk * 128;             // 8 KB
 constexpr uint32_t kImgKdHi = 0;                         // [t][channel]
 constexpr uint32_t kImgKdLo = kImgKdHi + 2 * kImgBlock;
-constexpr uint32_t kImgQd = kImgKdLo + 2 * kImgBlock;    // [t][channel], hi only
-constexpr uint32_t kImgTHi = kImgQd + 2 * kImgBlock;     // [t][s]
+constexpr uint32_t kImgQdHi = kImgKdLo + 2 * kImgBlock;  // [t][channel]
+constexpr uint32_t kImgQdLo = kImgQdHi + 2 * kImgBlock;
+constexpr uint32_t kImgTHi = kImgQdLo + 2 * kImgBlock;   // [t][s]
 constexpr uint32_t kImgTLo = kImgTHi + kImgBlock;
 constexpr uint32_t kImgKeHi = kImgTLo + kImgBlock;       // [s][channel]
 constexpr uint32_t kImgKeLo = kImgKeHi + 2 * kImgBlock;
-constexpr uint32_t kImgA = kImgKeLo + 2 * kImgBlock;     // [t][s], hi only
-constexpr uint32_t kImgDecay = kImgA + kImgBlock;        // e^{G_end}, 128 FP32
+constexpr uint32_t kImgAHi = kImgKeLo + 2 * kImgBlock;   // [t][s]
+constexpr uint32_t kImgALo = kImgAHi + kImgBlock;
+constexpr uint32_t kImgDecay = kImgALo + kImgBlock;      // e^{G_end}, 128 FP32
 // Behind the decays, FP32, what bounds the states to come (kScal..)
 constexpr uint32_t kImgTail = (128 + 32) * 4;            // decays and scalars
 constexpr uint32_t kImgBytes = kImgDecay + kImgTail;
@@ -57,6 +61,22 @@ constexpr uint32_t kImgBytes = kImgDecay + kImgTail;
 // p + 64 p^2.
 constexpr int kScalEnd = 128, kScalLeft = 132, kScalBeta = 144, kScalValue = 145;
 constexpr float kEndFactor = 2.03f / 4096.f, kLeftFactor = 130.f;
+
+// x - h, by a multiply-add of FP16 factors to an FP32 sum: exact for h = x
+// rounded to FP16, and no conversion of h, which shares its unit with the
+// roundings (two conversions and a packed multiply-add: 3.1 us a chunk and not
+// 2.8).
+__device__ __forceinline__ float2 less_half(float2 x, __half2 h) {
+  const uint16_t minus_one = 0xBC00;
+  float2 d;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;"
+      : "=f"(d.x)
+      : "h"(__half_as_ushort(__low2half(h))), "h"(minus_one), "f"(x.x));
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;"
+      : "=f"(d.y)
+      : "h"(__half_as_ushort(__high2half(h))), "h"(minus_one), "f"(x.y));
+  return d;
+}
 
 struct PrefillChunk {
   int t0, count;  // tokens t0 .. t0 + count - 1 of the packed activations

@@ -12,7 +12,11 @@
 // with M on the tensor cores (M = 128 rows, the first operand in TMEM, the
 // second the image in shared memory) and E on warps 0-15: warp w holds lanes
 // (rows) 32 (w & 3) .. and quarter w >> 2 of the columns.  O leaves while the
-// next chunk's M1 runs.  Warp 16 issues the MMAs, warp 17 the copies.
+// next chunk's M1 runs.  Warp 16 issues the MMAs, warp 17 the copies.  All
+// products take hi.hi + hi.lo + lo.hi.  (With the high parts alone for O, 16
+// prompts took 578 us in place of 639 and one of 16384 tokens 832 in place of
+// 890, and 15 % of the outputs rounded to another BF16 value than the exact ones;
+// so do 0.1 % now.)
 //
 // FP16 parts of a row are taken times powers of two: S times 2^6 f, U times f,
 // R times a factor fr of its own, so that with the images' scales dS comes out
@@ -47,12 +51,12 @@
 // to over and over loses up to a unit of its last place each time, so dS is
 // summed apart, smallest parts first.
 //
-// What bounds it: a chunk's products and passes depend on one another, some 6 K
-// cycles (3.1 us) of which the tensor cores run 2.3 K, with 8 CTAs on the GPU
-// (763 us for 256 chunks) nearly as with 32; 265 chunks of 32 heads in 16 prompts
-// take 229 us, most of them the longest prompt's 78 chunks.  TMEM and shared
-// memory hold one item an SM.  (One factor for R, S and U, from bounds that know
-// no decay, was 0.3 us a chunk less, and lost what the above keeps.)  Eight row
+// What bounds it: a chunk's products and passes depend on one another, some 6.5 K
+// cycles (3.3 us) of which the tensor cores run 2.8 K, with 8 CTAs on the GPU
+// nearly as with 32; 265 chunks of 32 heads in 16 prompts take 248 us, most of
+// them the longest prompt's 78 chunks.  TMEM and shared memory hold one item an
+// SM.  (One factor for R, S and U, from bounds that know no decay, was 0.3 us a
+// chunk less, and lost what the above keeps.)  Eight row
 // warps in place of 16 took longer, and so did the outputs' stores between R and
 // U (2 to 6 %): what the other warps split then waits.
 #include <cuda_fp16.h>
@@ -74,12 +78,13 @@ constexpr int kRowWarps = 16;
 constexpr int kChainThreads = 32 * (kRowWarps + 2);  // and the MMA and copy warps
 constexpr int kParts = kRowWarps / 4;  // threads of a row
 constexpr int kKeys = kDim / kParts, kToks = kChunk / kParts;  // their columns
-constexpr uint32_t kPartA = kImgTHi;                  // Kd, Qd: 48 KB
+constexpr uint32_t kPartA = kImgQdHi;                 // Kd: 32 KB
+constexpr uint32_t kPartQ = kImgTHi - kImgQdHi;       // Qd: 32 KB
 constexpr uint32_t kPartB = kImgKeHi - kImgTHi;       // T: 16 KB
-constexpr uint32_t kPartC = kImgDecay - kImgKeHi;     // Ke, A: 40 KB
+constexpr uint32_t kPartC = kImgDecay - kImgKeHi;     // Ke, A: 48 KB
 // Buffers of each.  C is released last, a chunk's end, and needed soonest: a
-// second one takes 2 to 3 % off the chain (of A or B: nothing).
-constexpr int kBufA = 1, kBufB = 1, kBufC = 2;
+// second one takes 2 to 3 % off the chain (of the others or of v: nothing).
+constexpr int kBufA = 1, kBufQ = 1, kBufB = 1, kBufC = 2;
 constexpr uint32_t kVBytes = kChunk * kDim * 2;       // 16 KB
 
 // TMEM columns
@@ -98,8 +103,9 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t n, bool mn) {
 }
 
 struct ChainSmem {
-  uint8_t a[kBufA][kPartA], b[kBufB][kPartB], c[kBufC][kPartC];  // multiples of 1024 bytes
-  uint8_t v[2][kVBytes];
+  // (multiples of 1024 bytes)
+  uint8_t a[kBufA][kPartA], q[kBufQ][kPartQ], b[kBufB][kPartB], c[kBufC][kPartC];
+  uint8_t v[kVBytes];
   float decay[4][kImgTail / 4];  // decays and scalars of chunk i at i & 3
   PrefillChunk chunk[4];  // chunk i at i & 3, there when its v is
   // [chunk parity][part][row]: squares of S and of U', in parts' units; next |v|;
@@ -114,9 +120,9 @@ struct ChainSmem {
   struct {
     int b, h, n, bnd_at, ends;
   } item;
-  uint64_t a_full[kBufA], a_free[kBufA], b_full[kBufB], b_free[kBufB];
-  uint64_t c_full[kBufC], c_free[kBufC];
-  uint64_t v_full[2], v_free[2], d_full[4];
+  uint64_t a_full[kBufA], a_free[kBufA], q_full[kBufQ], q_free[kBufQ];
+  uint64_t b_full[kBufB], b_free[kBufB], c_full[kBufC], c_free[kBufC];
+  uint64_t v_full, v_free, d_full[4];
   uint64_t s_ready[2], r_ready, u_ready, w_full, u_full, ds_full[2], o_full, drained;
   uint64_t factors[4], advanced[4], token[4];  // of the four warps of the same rows
   uint32_t tmem;
@@ -205,22 +211,6 @@ __device__ __forceinline__ float sqrt_fast(float x) {
 
 __device__ __forceinline__ float pow2_inverse(float s) {
   return __uint_as_float((254u << 23) - __float_as_uint(s));
-}
-
-// x - h, by a multiply-add of FP16 factors to an FP32 sum: exact for h = x
-// rounded to FP16, and no conversion of h, which shares its unit with the
-// roundings (two conversions and a packed multiply-add: 3.1 us a chunk and not
-// 2.8).
-__device__ __forceinline__ float2 less_half(float2 x, __half2 h) {
-  const uint16_t minus_one = 0xBC00;
-  float2 d;
-  asm("fma.rn.f32.f16 %0, %1, %2, %3;"
-      : "=f"(d.x)
-      : "h"(__half_as_ushort(__low2half(h))), "h"(minus_one), "f"(x.x));
-  asm("fma.rn.f32.f16 %0, %1, %2, %3;"
-      : "=f"(d.y)
-      : "h"(__half_as_ushort(__high2half(h))), "h"(minus_one), "f"(x.y));
-  return d;
 }
 
 // Two values as FP16 and what that leaves.
@@ -316,6 +306,21 @@ struct KMajor {
     return b;
   }
 };
+// The MMAs of a product with T or A, which have nothing above their diagonals:
+// K step ks (columns 16 ks .. 16 ks + 15) only from row 16 ks on, N = 64 - 16 ks
+// (all of N: 1.5 % longer, 16384 tokens).
+__device__ __forceinline__ void mma_lower(uint32_t d, uint32_t a_hi, uint32_t a_lo, KMajor hi,
+                                          KMajor lo, bool accumulate, uint32_t lead) {
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const KMajor &b = j == 1 ? lo : hi;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+      umma_ts(d + 16 * ks, (j == 0 ? a_lo : a_hi) + 8 * ks,
+              b(ks) + (uint64_t)((uint32_t)ks * 2048u >> 4), idesc_f16(64 - 16 * ks, false),
+              accumulate || j > 0 || ks > 0, lead);
+  }
+}
 // MN-major parts: a K step is 16 rows of 128 bytes.
 struct MnMajor {
   uint64_t desc;
@@ -437,11 +442,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
     };
     init(sm.a_full, sm.a_free, kBufA);
+    init(sm.q_full, sm.q_free, kBufQ);
     init(sm.b_full, sm.b_free, kBufB);
     init(sm.c_full, sm.c_free, kBufC);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_free[i], kRowWarps);
       mbar_init(&sm.d_full[i], 1);
       mbar_init(&sm.d_full[i + 2], 1);
       mbar_init(&sm.s_ready[i], kRowWarps / 2);
@@ -452,6 +456,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       mbar_init(&sm.advanced[i], kParts);
       mbar_init(&sm.token[i], kParts);
     }
+    mbar_init(&sm.v_full, 1);
+    mbar_init(&sm.v_free, kRowWarps);
     mbar_init(&sm.r_ready, kRowWarps);
     mbar_init(&sm.u_ready, kRowWarps);
     mbar_init(&sm.w_full, 1);
@@ -511,11 +517,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   } else if (warp == kRowWarps + 1) {
     // -- copies ---------------------------------------------------------------
     bool ok = true;
-    int n_v = 0, n_a = 0, n_b = 0, n_c = 0;  // copies issued of each kind
+    int n_v = 0, n_a = 0, n_q = 0, n_b = 0, n_c = 0;  // copies issued of each kind
     PrefillChunk coming = p.chunks[place(0)];  // the next chunk whose v is copied
     const auto load_v = [&](int i) {
-      uint64_t *bar = &sm.v_full[i & 1];
-      if (i >= 2) ok = ok && mbar_wait_bounded(&sm.v_free[i & 1], (uint32_t)((i >> 1) - 1) & 1u);
+      uint64_t *bar = &sm.v_full;
+      if (i >= 1) ok = ok && mbar_wait_bounded(&sm.v_free, (uint32_t)(i - 1) & 1u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       n_v = i + 1;
@@ -526,12 +532,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const PrefillChunk ck = coming;
       coming = p.chunks[place(min(i + 1, n - 1))];
       // (the places of chunk i - 4: its outputs and state were done before any
-      // row warp released v of chunk i - 2)
+      // row warp released v of chunk i - 1)
       sm.chunk[i & 3] = ck;
       mbar_arrive_expect_tx(&sm.d_full[i & 3], kImgTail);
       bulk_g2s(sm.decay[i & 3], image(i) + kImgDecay, kImgTail, &sm.d_full[i & 3]);
       mbar_arrive_expect_tx(bar, kVBytes);
-      tma_load_3d(sm.v[i & 1], &v_map, 0, h, ck.t0, bar);
+      tma_load_3d(sm.v, &v_map, 0, h, ck.t0, bar);
     };
     const auto load_part = [&](int i, int buffers, uint64_t *full, uint64_t *free, uint8_t *dst,
                                uint32_t at, uint32_t bytes, int &issued) {
@@ -548,8 +554,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     for (int i = 0; i < n && ok; ++i) {
       load_part(i, kBufA, sm.a_full, sm.a_free, sm.a[0], 0, kPartA, n_a);
       if (ok && i + 1 < n) load_v(i + 1);
-      if (ok) load_part(i, kBufB, sm.b_full, sm.b_free, sm.b[0], kPartA, kPartB, n_b);
-      if (ok) load_part(i, kBufC, sm.c_full, sm.c_free, sm.c[0], kPartA + kPartB, kPartC, n_c);
+      if (ok) load_part(i, kBufB, sm.b_full, sm.b_free, sm.b[0], kImgTHi, kPartB, n_b);
+      if (ok) load_part(i, kBufQ, sm.q_full, sm.q_free, sm.q[0], kImgQdHi, kPartQ, n_q);
+      if (ok) load_part(i, kBufC, sm.c_full, sm.c_free, sm.c[0], kImgKeHi, kPartC, n_c);
     }
     if (!ok) {
       // every copy issued lands before the CTA can exit: the last phase in
@@ -562,19 +569,19 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         for (int j = 0; j < buffers; ++j) settle(bar + j, (uses - j + buffers - 1) / buffers);
       };
       settle_all(sm.a_full, kBufA, n_a);
+      settle_all(sm.q_full, kBufQ, n_q);
       settle_all(sm.b_full, kBufB, n_b);
       settle_all(sm.c_full, kBufC, n_c);
       settle_all(sm.d_full, 4, n_v);
-      settle(&sm.v_full[0], (n_v + 1) / 2);
-      settle(&sm.v_full[1], n_v / 2);
+      settle(&sm.v_full, n_v);
     }
   } else if (warp == kRowWarps) {
     // -- tensor cores: the whole warp, converged ------------------------------
     const uint32_t lead = elect_one();
     const auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
     const uint32_t tm = uniform(tmem);
-    const uint32_t base_a = uniform(smem_u32(sm.a)), base_b = uniform(smem_u32(sm.b));
-    const uint32_t base_c = uniform(smem_u32(sm.c));
+    const uint32_t base_a = uniform(smem_u32(sm.a)), base_q = uniform(smem_u32(sm.q));
+    const uint32_t base_b = uniform(smem_u32(sm.b)), base_c = uniform(smem_u32(sm.c));
     constexpr uint32_t k64 = idesc_f16(64, false), k64mn = idesc_f16(64, true);
     const uint32_t w = tm + kColW, s_hi = tm + kColSHi, s_lo = tm + kColSLo;
     const uint32_t r_hi = tm + kColRHi, r_lo = tm + kColRLo;
@@ -586,11 +593,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     for (int i = 0; i < n; ++i) {
       const uint32_t ph = (uint32_t)i & 1u;
       const uint32_t o = tm + kColO + 64u * ph;
-      const uint32_t ia = (uint32_t)i % kBufA, ib = (uint32_t)i % kBufB, ic = (uint32_t)i % kBufC;
-      const uint32_t sa = base_a + ia * kPartA, sb = base_b + ib * kPartB;
-      const uint32_t sc = base_c + ic * kPartC;
-      const KMajor kd_hi(sa + kImgKdHi), kd_lo(sa + kImgKdLo), qd(sa + kImgQd);
-      const KMajor am(sc + 4 * kImgBlock), t_hi(sb), t_lo(sb + kImgBlock);
+      const uint32_t ia = (uint32_t)i % kBufA, iq = (uint32_t)i % kBufQ;
+      const uint32_t ib = (uint32_t)i % kBufB, ic = (uint32_t)i % kBufC;
+      const uint32_t sa = base_a + ia * kPartA, sq = base_q + iq * kPartQ;
+      const uint32_t sb = base_b + ib * kPartB, sc = base_c + ic * kPartC;
+      const KMajor kd_hi(sa + kImgKdHi), kd_lo(sa + kImgKdLo);
+      const KMajor qd_hi(sq), qd_lo(sq + kImgQdLo - kImgQdHi), t_hi(sb), t_lo(sb + kImgBlock);
+      const KMajor a_hi(sc + 4 * kImgBlock), a_lo(sc + 5 * kImgBlock);
       const MnMajor ke_hi(sc), ke_lo(sc + 2 * kImgBlock);
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.a_full[ia], (uint32_t)(i / kBufA) & 1u));
       for (int half = 0; half < 2 && ok; ++half) {
@@ -603,15 +612,22 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       if (!ok) break;
       commit(&sm.w_full);
-      mma_part<8>(o, s_hi, qd, k64, false, lead);
       commit(&sm.a_free[ia]);
+      // (of O a third under the rows' way from W to R, the rest under theirs from
+      // U to its parts)
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.q_full[iq], (uint32_t)(i / kBufQ) & 1u));
+      if (!ok) break;
+      mma_part<8>(o, s_hi, qd_hi, k64, false, lead);
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.b_full[ib], (uint32_t)(i / kBufB) & 1u) &&
                                        mbar_wait_bounded(&sm.r_ready, ph));
       if (!ok) break;
       tc_fence_after();
-      mma_split<4>(w, r_hi, r_lo, t_hi, t_lo, k64, false, lead);
+      mma_lower(w, r_hi, r_lo, t_hi, t_lo, false, lead);
       commit(&sm.u_full);
       commit(&sm.b_free[ib]);
+      mma_part<8>(o, s_lo, qd_hi, k64, true, lead);
+      mma_part<8>(o, s_hi, qd_lo, k64, true, lead);
+      commit(&sm.q_free[iq]);
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.c_full[ic], (uint32_t)(i / kBufC) & 1u) &&
                                        mbar_wait_bounded(&sm.u_ready, ph));
       if (!ok) break;
@@ -621,7 +637,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                      k64mn, false, lead);
         commit(&sm.ds_full[half]);
       }
-      mma_part<4>(o, r_hi, am, k64, true, lead);
+      mma_lower(o, r_hi, r_lo, a_hi, a_lo, true, lead);
       commit(&sm.o_full);
       commit(&sm.c_free[ic]);
     }
@@ -676,9 +692,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     // v of chunk i: this row's tokens from kToks qt on, and their peak
     uint32_t v2[kToks / 2];
     const auto load_v = [&](int i) {
-      if (!wait(&sm.v_full[i & 1], (uint32_t)(i >> 1) & 1u)) return 0.f;
+      if (!wait(&sm.v_full, (uint32_t)i & 1u)) return 0.f;
       const int count = sm.chunk[i & 3].count;
-      const uint16_t *v = reinterpret_cast<const uint16_t *>(sm.v[i & 1]) + kToks * qt * kDim + row;
+      const uint16_t *v = reinterpret_cast<const uint16_t *>(sm.v) + kToks * qt * kDim + row;
       const int left = count - kToks * qt;
       if (left >= kToks) {
 #pragma unroll
@@ -696,7 +712,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       for (int j = 0; j < kToks / 2; ++j)
         peak = __hmax2(peak, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v2[j])));
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_free[i & 1]);
+      if (lane == 0) mbar_arrive(&sm.v_free);
       return fmaxf(__low2float(peak), __high2float(peak));
     };
     // the sum of what this row's parts left at [i & 1], of |v| the largest, of

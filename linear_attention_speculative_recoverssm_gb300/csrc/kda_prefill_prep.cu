@@ -12,8 +12,7 @@
 // both factors, from t back to it and from it back to s, are at most 1:
 // blocks 0-1 | 2-3 with the border at token 32, blocks 0 | 1 and 2 | 3 with
 // theirs at 16 and 48, in FP16 parts through shared memory.  The key products
-// take hi.hi + hi.lo + lo.hi (their errors reach the state); the query
-// products round q alone to 11 bits, whose result rounds to BF16's 8.
+// and the query products take hi.hi + hi.lo + lo.hi.
 //
 // The references are powers of two: with B_i the sum of the log2 decays
 // before block i rounded to an integer, a row operand is R_t = kn_t
@@ -21,13 +20,14 @@
 // FP16 parts once; from another block's border, or the chunk's start, they
 // are the same parts times an exact 2^n.
 //
-// What bounds it: 265 chunks of 32 heads read 0.42 GB and write 0.89 GB, 192 us
-// at a copy's rate, and take 327.  16 warps an SM is what registers (128, with 8
-// bytes spilled) and shared memory leave room for; they issue every
-// other cycle, the operands' pass (44 % of an item's 22 K cycles) on exponents,
-// FP16 splits and their stores.  Laid out without care for banks, and with A
-// and T stored from registers, it took 342; an item to a CTA, without the next
-// one's inputs on their way, 415.
+// What bounds it: 265 chunks of 32 heads read 0.42 GB and write 1.1 GB, 225 us at
+// a copy's rate, and take 369.  16 warps an SM is what registers (128, with 20
+// bytes spilled) and shared memory leave room for; they issue every other cycle,
+// the operands' pass on exponents, FP16 splits and their stores.  (Splits by a
+// conversion of the high part in place of a multiply-add of FP16 to FP32: 382.)
+// With the high parts of the query operands alone it took 327; then, laid out
+// without care for banks, and with A and T stored from registers, 342, and with
+// an item to a CTA, without the next one's inputs on their way, 415.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -44,12 +44,17 @@ namespace {
 constexpr int kPrepThreads = 256;
 constexpr uint32_t kXPitch = 256;  // bytes of a 128-channel FP16 row
 constexpr uint32_t kXBytes = kChunk * kXPitch;
-constexpr uint32_t kYBytes = 32 * kXPitch;
+constexpr uint32_t kX3Bytes = 48 * kXPitch;  // three blocks' rows
 // Pitches (floats): rows four or eight banks apart, as their readers want.
 constexpr int kLPitch = 36, kL16Pitch = 20, kXPitchF = 68, kYPitch = 40, kLtPitch = 20;
-constexpr int kDPitch = 20;
 constexpr int kLtSize = 16 * kLtPitch + 16;  // (two blocks apart by half the banks)
 constexpr uint32_t kRowsBytes = kChunk * kDim * 2;  // a chunk's rows of an input
+
+// Where columns c .. c + 3 of row r of a 16 x 16 block lie: pieces of 16 bytes,
+// of eight rows one each meet every bank.
+__device__ __forceinline__ int part_at(int r, int c) {
+  return 16 * r + (((c >> 2) ^ ((r >> 1) & 3)) << 2);
+}
 
 // Shared memory, by phases: the FP16 operands of the products between blocks;
 // then, in their place, L between blocks, X = (I + L)^-1 and a scratch matrix,
@@ -60,8 +65,10 @@ struct PrepSmem {
       // (before they hold operands, x16_hi and x16_lo hold the log2 decay
       // sums of each half block: of a 16-byte piece's eight channels the first
       // and last four)
-      uint8_t x16_hi[kXBytes], x16_lo[kXBytes], x32_hi[kXBytes], x32_lo[kXBytes];
-      uint8_t y16[kYBytes], y32[kYBytes];
+      uint8_t x16_hi[kXBytes], x16_lo[kXBytes];
+      // of 32, blocks 0 .. 2 (block 3's are its rows of 48 times powers of two)
+      uint8_t x32_hi[kX3Bytes], x32_lo[kX3Bytes];
+      uint8_t y_hi[kX3Bytes], y_lo[kX3Bytes];  // query rows of blocks 1 .. 3
     } x;
     struct {
       float L[32 * kLPitch];          // rows 32 .. 63 by columns 0 .. 31
@@ -82,15 +89,15 @@ struct PrepSmem {
       uint16_t pow[4][128];    // FP16 2^n: of Kd and Qd
       uint16_t pow32[2][128];  // of the operands at 32, blocks 0 and 3
       float tot[2][4][128];    // log2 decays of a block's two halves
+      float norm[2][kChunk][2];  // sums of squares per channel half
     };
-    __align__(16) uint8_t a[kImgBlock];  // then the image's A
+    __align__(16) uint8_t a[2 * kImgBlock];  // then the image's A
   };
   union {
     // a block's products kn kn^T and qn kn^T, over either half of the channels
-    __align__(16) float part[4][2][2][16 * kDPitch];
+    __align__(16) float part[4][2][2][16 * 16];
     uint8_t t[2 * kImgBlock];  // then the image's T
   };
-  float norm[2][kChunk][2];        // sums of squares per channel half
   float beta[kChunk];
   uint64_t landed;  // the item's q, k and raw_g are there
 };
@@ -131,13 +138,9 @@ __device__ __forceinline__ float beta_power(const float *beta, int lane) {
   return __uint_as_float((uint32_t)min(max(e, 27), 128) << 23);
 }
 
-// The leading 11 bits of x (truncated), and x rounded to them as the tensor
-// cores, which drop the rest, then see it.
+// The leading 11 bits of x (truncated).
 __device__ __forceinline__ float tf32_hi(float x) {
   return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
-}
-__device__ __forceinline__ float tf32_round(float x) {
-  return __uint_as_float(__float_as_uint(x) + 0x1000u);
 }
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], float b0, float b1) {
@@ -170,18 +173,13 @@ __device__ __forceinline__ uint32_t h2_bits(__half2 h) {
 }
 
 // Eight values (four pairs) as FP16, and what that leaves.
-__device__ __forceinline__ uint4 half8(const float2 (&x)[4]) {
-  return make_uint4(h2_bits(__float22half2_rn(x[0])), h2_bits(__float22half2_rn(x[1])),
-                    h2_bits(__float22half2_rn(x[2])), h2_bits(__float22half2_rn(x[3])));
-}
-
 __device__ __forceinline__ void split8(const float2 (&x)[4], uint4 &hi, uint4 &lo) {
   uint32_t w[4], v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2 h = __float22half2_rn(x[i]);
     w[i] = h2_bits(h);
-    v[i] = h2_bits(__float22half2_rn(ffma2(__half22float2(h), make_float2(-1.f, -1.f), x[i])));
+    v[i] = h2_bits(__float22half2_rn(less_half(x[i], h)));
   }
   hi = make_uint4(w[0], w[1], w[2], w[3]);
   lo = make_uint4(v[0], v[1], v[2], v[3]);
@@ -199,6 +197,17 @@ __device__ __forceinline__ uint4 scale8(uint4 x, uint4 f) {
   r.z = mul(x.z, f.z);
   r.w = mul(x.w, f.w);
   return r;
+}
+
+// An operand's 16 x 16 tile times powers of two by channel: the first and the
+// last eight channels' at this lane's place.
+__device__ __forceinline__ void scale_rows(uint32_t (&x)[4], uint32_t p0, uint32_t p1) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t p = i < 2 ? p0 : p1;
+    x[i] = h2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&x[i]),
+                           *reinterpret_cast<const __half2 *>(&p)));
+  }
 }
 
 __device__ __forceinline__ float2 bf16x2_f32(uint32_t w) {
@@ -490,11 +499,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
       }
     }
   }
+  // (queries at Qd's scale throughout)
+  constexpr float kQDown = kImgQdScale / kImgScale;
   float rk[2], rq[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     rk[r] = rsqrtf(sm.norm[0][row[r]][0] + sm.norm[1][row[r]][0] + kNormEps);
-    rq[r] = rsqrtf(sm.norm[0][row[r]][1] + sm.norm[1][row[r]][1] + kNormEps);
+    rq[r] = rsqrtf(sm.norm[0][row[r]][1] + sm.norm[1][row[r]][1] + kNormEps) * kQDown;
     if (row[r] > last) rk[r] = rq[r] = 0.f;
   }
   if (tid == 0) bulk_stores_read<0>();  // and T's
@@ -509,8 +520,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   // Token g's places; token g + 8 lies 8 rows further, and slice 1 four pieces
   // on, which flips bit 6 of the permuted place.
   const uint32_t img0 = img_at(row[0], ch0), x0 = x_at(row[0], ch0 >> 3);
-  const uint32_t y16_0 = x_at((blk >> 1) * 16 + g, ch0 >> 3);
-  const uint32_t y32_0 = x_at((blk & 1) * 16 + g, ch0 >> 3);
+  const uint32_t y0 = x_at((max(blk, 1) - 1) * 16 + g, ch0 >> 3);
 #pragma unroll
   for (int sl = 0; sl < 2; ++sl) {
     const int c = ch0 + 32 * sl;
@@ -547,13 +557,14 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
     for (int e = 0; e < 4; ++e) {
       // columns tig and tig + 4 of the operand are channels 2 e and 2 e + 1
       const float a[4] = {kf[0][e].x, kf[1][e].x, kf[0][e].y, kf[1][e].y};
-      const float aq[4] = {tf32_round(qf[0][e].x), tf32_round(qf[1][e].x),
-                           tf32_round(qf[0][e].y), tf32_round(qf[1][e].y)};
-      float ah[4], al[4];
+      const float aq[4] = {qf[0][e].x, qf[1][e].x, qf[0][e].y, qf[1][e].y};
+      float ah[4], al[4], qh[4], ql[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         ah[i] = tf32_hi(a[i]);
         al[i] = a[i] - ah[i];
+        qh[i] = tf32_hi(aq[i]);
+        ql[i] = aq[i] - qh[i];
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -562,8 +573,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
         mma_tf32(dk[n], al, h0, h1);
         mma_tf32(dk[n], ah, l0, l1);
         mma_tf32(dk[n], ah, h0, h1);
-        mma_tf32(dq[n], aq, l0, l1);
-        mma_tf32(dq[n], aq, h0, h1);
+        mma_tf32(dq[n], ql, h0, h1);
+        mma_tf32(dq[n], qh, l0, l1);
+        mma_tf32(dq[n], qh, h0, h1);
       }
     }
     const uint4 pow32 = *reinterpret_cast<const uint4 *>(&sm.pow32[blk >> 1][c]);
@@ -619,20 +631,18 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
           put(sm.u.x.x16_hi + xat, hi);
           put(sm.u.x.x16_lo + xat, lo);
         }
-        if (blk >= 2) {
-          put(sm.u.x.x32_hi + xat, blk == 3 ? scale8(hi, pow32) : hi);
-          put(sm.u.x.x32_lo + xat, blk == 3 ? scale8(lo, pow32) : lo);
+        if (blk == 2) {
+          put(sm.u.x.x32_hi + xat, hi);
+          put(sm.u.x.x32_lo + xat, lo);
         }
         times(qf[r], fac, x);
-        hi = half8(x);
-        constexpr uint32_t kDown = 0x24002400u;  // FP16 2^-6, twice: Qd's own scale
-        static_assert(kImgQdScale == kImgScale / 64, "2^-6");
-        put(im + 1024 * r + kImgQd,
-            scale8(blk == 0 ? hi : scale8(hi, pow0), make_uint4(kDown, kDown, kDown, kDown)));
-        if (blk & 1) put(sm.u.x.y16 + (y16_0 ^ (64u * sl)) + 8 * r * kXPitch, hi);
-        if (blk >= 2)
-          put(sm.u.x.y32 + (y32_0 ^ (64u * sl)) + 8 * r * kXPitch,
-              blk == 3 ? scale8(hi, pow32) : hi);
+        split8(x, hi, lo);
+        if (blk > 0) {
+          put(sm.u.x.y_hi + (y0 ^ (64u * sl)) + 8 * r * kXPitch, hi);
+          put(sm.u.x.y_lo + (y0 ^ (64u * sl)) + 8 * r * kXPitch, lo);
+        }
+        put(im + 1024 * r + kImgQdHi, blk == 0 ? hi : scale8(hi, pow0));
+        put(im + 1024 * r + kImgQdLo, blk == 0 ? lo : scale8(lo, pow0));
       }
     }
   }
@@ -640,7 +650,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-      const int at = (g + 4 * i) * kDPitch + 8 * n + 2 * tig;
+      const int at = part_at(g + 4 * i, 8 * n + 2 * tig) + 2 * (tig & 1);
       *reinterpret_cast<float2 *>(&sm.part[blk][0][hf][at]) = make_float2(dk[n][i], dk[n][i + 1]);
       *reinterpret_cast<float2 *>(&sm.part[blk][1][hf][at]) = make_float2(dq[n][i], dq[n][i + 1]);
     }
@@ -661,41 +671,53 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
   for (int t = 0; t < 16; ++t) x[t] = 0.f;
   int r0 = 0, c0 = 0;
   if (warp < 6) {
-    const uint8_t *xh = sm.u.x.x32_hi, *xl = sm.u.x.x32_lo, *y = sm.u.x.y32;
-    int y0;
+    // rows of block 2 by 32's columns, all others by what is kept of 16 and 48
+    // (block 3's by 32's columns times 2^n); columns of 32 by 32's
     if (warp < 4) {
       r0 = 32 + 16 * (warp >> 1);
       c0 = 16 * (warp & 1);
-      y0 = r0 - 32;
     } else {
       r0 = 32 * (warp - 4) + 16;
       c0 = r0 - 16;
-      y0 = 16 * (warp - 4);
-      xh = sm.u.x.x16_hi;
-      xl = sm.u.x.x16_lo;
-      y = sm.u.x.y16;
     }
+    const bool rows32 = warp < 2, cols32 = warp < 4, scaled = warp == 2 || warp == 3;
     const int ar = lane & 15, br = (lane & 7) + ((lane >> 4) << 3);
-    const uint32_t ah0 = smem_u32(xh), al0 = smem_u32(xl), aq0 = smem_u32(y);
+    const uint32_t ah0 = smem_u32(rows32 ? sm.u.x.x32_hi : sm.u.x.x16_hi);
+    const uint32_t al0 = smem_u32(rows32 ? sm.u.x.x32_lo : sm.u.x.x16_lo);
+    const uint32_t bh0 = smem_u32(cols32 ? sm.u.x.x32_hi : sm.u.x.x16_hi);
+    const uint32_t bl0 = smem_u32(cols32 ? sm.u.x.x32_lo : sm.u.x.x16_lo);
+    const uint32_t qh0 = smem_u32(sm.u.x.y_hi), ql0 = smem_u32(sm.u.x.y_lo);
     // (K step ks: pieces 2 ks and 2 ks + 1 of the rows, bits 5 and 6 of the
     // permuted place within a half)
     const uint32_t a0 = x_at(r0 + ar, lane >> 4), b0 = x_at(c0 + br, (lane >> 3) & 1);
-    const uint32_t q0 = x_at(y0 + ar, lane >> 4);
+    const uint32_t q0 = x_at(r0 - 16 + ar, lane >> 4);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
-      uint32_t ah[4], al[4], aq[4], bh[4], bl[4];
+      uint32_t ah[4], al[4], qh[4], ql[4], bh[4], bl[4];
       const uint32_t flip = 32u * (ks & 3), half = 128u * (ks >> 2);
       ldmatrix4(ah, ah0 + (a0 ^ flip) + half);
       ldmatrix4(al, al0 + (a0 ^ flip) + half);
-      ldmatrix4(aq, aq0 + (q0 ^ flip) + half);
-      ldmatrix4(bh, ah0 + (b0 ^ flip) + half);
-      ldmatrix4(bl, al0 + (b0 ^ flip) + half);
+      ldmatrix4(qh, qh0 + (q0 ^ flip) + half);
+      ldmatrix4(ql, ql0 + (q0 ^ flip) + half);
+      ldmatrix4(bh, bh0 + (b0 ^ flip) + half);
+      ldmatrix4(bl, bl0 + (b0 ^ flip) + half);
+      if (scaled) {
+        const uint16_t *const at = &sm.pow32[1][16 * ks + 2 * tig];
+        const uint32_t p0 = *reinterpret_cast<const uint32_t *>(at);
+        const uint32_t p1 = *reinterpret_cast<const uint32_t *>(at + 8);
+        scale_rows(ah, p0, p1);
+        scale_rows(al, p0, p1);
+        scale_rows(qh, p0, p1);
+        scale_rows(ql, p0, p1);
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         mma_f16(ok[n], al, bh[2 * n], bh[2 * n + 1]);
         mma_f16(ok[n], ah, bl[2 * n], bl[2 * n + 1]);
         mma_f16(ok[n], ah, bh[2 * n], bh[2 * n + 1]);
-        mma_f16(oq[n], aq, bh[2 * n], bh[2 * n + 1]);
+        mma_f16(oq[n], ql, bh[2 * n], bh[2 * n + 1]);
+        mma_f16(oq[n], qh, bl[2 * n], bl[2 * n + 1]);
+        mma_f16(oq[n], qh, bh[2 * n], bh[2 * n + 1]);
       }
     }
   } else {
@@ -705,8 +727,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
     const float b = sm.beta[r0 + j];
 #pragma unroll
     for (int c = 0; c < 16; c += 4) {
-      const float4 p0 = lds4(&sm.part[bi][0][0][j * kDPitch + c]);
-      const float4 p1 = lds4(&sm.part[bi][0][1][j * kDPitch + c]);
+      const float4 p0 = lds4(&sm.part[bi][0][0][part_at(j, c)]);
+      const float4 p1 = lds4(&sm.part[bi][0][1][part_at(j, c)]);
       const float v[4] = {p0.x + p1.x, p0.y + p1.y, p0.z + p1.z, p0.w + p1.w};
       // (above the diagonal the factors may have overflowed: dropped, not
       // multiplied by zero)
@@ -761,8 +783,12 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
         make_float2(sign * c[2], sign * c[3]);
   };
   const auto put_a = [&](int t, int s, float x0, float x1) {  // s even
-    *reinterpret_cast<uint32_t *>(sm.a + img_at(t, s & ~7) + (s & 7) * 2) =
-        h2_bits(__floats2half2_rn(x0, x1));
+    const uint32_t at = img_at(t, s & ~7) + (s & 7) * 2;
+    const float2 x = make_float2(x0, x1);
+    const __half2 hi = __float22half2_rn(x);
+    *reinterpret_cast<uint32_t *>(sm.a + at) = h2_bits(hi);
+    *reinterpret_cast<uint32_t *>(sm.a + kImgBlock + at) =
+        h2_bits(__float22half2_rn(ffma2(__half22float2(hi), make_float2(-1.f, -1.f), x)));
   };
   // X10 = -X11 (L10 X00) and X32 = -X33 (L32 X22), 16 x 8 a warp
   const int lo = 32 * ((warp >> 1) & 1), hi = lo + 16, n16 = 8 * (warp & 1);
@@ -782,8 +808,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int i = 0; i < 4; i += 2)
-        put_a(r0 + g + 4 * i, c0 + 8 * n + 2 * tig, oq[n][i] * (kImgScale * kUnit),
-              oq[n][i + 1] * (kImgScale * kUnit));
+        put_a(r0 + g + 4 * i, c0 + 8 * n + 2 * tig, oq[n][i] * (1.f / kImgQdScale),
+              oq[n][i + 1] * (1.f / kImgQdScale));
   }
   __syncthreads();
   load_head(tid, next, more ? h : 0);
@@ -799,22 +825,26 @@ __global__ void __launch_bounds__(kPrepThreads, 2)
       const int piece = 2 * (tid >> 6) + e, s0 = 8 * (piece & 1);
       if ((piece >> 1) < bt) continue;  // (below: by the products' own warps)
       float2 v[4];
+      constexpr float kAUp = kImgScale / kQDown;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 p0 = lds4(&sm.part[bt][1][0][tl * kDPitch + s0 + 4 * i]);
-        const float4 p1 = lds4(&sm.part[bt][1][1][tl * kDPitch + s0 + 4 * i]);
+        const float4 p0 = lds4(&sm.part[bt][1][0][part_at(tl, s0 + 4 * i)]);
+        const float4 p1 = lds4(&sm.part[bt][1][1][part_at(tl, s0 + 4 * i)]);
         const int s = 8 * piece + 4 * i;
-        v[2 * i] = make_float2(s <= t ? (p0.x + p1.x) * kImgScale : 0.f,
-                               s + 1 <= t ? (p0.y + p1.y) * kImgScale : 0.f);
-        v[2 * i + 1] = make_float2(s + 2 <= t ? (p0.z + p1.z) * kImgScale : 0.f,
-                                   s + 3 <= t ? (p0.w + p1.w) * kImgScale : 0.f);
+        v[2 * i] = make_float2(s <= t ? (p0.x + p1.x) * kAUp : 0.f,
+                               s + 1 <= t ? (p0.y + p1.y) * kAUp : 0.f);
+        v[2 * i + 1] = make_float2(s + 2 <= t ? (p0.z + p1.z) * kAUp : 0.f,
+                                   s + 3 <= t ? (p0.w + p1.w) * kAUp : 0.f);
       }
-      *reinterpret_cast<uint4 *>(sm.a + img_at(t, 8 * piece)) = half8(v);
+      uint4 hi, lo;
+      split8(v, hi, lo);
+      *reinterpret_cast<uint4 *>(sm.a + img_at(t, 8 * piece)) = hi;
+      *reinterpret_cast<uint4 *>(sm.a + kImgBlock + img_at(t, 8 * piece)) = lo;
     }
   }
   fence_proxy_async_smem();
   __syncthreads();
-  if (tid == 0) bulk_store(img + kImgA, sm.a, kImgBlock);
+  if (tid == 0) bulk_store(img + kImgAHi, sm.a, 2 * kImgBlock);
   tile_mm(c, &X[(32 + m32) * kXPitchF + 32], kXPitchF, &Y[n32], kYPitch, 0, m32 / 8 + 2, lane);
   // -- T = X diag(beta): the lower left quarter from registers, the two on the
   //    diagonal from X, zeros above ------------------------------------------

@@ -236,3 +236,24 @@ def test_not_finite(name, bits, at):
     assert np.all((np.abs(got[fin] - want[fin]) <= rounded[fin]))
     fin = np.isfinite(left)
     assert np.all(np.abs(state[fin] - left[fin]) <= 2 * REL * np.abs(left[fin]).max())
+
+
+@pytest.mark.parametrize("pool", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[64, 41], [300, 130, 70], [2100]])
+def test_outputs_as_good_as_token_by_token(pool, lens):
+    """The chunked form's outputs before their rounding to BF16: off by what its
+    operands' 22 bits leave of what they are sums of, 3 2^-22 for each of the two
+    products (hi.lo and lo.hi rounded, lo.lo left out) and twice that for the
+    operands of A, which are products themselves; so nearly all round to what
+    the FP64 recurrence's round to."""
+    case = ragged_case(lens=lens, H=3, seed=sum(lens), pool=pool, resume=range(1, len(lens)),
+                       boundary={0: lens[0] // 2})
+    got, _, status = run("prefill", case)
+    ref = {k: x.copy() if isinstance(x, np.ndarray) else x for k, x in case.items()}
+    f64, sizes = np.zeros(case["v"].shape), np.zeros(case["v"].shape)
+    assert po.rule(out_f64=f64, sizes=sizes, **ref) == 0 and status == 0
+    out = ko.bf16_to_f64(got)
+    # (and the decays', REL's 2.5e-5 of a state, on what is left of a token)
+    slack = (9 * 2.0 ** -22 + 2.5e-5) * sizes
+    assert np.all(np.abs(out - f64) <= 2.0 ** -8 * np.abs(f64) + slack)
+    assert np.mean(got == ref["out"]) >= 0.995
