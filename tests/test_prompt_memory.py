@@ -25,9 +25,9 @@ def test_size_follows_the_windows(lib):
         assert sizes == sorted(sizes) and sizes[2] > 0
         assert sizes[-1] == sizes[-2] == lib.kda_prefill_workspace_bytes(T, B, H)
         assert size(T, B, H, T, 0) <= size(T, B, H, T, 1)
-    # an image of a chunk, 104.6 KB, and no more than 2 % beside it, for windows
+    # an image of a chunk, 128.6 KB, and no more than 2 % beside it, for windows
     # of whole chunks without boundaries (a chunk more where the windows may differ)
-    image, need = 837 * 128, size(64 * 256, 1, 32, 64 * 256, 0)
+    image, need = 1029 * 128, size(64 * 256, 1, 32, 64 * 256, 0)
     assert 32 * 256 * image <= need <= 1.02 * 32 * 257 * image + 64 * 1024 * 32
 
 
