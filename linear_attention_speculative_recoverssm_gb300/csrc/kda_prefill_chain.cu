@@ -821,8 +821,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     // S <- S e^{G_end} + dS of chunk i
     const auto advance = [&](int i) {
       if (!wait(&sm.ds_full[half], (uint32_t)i & 1u)) return;
-      if (CAREFUL && by_token) return check(i);
       tc_fence_after();
+      if (CAREFUL && by_token) return check(i);
       const float *dec = sm.decay[i & 3] + kKeys * qt;
 #pragma unroll
       for (int j = 0; j < kKeys / 16; ++j) {
@@ -989,9 +989,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           tmem_store8(lanes + kColRLo + (uint32_t)(kToks / 2 * qt + 8 * k), lo);
         }
         const float u2 = (uu[0].x + uu[0].y) + (uu[1].x + uu[1].y);
-        // (a block past the chunk's tokens has none)
+        // (a block past the chunk's tokens has none; one of zeros, as of padding,
+        // to a state of zeros has lost none: [i + 1] still holds its largest |v|)
+        const float v_block = sm.peak[(i + 1) & 1][qt][row].z;
+        const bool none = kToks * qt >= sm.chunk[i & 3].count ||
+                          (u2 == 0.f && v_block == 0.f && peak[0] == 0.f);
         peak[1] = left * u2;
-        peak[3] = kToks * qt < sm.chunk[i & 3].count ? u2 : __int_as_float(0x7f800000);
+        peak[3] = none ? __int_as_float(0x7f800000) : u2;
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();

@@ -257,3 +257,16 @@ def test_outputs_as_good_as_token_by_token(pool, lens):
     slack = (9 * 2.0 ** -22 + 2.5e-5) * sizes
     assert np.all(np.abs(out - f64) <= 2.0 ** -8 * np.abs(f64) + slack)
     assert np.mean(got == ref["out"]) >= 0.995
+
+
+@OPS
+@pytest.mark.parametrize("log_decay", [-0.1, -4.0])
+def test_padding_rows(op, log_decay):
+    """Tokens of zeros before a prompt, inside it and over whole chunks: zero
+    keys and values write nothing, and the gates forget meanwhile."""
+    case = ragged_case(lens=[300, 150, 70], H=2, seed=15, resume=(1,), boundary={0: 100})
+    set_decay(case, log_decay)
+    for a, b in ((0, 40), (90, 110), (128, 260), (300, 375), (450, 451)):
+        for name in ("q", "k", "v"):
+            case[name][a:b] = 0
+    check(op, case)
