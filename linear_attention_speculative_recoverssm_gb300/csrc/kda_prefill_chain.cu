@@ -971,6 +971,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const float by = f * tail[kScalBeta] * (pow2_inverse(fr) * (1.f / kImgTScale));
       static_assert(kToks == 16, "a part's tokens are a block of the scalars'");
       const float left = qt < kParts - 1 ? max4(tail + kScalLeft + 4 * qt) : kLeftFactor;
+      // (a block past the chunk's tokens has no U; one of zeros, as of padding, to a
+      // state of zeros has lost none: [i + 1] still holds its largest |v|)
+      const bool past = kToks * qt >= sm.chunk[i & 3].count;
+      const bool blank = sm.peak[(i + 1) & 1][qt][row].z == 0.f && peak[0] == 0.f;
       float2 uu[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       if (!wait(&sm.u_full, (uint32_t)i & 1u)) return false;
       tc_fence_after();
@@ -989,13 +993,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           tmem_store8(lanes + kColRLo + (uint32_t)(kToks / 2 * qt + 8 * k), lo);
         }
         const float u2 = (uu[0].x + uu[0].y) + (uu[1].x + uu[1].y);
-        // (a block past the chunk's tokens has none; one of zeros, as of padding,
-        // to a state of zeros has lost none: [i + 1] still holds its largest |v|)
-        const float v_block = sm.peak[(i + 1) & 1][qt][row].z;
-        const bool none = kToks * qt >= sm.chunk[i & 3].count ||
-                          (u2 == 0.f && v_block == 0.f && peak[0] == 0.f);
         peak[1] = left * u2;
-        peak[3] = none ? __int_as_float(0x7f800000) : u2;
+        peak[3] = past || (blank && u2 == 0.f) ? __int_as_float(0x7f800000) : u2;
         tmem_store_wait();
         tc_fence_before();
         __syncwarp();

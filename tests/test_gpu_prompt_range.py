@@ -270,3 +270,37 @@ def test_padding_rows(op, log_decay):
         for name in ("q", "k", "v"):
             case[name][a:b] = 0
     check(op, case)
+
+
+def test_captured_and_at_once():
+    """One captured call replayed on inputs that the parts hold, do not hold and
+    hold again, beside eager calls of the other kind on another stream: bit for
+    bit what each gives alone."""
+    import torch
+    cases = []
+    for seed, size in ((16, 1.0), (17, 1e8), (18, 1.0)):
+        case = ragged_case(lens=[130, 70, 200], H=3, seed=seed, resume=range(3),
+                           boundary={0: 64, 2: 101})
+        set_decay(case, -0.5)
+        case["state"] *= np.float32(size)
+        cases.append(case)
+    for c in cases[1:]:
+        for name in ("sources", "destinations", "boundaries"):
+            c[name] = cases[0][name]
+    alone = [run("prefill", c) for c in cases]
+    d = on_device(cases[0])
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call_rule(ops()["prefill"], cases[0], d)
+    for i, case in enumerate(cases):
+        other = on_device(cases[(i + 1) % 3])
+        for name, t in on_device(case).items():
+            d[name].copy_(t)
+        torch.cuda.synchronize()
+        graph.replay()
+        call_rule(ops()["prefill"], case, other, stream=side)
+        torch.cuda.synchronize()
+        for got, want in ((d, alone[i]), (other, alone[(i + 1) % 3])):
+            np.testing.assert_array_equal(to_numpy(got["out"]), want[0])
+            np.testing.assert_array_equal(to_numpy(got["state"]), want[1])
