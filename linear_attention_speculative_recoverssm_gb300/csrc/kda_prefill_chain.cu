@@ -28,10 +28,10 @@
 // least its largest beta,
 //   |R| <= V + sqrt(128) B,  |U| <= (p + 64 p^2) V + sqrt(128) p B
 // (unit keys; a row's norm grows by at most beta |v| a token), and B itself is
-//   |S before|_2 max e^{G_end} + 8 |U'|_2,
+//   max |S before| max e^{G_end} + 8 |U'|_2,
 // U' being U times the largest decay from the end of its block of 16 tokens to
 // the chunk's (the sum of 64 of them is at most 8 times their norm); (x + y)^2
-// <= 2 x^2 + 2 y^2 makes Z = (f B)^2 of two sums of squares.  f is kept while
+// <= 2 x^2 + 2 y^2 makes Z = (f B)^2 of their squares.  f is kept while
 // Z < 2^18 and f (p + 64 p^2) V < 2^14, which hold S and U below 2^15, and one
 // of them is not 2^10 or 2^5 below that.  All of it is known before dS is, from
 // a chunk's image and U: the rows' quarters exchange squares while M3 runs, and
@@ -42,7 +42,7 @@
 // Where a chunk leaves less in all rows of a group of 32 (those of one warp), or
 // has tokens whose sizes are as far below the largest, or something in it is not
 // finite, the parts cannot hold it.
-// The chain finds that when it has the next state's norms; the group's rows then
+// The chain finds that when it has the next state's sizes; the group's rows then
 // go through the chunks once more, from the source, in a second kernel behind
 // it, which looks before it goes on and does such a chunk token by token
 // (CAREFUL): 150 us for such a chunk, 5 for the others.  Both in one kernel leave
@@ -108,8 +108,8 @@ struct ChainSmem {
   uint8_t v[kVBytes];
   float decay[4][kImgTail / 4];  // decays and scalars of chunk i at i & 3
   PrefillChunk chunk[4];  // chunk i at i & 3, there when its v is
-  // [chunk parity][part][row]: squares of S and of U', in parts' units; next |v|;
-  // squares of U over the part's block of tokens
+  // [chunk parity][part][row]: the largest |S|, squares of U', in parts' units; the
+  // next |v|; squares of U over the part's block of tokens
   float4 peak[2][kParts][128];
   uint32_t kept[4][kParts];  // by row warps w & 3 and part: what a chunk left (CAREFUL)
   float2 next[128];          // by row: f of the next chunk and most_r's bits
@@ -203,6 +203,13 @@ __device__ __forceinline__ float row_factor(float b, float v) {
   return pow2(min(max(min(8 - exponent(b), 13 - exponent(v)) - 2, -109), kMostExp));
 }
 
+// The larger; NaN where one is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 __device__ __forceinline__ float sqrt_fast(float x) {
   float y;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -213,9 +220,10 @@ __device__ __forceinline__ float pow2_inverse(float s) {
   return __uint_as_float((254u << 23) - __float_as_uint(s));
 }
 
-// Two values as FP16 and what that leaves.
-__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+// Two values as FP16 and what that leaves; `most` the largest |hi| so far.
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo, __half2 &most) {
   const __half2 h = __float22half2_rn(x);
+  most = __hmax2_nan(most, __habs2(h));
   const __half2 l = __float22half2_rn(less_half(x, h));
   hi = *reinterpret_cast<const uint32_t *>(&h);
   lo = *reinterpret_cast<const uint32_t *>(&l);
@@ -715,14 +723,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       if (lane == 0) mbar_arrive(&sm.v_free);
       return fmaxf(__low2float(peak), __high2float(peak));
     };
-    // the sum of what this row's parts left at [i & 1], of |v| the largest, of
-    // the blocks' U the smallest
+    // the sum of what this row's parts left at [i & 1], of |S| and |v| the largest,
+    // of the blocks' U the smallest
     const auto joined = [&](int i) {
       float4 m = sm.peak[i & 1][0][row];
 #pragma unroll
       for (int j = 1; j < kParts; ++j) {
         const float4 x = sm.peak[i & 1][j][row];
-        m = make_float4(m.x + x.x, m.y + x.y, fmaxf(m.z, x.z), fminf(m.w, x.w));
+        m = make_float4(max_nan(m.x, x.x), m.y + x.y, fmaxf(m.z, x.z), fminf(m.w, x.w));
       }
       return m;
     };
@@ -730,12 +738,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const float4 v = lds4(x);
       return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
     };
-    float most_s = 0.f;  // largest |S| of this part
+    const auto largest = [&] {  // of this part's s
+      float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < kKeys / 2; ++e)
-      most_s = fmaxf(most_s, fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
-    static_assert(kKeys == 32, "5.7 is above its root");
-    sm.peak[1][qt][row] = make_float4(5.7f * most_s, 0.f, load_v(0), 0.f);
+      for (int e = 0; e < kKeys / 2; ++e) m = max_nan(m, max_nan(fabsf(s[e].x), fabsf(s[e].y)));
+      return m;
+    };
+    sm.peak[1][qt][row] = make_float4(largest(), 0.f, load_v(0), 0.f);
     wait(&sm.d_full[0], 0u);
     bad = named_bar_or(1, 32 * kRowWarps, bad);
     // s holds the state times 2^6 f from here on; inv = 1 / f
@@ -750,25 +759,16 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     }
 #pragma unroll
     for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(s[e], both(f * kUnit));
-    float squares = 0.f;  // of s
-    const auto square = [&] {
-      float2 ss[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int e = 0; e < kKeys / 2; ++e) ss[e & 1] = ffma2(s[e], s[e], ss[e & 1]);
-      squares = (ss[0].x + ss[0].y) + (ss[1].x + ss[1].y);
-    };
     const auto is_marked = [&] { return ((now(sm.lost) >> group) & 1) != 0; };
-    square();
     // The parts end a fixed way below what they could hold, 2^-24 / f, and what
     // of that reaches the state measures some 2^-27 / f.  A chunk is lost for a
-    // group of rows that is left with norms below 2^-11 / f throughout: 2^-16 of
-    // the largest row.  So it is where a block of 16 tokens has no U above that,
+    // group of rows that is left with nothing above 2^-12 / f: 2^-15 of its largest
+    // entry.  So it is where a block of 16 tokens has no U above that,
     // nor had the state before the chunk: of its outputs not enough would be left
     // (values before an outlying one).
-    constexpr float kLeast = 0x1p-11f;
-    constexpr float kLeastSquare = kLeast * kUnit * (kLeast * kUnit);
+    constexpr float kLeast = 0x1p-12f;
     // (CAREFUL) Before the next chunk: where that is so for the largest of the
-    // four parts' norms, the chunk is done again token by token, from the state
+    // four parts' entries, the chunk is done again token by token, from the state
     // before it.  Its parts are still in TMEM, and hold it to 2^-19 of its rows;
     // where they would not, `by_token` was set before dS was there.  All four
     // warps come to that together: one whose rows all keep more says so, and
@@ -777,11 +777,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     const auto check = [&](int i) {
       uint32_t mine = 0xffffffffu;  // (every row keeps enough)
       bool finite = true;
+      const float top = largest();
       const bool doubt = !by_token && live &&
-                         !__all_sync(0xffffffffu, squares >= kLeastSquare || f == pow2(kMostExp));
+                         !__all_sync(0xffffffffu, top >= kLeast * kUnit || f == pow2(kMostExp));
       if (doubt) {
         // (a row that is not finite asks for nothing)
-        const float n = sqrt_fast(squares) * (inv * kPerUnit);
+        const float n = top * (inv * kPerUnit);
         finite = is_finite(n);
         mine = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(n) : 0u);
       }
@@ -808,11 +809,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           s[e] = ffma2(both(1.f), s[e], __half22float2(*reinterpret_cast<const __half2 *>(&d[e])));
       }
     };
-    // The same of rows whose squares are brought together, in units of f;
-    // `least` is kLeastSquare in those units where f is not the chunk's.
-    const auto is_lost = [&](float squares, float least) {
-      const float n = sqrt_fast(squares) * (inv * kPerUnit);
-      const float floor = sqrt_fast(least) * (inv * kPerUnit);
+    // The same of rows whose largest are brought together, times f; `least` is
+    // kLeast times the present f over the chunk's.
+    const auto is_lost = [&](float top, float least) {
+      const float n = top * inv, floor = least * inv;
       const bool finite = is_finite(n);
       const uint32_t most = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(n) : 0u);
       const uint32_t worst = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(floor) : 0u);
@@ -836,7 +836,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           y = ffma2(y, make_float2(g.z, g.w), f2(d[2 * e + 2], d[2 * e + 3]));
         }
       }
-      square();
       if constexpr (CAREFUL) check(i);
     };
     // the outputs of chunk i
@@ -895,13 +894,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     // What a state that is ready goes through.
     const auto rescale = [&] {
       if (changes) {
-        if (!CAREFUL && qt == kParts - 1) sm.least[row] *= f_next * inv * (f_next * inv);
+        if (!CAREFUL && qt == kParts - 1) sm.least[row] *= f_next * inv;
         // (one after the other: the factors' quotient may be out of range)
 #pragma unroll
         for (int e = 0; e < kKeys / 2; ++e) s[e] = fmul2(fmul2(s[e], both(f_next)), both(inv));
         f = f_next;
         inv = pow2_inverse(f);
-        square();
         changes = false;
       }
     };
@@ -918,14 +916,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       // (what the factors are made of goes to memory at once: the registers are
       // wanted)
       float *const peak = reinterpret_cast<float *>(&sm.peak[i & 1][qt][row]);
-      peak[0] = squares;
       // S as parts
       {
+        __half2 most = __float2half2_rn(0.f);
 #pragma unroll
         for (int j = 0; j < kKeys / 16; ++j) {
           uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) split2(s[8 * j + e], hi[e], lo[e]);
+          for (int e = 0; e < 8; ++e) split2(s[8 * j + e], hi[e], lo[e], most);
           tmem_store8(lanes + kColSHi + (uint32_t)(kKeys / 2 * qt + 8 * j), hi);
           tmem_store8(lanes + kColSLo + (uint32_t)(kKeys / 2 * qt + 8 * j), lo);
         }
@@ -933,6 +931,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.s_ready[half]);
+        const float2 x = __half22float2(most);
+        peak[0] = max_nan(x.x, x.y);
       }
       if (i > 0) emit(i - 1, inv_before);
       // R = V - W
@@ -940,6 +940,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const float w = -kDown * kPerUnit * fr * inv;
       if (!wait(&sm.w_full, (uint32_t)i & 1u)) return false;
       tc_fence_after();
+      __half2 unused = __float2half2_rn(0.f);
       {
 #pragma unroll
         for (int k = 0; k < kToks / 16; ++k) {
@@ -951,7 +952,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             const float2 v = make_float2(__uint_as_float(vv << 16),
                                          __uint_as_float(vv & 0xffff0000u));
             split2(ffma2(f2(d[2 * j], d[2 * j + 1]), both(w), fmul2(v, both(fr))), hi[j],
-                   lo[j]);
+                   lo[j], unused);
           }
           tmem_store8(lanes + kColRHi + (uint32_t)(kToks / 2 * qt + 8 * k), hi);
           tmem_store8(lanes + kColRLo + (uint32_t)(kToks / 2 * qt + 8 * k), lo);
@@ -987,7 +988,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           for (int j = 0; j < 8; ++j) {
             const float2 u = fmul2(f2(d[2 * j], d[2 * j + 1]), both(by));
             uu[j & 1] = ffma2(u, u, uu[j & 1]);
-            split2(u, hi[j], lo[j]);
+            split2(u, hi[j], lo[j], unused);
           }
           tmem_store8(lanes + kColRHi + (uint32_t)(kToks / 2 * qt + 8 * k), hi);
           tmem_store8(lanes + kColRLo + (uint32_t)(kToks / 2 * qt + 8 * k), lo);
@@ -1000,14 +1001,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.u_ready);
       }
-      // under M3: every row's squares are there once all warps have arrived.  One
+      // under M3: every row's sums are there once all warps have arrived.  One
       // of a row's four warps, of those whose half of dS comes last, works out
       // what all of them go by (an E's four warps share a scheduler: all four
       // would take it 350 issue slots a chunk)
       if (CAREFUL || qt == kParts - 1) {  // (of the last chunk: what was lost before it)
         if (!wait(&sm.u_ready, (uint32_t)i & 1u)) return false;
         const float4 m = joined(i);
-        const float z = fmaf(m.x, max4(tail + kScalEnd), m.y);
+        const float z = fmaf(m.x * m.x, max4(tail + kScalEnd), m.y);
         // (a chunk whose V is infinite goes token by token, from this state)
         const float v0 = m.z * sm.decay[(i + 1) & 3][kScalValue];
         const float v = is_finite(v0) ? v0 : 0.f, fv = f * v;
@@ -1016,17 +1017,18 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         // (CAREFUL: a state that its parts would not give back; a fresh one is
         // zeros)
         const float least = CAREFUL || i == 0 ? 0.f : sm.least[row];
-        const bool low = CAREFUL ? m.x < 0x1p-12f && f != pow2(kMostExp) && (i > 0 || src >= 0)
-                                 : m.x < least;
-        const float some = fmaxf(m.x, kUnit * kUnit * m.w);
-        if (__any_sync(0xffffffffu, !keep || low || some < kLeastSquare)) {
+        const float top = kPerUnit * m.x;  // of f |S|
+        const bool low = CAREFUL ? top < 0x1p-12f && f != pow2(kMostExp) && (i > 0 || src >= 0)
+                                 : top < least;
+        const bool little = top < kLeast && m.w < kLeast * kLeast;
+        if (__any_sync(0xffffffffu, !keep || low || little)) {
           // An infinity or a NaN of one token is in the U of all of its chunk's
           // (zeros of T times it), and not of those before it by the rule.  (A
           // state that is not finite spoils all that follows by either.)
           const bool wild = __any_sync(0xffffffffu, !is_finite(m.y) && is_finite(m.x));
-          const bool thin = wild || is_lost(some, kLeastSquare);
+          const bool thin = wild || is_lost(fmaxf(top, sqrt_fast(m.w)), kLeast);
           if constexpr (CAREFUL) by_token = live && (__any_sync(0xffffffffu, low) || thin);
-          else if ((thin || is_lost(m.x, least)) && lane == 0) atomicOr(&sm.lost, 1 << group);
+          else if ((thin || is_lost(top, least)) && lane == 0) atomicOr(&sm.lost, 1 << group);
           f_next = keep ? f : row_factor(sqrt_fast(z) * inv, v);
           if constexpr (CAREFUL) changes = __any_sync(0xffffffffu, f_next != f);
         }
@@ -1034,7 +1036,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         most_r = max(((exponent(z) + 1) >> 1) - exponent(f) + 4, exponent(m.z)) + 2;
         if constexpr (!CAREFUL) {
           sm.next[row] = make_float2(f_next, __int_as_float(most_r));
-          sm.least[row] = kLeastSquare;
+          sm.least[row] = kLeast;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.factors[group]);
         }
@@ -1091,7 +1093,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             s[e] = fmul2(make_float2(held[2 * e], held[2 * e + 1]), both(f * kUnit));
 #pragma unroll
           for (int e = 0; e < kToks / 2; ++e) v2[e] = __float_as_uint(held[kKeys + e]);
-          square();
         }
         ++i;
         if (i == now(sm.item.bnd_at)) store_boundary();
@@ -1099,12 +1100,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
     }
     if constexpr (!CAREFUL) {
-      // the last chunk's, whose norms nothing else brings together
+      // the last chunk's, whose state nothing else brings together
       const int n = now(sm.item.n);
-      sm.peak[n & 1][qt][row].x = squares;
+      sm.peak[n & 1][qt][row].x = kPerUnit * largest();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.advanced[group]);
-      if (!bad && wait(&sm.advanced[group], 0u) && is_lost(joined(n).x, kLeastSquare) && lane == 0)
+      if (!bad && wait(&sm.advanced[group], 0u) && is_lost(joined(n).x, kLeast) && lane == 0)
         atomicOr(&sm.lost, 1 << group);
       __syncwarp();
     }
