@@ -818,8 +818,22 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const uint32_t worst = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(floor) : 0u);
       return most < worst && __uint_as_float(worst) > 0x1p-100f;
     };
+    float f_next = f;
+    bool changes = false;   // for any row of the warp
+    // (else) What the rows' warps go by after chunk i.
+    const auto take = [&](int i) {
+      if (!wait(&sm.factors[group], (uint32_t)i & 1u)) return false;
+      const float2 x = sm.next[row];
+      f_next = x.x;
+      most_r = __float_as_int(x.y);
+      changes = __any_sync(0xffffffffu, f_next != f);
+      return true;
+    };
     // S <- S e^{G_end} + dS of chunk i
     const auto advance = [&](int i) {
+      if constexpr (!CAREFUL) {  // (while dS is on its way: after it, 2 % longer)
+        if (!take(i)) return;
+      }
       if (!wait(&sm.ds_full[half], (uint32_t)i & 1u)) return;
       tc_fence_after();
       if (CAREFUL && by_token) return check(i);
@@ -889,8 +903,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll 1
       for (int e = 0; e < kPieces; ++e) to[e] = from[e];
     };
-    float f_next = f;
-    bool changes = false;   // for any row of the warp
     // What a state that is ready goes through.
     const auto rescale = [&] {
       if (changes) {
@@ -902,15 +914,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         inv = pow2_inverse(f);
         changes = false;
       }
-    };
-    // (else) What the rows' warps go by after chunk i.
-    const auto take = [&](int i) {
-      if (!wait(&sm.factors[group], (uint32_t)i & 1u)) return false;
-      const float2 x = sm.next[row];
-      f_next = x.x;
-      most_r = __float_as_int(x.y);
-      changes = __any_sync(0xffffffffu, f_next != f);
-      return true;
     };
     const auto pass = [&](int i, float inv_before) {
       // (what the factors are made of goes to memory at once: the registers are
@@ -1049,14 +1052,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         if (i > 0) {
           advance(i - 1);
           if (bad) break;
-          if (!take(i - 1)) break;
           if (i == now(sm.item.bnd_at)) store_boundary();
           rescale();
         }
         if (!pass(i, inv_before)) break;
       }
       if (!bad) advance(now(sm.item.n) - 1);
-      if (!bad) take(now(sm.item.n) - 1);
       if (!bad && now(sm.item.n) == now(sm.item.bnd_at)) store_boundary();
     } else {
       // (by token: through memory, so that what the chunks need in registers is
