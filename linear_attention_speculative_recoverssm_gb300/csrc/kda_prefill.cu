@@ -14,10 +14,10 @@ namespace {
 
 // Windows of at most so many tokens go through the token-by-token kernel, where
 // a call has none longer: 40 tokens of 1 / 4 / 32 requests of 32 heads take 30 /
-// 36 / 159 us there and 35 / 38 / 157 as a chunk each, 48 tokens 35 / 41 / 188
-// and 36 / 39 / 157.  Beside longer ones fewer, since that kernel finds room
-// only as the chain ends: prompts of 63 x 24 and 2000 tokens take 286 us with
-// 24 and 329 with 16 in its place, 37 and 5 x 1600 tokens 341 with 24 and 359
+// 36 / 159 us there and 38 / 40 / 161 as a chunk each, 48 tokens 34 / 41 / 189
+// and 36 / 40 / 161.  Beside longer ones fewer, since that kernel finds room
+// only as the chain ends: prompts of 63 x 24 and 2000 tokens take 292 us with
+// 24 and 337 with 16 in its place, 37 and 5 x 1600 tokens 368 with 24 and 385
 // with 40.
 constexpr int kShortLen = 40, kMixedLen = 24;
 constexpr int kListThreads = 1024;
@@ -31,8 +31,8 @@ constexpr int kListThreads = 1024;
 // after a short first one, and there are few.  With more items the chain fills
 // the GPU by itself, and a segment only costs its launches and the state's way
 // through memory.  One prompt of 16384 tokens, us in one segment / in eight of
-// 32 chunks / in four from 18 chunks on: 8 heads 778 / 826 / 763, 32 heads 1011 /
-// 913 / 836, 48 heads 1167 / 964 / 1076, 64 heads 1334 / 1264 / 1468.  (The
+// 32 chunks / in four from 18 chunks on: 8 heads 757 / 818 / 751, 32 heads 1022 /
+// 932 / 845, 48 heads 1197 / 1046 / 1171, 64 heads 1384 / 1455 / 1613.  (The
 // workspace's size depends on it, so it goes by the SMs of a GB300, not of the
 // device at hand.)
 constexpr int kSms = 152;

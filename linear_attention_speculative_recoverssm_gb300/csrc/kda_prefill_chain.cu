@@ -15,8 +15,8 @@
 // next chunk's M1 runs.  Warp 16 issues the MMAs, warp 17 the copies.  All
 // products take hi.hi + hi.lo + lo.hi.  (With the high parts alone for O, 16
 // prompts took 578 us in place of 639 and one of 16384 tokens 832 in place of
-// 890, and 15 % of the outputs rounded to another BF16 value than the exact ones;
-// so do 0.1 % now.)
+// 890, and 15 % of the outputs rounded to another BF16 value than the exact
+// ones; now fewer than 0.5 % do.)
 //
 // FP16 parts of a row are taken times powers of two: S times 2^6 f, U times f,
 // R times a factor fr of its own, so that with the images' scales dS comes out
@@ -45,18 +45,18 @@
 // The chain finds that when it has the next state's sizes; the group's rows then
 // go through the chunks once more, from the source, in a second kernel behind
 // it, which looks before it goes on and does such a chunk token by token
-// (CAREFUL): 150 us for such a chunk, 5 for the others.  Both in one kernel leave
-// every chunk's path too few registers: 16384 tokens took 895 us in place of 843.
+// (CAREFUL): 150 us for such a chunk, 5 for the others.  (Both in one kernel left
+// every chunk's path too few registers: 16384 tokens took 895 us in place of 843.)
 // The state itself stays in FP32, in registers: an accumulator that is added
 // to over and over loses up to a unit of its last place each time, so dS is
 // summed apart, smallest parts first.
 //
-// What bounds it: a chunk's products and passes depend on one another, some 6.5 K
-// cycles (3.3 us) of which the tensor cores run 2.8 K, with 8 CTAs on the GPU
-// nearly as with 32; 265 chunks of 32 heads in 16 prompts take 248 us, most of
-// them the longest prompt's 78 chunks.  TMEM and shared memory hold one item an
-// SM.  (One factor for R, S and U, from bounds that know no decay, was 0.3 us a
-// chunk less, and lost what the above keeps.)  Eight row
+// What bounds it: a chunk's products and passes depend on one another, some 6.2 K
+// cycles (3.2 us) of which the tensor cores run 2.8 K, with 8 CTAs on the GPU (751
+// us for 256 chunks) nearly as with 32; 265 chunks of 32 heads in 16 prompts take
+// 245 us, most of them the longest prompt's 78 chunks.  TMEM and shared memory
+// hold one item an SM.  (One factor for R, S and U, from bounds that know no
+// decay, was 0.2 us a chunk less, and lost what the above keeps.)  Eight row
 // warps in place of 16 took longer, and so did the outputs' stores between R and
 // U (2 to 6 %): what the other warps split then waits.
 #include <cuda_fp16.h>

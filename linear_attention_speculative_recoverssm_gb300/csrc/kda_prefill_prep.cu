@@ -21,7 +21,7 @@
 // are the same parts times an exact 2^n.
 //
 // What bounds it: 265 chunks of 32 heads read 0.42 GB and write 1.1 GB, 225 us at
-// a copy's rate, and take 369.  16 warps an SM is what registers (128, with 20
+// a copy's rate, and take 373.  16 warps an SM is what registers (128, with 20
 // bytes spilled) and shared memory leave room for; they issue every other cycle,
 // the operands' pass on exponents, FP16 splits and their stores.  (Splits by a
 // conversion of the high part in place of a multiply-add of FP16 to FP32: 382.)
