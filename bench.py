@@ -17,6 +17,9 @@ in HBM.  Prints one JSON line (rank 0):
               every host core (one worker process per core, forked before
               any CUDA call), with the one-core figure beside it
 
+`--operators` times the prompt operators' cases (perf/operators.py) instead and
+prints one line of them.
+
 `--impl reference` times the oracle alone (every host core, a bounded sample
 of items per step) and prints the same line with "impl": "reference".
 """
@@ -1087,6 +1090,43 @@ def run_ours(args):
         dist.destroy_process_group()
 
 
+def measure_operators(names, reps=15):
+    """The cases of perf/operators.py, each pass through the library's calls:
+    device time (CUDA events behind a device-side sleep, L2 written over before
+    each pass, the median of ``reps``) and the share of the floor that its bytes
+    take at the measured copy rate."""
+    import importlib.util
+    import torch
+    spec = importlib.util.spec_from_file_location("operators",
+                                                  os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    with open(os.path.join(ROOT, "MEASURED_PEAKS.json")) as f:
+        peak = float(json.load(f).get("hbm_gbs", 6800.0))
+    flush = torch.empty(64 * 2 ** 20, device="cuda")  # 256 MB
+    rows = []
+    for case in ops.listed():
+        if names and case["name"] not in names:
+            continue
+        state, times = ops.prepare(case, 1), []
+        for i in range(reps + 3):
+            flush.zero_()
+            e0, e1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda._sleep(_HEAD_START_CYCLES // 20)
+            e0.record()
+            ops.run(state)
+            e1.record()
+            torch.cuda.synchronize()
+            if i >= 3:
+                times.append(e0.elapsed_time(e1) * 1e3)
+        us, floor = statistics.median(times), ops.work(case)["bytes"] / peak / 1e3
+        rows.append({"case": case["name"], "us": round(us, 2), "floor_us": round(floor, 2)})
+        del state
+    print(json.dumps({"metric": "prompt operators, device time", "unit": "us", "l2": "flushed",
+                      "data": "synthetic", "rows": rows}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -1107,8 +1147,12 @@ def main():
     ap.add_argument("--ref-step-seconds", type=float, default=1.0)
     ap.add_argument("--traffic", type=float, default=None,
                     help="ncu dram bytes per launch of the current kernel, if measured")
+    ap.add_argument("--operators", nargs="?", const="", default=None, metavar="CASE,CASE",
+                    help="time the prompt operators' cases (all, or those named) and nothing else")
     args = ap.parse_args()
-    if args.impl == "reference":
+    if args.operators is not None:
+        measure_operators([n for n in args.operators.split(",") if n])
+    elif args.impl == "reference":
         run_reference(args)
     else:
         run_ours(args)
