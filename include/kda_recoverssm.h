@@ -84,6 +84,12 @@ extern "C" {
 #define KDA_MAX_LAYERS 64
 #define KDA_PROMPT_MAX_HEADS 1024 /* heads of the prompt operators */
 #define KDA_PLAN_MAX_REQUESTS (1 << 24) /* requests of one kda_slot_plan */
+#define KDA_TREE_MAX_NODES 64 /* drafted tokens of one request's tree, its root among them */
+#define KDA_TREE_MAX_DEPTH KDA_MAX_WINDOW /* tokens of a path: what a record row holds */
+#define KDA_MAX_VOCAB (1 << 20) /* tokens of kda_draft_accept's vocabulary */
+
+#define KDA_PROBS_F32 0
+#define KDA_PROBS_BF16 1
 
 typedef uint16_t kda_bf16;
 
@@ -630,6 +636,177 @@ int kda_recurrent(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const
                   const int32_t *boundary_lens, const int32_t *query_start_loc, int n_tokens,
                   kda_bf16 *out, int B, int H, int Q, int null_slot, int32_t *status,
                   void *stream);
+
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens.  The step at the top of this file verifies one
+ * chain of drafts per request.  The calls below verify a tree of them, each
+ * token from the state and the convolution window behind its own ancestors,
+ * take the drafts against the target's probabilities, and leave the accepted
+ * path where the next step's replay (of a chain or of another tree) and its
+ * convolution find it:
+ *
+ *   kda_tree_conv -> kda_tree_verify -> (the model's logits) ->
+ *   kda_draft_accept -> kda_tree_select -> kda_defer_commit.
+ *
+ * Conventions that the four share, beside those at the top of this file:
+ *  - Request b's nodes are the tokens query_start_loc[b] ..
+ *    query_start_loc[b + 1] - 1 of the packed activations (b*Q .. b*Q + Q - 1
+ *    when query_start_loc is NULL; n_tokens is B*Q then), n_b <= Q <=
+ *    KDA_TREE_MAX_NODES of them.
+ *  - parents [n_tokens] int32: node t's parent within its request, -1 <=
+ *    parents[t] < t; -1 hangs the node on the checkpoint (a root; the
+ *    operators that move states take any number of them, kda_draft_accept one
+ *    alone, node 0, the last token that was sampled).  A path holds at most
+ *    KDA_TREE_MAX_DEPTH tokens.  NULL: every request's nodes are a chain, and
+ *    Q is at most that many.
+ *  - A request whose window is bad (see the top) or whose parents are not
+ *    such a tree is reported as KDA_ERR_ARG in the status word, and nothing
+ *    of it is read or written but what an operator below names.  Rows of the
+ *    activations that belong to no request are not touched.
+ *  - A request with state_slots[b] <= null_slot is inert; null_slot >= -1.
+ *    record_rows NULL: request b's record row is b.
+ *  - 1 <= H <= KDA_PROMPT_MAX_HEADS; n_tokens * H and B * H fit 31 bits.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kda_tree_conv -- kda_layer_prologue's convolution and SiLU over trees.  Per
+ * node t and channel ch, with W = conv_state[slot, ch], n = the pending count
+ * clamped to [0, conv_width - 2] (0 without a record row or with pending
+ * NULL) and off = n > 0 ? n - 1 : 0:
+ *   s_3 = x[t, ch], and s_2, s_1, s_0 the entries of t's parent, of the
+ *   parent's parent and of that one's; above a root stand W[off + 2],
+ *   W[off + 1] and W[off], the last first;
+ *   out_t = BF16(silu(bias[ch] + sum_{i<4} conv_weight[part, i, h*128 + c] *
+ *           s_i)) to q / k / v.
+ * On a chain these are kda_layer_prologue's values.  The window is only read:
+ * which nodes' inputs follow in it is known after sampling
+ * (kda_tree_select).  Inert requests are skipped.
+ *   x [n_tokens, 3*D], conv_weight [3, 4, D], conv_bias [3*D] or NULL BF16;
+ *   conv_state [n_slots, 3*D, conv_width] BF16, 3 <= conv_width <= 10 (rq + 2
+ *   of the layer calls), slot stride a multiple of 8 elements; q, k, v
+ *   [n_tokens, H, 128] BF16.  16-byte aligned.  pending [n_rows].
+ */
+int kda_tree_conv(const kda_bf16 *x, const kda_bf16 *conv_weight, const kda_bf16 *conv_bias,
+                  const kda_bf16 *conv_state, int64_t conv_slot_stride, int conv_width,
+                  int n_slots, const int32_t *state_slots, const int32_t *record_rows,
+                  const int32_t *pending, int n_rows, const int32_t *parents,
+                  const int32_t *query_start_loc, int n_tokens, kda_bf16 *q, kda_bf16 *k,
+                  kda_bf16 *v, int B, int H, int Q, int null_slot, int32_t *status,
+                  void *stream);
+
+/*
+ * kda_tree_verify -- the delta rule over trees, from the checkpoints.  Per
+ * (request b, head h), with n = clamp(pending[r], 0, rq) accepted tokens in
+ * record row r (none without a row or with pending NULL), S_n as in
+ * kda_replay_verify step 1, written back to state_pool[slot, h] iff n > 0,
+ * and for every node t with parent a (S_a = S_n where a = -1):
+ *   S_t' = S_a diag(d_t); u_t = sigmoid(raw_beta_t) (v_t - S_t' kn_t);
+ *   S_t = S_t' + u_t kn_t^T; out_t = BF16(S_t qn_t)
+ * with d_t, kn_t and qn_t as in kda_verify, computed in closed form: no S_t
+ * is formed.  node_corr[t, h, :] = u_t (FP32), from which kda_tree_select
+ * takes the accepted path's.  The records are only read.  The replay does not
+ * depend on the window: it runs for an empty one too, and with n_tokens == 0.
+ * Inert requests get zeros in `out`, and nothing else is written.
+ *   What is held in fewer bits: the products of the state with the nodes'
+ *   keys and queries take their operands with 22 bits (TF32 in two parts);
+ *   states, sums, norms, gates and decays are FP32.
+ *   q, k, v, raw_g, out [n_tokens, H, 128], raw_beta [n_tokens, H] BF16;
+ *   A_log [H], dt_bias [H, 128], node_corr [n_tokens, H, 128] FP32;
+ *   state_pool [n_slots, H, 128, 128] of state_dtype, slot stride
+ *   `slot_stride` elements; corr [n_rows, H, rq, 128] FP32 and key_gate
+ *   [n_rows, H, rq, 256] BF16 with row strides as in kda_replay_verify,
+ *   1 <= rq <= 8.  pending, corr and key_gate may be NULL together: no replay,
+ *   and the pool is only read.  A BF16 pool takes no replay (fold it in with
+ *   kda_commit): KDA_ERR_UNSUPPORTED.  -10 <= lower_bound <= 10.
+ * All pointers but raw_beta, A_log and the index arrays 16-byte aligned.
+ */
+int kda_tree_verify(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v,
+                    const kda_bf16 *raw_g, const kda_bf16 *raw_beta, const float *A_log,
+                    const float *dt_bias, float lower_bound, float q_scale, void *state_pool,
+                    int state_dtype, int64_t slot_stride, int n_slots,
+                    const int32_t *state_slots, const int32_t *parents,
+                    const int32_t *query_start_loc, int n_tokens, const int32_t *record_rows,
+                    const int32_t *pending, const float *corr, const kda_bf16 *key_gate,
+                    int64_t corr_row_stride, int64_t kg_row_stride, int n_rows, int rq,
+                    float *node_corr, kda_bf16 *out, int B, int H, int Q, int null_slot,
+                    int32_t *status, void *stream);
+
+/*
+ * kda_draft_accept -- drafted tokens against the target's probabilities, from
+ * given random numbers; lossless: the tokens follow the target's
+ * distribution.  p_t = target[t], the target's next-token weights after node
+ * t; x_t = tokens[t].  Per request, from node a = 0, its last sampled token:
+ *   with draft probabilities (chains; draft[t] = q_t, what x_t was drawn
+ *   from): the child t = a + 1 is accepted iff u_a q_t(x_t) < p_a(x_t);
+ *   without (drafts taken for sure: trees of likely tokens, or a chain): of
+ *   a's children in index order the first with u_a < the sum of p_a over the
+ *   children's tokens so far is accepted; a token that an earlier sibling has
+ *   adds nothing, and its node is never taken;
+ *   an accepted child is the next a.  u = accept_uniforms[a].
+ * Then a token is drawn after the last a: with weights max(p_a - q_t, 0)
+ * where a drafted child t was refused, p_a without the refused children's
+ * tokens where there are no draft probabilities, p_a where a has no child or
+ * those weights are all zero; it is the first token where the running sum of
+ * the weights exceeds sample_uniforms[b] times their total.
+ *   accepted[b] = the path's nodes, root included (the count that
+ *   kda_defer_commit takes); path[b, 0 .. 7] = its nodes within the request,
+ *   -1 behind the last; next_tokens[b] = the token drawn.
+ *   Inert requests (state_slots may be NULL: none is), empty windows and
+ *   reported ones get 0, -1s and -1.  Reported too: a parent of node 0, a
+ *   second root, a token outside 0 .. vocab - 1 (the root's is not looked
+ *   at), weights whose total is not above zero and finite (accepted and path
+ *   are kept then).  A weight that is NaN or negative counts as 0.
+ *   Uniforms lie in [0, 1).
+ *   Comparisons and sums run at 48 bits or more, so that a token does not
+ *   depend on the order of a sum.
+ *   target [n_tokens, vocab] and draft (NULL, or the same, with parents NULL)
+ *   of probs_dtype, rows target_row_stride / draft_row_stride >= vocab
+ *   elements apart, aligned to their elements; 1 <= vocab <= KDA_MAX_VOCAB;
+ *   tokens [n_tokens], accepted, next_tokens, state_slots [B], path [B,
+ *   KDA_TREE_MAX_DEPTH] int32; accept_uniforms [n_tokens], sample_uniforms
+ *   [B] FP32.
+ */
+int kda_draft_accept(const void *target, const void *draft, int probs_dtype,
+                     int64_t target_row_stride, int64_t draft_row_stride, int vocab,
+                     const int32_t *tokens, const int32_t *parents,
+                     const float *accept_uniforms, const float *sample_uniforms,
+                     const int32_t *state_slots, const int32_t *query_start_loc, int n_tokens,
+                     int32_t *accepted, int32_t *path, int32_t *next_tokens, int B, int Q,
+                     int null_slot, int32_t *status, void *stream);
+
+/*
+ * kda_tree_select -- the accepted path's nodes to the front of the request's
+ * records and convolution window, as if they had been verified as a chain.
+ * Per live request b with record row r >= 0, m = accepted[b] and i < m, for
+ * t_i = path[b, i] and every head h:
+ *   corr[r, h, i, :] = node_corr[t_i, h, :];
+ *   key_gate[r, h, i, 0:128] = k[t_i, h, :], [128:256] = raw_g[t_i, h, :];
+ * and with conv_state given, per channel, W = conv_state[slot, ch] and off
+ * from the pending count that kda_tree_conv saw:
+ *   m > 0: W <- [W[off + 1], W[off + 2], x[t_0, ch] .. x[t_{m-1}, ch]];
+ *   m = 0, or eager[b] != 0 (eager [B] uint8 or NULL: the rows that
+ *   kda_defer_commit will leave without a pending count): the last three of
+ *   [W[off], W[off + 1], W[off + 2], x[t_0, ch] .. x[t_{m-1}, ch]] become
+ *   entries 0 .. 2; later entries are kept.
+ * `pending` is only read; kda_defer_commit (with the accepted counts) makes
+ * the path the next replay.  Requests that are inert or without a record row
+ * are left alone.  A count outside 0 .. rq (with conv_state, conv_width - 2)
+ * or a path entry outside the window is reported (KDA_ERR_ARG) and its
+ * request left alone.
+ *   path [B, KDA_TREE_MAX_DEPTH], accepted [B] int32; k, raw_g BF16 and
+ *   node_corr FP32 [n_tokens, H, 128] as kda_tree_verify took and left them;
+ *   corr, key_gate, their strides, n_rows and rq as there; x, conv_state,
+ *   conv_slot_stride, conv_width and pending as in kda_tree_conv, x and
+ *   conv_state both NULL for records alone.
+ */
+int kda_tree_select(const int32_t *path, const int32_t *accepted, const uint8_t *eager,
+                    const kda_bf16 *k, const kda_bf16 *raw_g, const float *node_corr,
+                    const int32_t *state_slots, const int32_t *record_rows, const int32_t *pending, float *corr,
+                    kda_bf16 *key_gate, int64_t corr_row_stride, int64_t kg_row_stride,
+                    int n_rows, int rq, const kda_bf16 *x, kda_bf16 *conv_state,
+                    int64_t conv_slot_stride, int conv_width, int n_slots,
+                    const int32_t *query_start_loc, int n_tokens, int B, int H, int Q,
+                    int null_slot, int32_t *status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -17,13 +17,19 @@ from ._lib import (  # noqa: F401
     KDA_ERR_TIMEOUT,
     KDA_ERR_UNSUPPORTED,
     KDA_LAYER_STEP_NOALLOC_MAX_BYTES,
+    KDA_MAX_VOCAB,
     KDA_OK,
+    KDA_PROBS_BF16,
+    KDA_PROBS_F32,
     KDA_STATE_BF16,
     KDA_STATE_F32,
+    KDA_TREE_MAX_DEPTH,
+    KDA_TREE_MAX_NODES,
     KdaError,
     kda_check_status,
     kda_commit,
     kda_defer_commit,
+    kda_draft_accept,
     kda_flush_plan,
     kda_layer_epilogue,
     kda_layer_prologue,
@@ -38,6 +44,9 @@ from ._lib import (  # noqa: F401
     kda_replay_verify_layers,
     kda_selftest_wait_timeout,
     kda_slot_plan,
+    kda_tree_conv,
+    kda_tree_select,
+    kda_tree_verify,
     kda_verify,
     layer_tables,
     load,

@@ -26,6 +26,11 @@ KDA_ERR_SLOTS = -7
 KDA_LAYER_STEP_NOALLOC_MAX_BYTES = 16 * 1024 * 1024
 KDA_STATE_F32 = 0
 KDA_STATE_BF16 = 1
+KDA_PROBS_F32 = 0
+KDA_PROBS_BF16 = 1
+KDA_TREE_MAX_NODES = 64
+KDA_TREE_MAX_DEPTH = 8
+KDA_MAX_VOCAB = 1 << 20
 
 EXPORTS = ("kda_abi_version", "kda_error_string", "kda_check_status", "kda_verify",
            "kda_replay_verify", "kda_replay_verify_layers",
@@ -33,7 +38,8 @@ EXPORTS = ("kda_abi_version", "kda_error_string", "kda_check_status", "kda_verif
            "kda_layer_prologue", "kda_layer_epilogue", "kda_layer_step_workspace_bytes",
            "kda_layer_step", "kda_layer_step_noalloc", "kda_slot_plan", "kda_prefill_conv",
            "kda_prefill_workspace_bytes", "kda_prefill_workspace_bytes_for", "kda_prefill",
-           "kda_recurrent")
+           "kda_recurrent", "kda_tree_conv", "kda_tree_verify", "kda_draft_accept",
+           "kda_tree_select")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -74,6 +80,14 @@ _SIGS = {
                     + [_I, _I, _I, _I, _P, _P], _I),
     "kda_recurrent": ([_P] * 7 + [_F, _F, _P, _I, _I64, _I] + [_P] * 5 + [_I, _P]
                       + [_I, _I, _I, _I, _P, _P], _I),
+    "kda_tree_conv": ([_P] * 4 + [_I64, _I, _I, _P, _P, _P, _I, _P, _P, _I, _P, _P, _P]
+                      + [_I, _I, _I, _I, _P, _P], _I),
+    "kda_tree_verify": ([_P] * 7 + [_F, _F, _P, _I, _I64, _I, _P, _P, _P, _I, _P, _P, _P, _P,
+                                    _I64, _I64, _I, _I, _P, _P] + [_I, _I, _I, _I, _P, _P], _I),
+    "kda_draft_accept": ([_P, _P, _I, _I64, _I64, _I] + [_P] * 6 + [_I, _P, _P, _P]
+                         + [_I, _I, _I, _P, _P], _I),
+    "kda_tree_select": ([_P] * 11 + [_I64, _I64, _I, _I, _P, _P, _I64, _I, _I, _P, _I]
+                        + [_I, _I, _I, _I, _P, _P], _I),
 }
 
 _lib = None
@@ -642,3 +656,192 @@ def kda_recurrent(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, sources,
             _address(boundaries), _address(boundary_lens), _address(query_start_loc), T,
             out.data_ptr(), sources.shape[0], H, Q, null_slot, _address(status), st))
     return _check("kda_recurrent", rc, raise_on_error)
+
+
+# ---------------------------------------------------------------------------
+# trees of drafted tokens
+# ---------------------------------------------------------------------------
+
+def kda_tree_conv(x, conv_weight, conv_bias, conv_state, state_slots, parents, q, k, v, *, Q,
+                  record_rows=None, pending=None, query_start_loc=None, null_slot=0, status=None,
+                  stream=None, raise_on_error=True):
+    """The layer's convolution + SiLU over trees of drafted tokens: x
+    [T, 3*H*128] to q, k, v [T, H, 128], each node behind its own ancestors
+    (``parents`` [T], within the request, -1 above a root; None: chains) and
+    the windows of conv_state [slots, 3*H*128, width] (read only), whose live
+    entries the pending counts tell.  Q: at least the largest tree;
+    query_start_loc None: trees of Q nodes."""
+    import torch
+    bf, i32, dev = torch.bfloat16, torch.int32, x.device
+    T, H, _ = q.shape
+    D, B = H * 128, state_slots.shape[0]
+    per, heads = (B,), (T, H, 128)
+    _expect_tensors(dev, ("x", x, bf, (T, 3 * D)), ("conv_weight", conv_weight, bf, (3, 4, D)),
+                    ("conv_bias", conv_bias, bf, (3 * D,)), ("q", q, bf, heads),
+                    ("k", k, bf, heads), ("v", v, bf, heads),
+                    ("state_slots", state_slots, i32, per), ("parents", parents, i32, (T,)),
+                    ("record_rows", record_rows, i32, per),
+                    ("query_start_loc", query_start_loc, i32, (B + 1,)),
+                    ("status", status, i32, (1,)))
+    n_rows = 0
+    if pending is not None:
+        n_rows = pending.shape[0]
+        _expect_tensors(dev, ("pending", pending, i32, (n_rows,)))
+    _expect_rows(dev, "conv_state", conv_state, bf, (3 * D, None))
+    rc = _call_on(dev, stream, lambda st: load().kda_tree_conv(
+            x.data_ptr(), conv_weight.data_ptr(), _address(conv_bias), conv_state.data_ptr(),
+            _row_stride(conv_state, 3 * D * conv_state.shape[2]), conv_state.shape[2],
+            conv_state.shape[0], state_slots.data_ptr(), _address(record_rows),
+            _address(pending), n_rows, _address(parents), _address(query_start_loc), T,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, Q, null_slot, _address(status), st))
+    return _check("kda_tree_conv", rc, raise_on_error)
+
+
+def _expect_records(dev, corr, key_gate, H):
+    """Record rows: corr [rows, H, rq, 128], key_gate [rows, H, rq, 256]; the
+    rows' strides."""
+    import torch
+    rq = corr.shape[2] if corr.dim() == 4 else 0
+    _expect_rows(dev, "corr", corr, torch.float32, (H, rq, 128))
+    _expect_rows(dev, "key_gate", key_gate, torch.bfloat16, (H, rq, 256))
+    if key_gate.shape[0] != corr.shape[0]:
+        raise ValueError(f"key_gate must have {corr.shape[0]} rows, got {key_gate.shape[0]}")
+    return _row_stride(corr, H * rq * 128), _row_stride(key_gate, H * rq * 256)
+
+
+def kda_tree_verify(q, k, v, raw_g, raw_beta, A_log, dt_bias, state_pool, state_slots, parents,
+                    node_corr, out, *, Q, lower_bound, q_scale, record_rows=None, pending=None,
+                    corr=None, key_gate=None, query_start_loc=None, null_slot=0, status=None,
+                    stream=None, raise_on_error=True):
+    """The delta rule over trees of drafted tokens: q, k, v, raw_g, out
+    [T, H, 128], raw_beta [T, H] BF16, every node from the state behind its
+    ancestors (``parents`` as in kda_tree_conv), starting from the request's
+    page of state_pool [slots, H, 128, 128]; node_corr [T, H, 128] FP32 takes
+    the nodes' corrections.  With ``pending`` [rows], corr and key_gate (a
+    float32 pool) the pending replay of a request's record row is folded into
+    its page first; without, the pool (float32 or bfloat16) is only read."""
+    import torch
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, q.device
+    T, H, _ = q.shape
+    B = state_slots.shape[0]
+    per, heads = (B,), (T, H, 128)
+    dtype = state_pool.dtype
+    if dtype != f32 and dtype != bf:
+        raise TypeError("state_pool must be float32 or bfloat16")
+    _expect_tensors(dev, ("q", q, bf, heads), ("k", k, bf, heads), ("v", v, bf, heads),
+                    ("raw_g", raw_g, bf, heads), ("out", out, bf, heads),
+                    ("node_corr", node_corr, f32, heads), ("raw_beta", raw_beta, bf, (T, H)),
+                    ("A_log", A_log, f32, (H,)), ("dt_bias", dt_bias, f32, (H, 128)),
+                    ("state_slots", state_slots, i32, per), ("parents", parents, i32, (T,)),
+                    ("record_rows", record_rows, i32, per),
+                    ("query_start_loc", query_start_loc, i32, (B + 1,)),
+                    ("status", status, i32, (1,)))
+    _expect_rows(dev, "state_pool", state_pool, dtype, (H, 128, 128))
+    if (pending is None) != (corr is None) or (corr is None) != (key_gate is None):
+        raise ValueError("pending, corr and key_gate come together")
+    n_rows = rq = corr_stride = kg_stride = 0
+    if pending is not None:
+        corr_stride, kg_stride = _expect_records(dev, corr, key_gate, H)
+        n_rows, rq = corr.shape[0], corr.shape[2]
+        _expect_tensors(dev, ("pending", pending, i32, (n_rows,)))
+    rc = _call_on(dev, stream, lambda st: load().kda_tree_verify(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), raw_g.data_ptr(), raw_beta.data_ptr(),
+            A_log.data_ptr(), dt_bias.data_ptr(), lower_bound, q_scale, state_pool.data_ptr(),
+            KDA_STATE_F32 if dtype == f32 else KDA_STATE_BF16,
+            _row_stride(state_pool, H * 128 * 128), state_pool.shape[0], state_slots.data_ptr(),
+            _address(parents), _address(query_start_loc), T, _address(record_rows),
+            _address(pending), _address(corr), _address(key_gate), corr_stride, kg_stride, n_rows,
+            rq, node_corr.data_ptr(), out.data_ptr(), B, H, Q, null_slot, _address(status), st))
+    return _check("kda_tree_verify", rc, raise_on_error)
+
+
+def kda_draft_accept(target_probs, tokens, accept_uniforms, sample_uniforms, accepted, path,
+                     next_tokens, *, Q, draft_probs=None, parents=None, state_slots=None,
+                     query_start_loc=None, null_slot=0, status=None, stream=None,
+                     raise_on_error=True):
+    """Drafted ``tokens`` [T] against the target's next-token probabilities
+    target_probs [T, vocab] (float32 or bfloat16, rows of any stride), from
+    uniform numbers accept_uniforms [T] (one a node, for its children) and
+    sample_uniforms [B] in [0, 1).  Chains with draft_probs [T, vocab] (what
+    each token was drawn from), or trees (``parents``) and chains of drafts
+    that were taken for sure.  Out, int32: accepted [B] (tokens of the path,
+    the root among them), path [B, 8] (its nodes, -1 behind), next_tokens [B]
+    (drawn from the target after the path).  The rules are in
+    include/kda_recoverssm.h."""
+    import torch
+    f32, i32, dev = torch.float32, torch.int32, target_probs.device
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must have shape (tokens, vocab)")
+    T, V = target_probs.shape
+    B = sample_uniforms.shape[0]
+    dtype, per = target_probs.dtype, (B,)
+    if dtype != f32 and dtype != torch.bfloat16:
+        raise TypeError("target_probs must be float32 or bfloat16")
+    if draft_probs is not None and parents is not None:
+        raise ValueError("draft_probs go with chains: parents must be None")
+    _expect_tensors(dev, ("tokens", tokens, i32, (T,)),
+                    ("accept_uniforms", accept_uniforms, f32, (T,)),
+                    ("sample_uniforms", sample_uniforms, f32, per),
+                    ("accepted", accepted, i32, per), ("path", path, i32, (B, KDA_TREE_MAX_DEPTH)),
+                    ("next_tokens", next_tokens, i32, per), ("parents", parents, i32, (T,)),
+                    ("state_slots", state_slots, i32, per),
+                    ("query_start_loc", query_start_loc, i32, (B + 1,)),
+                    ("status", status, i32, (1,)))
+    _expect_rows(dev, "target_probs", target_probs, dtype, (V,))
+    draft_stride = 0
+    if draft_probs is not None:
+        _expect_rows(dev, "draft_probs", draft_probs, dtype, (V,))
+        if draft_probs.shape[0] != T:
+            raise ValueError(f"draft_probs must have {T} rows, got {draft_probs.shape[0]}")
+        draft_stride = _row_stride(draft_probs, V)
+    rc = _call_on(dev, stream, lambda st: load().kda_draft_accept(
+            target_probs.data_ptr(), _address(draft_probs),
+            KDA_PROBS_F32 if dtype == f32 else KDA_PROBS_BF16, _row_stride(target_probs, V),
+            draft_stride, V, tokens.data_ptr(), _address(parents), accept_uniforms.data_ptr(),
+            sample_uniforms.data_ptr(), _address(state_slots), _address(query_start_loc), T,
+            accepted.data_ptr(), path.data_ptr(), next_tokens.data_ptr(), B, Q, null_slot,
+            _address(status), st))
+    return _check("kda_draft_accept", rc, raise_on_error)
+
+
+def kda_tree_select(path, accepted, k, raw_g, node_corr, state_slots, record_rows, corr, key_gate,
+                    *, Q, x=None, conv_state=None, pending=None, eager=None, query_start_loc=None,
+                    null_slot=0, status=None, stream=None, raise_on_error=True):
+    """The accepted paths (``path`` [B, 8] and ``accepted`` [B], as
+    kda_draft_accept leaves them) to the front of the requests' records: the
+    nodes' corrections, keys and raw gates to corr [rows, H, rq, 128] and
+    key_gate [rows, H, rq, 256]; with x [T, 3*H*128] and conv_state
+    [slots, 3*H*128, width] (and ``pending`` as kda_tree_conv had it), the
+    path's inputs to the convolution windows as well.  kda_defer_commit then
+    makes the path the pending replay; rows that it will leave without one,
+    being committed at once, are marked in ``eager`` (uint8 [B])."""
+    import torch
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, k.device
+    T, H, _ = k.shape
+    D, B = H * 128, state_slots.shape[0]
+    per, heads = (B,), (T, H, 128)
+    if (x is None) != (conv_state is None):
+        raise ValueError("x and conv_state come together")
+    _expect_tensors(dev, ("path", path, i32, (B, KDA_TREE_MAX_DEPTH)),
+                    ("accepted", accepted, i32, per), ("eager", eager, torch.uint8, per),
+                    ("k", k, bf, heads),
+                    ("raw_g", raw_g, bf, heads), ("node_corr", node_corr, f32, heads),
+                    ("state_slots", state_slots, i32, per),
+                    ("record_rows", record_rows, i32, per), ("x", x, bf, (T, 3 * D)),
+                    ("query_start_loc", query_start_loc, i32, (B + 1,)),
+                    ("status", status, i32, (1,)))
+    corr_stride, kg_stride = _expect_records(dev, corr, key_gate, H)
+    n_rows = corr.shape[0]
+    _expect_tensors(dev, ("pending", pending, i32, (n_rows,)))
+    n_slots, slot_stride, width = 0x7fffffff, 0, 0
+    if conv_state is not None:
+        _expect_rows(dev, "conv_state", conv_state, bf, (3 * D, None))
+        n_slots, width = conv_state.shape[0], conv_state.shape[2]
+        slot_stride = _row_stride(conv_state, 3 * D * width)
+    rc = _call_on(dev, stream, lambda st: load().kda_tree_select(
+            path.data_ptr(), accepted.data_ptr(), _address(eager), k.data_ptr(),
+            raw_g.data_ptr(), node_corr.data_ptr(), state_slots.data_ptr(),
+            _address(record_rows), _address(pending), corr.data_ptr(), key_gate.data_ptr(), corr_stride, kg_stride,
+            n_rows, corr.shape[2], _address(x), _address(conv_state), slot_stride, width, n_slots,
+            _address(query_start_loc), T, B, H, Q, null_slot, _address(status), st))
+    return _check("kda_tree_select", rc, raise_on_error)

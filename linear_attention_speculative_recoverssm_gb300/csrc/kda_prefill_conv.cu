@@ -19,6 +19,7 @@
 #include "../../include/kda_recoverssm.h"
 #include "kda_launch.h"
 #include "kda_prompt.cuh"
+#include "kda_silu.cuh"
 
 namespace kda {
 namespace {
@@ -52,20 +53,6 @@ __device__ __forceinline__ int find_request(const int32_t *qsl, int B, int t, in
     hi = end < hi ? end : hi;
   }
   return lo;
-}
-
-// z / (1 + 2^(-z log2 e)), the two functions of the special unit once each
-// (the reciprocal is flushed from 2^126 on, as in kda_layer_prologue's: below
-// z = -87.3, where silu is under 2^-119 in size, it is -0)
-__device__ __forceinline__ float2 silu2(float2 z) {
-  const float2 t = fmul2(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-  float2 e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-  e = __fadd2_rn(e, make_float2(1.f, 1.f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
-  return fmul2(z, r);
 }
 
 struct Four {
@@ -127,11 +114,6 @@ struct Windows {
     set(3 * W + i, x.y >> 16);
   }
 };
-
-__device__ __forceinline__ uint32_t silu_pair(float2 z) {
-  const __nv_bfloat162 r = __float22bfloat162_rn(silu2(z));
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
 
 template <int W>
 __global__ void __launch_bounds__(kPcThreads, 6) kda_prefill_conv_kernel(const ConvParams p) {

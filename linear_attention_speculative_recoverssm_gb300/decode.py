@@ -17,6 +17,9 @@ steps can be captured in a CUDA graph.
   the pending replays were just folded in by ``flush``;
 * ``accept``: the accepted counts become the pending replays (defer); rows
   marked eager are committed at once from the records this step wrote;
+* ``verify_tree`` and ``accept_tree``: the same two for a tree of drafted
+  tokens in place of a chain (any step may be either); kda_draft_accept makes
+  the accepted path from the target's probabilities between them;
 * ``flush``: every pending replay is folded into its checkpoint in place
   (flush plan + commit); the next ``verify`` is then the stock one, because
   the plan leaves the pending counts as they are.
@@ -24,7 +27,8 @@ steps can be captured in a CUDA graph.
 from __future__ import annotations
 
 from ._lib import (KDA_STATE_F32, kda_commit, kda_defer_commit, kda_flush_plan,
-                   kda_prefill, kda_replay_verify, kda_verify, layer_tables)
+                   kda_prefill, kda_replay_verify, kda_tree_select, kda_tree_verify, kda_verify,
+                   layer_tables)
 
 
 class DeferredRecoverSSM:
@@ -144,6 +148,33 @@ class DeferredRecoverSSM:
         if eager is not None:
             self._commit(accepted, self.state_slots)
         self.flushed = False
+
+    def verify_tree(self, q, k, v, raw_g, raw_beta, parents, node_corr, out, *, Q,
+                    query_start_loc=None):
+        """Verify this step's trees of up to Q drafted tokens (q, k, v, raw_g,
+        out BF16 [T, H, 128], raw_beta BF16 [T, H], parents int32 [T]; T =
+        B*Q, or packed by query_start_loc [B + 1]), every node from the state
+        behind its ancestors.  node_corr FP32 [T, H, 128] takes the nodes'
+        corrections, for ``accept_tree``; the records are not written."""
+        replay = {} if self.flushed else dict(pending=self.pending, corr=self.corr,
+                                              key_gate=self.key_gate)
+        kda_tree_verify(q, k, v, raw_g, raw_beta, self.A_log, self.dt_bias, self.state_pool,
+                        self.state_slots, parents, node_corr, out, Q=Q,
+                        lower_bound=self.lower_bound, q_scale=self.q_scale,
+                        record_rows=self.record_rows, query_start_loc=query_start_loc,
+                        null_slot=self.null_slot, status=self.status, stream=self.stream, **replay)
+
+    def accept_tree(self, path, accepted, k, raw_g, node_corr, *, Q, query_start_loc=None, x=None,
+                    conv_state=None, eager=None):
+        """After sampling from a tree: the accepted paths (path int32 [B, 8],
+        accepted int32 [B], overwritten as in ``accept``) move to the front
+        of the records, and with x and conv_state their inputs to the layer's
+        convolution windows; then as ``accept``."""
+        kda_tree_select(path, accepted, k, raw_g, node_corr, self.state_slots, self.record_rows,
+                        self.corr, self.key_gate, Q=Q, x=x, conv_state=conv_state,
+                        pending=self.pending, eager=eager, query_start_loc=query_start_loc,
+                        null_slot=self.null_slot, status=self.status, stream=self.stream)
+        self.accept(accepted, eager)
 
     def flush(self):
         """Fold every pending replay into its checkpoint, in place."""
