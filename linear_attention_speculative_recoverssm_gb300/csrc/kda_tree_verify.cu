@@ -282,5 +282,5 @@ extern "C" int kda_tree_verify(
   const long long items = (long long)B * H;
   if (items * 4 <= sms)
     return bf16 ? kda::launch_rows<32, true>(p, st) : kda::launch_rows<32, false>(p, st);
-  return bf16 ? kda::launch_rows<128, true>(p, st) : kda::launch_rows<128, false>(p, st);
+  return kda::launch_tree_mma(p, bf16, sms, st);
 }

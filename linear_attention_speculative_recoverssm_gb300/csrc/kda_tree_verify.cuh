@@ -12,6 +12,8 @@
 // they hold, are never met.
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include "kda_tree.cuh"
 
 namespace kda {
@@ -30,6 +32,9 @@ struct TreeVerifyParams {
   uint16_t *out;
   int H;
 };
+
+// The variant on the tensor cores (kda_tree_verify_mma.cu).
+int launch_tree_mma(const TreeVerifyParams &p, bool bf16, int sms, cudaStream_t stream);
 
 // Coefficients of a node, in shared memory: A[0 .. 6], B[0 .. 6], B_self, beta.
 constexpr int kTreeCoefs = 16;

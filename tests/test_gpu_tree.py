@@ -78,17 +78,18 @@ SHAPES = {
 }
 
 
-@pytest.mark.parametrize("H", [1, 3])
+@pytest.mark.parametrize("H", [1, 3, 40])
 @pytest.mark.parametrize("shape", SHAPES)
 def test_verify_shapes(shape, H):
     case = tt.tree_case(SHAPES[shape], H, seed=3, tail=2)
     check_verify(case, run_verify(case))
 
 
+@pytest.mark.parametrize("H", [2, 41])
 @pytest.mark.parametrize("pool,replay", [("f32", False), ("bf16", False)])
 @pytest.mark.parametrize("shape", ["one", "combs", "random", "forests"])
-def test_verify_reads_the_pool(shape, pool, replay):
-    case = tt.tree_case(SHAPES[shape], 2, seed=4, pool=pool, replay=replay)
+def test_verify_reads_the_pool(shape, pool, replay, H):
+    case = tt.tree_case(SHAPES[shape], H, seed=4, pool=pool, replay=replay)
     check_verify(case, run_verify(case))
 
 
