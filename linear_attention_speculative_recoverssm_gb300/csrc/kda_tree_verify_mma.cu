@@ -1,33 +1,46 @@
-// The delta rule over trees on the tensor cores: two CTAs an SM, each taking
+// The delta rule over trees on the tensor cores: persistent CTAs, each taking
 // (request, head) items one after the other.
 //
-// Per item, S the state page after its replay and X_k, X_q the nodes' vectors:
-//   [w; y] = S [X_k; X_q]^T             (tcgen05: M = 128 rows of the page,
-//                                        N = two columns a node, K = 128)
+// Per item, S the state page after its replay, G_t the product of the decays
+// down the path to node t:
+//   X = [G_t kn_t; G_t qn_t], Y = [kn_s / G_s]    (two rows a node, and one)
+//   P = X Y^T                  the products of t's key and query with its
+//                              ancestors' keys, decayed from one to the other
+//   [w y] = S X^T              (M = 128 rows of the page)
 //   R_s = v_s - w_s
-//   u_t = sum_s T[t][s] R_s, o_t = y_t + sum_s C[t][s] R_s
-// s over t and its ancestors, where T inverts u_t = beta_t (R_t - sum A u) and
-// C is B T: at most eight terms a node, none of which waits for another.
+//   [u o] = R [T; C]^T + [0 y]
+// where T inverts u_t = beta_t (R_t - sum_s P_ts u_s) and C = P_q T: at most
+// eight entries a row, at the node and its ancestors.  A path holds at most
+// eight decays, each within e^-10 .. e^10, so that 1 / G stays inside FP32.
+// Of P only the entries of ancestors are looked at.
 //
 // Operands are BF16 in three parts (24 bits): x = hi + mid + lo, six products
 // of parts whose sizes are above 2^-24 of the first's (a BF16 page is its own
 // only part: three products).  FP32's exponents, so that no scale is needed.
-// TF32 in two parts costs the same tensor time for 22 bits, and twice the
-// columns of tensor memory.
+// TF32 in two parts costs the same tensor time for 22 bits, and more of tensor
+// memory.  (Where a channel's G is within 2^16 of FP32's ends, its last part
+// underflows: 16 bits of it are left.)
 //
 // The page goes from HBM to registers in the layout of tcgen05.st's 16x256b
 // (16 bytes a lane, four lanes to 64 bytes of a row), is replayed there,
 // written back from there, split there, and stored to tensor memory as the
 // A operand: it never passes through shared memory, which holds the nodes.
-// While an item is worked on, the next one's page and operands are fetched to
-// L2; the two CTAs of an SM cover each other's waits.
+// R goes the same way.
 //
-// Per group of up to G nodes the warps (1) walk up the nodes' paths, writing
-// X in parts and the coefficients A, B; (2) one thread issues the products,
-// and meanwhile warp 0 makes T and C; (3) R and y go from tensor memory to
-// shared memory, a thread a row; (4) u and o, a warp a node.  A node's
-// ancestors are in its group or in an earlier one.
+// R and [T; C] are multiplied whole, and zero times NaN is NaN: an R that is
+// not finite is left out as zero, and the outputs of its node and of those
+// below it are made NaN at the end (nothing is looked at where all are finite).
+//
+// One CTA an SM, whose warps divide the work by its kind and run one behind
+// the other, some items apart, as barriers in shared memory let them: the
+// requests (validated, their paths listed) a warp; nodes to X and Y; pages; T
+// and C; R and the outputs; and two warps that issue the products, of X and
+// of R.  One phase after the other by all warps, two CTAs an SM, took 2.4
+// times as long: each phase is a chain of latencies (shared memory, the
+// shuffles of a norm, a product's hand-off) that more warps do not shorten.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "kda_launch.h"
 #include "kda_tcgen05.cuh"
@@ -36,12 +49,9 @@
 namespace kda {
 namespace {
 
-constexpr int kTmThreads = 256;
-constexpr int kTmWarps = kTmThreads / 32;
-constexpr uint32_t kTmCols = 256;     // of tensor memory, a CTA
 constexpr uint32_t kTmPartCols = kDim / 2;  // of one part of the page: two keys a column
-constexpr uint32_t kTmD = 3 * kTmPartCols;  // the products
-constexpr int kPath = kTreeDepth;           // T and C: t itself and its ancestors
+constexpr uint32_t kTmD = 3 * kTmPartCols;  // w, then u; y, then o
+constexpr int kPath = kTreeDepth;           // a node and its ancestors
 
 // Instruction descriptor of kind::f16: FP32 accumulator, A and B BF16, both
 // K-major, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
@@ -60,9 +70,9 @@ __device__ __forceinline__ uint32_t tm_elect() {
   return p;
 }
 
-// D[tmem] (+)= A[tmem, 128 x 16] . B[N x 16]^T, issued by the lane with
-// `lead` while its warp runs along (the operands then live in uniform
-// registers).
+// D[tmem] (+)= A[128 x 16] . B[N x 16]^T, A in tensor memory or in shared
+// memory, issued by the lane with `lead` while its warp runs along (the
+// operands then live in uniform registers).
 __device__ __forceinline__ void tm_mma(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
                                        bool accumulate, uint32_t lead) {
   asm volatile(
@@ -73,522 +83,837 @@ __device__ __forceinline__ void tm_mma(uint32_t d, uint32_t a, uint64_t bdesc, u
       "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
       : "memory");
 }
-
-// 16 lanes (from taddr's), 32 columns: a thread's registers 4 j .. 4 j + 3 are
-// columns 8 j + 2 (lane % 4) + 0, 1 of row lane / 4, then of row lane / 4 + 8.
-__device__ __forceinline__ void tm_store_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tm_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, bool accumulate, uint32_t lead) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
       : "memory");
 }
 
-// 4 columns of this warp's 32 lanes, a lane a thread (no wait).
-__device__ __forceinline__ void tm_load4(uint32_t taddr, float (&r)[4]) {
-  uint32_t x[4];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-               : "r"(taddr)
+// 16 lanes (from taddr's), 16 columns: a thread's registers 4 j .. 4 j + 3 are
+// columns 8 j + 2 (lane % 4) + 0, 1 of row lane / 4, then of row lane / 4 + 8.
+__device__ __forceinline__ void tm_store_16x16(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// 4 columns of this warp's 32 lanes, a lane a thread.
+__device__ __forceinline__ void tm_store_32x4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c,
+                                              uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
+}
+
+__device__ __forceinline__ void tm_store_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 16 or 8 columns of this warp's 32 lanes, a lane a thread (no wait).
+__device__ __forceinline__ void tm_load(uint32_t taddr, float (&r)[16]) {
+  uint32_t x[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+        "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]),
+        "=r"(x[14]), "=r"(x[15])
+      : "r"(taddr)
+      : "memory");
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = __uint_as_float(x[i]);
+  for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(x[i]);
+}
+__device__ __forceinline__ void tm_load(uint32_t taddr, float (&r)[8]) {
+  uint32_t x[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+        "=r"(x[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(x[i]);
+}
+__device__ __forceinline__ void tm_load_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void prefetch_l2(const void *at) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
 }
 
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // A pair's next part: BF16 of both (returned packed), the rest left in them.
 __device__ __forceinline__ uint32_t take_part(float2 &x) {
   uint32_t w;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(x.y), "f"(x.x));
-  x.x -= __uint_as_float(w << 16);
-  x.y -= __uint_as_float(w & 0xffff0000u);
+  x = __fadd2_rn(x, make_float2(-__uint_as_float(w << 16), -__uint_as_float(w & 0xffff0000u)));
   return w;
 }
 
-// NC: nodes of the largest window; G: nodes of a group.
-template <int NC, int G>
+// A request as its warp hands it to the others: heads h0 .. h1 - 1 of it are this
+// CTA's.  n < 0: there is none any more.
+struct TreeTask {
+  int t0, n, slot, row, pending, h0, h1;
+  // per node the number of its ancestors, then they, the nearest first, a byte
+  // each; the node itself where there are no more
+  uint2 path[kTreeNodes];
+};
+
+// Between the groups of warps: `full` when what it names is there, `free` when
+// its place may be written again.
+struct TreeBars {
+  uint64_t task_full[4], task_free[4];
+  uint64_t x_full, x_free, y_free;  // X and Y
+  uint64_t p_full, p_free;          // P in tensor memory
+  uint64_t a_full, a_free;          // the page's parts
+  uint64_t d_full[2], d_free[2];    // w and y, until o is out
+  uint64_t t_full, t_free;          // [T; C]
+  uint64_t r_full, o_full;          // R's parts; u and o
+  uint64_t done[2];                 // every product that a warp issued
+};
+
+// NC: nodes of the largest window.
+template <int NC>
 struct TreeMma {
-  static constexpr uint32_t kBlock = 2 * G * 128;  // 64 keys of a part of X: rows of 128 bytes
-  static constexpr uint32_t kPart = 2 * kBlock;
-  // byte offsets of dynamic shared memory, from a 1024-byte boundary
+  // warps: pages (two to a quarter of the rows), R and outputs, T and C (a lane
+  // a row of P), the two that issue, the one with the requests, nodes
+  static constexpr int kPageWarps = 8, kRWarps = 4, kTWarps = 2 * NC / 32,
+                       kNodeWarps = NC <= 32 ? 7 : 8;
+  static constexpr int kR0 = kPageWarps, kT0 = kR0 + kRWarps, kIssue0 = kT0 + kTWarps,
+                       kTask0 = kIssue0 + 2, kNode0 = kTask0 + 1, kWarps = kNode0 + kNodeWarps;
+  static_assert(kR0 % 4 == 0 && kT0 % 4 == 0, "a warp reaches the tensor memory lanes of its number");
+  static constexpr int kThreads = 32 * kWarps;
+  // tensor memory: the page, w and y (twice where there is room), P, R
+  static constexpr int kDBufs = NC <= 32 ? 2 : 1;
+  static constexpr uint32_t kTmP = kTmD + kDBufs * 2 * NC, kTmR = kTmP + NC;
+  static_assert(kTmR + 3 * NC / 2 <= 512, "tensor memory");
+  // tiles of 128-byte rows (64 keys of a part), 128-byte swizzled
+  static constexpr uint32_t kXBlock = 2 * NC * 128, kXPart = 2 * kXBlock;
+  static constexpr uint32_t kYBlock = NC * 128, kYPart = 2 * kYBlock;
+  static constexpr uint32_t kTCPart = 2 * NC * 128;  // [T; C], NC columns of a row used
+  // Byte offsets of dynamic shared memory, 1024-byte aligned.  Of trees of more
+  // than 32 nodes P and then [T; C] stand where Y was, which is free again when
+  // u and o are there; of smaller ones they have places of their own.
+  static constexpr bool kOverY = NC > 32;
   static constexpr uint32_t kX = 0;
-  static constexpr uint32_t kD = kX + 3 * kPart;         // decays [NC][128] FP32
-  static constexpr uint32_t kK = kD + NC * kDim * 4;     // keys [NC][128] BF16
-  static constexpr uint32_t kR = kK + NC * kDim * 2;     // R of all groups but the last
-  static constexpr uint32_t kCoef = kR + (NC - G) * kDim * 4;
-  static constexpr uint32_t kTC = kCoef + NC * kTreeCoefs * 4;  // T[8], C[8] of a node
-  static constexpr uint32_t kNorm = kTC + NC * 2 * kPath * 4;
-  static constexpr uint32_t kAnc = kNorm + NC * 4;  // depth, then the ancestors, a byte each
-  static constexpr uint32_t kParent = kAnc + kTreeNodes * 8;
-  static constexpr uint32_t kBar = kParent + kTreeNodes;
-  static constexpr uint32_t kEnd = kBar + 32;
-  // (two CTAs an SM, and no third, whose tensor memory would not be there)
-  static constexpr uint32_t kBytes = kEnd + 1024 > 78 * 1024 ? kEnd + 1024 : 78 * 1024;
-  static_assert(kBytes <= 113 * 1024, "two CTAs an SM");
-  // the replay's operands stand where X comes later; y and the last group's R
-  // where X was
-  static constexpr uint32_t kReplayK = kX, kReplayD = kReplayK + kMaxQ * kDim * 4,
-                            kReplayU = kReplayD + kMaxQ * kDim * 4,
-                            kReplayDn = kReplayU + kMaxQ * kDim * 4;
-  static_assert(kReplayDn + kDim * 4 <= kD, "the replay's operands in X");
-  static_assert(2 * G * kDim * 4 <= 3 * kPart, "y and R in X");
+  static constexpr uint32_t kY = kX + 3 * kXPart;
+  static constexpr uint32_t kTC = kOverY ? kY : kY + 3 * kYPart;
+  // P, [2 NC][NC] FP32, column c of row r at c ^ (r & 31)
+  static constexpr uint32_t kP = kOverY ? kY : kTC + 3 * kTCPart;
+  static_assert(!kOverY || (3 * kTCPart <= 3 * kYPart && 2 * NC * NC * 4 <= 3 * kYPart), "over Y");
+  // decays [NC][128] FP32; a row's raw gates arrive in its first half
+  static constexpr uint32_t kD = kOverY ? kY + 3 * kYPart : kP + 2 * NC * NC * 4;
+  static constexpr uint32_t kK = kD + NC * kDim * 4;  // keys and queries [NC][128] BF16
+  static constexpr uint32_t kQ = kK + NC * kDim * 2;
+  static constexpr uint32_t kReplayK = kQ + NC * kDim * 2;  // the replay's operands
+  static constexpr uint32_t kReplayD = kReplayK + kMaxQ * kDim * 4;
+  static constexpr uint32_t kReplayU = kReplayD + kMaxQ * kDim * 4;
+  static constexpr uint32_t kReplayDn = kReplayU + kMaxQ * kDim * 4;
+  static constexpr uint32_t kDt = kReplayDn + kDim * 4;  // dt_bias of the head
+  // per node: P with its ancestors' keys, the nearest's first, and beta
+  static constexpr uint32_t kA = kDt + kDim * 4;
+  static constexpr uint32_t kNorms = kA + NC * kPath * 4;  // of keys, then of queries
+  static constexpr uint32_t kBad = kNorms + 2 * NC * 4;    // [NC / 8][128] nodes, a byte's bits
+  static constexpr uint32_t kTasks = kBad + NC / 8 * kDim;
+  static constexpr uint32_t kParent = kTasks + 4 * sizeof(TreeTask);
+  static constexpr uint32_t kBars = kParent + kTreeNodes;
+  static constexpr uint32_t kSlot = kBars + sizeof(TreeBars);
+  static constexpr uint32_t kBytes = kSlot + 8;
+  static_assert(kTasks % 8 == 0 && kBars % 8 == 0 && sizeof(TreeTask) % 8 == 0, "alignment");
+  static_assert(kBytes <= 227 * 1024 && 2 * kBytes > 228 * 1024, "one CTA an SM");
 };
 
 // A page's part of a thread: rows 16 rh + lane / 4 + 8 i of the warp's 32,
-// keys 16 j + 4 (lane % 4) + 0 .. 3 of the warp's 64.
+// keys 16 j + 4 (lane % 4) + 0 .. 3 of the warp's 16 J; one rh at a time.
+template <bool BF16, int J>
 struct PageRegs {
-  float4 s[2][4][2];  // [rh][j][i]
+  using Four = typename std::conditional<BF16, uint2, float4>::type;
+  Four s[J][2];  // [j][i]
+  __device__ __forceinline__ void load(const void *pool, long long at) {
+    const auto *from = reinterpret_cast<const Four *>(static_cast<const char *>(pool) + at * (BF16 ? 2 : 4));
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[j][i] = __ldcs(from + (8 * i * kDim + 16 * j) / 4);
+  }
 };
 
-template <int NC, int G, bool BF16>
-__global__ void __launch_bounds__(kTmThreads, 2) kda_tree_mma_kernel(const TreeVerifyParams p,
-                                                                    int n_items) {
-  using L = TreeMma<NC, G>;
-  extern __shared__ uint8_t raw[];
-  uint8_t *mem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  float *decay = reinterpret_cast<float *>(mem + L::kD);
-  uint16_t *keys = reinterpret_cast<uint16_t *>(mem + L::kK);
-  float *coefs = reinterpret_cast<float *>(mem + L::kCoef);
-  float *tc = reinterpret_cast<float *>(mem + L::kTC);
-  float *norms = reinterpret_cast<float *>(mem + L::kNorm);
-  uint8_t *anc = mem + L::kAnc;
-  int8_t *parent = reinterpret_cast<int8_t *>(mem + L::kParent);
-  uint64_t *bar = reinterpret_cast<uint64_t *>(mem + L::kBar);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mem + L::kBar + 8);
-  int *good = reinterpret_cast<int *>(mem + L::kBar + 16);
+// Swizzled place of channels 4 lane .. 4 lane + 3 of a tile's row.
+__device__ __forceinline__ uint32_t tile_place(int row, int lane, uint32_t block) {
+  return (uint32_t)(lane >> 4) * block + row * 128 + ((((lane & 15) >> 1) ^ (row & 7)) << 4) +
+         (lane & 1) * 8;
+}
+
+__device__ __forceinline__ void store_parts(uint8_t *to, uint32_t part, float4 x) {
+  float2 lo = make_float2(x.x, x.y), hi = make_float2(x.z, x.w);
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    const uint32_t c = take_part(lo);
+    *reinterpret_cast<uint2 *>(to + e * part) = make_uint2(c, take_part(hi));
+  }
+}
+
+// j-th byte of a node's path.
+__device__ __forceinline__ int path_byte(uint2 path, int j) {
+  return ((j < 4 ? path.x : path.y) >> (8 * (j & 3))) & 0xff;
+}
+
+// A warp's way through the CTA's items.  A group of warps that has a barrier of
+// its own agrees there, item by item, that no wait of any has run out.
+struct TreeItems {
+  const TreeTask *tasks;
+  TreeBars *bars;
+  int seq, t0, n, slot, row, pending, h, h1;
+  bool ok;  // no wait has run out
+
+  __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity)) && ok;
+    return ok;
+  }
+  // The next task; false where there is none.
+  __device__ __forceinline__ bool load() {
+    if (!wait(&bars->task_full[seq & 3], (uint32_t)(seq >> 2) & 1u)) return false;
+    const TreeTask &t = tasks[seq & 3];
+    t0 = t.t0, n = t.n, slot = t.slot, row = t.row, pending = t.pending, h = t.h0, h1 = t.h1;
+    return n >= 0;
+  }
+  __device__ __forceinline__ bool start(const TreeTask *ts, TreeBars *bs) {
+    tasks = ts, bars = bs, seq = 0, ok = true;
+    return load();
+  }
+  // The next item; hands a task's place back behind its last one.
+  __device__ __forceinline__ bool next(int lane) {
+    if (++h < h1) return true;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->task_free[seq & 3]);
+    ++seq;
+    return load();
+  }
+  __device__ __forceinline__ const uint2 *paths() const { return tasks[seq & 3].path; }
+};
+
+template <int NC, bool BF16>
+__global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
+    kda_tree_mma_kernel(const TreeVerifyParams p, int n_items) {
+  using L = TreeMma<NC>;
+  // (its alignment known, the addresses below are constants, which take no
+  // registers)
+  extern __shared__ __align__(1024) uint8_t mem[];
+  float *const decay = reinterpret_cast<float *>(mem + L::kD);
+  uint16_t *const keys = reinterpret_cast<uint16_t *>(mem + L::kK);
+  uint16_t *const queries = reinterpret_cast<uint16_t *>(mem + L::kQ);
+  float *const coefs = reinterpret_cast<float *>(mem + L::kA);
+  TreeTask *const tasks = reinterpret_cast<TreeTask *>(mem + L::kTasks);
+  TreeBars *const bars = reinterpret_cast<TreeBars *>(mem + L::kBars);
+  uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(mem + L::kSlot);
   const TreeMaps &mp = p.maps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quarter = warp & 3, half = warp >> 2;
+  const int begin = (int)((long long)n_items * blockIdx.x / gridDim.x);
+  const int end = (int)((long long)n_items * (blockIdx.x + 1) / gridDim.x);
   if (tid == 0) {
-    mbar_init(bar, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->task_full[i], 1);
+      mbar_init(&bars->task_free[i], L::kWarps - 1);
+    }
+    mbar_init(&bars->x_full, L::kNodeWarps);
+    mbar_init(&bars->x_free, 1);
+    mbar_init(&bars->y_free, 1);
+    mbar_init(&bars->p_full, 1);
+    mbar_init(&bars->p_free, L::kTWarps);
+    mbar_init(&bars->a_full, L::kPageWarps);
+    mbar_init(&bars->a_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->d_full[i], 1);
+      mbar_init(&bars->d_free[i], L::kRWarps);
+      mbar_init(&bars->done[i], 1);
+    }
+    mbar_init(&bars->t_full, L::kTWarps);
+    mbar_init(&bars->t_free, 1);
+    mbar_init(&bars->r_full, L::kRWarps);
+    mbar_init(&bars->o_full, 1);
     mbar_init_fence();
   }
-  if (warp == 0) tmem_alloc(tmem_slot, kTmCols);
+  if (warp == 0) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t my_lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-  const int begin = (int)((long long)n_items * blockIdx.x / gridDim.x);
-  const int end = (int)((long long)n_items * (blockIdx.x + 1) / gridDim.x);
-  uint32_t rounds = 0;  // of products, for the barrier's parity
-  bool failed = false;
-  int request = -1;
-  TreeRequest r;
-  r.error = KDA_ERR_ARG;
-  r.t0 = r.n = r.pending = 0;
-  r.slot = r.row = -1;
-  bool tree_ok = false;
-  for (int item = begin; item < end && !failed; ++item) {
-    const int b = item / p.H, h = item - b * p.H;
-    if (b != request) {
-      request = b;
-      r = tree_request(mp, b);
-      if (warp == 0) {
-        const bool ok = r.error == KDA_OK && (r.slot < 0 || load_tree(mp, r, parent, lane));
-        if (lane == 0) {
-          *good = ok;
-          if (!ok) report(mp.status, KDA_ERR_ARG);
-        }
-        if (ok && r.slot >= 0) {
-#pragma unroll
-          for (int i = 0; i < NC / 32 + (NC < 32); ++i) {
-            const int t = lane + 32 * i;
-            if (t >= NC) break;
-            uint8_t path[8];
-            int m = 0, a = parent[t];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) {
-              path[j] = (uint8_t)a;
-              m += a >= 0;
-              a = a >= 0 ? parent[a] : -1;
-            }
-            path[0] = (uint8_t)m;
-            uint2 w;
-            w.x = path[0] | path[1] << 8 | path[2] << 16 | (uint32_t)path[3] << 24;
-            w.y = path[4] | path[5] << 8 | path[6] << 16 | (uint32_t)path[7] << 24;
-            *reinterpret_cast<uint2 *>(anc + 8 * t) = w;
-          }
-        }
-      }
-      __syncthreads();
-      tree_ok = *good != 0;
-      __syncthreads();  // (read before the next request's)
-    }
-    if (!tree_ok) continue;
-    const long long first = (long long)r.t0 * p.H + h;  // the (token, head) row of node 0
-    if (r.slot < 0) {
-      for (int i = tid; i < r.n * (kDim / 8); i += kTmThreads)
-        *reinterpret_cast<uint4 *>(p.out + (first + (long long)(i / (kDim / 8)) * p.H) * kDim +
-                                   i % (kDim / 8) * 8) = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    const int n = r.n, replay = r.pending;
-    if (n == 0 && replay == 0) continue;
-    const long long page = r.slot * p.slot_stride + (long long)h * kDim * kDim;
-    const float a = expf(p.A_log[h]);
-    const float4 dt = __ldg(reinterpret_cast<const float4 *>(p.dt_bias + h * kDim) + lane);
+  const auto page_of = [&](int slot, int h) { return slot * p.slot_stride + (long long)h * kDim * kDim; };
+  // a warp's part of what is handed over is done
+  const auto arrive = [&](uint64_t *bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  bool ok = true;
+
+  if (warp < L::kR0) {
+    // ======== pages: rows 32 quarter .. + 31, keys 64 which .. + 63
+    constexpr int J = 4, kThreads = 32 * L::kPageWarps;
+    const int quarter = warp & 3, which = warp >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     float *const rk = reinterpret_cast<float *>(mem + L::kReplayK);
     float *const rd = reinterpret_cast<float *>(mem + L::kReplayD);
     float *const ru = reinterpret_cast<float *>(mem + L::kReplayU);
     float *const rdn = reinterpret_cast<float *>(mem + L::kReplayDn);
-    // ---- the page is asked for
-    PageRegs pg;
-    uint2 pgb[BF16 ? 16 : 1];
-    const long long at = page + (long long)(32 * quarter + lane / 4) * kDim + 64 * half +
-                         4 * (lane & 3);
-    if constexpr (BF16) {
+    const int k0 = 16 * J * which + 4 * (lane & 3);
+    TreeItems it;
+    int done = 0;  // items with nodes
+    bool more = it.start(tasks, bars);
+    if (named_bar_or(3, kThreads, !it.ok)) more = it.ok = false;
+    while (more) {
+      const int replay = it.pending;
+      const long long page = page_of(it.slot, it.h) + (long long)(32 * quarter + lane / 4) * kDim + k0;
+      PageRegs<BF16, J> pg[2];
+      pg[0].load(p.state, page);
+      if (BF16) pg[1].load(p.state, page + 16 * kDim);
+      // the next head's page on its way to L2
+      if (it.h + 1 < it.h1)
 #pragma unroll
-      for (int rh = 0; rh < 2; ++rh)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            pgb[(rh * 4 + j) * 2 + i] = __ldcs(reinterpret_cast<const uint2 *>(
-                static_cast<const uint16_t *>(p.state) + at + (16 * rh + 8 * i) * kDim + 16 * j));
-    } else {
-#pragma unroll
-      for (int rh = 0; rh < 2; ++rh)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            pg.s[rh][j][i] = __ldcs(reinterpret_cast<const float4 *>(
-                static_cast<const float *>(p.state) + at + (16 * rh + 8 * i) * kDim + 16 * j));
-    }
-    // ---- the recorded tokens and the nodes: norms and decays
-    for (int t = warp; t < replay; t += kTmWarps) {
-      const uint16_t *rec = p.kg + r.row * p.kg_stride + ((long long)h * mp.rq + t) * 2 * kDim;
-      const float4 k = bf16x4(__ldg(reinterpret_cast<const uint2 *>(rec) + lane));
-      const float4 g = bf16x4(__ldg(reinterpret_cast<const uint2 *>(rec + kDim) + lane));
-      const float4 u = __ldg(reinterpret_cast<const float4 *>(
-                                 p.corr + r.row * p.corr_stride + ((long long)h * mp.rq + t) * kDim) +
-                             lane);
-      sts4(rk + t * kDim + 4 * lane, scale4(k, rsqrtf(warp_sum(dot4(k, k)) + kNormEps)));
-      sts4(rd + t * kDim + 4 * lane, decay4(a, g, dt, p.lower_bound));
-      sts4(ru + t * kDim + 4 * lane, u);
-    }
-#pragma unroll 2
-    for (int t = warp; t < n; t += kTmWarps) {
-      const long long row = first + (long long)t * p.H;
-      const uint2 kb = __ldg(reinterpret_cast<const uint2 *>(p.k + row * kDim) + lane);
-      const uint2 gb = __ldg(reinterpret_cast<const uint2 *>(p.g + row * kDim) + lane);
-      const uint16_t beta = __ldg(p.beta + row);
-      const float4 k = bf16x4(kb);
-      const float norm = rsqrtf(warp_sum(dot4(k, k)) + kNormEps);
-      *reinterpret_cast<uint2 *>(keys + t * kDim + 4 * lane) = kb;
-      sts4(decay + t * kDim + 4 * lane, decay4(a, bf16x4(gb), dt, p.lower_bound));
-      if (lane == 0) {
-        norms[t] = norm;
-        coefs[t * kTreeCoefs + kCoefBeta] = sigmoidf_fast(bf16_bits_to_f32(beta));
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+          prefetch_l2(static_cast<const char *>(p.state) + page_of(it.slot, it.h + 1) * (BF16 ? 2 : 4) +
+                      (i * kThreads + tid) * 128);
+      if (replay > 0) {
+        if (warp < replay) {
+          const long long row = (long long)it.h * mp.rq + warp;
+          const uint2 *rec = reinterpret_cast<const uint2 *>(p.kg + it.row * p.kg_stride + row * 2 * kDim) + lane;
+          const float4 k = bf16x4(__ldg(rec)), g = bf16x4(__ldg(rec + 32));
+          const float4 u = __ldg(reinterpret_cast<const float4 *>(p.corr + it.row * p.corr_stride + row * kDim) + lane);
+          const float4 dt = __ldg(reinterpret_cast<const float4 *>(p.dt_bias + it.h * kDim) + lane);
+          const float a = expf(__ldg(p.A_log + it.h));
+          sts4(rk + warp * kDim + 4 * lane, scale4(k, rsqrtf(warp_sum(dot4(k, k)) + kNormEps)));
+          sts4(rd + warp * kDim + 4 * lane, decay4(a, g, dt, p.lower_bound));
+          sts4(ru + warp * kDim + 4 * lane, u);
+        }
+        named_bar(3, kThreads);
+        if (tid < kDim) replay_suffix(rk, rd, rdn, replay, tid);
+        named_bar(3, kThreads);
       }
-    }
-    // ---- the next head's page and operands on their way to L2
-    if (item + 1 < end && h + 1 < p.H) {
-      const char *next = static_cast<const char *>(p.state) + (page + kDim * kDim) * (BF16 ? 2 : 4);
-#pragma unroll
-      for (int i = 0; i < (BF16 ? 1 : 2); ++i) prefetch_l2(next + (i * kTmThreads + tid) * 128);
-      for (int i = tid; i < 8 * n; i += kTmThreads) {
-        const long long byte = ((first + 1 + (long long)(i >> 3) * p.H) * kDim) * 2 + (i & 1) * 128;
-        const uint16_t *from = (i & 7) < 4 ? ((i & 7) < 2 ? p.k : p.g) : ((i & 7) < 6 ? p.q : p.v);
-        prefetch_l2(reinterpret_cast<const char *>(from) + byte);
-      }
-    }
-    if (replay > 0) {
-      __syncthreads();
-      if (tid < kDim) replay_suffix(rk, rd, rdn, replay, tid);
-      __syncthreads();
-    }
-    // ---- S_n, and its parts to tensor memory
-    if constexpr (BF16) {
+      // S_n, and its parts to tensor memory, 16 rows and 32 keys at a time (all
+      // rows at once do not fit the registers)
 #pragma unroll
       for (int rh = 0; rh < 2; ++rh) {
-        uint32_t w[16];
+        if constexpr (!BF16) {
+          if (rh == 1) pg[1].load(p.state, page + 16 * kDim);
+          if (replay > 0) {
+            const float *up = ru + 32 * quarter + 16 * rh + lane / 4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            w[4 * j + 2 * i] = pgb[(rh * 4 + j) * 2 + i].x;
-            w[4 * j + 2 * i + 1] = pgb[(rh * 4 + j) * 2 + i].y;
-          }
-        tm_store_16x32(my_lanes + ((uint32_t)(16 * rh) << 16) + 32 * half, w);
-      }
-    } else {
-      if (replay > 0) {
-        const float *dn = rdn + 64 * half + 4 * (lane & 3);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 x = lds4(dn + 16 * j);
-#pragma unroll
-          for (int rh = 0; rh < 2; ++rh)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) pg.s[rh][j][i] = fmul4(pg.s[rh][j][i], x);
-        }
+            for (int j = 0; j < J; ++j) {
+              const float4 x = lds4(rdn + k0 + 16 * j);
+              pg[rh].s[j][0] = fmul4(pg[rh].s[j][0], x);
+              pg[rh].s[j][1] = fmul4(pg[rh].s[j][1], x);
+            }
 #pragma unroll 1
-        for (int t = 0; t < replay; ++t) {
-          const float *kp = rk + t * kDim + 64 * half + 4 * (lane & 3);
-          const float *up = ru + t * kDim + 32 * quarter + lane / 4;
-          float u[2][2];
+            for (int t = 0; t < replay; ++t) {
+              const float u0 = up[t * kDim], u1 = up[t * kDim + 8];
 #pragma unroll
-          for (int rh = 0; rh < 2; ++rh)
+              for (int j = 0; j < J; ++j) {
+                const float4 x = lds4(rk + t * kDim + k0 + 16 * j);
+                pg[rh].s[j][0] = ffma4s(u0, x, pg[rh].s[j][0]);
+                pg[rh].s[j][1] = ffma4s(u1, x, pg[rh].s[j][1]);
+              }
+            }
+            float *to = static_cast<float *>(p.state) + page + 16 * rh * kDim;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) u[rh][i] = up[16 * rh + 8 * i];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 x = lds4(kp + 16 * j);
-#pragma unroll
-            for (int rh = 0; rh < 2; ++rh)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) pg.s[rh][j][i] = ffma4s(u[rh][i], x, pg.s[rh][j][i]);
+            for (int j = 0; j < J; ++j) {
+              stg4(to + 16 * j, pg[rh].s[j][0]);
+              stg4(to + 8 * kDim + 16 * j, pg[rh].s[j][1]);
+            }
           }
         }
-        float *to = static_cast<float *>(p.state) + at;
-#pragma unroll
-        for (int rh = 0; rh < 2; ++rh)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              stg4(to + (16 * rh + 8 * i) * kDim + 16 * j, pg.s[rh][j][i]);
-      }
-      if (n > 0) {
-#pragma unroll
-        for (int rh = 0; rh < 2; ++rh)
-#pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float4 &s = pg.s[rh][j][i];
-                float2 lo = make_float2(s.x, s.y), hi = make_float2(s.z, s.w);
-                w[4 * j + 2 * i] = take_part(lo);
-                w[4 * j + 2 * i + 1] = take_part(hi);
-                s = make_float4(lo.x, lo.y, hi.x, hi.y);
-              }
-            tm_store_16x32(my_lanes + ((uint32_t)(16 * rh) << 16) + kTmPartCols * part + 32 * half, w);
+        if (it.n > 0) {
+          if (rh == 0 && done > 0) {
+            it.wait(&bars->a_free, (uint32_t)(done - 1) & 1u);
+            tc_fence_after();
           }
+#pragma unroll
+          for (int j0 = 0; j0 < J; j0 += 2)
+#pragma unroll
+            for (int part = 0; part < (BF16 ? 1 : 3); ++part) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                auto &s = pg[rh].s[j0 + e / 2][e % 2];
+                if constexpr (BF16) {
+                  w[2 * e] = s.x;
+                  w[2 * e + 1] = s.y;
+                } else {
+                  float2 lo = make_float2(s.x, s.y), hi = make_float2(s.z, s.w);
+                  w[2 * e] = take_part(lo);
+                  w[2 * e + 1] = take_part(hi);
+                  s = make_float4(lo.x, lo.y, hi.x, hi.y);
+                }
+              }
+              tm_store_16x16(lanes + ((uint32_t)(16 * rh) << 16) + kTmPartCols * part +
+                                 8 * (J * which + j0),
+                             w);
+            }
+        }
       }
+      if (it.n > 0) {
+        tm_store_wait();
+        tc_fence_before();
+        arrive(&bars->a_full);
+        ++done;
+      }
+      more = it.next(lane);
+      // (the replay's operands are read)
+      if (named_bar_or(3, kThreads, !it.ok)) more = it.ok = false;
     }
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-    tc_fence_before();
-    __syncthreads();  // the nodes' operands are there, and the replay's are read
-    const int groups = (n + G - 1) / G;
-    for (int g = 0; g < groups; ++g) {
-      const int n0 = g * G, ng = n - n0 < G ? n - n0 : G;
-      const int cols = (ng + 7) & ~7;  // of w, and of y behind them
-      // ---- (1) paths
-#pragma unroll 1
-      for (int i = warp; i < ng; i += kTmWarps) {
-        const int t = n0 + i;
-        const uint2 qb = __ldg(reinterpret_cast<const uint2 *>(p.q + (first + (long long)t * p.H) * kDim) + lane);
-        const float4 q = bf16x4(qb);
-        float4 xk = scale4(bf16x4(*reinterpret_cast<const uint2 *>(keys + t * kDim + 4 * lane)), norms[t]);
-        float4 xq = scale4(q, rsqrtf(warp_sum(dot4(q, q)) + kNormEps) * p.q_scale);
-        float v[kTreeCoefs];
-#pragma unroll
-        for (int c = 0; c < kTreeCoefs; ++c) v[c] = 0.f;
-        v[kCoefSelf] = dot4(xk, xq);
-        int s = t;
-#pragma unroll
-        for (int j = 0; j < kTreeDepth; ++j) {
-          const float4 ds = lds4(decay + s * kDim + 4 * lane);
-          xk = fmul4(xk, ds);
-          xq = fmul4(xq, ds);
-          s = parent[s];
-          if (s < 0) break;  // (the same in every lane)
-          if (j < kTreeDepth - 1) {
-            const float4 ks = scale4(bf16x4(*reinterpret_cast<const uint2 *>(keys + s * kDim + 4 * lane)), norms[s]);
-            v[j] = dot4(xk, ks);
-            v[kCoefB + j] = dot4(xq, ks);
-          }
-        }
-        // lane l of each half warp ends with value l
-        reduce_scatter<kTreeCoefs, 16>(v, lane);
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-        if (lane < kCoefBeta) coefs[t * kTreeCoefs + lane] = v[0];
-        // X's rows i and cols + i: keys 4 lane .. + 3 of 64-key block lane / 16
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int row = w * cols + i;
-          uint8_t *to = mem + L::kX + (lane >> 4) * L::kBlock + row * 128 +
-                        ((((lane & 15) >> 1) ^ (row & 7)) << 4) + (lane & 1) * 8;
-          const float4 x = w ? xq : xk;
-          float2 lo = make_float2(x.x, x.y), hi = make_float2(x.z, x.w);
-#pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const uint32_t c = take_part(lo);
-            *reinterpret_cast<uint2 *>(to + part * L::kPart) = make_uint2(c, take_part(hi));
-          }
-        }
+    ok = it.ok;
+  } else if (warp < L::kT0) {
+    // ======== R and the outputs: a row a lane, eight nodes at a time
+    const int quarter = warp & 3, at = 32 * quarter + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    TreeItems it;
+    int done = 0;
+    bool more = it.start(tasks, bars);
+    if (named_bar_or(4, 32 * L::kRWarps, !it.ok)) more = it.ok = false;
+    while (more) {
+      const int n = it.n, cols = (n + 15) & ~15;
+      if (n == 0) {
+        more = it.next(lane);
+        if (named_bar_or(4, 32 * L::kRWarps, !it.ok)) more = it.ok = false;
+        continue;
       }
-      fence_proxy_async_smem();
-      __syncthreads();
-      // ---- (2) products; T and C
-      if (warp == kTmWarps - 1) {
-        tc_fence_after();
-        const uint32_t lead = tm_elect();
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint32_t idesc = __shfl_sync(0xffffffffu, tm_idesc(2 * cols), 0);
-        const uint32_t x0 = __shfl_sync(0xffffffffu, smem_u32(mem + L::kX), 0);
-        {
-          // the smallest products first
-          constexpr int kTerms = BF16 ? 3 : 6;
-          constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
-          constexpr int kB1[3] = {2, 1, 0};
+      const int buf = done % L::kDBufs;
+      const uint32_t d = kTmD + buf * 2 * NC;
+      const long long first = ((long long)it.t0 * p.H + it.h) * kDim + at;
+      const long long step = (long long)p.H * kDim;
+      uint32_t v[8];
+      const auto ask = [&](int i0) {
 #pragma unroll
-          for (int e = 0; e < kTerms; ++e) {
-            const uint32_t pa = BF16 ? 0 : kA[e], pb = BF16 ? kB1[e % 3] : kB[e];
-#pragma unroll
-            for (int ks = 0; ks < kDim / 16; ++ks)
-              tm_mma(tm + kTmD, tm + pa * kTmPartCols + 8 * ks,
-                     umma_desc_sw128(x0 + pb * L::kPart + (ks >> 2) * L::kBlock + (ks & 3) * 32),
-                     idesc, e > 0 || ks > 0, lead);
-          }
-          if (lead) umma_commit(bar);
-        }
-        __syncwarp();
-      } else if (warp == 0) {
-        // a lane a node, level by level
-        for (int level = 0; level < kTreeDepth; ++level) {
-          const int t = n0 + lane;
-          const bool mine = lane < ng && anc[8 * t] == level;
-          if (mine) {
-            const float *c = coefs + t * kTreeCoefs;
-            const float beta = c[kCoefBeta], self = c[kCoefSelf];
-            float ta[kPath], ca[kPath];
-#pragma unroll
-            for (int j = 0; j < kPath; ++j) ta[j] = ca[j] = 0.f;
-#pragma unroll
-            for (int i = 1; i < kPath; ++i) {
-              if (i > level) break;
-              const float *up = tc + anc[8 * t + i] * 2 * kPath;
-              const float A = c[i - 1], B = c[kCoefB + i - 1];
-              const float4 x = lds4(up), y = lds4(up + 4);
-              const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-              for (int k = 0; k + i < kPath; ++k) {
-                ta[i + k] = fmaf(A, f[k], ta[i + k]);
-                ca[i + k] = fmaf(B, f[k], ca[i + k]);
-              }
-            }
-            float *to = tc + t * 2 * kPath;
-            ta[0] = -1.f;
-#pragma unroll
-            for (int j = 0; j < kPath; ++j) {
-              ta[j] *= -beta;
-              ca[j] = fmaf(self, ta[j], ca[j]);
-            }
-            sts4(to, make_float4(ta[0], ta[1], ta[2], ta[3]));
-            sts4(to + 4, make_float4(ta[4], ta[5], ta[6], ta[7]));
-            sts4(to + 8, make_float4(ca[0], ca[1], ca[2], ca[3]));
-            sts4(to + 12, make_float4(ca[4], ca[5], ca[6], ca[7]));
-          }
-          __syncwarp();
-        }
-      }
-      // ---- (3) R and y: four nodes at a time, the halves in turn
-      const uint16_t *vp = p.v + (first + (long long)n0 * p.H) * kDim + 32 * quarter + lane;
-      constexpr int kChunks = G / 8;  // of a half, at most
-      uint16_t vb[kChunks][4];
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 8 * c + 4 * half + e;
-          vb[c][e] = i < ng ? __ldg(vp + (long long)i * p.H * kDim) : 0;
-        }
-      const bool ok = mbar_wait_bounded(bar, rounds & 1u);
-      ++rounds;
-      if (__syncthreads_or(!ok)) {
-        if (tid == 0) report(mp.status, KDA_ERR_TIMEOUT);
-        failed = true;
-        break;
-      }
+        for (int i = 0; i < 8; ++i) v[i] = __ldg(p.v + first + (i0 + i < n ? i0 + i : n - 1) * step);
+      };
+      ask(0);
+      it.wait(&bars->d_full[buf], (uint32_t)(done / L::kDBufs) & 1u);
       tc_fence_after();
-      const bool last = g + 1 == groups;
-      float *const ys = reinterpret_cast<float *>(mem + L::kX);
-      float *const rs = reinterpret_cast<float *>(mem + L::kR);
-      // R of node t: rs + t * kDim, or in X for the last group's
-      float *const rx = ys + (G - n0) * kDim;
-      float *const to = (last ? rx : rs) + n0 * kDim + 32 * quarter + lane;
+      bool bad = false;
+#pragma unroll 1
+      for (int i0 = 0; i0 < cols; i0 += 8) {
+        float x[8];
+        tm_load(lanes + d + i0, x);
+        uint32_t bits = 0;
+        tm_load_wait();
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int i0 = 8 * c + 4 * half;
-        if (i0 < cols) {
-          float w[4], y[4];
-          tm_load4(my_lanes + kTmD + i0, w);
-          tm_load4(my_lanes + kTmD + cols + i0, y);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            to[(i0 + e) * kDim] = bf16_bits_to_f32(vb[c][e]) - w[e];
-            ys[(i0 + e) * kDim + 32 * quarter + lane] = y[e];
+        for (int i = 0; i < 8; ++i) {
+          x[i] = i0 + i < n ? __uint_as_float(v[i] << 16) - x[i] : 0.f;
+          if (!(fabsf(x[i]) < __int_as_float(0x7f800000))) {
+            bits |= 1u << i;
+            x[i] = 0.f;
           }
         }
+        if (i0 + 8 < n) ask(i0 + 8);
+        mem[L::kBad + i0 / 8 * kDim + at] = (uint8_t)bits;
+        bad = bad || bits != 0;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 pair = make_float2(x[2 * i], x[2 * i + 1]);
+            w[i] = take_part(pair);
+            x[2 * i] = pair.x, x[2 * i + 1] = pair.y;
+          }
+          tm_store_32x4(lanes + L::kTmR + (NC / 2) * part + i0 / 2, w[0], w[1], w[2], w[3]);
+        }
+        // (u is added up on zeros, o on y)
+        tm_store_32x4(lanes + d + i0, 0, 0, 0, 0);
+        tm_store_32x4(lanes + d + i0 + 4, 0, 0, 0, 0);
+      }
+      tm_store_wait();
+      tc_fence_before();
+      arrive(&bars->r_full);
+      const bool any_bad = named_bar_or(4, 32 * L::kRWarps, bad);
+      it.wait(&bars->o_full, (uint32_t)done & 1u);
+      tc_fence_after();
+#pragma unroll 1
+      for (int i0 = 0; i0 < n; i0 += 8) {
+        float u[8], o[8];
+        tm_load(lanes + d + i0, u);
+        tm_load(lanes + d + cols + i0, o);
+        tm_load_wait();
+        if (any_bad) {
+#pragma unroll 1
+          for (int i = 0; i < 8 && i0 + i < n; ++i) {
+            const uint2 way = it.paths()[i0 + i];
+            bool hit = false;
+            for (int j = 0; j <= (int)(way.x & 0xff); ++j) {
+              const int s = j == 0 ? i0 + i : path_byte(way, j);
+              hit = hit || (mem[L::kBad + (s >> 3) * kDim + at] >> (s & 7) & 1u);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (hit && e == i) u[e] = o[e] = __int_as_float(0x7fffffff);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < n) {
+            p.node_corr[first + (i0 + i) * step] = u[i];
+            p.out[first + (i0 + i) * step] = f32_to_bf16_bits(o[i]);
+          }
       }
       tc_fence_before();
-      __syncthreads();
-      // ---- (4) u and o
+      arrive(&bars->d_free[buf]);
+      ++done;
+      more = it.next(lane);
+      if (named_bar_or(4, 32 * L::kRWarps, !it.ok)) more = it.ok = false;
+    }
+    ok = it.ok;
+  } else if (warp < L::kIssue0) {
+    // ======== T and C: a lane a row of P, nodes' keys, then their queries
+    const int tw = warp - L::kT0, row = 32 * tw + lane;
+    float *const mine = reinterpret_cast<float *>(mem + L::kP) + row * NC;
+    TreeItems it;
+    int done = 0;
+    bool more = it.start(tasks, bars);
+    if (named_bar_or(2, 32 * L::kTWarps, !it.ok)) more = it.ok = false;
+    while (more) {
+      const int n = it.n, cols = (n + 15) & ~15;
+      if (n == 0) {
+        more = it.next(lane);
+        if (named_bar_or(2, 32 * L::kTWarps, !it.ok)) more = it.ok = false;
+        continue;
+      }
+      const bool key = row < cols;
+      const int t = key ? row : row - cols;
+      const bool live = row < 2 * cols && t < n;
+      const uint2 path = live ? it.paths()[t] : make_uint2(0, 0);
+      const int m = live ? (int)(path.x & 0xff) : -1;
+      float beta = 0.f;
+      if (live) beta = sigmoidf_fast(bf16_bits_to_f32(__ldg(p.beta + (long long)(it.t0 + t) * p.H + it.h)));
+      it.wait(&bars->p_full, (uint32_t)done & 1u);
+      tc_fence_after();
+      for (int c = 0; c < cols; c += 16) {
+        float x[16];
+        tm_load(tmem + ((uint32_t)(32 * tw) << 16) + L::kTmP + c, x);
+        tm_load_wait();
+        if (row < 2 * cols)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mine[(c + i) ^ lane] = x[i];
+      }
+      tc_fence_before();
+      arrive(&bars->p_free);
+      // A row's weights: of u_s in u_t (in o_t) over all ways down the path from
+      // s, W_s = -sum W_r beta_r A[r][s] over the r between (and P's entry); then
+      // R_s enters with W_s beta_s.
+      float wt[kPath];
+      wt[0] = m < 0 || key ? 1.f : mine[t ^ lane];
+#pragma unroll
+      for (int j = 1; j < kPath; ++j) wt[j] = j <= m ? mine[path_byte(path, j) ^ lane] : 0.f;
+      if (key && live) {
+        sts4(coefs + t * kPath, make_float4(wt[1], wt[2], wt[3], wt[4]));
+        sts4(coefs + t * kPath + 4, make_float4(wt[5], wt[6], wt[7], beta));
+#pragma unroll
+        for (int j = 1; j < kPath; ++j) wt[j] = 0.f;
+      }
+      named_bar(2, 32 * L::kTWarps);
+#pragma unroll
+      for (int i = 0; i < kPath; ++i) {
+        const float *c = coefs + (i == 0 ? (m < 0 ? 0 : t) : path_byte(path, i)) * kPath;
+        const float4 x = lds4(c), y = lds4(c + 4);
+        const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        wt[i] *= f[7];
+#pragma unroll
+        for (int k = 1; i + k < kPath; ++k)
+          if (i + k <= m) wt[i + k] = fmaf(-wt[i], f[k - 1], wt[i + k]);
+      }
+      // [T; C] in parts: zeros, and a row's entries
+      if (done > 0) it.wait(&bars->t_free, (uint32_t)(done - 1) & 1u);
+      if (row < 2 * cols) {
+        uint8_t *const to = mem + L::kTC + row * 128;
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          for (int c = 0; c < cols / 8; ++c)
+            *reinterpret_cast<uint4 *>(to + e * L::kTCPart + ((c ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kPath; ++j)
+          if (j <= m) {
+            const int s = j == 0 ? t : path_byte(path, j);
+            uint8_t *const place = to + (((s >> 3) ^ (row & 7)) << 4) + (s & 7) * 2;
+            float2 x = make_float2(wt[j], 0.f);
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              *reinterpret_cast<uint16_t *>(place + e * L::kTCPart) = (uint16_t)take_part(x);
+          }
+      }
+      fence_proxy_async_smem();
+      arrive(&bars->t_full);
+      ++done;
+      more = it.next(lane);
+      if (named_bar_or(2, 32 * L::kTWarps, !it.ok)) more = it.ok = false;
+    }
+    ok = it.ok;
+  } else if (warp < L::kTask0) {
+    // ======== products
+    const uint32_t lead = tm_elect();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t x0 = __shfl_sync(0xffffffffu, smem_u32(mem + L::kX), 0);
+    const uint32_t y0 = __shfl_sync(0xffffffffu, smem_u32(mem + L::kY), 0);
+    const uint32_t c0 = __shfl_sync(0xffffffffu, smem_u32(mem + L::kTC), 0);
+    const auto commit = [&](uint64_t *bar) {
+      if (lead) umma_commit(bar);
+      __syncwarp();
+    };
+    // parts of A and of B of the six products, the smallest first, two bits each
+    constexpr uint32_t kA6 = 2 | 0 << 2 | 1 << 4 | 1 << 6 | 0 << 8 | 0 << 10,
+                       kB6 = 0 | 2 << 2 | 1 << 4 | 0 << 6 | 1 << 8 | 0 << 10;
+    TreeItems it;
+    uint32_t done = 0;
+    if (warp == L::kIssue0) {
+      for (bool more = it.start(tasks, bars); more; more = it.next(lane)) {
+        if (it.n == 0) continue;
+        const uint32_t cols = __shfl_sync(0xffffffffu, (uint32_t)(it.n + 15) & ~15u, 0);
+        const uint32_t buf = done % L::kDBufs, d = tm + kTmD + buf * 2 * NC;
+        it.wait(&bars->x_full, done & 1u);
+        if (done > 0) it.wait(&bars->p_free, (done - 1) & 1u);
+        if (!it.ok) break;
+        tc_fence_after();
 #pragma unroll 1
-      for (int i = warp; i < ng; i += kTmWarps) {
-        const int t = n0 + i;
-        const uint2 path = *reinterpret_cast<const uint2 *>(anc + 8 * t);
-        const float *c = tc + t * 2 * kPath;
+        for (uint32_t e = 0; e < 6; ++e) {
+          const uint32_t x = x0 + (kA6 >> 2 * e & 3) * L::kXPart, y = y0 + (kB6 >> 2 * e & 3) * L::kYPart;
+#pragma unroll
+          for (int ks = 0; ks < kDim / 16; ++ks)
+            // (M = 128 rows: those behind X's are other operands', and P's rows of
+            // them nobody reads)
+            tm_mma_ss(tm + L::kTmP, umma_desc_sw128(x + (ks >> 2) * L::kXBlock + (ks & 3) * 32),
+                      umma_desc_sw128(y + (ks >> 2) * L::kYBlock + (ks & 3) * 32), tm_idesc(cols),
+                      e > 0 || ks > 0, lead);
+        }
+        commit(&bars->p_full);
+        if (!L::kOverY) commit(&bars->y_free);
+        it.wait(&bars->a_full, done & 1u);
+        if (done >= (uint32_t)L::kDBufs) it.wait(&bars->d_free[buf], (done / L::kDBufs - 1) & 1u);
+        if (!it.ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (uint32_t e = 0; e < (BF16 ? 3 : 6); ++e) {
+          const uint32_t s = tm + (BF16 ? 0 : (kA6 >> 2 * e & 3)) * kTmPartCols;
+          const uint32_t x = x0 + (BF16 ? 2 - e : (kB6 >> 2 * e & 3)) * L::kXPart;
+#pragma unroll
+          for (int ks = 0; ks < kDim / 16; ++ks)
+            tm_mma(d, s + 8 * ks, umma_desc_sw128(x + (ks >> 2) * L::kXBlock + (ks & 3) * 32),
+                   tm_idesc(2 * cols), e > 0 || ks > 0, lead);
+        }
+        commit(&bars->d_full[buf]);
+        commit(&bars->a_free);
+        commit(&bars->x_free);
+        ++done;
+      }
+    } else {
+      for (bool more = it.start(tasks, bars); more; more = it.next(lane)) {
+        if (it.n == 0) continue;
+        const uint32_t cols = __shfl_sync(0xffffffffu, (uint32_t)(it.n + 15) & ~15u, 0);
+        const uint32_t d = tm + kTmD + done % L::kDBufs * 2 * NC;
+        it.wait(&bars->t_full, done & 1u);
+        it.wait(&bars->r_full, done & 1u);
+        if (!it.ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (uint32_t e = 0; e < 6; ++e)
+#pragma unroll 1
+          for (uint32_t ks = 0; ks < cols / 16; ++ks)
+            tm_mma(d, tm + L::kTmR + (kA6 >> 2 * e & 3) * (NC / 2) + 8 * ks,
+                   umma_desc_sw128(c0 + (kB6 >> 2 * e & 3) * L::kTCPart + ks * 32),
+                   tm_idesc(2 * cols), true, lead);
+        commit(&bars->o_full);
+        commit(&bars->t_free);
+        if (L::kOverY) commit(&bars->y_free);
+        ++done;
+      }
+    }
+    ok = it.ok;
+    // every product issued has completed before the columns are released
+    commit(&bars->done[warp - L::kIssue0]);
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->done[warp - L::kIssue0], 0u)) && ok;
+  } else if (warp < L::kNode0) {
+    // ======== requests: checked, their paths listed; the inert ones' zeros
+    int8_t *const parent = reinterpret_cast<int8_t *>(mem + L::kParent);
+    int seq = 0;
+    const auto place = [&] {
+      if (seq >= 4)
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->task_free[seq & 3], (uint32_t)((seq >> 2) - 1) & 1u));
+      return ok;
+    };
+    for (int item = begin; item < end && ok;) {
+      const int b = item / p.H, h0 = item - b * p.H;
+      const int h1 = p.H - h0 < end - item ? p.H : h0 + (end - item);
+      item += h1 - h0;
+      const TreeRequest r = tree_request(mp, b);
+      if (r.error == KDA_OK && r.slot < 0) {
+        for (long long i = lane; i < (long long)r.n * (h1 - h0) * (kDim / 8); i += 32) {
+          const int c = (int)(i % (kDim / 8)), h = h0 + (int)(i / (kDim / 8) % (h1 - h0));
+          const long long t = r.t0 + i / (kDim / 8) / (h1 - h0);
+          *reinterpret_cast<uint4 *>(p.out + (t * p.H + h) * kDim + 8 * c) = make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
+      if (r.error != KDA_OK || !load_tree(mp, r, parent, lane)) {
+        if (lane == 0) report(mp.status, KDA_ERR_ARG);
+        continue;
+      }
+      if (r.n == 0 && r.pending == 0) continue;
+      if (!place()) break;
+      TreeTask &task = tasks[seq & 3];
+#pragma unroll
+      for (int i = 0; i < NC / 32; ++i) {
+        const int t = lane + 32 * i;
+        uint32_t path[8];
+        int a = parent[t];
+        path[0] = 0;
+#pragma unroll
+        for (int j = 1; j < 8; ++j) {
+          path[j] = a >= 0 ? a : t;
+          path[0] += a >= 0;
+          a = a >= 0 ? parent[a] : -1;
+        }
+        task.path[t] = make_uint2(path[0] | path[1] << 8 | path[2] << 16 | path[3] << 24,
+                                  path[4] | path[5] << 8 | path[6] << 16 | path[7] << 24);
+      }
+      if (lane == 0) {
+        task.t0 = r.t0, task.n = r.n, task.slot = r.slot, task.row = r.row;
+        task.pending = r.pending, task.h0 = h0, task.h1 = h1;
+      }
+      arrive(&bars->task_full[seq & 3]);
+      ++seq;
+    }
+    if (ok && place()) {
+      if (lane == 0) tasks[seq & 3].n = -1;
+      arrive(&bars->task_full[seq & 3]);
+    }
+  } else {
+    // ======== nodes
+    constexpr int kThreads = 32 * L::kNodeWarps;
+    const int nw = warp - L::kNode0, ntid = tid - 32 * L::kNode0;
+    float *const dts = reinterpret_cast<float *>(mem + L::kDt);
+    float *const norms = reinterpret_cast<float *>(mem + L::kNorms);
+    TreeItems it;
+    // the next item with nodes, whose operands are then on their way
+    const auto settle = [&](bool more) {
+      while (more && it.n == 0) more = it.next(lane);
+      if (named_bar_or(1, kThreads, !it.ok)) return it.ok = false;
+      if (more) {
+        for (int i = ntid; i < it.n * 48; i += kThreads) {
+          const int t = i / 48, c = i - t * 48, c8 = 8 * (c & 15);
+          const long long at = ((long long)(it.t0 + t) * p.H + it.h) * kDim + c8;
+          if (c < 16) {
+            cp_async16(keys + t * kDim + c8, p.k + at);
+          } else if (c < 32) {
+            cp_async16(queries + t * kDim + c8, p.q + at);
+          } else {
+            cp_async16(decay + t * kDim + c8 / 2, p.g + at);
+          }
+        }
+        if (ntid < kDim / 4) cp_async16(dts + 4 * ntid, p.dt_bias + it.h * kDim + 4 * ntid);
+      }
+      return more;
+    };
+    int done = 0;
+    bool more = settle(it.start(tasks, bars));
+    while (more) {
+      const int n = it.n, cols = (n + 15) & ~15;
+      const float a = expf(__ldg(p.A_log + it.h));
+      cp_async_wait_all();
+      named_bar(1, kThreads);
+      // norms and decays: two nodes a warp, eight channels a lane
+      {
+        const int hw = lane >> 4, c8 = 8 * (lane & 15);
+        const float4 dta = lds4(dts + c8), dtb = lds4(dts + c8 + 4);
+#pragma unroll 1
+        for (int t0 = 2 * nw; t0 < n; t0 += 2 * L::kNodeWarps) {
+          const int t = t0 + hw < n ? t0 + hw : t0;
+          const uint4 kb = *reinterpret_cast<const uint4 *>(keys + t * kDim + c8);
+          const uint4 qb = *reinterpret_cast<const uint4 *>(queries + t * kDim + c8);
+          const uint4 gb = *reinterpret_cast<const uint4 *>(
+              reinterpret_cast<const uint16_t *>(decay + t * kDim) + c8);
+          const float4 ka = bf16x4(make_uint2(kb.x, kb.y)), kc = bf16x4(make_uint2(kb.z, kb.w));
+          const float4 qa = bf16x4(make_uint2(qb.x, qb.y)), qc = bf16x4(make_uint2(qb.z, qb.w));
+          float kk = dot4(ka, ka) + dot4(kc, kc), qq = dot4(qa, qa) + dot4(qc, qc);
+#pragma unroll
+          for (int o = 8; o >= 1; o >>= 1) {
+            kk += __shfl_xor_sync(0xffffffffu, kk, o);
+            qq += __shfl_xor_sync(0xffffffffu, qq, o);
+          }
+          __syncwarp();  // the row's gates are read
+          if (t0 + hw < n) {
+            sts4(decay + t * kDim + c8, decay4(a, bf16x4(make_uint2(gb.x, gb.y)), dta, p.lower_bound));
+            sts4(decay + t * kDim + c8 + 4, decay4(a, bf16x4(make_uint2(gb.z, gb.w)), dtb, p.lower_bound));
+            if ((lane & 15) == 0) {
+              norms[t] = rsqrtf(kk + kNormEps);
+              norms[NC + t] = rsqrtf(qq + kNormEps) * p.q_scale;
+            }
+          }
+        }
+      }
+      named_bar(1, kThreads);
+      if (done > 0) {
+        it.wait(&bars->x_free, (uint32_t)(done - 1) & 1u);
+        it.wait(&bars->y_free, (uint32_t)(done - 1) & 1u);
+      }
+      // X and Y: a node a warp, four channels a lane
+#pragma unroll 1
+      for (int t = nw; t < n; t += L::kNodeWarps) {
+        const uint2 path = it.paths()[t];
         const int m = path.x & 0xff;
-        float4 x = lds4((last ? rx : rs) + t * kDim + 4 * lane);
-        float4 u = scale4(x, c[0]);
-        float4 o = ffma4s(c[kPath], x, lds4(ys + i * kDim + 4 * lane));
+        float4 g = lds4(decay + t * kDim + 4 * lane);
+        const float4 k = scale4(bf16x4(*reinterpret_cast<const uint2 *>(keys + t * kDim + 4 * lane)), norms[t]);
+        const float4 q = scale4(bf16x4(*reinterpret_cast<const uint2 *>(queries + t * kDim + 4 * lane)), norms[NC + t]);
 #pragma unroll
         for (int j = 1; j < kPath; ++j) {
-          if (j > m) break;
-          const int s = ((j < 4 ? path.x : path.y) >> (8 * (j & 3))) & 0xff;
-          x = lds4((s >= n0 && last ? rx : rs) + s * kDim + 4 * lane);
-          u = ffma4s(c[j], x, u);
-          o = ffma4s(c[kPath + j], x, o);
+          if (j > m) break;  // (the same in every lane)
+          g = fmul4(g, lds4(decay + path_byte(path, j) * kDim + 4 * lane));
         }
-        const long long row = (first + (long long)t * p.H) * kDim + 4 * lane;
-        stg4(p.node_corr + row, u);
-        *reinterpret_cast<uint2 *>(p.out + row) =
-            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        store_parts(mem + L::kX + tile_place(t, lane, L::kXBlock), L::kXPart, fmul4(k, g));
+        store_parts(mem + L::kX + tile_place(cols + t, lane, L::kXBlock), L::kXPart, fmul4(q, g));
+        store_parts(mem + L::kY + tile_place(t, lane, L::kYBlock), L::kYPart,
+                    make_float4(__fdividef(k.x, g.x), __fdividef(k.y, g.y), __fdividef(k.z, g.z),
+                                __fdividef(k.w, g.w)));
       }
-      __syncthreads();  // X, R and the coefficients may be written again
-      tc_fence_after();
+      fence_proxy_async_smem();
+      arrive(&bars->x_full);
+      ++done;
+      more = settle(it.next(lane));  // (its barrier: the nodes are read)
     }
+    cp_async_wait_all();
+    ok = it.ok;
   }
-  if (failed && warp == kTmWarps - 1) mbar_wait_bounded(bar, (rounds - 1) & 1u);
+  if (!ok && lane == 0) report(mp.status, KDA_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmCols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
-template <int NC, int G, bool BF16>
+template <int NC, bool BF16>
 int launch(const TreeVerifyParams &p, int sms, cudaStream_t stream) {
-  const auto kernel = kda_tree_mma_kernel<NC, G, BF16>;
-  constexpr int bytes = (int)TreeMma<NC, G>::kBytes;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+  using L = TreeMma<NC>;
+  const auto kernel = kda_tree_mma_kernel<NC, BF16>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes) !=
       cudaSuccess)
     return KDA_ERR_CUDA;
   const int items = p.maps.B * p.H;
-  kernel<<<items < 2 * sms ? items : 2 * sms, kTmThreads, bytes, stream>>>(p, items);
+  kernel<<<items < sms ? items : sms, L::kThreads, L::kBytes, stream>>>(p, items);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // namespace
 
 int launch_tree_mma(const TreeVerifyParams &p, bool bf16, int sms, cudaStream_t stream) {
-  if (p.maps.Q <= 32)
-    return bf16 ? launch<32, 32, true>(p, sms, stream) : launch<32, 32, false>(p, sms, stream);
-  return bf16 ? launch<64, 16, true>(p, sms, stream) : launch<64, 16, false>(p, sms, stream);
+  if (p.maps.Q <= 32) return bf16 ? launch<32, true>(p, sms, stream) : launch<32, false>(p, sms, stream);
+  return bf16 ? launch<64, true>(p, sms, stream) : launch<64, false>(p, sms, stream);
 }
 
 }  // namespace kda
