@@ -186,12 +186,15 @@ struct TreeBars {
 // NC: nodes of the largest window.
 template <int NC>
 struct TreeMma {
-  // warps: pages (two to a quarter of the rows), R and outputs, T and C (a lane
-  // a row of P), the two that issue, the one with the requests, nodes
-  static constexpr int kPageWarps = 8, kRWarps = 4, kTWarps = 2 * NC / 32,
-                       kNodeWarps = NC <= 32 ? 7 : 8;
+  // warps: pages and R (two of each to a quarter of the rows), T and C (a lane a
+  // row of P), the two that issue, the one with the requests, nodes
+  static constexpr int kWarps = 32, kPageWarps = 8, kRWarps = 8, kTWarps = 2 * NC / 32;
   static constexpr int kR0 = kPageWarps, kT0 = kR0 + kRWarps, kIssue0 = kT0 + kTWarps,
-                       kTask0 = kIssue0 + 2, kNode0 = kTask0 + 1, kWarps = kNode0 + kNodeWarps;
+                       kTask0 = kIssue0 + 2, kNode0 = kTask0 + 1, kNodeWarps = kWarps - kNode0;
+  // registers a thread: at launch, of pages (whole warpgroups), of the others
+  static constexpr int kPageRegs = 88, kOtherRegs = 56;
+  static_assert(kPageWarps * kPageRegs + (kWarps - kPageWarps) * kOtherRegs <= kWarps * 64,
+                "what the warps of pages take, the others have given");
   static_assert(kR0 % 4 == 0 && kT0 % 4 == 0, "a warp reaches the tensor memory lanes of its number");
   static constexpr int kThreads = 32 * kWarps;
   // tensor memory: the page, w and y (twice where there is room), P, R
@@ -262,6 +265,13 @@ __device__ __forceinline__ void store_parts(uint8_t *to, uint32_t part, float4 x
     const uint32_t c = take_part(lo);
     *reinterpret_cast<uint2 *>(to + e * part) = make_uint2(c, take_part(hi));
   }
+}
+
+// 1 / x, within a unit of the last place (x is far from FP32's ends).
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // j-th byte of a node's path.
@@ -356,6 +366,11 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
     if (lane == 0) mbar_arrive(bar);
   };
   bool ok = true;
+  if (warp < L::kR0) {
+    warpgroup_reg_alloc<L::kPageRegs>();
+  } else {
+    warpgroup_reg_dealloc<L::kOtherRegs>();
+  }
 
   if (warp < L::kR0) {
     // ======== pages: rows 32 quarter .. + 31, keys 64 which .. + 63
@@ -369,42 +384,54 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
     const int k0 = 16 * J * which + 4 * (lane & 3);
     TreeItems it;
     int done = 0;  // items with nodes
-    bool more = it.start(tasks, bars);
-    if (named_bar_or(3, kThreads, !it.ok)) more = it.ok = false;
-    while (more) {
-      const int replay = it.pending;
-      const long long page = page_of(it.slot, it.h) + (long long)(32 * quarter + lane / 4) * kDim + k0;
-      PageRegs<BF16, J> pg[2];
-      pg[0].load(p.state, page);
-      if (BF16) pg[1].load(p.state, page + 16 * kDim);
-      // the next head's page on its way to L2
+    PageRegs<BF16, J> pg[2];
+    uint2 rec_k, rec_g;
+    float4 rec_u;
+    // an item's records (a warp one) and the first half of its rows, ahead of its
+    // turn; and the next head's page on its way to L2
+    const auto page_part = [&] {
+      return page_of(it.slot, it.h) + (long long)(32 * quarter + lane / 4) * kDim + k0;
+    };
+    const auto ask = [&] {
+      if (warp < it.pending) {
+        const long long row = (long long)it.h * mp.rq + warp;
+        const uint2 *rec = reinterpret_cast<const uint2 *>(p.kg + it.row * p.kg_stride + row * 2 * kDim) + lane;
+        rec_k = __ldg(rec);
+        rec_g = __ldg(rec + 32);
+        rec_u = __ldg(reinterpret_cast<const float4 *>(p.corr + it.row * p.corr_stride + row * kDim) + lane);
+      }
+      pg[0].load(p.state, page_part());
+      if (BF16) pg[1].load(p.state, page_part() + 16 * kDim);
       if (it.h + 1 < it.h1)
 #pragma unroll
         for (int i = 0; i < (BF16 ? 1 : 2); ++i)
           prefetch_l2(static_cast<const char *>(p.state) + page_of(it.slot, it.h + 1) * (BF16 ? 2 : 4) +
                       (i * kThreads + tid) * 128);
+    };
+    bool more = it.start(tasks, bars);
+    if (more) ask();
+    if (named_bar_or(3, kThreads, !it.ok)) more = it.ok = false;
+    while (more) {
+      const int replay = it.pending;
+      const long long page = page_part();
       if (replay > 0) {
         if (warp < replay) {
-          const long long row = (long long)it.h * mp.rq + warp;
-          const uint2 *rec = reinterpret_cast<const uint2 *>(p.kg + it.row * p.kg_stride + row * 2 * kDim) + lane;
-          const float4 k = bf16x4(__ldg(rec)), g = bf16x4(__ldg(rec + 32));
-          const float4 u = __ldg(reinterpret_cast<const float4 *>(p.corr + it.row * p.corr_stride + row * kDim) + lane);
+          const float4 k = bf16x4(rec_k);
           const float4 dt = __ldg(reinterpret_cast<const float4 *>(p.dt_bias + it.h * kDim) + lane);
           const float a = expf(__ldg(p.A_log + it.h));
           sts4(rk + warp * kDim + 4 * lane, scale4(k, rsqrtf(warp_sum(dot4(k, k)) + kNormEps)));
-          sts4(rd + warp * kDim + 4 * lane, decay4(a, g, dt, p.lower_bound));
-          sts4(ru + warp * kDim + 4 * lane, u);
+          sts4(rd + warp * kDim + 4 * lane, decay4(a, bf16x4(rec_g), dt, p.lower_bound));
+          sts4(ru + warp * kDim + 4 * lane, rec_u);
         }
         named_bar(3, kThreads);
         if (tid < kDim) replay_suffix(rk, rd, rdn, replay, tid);
         named_bar(3, kThreads);
       }
-      // S_n, and its parts to tensor memory, 16 rows and 32 keys at a time (all
-      // rows at once do not fit the registers)
+      // S_n, and its parts to tensor memory, 16 rows and 32 keys at a time; the
+      // second half of the rows is asked for once the first is replayed
 #pragma unroll
       for (int rh = 0; rh < 2; ++rh) {
         if constexpr (!BF16) {
-          if (rh == 1) pg[1].load(p.state, page + 16 * kDim);
           if (replay > 0) {
             const float *up = ru + 32 * quarter + 16 * rh + lane / 4;
 #pragma unroll
@@ -430,6 +457,7 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
               stg4(to + 8 * kDim + 16 * j, pg[rh].s[j][1]);
             }
           }
+          if (rh == 0) pg[1].load(p.state, page + 16 * kDim);
         }
         if (it.n > 0) {
           if (rh == 0 && done > 0) {
@@ -467,13 +495,14 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
         ++done;
       }
       more = it.next(lane);
+      if (more) ask();
       // (the replay's operands are read)
       if (named_bar_or(3, kThreads, !it.ok)) more = it.ok = false;
     }
     ok = it.ok;
   } else if (warp < L::kT0) {
     // ======== R and the outputs: a row a lane, eight nodes at a time
-    const int quarter = warp & 3, at = 32 * quarter + lane;
+    const int quarter = warp & 3, which = (warp - L::kR0) >> 2, at = 32 * quarter + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     TreeItems it;
     int done = 0;
@@ -492,30 +521,40 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
       const long long step = (long long)p.H * kDim;
       uint32_t v[8];
       const auto ask = [&](int i0) {
+        const uint16_t *from = p.v + first + i0 * step;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __ldg(p.v + first + (i0 + i < n ? i0 + i : n - 1) * step);
+        for (int i = 0; i < 8; ++i) {
+          v[i] = __ldg(from);
+          if (i0 + i + 1 < n) from += step;  // (behind the last: again the last)
+        }
       };
-      ask(0);
+      if (8 * which < n) ask(8 * which);
       it.wait(&bars->d_full[buf], (uint32_t)(done / L::kDBufs) & 1u);
       tc_fence_after();
       bool bad = false;
 #pragma unroll 1
-      for (int i0 = 0; i0 < cols; i0 += 8) {
+      for (int i0 = 8 * which; i0 < cols; i0 += 16) {
         float x[8];
         tm_load(lanes + d + i0, x);
-        uint32_t bits = 0;
         tm_load_wait();
+        float all = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           x[i] = i0 + i < n ? __uint_as_float(v[i] << 16) - x[i] : 0.f;
-          if (!(fabsf(x[i]) < __int_as_float(0x7f800000))) {
-            bits |= 1u << i;
-            x[i] = 0.f;
-          }
+          all += fabsf(x[i]);
         }
-        if (i0 + 8 < n) ask(i0 + 8);
+        if (i0 + 16 < n) ask(i0 + 16);
+        uint32_t bits = 0;
+        if (!(all < __int_as_float(0x7f800000))) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!(fabsf(x[i]) < __int_as_float(0x7f800000))) {
+              bits |= 1u << i;
+              x[i] = 0.f;
+            }
+          bad = bad || bits != 0;
+        }
         mem[L::kBad + i0 / 8 * kDim + at] = (uint8_t)bits;
-        bad = bad || bits != 0;
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
           uint32_t w[4];
@@ -538,7 +577,7 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
       it.wait(&bars->o_full, (uint32_t)done & 1u);
       tc_fence_after();
 #pragma unroll 1
-      for (int i0 = 0; i0 < n; i0 += 8) {
+      for (int i0 = 8 * which; i0 < n; i0 += 16) {
         float u[8], o[8];
         tm_load(lanes + d + i0, u);
         tm_load(lanes + d + cols + i0, o);
@@ -557,12 +596,16 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
               if (hit && e == i) u[e] = o[e] = __int_as_float(0x7fffffff);
           }
         }
+        float *to_u = p.node_corr + first + i0 * step;
+        uint16_t *to_o = p.out + first + i0 * step;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
           if (i0 + i < n) {
-            p.node_corr[first + (i0 + i) * step] = u[i];
-            p.out[first + (i0 + i) * step] = f32_to_bf16_bits(o[i]);
+            *to_u = u[i];
+            *to_o = f32_to_bf16_bits(o[i]);
           }
+          to_u += step, to_o += step;
+        }
       }
       tc_fence_before();
       arrive(&bars->d_free[buf]);
@@ -591,6 +634,16 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
       const bool live = row < 2 * cols && t < n;
       const uint2 path = live ? it.paths()[t] : make_uint2(0, 0);
       const int m = live ? (int)(path.x & 0xff) : -1;
+      // this item's values on their way to L2, and the next head's nodes
+      for (int i = row; i < n * 8; i += 32 * L::kTWarps) {
+        const int what = i >> 1 & 3;
+        const long long at = ((long long)(it.t0 + (i >> 3)) * p.H + it.h) * kDim + (i & 1) * (kDim / 2);
+        if (what == 0) {
+          prefetch_l2(p.v + at);
+        } else if (it.h + 1 < it.h1) {
+          prefetch_l2((what == 1 ? p.k : (what == 2 ? p.q : p.g)) + at + kDim);
+        }
+      }
       float beta = 0.f;
       if (live) beta = sigmoidf_fast(bf16_bits_to_f32(__ldg(p.beta + (long long)(it.t0 + t) * p.H + it.h)));
       it.wait(&bars->p_full, (uint32_t)done & 1u);
@@ -804,16 +857,12 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
       while (more && it.n == 0) more = it.next(lane);
       if (named_bar_or(1, kThreads, !it.ok)) return it.ok = false;
       if (more) {
-        for (int i = ntid; i < it.n * 48; i += kThreads) {
-          const int t = i / 48, c = i - t * 48, c8 = 8 * (c & 15);
+        const int c8 = 8 * (lane & 15);
+#pragma unroll 1
+        for (int t = nw; t < it.n; t += L::kNodeWarps) {
           const long long at = ((long long)(it.t0 + t) * p.H + it.h) * kDim + c8;
-          if (c < 16) {
-            cp_async16(keys + t * kDim + c8, p.k + at);
-          } else if (c < 32) {
-            cp_async16(queries + t * kDim + c8, p.q + at);
-          } else {
-            cp_async16(decay + t * kDim + c8 / 2, p.g + at);
-          }
+          cp_async16((lane < 16 ? keys : queries) + t * kDim + c8, (lane < 16 ? p.k : p.q) + at);
+          if (lane < 16) cp_async16(decay + t * kDim + c8 / 2, p.g + at);
         }
         if (ntid < kDim / 4) cp_async16(dts + 4 * ntid, p.dt_bias + it.h * kDim + 4 * ntid);
       }
@@ -874,11 +923,13 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
           if (j > m) break;  // (the same in every lane)
           g = fmul4(g, lds4(decay + path_byte(path, j) * kDim + 4 * lane));
         }
-        store_parts(mem + L::kX + tile_place(t, lane, L::kXBlock), L::kXPart, fmul4(k, g));
-        store_parts(mem + L::kX + tile_place(cols + t, lane, L::kXBlock), L::kXPart, fmul4(q, g));
+        // (queries stand a multiple of 16 rows behind the keys: the same swizzle)
+        uint8_t *const x = mem + L::kX + tile_place(t, lane, L::kXBlock);
+        store_parts(x, L::kXPart, fmul4(k, g));
+        store_parts(x + cols * 128, L::kXPart, fmul4(q, g));
         store_parts(mem + L::kY + tile_place(t, lane, L::kYBlock), L::kYPart,
-                    make_float4(__fdividef(k.x, g.x), __fdividef(k.y, g.y), __fdividef(k.z, g.z),
-                                __fdividef(k.w, g.w)));
+                    make_float4(k.x * rcp_fast(g.x), k.y * rcp_fast(g.y), k.z * rcp_fast(g.z),
+                                k.w * rcp_fast(g.w)));
       }
       fence_proxy_async_smem();
       arrive(&bars->x_full);
