@@ -184,11 +184,12 @@ struct TreeBars {
 };
 
 // NC: nodes of the largest window.
-template <int NC>
+template <int NC, bool BF16>
 struct TreeMma {
-  // warps: pages and R (two of each to a quarter of the rows), T and C (a lane a
-  // row of P), the two that issue, the one with the requests, nodes
-  static constexpr int kWarps = 32, kPageWarps = 8, kRWarps = 8, kTWarps = 2 * NC / 32;
+  // warps: pages (two to a quarter of the rows; BF16 pages, which are only read,
+  // one), R (two), T and C (a lane a row of P), the two that issue, the one with
+  // the requests, nodes
+  static constexpr int kWarps = 32, kPageWarps = BF16 ? 4 : 8, kRWarps = 8, kTWarps = 2 * NC / 32;
   static constexpr int kR0 = kPageWarps, kT0 = kR0 + kRWarps, kIssue0 = kT0 + kTWarps,
                        kTask0 = kIssue0 + 2, kNode0 = kTask0 + 1, kNodeWarps = kWarps - kNode0;
   // registers a thread: at launch, of pages (whole warpgroups), of the others
@@ -314,9 +315,9 @@ struct TreeItems {
 };
 
 template <int NC, bool BF16>
-__global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
+__global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     kda_tree_mma_kernel(const TreeVerifyParams p, int n_items) {
-  using L = TreeMma<NC>;
+  using L = TreeMma<NC, BF16>;
   // (its alignment known, the addresses below are constants, which take no
   // registers)
   extern __shared__ __align__(1024) uint8_t mem[];
@@ -373,8 +374,8 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
   }
 
   if (warp < L::kR0) {
-    // ======== pages: rows 32 quarter .. + 31, keys 64 which .. + 63
-    constexpr int J = 4, kThreads = 32 * L::kPageWarps;
+    // ======== pages: rows 32 quarter .. + 31, keys 16 J which .. + 16 J - 1
+    constexpr int J = 32 / L::kPageWarps, kThreads = 32 * L::kPageWarps;
     const int quarter = warp & 3, which = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     float *const rk = reinterpret_cast<float *>(mem + L::kReplayK);
@@ -401,10 +402,9 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
         rec_u = __ldg(reinterpret_cast<const float4 *>(p.corr + it.row * p.corr_stride + row * kDim) + lane);
       }
       pg[0].load(p.state, page_part());
-      if (BF16) pg[1].load(p.state, page_part() + 16 * kDim);
       if (it.h + 1 < it.h1)
 #pragma unroll
-        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+        for (int i = 0; i < 2; ++i)
           prefetch_l2(static_cast<const char *>(p.state) + page_of(it.slot, it.h + 1) * (BF16 ? 2 : 4) +
                       (i * kThreads + tid) * 128);
     };
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
               stg4(to + 8 * kDim + 16 * j, pg[rh].s[j][1]);
             }
           }
-          if (rh == 0) pg[1].load(p.state, page + 16 * kDim);
         }
+        if (rh == 0) pg[1].load(p.state, page + 16 * kDim);
         if (it.n > 0) {
           if (rh == 0 && done > 0) {
             it.wait(&bars->a_free, (uint32_t)(done - 1) & 1u);
@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(TreeMma<NC>::kThreads, 1)
 
 template <int NC, bool BF16>
 int launch(const TreeVerifyParams &p, int sms, cudaStream_t stream) {
-  using L = TreeMma<NC>;
+  using L = TreeMma<NC, BF16>;
   const auto kernel = kda_tree_mma_kernel<NC, BF16>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes) !=
       cudaSuccess)
