@@ -17,8 +17,8 @@ namespace kda {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Few items: a CTA a slice of an item's rows, its part of the state in
-// registers, products by FMA.
+// Windows of a few nodes: a CTA an item, or a slice of its rows, its part of the
+// state in registers, products by FMA.  (Larger ones: kda_tree_verify_mma.cu.)
 // ---------------------------------------------------------------------------
 
 constexpr int kTrThreads = 256;
@@ -279,8 +279,13 @@ extern "C" int kda_tree_verify(
   if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
   const int sms = kda::device_sm_count(dev);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const long long items = (long long)B * H;
-  if (items * 4 <= sms)
+  // Windows of a few nodes by FMA, and of few items by a CTA for every 32 rows;
+  // all others on the tensor cores.  FP32 pages with a replay, us by rows of
+  // 32 / by whole pages / on the tensor cores: 4 nodes, 32 items 14 / 15 / 17,
+  // 192 items 25 / 19 / 25, 1536 items 130 / 74 / 83; 8 nodes, 32 items 17 / 19 /
+  // 17, 1536 items 181 / 95 / 85; 15 nodes, 32 items 23 / 25 / 17.
+  if (Q > 6) return kda::launch_tree_mma(p, bf16, sms, st);
+  if ((long long)B * H * 4 <= sms)
     return bf16 ? kda::launch_rows<32, true>(p, st) : kda::launch_rows<32, false>(p, st);
-  return kda::launch_tree_mma(p, bf16, sms, st);
+  return bf16 ? kda::launch_rows<128, true>(p, st) : kda::launch_rows<128, false>(p, st);
 }

@@ -74,6 +74,7 @@ SHAPES = {
     "combs": [tt.comb(64), tt.comb(31), tt.comb(33), tt.comb(17)],
     "random": [tt.random_tree(RNG, n) for n in (1, 5, 64, 15, 16, 17, 24, 32, 33, 48, 63)],
     "forests": [tt.random_tree(RNG, n, roots=r) for n, r in ((12, 3), (64, 64), (40, 2), (7, 7))],
+    "small": [tt.random_tree(RNG, n) for n in (3, 6, 1, 5, 2, 4, 6, 6, 1, 3, 5, 4)],
     "empty": [[], tt.random_tree(RNG, 6), [], tt.chain(4), []],
 }
 
@@ -87,13 +88,14 @@ def test_verify_shapes(shape, H):
 
 @pytest.mark.parametrize("H", [2, 41])
 @pytest.mark.parametrize("pool,replay", [("f32", False), ("bf16", False)])
-@pytest.mark.parametrize("shape", ["one", "combs", "random", "forests"])
+@pytest.mark.parametrize("shape", ["one", "small", "combs", "random", "forests"])
 def test_verify_reads_the_pool(shape, pool, replay, H):
     case = tt.tree_case(SHAPES[shape], H, seed=4, pool=pool, replay=replay)
     check_verify(case, run_verify(case))
 
 
-@pytest.mark.parametrize("B,H,n", [(6, 32, 12), (40, 8, 30), (3, 64, 64), (160, 1, 9)])
+@pytest.mark.parametrize("B,H,n", [(6, 32, 12), (40, 8, 30), (3, 64, 64), (160, 1, 9), (9, 3, 6),
+                                   (50, 7, 4)])
 def test_verify_batches(B, H, n):
     """Few and many items to an SM: every launch shape."""
     rng = np.random.default_rng(B)
@@ -102,11 +104,11 @@ def test_verify_batches(B, H, n):
     check_verify(case, run_verify(case))
 
 
-@pytest.mark.parametrize("B,H", [(3, 2), (60, 4)])
+@pytest.mark.parametrize("B,H,n", [(3, 2, 11), (60, 4, 11), (3, 2, 5), (60, 4, 5), (5, 3, 40)])
 @pytest.mark.parametrize("rq,pending", [(1, 1), (3, 9), (8, 8), (8, 0), (8, -4), (5, 3)])
-def test_verify_pending(rq, pending, B, H):
+def test_verify_pending(rq, pending, B, H, n):
     """Counts beyond the row are clamped; none leaves the page as it is."""
-    trees = [tt.random_tree(RNG, 11) for _ in range(B)]
+    trees = [tt.random_tree(RNG, n) for _ in range(B)]
     case = tt.tree_case(trees, H, seed=6, rq=rq, pending=pending)
     check_verify(case, run_verify(case))
 
@@ -120,11 +122,12 @@ def test_verify_gates(lower_bound, B):
     check_verify(case, run_verify(case))
 
 
+@pytest.mark.parametrize("n", [6, 13])
 @pytest.mark.parametrize("B", [5, 90])
-def test_verify_inert_and_rowless(B):
+def test_verify_inert_and_rowless(B, n):
     """Inert requests get zeros whatever their parents hold; without a record
     row nothing is replayed; rows behind the last request stay."""
-    trees = [tt.random_tree(RNG, 6) for _ in range(B)]
+    trees = [tt.random_tree(RNG, n) for _ in range(B)]
     case = tt.tree_case(trees, 2, seed=8, inert=(0, 3), rowless=(1,), tail=3)
     t0 = case["query_start_loc"][3]
     case["parents"][t0:t0 + 6] = [9, -7, 100, 2, 2, 1]
@@ -224,21 +227,22 @@ def test_verify_slots_beyond_32_bits():
     check_verify(case, d)
 
 
+@pytest.mark.parametrize("par", [[-1, 0, 0, 1, 2, 3, 4, 2, 0, 8], [-1, 0, 0, 1, 2, 0]])
 @pytest.mark.parametrize("B,H", [(2, 2), (50, 4)])
-def test_verify_other_branches_are_never_met(B, H):
+def test_verify_other_branches_are_never_met(B, H, par):
     """NaNs and infinities in one branch (and behind the windows) reach that
     branch's nodes alone: the others hold the same bits as without them."""
-    par = [-1, 0, 0, 1, 2, 3, 4, 2, 0, 8]
+    N = len(par)
     case = tt.tree_case([par] * B, H, seed=15, tail=2)
     clean = run_verify(case)
-    hit = [2, 4, 6, 7]  # the branch of node 2
+    hit = [2, 4, 6, 7] if N == 10 else [2, 4]  # the branch of node 2
     nan, inf = 0x7FC0, 0x7F80
     dirty = tt.copy_case(case)
     for b in range(B):
         t = case["query_start_loc"][b] + 2
         dirty["k"][t], dirty["q"][t], dirty["v"][t] = nan, inf, inf
         dirty["raw_g"][t], dirty["raw_beta"][t] = nan, nan
-        t = case["query_start_loc"][b] + 9  # a leaf
+        t = case["query_start_loc"][b] + N - 1  # a leaf
         dirty["q"][t] = nan
     for n in ("q", "k", "v", "raw_g", "raw_beta"):
         dirty[n][-2:] = nan
@@ -247,7 +251,7 @@ def test_verify_other_branches_are_never_met(B, H):
     leaf = np.zeros_like(own)
     for b in range(B):
         own[case["query_start_loc"][b] + np.array(hit)] = False
-        leaf[case["query_start_loc"][b] + 9] = True
+        leaf[case["query_start_loc"][b] + N - 1] = True
     for n in ("out", "node_corr"):
         got, want = tt.to_numpy(d[n]), tt.to_numpy(clean[n])
         keep = own & ~leaf if n == "out" else own
