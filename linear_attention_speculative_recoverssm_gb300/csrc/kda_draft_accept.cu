@@ -5,8 +5,8 @@
 // sums over siblings in a tree; every CTA of a request works it out for
 // itself, a lane a node.  The token behind it is drawn by inverse CDF from
 // one row of the target's weights (less the refused draft's row): the first i
-// whose running sum exceeds s Z.  A cluster of 8 CTAs takes a request, each
-// an eighth of the row; a warp adds up 512 weights at a time; the sums of
+// whose running sum exceeds s Z.  A cluster of up to 8 CTAs takes a request, each
+// its share of the row; a warp adds up 512 weights at a time; the sums of
 // those tiles are scanned, the CTAs' totals go round through distributed
 // shared memory, and the tile with the crossing is read again.
 //
@@ -26,13 +26,13 @@
 namespace kda {
 namespace {
 
-constexpr int kDaCtas = 8;  // of a request
+constexpr int kDaMaxCtas = 8;  // of a request
 constexpr int kDaThreads = 256;
 constexpr int kDaWarps = kDaThreads / 32;
 constexpr int kDaTile = 512;
 constexpr int kDaPer = kDaTile / 32;  // weights a lane
-constexpr int kDaTiles = KDA_MAX_VOCAB / kDaTile / kDaCtas;  // of a CTA, at most
-static_assert(kDaTiles == kDaThreads, "a thread takes a tile in the scan");
+constexpr int kDaOccupancy = 4;       // CTAs an SM
+constexpr int kDaTiles = KDA_MAX_VOCAB / kDaTile;  // of a CTA, at most
 
 struct AcceptParams {
   TreeMaps maps;
@@ -119,7 +119,7 @@ struct AcceptSmem {
   bool ok;
   Sum2 tile[kDaTiles];
   double warp_sum[kDaWarps];
-  double total[2][kDaCtas];  // written by every CTA of the cluster
+  double total[2][kDaMaxCtas];  // written by every CTA of the cluster
   int best, any;
 };
 
@@ -222,10 +222,10 @@ __device__ bool walk(const AcceptParams &p, const TreeRequest &r, int b, int lan
   }
   int cur = 0, n = 1, node = lane == 0 ? 0 : -1;  // lane i < 8: the path's i-th node
   uint32_t kids[2];
+  const int up0 = sm.parent[lane], up1 = sm.parent[lane + 32];
   while (true) {
-    children_of(sm.parent, cur, kids);
-    kids[0] &= live[0];
-    kids[1] &= live[1];
+    kids[0] = __ballot_sync(0xffffffffu, up0 == cur) & live[0];
+    kids[1] = __ballot_sync(0xffffffffu, up1 == cur) & live[1];
     const uint32_t m0 = kids[0] & taken[0], m1 = kids[1] & taken[1];
     if ((m0 | m1) == 0 || n == kTreeDepth) break;  // (no path is longer)
     cur = m0 != 0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
@@ -329,11 +329,11 @@ __device__ __forceinline__ double block_scan(double x, AcceptSmem &sm) {
 }
 
 template <typename T>
-__global__ void __cluster_dims__(kDaCtas, 1, 1) __launch_bounds__(kDaThreads)
-    kda_draft_accept_kernel(const AcceptParams p) {
+__global__ void __launch_bounds__(kDaThreads, kDaOccupancy)
+    kda_draft_accept_kernel(const AcceptParams p, int ctas) {
   __shared__ AcceptSmem sm;
   const TreeMaps &mp = p.maps;
-  const int b = blockIdx.x / kDaCtas, rank = blockIdx.x % kDaCtas;
+  const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   const int tid = threadIdx.x, lane = tid & 31;
   cluster_arrive();  // waited for before the first store to another CTA
   const TreeRequest r = tree_request(mp, b);
@@ -365,10 +365,11 @@ __global__ void __cluster_dims__(kDaCtas, 1, 1) __launch_bounds__(kDaThreads)
                                        (long long)(r.t0 + sm.refused) * p.draft_stride;
   int n_removed = sm.n_removed;
   const bool vec = ((reinterpret_cast<uintptr_t>(prow) | reinterpret_cast<uintptr_t>(qrow)) & 15) == 0;
-  const int all = (p.vocab + kDaTile - 1) / kDaTile, per = (all + kDaCtas - 1) / kDaCtas;
+  const int all = (p.vocab + kDaTile - 1) / kDaTile, per = (all + ctas - 1) / ctas;
   const int first = rank * per;
   const int tiles = first >= all ? 0 : (all - first < per ? all - first : per);
-  double upto, before, whole, goal;
+  const int each = (tiles + kDaThreads - 1) / kDaThreads;
+  double mine, upto, before, whole, goal;
   int owner, pass = 0;
   for (;; ++pass) {
     if (vec) {
@@ -377,17 +378,19 @@ __global__ void __cluster_dims__(kDaCtas, 1, 1) __launch_bounds__(kDaThreads)
       tile_sums<T, false>(prow, qrow, n_removed, p.vocab, first, tiles, sm);
     }
     __syncthreads();
-    const double mine = tid < tiles ? sm.tile[tid].value() : 0.0;
+    // a thread takes `each` tiles, one after the other
+    mine = 0.0;
+    for (int i = tid * each; i < (tid + 1) * each && i < tiles; ++i) mine += sm.tile[i].value();
     upto = block_scan(mine, sm);
     if (pass == 0) cluster_wait();
     if (tid == kDaThreads - 1)
 #pragma unroll 1
-      for (int i = 0; i < kDaCtas; ++i) store_to_rank(&sm.total[pass][rank], i, upto);
+      for (int i = 0; i < ctas; ++i) store_to_rank(&sm.total[pass][rank], i, upto);
     cluster_arrive();
     cluster_wait();
-    // the same in every CTA: the total, and whose eighth holds the crossing
+    // the same in every CTA: the total, and whose share holds the crossing
     whole = 0.0;
-    for (int i = 0; i < kDaCtas; ++i) whole += sm.total[pass][i];
+    for (int i = 0; i < ctas; ++i) whole += sm.total[pass][i];
     if (whole > 0.0 || pass == 1 || (qrow == nullptr && n_removed == 0)) break;
     qrow = nullptr;  // nothing is left without them: p itself
     n_removed = 0;
@@ -407,7 +410,7 @@ __global__ void __cluster_dims__(kDaCtas, 1, 1) __launch_bounds__(kDaThreads)
   double sum = 0.0;
   before = 0.0;
 #pragma unroll 1
-  for (int i = 0; i < kDaCtas; ++i) {
+  for (int i = 0; i < ctas; ++i) {
     const double t = sm.total[pass][i];
     if (t > 0.0) {
       owner = i;
@@ -417,16 +420,25 @@ __global__ void __cluster_dims__(kDaCtas, 1, 1) __launch_bounds__(kDaThreads)
     if (t > 0.0 && sum > goal) break;
   }
   if (owner != rank) return;
-  // the tile of the crossing
-  if (tid < tiles) {
-    const bool some = sm.tile[tid].hi > 0.f;
-    if (some && before + upto > goal) atomicMin(&sm.best, tid);
-    if (some) atomicMax(&sm.any, tid);
+  // the tile of the crossing, among the thread's
+  double from = before + (upto - mine);
+  for (int i = tid * each; i < (tid + 1) * each && i < tiles; ++i) {
+    const bool some = sm.tile[i].hi > 0.f;
+    from += sm.tile[i].value();
+    if (some && from > goal) {
+      atomicMin(&sm.best, i);
+      break;
+    }
+    if (some) atomicMax(&sm.any, i);
   }
   __syncthreads();
   const int tile = sm.best != 0x7fffffff ? sm.best : sm.any;
   // (what lies before it, from the thread that has the sum)
-  if (tid == tile) sm.warp_sum[0] = before + (upto - sm.tile[tid].value());
+  if (tid == tile / each) {
+    from = before + (upto - mine);
+    for (int i = tid * each; i < tile; ++i) from += sm.tile[i].value();
+    sm.warp_sum[0] = from;
+  }
   __syncthreads();
   const double start = sm.warp_sum[0];
   if (tid == 0) {
@@ -478,7 +490,7 @@ extern "C" int kda_draft_accept(const void *target, const void *draft, int probs
   if (parents == nullptr ? Q > KDA_TREE_MAX_DEPTH : draft != nullptr) return KDA_ERR_ARG;
   if (vocab < 1 || vocab > KDA_MAX_VOCAB) return KDA_ERR_ARG;
   if (B == 0) return KDA_OK;
-  if (B > 0x7fffffff / kda::kDaCtas) return KDA_ERR_ARG;
+  if (B > 0x7fffffff / kda::kDaMaxCtas) return KDA_ERR_ARG;
   if (!sample_uniforms || !accepted || !path || !next_tokens) return KDA_ERR_ARG;
   if (n_tokens > 0 && (!target || !tokens || !accept_uniforms)) return KDA_ERR_ARG;
   if (target_row_stride < vocab || (draft != nullptr && draft_row_stride < vocab))
@@ -497,11 +509,26 @@ extern "C" int kda_draft_accept(const void *target, const void *draft, int probs
   p.accepted = accepted;
   p.path = path;
   p.next = next_tokens;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (probs_dtype == KDA_PROBS_F32) {
-    kda::kda_draft_accept_kernel<float><<<B * kda::kDaCtas, kda::kDaThreads, 0, st>>>(p);
-  } else {
-    kda::kda_draft_accept_kernel<uint16_t><<<B * kda::kDaCtas, kda::kDaThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
+  const int sms = kda::device_sm_count(dev);
+  // as many CTAs a request as still run all at once
+  int ctas = kda::kDaMaxCtas;
+  while (ctas > 1 && (long long)B * ctas > (long long)kda::kDaOccupancy * sms) ctas /= 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(B * ctas));
+  cfg.blockDim = dim3(kda::kDaThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e =
+      probs_dtype == KDA_PROBS_F32
+          ? cudaLaunchKernelEx(&cfg, kda::kda_draft_accept_kernel<float>, p, ctas)
+          : cudaLaunchKernelEx(&cfg, kda::kda_draft_accept_kernel<uint16_t>, p, ctas);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

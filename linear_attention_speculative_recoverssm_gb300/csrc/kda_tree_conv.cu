@@ -101,10 +101,9 @@ __global__ void __launch_bounds__(kTcThreads, 4) kda_tree_conv_kernel(const Tree
     return a >= 0 ? __ldg(reinterpret_cast<const uint4 *>(x + (long long)a * (3 * D)))
                   : (a == -1 ? h1 : (a == -2 ? h2 : h3));
   };
-#pragma unroll 2
-  for (int t = first; t < past; ++t) {
+  const auto step = [&](uint4 own, int t) {
     const char4 up = above[t];
-    const Eight s3 = unpack8(input(t)), s2 = unpack8(input(up.x)), s1 = unpack8(input(up.y)),
+    const Eight s3 = unpack8(own), s2 = unpack8(input(up.x)), s1 = unpack8(input(up.y)),
                 s0 = unpack8(input(up.z));
     uint32_t res[4];
 #pragma unroll
@@ -116,6 +115,23 @@ __global__ void __launch_bounds__(kTcThreads, 4) kda_tree_conv_kernel(const Tree
       res[i] = silu_pair(ffma2(s3.p[i], w[3].p[i], z));
     }
     *reinterpret_cast<uint4 *>(out + (long long)t * D) = make_uint4(res[0], res[1], res[2], res[3]);
+  };
+  // the next four nodes are asked for while four are worked on
+  constexpr int kAhead = 4;
+  uint4 next[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) next[i] = input(first + i < past ? first + i : first);
+#pragma unroll 1
+  for (int t = first; t < past; t += kAhead) {
+    uint4 own[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) own[i] = next[i];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (t + kAhead + i < past) next[i] = input(t + kAhead + i);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (t + i < past) step(own[i], t + i);
   }
 }
 

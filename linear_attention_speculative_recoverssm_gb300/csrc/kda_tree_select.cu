@@ -36,20 +36,19 @@ struct TreeSelectParams {
   int record_ctas;     // CTAs of a request that move records
 };
 
-__global__ void __launch_bounds__(kTsThreads) kda_tree_select_kernel(const TreeSelectParams p) {
+__global__ void __launch_bounds__(kTsThreads, 6) kda_tree_select_kernel(const TreeSelectParams p) {
   __shared__ __align__(16) uint16_t rows[kTsChannels * kTsMaxWidth];
   const TreeMaps &mp = p.maps;
   const int b = blockIdx.x, lane = threadIdx.x & 31;
   const TreeRequest r = tree_request(mp, b);
   const int m = p.accepted[b];
-  int nodes[kTreeDepth];
+  const int32_t *path = p.path + (long long)b * kTreeDepth;
   bool ok = r.error == KDA_OK;
   if (ok && r.slot >= 0 && r.row >= 0) {
     ok = m >= 0 && m <= p.most;
-    const int4 lo = reinterpret_cast<const int4 *>(p.path)[2 * b],
-               hi = reinterpret_cast<const int4 *>(p.path)[2 * b + 1];
-    nodes[0] = lo.x, nodes[1] = lo.y, nodes[2] = lo.z, nodes[3] = lo.w;
-    nodes[4] = hi.x, nodes[5] = hi.y, nodes[6] = hi.z, nodes[7] = hi.w;
+    const int4 lo = reinterpret_cast<const int4 *>(path)[0],
+               hi = reinterpret_cast<const int4 *>(path)[1];
+    const int nodes[kTreeDepth] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
     for (int i = 0; i < kTreeDepth; ++i) ok = ok && (i >= m || (nodes[i] >= 0 && nodes[i] < r.n));
   }
@@ -62,20 +61,24 @@ __global__ void __launch_bounds__(kTsThreads) kda_tree_select_kernel(const TreeS
     float *corr = p.corr + r.row * p.corr_stride + (long long)h * mp.rq * kDim;
     uint16_t *kg = p.kg + r.row * p.kg_stride + (long long)h * mp.rq * 2 * kDim;
     const uint16_t *half = lane < 16 ? p.k : p.g;
-    float4 u[kTreeDepth];
-    uint4 e[kTreeDepth];
+    // (three at a time: more registers leave fewer CTAs on an SM)
+#pragma unroll 1
+    for (int i0 = 0; i0 < m; i0 += 3) {
+      float4 u[3];
+      uint4 e[3];
 #pragma unroll
-    for (int i = 0; i < kTreeDepth; ++i) {
-      if (i >= m) break;
-      const long long row = at + (long long)nodes[i] * p.H;
-      u[i] = __ldcs(reinterpret_cast<const float4 *>(p.node_corr + row * kDim) + lane);
-      e[i] = __ldcs(reinterpret_cast<const uint4 *>(half + row * kDim) + (lane & 15));
-    }
+      for (int i = 0; i < 3; ++i)
+        if (i0 + i < m) {
+          const long long row = at + (long long)__ldg(path + i0 + i) * p.H;
+          u[i] = __ldcs(reinterpret_cast<const float4 *>(p.node_corr + row * kDim) + lane);
+          e[i] = __ldcs(reinterpret_cast<const uint4 *>(half + row * kDim) + (lane & 15));
+        }
 #pragma unroll
-    for (int i = 0; i < kTreeDepth; ++i) {
-      if (i >= m) break;
-      reinterpret_cast<float4 *>(corr + i * kDim)[lane] = u[i];
-      reinterpret_cast<uint4 *>(kg + i * 2 * kDim)[lane] = e[i];
+      for (int i = 0; i < 3; ++i)
+        if (i0 + i < m) {
+          reinterpret_cast<float4 *>(corr + (i0 + i) * kDim)[lane] = u[i];
+          reinterpret_cast<uint4 *>(kg + (i0 + i) * 2 * kDim)[lane] = e[i];
+        }
     }
     return;
   }
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(kTsThreads) kda_tree_select_kernel(const TreeS
     for (int i = 0; i < kTreeDepth; ++i)
       if (i < m)
         in[i] = __ldg(reinterpret_cast<const uint32_t *>(
-            p.x + ((long long)r.t0 + nodes[i]) * D3 + ch0 + c));
+            p.x + ((long long)r.t0 + __ldg(path + i)) * D3 + ch0 + c));
   }
   __syncthreads();
   if (c < count) {
