@@ -6,9 +6,9 @@
 //
 // What bounds it: HBM, 4 bytes a node and channel (one input, one output) and
 // the windows' sectors once a request.  A CTA takes a request's nodes, or a
-// run of them, in 1024 channels, eight a thread.  Every node asks for its own
-// input and its ancestors'; those were asked for just before, and come from
-// the first-level cache.
+// run of them, in 512 channels, four a thread (eight take the registers of
+// twice the warps).  Every node asks for its own input and its ancestors'; those
+// were asked for just before, and come from the first-level cache.
 #include <cuda_runtime.h>
 
 #include "kda_launch.h"
@@ -28,30 +28,23 @@ struct TreeConvParams {
   uint16_t *q, *k, *v;
 };
 
-struct Eight {
-  float2 p[4];
+struct Four {
+  float2 a, b;
 };
 
-__device__ __forceinline__ Eight unpack8(uint4 x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  Eight e;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    e.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-  return e;
+__device__ __forceinline__ Four unpack4(uint2 x) {
+  return Four{make_float2(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u)),
+              make_float2(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u))};
 }
 
-// Entry `at` of a thread's eight channels' windows, `width` entries each.
-__device__ __forceinline__ uint4 window_entry(const uint16_t *win, int width, int at) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = (uint32_t)__ldg(win + 2 * i * width + at) |
-           (uint32_t)__ldg(win + (2 * i + 1) * width + at) << 16;
-  return make_uint4(w[0], w[1], w[2], w[3]);
+// Entry `at` of a thread's four channels' windows, `width` entries each.
+__device__ __forceinline__ uint2 window_entry(const uint16_t *win, int width, int at) {
+  return make_uint2((uint32_t)__ldg(win + at) | (uint32_t)__ldg(win + width + at) << 16,
+                    (uint32_t)__ldg(win + 2 * width + at) |
+                        (uint32_t)__ldg(win + 3 * width + at) << 16);
 }
 
-__global__ void __launch_bounds__(kTcThreads, 4) kda_tree_conv_kernel(const TreeConvParams p) {
+__global__ void __launch_bounds__(kTcThreads, 8) kda_tree_conv_kernel(const TreeConvParams p) {
   __shared__ int8_t parent[kTreeNodes];
   __shared__ char4 above[kTreeNodes];  // x, y, z: the nearest ancestor first
   __shared__ int good;
@@ -59,10 +52,28 @@ __global__ void __launch_bounds__(kTcThreads, 4) kda_tree_conv_kernel(const Tree
   const int b = blockIdx.x, lane = threadIdx.x & 31;
   const int D = p.H * kDim;
   const int group = blockIdx.y * kTcThreads + threadIdx.x;
-  const bool active = group < 3 * D / 8;
-  const int ch = active ? 8 * group : 0, part = ch / D, hc = ch - part * D;
+  const bool active = group < 3 * D / 4;
+  const int ch = active ? 4 * group : 0, part = ch / D, hc = ch - part * D;
   const TreeRequest r = tree_request(mp, b);
   if (r.error == KDA_OK && r.slot < 0) return;
+  const int first = blockIdx.z * p.run;
+  const int past = r.n - first > p.run ? first + p.run : r.n;
+  // the first nodes' inputs, and the entries above a root (the newest first),
+  // are asked for before the tree is looked at
+  constexpr int kAhead = 4;
+  const uint16_t *x = p.x + (long long)r.t0 * (3 * D) + ch;
+  uint2 next[kAhead], h1, h2, h3;
+  if (r.error == KDA_OK && first < past) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      next[i] = __ldg(reinterpret_cast<const uint2 *>(
+          x + (long long)(first + i < past ? first + i : first) * (3 * D)));
+    const uint16_t *win = p.window + r.slot * p.slot_stride + (long long)ch * p.width;
+    const int off = r.pending > 0 ? r.pending - 1 : 0;
+    h1 = window_entry(win, p.width, off + 2);
+    h2 = window_entry(win, p.width, off + 1);
+    h3 = window_entry(win, p.width, off);
+  }
   if (threadIdx.x < 32) {
     const bool ok = r.error == KDA_OK && load_tree(mp, r, parent, lane);
     if (lane == 0) {
@@ -80,50 +91,35 @@ __global__ void __launch_bounds__(kTcThreads, 4) kda_tree_conv_kernel(const Tree
       }
     }
   }
-  Eight w[4], bias;
+  Four w[4], bias;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = unpack8(__ldg(reinterpret_cast<const uint4 *>(p.w + (long long)(part * 4 + i) * D + hc)));
-  bias = unpack8(p.bias != nullptr ? __ldg(reinterpret_cast<const uint4 *>(p.bias + ch))
-                                   : make_uint4(0, 0, 0, 0));
+    w[i] = unpack4(__ldg(reinterpret_cast<const uint2 *>(p.w + (long long)(part * 4 + i) * D + hc)));
+  bias = unpack4(p.bias != nullptr ? __ldg(reinterpret_cast<const uint2 *>(p.bias + ch))
+                                   : make_uint2(0, 0));
   __syncthreads();
-  const int first = blockIdx.z * p.run;
-  const int past = r.n - first > p.run ? first + p.run : r.n;
   if (!good || !active || first >= past) return;
-  // the entries above a root, the newest first
-  const uint16_t *win = p.window + r.slot * p.slot_stride + (long long)ch * p.width;
-  const int off = r.pending > 0 ? r.pending - 1 : 0;
-  const uint4 h1 = window_entry(win, p.width, off + 2), h2 = window_entry(win, p.width, off + 1),
-              h3 = window_entry(win, p.width, off);
-  const uint16_t *x = p.x + (long long)r.t0 * (3 * D) + ch;
   uint16_t *out = (part == 0 ? p.q : (part == 1 ? p.k : p.v)) + (long long)r.t0 * D + hc;
   const auto input = [&](int a) {
-    return a >= 0 ? __ldg(reinterpret_cast<const uint4 *>(x + (long long)a * (3 * D)))
+    return a >= 0 ? __ldg(reinterpret_cast<const uint2 *>(x + (long long)a * (3 * D)))
                   : (a == -1 ? h1 : (a == -2 ? h2 : h3));
   };
-  const auto step = [&](uint4 own, int t) {
+  const auto step = [&](uint2 own, int t) {
     const char4 up = above[t];
-    const Eight s3 = unpack8(own), s2 = unpack8(input(up.x)), s1 = unpack8(input(up.y)),
-                s0 = unpack8(input(up.z));
-    uint32_t res[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // in tap order, as in kda_layer_prologue
-      float2 z = ffma2(s0.p[i], w[0].p[i], bias.p[i]);
-      z = ffma2(s1.p[i], w[1].p[i], z);
-      z = ffma2(s2.p[i], w[2].p[i], z);
-      res[i] = silu_pair(ffma2(s3.p[i], w[3].p[i], z));
-    }
-    *reinterpret_cast<uint4 *>(out + (long long)t * D) = make_uint4(res[0], res[1], res[2], res[3]);
+    const Four s3 = unpack4(own), s2 = unpack4(input(up.x)), s1 = unpack4(input(up.y)),
+               s0 = unpack4(input(up.z));
+    // in tap order, as in kda_layer_prologue
+    Four z{ffma2(s0.a, w[0].a, bias.a), ffma2(s0.b, w[0].b, bias.b)};
+    z = Four{ffma2(s1.a, w[1].a, z.a), ffma2(s1.b, w[1].b, z.b)};
+    z = Four{ffma2(s2.a, w[2].a, z.a), ffma2(s2.b, w[2].b, z.b)};
+    z = Four{ffma2(s3.a, w[3].a, z.a), ffma2(s3.b, w[3].b, z.b)};
+    *reinterpret_cast<uint2 *>(out + (long long)t * D) =
+        make_uint2(silu_pair(z.a), silu_pair(z.b));
   };
   // the next four nodes are asked for while four are worked on
-  constexpr int kAhead = 4;
-  uint4 next[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) next[i] = input(first + i < past ? first + i : first);
 #pragma unroll 1
   for (int t = first; t < past; t += kAhead) {
-    uint4 own[kAhead];
+    uint2 own[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) own[i] = next[i];
 #pragma unroll
@@ -181,7 +177,7 @@ extern "C" int kda_tree_conv(const kda_bf16 *x, const kda_bf16 *conv_weight,
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
   const int sms = kda::device_sm_count(dev);
-  const int channels = (3 * H * KDA_HEAD_DIM / 8 + kda::kTcThreads - 1) / kda::kTcThreads;
+  const int channels = (3 * H * KDA_HEAD_DIM / 4 + kda::kTcThreads - 1) / kda::kTcThreads;
   // whole requests where they fill the SMs, else runs of their nodes
   int run = Q;
   while (run > 2 && (long long)B * channels * ((Q - 1) / run + 1) < 4LL * sms) run = (run + 1) / 2;

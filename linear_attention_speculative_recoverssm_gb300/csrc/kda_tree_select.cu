@@ -6,10 +6,9 @@
 //
 // What bounds it: HBM, and copies are all there is.  Record CTAs take a
 // request's heads, 8 at a time (a warp a head, 16 bytes a lane); window CTAs
-// take 512 channels of a request: their window, one piece of memory, goes
+// take 1024 channels of a request: their window, one piece of memory, goes
 // through shared memory whole, where a thread rewrites the few entries of its
-// channels (rows of 20 bytes: no two lanes' in the same bank), and comes back
-// in 16-byte pieces.
+// four channels, and comes back in 16-byte pieces.
 #include <cuda_runtime.h>
 
 #include "kda_launch.h"
@@ -20,7 +19,7 @@ namespace {
 
 constexpr int kTsThreads = 256;
 constexpr int kTsHeads = kTsThreads / 32;
-constexpr int kTsChannels = 2 * kTsThreads;
+constexpr int kTsChannels = 4 * kTsThreads;
 constexpr int kTsMaxWidth = KDA_MAX_WINDOW + 2;
 
 struct TreeSelectParams {
@@ -36,7 +35,7 @@ struct TreeSelectParams {
   int record_ctas;     // CTAs of a request that move records
 };
 
-__global__ void __launch_bounds__(kTsThreads, 6) kda_tree_select_kernel(const TreeSelectParams p) {
+__global__ void __launch_bounds__(kTsThreads, 5) kda_tree_select_kernel(const TreeSelectParams p) {
   __shared__ __align__(16) uint16_t rows[kTsChannels * kTsMaxWidth];
   const TreeMaps &mp = p.maps;
   const int b = blockIdx.x, lane = threadIdx.x & 31;
@@ -89,34 +88,44 @@ __global__ void __launch_bounds__(kTsThreads, 6) kda_tree_select_kernel(const Tr
   uint4 *staged = reinterpret_cast<uint4 *>(rows);
   const int pieces = count * p.width / 8;  // (count is a multiple of 128)
   for (int i = threadIdx.x; i < pieces; i += kTsThreads) staged[i] = memory[i];
-  const int c = 2 * threadIdx.x;
-  uint32_t in[kTreeDepth];
+  const int c = 4 * threadIdx.x;
+  uint2 in[kTreeDepth];
   if (c < count) {
 #pragma unroll
     for (int i = 0; i < kTreeDepth; ++i)
       if (i < m)
-        in[i] = __ldg(reinterpret_cast<const uint32_t *>(
+        in[i] = __ldg(reinterpret_cast<const uint2 *>(
             p.x + ((long long)r.t0 + __ldg(path + i)) * D3 + ch0 + c));
   }
   __syncthreads();
   if (c < count) {
-    uint16_t *w0 = rows + c * p.width, *w1 = w0 + p.width;
+    uint16_t *const w = rows + c * p.width;
+    const auto get = [&](int i) {
+      return make_uint2(w[i] | (uint32_t)w[p.width + i] << 16,
+                        w[2 * p.width + i] | (uint32_t)w[3 * p.width + i] << 16);
+    };
+    const auto set = [&](int i, uint2 v) {
+      w[i] = (uint16_t)v.x, w[p.width + i] = (uint16_t)(v.x >> 16);
+      w[2 * p.width + i] = (uint16_t)v.y, w[3 * p.width + i] = (uint16_t)(v.y >> 16);
+    };
     const int off = r.pending > 0 ? r.pending - 1 : 0;
     if (m == 0 || (p.eager != nullptr && p.eager[b] != 0)) {
       // the last three of the window's and the path's (in order: what an
       // entry takes lies at its place or behind)
       for (int i = 0; i < 3; ++i) {
         const int j = m + i;
-        uint32_t v = j < 3 ? w0[off + j] | (uint32_t)w1[off + j] << 16 : 0;
+        uint2 v = make_uint2(0, 0);
+        if (j < 3) v = get(off + j);
 #pragma unroll
-        for (int e = 0; e < kTreeDepth; ++e) v = j - 3 == e ? in[e] : v;
-        w0[i] = (uint16_t)v, w1[i] = (uint16_t)(v >> 16);
+        for (int e = 0; e < kTreeDepth; ++e)
+          if (j - 3 == e) v = in[e];
+        set(i, v);
       }
     } else {
-      for (int i = 0; i < 2; ++i) w0[i] = w0[off + 1 + i], w1[i] = w1[off + 1 + i];
+      for (int i = 0; i < 2; ++i) set(i, get(off + 1 + i));
 #pragma unroll
       for (int i = 0; i < kTreeDepth; ++i)
-        if (i < m) w0[2 + i] = (uint16_t)in[i], w1[2 + i] = (uint16_t)(in[i] >> 16);
+        if (i < m) set(2 + i, in[i]);
     }
   }
   __syncthreads();
