@@ -6,9 +6,9 @@
 //
 // What bounds it: HBM, 4 bytes a node and channel (one input, one output) and
 // the windows' sectors once a request.  A CTA takes a request's nodes, or a
-// run of them, in 512 channels, four a thread (eight take the registers of
-// twice the warps).  Every node asks for its own input and its ancestors'; those
-// were asked for just before, and come from the first-level cache.
+// run of them, in 512 channels, four a thread.  All inputs are copied to shared
+// memory at once, asynchronously, and a node's four taps read there: window
+// entries and inputs alike, without a branch.
 #include <cuda_runtime.h>
 
 #include "kda_launch.h"
@@ -37,16 +37,18 @@ __device__ __forceinline__ Four unpack4(uint2 x) {
               make_float2(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u))};
 }
 
-// Entry `at` of a thread's four channels' windows, `width` entries each.
-__device__ __forceinline__ uint2 window_entry(const uint16_t *win, int width, int at) {
-  return make_uint2((uint32_t)__ldg(win + at) | (uint32_t)__ldg(win + width + at) << 16,
-                    (uint32_t)__ldg(win + 2 * width + at) |
-                        (uint32_t)__ldg(win + 3 * width + at) << 16);
+// 8-byte asynchronous copy global -> shared.
+__device__ __forceinline__ void cp_async8(void *smem_dst, const void *gmem_src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src)
+               : "memory");
 }
 
-__global__ void __launch_bounds__(kTcThreads, 8) kda_tree_conv_kernel(const TreeConvParams p) {
+__global__ void __launch_bounds__(kTcThreads) kda_tree_conv_kernel(const TreeConvParams p) {
+  // rows of this CTA's channels: the window's three entries, the oldest first,
+  // then the nodes' inputs; a thread reads what it copied itself
+  extern __shared__ uint2 rows[];
   __shared__ int8_t parent[kTreeNodes];
-  __shared__ char4 above[kTreeNodes];  // x, y, z: the nearest ancestor first
+  __shared__ uint2 taps[kTreeNodes];  // a node's four rows, the oldest first
   __shared__ int good;
   const TreeMaps &mp = p.maps;
   const int b = blockIdx.x, lane = threadIdx.x & 31;
@@ -58,21 +60,42 @@ __global__ void __launch_bounds__(kTcThreads, 8) kda_tree_conv_kernel(const Tree
   if (r.error == KDA_OK && r.slot < 0) return;
   const int first = blockIdx.z * p.run;
   const int past = r.n - first > p.run ? first + p.run : r.n;
-  // the first nodes' inputs, and the entries above a root (the newest first),
-  // are asked for before the tree is looked at
-  constexpr int kAhead = 4;
-  const uint16_t *x = p.x + (long long)r.t0 * (3 * D) + ch;
-  uint2 next[kAhead], h1, h2, h3;
+  // All is asked for before the tree is looked at (ancestors come before their
+  // nodes).  A warp's windows, one piece of memory, take the places of its last
+  // nodes' inputs until three entries of each channel are picked from them.
   if (r.error == KDA_OK && first < past) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      next[i] = __ldg(reinterpret_cast<const uint2 *>(
-          x + (long long)(first + i < past ? first + i : first) * (3 * D)));
-    const uint16_t *win = p.window + r.slot * p.slot_stride + (long long)ch * p.width;
+    const int late = past > p.width ? past - p.width : 0;
+    const int warp_ch = 4 * (group - lane), warp_at = threadIdx.x - lane;
+    uint2 *const held = rows + (3 + late) * kTcThreads + warp_at;
+    const auto held_at = [&](int byte) {  // of the warp's windows
+      return reinterpret_cast<char *>(held + (byte >> 8) * kTcThreads) + (byte & 255);
+    };
+    if (warp_ch < 3 * D) {
+      const uint16_t *win = p.window + r.slot * p.slot_stride + (long long)warp_ch * p.width;
+      for (int i = lane; i < 16 * p.width; i += 32) cp_async16(held_at(16 * i), win + 8 * i);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint16_t *x = p.x + (long long)r.t0 * (3 * D) + ch;
+    uint2 *to = rows + 3 * kTcThreads + threadIdx.x;
+    int t = 0;
+    for (; t < late; ++t, x += 3 * D, to += kTcThreads) cp_async8(to, x);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
     const int off = r.pending > 0 ? r.pending - 1 : 0;
-    h1 = window_entry(win, p.width, off + 2);
-    h2 = window_entry(win, p.width, off + 1);
-    h3 = window_entry(win, p.width, off);
+    uint2 h[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      uint32_t e[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        e[c] = *reinterpret_cast<const uint16_t *>(held_at(2 * ((4 * lane + c) * p.width + off + i)));
+      h[i] = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+    }
+    __syncwarp();
+    for (; t < past; ++t, x += 3 * D, to += kTcThreads) cp_async8(to, x);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) rows[i * kTcThreads + threadIdx.x] = h[i];
   }
   if (threadIdx.x < 32) {
     const bool ok = r.error == KDA_OK && load_tree(mp, r, parent, lane);
@@ -87,7 +110,9 @@ __global__ void __launch_bounds__(kTcThreads, 8) kda_tree_conv_kernel(const Tree
         const int a = parent[t];
         const int c = a >= 0 ? parent[a] : a - 1;
         const int e = c >= 0 ? parent[c] : c - 1;
-        above[t] = make_char4((char)a, (char)c, (char)e, 0);
+        // (row of node or entry s: s + 3)
+        taps[t] = make_uint2((uint32_t)(e + 3) | (uint32_t)(c + 3) << 16,
+                             (uint32_t)(a + 3) | (uint32_t)(t + 3) << 16);
       }
     }
   }
@@ -97,37 +122,25 @@ __global__ void __launch_bounds__(kTcThreads, 8) kda_tree_conv_kernel(const Tree
     w[i] = unpack4(__ldg(reinterpret_cast<const uint2 *>(p.w + (long long)(part * 4 + i) * D + hc)));
   bias = unpack4(p.bias != nullptr ? __ldg(reinterpret_cast<const uint2 *>(p.bias + ch))
                                    : make_uint2(0, 0));
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   if (!good || !active || first >= past) return;
-  uint16_t *out = (part == 0 ? p.q : (part == 1 ? p.k : p.v)) + (long long)r.t0 * D + hc;
-  const auto input = [&](int a) {
-    return a >= 0 ? __ldg(reinterpret_cast<const uint2 *>(x + (long long)a * (3 * D)))
-                  : (a == -1 ? h1 : (a == -2 ? h2 : h3));
-  };
-  const auto step = [&](uint2 own, int t) {
-    const char4 up = above[t];
-    const Four s3 = unpack4(own), s2 = unpack4(input(up.x)), s1 = unpack4(input(up.y)),
-               s0 = unpack4(input(up.z));
+  uint16_t *out =
+      (part == 0 ? p.q : (part == 1 ? p.k : p.v)) + (long long)(r.t0 + first) * D + hc;
+  const uint2 *mine = rows + threadIdx.x;
+#pragma unroll 2
+  for (int t = first; t < past; ++t, out += D) {
+    const uint2 tap = taps[t];
+    const Four s0 = unpack4(mine[(tap.x & 0xffffu) * kTcThreads]),
+               s1 = unpack4(mine[(tap.x >> 16) * kTcThreads]),
+               s2 = unpack4(mine[(tap.y & 0xffffu) * kTcThreads]),
+               s3 = unpack4(mine[(tap.y >> 16) * kTcThreads]);
     // in tap order, as in kda_layer_prologue
     Four z{ffma2(s0.a, w[0].a, bias.a), ffma2(s0.b, w[0].b, bias.b)};
     z = Four{ffma2(s1.a, w[1].a, z.a), ffma2(s1.b, w[1].b, z.b)};
     z = Four{ffma2(s2.a, w[2].a, z.a), ffma2(s2.b, w[2].b, z.b)};
     z = Four{ffma2(s3.a, w[3].a, z.a), ffma2(s3.b, w[3].b, z.b)};
-    *reinterpret_cast<uint2 *>(out + (long long)t * D) =
-        make_uint2(silu_pair(z.a), silu_pair(z.b));
-  };
-  // the next four nodes are asked for while four are worked on
-#pragma unroll 1
-  for (int t = first; t < past; t += kAhead) {
-    uint2 own[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) own[i] = next[i];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (t + kAhead + i < past) next[i] = input(t + kAhead + i);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (t + i < past) step(own[i], t + i);
+    *reinterpret_cast<uint2 *>(out) = make_uint2(silu_pair(z.a), silu_pair(z.b));
   }
 }
 
@@ -183,6 +196,12 @@ extern "C" int kda_tree_conv(const kda_bf16 *x, const kda_bf16 *conv_weight,
   while (run > 2 && (long long)B * channels * ((Q - 1) / run + 1) < 4LL * sms) run = (run + 1) / 2;
   p.run = run;
   const dim3 grid(B, channels, (Q - 1) / run + 1);
-  kda::kda_tree_conv_kernel<<<grid, kda::kTcThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  constexpr int kRow = kda::kTcThreads * (int)sizeof(uint2);
+  // (the largest call's, always: another thread's call may come in between)
+  if (cudaFuncSetAttribute(kda::kda_tree_conv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (3 + KDA_TREE_MAX_NODES) * kRow) != cudaSuccess)
+    return KDA_ERR_CUDA;
+  const int bytes = (3 + (Q > conv_width ? Q : conv_width)) * kRow;
+  kda::kda_tree_conv_kernel<<<grid, kda::kTcThreads, bytes, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -23,6 +23,8 @@ namespace {
 
 constexpr int kTrThreads = 256;
 constexpr int kTrWarps = kTrThreads / 32;
+constexpr int kTrNodes = 8;  // room for windows of up to kTrMaxQ nodes
+constexpr int kTrMaxQ = 6;
 
 // Shared memory of a CTA whose windows hold up to `nodes` (a multiple of 4)
 // nodes, in floats: X, [2 nodes][128]; kn and d, [nodes][128] each, whose
@@ -48,7 +50,6 @@ __host__ __device__ constexpr RowsLayout rows_layout(int nodes, int rows) {
   l.floats = l.dn + kDim;
   return l;
 }
-static_assert(rows_layout(kTreeNodes, kDim).floats * 4 <= 227 * 1024, "shared memory");
 
 template <bool BF16>
 __device__ __forceinline__ float4 state_load(const void *state, long long at) {
@@ -208,8 +209,9 @@ int launch_rows(const TreeVerifyParams &p, cudaStream_t stream) {
   const int nodes = round_up(p.maps.Q, 4);
   const int bytes = rows_layout(nodes, ROWS).floats * 4;
   const auto kernel = kda_tree_rows_kernel<ROWS, BF16>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-      cudaSuccess)
+  // (the largest call's, always: another thread's call may come in between)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           rows_layout(kTrNodes, ROWS).floats * 4) != cudaSuccess)
     return KDA_ERR_CUDA;
   kernel<<<(unsigned)p.maps.B * p.H * (kDim / ROWS), kTrThreads, bytes, stream>>>(p, nodes);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
@@ -284,7 +286,7 @@ extern "C" int kda_tree_verify(
   // 32 / by whole pages / on the tensor cores: 4 nodes, 32 items 14 / 15 / 17,
   // 192 items 25 / 19 / 25, 1536 items 130 / 74 / 83; 8 nodes, 32 items 17 / 19 /
   // 17, 1536 items 181 / 95 / 85; 15 nodes, 32 items 23 / 25 / 17.
-  if (Q > 6) return kda::launch_tree_mma(p, bf16, sms, st);
+  if (Q > kda::kTrMaxQ) return kda::launch_tree_mma(p, bf16, sms, st);
   if ((long long)B * H * 4 <= sms)
     return bf16 ? kda::launch_rows<32, true>(p, st) : kda::launch_rows<32, false>(p, st);
   return bf16 ? kda::launch_rows<128, true>(p, st) : kda::launch_rows<128, false>(p, st);
