@@ -20,6 +20,8 @@
 // doubles behind them: FP64 for each weight would cost more than reading it.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kda_launch.h"
 #include "kda_tree.cuh"
 
@@ -31,7 +33,7 @@ constexpr int kDaThreads = 256;
 constexpr int kDaWarps = kDaThreads / 32;
 constexpr int kDaTile = 512;
 constexpr int kDaPer = kDaTile / 32;  // weights a lane
-constexpr int kDaOccupancy = 4;       // CTAs an SM
+constexpr int kDaOccupancy = 2;       // CTAs an SM
 constexpr int kDaTiles = KDA_MAX_VOCAB / kDaTile;  // of a CTA, at most
 
 struct AcceptParams {
@@ -70,14 +72,16 @@ struct TileAccess {
   static __device__ __forceinline__ int index(int j, int lane) {
     return (j / kPiece) * (32 * kPiece) + lane * kPiece + j % kPiece;
   }
+  // as they are in memory: pieces, or a weight each
+  static constexpr int kRaw = VEC ? kDaPer / kPiece : kDaPer;
+  using Raw = typename std::conditional<VEC, uint4, T>::type;
   static __device__ __forceinline__ void load(const T *row, int first, int vocab, int lane,
-                                              float (&w)[kDaPer]) {
-    if constexpr (VEC) {
-      uint4 raw[kDaPer / kPiece];
+                                              Raw (&raw)[kRaw]) {
 #pragma unroll
-      for (int c = 0; c < kDaPer / kPiece; ++c) {
-        const int i = first + index(c * kPiece, lane);
-        raw[c] = make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < kRaw; ++c) {
+      const int i = first + index(c * kPiece, lane);
+      raw[c] = Raw{};
+      if constexpr (VEC) {
         if (i + kPiece <= vocab) {
           raw[c] = __ldg(reinterpret_cast<const uint4 *>(row + i));
         } else if (i < vocab) {  // the row's last piece, in part
@@ -86,9 +90,15 @@ struct TileAccess {
           for (int e = 0; e < kPiece; ++e) last[e] = i + e < vocab ? row[i + e] : T(0);
           memcpy(&raw[c], last, 16);
         }
+      } else {
+        if (i < vocab) raw[c] = __ldg(row + i);
       }
+    }
+  }
+  static __device__ __forceinline__ void values(const Raw (&raw)[kRaw], float (&w)[kDaPer]) {
 #pragma unroll
-      for (int c = 0; c < kDaPer / kPiece; ++c) {
+    for (int c = 0; c < kRaw; ++c) {
+      if constexpr (VEC) {
         const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
         for (int e = 0; e < kPiece; ++e)
@@ -96,12 +106,10 @@ struct TileAccess {
               sizeof(T) == 4 ? __uint_as_float(x[e % 4])
                              : __uint_as_float(e & 1 ? x[e / 2 % 4] & 0xffff0000u
                                                      : x[e / 2 % 4] << 16);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kDaPer; ++j) {
-        const int i = first + index(j, lane);
-        w[j] = i < vocab ? weight_at(row, i) : 0.f;
+      } else if constexpr (sizeof(T) == 4) {
+        w[c] = raw[c];
+      } else {
+        w[c] = bf16_bits_to_f32(raw[c]);
       }
     }
   }
@@ -255,53 +263,56 @@ __device__ bool walk(const AcceptParams &p, const TreeRequest &r, int b, int lan
   return true;
 }
 
-// The weights of a tile: max(p - q, 0), p without the removed tokens, or p;
-// err: what the difference's rounding left out.
-template <typename T, bool VEC>
-__device__ __forceinline__ void tile_weights(const T *prow, const T *qrow, const int *removed,
-                                             int n_removed, int tile, int vocab, int lane,
-                                             float (&w)[kDaPer], float (&err)[kDaPer]) {
-  using A = TileAccess<T, VEC>;
-  A::load(prow, tile * kDaTile, vocab, lane, w);
-  if (qrow != nullptr) {
-    float q[kDaPer];
-    A::load(qrow, tile * kDaTile, vocab, lane, q);
-#pragma unroll
-    for (int j = 0; j < kDaPer; ++j) {
-      const float d = w[j] - q[j];
-      const bool more = w[j] > q[j];
-      err[j] = more ? (w[j] - d) - q[j] : 0.f;
-      w[j] = more ? d : 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < kDaPer; ++j) {
-      w[j] = w[j] > 0.f ? w[j] : 0.f;
-      err[j] = 0.f;
-    }
-    for (int i = 0; i < n_removed; i += 32) {
-      const int x = i + lane < n_removed ? removed[i + lane] : -1;
-      for (uint32_t m = __ballot_sync(0xffffffffu, x >= 0 && x / kDaTile == tile); m != 0;
-           m &= m - 1) {
-        const int at = __shfl_sync(0xffffffffu, x, __ffs(m) - 1) % kDaTile;
-#pragma unroll
-        for (int j = 0; j < kDaPer; ++j)
-          if (A::index(j, lane) == at) w[j] = 0.f;
-      }
-    }
-  }
-}
-
-template <typename T, bool VEC>
+// The sums of a CTA's tiles of weights max(p - q, 0), p without the removed
+// tokens, or p, a warp a tile; the next tile is on its way meanwhile.
+template <typename T, bool VEC, bool DIFF>
 __device__ __forceinline__ void tile_sums(const T *prow, const T *qrow, int n_removed, int vocab,
                                           int first, int tiles, AcceptSmem &sm) {
+  using A = TileAccess<T, VEC>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  typename A::Raw p_raw[A::kRaw], q_raw[A::kRaw];
+  const auto ask = [&](int i) {
+    A::load(prow, (first + i) * kDaTile, vocab, lane, p_raw);
+    if (DIFF) A::load(qrow, (first + i) * kDaTile, vocab, lane, q_raw);
+  };
+  if (warp < tiles) ask(warp);
   for (int i = warp; i < tiles; i += kDaWarps) {
-    float w[kDaPer], err[kDaPer];
-    tile_weights<T, VEC>(prow, qrow, sm.removed, n_removed, first + i, vocab, lane, w, err);
-    Sum2 s{0.f, 0.f};
+    float w[kDaPer], q[kDaPer];
+    A::values(p_raw, w);
+    if (DIFF) A::values(q_raw, q);
+    if (i + kDaWarps < tiles) ask(i + kDaWarps);
+    if (!DIFF) {
 #pragma unroll
-    for (int j = 0; j < kDaPer; ++j) s.add(w[j], err[j]);
+      for (int j = 0; j < kDaPer; ++j) w[j] = w[j] > 0.f ? w[j] : 0.f;
+      for (int k = 0; k < n_removed; k += 32) {
+        const int x = k + lane < n_removed ? sm.removed[k + lane] : -1;
+        for (uint32_t m = __ballot_sync(0xffffffffu, x >= 0 && x / kDaTile == first + i); m != 0;
+             m &= m - 1) {
+          const int at = __shfl_sync(0xffffffffu, x, __ffs(m) - 1) % kDaTile;
+#pragma unroll
+          for (int j = 0; j < kDaPer; ++j)
+            if (A::index(j, lane) == at) w[j] = 0.f;
+        }
+      }
+    }
+    Sum2 s{0.f, 0.f}, s2{0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kDaPer; ++j) {
+      float x = w[j], err = 0.f;
+      if (DIFF) {
+        // (what the difference's rounding leaves out is itself a float)
+        const float d = w[j] - q[j];
+        const bool more = w[j] > q[j];
+        err = more ? (w[j] - d) - q[j] : 0.f;
+        x = more ? d : 0.f;
+      }
+      if (j % 2) {
+        s2.add(x, err);
+      } else {
+        s.add(x, err);
+      }
+    }
+    s.add(s2.hi, s2.lo);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
       const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
@@ -372,10 +383,16 @@ __global__ void __launch_bounds__(kDaThreads, kDaOccupancy)
   double mine, upto, before, whole, goal;
   int owner, pass = 0;
   for (;; ++pass) {
-    if (vec) {
-      tile_sums<T, true>(prow, qrow, n_removed, p.vocab, first, tiles, sm);
+    if (qrow != nullptr) {
+      if (vec) {
+        tile_sums<T, true, true>(prow, qrow, 0, p.vocab, first, tiles, sm);
+      } else {
+        tile_sums<T, false, true>(prow, qrow, 0, p.vocab, first, tiles, sm);
+      }
+    } else if (vec) {
+      tile_sums<T, true, false>(prow, qrow, n_removed, p.vocab, first, tiles, sm);
     } else {
-      tile_sums<T, false>(prow, qrow, n_removed, p.vocab, first, tiles, sm);
+      tile_sums<T, false, false>(prow, qrow, n_removed, p.vocab, first, tiles, sm);
     }
     __syncthreads();
     // a thread takes `each` tiles, one after the other
@@ -512,7 +529,9 @@ extern "C" int kda_draft_accept(const void *target, const void *draft, int probs
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
   const int sms = kda::device_sm_count(dev);
-  // as many CTAs a request as still run all at once
+  // As many CTAs a request as run all at once, two to an SM.  131072 FP32 weights
+  // and drafts, us by 1 / 2 / 4 / 8 CTAs a request: 64 requests 54 / 38 / 33 / 40,
+  // 128 requests 58 / 48 / 48 / 62, 256 requests 72 / 72 / 81 / 97.
   int ctas = kda::kDaMaxCtas;
   while (ctas > 1 && (long long)B * ctas > (long long)kda::kDaOccupancy * sms) ctas /= 2;
   cudaLaunchAttribute attr[1];
