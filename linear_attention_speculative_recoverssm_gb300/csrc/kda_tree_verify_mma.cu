@@ -193,7 +193,7 @@ struct TreeMma {
   static constexpr int kR0 = kPageWarps, kT0 = kR0 + kRWarps, kIssue0 = kT0 + kTWarps,
                        kTask0 = kIssue0 + 2, kNode0 = kTask0 + 1, kNodeWarps = kWarps - kNode0;
   // registers a thread: at launch, of pages (whole warpgroups), of the others
-  static constexpr int kPageRegs = 88, kOtherRegs = 56;
+  static constexpr int kPageRegs = kPageWarps == 4 ? 120 : 88, kOtherRegs = 56;
   static_assert(kPageWarps * kPageRegs + (kWarps - kPageWarps) * kOtherRegs <= kWarps * 64,
                 "what the warps of pages take, the others have given");
   static_assert(kR0 % 4 == 0 && kT0 % 4 == 0, "a warp reaches the tensor memory lanes of its number");
@@ -238,16 +238,16 @@ struct TreeMma {
   static_assert(kBytes <= 227 * 1024 && 2 * kBytes > 228 * 1024, "one CTA an SM");
 };
 
-// A page's part of a thread: rows 16 rh + lane / 4 + 8 i of the warp's 32,
-// keys 16 j + 4 (lane % 4) + 0 .. 3 of the warp's 16 J; one rh at a time.
-template <bool BF16, int J>
-struct PageRegs {
+// A thread's part of 16 rows and 32 keys of the page: rows lane / 4 + 8 i, keys 16
+// j + 4 (lane % 4) + 0 .. 3.
+template <bool BF16>
+struct PageUnit {
   using Four = typename std::conditional<BF16, uint2, float4>::type;
-  Four s[J][2];  // [j][i]
+  Four s[2][2];  // [j][i]
   __device__ __forceinline__ void load(const void *pool, long long at) {
     const auto *from = reinterpret_cast<const Four *>(static_cast<const char *>(pool) + at * (BF16 ? 2 : 4));
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) s[j][i] = __ldcs(from + (8 * i * kDim + 16 * j) / 4);
   }
@@ -374,37 +374,44 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
   }
 
   if (warp < L::kR0) {
-    // ======== pages: rows 32 quarter .. + 31, keys 16 J which .. + 16 J - 1
-    constexpr int J = 32 / L::kPageWarps, kThreads = 32 * L::kPageWarps;
+    // ======== pages: rows 32 quarter .. + 31, keys kKeys which .. + kKeys - 1
+    // units of 16 rows and 32 keys, those of the same rows first; the next (of BF16
+    // pages the next four) on its way
+    constexpr int kUnits = 32 / L::kPageWarps, kKeys = 16 * kUnits, kThreads = 32 * L::kPageWarps;
+    constexpr int kAhead = BF16 ? 4 : 1, kRecs = kMaxQ / L::kPageWarps;
+    const auto unit_at = [](int e) { return 16 * (e / (kUnits / 2)) * kDim + 32 * (e % (kUnits / 2)); };
     const int quarter = warp & 3, which = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     float *const rk = reinterpret_cast<float *>(mem + L::kReplayK);
     float *const rd = reinterpret_cast<float *>(mem + L::kReplayD);
     float *const ru = reinterpret_cast<float *>(mem + L::kReplayU);
     float *const rdn = reinterpret_cast<float *>(mem + L::kReplayDn);
-    const int k0 = 16 * J * which + 4 * (lane & 3);
+    const int k0 = kKeys * which + 4 * (lane & 3);
     TreeItems it;
     int done = 0;  // items with nodes
-    PageRegs<BF16, J> pg[2];
-    uint2 rec_k, rec_g;
-    float4 rec_u;
-    // an item's records (a warp one) and the first half of its rows, ahead of its
-    // turn; and the next head's page on its way to L2
+    PageUnit<BF16> pg[kUnits];
+    uint2 rec_k[kRecs], rec_g[kRecs];
+    float4 rec_u[kRecs];
+    // an item's records (a warp one) and first units, ahead of its turn; and the
+    // next head's page on its way to L2
     const auto page_part = [&] {
       return page_of(it.slot, it.h) + (long long)(32 * quarter + lane / 4) * kDim + k0;
     };
     const auto ask = [&] {
-      if (warp < it.pending) {
-        const long long row = (long long)it.h * mp.rq + warp;
-        const uint2 *rec = reinterpret_cast<const uint2 *>(p.kg + it.row * p.kg_stride + row * 2 * kDim) + lane;
-        rec_k = __ldg(rec);
-        rec_g = __ldg(rec + 32);
-        rec_u = __ldg(reinterpret_cast<const float4 *>(p.corr + it.row * p.corr_stride + row * kDim) + lane);
-      }
-      pg[0].load(p.state, page_part());
+#pragma unroll
+      for (int i = 0; i < kRecs; ++i)
+        if (warp + i * L::kPageWarps < it.pending) {
+          const long long row = (long long)it.h * mp.rq + warp + i * L::kPageWarps;
+          const uint2 *rec = reinterpret_cast<const uint2 *>(p.kg + it.row * p.kg_stride + row * 2 * kDim) + lane;
+          rec_k[i] = __ldg(rec);
+          rec_g[i] = __ldg(rec + 32);
+          rec_u[i] = __ldg(reinterpret_cast<const float4 *>(p.corr + it.row * p.corr_stride + row * kDim) + lane);
+        }
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) pg[e].load(p.state, page_part() + unit_at(e));
       if (it.h + 1 < it.h1)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < (BF16 ? 256 : 512) / kThreads; ++i)
           prefetch_l2(static_cast<const char *>(p.state) + page_of(it.slot, it.h + 1) * (BF16 ? 2 : 4) +
                       (i * kThreads + tid) * 128);
     };
@@ -415,78 +422,72 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       const int replay = it.pending;
       const long long page = page_part();
       if (replay > 0) {
-        if (warp < replay) {
-          const float4 k = bf16x4(rec_k);
-          const float4 dt = __ldg(reinterpret_cast<const float4 *>(p.dt_bias + it.h * kDim) + lane);
-          const float a = expf(__ldg(p.A_log + it.h));
-          sts4(rk + warp * kDim + 4 * lane, scale4(k, rsqrtf(warp_sum(dot4(k, k)) + kNormEps)));
-          sts4(rd + warp * kDim + 4 * lane, decay4(a, bf16x4(rec_g), dt, p.lower_bound));
-          sts4(ru + warp * kDim + 4 * lane, rec_u);
-        }
+#pragma unroll
+        for (int i = 0; i < kRecs; ++i)
+          if (const int t = warp + i * L::kPageWarps; t < replay) {
+            const float4 k = bf16x4(rec_k[i]);
+            const float4 dt = __ldg(reinterpret_cast<const float4 *>(p.dt_bias + it.h * kDim) + lane);
+            const float a = expf(__ldg(p.A_log + it.h));
+            sts4(rk + t * kDim + 4 * lane, scale4(k, rsqrtf(warp_sum(dot4(k, k)) + kNormEps)));
+            sts4(rd + t * kDim + 4 * lane, decay4(a, bf16x4(rec_g[i]), dt, p.lower_bound));
+            sts4(ru + t * kDim + 4 * lane, rec_u[i]);
+          }
         named_bar(3, kThreads);
         if (tid < kDim) replay_suffix(rk, rd, rdn, replay, tid);
         named_bar(3, kThreads);
       }
-      // S_n, and its parts to tensor memory, 16 rows and 32 keys at a time; the
-      // second half of the rows is asked for once the first is replayed
+      // S_n, and its parts to tensor memory
+      if (it.n > 0 && done > 0) {
+        it.wait(&bars->a_free, (uint32_t)(done - 1) & 1u);
+        tc_fence_after();
+      }
 #pragma unroll
-      for (int rh = 0; rh < 2; ++rh) {
+      for (int e = 0; e < kUnits; ++e) {
+        const int rh = e / (kUnits / 2), k32 = 32 * (e % (kUnits / 2));
         if constexpr (!BF16) {
           if (replay > 0) {
             const float *up = ru + 32 * quarter + 16 * rh + lane / 4;
+            const float *kp = rk + k0 + k32, *dp = rdn + k0 + k32;
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-              const float4 x = lds4(rdn + k0 + 16 * j);
-              pg[rh].s[j][0] = fmul4(pg[rh].s[j][0], x);
-              pg[rh].s[j][1] = fmul4(pg[rh].s[j][1], x);
+            for (int j = 0; j < 2; ++j) {
+              const float4 x = lds4(dp + 16 * j);
+              pg[e].s[j][0] = fmul4(pg[e].s[j][0], x);
+              pg[e].s[j][1] = fmul4(pg[e].s[j][1], x);
             }
 #pragma unroll 1
-            for (int t = 0; t < replay; ++t) {
-              const float u0 = up[t * kDim], u1 = up[t * kDim + 8];
-#pragma unroll
-              for (int j = 0; j < J; ++j) {
-                const float4 x = lds4(rk + t * kDim + k0 + 16 * j);
-                pg[rh].s[j][0] = ffma4s(u0, x, pg[rh].s[j][0]);
-                pg[rh].s[j][1] = ffma4s(u1, x, pg[rh].s[j][1]);
-              }
+            for (int t = 0; t < replay; ++t, kp += kDim, up += kDim) {
+              const float u0 = up[0], u1 = up[8];
+              const float4 x0 = lds4(kp), x1 = lds4(kp + 16);
+              pg[e].s[0][0] = ffma4s(u0, x0, pg[e].s[0][0]);
+              pg[e].s[0][1] = ffma4s(u1, x0, pg[e].s[0][1]);
+              pg[e].s[1][0] = ffma4s(u0, x1, pg[e].s[1][0]);
+              pg[e].s[1][1] = ffma4s(u1, x1, pg[e].s[1][1]);
             }
-            float *to = static_cast<float *>(p.state) + page + 16 * rh * kDim;
+            float *to = static_cast<float *>(p.state) + page + unit_at(e);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-              stg4(to + 16 * j, pg[rh].s[j][0]);
-              stg4(to + 8 * kDim + 16 * j, pg[rh].s[j][1]);
-            }
+            for (int c = 0; c < 4; ++c) stg4(to + 8 * (c % 2) * kDim + 16 * (c / 2), pg[e].s[c / 2][c % 2]);
           }
         }
-        if (rh == 0) pg[1].load(p.state, page + 16 * kDim);
-        if (it.n > 0) {
-          if (rh == 0 && done > 0) {
-            it.wait(&bars->a_free, (uint32_t)(done - 1) & 1u);
-            tc_fence_after();
-          }
+        if (it.n > 0)
 #pragma unroll
-          for (int j0 = 0; j0 < J; j0 += 2)
+          for (int part = 0; part < (BF16 ? 1 : 3); ++part) {
+            uint32_t w[8];
 #pragma unroll
-            for (int part = 0; part < (BF16 ? 1 : 3); ++part) {
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                auto &s = pg[rh].s[j0 + e / 2][e % 2];
-                if constexpr (BF16) {
-                  w[2 * e] = s.x;
-                  w[2 * e + 1] = s.y;
-                } else {
-                  float2 lo = make_float2(s.x, s.y), hi = make_float2(s.z, s.w);
-                  w[2 * e] = take_part(lo);
-                  w[2 * e + 1] = take_part(hi);
-                  s = make_float4(lo.x, lo.y, hi.x, hi.y);
-                }
+            for (int c = 0; c < 4; ++c) {
+              auto &s = pg[e].s[c / 2][c % 2];
+              if constexpr (BF16) {
+                w[2 * c] = s.x;
+                w[2 * c + 1] = s.y;
+              } else {
+                float2 lo = make_float2(s.x, s.y), hi = make_float2(s.z, s.w);
+                w[2 * c] = take_part(lo);
+                w[2 * c + 1] = take_part(hi);
+                s = make_float4(lo.x, lo.y, hi.x, hi.y);
               }
-              tm_store_16x16(lanes + ((uint32_t)(16 * rh) << 16) + kTmPartCols * part +
-                                 8 * (J * which + j0),
-                             w);
             }
-        }
+            tm_store_16x16(lanes + ((uint32_t)(16 * rh) << 16) + kTmPartCols * part + (kKeys * which + k32) / 2, w);
+          }
+        if (e + kAhead < kUnits) pg[e + kAhead].load(p.state, page + unit_at(e + kAhead));
       }
       if (it.n > 0) {
         tm_store_wait();
