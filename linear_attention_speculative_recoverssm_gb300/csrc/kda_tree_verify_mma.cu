@@ -24,8 +24,8 @@
 // The page goes from HBM to registers in the layout of tcgen05.st's 16x256b
 // (16 bytes a lane, four lanes to 64 bytes of a row), is replayed there,
 // written back from there, split there, and stored to tensor memory as the
-// A operand: it never passes through shared memory, which holds the nodes.
-// R goes the same way.
+// A operand.  R goes the same way.  Where shared memory has room beside the
+// nodes, an FP32 page waits there first (kStaged).
 //
 // R and [T; C] are multiplied whole, and zero times NaN is NaN: an R that is
 // not finite is left out as zero, and the outputs of its node and of those
@@ -35,9 +35,16 @@
 // the other, some items apart, as barriers in shared memory let them: the
 // requests (validated, their paths listed) a warp; nodes to X and Y; pages; T
 // and C; R and the outputs; and two warps that issue the products, of X and
-// of R.  One phase after the other by all warps, two CTAs an SM, took 2.4
-// times as long: each phase is a chain of latencies (shared memory, the
-// shuffles of a norm, a product's hand-off) that more warps do not shorten.
+// of R.  Each kind is a chain of latencies (shared memory, the shuffles of a
+// norm, a product's hand-off); one phase after the other by all warps, two CTAs
+// an SM, was slower: 804 against 646 us (128 windows of 64 nodes and 64 heads),
+// 111 against 91 (48 of up to 32 nodes, 32 heads), 115 against 113 (100 of 24,
+// BF16 pages).
+//
+// Those three move 2053, 274 and 243 MB at 3.2, 3.0 and 2.1 TB/s (a copy's rate:
+// 6.7).  What bounds them is not HBM but instructions and the chains' latencies:
+// 43 thousand warp instructions an item of 64 nodes, 46% of the issue slots,
+// half of the shared memory's wavefronts, a quarter of the tensor pipe's cycles.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -231,7 +238,13 @@ struct TreeMma {
   static constexpr uint32_t kBad = kNorms + 2 * NC * 4;    // [NC / 8][128] nodes, a byte's bits
   static constexpr uint32_t kTasks = kBad + NC / 8 * kDim;
   static constexpr uint32_t kParent = kTasks + 4 * sizeof(TreeTask);
-  static constexpr uint32_t kBars = kParent + kTreeNodes;
+  // An FP32 page comes here by asynchronous copies, a whole item ahead, 8 KB a warp,
+  // where there is room (48 requests of up to 32 nodes: 97 -> 91 us); else to
+  // registers, a unit ahead.  BF16 pages, which have four units ahead in registers,
+  // gain nothing by it (113 us either way).
+  static constexpr bool kStaged = NC <= 32 && !BF16;
+  static constexpr uint32_t kPage = round_up(kParent + kTreeNodes, 128);
+  static constexpr uint32_t kBars = kPage + (kStaged ? kPageWarps * 8192 : 0);
   static constexpr uint32_t kSlot = kBars + sizeof(TreeBars);
   static constexpr uint32_t kBytes = kSlot + 8;
   static_assert(kTasks % 8 == 0 && kBars % 8 == 0 && sizeof(TreeTask) % 8 == 0, "alignment");
@@ -250,6 +263,20 @@ struct PageUnit {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) s[j][i] = __ldcs(from + (8 * i * kDim + 16 * j) / 4);
+  }
+  // From a warp's staged rows, 256 bytes of each: 16-byte piece c of row r stands at
+  // place(r, c), where no two of eight lanes meet in a bank.
+  static __device__ __forceinline__ int place(int r, int c) {
+    return r * 256 + ((c >> 2 ^ (r & 1)) << 6) + (c & 3) * 16;
+  }
+  __device__ __forceinline__ void load_staged(const uint8_t *rows, int row, int key, int lane) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = row + lane / 4 + 8 * i, c = (key + 16 * j) / 4 + (lane & 3);
+        s[j][i] = *reinterpret_cast<const Four *>(rows + place(r, c));
+      }
   }
 };
 
@@ -376,9 +403,10 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
   if (warp < L::kR0) {
     // ======== pages: rows 32 quarter .. + 31, keys kKeys which .. + kKeys - 1
     // units of 16 rows and 32 keys, those of the same rows first; the next (of BF16
-    // pages the next four) on its way
+    // pages the next four) on its way, or the next item's page, to shared memory
     constexpr int kUnits = 32 / L::kPageWarps, kKeys = 16 * kUnits, kThreads = 32 * L::kPageWarps;
-    constexpr int kAhead = BF16 ? 4 : 1, kRecs = kMaxQ / L::kPageWarps;
+    constexpr int kAhead = L::kStaged ? 0 : BF16 ? 4 : 1, kRecs = kMaxQ / L::kPageWarps;
+    uint8_t *const staged = mem + L::kPage + warp * 8192;
     const auto unit_at = [](int e) { return 16 * (e / (kUnits / 2)) * kDim + 32 * (e % (kUnits / 2)); };
     const int quarter = warp & 3, which = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
@@ -407,8 +435,16 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
           rec_g[i] = __ldg(rec + 32);
           rec_u[i] = __ldg(reinterpret_cast<const float4 *>(p.corr + it.row * p.corr_stride + row * kDim) + lane);
         }
+      if constexpr (L::kStaged) {
+        const float *from = static_cast<const float *>(p.state) + page_of(it.slot, it.h) +
+                            32 * quarter * kDim + kKeys * which;
+#pragma unroll 4
+        for (int i = lane; i < 512; i += 32)
+          cp_async16(staged + PageUnit<BF16>::place(i >> 4, i & 15), from + (i >> 4) * kDim + 4 * (i & 15));
+      } else {
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e) pg[e].load(p.state, page_part() + unit_at(e));
+        for (int e = 0; e < kAhead; ++e) pg[e].load(p.state, page_part() + unit_at(e));
+      }
       if (it.h + 1 < it.h1)
 #pragma unroll
         for (int i = 0; i < (BF16 ? 256 : 512) / kThreads; ++i)
@@ -441,9 +477,14 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         it.wait(&bars->a_free, (uint32_t)(done - 1) & 1u);
         tc_fence_after();
       }
+      if (L::kStaged) {
+        cp_async_wait_all();
+        __syncwarp();
+      }
 #pragma unroll
       for (int e = 0; e < kUnits; ++e) {
         const int rh = e / (kUnits / 2), k32 = 32 * (e % (kUnits / 2));
+        if constexpr (L::kStaged) pg[e].load_staged(staged, 16 * rh, k32, lane);
         if constexpr (!BF16) {
           if (replay > 0) {
             const float *up = ru + 32 * quarter + 16 * rh + lane / 4;
@@ -487,7 +528,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
             }
             tm_store_16x16(lanes + ((uint32_t)(16 * rh) << 16) + kTmPartCols * part + (kKeys * which + k32) / 2, w);
           }
-        if (e + kAhead < kUnits) pg[e + kAhead].load(p.state, page + unit_at(e + kAhead));
+        if (!L::kStaged && e + kAhead < kUnits) pg[(e + kAhead) % kUnits].load(p.state, page + unit_at(e + kAhead));
       }
       if (it.n > 0) {
         tm_store_wait();
@@ -496,10 +537,12 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         ++done;
       }
       more = it.next(lane);
+      __syncwarp();  // (the staged rows are read)
       if (more) ask();
       // (the replay's operands are read)
       if (named_bar_or(3, kThreads, !it.ok)) more = it.ok = false;
     }
+    if (L::kStaged) cp_async_wait_all();
     ok = it.ok;
   } else if (warp < L::kT0) {
     // ======== R and the outputs: a row a lane, eight nodes at a time
