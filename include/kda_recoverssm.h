@@ -707,9 +707,12 @@ int kda_tree_conv(const kda_bf16 *x, const kda_bf16 *conv_weight, const kda_bf16
  * takes the accepted path's.  The records are only read.  The replay does not
  * depend on the window: it runs for an empty one too, and with n_tokens == 0.
  * Inert requests get zeros in `out`, and nothing else is written.
- *   What is held in fewer bits: the products of the state with the nodes'
- *   keys and queries take their operands with 22 bits (TF32 in two parts);
- *   states, sums, norms, gates and decays are FP32.
+ *   What is held in fewer bits: windows of more than six nodes form the
+ *   products of the state and of pairs of nodes from operands in three BF16
+ *   parts (24 bits; a gate path whose decays multiply to less than 2^-110 or
+ *   so loses its last part); states, sums, norms, gates and decays are FP32.
+ *   A NaN or an infinity in a node, its gates or a state row reaches that
+ *   node's descendants (that row) and no other node.
  *   q, k, v, raw_g, out [n_tokens, H, 128], raw_beta [n_tokens, H] BF16;
  *   A_log [H], dt_bias [H, 128], node_corr [n_tokens, H, 128] FP32;
  *   state_pool [n_slots, H, 128, 128] of state_dtype, slot stride

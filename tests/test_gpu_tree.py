@@ -6,7 +6,7 @@ value); before that, corrections and states are off by 1e-4 of the head's
 largest value at most, the framework's bound for FP32 states (its parts are
 derived in prompt_testutil: decays good to 2^-22, here over at most 16 tokens,
 sums of 128 products, 128 2^-24, and of at most eight corrections).  The
-products' operands hold 22 bits: 2 2^-22 of |S row| |x| <= 1e-6 of it.
+products' operands hold 22 bits at least: 2 2^-22 of |S row| |x| <= 1e-6 of it.
 """
 import numpy as np
 import pytest
