@@ -33,24 +33,29 @@
 //
 // One CTA an SM, whose warps divide the work by its kind and run one behind
 // the other, some items apart, as barriers in shared memory let them: the
-// requests (validated, their paths listed) a warp; nodes to X and Y; pages; T
-// and C; R and the outputs; and two warps that issue the products, of X and
-// of R.  Each kind is a chain of latencies (shared memory, the shuffles of a
+// requests (validated, their paths listed, copies of their nodes sent for) a
+// warp; nodes to X and Y; pages; T and C; R and the outputs; and two warps that
+// issue the products, of X and of R.  Each kind is a chain of latencies (shared memory, the shuffles of a
 // norm, a product's hand-off); one phase after the other by all warps, two CTAs
 // an SM, was slower: 804 against 646 us (128 windows of 64 nodes and 64 heads),
-// 111 against 91 (48 of up to 32 nodes, 32 heads), 115 against 113 (100 of 24,
+// 111 against 89 (48 of up to 32 nodes, 32 heads), 115 against 101 (100 of 24,
 // BF16 pages).
 //
-// Those three move 2053, 274 and 243 MB at 3.2, 3.0 and 2.1 TB/s (a copy's rate:
-// 6.7).  What bounds them is not HBM but instructions and the chains' latencies:
-// 43 thousand warp instructions an item of 64 nodes, 46% of the issue slots,
-// half of the shared memory's wavefronts, a quarter of the tensor pipe's cycles.
+// Those three move 2053, 274 and 243 MB at 3.2, 3.1 and 2.4 TB/s (a copy's rate:
+// 6.7).  What bounds them is not HBM but instructions, their fetch, and the chains'
+// latencies: 43 thousand warp instructions an item of 64 nodes, 18 of 24, half of
+// the issue slots, half of the shared memory's wavefronts, a quarter of the
+// tensor pipe's cycles.  The roles' code, all of it in use at once, is more than
+// an SM's instruction cache holds: loops are rolled up wherever their state
+// allows it (BF16 pages, 24 nodes: 115 -> 101 us, the cache's hits from 64 to 84%
+// of the requests).
 #include <cuda_runtime.h>
 
 #include <type_traits>
 
 #include "kda_launch.h"
 #include "kda_tcgen05.cuh"
+#include "kda_tensor_map.h"
 #include "kda_tree_verify.cuh"
 
 namespace kda {
@@ -156,6 +161,14 @@ __device__ __forceinline__ void prefetch_l2(const void *at) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
 }
 
+// A box of a tensor on its way to L2 (coordinates as in tma_load_3d).
+__device__ __forceinline__ void prefetch_box(const void *tmap, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -166,6 +179,19 @@ __device__ __forceinline__ uint32_t take_part(float2 &x) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(x.y), "f"(x.x));
   x = __fadd2_rn(x, make_float2(-__uint_as_float(w << 16), -__uint_as_float(w & 0xffff0000u)));
   return w;
+}
+
+// mbar_wait_bounded in few instructions: the roles' code, all of it in use at
+// once, is more than an SM's instruction cache holds.
+__device__ __forceinline__ bool tm_wait(uint64_t *bar, uint32_t parity) {
+  static_assert(kWaitLimitNs < 0x7fffffff, "32 bits of the timer");
+  uint32_t start = 0, now;
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 1000000u))) return true;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+    if (start == 0) start = now | 1u;  // (odd: it may lie a nanosecond ahead)
+    if ((int)(now - start) > (int)kWaitLimitNs) return false;
+  }
 }
 
 // A request as its warp hands it to the others: heads h0 .. h1 - 1 of it are this
@@ -181,12 +207,13 @@ struct TreeTask {
 // its place may be written again.
 struct TreeBars {
   uint64_t task_full[4], task_free[4];
+  uint64_t raw_full[2], raw_free[2];  // keys, queries and gates as they are
   uint64_t x_full, x_free, y_free;  // X and Y
   uint64_t p_full, p_free;          // P in tensor memory
   uint64_t a_full, a_free;          // the page's parts
   uint64_t d_full[2], d_free[2];    // w and y, until o is out
   uint64_t t_full, t_free;          // [T; C]
-  uint64_t r_full, o_full;          // R's parts; u and o
+  uint64_t r_full[2], o_full[2];    // R's parts; u and o
   uint64_t done[2];                 // every product that a warp issued
 };
 
@@ -205,13 +232,17 @@ struct TreeMma {
                 "what the warps of pages take, the others have given");
   static_assert(kR0 % 4 == 0 && kT0 % 4 == 0, "a warp reaches the tensor memory lanes of its number");
   static constexpr int kThreads = 32 * kWarps;
-  // tensor memory: the page, w and y (twice where there is room), P, R
+  // tensor memory: the page, w and y (twice where there is room), P, R (as often)
   static constexpr int kDBufs = NC <= 32 ? 2 : 1;
-  static constexpr uint32_t kTmP = kTmD + kDBufs * 2 * NC, kTmR = kTmP + NC;
-  static_assert(kTmR + 3 * NC / 2 <= 512, "tensor memory");
+  // P: by part of Y, where there is room
+  static constexpr int kPParts = NC <= 32 ? 3 : 1;
+  static constexpr uint32_t kTmP = kTmD + kDBufs * 2 * NC, kTmR = kTmP + kPParts * NC;
+  static_assert(kTmR + kDBufs * 3 * NC / 2 <= 512, "tensor memory");
   // tiles of 128-byte rows (64 keys of a part), 128-byte swizzled
   static constexpr uint32_t kXBlock = 2 * NC * 128, kXPart = 2 * kXBlock;
-  static constexpr uint32_t kYBlock = NC * 128, kYPart = 2 * kYBlock;
+  // (of Y a block is of all three parts, where one product takes them together)
+  static constexpr uint32_t kYBlock = kPParts * NC * 128, kYPart = kPParts == 1 ? 2 * kYBlock : NC * 128;
+  static constexpr uint32_t kYBytes = 3 * 2 * NC * 128;
   static constexpr uint32_t kTCPart = 2 * NC * 128;  // [T; C], NC columns of a row used
   // Byte offsets of dynamic shared memory, 1024-byte aligned.  Of trees of more
   // than 32 nodes P and then [T; C] stand where Y was, which is free again when
@@ -219,30 +250,35 @@ struct TreeMma {
   static constexpr bool kOverY = NC > 32;
   static constexpr uint32_t kX = 0;
   static constexpr uint32_t kY = kX + 3 * kXPart;
-  static constexpr uint32_t kTC = kOverY ? kY : kY + 3 * kYPart;
+  static constexpr uint32_t kTC = kOverY ? kY : kY + kYBytes;
   // P, [2 NC][NC] FP32, column c of row r at c ^ (r & 31)
   static constexpr uint32_t kP = kOverY ? kY : kTC + 3 * kTCPart;
-  static_assert(!kOverY || (3 * kTCPart <= 3 * kYPart && 2 * NC * NC * 4 <= 3 * kYPart), "over Y");
-  // decays [NC][128] FP32; a row's raw gates arrive in its first half
-  static constexpr uint32_t kD = kOverY ? kY + 3 * kYPart : kP + 2 * NC * NC * 4;
-  static constexpr uint32_t kK = kD + NC * kDim * 4;  // keys and queries [NC][128] BF16
-  static constexpr uint32_t kQ = kK + NC * kDim * 2;
-  static constexpr uint32_t kReplayK = kQ + NC * kDim * 2;  // the replay's operands
+  static_assert(!kOverY || (3 * kTCPart <= kYBytes && 2 * NC * NC * 4 <= kYBytes), "over Y");
+  // decays [NC][128] FP32; where gates have no place of their own a row's arrive
+  // in its first half
+  static constexpr uint32_t kD = kOverY ? kY + kYBytes : kP + 2 * NC * NC * 4;
+  // Keys and queries [NC][128] BF16.  Where there is room gates stand behind them,
+  // and the three come by tensor copies of eight nodes, which the warp with the
+  // requests sends for ahead of their turn; else by the nodes' warps' own copies.
+  static constexpr int kRawBufs = NC > 32 ? 0 : (BF16 ? 2 : 1), kCopies = kRawBufs > 0 ? kRawBufs : 1;
+  static constexpr uint32_t kRows = NC * kDim * 2;
+  static constexpr uint32_t kRaw = (kRawBufs > 0 ? 3 : 2) * kRows;
+  static constexpr uint32_t kK = kD + NC * kDim * 4;
+  static constexpr uint32_t kReplayK = kK + kCopies * kRaw;  // the replay's operands
   static constexpr uint32_t kReplayD = kReplayK + kMaxQ * kDim * 4;
   static constexpr uint32_t kReplayU = kReplayD + kMaxQ * kDim * 4;
   static constexpr uint32_t kReplayDn = kReplayU + kMaxQ * kDim * 4;
   static constexpr uint32_t kDt = kReplayDn + kDim * 4;  // dt_bias of the head
   // per node: P with its ancestors' keys, the nearest's first, and beta
-  static constexpr uint32_t kA = kDt + kDim * 4;
+  static constexpr uint32_t kA = kDt + kCopies * kDim * 4;
   static constexpr uint32_t kNorms = kA + NC * kPath * 4;  // of keys, then of queries
   static constexpr uint32_t kBad = kNorms + 2 * NC * 4;    // [NC / 8][128] nodes, a byte's bits
-  static constexpr uint32_t kTasks = kBad + NC / 8 * kDim;
+  static constexpr uint32_t kTasks = kBad + kDBufs * NC / 8 * kDim;
   static constexpr uint32_t kParent = kTasks + 4 * sizeof(TreeTask);
-  // An FP32 page comes here by asynchronous copies, a whole item ahead, 8 KB a warp,
-  // where there is room (48 requests of up to 32 nodes: 97 -> 91 us); else to
-  // registers, a unit ahead.  BF16 pages, which have four units ahead in registers,
-  // gain nothing by it (113 us either way).
-  static constexpr bool kStaged = NC <= 32 && !BF16;
+  // A page comes here by asynchronous copies, a whole item ahead, 8 KB a warp, where
+  // there is room (48 requests of up to 32 nodes: 97 -> 91 us); else to registers, a
+  // unit ahead, of BF16 pages four.
+  static constexpr bool kStaged = NC <= 32;
   static constexpr uint32_t kPage = round_up(kParent + kTreeNodes, 128);
   static constexpr uint32_t kBars = kPage + (kStaged ? kPageWarps * 8192 : 0);
   static constexpr uint32_t kSlot = kBars + sizeof(TreeBars);
@@ -267,15 +303,16 @@ struct PageUnit {
   // From a warp's staged rows, 256 bytes of each: 16-byte piece c of row r stands at
   // place(r, c), where no two of eight lanes meet in a bank.
   static __device__ __forceinline__ int place(int r, int c) {
-    return r * 256 + ((c >> 2 ^ (r & 1)) << 6) + (c & 3) * 16;
+    return BF16 ? r * 256 + ((c >> 1 ^ (r & 3)) << 5) + (c & 1) * 16
+                : r * 256 + ((c >> 2 ^ (r & 1)) << 6) + (c & 3) * 16;
   }
   __device__ __forceinline__ void load_staged(const uint8_t *rows, int row, int key, int lane) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = row + lane / 4 + 8 * i, c = (key + 16 * j) / 4 + (lane & 3);
-        s[j][i] = *reinterpret_cast<const Four *>(rows + place(r, c));
+        const int r = row + lane / 4 + 8 * i, byte = (key + 16 * j + 4 * (lane & 3)) * (BF16 ? 2 : 4);
+        s[j][i] = *reinterpret_cast<const Four *>(rows + place(r, byte >> 4) + (byte & 15));
       }
   }
 };
@@ -316,7 +353,7 @@ struct TreeItems {
   bool ok;  // no wait has run out
 
   __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
-    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity)) && ok;
+    ok = tm_wait(bar, parity) && ok;
     return ok;
   }
   // The next task; false where there is none.
@@ -341,16 +378,21 @@ struct TreeItems {
   __device__ __forceinline__ const uint2 *paths() const { return tasks[seq & 3].path; }
 };
 
+// k, q, raw_g and v [n_tokens, H, 128] in boxes of eight tokens of a head.
+constexpr int kBoxTokens = 8;
+struct TreeTokenMaps {
+  CUtensorMap of[4];
+};
+
 template <int NC, bool BF16>
 __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
-    kda_tree_mma_kernel(const TreeVerifyParams p, int n_items) {
+    kda_tree_mma_kernel(const TreeVerifyParams p, const __grid_constant__ TreeTokenMaps maps,
+                        int n_items) {
   using L = TreeMma<NC, BF16>;
   // (its alignment known, the addresses below are constants, which take no
   // registers)
   extern __shared__ __align__(1024) uint8_t mem[];
   float *const decay = reinterpret_cast<float *>(mem + L::kD);
-  uint16_t *const keys = reinterpret_cast<uint16_t *>(mem + L::kK);
-  uint16_t *const queries = reinterpret_cast<uint16_t *>(mem + L::kQ);
   float *const coefs = reinterpret_cast<float *>(mem + L::kA);
   TreeTask *const tasks = reinterpret_cast<TreeTask *>(mem + L::kTasks);
   TreeBars *const bars = reinterpret_cast<TreeBars *>(mem + L::kBars);
@@ -362,7 +404,8 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->task_full[i], 1);
-      mbar_init(&bars->task_free[i], L::kWarps - 1);
+      // (the warps of R may go through the tasks twice)
+      mbar_init(&bars->task_free[i], L::kWarps - 1 + (L::kDBufs > 1 ? L::kRWarps : 0));
     }
     mbar_init(&bars->x_full, L::kNodeWarps);
     mbar_init(&bars->x_free, 1);
@@ -374,12 +417,14 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->d_full[i], 1);
       mbar_init(&bars->d_free[i], L::kRWarps);
+      mbar_init(&bars->r_full[i], L::kRWarps);
+      mbar_init(&bars->o_full[i], 1);
       mbar_init(&bars->done[i], 1);
+      mbar_init(&bars->raw_full[i], 1);
+      mbar_init(&bars->raw_free[i], L::kNodeWarps);
     }
     mbar_init(&bars->t_full, L::kTWarps);
     mbar_init(&bars->t_free, 1);
-    mbar_init(&bars->r_full, L::kRWarps);
-    mbar_init(&bars->o_full, 1);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(tmem_slot, 512);
@@ -402,8 +447,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
 
   if (warp < L::kR0) {
     // ======== pages: rows 32 quarter .. + 31, keys kKeys which .. + kKeys - 1
-    // units of 16 rows and 32 keys, those of the same rows first; the next (of BF16
-    // pages the next four) on its way, or the next item's page, to shared memory
+    // units of 16 rows and 32 keys, those of the same rows first
     constexpr int kUnits = 32 / L::kPageWarps, kKeys = 16 * kUnits, kThreads = 32 * L::kPageWarps;
     constexpr int kAhead = L::kStaged ? 0 : BF16 ? 4 : 1, kRecs = kMaxQ / L::kPageWarps;
     uint8_t *const staged = mem + L::kPage + warp * 8192;
@@ -417,7 +461,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     const int k0 = kKeys * which + 4 * (lane & 3);
     TreeItems it;
     int done = 0;  // items with nodes
-    PageUnit<BF16> pg[kUnits];
+    PageUnit<BF16> pg[L::kStaged ? 1 : kUnits];
     uint2 rec_k[kRecs], rec_g[kRecs];
     float4 rec_u[kRecs];
     // an item's records (a warp one) and first units, ahead of its turn; and the
@@ -436,11 +480,12 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
           rec_u[i] = __ldg(reinterpret_cast<const float4 *>(p.corr + it.row * p.corr_stride + row * kDim) + lane);
         }
       if constexpr (L::kStaged) {
-        const float *from = static_cast<const float *>(p.state) + page_of(it.slot, it.h) +
-                            32 * quarter * kDim + kKeys * which;
-#pragma unroll 4
+        const char *from = static_cast<const char *>(p.state) +
+                           (page_of(it.slot, it.h) + 32 * quarter * kDim + kKeys * which) * (BF16 ? 2 : 4);
+#pragma unroll 2
         for (int i = lane; i < 512; i += 32)
-          cp_async16(staged + PageUnit<BF16>::place(i >> 4, i & 15), from + (i >> 4) * kDim + 4 * (i & 15));
+          cp_async16(staged + PageUnit<BF16>::place(i >> 4, i & 15),
+                     from + (i >> 4) * (kDim * (BF16 ? 2 : 4)) + 16 * (i & 15));
       } else {
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) pg[e].load(p.state, page_part() + unit_at(e));
@@ -457,7 +502,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     while (more) {
       const int replay = it.pending;
       const long long page = page_part();
-      if (replay > 0) {
+      if (!BF16 && replay > 0) {
 #pragma unroll
         for (int i = 0; i < kRecs; ++i)
           if (const int t = warp + i * L::kPageWarps; t < replay) {
@@ -481,10 +526,11 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         cp_async_wait_all();
         __syncwarp();
       }
-#pragma unroll
+#pragma unroll(L::kStaged ? 1 : kUnits)
       for (int e = 0; e < kUnits; ++e) {
+        PageUnit<BF16> &unit = pg[L::kStaged ? 0 : e];
         const int rh = e / (kUnits / 2), k32 = 32 * (e % (kUnits / 2));
-        if constexpr (L::kStaged) pg[e].load_staged(staged, 16 * rh, k32, lane);
+        if constexpr (L::kStaged) unit.load_staged(staged, 16 * rh, k32, lane);
         if constexpr (!BF16) {
           if (replay > 0) {
             const float *up = ru + 32 * quarter + 16 * rh + lane / 4;
@@ -492,21 +538,21 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float4 x = lds4(dp + 16 * j);
-              pg[e].s[j][0] = fmul4(pg[e].s[j][0], x);
-              pg[e].s[j][1] = fmul4(pg[e].s[j][1], x);
+              unit.s[j][0] = fmul4(unit.s[j][0], x);
+              unit.s[j][1] = fmul4(unit.s[j][1], x);
             }
 #pragma unroll 1
             for (int t = 0; t < replay; ++t, kp += kDim, up += kDim) {
               const float u0 = up[0], u1 = up[8];
               const float4 x0 = lds4(kp), x1 = lds4(kp + 16);
-              pg[e].s[0][0] = ffma4s(u0, x0, pg[e].s[0][0]);
-              pg[e].s[0][1] = ffma4s(u1, x0, pg[e].s[0][1]);
-              pg[e].s[1][0] = ffma4s(u0, x1, pg[e].s[1][0]);
-              pg[e].s[1][1] = ffma4s(u1, x1, pg[e].s[1][1]);
+              unit.s[0][0] = ffma4s(u0, x0, unit.s[0][0]);
+              unit.s[0][1] = ffma4s(u1, x0, unit.s[0][1]);
+              unit.s[1][0] = ffma4s(u0, x1, unit.s[1][0]);
+              unit.s[1][1] = ffma4s(u1, x1, unit.s[1][1]);
             }
             float *to = static_cast<float *>(p.state) + page + unit_at(e);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) stg4(to + 8 * (c % 2) * kDim + 16 * (c / 2), pg[e].s[c / 2][c % 2]);
+            for (int c = 0; c < 4; ++c) stg4(to + 8 * (c % 2) * kDim + 16 * (c / 2), unit.s[c / 2][c % 2]);
           }
         }
         if (it.n > 0)
@@ -515,7 +561,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
             uint32_t w[8];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              auto &s = pg[e].s[c / 2][c % 2];
+              auto &s = unit.s[c / 2][c % 2];
               if constexpr (BF16) {
                 w[2 * c] = s.x;
                 w[2 * c + 1] = s.y;
@@ -528,7 +574,8 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
             }
             tm_store_16x16(lanes + ((uint32_t)(16 * rh) << 16) + kTmPartCols * part + (kKeys * which + k32) / 2, w);
           }
-        if (!L::kStaged && e + kAhead < kUnits) pg[(e + kAhead) % kUnits].load(p.state, page + unit_at(e + kAhead));
+        if constexpr (!L::kStaged)
+          if (e + kAhead < kUnits) pg[e + kAhead].load(p.state, page + unit_at(e + kAhead));
       }
       if (it.n > 0) {
         tm_store_wait();
@@ -546,30 +593,25 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     ok = it.ok;
   } else if (warp < L::kT0) {
     // ======== R and the outputs: a row a lane, eight nodes at a time
+    // Where w and y have two places an item's R comes before the outputs of the
+    // one ahead of it, whose product is meanwhile formed.
     const int quarter = warp & 3, which = (warp - L::kR0) >> 2, at = 32 * quarter + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-    TreeItems it;
-    int done = 0;
-    bool more = it.start(tasks, bars);
-    if (named_bar_or(4, 32 * L::kRWarps, !it.ok)) more = it.ok = false;
-    while (more) {
-      const int n = it.n, cols = (n + 15) & ~15;
-      if (n == 0) {
-        more = it.next(lane);
-        if (named_bar_or(4, 32 * L::kRWarps, !it.ok)) more = it.ok = false;
-        continue;
-      }
-      const int buf = done % L::kDBufs;
-      const uint32_t d = kTmD + buf * 2 * NC;
-      const long long first = ((long long)it.t0 * p.H + it.h) * kDim + at;
-      const long long step = (long long)p.H * kDim;
+    const long long step = (long long)p.H * kDim;
+    const auto agree = [&](bool x) { return named_bar_or(4, 32 * L::kRWarps, x); };
+    // R of `it`, its parts to tensor memory; true where an entry is not finite
+    const auto front = [&](TreeItems &it, int done) {
+      const int n = it.n, cols = (n + 15) & ~15, buf = done % L::kDBufs;
+      const uint32_t d = kTmD + buf * 2 * NC, to_r = L::kTmR + buf * (3 * NC / 2);
+      uint8_t *const marks = mem + L::kBad + buf * (NC / 8 * kDim) + at;
+      const uint16_t *from = p.v + ((long long)it.t0 * p.H + it.h) * kDim + at;
       uint32_t v[8];
       const auto ask = [&](int i0) {
-        const uint16_t *from = p.v + first + i0 * step;
+        const uint16_t *x = from + i0 * step;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          v[i] = __ldg(from);
-          if (i0 + i + 1 < n) from += step;  // (behind the last: again the last)
+          v[i] = __ldg(x);
+          if (i0 + i + 1 < n) x += step;  // (behind the last: again the last)
         }
       };
       if (8 * which < n) ask(8 * which);
@@ -598,7 +640,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
             }
           bad = bad || bits != 0;
         }
-        mem[L::kBad + i0 / 8 * kDim + at] = (uint8_t)bits;
+        marks[i0 / 8 * kDim] = (uint8_t)bits;
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
           uint32_t w[4];
@@ -608,7 +650,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
             w[i] = take_part(pair);
             x[2 * i] = pair.x, x[2 * i + 1] = pair.y;
           }
-          tm_store_32x4(lanes + L::kTmR + (NC / 2) * part + i0 / 2, w[0], w[1], w[2], w[3]);
+          tm_store_32x4(lanes + to_r + (NC / 2) * part + i0 / 2, w[0], w[1], w[2], w[3]);
         }
         // (u is added up on zeros, o on y)
         tm_store_32x4(lanes + d + i0, 0, 0, 0, 0);
@@ -616,9 +658,16 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       }
       tm_store_wait();
       tc_fence_before();
-      arrive(&bars->r_full);
-      const bool any_bad = named_bar_or(4, 32 * L::kRWarps, bad);
-      it.wait(&bars->o_full, (uint32_t)done & 1u);
+      arrive(&bars->r_full[buf]);
+      return bad;
+    };
+    // the outputs of `it`
+    const auto back = [&](TreeItems &it, int done, bool any_bad) {
+      const int n = it.n, cols = (n + 15) & ~15, buf = done % L::kDBufs;
+      const uint32_t d = kTmD + buf * 2 * NC;
+      const uint8_t *const marks = mem + L::kBad + buf * (NC / 8 * kDim) + at;
+      const long long first = ((long long)it.t0 * p.H + it.h) * kDim + at;
+      it.wait(&bars->o_full[buf], (uint32_t)(done / L::kDBufs) & 1u);
       tc_fence_after();
 #pragma unroll 1
       for (int i0 = 8 * which; i0 < n; i0 += 16) {
@@ -633,7 +682,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
             bool hit = false;
             for (int j = 0; j <= (int)(way.x & 0xff); ++j) {
               const int s = j == 0 ? i0 + i : path_byte(way, j);
-              hit = hit || (mem[L::kBad + (s >> 3) * kDim + at] >> (s & 7) & 1u);
+              hit = hit || (marks[(s >> 3) * kDim] >> (s & 7) & 1u);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -653,11 +702,36 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       }
       tc_fence_before();
       arrive(&bars->d_free[buf]);
-      ++done;
+    };
+    // `out` is the item behind `it` (every one in its turn: the tasks of those
+    // without nodes are handed back too)
+    TreeItems it, out;
+    int done = 0;  // items whose R is formed
+    bool more = it.start(tasks, bars), first = true, owed = false, was_bad = false;
+    out.ok = true;
+    if (L::kDBufs > 1) out.start(tasks, bars);
+    while (true) {
+      const bool live = more && it.n > 0;
+      bool bad = false;
+      if (live) bad = front(it, done++);
+      // (whatever a warp has found, it comes here, where all go on or none)
+      if (agree(bad || !it.ok || !out.ok)) {
+        bad = agree(bad);
+        if (agree(!it.ok || !out.ok)) break;
+      }
+      if (L::kDBufs == 1) {
+        if (live) back(it, done - 1, bad);
+        if (bad) agree(false);  // (the marks are read)
+      } else {
+        if (owed) back(out, live ? done - 2 : done - 1, was_bad);
+        if (was_bad) agree(false);
+        if (!first && more) out.next(lane);
+        first = false, owed = live, was_bad = bad;
+      }
+      if (!more) break;
       more = it.next(lane);
-      if (named_bar_or(4, 32 * L::kRWarps, !it.ok)) more = it.ok = false;
     }
-    ok = it.ok;
+    ok = it.ok && out.ok;
   } else if (warp < L::kIssue0) {
     // ======== T and C: a lane a row of P, nodes' keys, then their queries
     const int tw = warp - L::kT0, row = 32 * tw + lane;
@@ -678,24 +752,34 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       const bool live = row < 2 * cols && t < n;
       const uint2 path = live ? it.paths()[t] : make_uint2(0, 0);
       const int m = live ? (int)(path.x & 0xff) : -1;
-      // this item's values on their way to L2, and the next head's nodes
-      for (int i = row; i < n * 8; i += 32 * L::kTWarps) {
-        const int what = i >> 1 & 3;
-        const long long at = ((long long)(it.t0 + (i >> 3)) * p.H + it.h) * kDim + (i & 1) * (kDim / 2);
-        if (what == 0) {
-          prefetch_l2(p.v + at);
-        } else if (it.h + 1 < it.h1) {
-          prefetch_l2((what == 1 ? p.k : (what == 2 ? p.q : p.g)) + at + kDim);
+      // this item's values on their way to L2, and the next head's nodes (elsewhere
+      // the warp with the requests sends for them)
+      if constexpr (L::kRawBufs == 0)
+        for (int i = row; i < n * 8; i += 32 * L::kTWarps) {
+          const int what = i >> 1 & 3;
+          const long long at = ((long long)(it.t0 + (i >> 3)) * p.H + it.h) * kDim + (i & 1) * (kDim / 2);
+          if (what == 0) {
+            prefetch_l2(p.v + at);
+          } else if (it.h + 1 < it.h1) {
+            prefetch_l2((what == 1 ? p.k : (what == 2 ? p.q : p.g)) + at + kDim);
+          }
         }
-      }
-      float beta = 0.f;
-      if (live) beta = sigmoidf_fast(bf16_bits_to_f32(__ldg(p.beta + (long long)(it.t0 + t) * p.H + it.h)));
+      uint16_t beta = 0;
+      if (live) beta = __ldg(p.beta + (long long)(it.t0 + t) * p.H + it.h);
       it.wait(&bars->p_full, (uint32_t)done & 1u);
       tc_fence_after();
       for (int c = 0; c < cols; c += 16) {
         float x[16];
         tm_load(tmem + ((uint32_t)(32 * tw) << 16) + L::kTmP + c, x);
         tm_load_wait();
+#pragma unroll
+        for (int part = 1; part < L::kPParts; ++part) {
+          float y[16];
+          tm_load(tmem + ((uint32_t)(32 * tw) << 16) + L::kTmP + part * NC + c, y);
+          tm_load_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] += y[i];
+        }
         if (row < 2 * cols)
 #pragma unroll
           for (int i = 0; i < 16; ++i) mine[(c + i) ^ lane] = x[i];
@@ -711,39 +795,37 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       for (int j = 1; j < kPath; ++j) wt[j] = j <= m ? mine[path_byte(path, j) ^ lane] : 0.f;
       if (key && live) {
         sts4(coefs + t * kPath, make_float4(wt[1], wt[2], wt[3], wt[4]));
-        sts4(coefs + t * kPath + 4, make_float4(wt[5], wt[6], wt[7], beta));
+        sts4(coefs + t * kPath + 4, make_float4(wt[5], wt[6], wt[7], sigmoidf_fast(bf16_bits_to_f32(beta))));
 #pragma unroll
         for (int j = 1; j < kPath; ++j) wt[j] = 0.f;
       }
       named_bar(2, 32 * L::kTWarps);
-#pragma unroll
-      for (int i = 0; i < kPath; ++i) {
-        const float *c = coefs + (i == 0 ? (m < 0 ? 0 : t) : path_byte(path, i)) * kPath;
-        const float4 x = lds4(c), y = lds4(c + 4);
-        const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        wt[i] *= f[7];
-#pragma unroll
-        for (int k = 1; i + k < kPath; ++k)
-          if (i + k <= m) wt[i + k] = fmaf(-wt[i], f[k - 1], wt[i + k]);
-      }
       // [T; C] in parts: zeros, and a row's entries
       if (done > 0) it.wait(&bars->t_free, (uint32_t)(done - 1) & 1u);
-      if (row < 2 * cols) {
-        uint8_t *const to = mem + L::kTC + row * 128;
+      uint8_t *const to = mem + L::kTC + row * 128;
+      if (row < 2 * cols)
 #pragma unroll
         for (int e = 0; e < 3; ++e)
+#pragma unroll 1
           for (int c = 0; c < cols / 8; ++c)
             *reinterpret_cast<uint4 *>(to + e * L::kTCPart + ((c ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+      // step i: wt[k] is the weight of the path's node i + k
+      uint2 way = path;
+      int s = t;
+      float4 x = lds4(coefs + (m < 0 ? 0 : t) * kPath), y = lds4(coefs + (m < 0 ? 0 : t) * kPath + 4);
+#pragma unroll 1
+      for (int i = 0; i <= m; ++i) {
+        float2 w = make_float2(wt[0] * y.w, 0.f);
+        const float f[kPath - 1] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z};
 #pragma unroll
-        for (int j = 0; j < kPath; ++j)
-          if (j <= m) {
-            const int s = j == 0 ? t : path_byte(path, j);
-            uint8_t *const place = to + (((s >> 3) ^ (row & 7)) << 4) + (s & 7) * 2;
-            float2 x = make_float2(wt[j], 0.f);
+        for (int k = 1; k < kPath; ++k) wt[k - 1] = fmaf(-w.x, f[k - 1], wt[k]);
+        uint8_t *const place = to + (((s >> 3) ^ (row & 7)) << 4) + (s & 7) * 2;
+        way = make_uint2(__funnelshift_r(way.x, way.y, 8), way.y >> 8);
+        s = way.x & 0xff;  // (behind the last: some node of the path, or 0)
+        x = lds4(coefs + s * kPath), y = lds4(coefs + s * kPath + 4);
 #pragma unroll
-            for (int e = 0; e < 3; ++e)
-              *reinterpret_cast<uint16_t *>(place + e * L::kTCPart) = (uint16_t)take_part(x);
-          }
+        for (int e = 0; e < 3; ++e)
+          *reinterpret_cast<uint16_t *>(place + e * L::kTCPart) = (uint16_t)take_part(w);
       }
       fence_proxy_async_smem();
       arrive(&bars->t_full);
@@ -777,15 +859,19 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         if (done > 0) it.wait(&bars->p_free, (done - 1) & 1u);
         if (!it.ok) break;
         tc_fence_after();
+        // (M = 128 rows: those behind X's are other operands', and P's rows of them
+        // nobody reads.)  A product reads its 128 rows of X from shared memory
+        // whatever its N: where tensor memory has room for P by parts of Y, one takes
+        // all parts of Y that go with a part of X.
 #pragma unroll 1
-        for (uint32_t e = 0; e < 6; ++e) {
-          const uint32_t x = x0 + (kA6 >> 2 * e & 3) * L::kXPart, y = y0 + (kB6 >> 2 * e & 3) * L::kYPart;
+        for (uint32_t e = 0; e < (L::kPParts == 1 ? 6 : 3); ++e) {
+          const uint32_t x = x0 + (L::kPParts == 1 ? (kA6 >> 2 * e & 3) : e) * L::kXPart;
+          const uint32_t y = y0 + (L::kPParts == 1 ? (kB6 >> 2 * e & 3) * L::kYPart : 0);
+          const uint32_t columns = L::kPParts == 1 ? cols : (2 - e) * NC + cols;
 #pragma unroll
           for (int ks = 0; ks < kDim / 16; ++ks)
-            // (M = 128 rows: those behind X's are other operands', and P's rows of
-            // them nobody reads)
             tm_mma_ss(tm + L::kTmP, umma_desc_sw128(x + (ks >> 2) * L::kXBlock + (ks & 3) * 32),
-                      umma_desc_sw128(y + (ks >> 2) * L::kYBlock + (ks & 3) * 32), tm_idesc(cols),
+                      umma_desc_sw128(y + (ks >> 2) * L::kYBlock + (ks & 3) * 32), tm_idesc(columns),
                       e > 0 || ks > 0, lead);
         }
         commit(&bars->p_full);
@@ -798,7 +884,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         for (uint32_t e = 0; e < (BF16 ? 3 : 6); ++e) {
           const uint32_t s = tm + (BF16 ? 0 : (kA6 >> 2 * e & 3)) * kTmPartCols;
           const uint32_t x = x0 + (BF16 ? 2 - e : (kB6 >> 2 * e & 3)) * L::kXPart;
-#pragma unroll
+#pragma unroll 4
           for (int ks = 0; ks < kDim / 16; ++ks)
             tm_mma(d, s + 8 * ks, umma_desc_sw128(x + (ks >> 2) * L::kXBlock + (ks & 3) * 32),
                    tm_idesc(2 * cols), e > 0 || ks > 0, lead);
@@ -812,19 +898,19 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       for (bool more = it.start(tasks, bars); more; more = it.next(lane)) {
         if (it.n == 0) continue;
         const uint32_t cols = __shfl_sync(0xffffffffu, (uint32_t)(it.n + 15) & ~15u, 0);
-        const uint32_t d = tm + kTmD + done % L::kDBufs * 2 * NC;
+        const uint32_t buf = done % L::kDBufs, d = tm + kTmD + buf * 2 * NC;
         it.wait(&bars->t_full, done & 1u);
-        it.wait(&bars->r_full, done & 1u);
+        it.wait(&bars->r_full[buf], (done / L::kDBufs) & 1u);
         if (!it.ok) break;
         tc_fence_after();
 #pragma unroll 1
         for (uint32_t e = 0; e < 6; ++e)
 #pragma unroll 1
           for (uint32_t ks = 0; ks < cols / 16; ++ks)
-            tm_mma(d, tm + L::kTmR + (kA6 >> 2 * e & 3) * (NC / 2) + 8 * ks,
+            tm_mma(d, tm + L::kTmR + buf * (3 * NC / 2) + (kA6 >> 2 * e & 3) * (NC / 2) + 8 * ks,
                    umma_desc_sw128(c0 + (kB6 >> 2 * e & 3) * L::kTCPart + ks * 32),
                    tm_idesc(2 * cols), true, lead);
-        commit(&bars->o_full);
+        commit(&bars->o_full[buf]);
         commit(&bars->t_free);
         if (L::kOverY) commit(&bars->y_free);
         ++done;
@@ -833,14 +919,15 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     ok = it.ok;
     // every product issued has completed before the columns are released
     commit(&bars->done[warp - L::kIssue0]);
-    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->done[warp - L::kIssue0], 0u)) && ok;
+    ok = tm_wait(&bars->done[warp - L::kIssue0], 0u) && ok;
   } else if (warp < L::kNode0) {
     // ======== requests: checked, their paths listed; the inert ones' zeros
     int8_t *const parent = reinterpret_cast<int8_t *>(mem + L::kParent);
     int seq = 0;
+    uint32_t sent = 0;  // items whose nodes' rows were sent for
     const auto place = [&] {
       if (seq >= 4)
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->task_free[seq & 3], (uint32_t)((seq >> 2) - 1) & 1u));
+        ok = tm_wait(&bars->task_free[seq & 3], (uint32_t)((seq >> 2) - 1) & 1u);
       return ok;
     };
     for (int item = begin; item < end && ok;) {
@@ -884,7 +971,32 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       }
       arrive(&bars->task_full[seq & 3]);
       ++seq;
+      if constexpr (L::kRawBufs > 0) {
+        const int boxes = (r.n + kBoxTokens - 1) / kBoxTokens;
+        for (int h = h0; h < h1 && boxes > 0; ++h, ++sent) {
+          const uint32_t buf = sent % L::kRawBufs;
+          if (sent >= (uint32_t)L::kRawBufs)
+            ok = tm_wait(&bars->raw_free[buf], (sent / L::kRawBufs - 1) & 1u);
+          if (!ok) break;
+          if (lane == 0)
+            mbar_arrive_expect_tx(&bars->raw_full[buf], 3 * boxes * kBoxTokens * kDim * 2 + kDim * 4);
+          __syncwarp();
+          const int which = lane >> 3, box = lane & 7;
+          if (which < 3 && box < boxes)
+            tma_load_3d(mem + L::kK + buf * L::kRaw + which * L::kRows + box * (kBoxTokens * kDim * 2),
+                        &maps.of[which], 0, h, r.t0 + kBoxTokens * box, &bars->raw_full[buf]);
+          // and to L2 this item's values, and the next one's nodes where they have to
+          // wait for their place
+          if (which == 3 && box < boxes) prefetch_box(&maps.of[3], 0, h, r.t0 + kBoxTokens * box);
+          if (L::kRawBufs == 1 && which < 3 && box < boxes && h + 1 < h1)
+            prefetch_box(&maps.of[which], 0, h + 1, r.t0 + kBoxTokens * box);
+          if (lane == 31) bulk_g2s(mem + L::kDt + buf * kDim * 4, p.dt_bias + h * kDim, kDim * 4, &bars->raw_full[buf]);
+        }
+      }
     }
+    // (no copy is on its way when the CTA ends)
+    for (uint32_t i = sent > (uint32_t)L::kRawBufs ? sent - L::kRawBufs : 0; i < sent; ++i)
+      ok = tm_wait(&bars->raw_full[i % L::kCopies], (i / L::kCopies) & 1u) && ok;
     if (ok && place()) {
       if (lane == 0) tasks[seq & 3].n = -1;
       arrive(&bars->task_full[seq & 3]);
@@ -893,43 +1005,53 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     // ======== nodes
     constexpr int kThreads = 32 * L::kNodeWarps;
     const int nw = warp - L::kNode0, ntid = tid - 32 * L::kNode0;
-    float *const dts = reinterpret_cast<float *>(mem + L::kDt);
     float *const norms = reinterpret_cast<float *>(mem + L::kNorms);
     TreeItems it;
+    // where `done`'s operands are, and where a node's gates
+    int done = 0;
+    const auto raw = [&](int which) {
+      return reinterpret_cast<uint16_t *>(mem + L::kK + done % L::kCopies * L::kRaw + which * L::kRows);
+    };
+    const auto dts = [&] { return reinterpret_cast<float *>(mem + L::kDt + done % L::kCopies * kDim * 4); };
+    const auto gates = [&](int t) {
+      return L::kRawBufs > 0 ? raw(2) + t * kDim : reinterpret_cast<uint16_t *>(decay + t * kDim);
+    };
     // the next item with nodes, whose operands are then on their way
     const auto settle = [&](bool more) {
       while (more && it.n == 0) more = it.next(lane);
       if (named_bar_or(1, kThreads, !it.ok)) return it.ok = false;
-      if (more) {
+      if (L::kRawBufs == 0 && more) {
         const int c8 = 8 * (lane & 15);
 #pragma unroll 1
         for (int t = nw; t < it.n; t += L::kNodeWarps) {
           const long long at = ((long long)(it.t0 + t) * p.H + it.h) * kDim + c8;
-          cp_async16((lane < 16 ? keys : queries) + t * kDim + c8, (lane < 16 ? p.k : p.q) + at);
-          if (lane < 16) cp_async16(decay + t * kDim + c8 / 2, p.g + at);
+          cp_async16(raw(lane >> 4) + t * kDim + c8, (lane < 16 ? p.k : p.q) + at);
+          if (lane < 16) cp_async16(gates(t) + c8, p.g + at);
         }
-        if (ntid < kDim / 4) cp_async16(dts + 4 * ntid, p.dt_bias + it.h * kDim + 4 * ntid);
+        if (ntid < kDim / 4) cp_async16(dts() + 4 * ntid, p.dt_bias + it.h * kDim + 4 * ntid);
       }
       return more;
     };
-    int done = 0;
     bool more = settle(it.start(tasks, bars));
     while (more) {
       const int n = it.n, cols = (n + 15) & ~15;
       const float a = expf(__ldg(p.A_log + it.h));
-      cp_async_wait_all();
-      named_bar(1, kThreads);
+      const uint16_t *const keys = raw(0), *const queries = raw(1);
+      if constexpr (L::kRawBufs > 0) {
+        it.wait(&bars->raw_full[done % L::kCopies], (uint32_t)(done / L::kCopies) & 1u);
+      } else {
+        cp_async_wait_all();
+        named_bar(1, kThreads);
+      }
       // norms and decays: two nodes a warp, eight channels a lane
       {
         const int hw = lane >> 4, c8 = 8 * (lane & 15);
-        const float4 dta = lds4(dts + c8), dtb = lds4(dts + c8 + 4);
 #pragma unroll 1
         for (int t0 = 2 * nw; t0 < n; t0 += 2 * L::kNodeWarps) {
           const int t = t0 + hw < n ? t0 + hw : t0;
           const uint4 kb = *reinterpret_cast<const uint4 *>(keys + t * kDim + c8);
           const uint4 qb = *reinterpret_cast<const uint4 *>(queries + t * kDim + c8);
-          const uint4 gb = *reinterpret_cast<const uint4 *>(
-              reinterpret_cast<const uint16_t *>(decay + t * kDim) + c8);
+          const uint4 gb = *reinterpret_cast<const uint4 *>(gates(t) + c8);
           const float4 ka = bf16x4(make_uint2(kb.x, kb.y)), kc = bf16x4(make_uint2(kb.z, kb.w));
           const float4 qa = bf16x4(make_uint2(qb.x, qb.y)), qc = bf16x4(make_uint2(qb.z, qb.w));
           float kk = dot4(ka, ka) + dot4(kc, kc), qq = dot4(qa, qa) + dot4(qc, qc);
@@ -940,8 +1062,12 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
           }
           __syncwarp();  // the row's gates are read
           if (t0 + hw < n) {
-            sts4(decay + t * kDim + c8, decay4(a, bf16x4(make_uint2(gb.x, gb.y)), dta, p.lower_bound));
-            sts4(decay + t * kDim + c8 + 4, decay4(a, bf16x4(make_uint2(gb.z, gb.w)), dtb, p.lower_bound));
+            uint2 g4 = make_uint2(gb.x, gb.y);
+#pragma unroll 1
+            for (int e = 0; e < 8; e += 4) {
+              sts4(decay + t * kDim + c8 + e, decay4(a, bf16x4(g4), lds4(dts() + c8 + e), p.lower_bound));
+              g4 = make_uint2(gb.z, gb.w);
+            }
             if ((lane & 15) == 0) {
               norms[t] = rsqrtf(kk + kNormEps);
               norms[NC + t] = rsqrtf(qq + kNormEps) * p.q_scale;
@@ -962,10 +1088,11 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         float4 g = lds4(decay + t * kDim + 4 * lane);
         const float4 k = scale4(bf16x4(*reinterpret_cast<const uint2 *>(keys + t * kDim + 4 * lane)), norms[t]);
         const float4 q = scale4(bf16x4(*reinterpret_cast<const uint2 *>(queries + t * kDim + 4 * lane)), norms[NC + t]);
-#pragma unroll
-        for (int j = 1; j < kPath; ++j) {
-          if (j > m) break;  // (the same in every lane)
-          g = fmul4(g, lds4(decay + path_byte(path, j) * kDim + 4 * lane));
+        uint2 way = path;
+#pragma unroll 1
+        for (int j = 0; j < m; ++j) {  // (the same in every lane)
+          way = make_uint2(__funnelshift_r(way.x, way.y, 8), way.y >> 8);
+          g = fmul4(g, lds4(decay + (way.x & 0xff) * kDim + 4 * lane));
         }
         // (queries stand a multiple of 16 rows behind the keys: the same swizzle)
         uint8_t *const x = mem + L::kX + tile_place(t, lane, L::kXBlock);
@@ -977,10 +1104,11 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       }
       fence_proxy_async_smem();
       arrive(&bars->x_full);
+      if (L::kRawBufs > 0 && lane == 0) mbar_arrive(&bars->raw_free[done % L::kCopies]);
       ++done;
       more = settle(it.next(lane));  // (its barrier: the nodes are read)
     }
-    cp_async_wait_all();
+    if (L::kRawBufs == 0) cp_async_wait_all();
     ok = it.ok;
   }
   if (!ok && lane == 0) report(mp.status, KDA_ERR_TIMEOUT);
@@ -999,8 +1127,24 @@ int launch(const TreeVerifyParams &p, int sms, cudaStream_t stream) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes) !=
       cudaSuccess)
     return KDA_ERR_CUDA;
+  TreeTokenMaps maps{};
+  if (L::kRawBufs > 0 && p.maps.n_tokens > 0) {
+    const auto encode = tensor_map_encoder();
+    if (encode == nullptr) return KDA_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)kDim, (cuuint64_t)p.H, (cuuint64_t)p.maps.n_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)kDim * 2, (cuuint64_t)p.H * kDim * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)kDim, 1, (cuuint32_t)kBoxTokens};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    const uint16_t *const src[4] = {p.k, p.q, p.g, p.v};
+    for (int i = 0; i < 4; ++i)
+      if (encode(&maps.of[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(src[i]),
+                 dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return KDA_ERR_CUDA;
+  }
   const int items = p.maps.B * p.H;
-  kernel<<<items < sms ? items : sms, L::kThreads, L::kBytes, stream>>>(p, items);
+  kernel<<<items < sms ? items : sms, L::kThreads, L::kBytes, stream>>>(p, maps, items);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
