@@ -25,7 +25,7 @@
 // (16 bytes a lane, four lanes to 64 bytes of a row), is replayed there,
 // written back from there, split there, and stored to tensor memory as the
 // A operand.  R goes the same way.  Where shared memory has room beside the
-// nodes, an FP32 page waits there first (kStaged).
+// nodes, a page waits there first (kStaged).
 //
 // R and [T; C] are multiplied whole, and zero times NaN is NaN: an R that is
 // not finite is left out as zero, and the outputs of its node and of those
@@ -35,20 +35,20 @@
 // the other, some items apart, as barriers in shared memory let them: the
 // requests (validated, their paths listed, copies of their nodes sent for) a
 // warp; nodes to X and Y; pages; T and C; R and the outputs; and two warps that
-// issue the products, of X and of R.  Each kind is a chain of latencies (shared memory, the shuffles of a
-// norm, a product's hand-off); one phase after the other by all warps, two CTAs
-// an SM, was slower: 804 against 646 us (128 windows of 64 nodes and 64 heads),
-// 111 against 89 (48 of up to 32 nodes, 32 heads), 115 against 101 (100 of 24,
-// BF16 pages).
+// issue the products, of X and of R.  Each kind is a chain of latencies (shared
+// memory, the shuffles of a norm, a product's hand-off); one phase after the
+// other by all warps, two CTAs an SM, was slower: 804 against 646 us (128
+// windows of 64 nodes and 64 heads), 111 against 89 (48 of up to 32 nodes, 32
+// heads), 115 against 101 (100 of 24, BF16 pages).
 //
 // Those three move 2053, 274 and 243 MB at 3.2, 3.1 and 2.4 TB/s (a copy's rate:
-// 6.7).  What bounds them is not HBM but instructions, their fetch, and the chains'
-// latencies: 43 thousand warp instructions an item of 64 nodes, 18 of 24, half of
-// the issue slots, half of the shared memory's wavefronts, a quarter of the
-// tensor pipe's cycles.  The roles' code, all of it in use at once, is more than
-// an SM's instruction cache holds: loops are rolled up wherever their state
-// allows it (BF16 pages, 24 nodes: 115 -> 101 us, the cache's hits from 64 to 84%
-// of the requests).
+// 6.7).  What bounds them is not HBM but instructions, their fetch, and the
+// chains' latencies: 43 thousand warp instructions an item of 64 nodes, 18 of
+// 24, half of the issue slots, half of the shared memory's wavefronts, a quarter
+// of the tensor pipe's cycles.  The roles' code, all of it in use at once, is
+// more than an SM's instruction cache holds: loops are rolled up wherever their
+// state allows it (BF16 pages, 24 nodes: 115 -> 101 us, the cache's hits from 64
+// to 84% of the requests).
 #include <cuda_runtime.h>
 
 #include <type_traits>
