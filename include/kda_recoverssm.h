@@ -758,7 +758,9 @@ int kda_tree_verify(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v,
  *   reported ones get 0, -1s and -1.  Reported too: a parent of node 0, a
  *   second root, a token outside 0 .. vocab - 1 (the root's is not looked
  *   at), weights whose total is not above zero and finite (accepted and path
- *   are kept then).  A weight that is NaN or negative counts as 0.
+ *   are kept then).  A target weight that is NaN or negative counts as 0; a
+ *   draft weight that is NaN refuses its token, which then has no weight in
+ *   the draw; draft weights are not negative.
  *   Uniforms lie in [0, 1).
  *   Comparisons and sums run at 48 bits or more, so that a token does not
  *   depend on the order of a sum.

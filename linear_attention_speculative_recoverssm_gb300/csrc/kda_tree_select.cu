@@ -31,7 +31,8 @@ struct TreeSelectParams {
   float *corr;
   uint16_t *kg, *window;
   long long corr_stride, kg_stride, slot_stride;
-  int width, H, most;  // most: the longest path that fits
+  int width, H, rq;    // (maps.rq is what the pending counts are clamped to)
+  int most;            // the longest path that fits
   int record_ctas;     // CTAs of a request that move records
 };
 
@@ -57,8 +58,8 @@ __global__ void __launch_bounds__(kTsThreads, 5) kda_tree_select_kernel(const Tr
     const int h = blockIdx.y * kTsHeads + (threadIdx.x >> 5);
     if (h >= p.H) return;
     const long long at = (long long)r.t0 * p.H + h;
-    float *corr = p.corr + r.row * p.corr_stride + (long long)h * mp.rq * kDim;
-    uint16_t *kg = p.kg + r.row * p.kg_stride + (long long)h * mp.rq * 2 * kDim;
+    float *corr = p.corr + r.row * p.corr_stride + (long long)h * p.rq * kDim;
+    uint16_t *kg = p.kg + r.row * p.kg_stride + (long long)h * p.rq * 2 * kDim;
     const uint16_t *half = lane < 16 ? p.k : p.g;
     // (three at a time: more registers leave fewer CTAs on an SM)
 #pragma unroll 1
@@ -183,6 +184,7 @@ extern "C" int kda_tree_select(const int32_t *path, const int32_t *accepted,
   p.slot_stride = conv_slot_stride;
   p.width = conv_width;
   p.H = H;
+  p.rq = rq;
   p.most = windows && conv_width - 2 < rq ? conv_width - 2 : rq;
   if (windows) p.maps.rq = conv_width - 2;  // what kda_tree_conv clamps the pending counts to
   p.record_ctas = (H + kda::kTsHeads - 1) / kda::kTsHeads;

@@ -240,6 +240,18 @@ def test_windows_beyond_32_bits():
     tg.check_select(case, d)
 
 
+@pytest.mark.parametrize("rq,width", [(4, 10), (8, 5), (1, 10), (8, 3), (3, 4)])
+def test_windows_of_another_length_than_the_records(rq, width):
+    """Records of rq tokens beside windows of width - 2: each keeps its own
+    layout, and a path fits both or is reported."""
+    case = tg.select_case([tt.chain(8), tt.comb(20), tt.star(5), tt.chain(2)], 3, 91, rq=rq)
+    rng = np.random.default_rng(91)
+    case["conv_state"] = rng.integers(0x3F00, 0x4000, case["conv_state"].shape[:2] + (width,)).astype(np.uint16)
+    too_long = int(((case["accepted"] > width - 2) & (case["state_slots"] > 0)).sum())
+    tg.check_conv(case, tg.run_conv(case))
+    tg.check_select(case, tg.run_select(case), bad=too_long)
+
+
 def test_select_the_same_node_twice():
     """A path is what it says, a tree's or not."""
     case = tg.select_case([tt.star(9), tt.chain(4), tt.comb(64)], 2, 87)
