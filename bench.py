@@ -17,8 +17,9 @@ in HBM.  Prints one JSON line (rank 0):
               every host core (one worker process per core, forked before
               any CUDA call), with the one-core figure beside it
 
-`--operators` times the prompt operators' cases (perf/operators.py) instead and
-prints one line of them.
+`--operators` times the cases of the prompt operators (perf/operators.py) and
+of the tree operators (perf/more_operators.py) instead and prints one line of
+them.
 
 `--impl reference` times the oracle alone (every host core, a bounded sample
 of items per step) and prints the same line with "impl": "reference".
@@ -1091,22 +1092,24 @@ def run_ours(args):
 
 
 def measure_operators(names, reps=15):
-    """The cases of perf/operators.py, each pass through the library's calls:
+    """The cases of the operators' files in perf/, each pass through the library's calls:
     device time (CUDA events behind a device-side sleep, L2 written over before
     each pass, the median of ``reps``) and the share of the floor that its bytes
     take at the measured copy rate."""
     import importlib.util
     import torch
-    spec = importlib.util.spec_from_file_location("operators",
-                                                  os.path.join(ROOT, "perf", "operators.py"))
-    ops = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(ops)
-    ops.own = True
+    cases = []
+    for file in ("operators", "more_operators"):
+        spec = importlib.util.spec_from_file_location(file, os.path.join(ROOT, "perf", file + ".py"))
+        ops = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ops)
+        ops.own = True
+        cases += [(ops, case) for case in ops.listed()]
     with open(os.path.join(ROOT, "MEASURED_PEAKS.json")) as f:
         peak = float(json.load(f).get("hbm_gbs", 6800.0))
     flush = torch.empty(64 * 2 ** 20, device="cuda")  # 256 MB
     rows = []
-    for case in ops.listed():
+    for ops, case in cases:
         if names and case["name"] not in names:
             continue
         state, times = ops.prepare(case, 1), []
@@ -1123,7 +1126,7 @@ def measure_operators(names, reps=15):
         us, floor = statistics.median(times), ops.work(case)["bytes"] / peak / 1e3
         rows.append({"case": case["name"], "us": round(us, 2), "floor_us": round(floor, 2)})
         del state
-    print(json.dumps({"metric": "prompt operators, device time", "unit": "us", "l2": "flushed",
+    print(json.dumps({"metric": "prompt and tree operators, device time", "unit": "us", "l2": "flushed",
                       "data": "synthetic", "rows": rows}), flush=True)
 
 
@@ -1148,7 +1151,7 @@ def main():
     ap.add_argument("--traffic", type=float, default=None,
                     help="ncu dram bytes per launch of the current kernel, if measured")
     ap.add_argument("--operators", nargs="?", const="", default=None, metavar="CASE,CASE",
-                    help="time the prompt operators' cases (all, or those named) and nothing else")
+                    help="time the prompt and tree operators' cases (all, or those named) and nothing else")
     args = ap.parse_args()
     if args.operators is not None:
         measure_operators([n for n in args.operators.split(",") if n])
