@@ -10,7 +10,7 @@
 // memory at once, asynchronously, and a node's four taps read there: window
 // entries and inputs alike, without a branch.
 //
-// 128 trees of up to 64 nodes, 32 heads (326 MB): 84 us, 3.9 TB/s (a copy: 6.7),
+// 128 trees of up to 33 nodes, 64 heads (326 MB): 84 us, 3.9 TB/s (a copy: 6.7),
 // with 55% of the issue slots and 44% of shared memory's wavefronts; the rows
 // leave room for a third of an SM's warps.  By events around the call 89 us; by
 // loads four nodes ahead in place of the copies 109, two channels a thread 112;

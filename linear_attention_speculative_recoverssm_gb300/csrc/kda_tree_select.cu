@@ -10,7 +10,7 @@
 // through shared memory whole, where a thread rewrites the few entries of its
 // four channels, and comes back in 16-byte pieces.
 //
-// 256 requests, 32 heads (285 MB of what has to move, 323 with the entries that
+// 256 requests, 64 heads (285 MB of what has to move, 323 with the entries that
 // are kept): 72 us, 4.0 TB/s (a copy: 6.7), the shared memory's path, where an
 // entry is 2 bytes, busy for 62%.  By events around the call 80 us, by one
 // channel a thread 95.
