@@ -209,6 +209,7 @@ struct TreeBars {
   uint64_t task_full[4], task_free[4];
   uint64_t raw_full[2], raw_free[2];  // keys, queries and gates as they are
   uint64_t x_full, x_free, y_free;  // X and Y
+  uint64_t n_full, n_free;          // norms and decays, where T's warps take nodes too
   uint64_t p_full, p_free;          // P in tensor memory
   uint64_t a_full, a_free;          // the page's parts
   uint64_t d_full[2], d_free[2];    // w and y, until o is out
@@ -226,6 +227,9 @@ struct TreeMma {
   static constexpr int kWarps = 32, kPageWarps = BF16 ? 4 : 8, kRWarps = 8, kTWarps = 2 * NC / 32;
   static constexpr int kR0 = kPageWarps, kT0 = kR0 + kRWarps, kIssue0 = kT0 + kTWarps,
                        kTask0 = kIssue0 + 2, kNode0 = kTask0 + 1, kNodeWarps = kWarps - kNode0;
+  // warps that make X and Y: of large trees T's and C's too, which wait meanwhile
+  static constexpr bool kTHelps = NC > 32;
+  static constexpr int kXWarps = kNodeWarps + (kTHelps ? kTWarps : 0);
   // registers a thread: at launch, of pages (whole warpgroups), of the others
   static constexpr int kPageRegs = kPageWarps == 4 ? 120 : 88, kOtherRegs = 56;
   static_assert(kPageWarps * kPageRegs + (kWarps - kPageWarps) * kOtherRegs <= kWarps * 64,
@@ -279,7 +283,7 @@ struct TreeMma {
   // there is room (48 requests of up to 32 nodes: 97 -> 91 us); else to registers, a
   // unit ahead, of BF16 pages four.
   static constexpr bool kStaged = NC <= 32;
-  static constexpr uint32_t kPage = round_up(kParent + kTreeNodes, 128);
+  static constexpr uint32_t kPage = kStaged ? round_up(kParent + kTreeNodes, 128) : kParent + kTreeNodes;
   static constexpr uint32_t kBars = kPage + (kStaged ? kPageWarps * 8192 : 0);
   static constexpr uint32_t kSlot = kBars + sizeof(TreeBars);
   static constexpr uint32_t kBytes = kSlot + 8;
@@ -407,7 +411,9 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       // (the warps of R may go through the tasks twice)
       mbar_init(&bars->task_free[i], L::kWarps - 1 + (L::kDBufs > 1 ? L::kRWarps : 0));
     }
-    mbar_init(&bars->x_full, L::kNodeWarps);
+    mbar_init(&bars->x_full, L::kXWarps);
+    mbar_init(&bars->n_full, L::kNodeWarps);
+    mbar_init(&bars->n_free, L::kTWarps);
     mbar_init(&bars->x_free, 1);
     mbar_init(&bars->y_free, 1);
     mbar_init(&bars->p_full, 1);
@@ -437,6 +443,40 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
   const auto arrive = [&](uint64_t *bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
+  };
+  // X and Y of `it`, the done-th item with nodes: nodes from the first-th on, a node
+  // a warp, four channels a lane
+  const auto make_xy = [&](TreeItems &it, const uint16_t *keys, const uint16_t *queries, int first,
+                           int done) {
+    const float *const norms = reinterpret_cast<const float *>(mem + L::kNorms);
+    const int n = it.n, cols = (n + 15) & ~15;
+    if (done > 0) {
+      it.wait(&bars->x_free, (uint32_t)(done - 1) & 1u);
+      it.wait(&bars->y_free, (uint32_t)(done - 1) & 1u);
+    }
+#pragma unroll 1
+    for (int t = first; t < n; t += L::kXWarps) {
+      const uint2 path = it.paths()[t];
+      const int m = path.x & 0xff;
+      float4 g = lds4(decay + t * kDim + 4 * lane);
+      const float4 k = scale4(bf16x4(*reinterpret_cast<const uint2 *>(keys + t * kDim + 4 * lane)), norms[t]);
+      const float4 q = scale4(bf16x4(*reinterpret_cast<const uint2 *>(queries + t * kDim + 4 * lane)), norms[NC + t]);
+      uint2 way = path;
+#pragma unroll 1
+      for (int j = 0; j < m; ++j) {  // (the same in every lane)
+        way = make_uint2(__funnelshift_r(way.x, way.y, 8), way.y >> 8);
+        g = fmul4(g, lds4(decay + (way.x & 0xff) * kDim + 4 * lane));
+      }
+      // (queries stand a multiple of 16 rows behind the keys: the same swizzle)
+      uint8_t *const x = mem + L::kX + tile_place(t, lane, L::kXBlock);
+      store_parts(x, L::kXPart, fmul4(k, g));
+      store_parts(x + cols * 128, L::kXPart, fmul4(q, g));
+      store_parts(mem + L::kY + tile_place(t, lane, L::kYBlock), L::kYPart,
+                  make_float4(k.x * rcp_fast(g.x), k.y * rcp_fast(g.y), k.z * rcp_fast(g.z),
+                              k.w * rcp_fast(g.w)));
+    }
+    fence_proxy_async_smem();
+    arrive(&bars->x_full);
   };
   bool ok = true;
   if (warp < L::kR0) {
@@ -752,6 +792,14 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       const bool live = row < 2 * cols && t < n;
       const uint2 path = live ? it.paths()[t] : make_uint2(0, 0);
       const int m = live ? (int)(path.x & 0xff) : -1;
+      uint16_t beta = 0;
+      if constexpr (L::kTHelps) {
+        it.wait(&bars->n_full, (uint32_t)done & 1u);
+        const uint16_t *const raw = reinterpret_cast<const uint16_t *>(mem + L::kK);
+        make_xy(it, raw, raw + NC * kDim, L::kNodeWarps + tw, done);
+        arrive(&bars->n_free);
+      }
+      if (live) beta = __ldg(p.beta + (long long)(it.t0 + t) * p.H + it.h);
       // this item's values on their way to L2, and the next head's nodes (elsewhere
       // the warp with the requests sends for them)
       if constexpr (L::kRawBufs == 0)
@@ -764,8 +812,6 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
             prefetch_l2((what == 1 ? p.k : (what == 2 ? p.q : p.g)) + at + kDim);
           }
         }
-      uint16_t beta = 0;
-      if (live) beta = __ldg(p.beta + (long long)(it.t0 + t) * p.H + it.h);
       it.wait(&bars->p_full, (uint32_t)done & 1u);
       tc_fence_after();
       for (int c = 0; c < cols; c += 16) {
@@ -1020,6 +1066,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     const auto settle = [&](bool more) {
       while (more && it.n == 0) more = it.next(lane);
       if (named_bar_or(1, kThreads, !it.ok)) return it.ok = false;
+      if (L::kTHelps && done > 0) it.wait(&bars->n_free, (uint32_t)(done - 1) & 1u);
       if (L::kRawBufs == 0 && more) {
         const int c8 = 8 * (lane & 15);
 #pragma unroll 1
@@ -1076,34 +1123,8 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         }
       }
       named_bar(1, kThreads);
-      if (done > 0) {
-        it.wait(&bars->x_free, (uint32_t)(done - 1) & 1u);
-        it.wait(&bars->y_free, (uint32_t)(done - 1) & 1u);
-      }
-      // X and Y: a node a warp, four channels a lane
-#pragma unroll 1
-      for (int t = nw; t < n; t += L::kNodeWarps) {
-        const uint2 path = it.paths()[t];
-        const int m = path.x & 0xff;
-        float4 g = lds4(decay + t * kDim + 4 * lane);
-        const float4 k = scale4(bf16x4(*reinterpret_cast<const uint2 *>(keys + t * kDim + 4 * lane)), norms[t]);
-        const float4 q = scale4(bf16x4(*reinterpret_cast<const uint2 *>(queries + t * kDim + 4 * lane)), norms[NC + t]);
-        uint2 way = path;
-#pragma unroll 1
-        for (int j = 0; j < m; ++j) {  // (the same in every lane)
-          way = make_uint2(__funnelshift_r(way.x, way.y, 8), way.y >> 8);
-          g = fmul4(g, lds4(decay + (way.x & 0xff) * kDim + 4 * lane));
-        }
-        // (queries stand a multiple of 16 rows behind the keys: the same swizzle)
-        uint8_t *const x = mem + L::kX + tile_place(t, lane, L::kXBlock);
-        store_parts(x, L::kXPart, fmul4(k, g));
-        store_parts(x + cols * 128, L::kXPart, fmul4(q, g));
-        store_parts(mem + L::kY + tile_place(t, lane, L::kYBlock), L::kYPart,
-                    make_float4(k.x * rcp_fast(g.x), k.y * rcp_fast(g.y), k.z * rcp_fast(g.z),
-                                k.w * rcp_fast(g.w)));
-      }
-      fence_proxy_async_smem();
-      arrive(&bars->x_full);
+      if (L::kTHelps) arrive(&bars->n_full);
+      make_xy(it, keys, queries, nw, done);
       if (L::kRawBufs > 0 && lane == 0) mbar_arrive(&bars->raw_free[done % L::kCopies]);
       ++done;
       more = settle(it.next(lane));  // (its barrier: the nodes are read)
