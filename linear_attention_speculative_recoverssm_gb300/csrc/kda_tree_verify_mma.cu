@@ -37,11 +37,11 @@
 // warp; nodes to X and Y; pages; T and C; R and the outputs; and two warps that
 // issue the products, of X and of R.  Each kind is a chain of latencies (shared
 // memory, the shuffles of a norm, a product's hand-off); one phase after the
-// other by all warps, two CTAs an SM, was slower: 804 against 646 us (128
+// other by all warps, two CTAs an SM, was slower: 804 against 605 us (128
 // windows of 64 nodes and 64 heads), 111 against 89 (48 of up to 32 nodes, 32
 // heads), 115 against 101 (100 of 24, BF16 pages).
 //
-// Those three move 2053, 274 and 243 MB at 3.2, 3.1 and 2.4 TB/s (a copy's rate:
+// Those three move 2053, 274 and 243 MB at 3.4, 3.1 and 2.4 TB/s (a copy's rate:
 // 6.7).  What bounds them is not HBM but instructions, their fetch, and the
 // chains' latencies: 43 thousand warp instructions an item of 64 nodes, 18 of
 // 24, half of the issue slots, half of the shared memory's wavefronts, a quarter
@@ -209,7 +209,7 @@ struct TreeBars {
   uint64_t task_full[4], task_free[4];
   uint64_t raw_full[2], raw_free[2];  // keys, queries and gates as they are
   uint64_t x_full, x_free, y_free;  // X and Y
-  uint64_t n_full, n_free;          // norms and decays, where T's warps take nodes too
+  uint64_t n_full;                  // norms and decays, where T's warps take nodes too
   uint64_t p_full, p_free;          // P in tensor memory
   uint64_t a_full, a_free;          // the page's parts
   uint64_t d_full[2], d_free[2];    // w and y, until o is out
@@ -228,6 +228,7 @@ struct TreeMma {
   static constexpr int kR0 = kPageWarps, kT0 = kR0 + kRWarps, kIssue0 = kT0 + kTWarps,
                        kTask0 = kIssue0 + 2, kNode0 = kTask0 + 1, kNodeWarps = kWarps - kNode0;
   // warps that make X and Y: of large trees T's and C's too, which wait meanwhile
+  // (64 nodes: 648 -> 605 us)
   static constexpr bool kTHelps = NC > 32;
   static constexpr int kXWarps = kNodeWarps + (kTHelps ? kTWarps : 0);
   // registers a thread: at launch, of pages (whole warpgroups), of the others
@@ -413,7 +414,6 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     }
     mbar_init(&bars->x_full, L::kXWarps);
     mbar_init(&bars->n_full, L::kNodeWarps);
-    mbar_init(&bars->n_free, L::kTWarps);
     mbar_init(&bars->x_free, 1);
     mbar_init(&bars->y_free, 1);
     mbar_init(&bars->p_full, 1);
@@ -797,7 +797,6 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         it.wait(&bars->n_full, (uint32_t)done & 1u);
         const uint16_t *const raw = reinterpret_cast<const uint16_t *>(mem + L::kK);
         make_xy(it, raw, raw + NC * kDim, L::kNodeWarps + tw, done);
-        arrive(&bars->n_free);
       }
       if (live) beta = __ldg(p.beta + (long long)(it.t0 + t) * p.H + it.h);
       // this item's values on their way to L2, and the next head's nodes (elsewhere
@@ -1066,7 +1065,8 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     const auto settle = [&](bool more) {
       while (more && it.n == 0) more = it.next(lane);
       if (named_bar_or(1, kThreads, !it.ok)) return it.ok = false;
-      if (L::kTHelps && done > 0) it.wait(&bars->n_free, (uint32_t)(done - 1) & 1u);
+      // (T's warps have read the nodes as well)
+      if (L::kTHelps && done > 0) it.wait(&bars->x_full, (uint32_t)(done - 1) & 1u);
       if (L::kRawBufs == 0 && more) {
         const int c8 = 8 * (lane & 15);
 #pragma unroll 1
