@@ -282,10 +282,13 @@ struct TreeMma {
   static constexpr uint32_t kParent = kTasks + 4 * sizeof(TreeTask);
   // A page comes here by asynchronous copies, a whole item ahead, 8 KB a warp, where
   // there is room (48 requests of up to 32 nodes: 97 -> 91 us); else to registers, a
-  // unit ahead, of BF16 pages four.
+  // unit ahead, of BF16 pages four.  A warp's rows of an FP32 page are one piece of
+  // memory and one copy, as they are (83 -> 82 us of the kernel alone); those of a BF16 page, whose rows would meet in
+  // the banks four times over, go by 16 bytes each to a place of their own.
   static constexpr bool kStaged = NC <= 32;
   static constexpr uint32_t kPage = kStaged ? round_up(kParent + kTreeNodes, 128) : kParent + kTreeNodes;
-  static constexpr uint32_t kBars = kPage + (kStaged ? kPageWarps * 8192 : 0);
+  static constexpr uint32_t kPageBars = kPage + (kStaged ? kPageWarps * 8192 : 0);  // its parts are there
+  static constexpr uint32_t kBars = kPageBars + (kStaged ? kPageWarps * 8 : 0);
   static constexpr uint32_t kSlot = kBars + sizeof(TreeBars);
   static constexpr uint32_t kBytes = kSlot + 8;
   static_assert(kTasks % 8 == 0 && kBars % 8 == 0 && sizeof(TreeTask) % 8 == 0, "alignment");
@@ -305,11 +308,11 @@ struct PageUnit {
 #pragma unroll
       for (int i = 0; i < 2; ++i) s[j][i] = __ldcs(from + (8 * i * kDim + 16 * j) / 4);
   }
-  // From a warp's staged rows, 256 bytes of each: 16-byte piece c of row r stands at
-  // place(r, c), where no two of eight lanes meet in a bank.
+  // From a warp's staged rows.  Of BF16, 256 bytes a row, 16-byte piece c of row r
+  // stands at place(r, c), where no two of 16 lanes meet in a bank; of FP32 the rows
+  // stand as in memory, and pairs of lanes meet.
   static __device__ __forceinline__ int place(int r, int c) {
-    return BF16 ? r * 256 + ((c >> 1 ^ (r & 3)) << 5) + (c & 1) * 16
-                : r * 256 + ((c >> 2 ^ (r & 1)) << 6) + (c & 3) * 16;
+    return r * 256 + ((c >> 1 ^ (r & 3)) << 5) + (c & 1) * 16;
   }
   __device__ __forceinline__ void load_staged(const uint8_t *rows, int row, int key, int lane) {
 #pragma unroll
@@ -317,7 +320,8 @@ struct PageUnit {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = row + lane / 4 + 8 * i, byte = (key + 16 * j + 4 * (lane & 3)) * (BF16 ? 2 : 4);
-        s[j][i] = *reinterpret_cast<const Four *>(rows + place(r, byte >> 4) + (byte & 15));
+        const int at = BF16 ? place(r, byte >> 4) + (byte & 15) : r * (kDim * 4) + byte;
+        s[j][i] = *reinterpret_cast<const Four *>(rows + at);
       }
   }
 };
@@ -420,6 +424,8 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     mbar_init(&bars->p_free, L::kTWarps);
     mbar_init(&bars->a_full, L::kPageWarps);
     mbar_init(&bars->a_free, 1);
+    if (L::kStaged)
+      for (int i = 0; i < L::kPageWarps; ++i) mbar_init(reinterpret_cast<uint64_t *>(mem + L::kPageBars) + i, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->d_full[i], 1);
       mbar_init(&bars->d_free[i], L::kRWarps);
@@ -486,30 +492,43 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
   }
 
   if (warp < L::kR0) {
-    // ======== pages: rows 32 quarter .. + 31, keys kKeys which .. + kKeys - 1
+    // ======== pages: of a quarter's rows half of the keys a warp, of FP32 staged ones
+    // half of the rows (and BF16 pages have one warp a quarter)
     // units of 16 rows and 32 keys, those of the same rows first
-    constexpr int kUnits = 32 / L::kPageWarps, kKeys = 16 * kUnits, kThreads = 32 * L::kPageWarps;
+    constexpr bool kBulk = L::kStaged && !BF16;
+    constexpr int kUnits = 32 / L::kPageWarps, kKeys = kBulk ? kDim : 16 * kUnits, kThreads = 32 * L::kPageWarps;
     constexpr int kAhead = L::kStaged ? 0 : BF16 ? 4 : 1, kRecs = kMaxQ / L::kPageWarps;
     uint8_t *const staged = mem + L::kPage + warp * 8192;
-    const auto unit_at = [](int e) { return 16 * (e / (kUnits / 2)) * kDim + 32 * (e % (kUnits / 2)); };
+    uint64_t *const page_full = reinterpret_cast<uint64_t *>(mem + L::kPageBars) + warp;
+    constexpr int kInRow = kKeys / 32;  // units of the same rows
+    const auto unit_at = [](int e) { return 16 * (e / kInRow) * kDim + 32 * (e % kInRow); };
     const int quarter = warp & 3, which = warp >> 2;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    const int row0 = 32 * quarter + (kBulk ? 16 * which : 0), key0 = kBulk ? 0 : kKeys * which;
+    const uint32_t lanes = tmem + ((uint32_t)row0 << 16);
     float *const rk = reinterpret_cast<float *>(mem + L::kReplayK);
     float *const rd = reinterpret_cast<float *>(mem + L::kReplayD);
     float *const ru = reinterpret_cast<float *>(mem + L::kReplayU);
     float *const rdn = reinterpret_cast<float *>(mem + L::kReplayDn);
-    const int k0 = kKeys * which + 4 * (lane & 3);
+    const int k0 = key0 + 4 * (lane & 3);
     TreeItems it;
     int done = 0;  // items with nodes
+    uint32_t asked = 0, had = 0;  // pages
+    float4 rec_dt;
+    float rec_a;
     PageUnit<BF16> pg[L::kStaged ? 1 : kUnits];
     uint2 rec_k[kRecs], rec_g[kRecs];
     float4 rec_u[kRecs];
-    // an item's records (a warp one) and first units, ahead of its turn; and the
-    // next head's page on its way to L2
+    // an item's records (a warp one; gates' constants where registers are left for
+    // them) and first units, ahead of its turn; and the next head's page on its way
+    // to L2
     const auto page_part = [&] {
-      return page_of(it.slot, it.h) + (long long)(32 * quarter + lane / 4) * kDim + k0;
+      return page_of(it.slot, it.h) + (long long)(row0 + lane / 4) * kDim + k0;
     };
     const auto ask = [&] {
+      if (kBulk && it.pending > 0) {
+        rec_dt = __ldg(reinterpret_cast<const float4 *>(p.dt_bias + it.h * kDim) + lane);
+        rec_a = __ldg(p.A_log + it.h);
+      }
 #pragma unroll
       for (int i = 0; i < kRecs; ++i)
         if (warp + i * L::kPageWarps < it.pending) {
@@ -519,13 +538,20 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
           rec_g[i] = __ldg(rec + 32);
           rec_u[i] = __ldg(reinterpret_cast<const float4 *>(p.corr + it.row * p.corr_stride + row * kDim) + lane);
         }
-      if constexpr (L::kStaged) {
+      if constexpr (kBulk) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(page_full, 8192);
+          bulk_g2s(staged, static_cast<const float *>(p.state) + page_of(it.slot, it.h) + row0 * kDim, 8192,
+                   page_full);
+        }
+        ++asked;
+      } else if constexpr (L::kStaged) {
         const char *from = static_cast<const char *>(p.state) +
-                           (page_of(it.slot, it.h) + 32 * quarter * kDim + kKeys * which) * (BF16 ? 2 : 4);
+                           (page_of(it.slot, it.h) + row0 * kDim) * 2;
 #pragma unroll 2
         for (int i = lane; i < 512; i += 32)
-          cp_async16(staged + PageUnit<BF16>::place(i >> 4, i & 15),
-                     from + (i >> 4) * (kDim * (BF16 ? 2 : 4)) + 16 * (i & 15));
+          cp_async16(staged + PageUnit<true>::place(i >> 4, i & 15),
+                     from + (i >> 4) * (kDim * 2) + 16 * (i & 15));
       } else {
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) pg[e].load(p.state, page_part() + unit_at(e));
@@ -547,10 +573,12 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         for (int i = 0; i < kRecs; ++i)
           if (const int t = warp + i * L::kPageWarps; t < replay) {
             const float4 k = bf16x4(rec_k[i]);
-            const float4 dt = __ldg(reinterpret_cast<const float4 *>(p.dt_bias + it.h * kDim) + lane);
-            const float a = expf(__ldg(p.A_log + it.h));
+            if (!kBulk) {
+              rec_dt = __ldg(reinterpret_cast<const float4 *>(p.dt_bias + it.h * kDim) + lane);
+              rec_a = __ldg(p.A_log + it.h);
+            }
             sts4(rk + t * kDim + 4 * lane, scale4(k, rsqrtf(warp_sum(dot4(k, k)) + kNormEps)));
-            sts4(rd + t * kDim + 4 * lane, decay4(a, bf16x4(rec_g[i]), dt, p.lower_bound));
+            sts4(rd + t * kDim + 4 * lane, decay4(expf(rec_a), bf16x4(rec_g[i]), rec_dt, p.lower_bound));
             sts4(ru + t * kDim + 4 * lane, rec_u[i]);
           }
         named_bar(3, kThreads);
@@ -562,18 +590,20 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         it.wait(&bars->a_free, (uint32_t)(done - 1) & 1u);
         tc_fence_after();
       }
-      if (L::kStaged) {
+      if (kBulk) {
+        it.wait(page_full, had++ & 1u);
+      } else if (L::kStaged) {
         cp_async_wait_all();
         __syncwarp();
       }
 #pragma unroll(L::kStaged ? 1 : kUnits)
       for (int e = 0; e < kUnits; ++e) {
         PageUnit<BF16> &unit = pg[L::kStaged ? 0 : e];
-        const int rh = e / (kUnits / 2), k32 = 32 * (e % (kUnits / 2));
+        const int rh = e / kInRow, k32 = 32 * (e % kInRow);
         if constexpr (L::kStaged) unit.load_staged(staged, 16 * rh, k32, lane);
         if constexpr (!BF16) {
           if (replay > 0) {
-            const float *up = ru + 32 * quarter + 16 * rh + lane / 4;
+            const float *up = ru + row0 + 16 * rh + lane / 4;
             const float *kp = rk + k0 + k32, *dp = rdn + k0 + k32;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -612,7 +642,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
                 s = make_float4(lo.x, lo.y, hi.x, hi.y);
               }
             }
-            tm_store_16x16(lanes + ((uint32_t)(16 * rh) << 16) + kTmPartCols * part + (kKeys * which + k32) / 2, w);
+            tm_store_16x16(lanes + ((uint32_t)(16 * rh) << 16) + kTmPartCols * part + (key0 + k32) / 2, w);
           }
         if constexpr (!L::kStaged)
           if (e + kAhead < kUnits) pg[e + kAhead].load(p.state, page + unit_at(e + kAhead));
@@ -629,7 +659,8 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
       // (the replay's operands are read)
       if (named_bar_or(3, kThreads, !it.ok)) more = it.ok = false;
     }
-    if (L::kStaged) cp_async_wait_all();
+    if (had < asked) it.wait(page_full, had & 1u);
+    if (L::kStaged && !kBulk) cp_async_wait_all();
     ok = it.ok;
   } else if (warp < L::kT0) {
     // ======== R and the outputs: a row a lane, eight nodes at a time
