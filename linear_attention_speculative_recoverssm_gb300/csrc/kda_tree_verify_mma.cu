@@ -38,12 +38,12 @@
 // issue the products, of X and of R.  Each kind is a chain of latencies (shared
 // memory, the shuffles of a norm, a product's hand-off); one phase after the
 // other by all warps, two CTAs an SM, was slower: 804 against 605 us (128
-// windows of 64 nodes and 64 heads), 111 against 89 (48 of up to 32 nodes, 32
+// windows of 64 nodes and 64 heads), 111 against 87 (48 of up to 32 nodes, 32
 // heads), 115 against 101 (100 of 24, BF16 pages).
 //
-// Those three move 2053, 274 and 243 MB at 3.4, 3.1 and 2.4 TB/s (a copy's rate:
+// Those three move 2053, 274 and 243 MB at 3.4, 3.2 and 2.4 TB/s (a copy's rate:
 // 6.7).  What bounds them is not HBM but instructions, their fetch, and the
-// chains' latencies: 43 thousand warp instructions an item of 64 nodes, 18 of
+// chains' latencies: 46 thousand warp instructions an item of 64 nodes, 18 of
 // 24, half of the issue slots, half of the shared memory's wavefronts, a quarter
 // of the tensor pipe's cycles.  The roles' code, all of it in use at once, is
 // more than an SM's instruction cache holds: loops are rolled up wherever their
