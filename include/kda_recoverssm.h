@@ -707,7 +707,7 @@ int kda_tree_conv(const kda_bf16 *x, const kda_bf16 *conv_weight, const kda_bf16
  * takes the accepted path's.  The records are only read.  The replay does not
  * depend on the window: it runs for an empty one too, and with n_tokens == 0.
  * Inert requests get zeros in `out`, and nothing else is written.
- *   What is held in fewer bits: windows of more than six nodes form the
+ *   What is held in fewer bits: windows of more than four nodes may form the
  *   products of the state and of pairs of nodes from operands in three BF16
  *   parts (24 bits; a gate path whose decays multiply to less than 2^-110 or
  *   so loses its last part); states, sums, norms, gates and decays are FP32.

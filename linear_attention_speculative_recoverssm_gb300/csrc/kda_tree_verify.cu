@@ -282,11 +282,13 @@ extern "C" int kda_tree_verify(
   const int sms = kda::device_sm_count(dev);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Windows of a few nodes by FMA, and of few items by a CTA for every 32 rows;
-  // all others on the tensor cores.  FP32 pages with a replay, us by rows of
-  // 32 / by whole pages / on the tensor cores: 4 nodes, 32 items 14 / 15 / 17,
-  // 192 items 25 / 19 / 25, 1536 items 130 / 74 / 83; 8 nodes, 32 items 17 / 19 /
-  // 17, 1536 items 181 / 95 / 85; 15 nodes, 32 items 23 / 25 / 17.
-  if (Q > kda::kTrMaxQ) return kda::launch_tree_mma(p, bf16, sms, st);
+  // all others on the tensor cores.  FP32 pages with a replay, us by FMA (by rows
+  // of 32 / by whole pages) and on the tensor cores: 4 nodes, 32 items 13 / 15 and
+  // 15, 192 items 25 / 19 and 25, 1536 items 130 / 74 and 74; 6 nodes, 32 items 15
+  // and 17, 192 items 21 and 25, 512 items 37 and 37, 1536 items 87 and 74; 8 nodes,
+  // 1536 items 95 and 75; 15 nodes, 32 items 23 / 25 and 17.
+  if (Q > kda::kTrMaxQ || (Q > 4 && (long long)B * H > 4LL * sms))
+    return kda::launch_tree_mma(p, bf16, sms, st);
   if ((long long)B * H * 4 <= sms)
     return bf16 ? kda::launch_rows<32, true>(p, st) : kda::launch_rows<32, false>(p, st);
   return bf16 ? kda::launch_rows<128, true>(p, st) : kda::launch_rows<128, false>(p, st);
