@@ -168,6 +168,17 @@ def test_a_state_row_that_is_not_finite(value, n):
         assert torch.equal(got[~hit], want[~hit])
 
 
+@pytest.mark.parametrize("cap", [6, 20, 64])
+@pytest.mark.parametrize("pool", ["f32", "bf16"])
+def test_fewer_tokens_than_a_window_may_hold(pool, cap):
+    """One token, and three in two requests, where windows may hold `cap`."""
+    for sizes in ([1], [2, 0, 1]):
+        case = tt.tree_case(trees_of(2, sizes), 2, seed=92, pool=pool, replay=pool == "f32")
+        case["Q"] = cap
+        tg.check_verify(case, tg.run_verify(case))
+        tg.check_conv(case, tg.run_conv(case))
+
+
 def test_rows_behind_the_last_hold_anything():
     """NaN in every row that belongs to no request, in slots and rows that
     none has, and between strides."""
