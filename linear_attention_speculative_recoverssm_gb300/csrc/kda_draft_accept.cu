@@ -191,6 +191,8 @@ __device__ bool walk(const AcceptParams &p, const TreeRequest &r, int b, int lan
     sm.p[t] = w > 0.f ? w : 0.f;
     if (draft != nullptr) qx[i] = weight_at(draft + (long long)(r.t0 + t) * p.draft_stride, x);
   }
+  // (tokens and weights are there for the other lanes: a vote orders no memory)
+  __syncwarp();
   if (!__all_sync(0xffffffffu, good)) return false;
   // (nodes past the window are nobody's children)
   const uint32_t live[2] = {r.n >= 32 ? 0xffffffffu : (1u << r.n) - 1u,

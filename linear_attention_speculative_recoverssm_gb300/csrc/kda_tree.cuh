@@ -80,6 +80,7 @@ __device__ __forceinline__ int tree_depth(const int8_t *parent, int t) {
 __device__ __forceinline__ bool load_tree(const TreeMaps &p, const TreeRequest &r,
                                           int8_t *parent, int lane) {
   bool good = true;
+  __syncwarp();  // (the tree that was there before is read)
 #pragma unroll
   for (int i = 0; i < kTreeNodes / 32; ++i) {
     const int t = lane + 32 * i;
