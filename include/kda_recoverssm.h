@@ -646,9 +646,10 @@ int kda_recurrent(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const
  * convolution find it:
  *
  *   kda_tree_conv -> kda_tree_verify -> (the model's logits) ->
- *   kda_draft_accept -> kda_tree_select -> kda_defer_commit.
+ *   kda_draft_accept -> kda_tree_settle -> kda_tree_select ->
+ *   kda_defer_commit.
  *
- * Conventions that the four share, beside those at the top of this file:
+ * Conventions that they share, beside those at the top of this file:
  *  - Request b's nodes are the tokens query_start_loc[b] ..
  *    query_start_loc[b + 1] - 1 of the packed activations (b*Q .. b*Q + Q - 1
  *    when query_start_loc is NULL; n_tokens is B*Q then), n_b <= Q <=
@@ -778,6 +779,31 @@ int kda_draft_accept(const void *target, const void *draft, int probs_dtype,
                      const int32_t *state_slots, const int32_t *query_start_loc, int n_tokens,
                      int32_t *accepted, int32_t *path, int32_t *next_tokens, int B, int Q,
                      int null_slot, int32_t *status, void *stream);
+
+/*
+ * kda_tree_settle -- which requests of the step go on.  kda_tree_verify leaves a
+ * request that it reports as it was, its replay pending; the zero that
+ * kda_draft_accept gives it would make kda_tree_select move its window, and
+ * kda_defer_commit drop the replay.  Per request b, with row = record_rows[b]:
+ *   inert, or without a record row: rows[b] = row;
+ *   its window, slot, row or (parents given) tree bad, or served[b] < 0:
+ *     reported (KDA_ERR_ARG), accepted[b] = 0 and rows[b] = -1, so that select
+ *     and defer, called with `rows` in place of record_rows, leave its records,
+ *     window and pending count alone; with folded != 0 (its replay was folded in
+ *     otherwise, by kda_flush_plan and kda_commit) rows[b] = row all the same, a
+ *     bad slot or row excepted: nothing of the step is accepted;
+ *   any other: rows[b] = row.
+ *   accepted [B] int32, read and written, or NULL; served [B] int32 or NULL: the
+ *   rows that an earlier call of the same step made, beside kda_tree_verify and
+ *   with its parents; rows [B] int32, may be served or record_rows itself;
+ *   parents NULL: no tree is looked at, and windows may hold up to
+ *   KDA_TREE_MAX_NODES tokens; n_slots of the state pool, n_rows of the records.
+ */
+int kda_tree_settle(int32_t *accepted, const int32_t *state_slots, int n_slots,
+                    const int32_t *record_rows, const int32_t *served, int n_rows,
+                    const int32_t *parents, const int32_t *query_start_loc, int n_tokens,
+                    int folded, int32_t *rows, int B, int Q, int null_slot, int32_t *status,
+                    void *stream);
 
 /*
  * kda_tree_select -- the accepted path's nodes to the front of the request's

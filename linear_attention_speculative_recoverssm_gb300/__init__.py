@@ -46,6 +46,7 @@ from ._lib import (  # noqa: F401
     kda_slot_plan,
     kda_tree_conv,
     kda_tree_select,
+    kda_tree_settle,
     kda_tree_verify,
     kda_verify,
     layer_tables,

@@ -39,7 +39,7 @@ EXPORTS = ("kda_abi_version", "kda_error_string", "kda_check_status", "kda_verif
            "kda_layer_step", "kda_layer_step_noalloc", "kda_slot_plan", "kda_prefill_conv",
            "kda_prefill_workspace_bytes", "kda_prefill_workspace_bytes_for", "kda_prefill",
            "kda_recurrent", "kda_tree_conv", "kda_tree_verify", "kda_draft_accept",
-           "kda_tree_select")
+           "kda_tree_settle", "kda_tree_select")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -86,6 +86,7 @@ _SIGS = {
                                     _I64, _I64, _I, _I, _P, _P] + [_I, _I, _I, _I, _P, _P], _I),
     "kda_draft_accept": ([_P, _P, _I, _I64, _I64, _I] + [_P] * 6 + [_I, _P, _P, _P]
                          + [_I, _I, _I, _P, _P], _I),
+    "kda_tree_settle": ([_P, _P, _I, _P, _P, _I, _P, _P, _I, _I, _P] + [_I, _I, _I, _P, _P], _I),
     "kda_tree_select": ([_P] * 11 + [_I64, _I64, _I, _I, _P, _P, _I64, _I, _I, _P, _I]
                         + [_I, _I, _I, _I, _P, _P], _I),
 }
@@ -802,6 +803,34 @@ def kda_draft_accept(target_probs, tokens, accept_uniforms, sample_uniforms, acc
             accepted.data_ptr(), path.data_ptr(), next_tokens.data_ptr(), B, Q, null_slot,
             _address(status), st))
     return _check("kda_draft_accept", rc, raise_on_error)
+
+
+def kda_tree_settle(state_slots, record_rows, rows, *, Q, n_tokens, n_slots, n_rows, accepted=None,
+                    parents=None, served=None, query_start_loc=None, folded=False, null_slot=0,
+                    status=None, stream=None, raise_on_error=True):
+    """Between kda_draft_accept and kda_tree_select: record_rows [B] to ``rows``
+    [B] (int32; they may be one), -1 for the requests that kda_tree_verify
+    reported, whose replays are still pending (bad windows, slots, rows and,
+    with ``parents`` [n_tokens], trees), and 0 to their ``accepted``.  Select and
+    kda_defer_commit, called with ``rows``, leave those as they were.
+    ``served``: the rows of an earlier call of the same step, beside the verify
+    (``parents`` are not needed then).  ``folded``: the replays were folded in
+    otherwise, and such a request keeps its row.  n_slots, n_rows: of the state
+    pool and of the records."""
+    import torch
+    i32, dev, B = torch.int32, state_slots.device, state_slots.shape[0]
+    per = (B,)
+    _expect_tensors(dev, ("state_slots", state_slots, i32, per),
+                    ("record_rows", record_rows, i32, per), ("rows", rows, i32, per),
+                    ("served", served, i32, per), ("accepted", accepted, i32, per),
+                    ("parents", parents, i32, (n_tokens,)),
+                    ("query_start_loc", query_start_loc, i32, (B + 1,)),
+                    ("status", status, i32, (1,)))
+    rc = _call_on(dev, stream, lambda st: load().kda_tree_settle(
+            _address(accepted), state_slots.data_ptr(), n_slots, _address(record_rows),
+            _address(served), n_rows, _address(parents), _address(query_start_loc), n_tokens,
+            int(folded), rows.data_ptr(), B, Q, null_slot, _address(status), st))
+    return _check("kda_tree_settle", rc, raise_on_error)
 
 
 def kda_tree_select(path, accepted, k, raw_g, node_corr, state_slots, record_rows, corr, key_gate,

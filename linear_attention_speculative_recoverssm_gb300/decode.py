@@ -27,8 +27,8 @@ steps can be captured in a CUDA graph.
 from __future__ import annotations
 
 from ._lib import (KDA_STATE_F32, kda_commit, kda_defer_commit, kda_flush_plan,
-                   kda_prefill, kda_replay_verify, kda_tree_select, kda_tree_verify, kda_verify,
-                   layer_tables)
+                   kda_prefill, kda_replay_verify, kda_tree_select, kda_tree_settle,
+                   kda_tree_verify, kda_verify, layer_tables)
 
 
 class DeferredRecoverSSM:
@@ -58,6 +58,9 @@ class DeferredRecoverSSM:
         self._fresh = torch.full((self.B,), self.null_slot, dtype=torch.int32, device=dev)
         self._none = torch.zeros(self.B, dtype=torch.int32, device=dev)
         self._no_row = torch.tensor(-1, dtype=torch.int32, device=dev)
+        # the record rows of the requests that verify_tree served, for accept_tree
+        self._rows = torch.full((self.B,), -1, dtype=torch.int32, device=dev)
+        self._settled = False  # they are this step's
         self.flushed = False
 
     def _commit(self, commit_lens, destinations, boundaries=None, boundary_lens=None):
@@ -142,12 +145,14 @@ class DeferredRecoverSSM:
         the commit plan, non-zero only on eager rows) becomes each request's
         pending replay; ``eager`` (uint8 [B] or None) marks rows committed
         now instead."""
-        kda_defer_commit(self.state_slots, accepted, self.record_rows, self.pending,
-                         eager=eager, null_slot=self.null_slot, status=self.status,
-                         stream=self.stream)
+        self._accept(accepted, self.record_rows, eager)
+
+    def _accept(self, accepted, rows, eager):
+        kda_defer_commit(self.state_slots, accepted, rows, self.pending, eager=eager,
+                         null_slot=self.null_slot, status=self.status, stream=self.stream)
         if eager is not None:
             self._commit(accepted, self.state_slots)
-        self.flushed = False
+        self.flushed = self._settled = False
 
     def verify_tree(self, q, k, v, raw_g, raw_beta, parents, node_corr, out, *, Q,
                     query_start_loc=None):
@@ -155,7 +160,9 @@ class DeferredRecoverSSM:
         out BF16 [T, H, 128], raw_beta BF16 [T, H], parents int32 [T]; T =
         B*Q, or packed by query_start_loc [B + 1]), every node from the state
         behind its ancestors.  node_corr FP32 [T, H, 128] takes the nodes'
-        corrections, for ``accept_tree``; the records are not written."""
+        corrections, for ``accept_tree``; the records are not written.  A
+        request that is reported (a bad tree or window) keeps its pending
+        replay, ``accept_tree`` included."""
         replay = {} if self.flushed else dict(pending=self.pending, corr=self.corr,
                                               key_gate=self.key_gate)
         kda_tree_verify(q, k, v, raw_g, raw_beta, self.A_log, self.dt_bias, self.state_pool,
@@ -163,18 +170,32 @@ class DeferredRecoverSSM:
                         lower_bound=self.lower_bound, q_scale=self.q_scale,
                         record_rows=self.record_rows, query_start_loc=query_start_loc,
                         null_slot=self.null_slot, status=self.status, stream=self.stream, **replay)
+        if not self.flushed:
+            self._settle(q.shape[0], parents=parents, Q=Q, query_start_loc=query_start_loc)
+            self._settled = True
+
+    def _settle(self, n_tokens, **kw):
+        """The record rows of the requests that go on, to self._rows."""
+        kda_tree_settle(self.state_slots, self.record_rows, self._rows, n_tokens=n_tokens,
+                        n_slots=self.state_pool.shape[0], n_rows=self.corr.shape[0],
+                        null_slot=self.null_slot, status=self.status, stream=self.stream, **kw)
 
     def accept_tree(self, path, accepted, k, raw_g, node_corr, *, Q, query_start_loc=None, x=None,
                     conv_state=None, eager=None):
-        """After sampling from a tree: the accepted paths (path int32 [B, 8],
-        accepted int32 [B], overwritten as in ``accept``) move to the front
-        of the records, and with x and conv_state their inputs to the layer's
-        convolution windows; then as ``accept``."""
-        kda_tree_select(path, accepted, k, raw_g, node_corr, self.state_slots, self.record_rows,
+        """After sampling from the trees of ``verify_tree``: the accepted paths
+        (path int32 [B, 8], accepted int32 [B], overwritten as in ``accept``)
+        move to the front of the records, and with x and conv_state their
+        inputs to the layer's convolution windows; then as ``accept``.  A
+        request that ``verify_tree`` reported comes out as it went in."""
+        # (behind a flush every replay is in its checkpoint, whatever the trees were)
+        self._settle(k.shape[0], accepted=accepted, folded=self.flushed,
+                     served=self._rows if self._settled else None, Q=Q,
+                     query_start_loc=query_start_loc)
+        kda_tree_select(path, accepted, k, raw_g, node_corr, self.state_slots, self._rows,
                         self.corr, self.key_gate, Q=Q, x=x, conv_state=conv_state,
                         pending=self.pending, eager=eager, query_start_loc=query_start_loc,
                         null_slot=self.null_slot, status=self.status, stream=self.stream)
-        self.accept(accepted, eager)
+        self._accept(accepted, self._rows, eager)
 
     def flush(self):
         """Fold every pending replay into its checkpoint, in place."""
