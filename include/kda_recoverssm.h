@@ -792,18 +792,23 @@ int kda_draft_accept(const void *target, const void *draft, int probs_dtype,
  *     window and pending count alone; with folded != 0 (its replay was folded in
  *     otherwise, by kda_flush_plan and kda_commit) rows[b] = row all the same, a
  *     bad slot or row excepted: nothing of the step is accepted;
- *   any other: rows[b] = row.
- *   accepted [B] int32, read and written, or NULL; served [B] int32 or NULL: the
+ *   any other: rows[b] = row, and where path is given and the count lies outside
+ *     0 .. most or one of the path's nodes outside the window (kda_tree_select
+ *     would leave the request alone, and defer have stale records replayed):
+ *     reported, accepted[b] = 0.  The replay was folded in, the path is not taken.
+ *   accepted [B] int32, read and written, or NULL, path then too; path [B,
+ *   KDA_TREE_MAX_DEPTH] int32 or NULL; most: the longest path that records (rq)
+ *   and windows (conv_width - 2) hold, 0 .. KDA_TREE_MAX_DEPTH; served [B] int32 or NULL: the
  *   rows that an earlier call of the same step made, beside kda_tree_verify and
  *   with its parents; rows [B] int32, may be served or record_rows itself;
  *   parents NULL: no tree is looked at, and windows may hold up to
  *   KDA_TREE_MAX_NODES tokens; n_slots of the state pool, n_rows of the records.
  */
-int kda_tree_settle(int32_t *accepted, const int32_t *state_slots, int n_slots,
-                    const int32_t *record_rows, const int32_t *served, int n_rows,
-                    const int32_t *parents, const int32_t *query_start_loc, int n_tokens,
-                    int folded, int32_t *rows, int B, int Q, int null_slot, int32_t *status,
-                    void *stream);
+int kda_tree_settle(const int32_t *path, int32_t *accepted, int most,
+                    const int32_t *state_slots, int n_slots, const int32_t *record_rows,
+                    const int32_t *served, int n_rows, const int32_t *parents,
+                    const int32_t *query_start_loc, int n_tokens, int folded, int32_t *rows, int B,
+                    int Q, int null_slot, int32_t *status, void *stream);
 
 /*
  * kda_tree_select -- the accepted path's nodes to the front of the request's

@@ -86,7 +86,7 @@ _SIGS = {
                                     _I64, _I64, _I, _I, _P, _P] + [_I, _I, _I, _I, _P, _P], _I),
     "kda_draft_accept": ([_P, _P, _I, _I64, _I64, _I] + [_P] * 6 + [_I, _P, _P, _P]
                          + [_I, _I, _I, _P, _P], _I),
-    "kda_tree_settle": ([_P, _P, _I, _P, _P, _I, _P, _P, _I, _I, _P] + [_I, _I, _I, _P, _P], _I),
+    "kda_tree_settle": ([_P, _P, _I, _P, _I, _P, _P, _I, _P, _P, _I, _I, _P] + [_I, _I, _I, _P, _P], _I),
     "kda_tree_select": ([_P] * 11 + [_I64, _I64, _I, _I, _P, _P, _I64, _I, _I, _P, _I]
                         + [_I, _I, _I, _I, _P, _P], _I),
 }
@@ -805,14 +805,17 @@ def kda_draft_accept(target_probs, tokens, accept_uniforms, sample_uniforms, acc
     return _check("kda_draft_accept", rc, raise_on_error)
 
 
-def kda_tree_settle(state_slots, record_rows, rows, *, Q, n_tokens, n_slots, n_rows, accepted=None,
-                    parents=None, served=None, query_start_loc=None, folded=False, null_slot=0,
-                    status=None, stream=None, raise_on_error=True):
+def kda_tree_settle(state_slots, record_rows, rows, *, Q, n_tokens, n_slots, n_rows, path=None,
+                    accepted=None, most=KDA_TREE_MAX_DEPTH, parents=None, served=None,
+                    query_start_loc=None, folded=False, null_slot=0, status=None, stream=None,
+                    raise_on_error=True):
     """Between kda_draft_accept and kda_tree_select: record_rows [B] to ``rows``
     [B] (int32; they may be one), -1 for the requests that kda_tree_verify
     reported, whose replays are still pending (bad windows, slots, rows and,
     with ``parents`` [n_tokens], trees), and 0 to their ``accepted``.  Select and
-    kda_defer_commit, called with ``rows``, leave those as they were.
+    kda_defer_commit, called with ``rows``, leave those as they were.  With
+    ``path`` [B, 8], 0 too to the counts above ``most`` (what records, rq, and
+    windows, width - 2, hold) and to those of paths outside their windows.
     ``served``: the rows of an earlier call of the same step, beside the verify
     (``parents`` are not needed then).  ``folded``: the replays were folded in
     otherwise, and such a request keeps its row.  n_slots, n_rows: of the state
@@ -823,13 +826,15 @@ def kda_tree_settle(state_slots, record_rows, rows, *, Q, n_tokens, n_slots, n_r
     _expect_tensors(dev, ("state_slots", state_slots, i32, per),
                     ("record_rows", record_rows, i32, per), ("rows", rows, i32, per),
                     ("served", served, i32, per), ("accepted", accepted, i32, per),
+                    ("path", path, i32, (B, KDA_TREE_MAX_DEPTH)),
                     ("parents", parents, i32, (n_tokens,)),
                     ("query_start_loc", query_start_loc, i32, (B + 1,)),
                     ("status", status, i32, (1,)))
     rc = _call_on(dev, stream, lambda st: load().kda_tree_settle(
-            _address(accepted), state_slots.data_ptr(), n_slots, _address(record_rows),
-            _address(served), n_rows, _address(parents), _address(query_start_loc), n_tokens,
-            int(folded), rows.data_ptr(), B, Q, null_slot, _address(status), st))
+            _address(path), _address(accepted), most, state_slots.data_ptr(), n_slots,
+            _address(record_rows), _address(served), n_rows, _address(parents),
+            _address(query_start_loc), n_tokens, int(folded), rows.data_ptr(), B, Q, null_slot,
+            _address(status), st))
     return _check("kda_tree_settle", rc, raise_on_error)
 
 

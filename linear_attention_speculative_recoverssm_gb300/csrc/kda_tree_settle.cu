@@ -5,7 +5,9 @@
 // pending.  A pending count of zero behind such a step would lose the tokens
 // accepted before it, so those requests get no record row here, and what
 // follows passes them by.  Where the replays were folded in otherwise (a flush),
-// such a request keeps its row, and nothing of the step is accepted.
+// such a request keeps its row, and nothing of the step is accepted.  Nor is
+// anything of a path that records or windows cannot hold: its count as the
+// pending one would replay what an earlier step left in the records.
 //
 // A warp a request, integer work only: two or three loads that depend on one
 // another, and a walk up the tree in shared memory.
@@ -21,8 +23,9 @@ constexpr int kTlWarps = 8;
 
 struct TreeSettleParams {
   TreeMaps maps;
-  const int32_t *served;
+  const int32_t *served, *path;
   int32_t *accepted, *rows;
+  int most;  // the longest path that fits
   bool folded;
 };
 
@@ -42,9 +45,16 @@ __global__ void __launch_bounds__(32 * kTlWarps) kda_tree_settle_kernel(const Tr
     ok = !left && r.error == KDA_OK &&
          (mp.parents == nullptr || load_tree(mp, r, parents[warp], lane));
     if (!ok) {
-      count = 0;
       if (left || !p.folded || slot >= mp.n_slots || row >= mp.n_rows) to = -1;
+    } else if (p.path != nullptr) {
+      bool fits = count >= 0 && count <= p.most;
+      if (fits && lane < count) {
+        const int t = p.path[(long long)b * kTreeDepth + lane];
+        fits = t >= 0 && t < r.n;
+      }
+      ok = __all_sync(0xffffffffu, fits);
     }
+    if (!ok) count = 0;
   }
   __syncwarp();  // (`rows` may be `served` or record_rows: all lanes have read)
   if (lane != 0) return;
@@ -56,7 +66,8 @@ __global__ void __launch_bounds__(32 * kTlWarps) kda_tree_settle_kernel(const Tr
 }  // namespace
 }  // namespace kda
 
-extern "C" int kda_tree_settle(int32_t *accepted, const int32_t *state_slots, int n_slots,
+extern "C" int kda_tree_settle(const int32_t *path, int32_t *accepted, int most,
+                               const int32_t *state_slots, int n_slots,
                                const int32_t *record_rows, const int32_t *served, int n_rows,
                                const int32_t *parents, const int32_t *query_start_loc,
                                int n_tokens, int folded, int32_t *rows, int B, int Q,
@@ -68,6 +79,10 @@ extern "C" int kda_tree_settle(int32_t *accepted, const int32_t *state_slots, in
   if (B == 0) return KDA_OK;
   if (!state_slots || !rows || n_slots < 1 || n_rows < 1 || (record_rows == nullptr && n_rows < B))
     return KDA_ERR_ARG;
+  if (path != nullptr && (accepted == nullptr || most < 0 || most > KDA_TREE_MAX_DEPTH))
+    return KDA_ERR_ARG;
+  p.path = path;
+  p.most = most;
   p.served = served;
   p.accepted = accepted;
   p.rows = rows;

@@ -186,9 +186,13 @@ class DeferredRecoverSSM:
         (path int32 [B, 8], accepted int32 [B], overwritten as in ``accept``)
         move to the front of the records, and with x and conv_state their
         inputs to the layer's convolution windows; then as ``accept``.  A
-        request that ``verify_tree`` reported comes out as it went in."""
+        request that ``verify_tree`` reported comes out as it went in; a path
+        that the records or windows cannot hold is reported and not taken."""
+        most = self.corr.shape[2]
+        if conv_state is not None:
+            most = max(0, min(most, conv_state.shape[2] - 2))
         # (behind a flush every replay is in its checkpoint, whatever the trees were)
-        self._settle(k.shape[0], accepted=accepted, folded=self.flushed,
+        self._settle(k.shape[0], path=path, accepted=accepted, most=most, folded=self.flushed,
                      served=self._rows if self._settled else None, Q=Q,
                      query_start_loc=query_start_loc)
         kda_tree_select(path, accepted, k, raw_g, node_corr, self.state_slots, self._rows,

@@ -133,7 +133,7 @@ LEFT = ("state", "conv", "pending", "corr", "kg", "out", "node_corr")
 def two_arms(spoil, instead, trees, *, rq=8, width=10, flushed=False, eager=None, windows=True, arm=Arm):
     """A good step, the spoilt one (`instead` in the other arm), a good one and
     a flush; the state of the spoilt arm's middle step."""
-    good = [tt.comb(7), tt.chain(3), tt.star(6), tt.chain(4)]
+    good = [tt.comb(7) if min(rq, width - 2) == 8 else tt.star(7), tt.chain(3), tt.star(6), tt.chain(4)]
     arms = [arm(rq, width), arm(rq, width)]
     first = [a.step(1, good, windows=windows) for a in arms]
     same(*first, LEFT)
@@ -182,6 +182,30 @@ def test_what_the_acceptance_alone_reports_is_as_empty(flushed):
     two_arms("token", "empty", LARGE, flushed=flushed)
 
 
+DEEP = [tt.star(11), tt.star(5), tt.chain(3), tt.chain(8)]
+FLAT = [tt.star(6), tt.star(5), tt.chain(3), tt.chain(5)]
+
+
+@pytest.mark.parametrize("flushed,eager", [(False, None), (False, [0, 1, 0, 1]), (True, None)])
+@pytest.mark.parametrize("trees,spoil,rq,width,windows", [
+    (DEEP, "count", 4, 6, True),    # a path of eight tokens, records of four
+    (FLAT, "count", 4, 6, True),
+    (DEEP, "count", 8, 6, True),    # windows of four
+    (DEEP, "count", 4, 10, True),
+    (DEEP, "count", 4, 10, False),  # records alone
+    (LARGE, "path", 8, 10, True),   # a node outside the window
+    (LARGE, "negative", 8, 10, True),
+])
+def test_a_path_that_does_not_fit(trees, spoil, rq, width, windows, flushed, eager):
+    """The replay before it was folded in, and nothing else is: no record of an
+    earlier step is replayed in its place."""
+    left = two_arms(spoil, "empty", trees, rq=rq, width=width, windows=windows, flushed=flushed,
+                    eager=eager)
+    assert int(left["accepted"][-1]) == 0
+    if spoil == "count":
+        assert int(left["count"][-1]) == len(trees[-1])
+
+
 class Calls(Arm):
     """The same step by the library's calls."""
 
@@ -204,7 +228,8 @@ class Calls(Arm):
         d, status = self.d, dict(status=self.d["status"])
         rows, plan = torch.empty_like(d["rows"]), accepted.clone()
         window = {n: common[n] for n in ("Q", "query_start_loc")}
-        kda_tree_settle(d["slots"], d["rows"], rows, accepted=accepted, parents=par,
+        most = min(d["corr"].shape[2], d["conv"].shape[2] - 2)
+        kda_tree_settle(d["slots"], d["rows"], rows, path=path, accepted=accepted, most=most, parents=par,
                         n_tokens=len(par), n_slots=len(d["state"]), n_rows=len(d["corr"]), **window,
                         **status)
         kda_tree_select(path, accepted, k, g, node_corr, d["slots"], rows, d["corr"], d["kg"],
@@ -213,8 +238,9 @@ class Calls(Arm):
         kda_defer_commit(d["slots"], plan, rows, d["pending"], **status)
 
 
-@pytest.mark.parametrize("spoil,instead", [("tree", "inert"), ("window", "inert"), ("slot", "inert"),
-                                           ("token", "empty")])
-def test_by_the_calls(spoil, instead):
-    left = two_arms(spoil, instead, LARGE, arm=Calls)
+@pytest.mark.parametrize("spoil,instead,trees,rq", [
+    ("tree", "inert", LARGE, 8), ("window", "inert", LARGE, 8), ("slot", "inert", LARGE, 8),
+    ("token", "empty", LARGE, 8), ("path", "empty", LARGE, 8), ("count", "empty", DEEP, 4)])
+def test_by_the_calls(spoil, instead, trees, rq):
+    left = two_arms(spoil, instead, trees, rq=rq, arm=Calls)
     assert int(left["accepted"][-1]) == 0

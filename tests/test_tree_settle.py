@@ -20,7 +20,7 @@ OK, ARG = _lib.KDA_OK, _lib.KDA_ERR_ARG
 
 
 def _settle(lib, **over):
-    a = dict(accepted=A, slots=A, n_slots=4, rows=A, served=A, n_rows=3, parents=A, qsl=A, T=10,
+    a = dict(path=A, accepted=A, most=8, slots=A, n_slots=4, rows=A, served=A, n_rows=3, parents=A, qsl=A, T=10,
              folded=0, to=A, B=2, Q=8, null=0, status=None, stream=None)
     return lib.kda_tree_settle(*{**a, **over}.values())
 
@@ -29,6 +29,7 @@ def _settle(lib, **over):
     (dict(B=-1), ARG), (dict(Q=0), ARG), (dict(Q=65), ARG), (dict(T=-1), ARG), (dict(null=-2), ARG),
     (dict(qsl=None), ARG), (dict(slots=None), ARG), (dict(to=None), ARG), (dict(n_slots=0), ARG),
     (dict(n_rows=0), ARG), (dict(rows=None, n_rows=1), ARG), (dict(B=0, slots=None), OK),
+    (dict(accepted=None), ARG), (dict(most=-1), ARG), (dict(most=9), ARG),
 ])
 def test_refusals(lib, over, code):
     assert _settle(lib, **over) == code
@@ -41,19 +42,19 @@ def test_binding_refusals(lib):
 
     def settle(**o):
         a = dict(state_slots=i32(2), record_rows=i32(2), rows=i32(2), Q=3, n_tokens=6, n_slots=4,
-                 n_rows=3, accepted=i32(2), parents=i32(6), served=i32(2), query_start_loc=i32(3))
+                 n_rows=3, accepted=i32(2), path=i32(2, 8), parents=i32(6), served=i32(2), query_start_loc=i32(3))
         return kda_tree_settle(**{**a, **o})
 
     for bad in (dict(rows=i32(2).long()), dict(accepted=torch.zeros(2)), dict(parents=i32(6).long())):
         with pytest.raises(TypeError):
             settle(**bad)
-    for bad in (dict(rows=i32(3)), dict(served=i32(1)), dict(parents=i32(5)),
+    for bad in (dict(rows=i32(3)), dict(served=i32(1)), dict(parents=i32(5)), dict(path=i32(2, 7)),
                 dict(query_start_loc=i32(2)), dict(record_rows=i32(4)[::2]), dict()):
         with pytest.raises(ValueError):
             settle(**bad)
 
 
-def rules(case, *, folded=False, trees=True):
+def rules(case, *, folded=False, trees=True, most=8):
     """(rows, accepted, whether one is reported) as the header has it."""
     T, n_slots, n_rows = len(case["q"]), len(case["state"]), len(case["corr"])
     to_rows, counts, bad = case["record_rows"].copy(), case["accepted"].copy(), 0
@@ -69,6 +70,10 @@ def rules(case, *, folded=False, trees=True):
             bad, counts[b] = bad + 1, 0
             if left or not folded or not here:
                 to_rows[b] = -1
+        elif case["path"] is not None and \
+                (not 0 <= counts[b] <= most or
+                 any(not 0 <= t < wins[b][1] for t in case["path"][b, :counts[b]])):
+            bad, counts[b] = bad + 1, 0
     return to_rows, counts, bad
 
 
@@ -81,7 +86,9 @@ def settle_case(B, seed, cap=12):
     case = tt.tree_case(trees, 1, seed=seed, inert=set(rng.permutation(B)[:B // 8]),
                         rowless=set(rng.permutation(B)[:B // 8]))
     case.update(accepted=rng.integers(-2, 9, B).astype(np.int32), served=case["record_rows"].copy(),
-                Q=cap)
+                path=rng.integers(0, np.maximum(sizes, 1)[:, None], (B, 8)).astype(np.int32), Q=cap)
+    spoilt = rng.random((B, 8)) < 0.05
+    case["path"][spoilt] = rng.choice([-1, cap, 1 << 30, -1 << 31], spoilt.sum())
     start = case["query_start_loc"]
     kinds = rng.integers(0, 12, B)
     for b in np.flatnonzero(sizes > 1):
@@ -101,11 +108,11 @@ def settle_case(B, seed, cap=12):
 def run(case, **kw):
     import torch
     from linear_attention_speculative_recoverssm_gb300 import kda_tree_settle
-    d = tt.on_device(case, ("state_slots", "record_rows", "accepted", "parents", "served",
+    d = tt.on_device(case, ("state_slots", "path", "record_rows", "accepted", "parents", "served",
                             "query_start_loc"))
     rows = torch.full_like(d["state_slots"], 99)
     a = dict(rows=rows, Q=case["Q"], n_tokens=len(case["q"]), n_slots=len(case["state"]),
-             n_rows=len(case["corr"]), accepted=d["accepted"], parents=d["parents"],
+             n_rows=len(case["corr"]), accepted=d["accepted"], path=d["path"], parents=d["parents"],
              served=d["served"], query_start_loc=d["query_start_loc"], null_slot=case["null_slot"],
              status=d["status"])
     a.update({n: d[v] if isinstance(v, str) else v for n, v in kw.items()})
@@ -132,8 +139,11 @@ def test_settle(lib, B, cap, served, folded):
         case["served"] = None
     d, rows = run(case, folded=folded)
     check(case, d, rows, folded=folded)
-    d, rows = run(case, folded=folded, parents=None)  # (no tree is looked at)
-    check(case, d, rows, folded=folded, trees=False)
+    d, rows = run(case, folded=folded, parents=None, most=3)  # (no tree is looked at)
+    check(case, d, rows, folded=folded, trees=False, most=3)
+    d, rows = run(case, path=None)
+    case["path"] = None
+    check(case, d, rows)
 
 
 @pytest.mark.gpu
@@ -144,6 +154,6 @@ def test_rows_over_the_rows(lib):
     for to_where in ("served", "record_rows"):
         d, rows = run(case, rows=to_where)
         check(case, d, rows)
-    d, rows = run(case, accepted=None)
+    d, rows = run(case, accepted=None, path=None)
     np.testing.assert_array_equal(tt.to_numpy(rows), rules(case)[0])
     np.testing.assert_array_equal(tt.to_numpy(d["accepted"]), case["accepted"])
