@@ -828,7 +828,9 @@ int kda_tree_settle(const int32_t *path, int32_t *accepted, int most,
  * the path the next replay.  Requests that are inert or without a record row
  * are left alone.  A count outside 0 .. rq (with conv_state, conv_width - 2)
  * or a path entry outside the window is reported (KDA_ERR_ARG) and its
- * request left alone.
+ * request left alone.  With m = 0 a bad window of tokens is reported too, but
+ * the convolution's moves: kda_tree_settle passes such a request on only where
+ * its replay is in the state.
  *   path [B, KDA_TREE_MAX_DEPTH], accepted [B] int32; k, raw_g BF16 and
  *   node_corr FP32 [n_tokens, H, 128] as kda_tree_verify took and left them;
  *   corr, key_gate, their strides, n_rows and rq as there; x, conv_state,

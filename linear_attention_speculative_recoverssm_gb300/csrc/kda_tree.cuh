@@ -29,7 +29,9 @@ struct TreeRequest {
   int error;  // KDA_OK or what to report
 };
 
-__device__ __forceinline__ TreeRequest tree_request(const TreeMaps &p, int b) {
+// A bad window ends it, or where none is needed is an empty one, error set.
+__device__ __forceinline__ TreeRequest tree_request(const TreeMaps &p, int b,
+                                                    bool needs_window = true) {
   TreeRequest r;
   r.error = KDA_OK;
   r.slot = r.row = -1;
@@ -41,9 +43,10 @@ __device__ __forceinline__ TreeRequest tree_request(const TreeMaps &p, int b) {
     if (r.t0 < 0 || n < 0 || n > p.Q || end > p.n_tokens) {
       r.error = KDA_ERR_ARG;
       r.t0 = r.n = 0;
-      return r;
+      if (needs_window) return r;
+    } else {
+      r.n = (int)n;
     }
-    r.n = (int)n;
   } else {
     r.t0 = b * p.Q;
     r.n = p.Q;

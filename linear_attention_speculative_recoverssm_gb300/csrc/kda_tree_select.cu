@@ -45,10 +45,12 @@ __global__ void __launch_bounds__(kTsThreads, 5) kda_tree_select_kernel(const Tr
   __shared__ __align__(16) uint16_t rows[kTsChannels * kTsMaxWidth];
   const TreeMaps &mp = p.maps;
   const int b = blockIdx.x, lane = threadIdx.x & 31;
-  const TreeRequest r = tree_request(mp, b);
   const int m = p.accepted[b];
+  // (behind nothing accepted the convolution's window moves without any token)
+  const TreeRequest r = tree_request(mp, b, m != 0);
   const int32_t *path = p.path + (long long)b * kTreeDepth;
   bool ok = r.error == KDA_OK;
+  const bool moves = !ok && m == 0 && r.slot >= 0;
   if (ok && r.slot >= 0 && r.row >= 0) {
     ok = m >= 0 && m <= p.most;
     const int4 lo = reinterpret_cast<const int4 *>(path)[0],
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(kTsThreads, 5) kda_tree_select_kernel(const Tr
     for (int i = 0; i < kTreeDepth; ++i) ok = ok && (i >= m || (nodes[i] >= 0 && nodes[i] < r.n));
   }
   if (!ok && blockIdx.y == 0 && threadIdx.x == 0) report(mp.status, KDA_ERR_ARG);
-  if (!ok || r.slot < 0 || r.row < 0) return;
+  if (!(ok || moves) || r.slot < 0 || r.row < 0) return;
   if ((int)blockIdx.y < p.record_ctas) {
     const int h = blockIdx.y * kTsHeads + (threadIdx.x >> 5);
     if (h >= p.H) return;

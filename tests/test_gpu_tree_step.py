@@ -169,7 +169,8 @@ def test_what_verify_reports_stays_pending(trees, spoil, eager):
     assert int(left["accepted"][-1]) == 0
 
 
-@pytest.mark.parametrize("trees,spoil", [(LARGE, "tree"), (SMALL, "tree"), (LARGE, "deep")])
+@pytest.mark.parametrize("trees,spoil", [(LARGE, "tree"), (SMALL, "tree"), (LARGE, "deep"),
+                                         (LARGE, "window"), (SMALL, "window")])
 def test_behind_a_flush_nothing_is_pending(trees, spoil):
     """The replay was folded in by the flush: it must not be folded in twice."""
     two_arms(spoil, "empty", trees, flushed=True)
@@ -244,3 +245,29 @@ class Calls(Arm):
 def test_by_the_calls(spoil, instead, trees, rq):
     left = two_arms(spoil, instead, trees, rq=rq, arm=Calls)
     assert int(left["accepted"][-1]) == 0
+
+
+def test_select_moves_the_window_of_a_bad_one():
+    """Nothing accepted and a bad window of tokens: reported, the convolution's
+    window moved; a bad slot or row, or a count above zero: left alone."""
+    import test_gpu_tree as tg
+    case = tg.select_case([tt.chain(4)] * 6, 2, 60)
+    case["accepted"][:] = [0, 2, 0, 0, 0, 1]
+    case["query_start_loc"] = np.array([0, 70, 4, 8, 12, 16, 20], np.int32)  # 0 and 1 are bad
+    case["state_slots"][2], case["record_rows"][3] = len(case["conv_state"]), len(case["corr"])
+    case["state_slots"][4] = 0
+    d = tg.run_select(case)
+    assert tt.to_numpy(d["status"])[0] == _lib.KDA_ERR_ARG
+    want, slot = case["conv_state"].copy(), case["state_slots"][0]
+    n = max(0, int(case["pending"][case["record_rows"][0]]))
+    off = n - 1 if n > 0 else 0
+    want[slot, :, :3] = case["conv_state"][slot, :, off:off + 3]
+    slot, row, t = case["state_slots"][5], case["record_rows"][5], 16 + case["path"][5, 0]
+    n = max(0, int(case["pending"][row]))
+    off = n - 1 if n > 0 else 0
+    want[slot, :, :2] = case["conv_state"][slot, :, off + 1:off + 3]
+    want[slot, :, 2] = case["x"][t]
+    corr = case["corr"].copy()
+    corr[row, :, 0] = case["node_corr"][t]
+    np.testing.assert_array_equal(tt.to_numpy(d["conv_state"]), want)
+    np.testing.assert_array_equal(tt.to_numpy(d["corr"]), corr)
