@@ -83,7 +83,7 @@ extern "C" {
 #define KDA_MAX_WINDOW 8
 #define KDA_MAX_LAYERS 64
 #define KDA_PROMPT_MAX_HEADS 1024 /* heads of the prompt operators */
-#define KDA_PLAN_MAX_REQUESTS (1 << 24) /* requests of one kda_slot_plan */
+#define KDA_PLAN_MAX_REQUESTS (1 << 24) /* requests of one kda_slot_plan or (Q > 4) kda_tree_verify */
 #define KDA_TREE_MAX_NODES 64 /* drafted tokens of one request's tree, its root among them */
 #define KDA_TREE_MAX_DEPTH KDA_MAX_WINDOW /* tokens of a path: what a record row holds */
 #define KDA_MAX_VOCAB (1 << 20) /* tokens of kda_draft_accept's vocabulary */
@@ -722,6 +722,7 @@ int kda_tree_conv(const kda_bf16 *x, const kda_bf16 *conv_weight, const kda_bf16
  *   1 <= rq <= 8.  pending, corr and key_gate may be NULL together: no replay,
  *   and the pool is only read.  A BF16 pool takes no replay (fold it in with
  *   kda_commit): KDA_ERR_UNSUPPORTED.  -10 <= lower_bound <= 10.
+ *   Q > 4: B <= KDA_PLAN_MAX_REQUESTS.
  * All pointers but raw_beta, A_log and the index arrays 16-byte aligned.
  */
 int kda_tree_verify(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v,

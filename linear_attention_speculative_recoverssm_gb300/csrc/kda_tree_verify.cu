@@ -25,6 +25,7 @@ constexpr int kTrThreads = 256;
 constexpr int kTrWarps = kTrThreads / 32;
 constexpr int kTrNodes = 8;  // room for windows of up to kTrMaxQ nodes
 constexpr int kTrMaxQ = 6;
+constexpr int kTrFewNodes = 4;  // windows that go by FMA however many items there are
 
 // Shared memory of a CTA whose windows hold up to `nodes` (a multiple of 4)
 // nodes, in floats: X, [2 nodes][128]; kn and d, [nodes][128] each, whose
@@ -243,6 +244,10 @@ extern "C" int kda_tree_verify(
   const bool bf16 = state_dtype == KDA_STATE_BF16;
   if (replay && bf16) return KDA_ERR_UNSUPPORTED;
   if (replay && (rq < 1 || rq > KDA_MAX_WINDOW)) return KDA_ERR_ARG;
+  // One warp of each of the tensor cores' CTAs looks through its requests, 0.6 us
+  // for each without nodes (2^24: 70 ms), while the others' waits run towards their
+  // limit of 2 s.
+  if (Q > kda::kTrFewNodes && B > KDA_PLAN_MAX_REQUESTS) return KDA_ERR_ARG;
   if (B == 0 || (n_tokens == 0 && !replay)) return KDA_OK;
   if (!A_log || !dt_bias || !state_pool || !state_slots || n_slots < 1) return KDA_ERR_ARG;
   if (n_tokens > 0 && (!q || !k || !v || !raw_g || !raw_beta || !node_corr || !out))
@@ -287,7 +292,7 @@ extern "C" int kda_tree_verify(
   // 15, 192 items 25 / 19 and 25, 1536 items 130 / 74 and 74; 6 nodes, 32 items 15
   // and 17, 192 items 21 and 25, 512 items 37 and 37, 1536 items 87 and 74; 8 nodes,
   // 1536 items 95 and 75; 15 nodes, 32 items 23 / 25 and 17.
-  if (Q > kda::kTrMaxQ || (Q > 4 && (long long)B * H > 4LL * sms))
+  if (Q > kda::kTrMaxQ || (Q > kda::kTrFewNodes && (long long)B * H > 4LL * sms))
     return kda::launch_tree_mma(p, bf16, sms, st);
   if ((long long)B * H * 4 <= sms)
     return bf16 ? kda::launch_rows<32, true>(p, st) : kda::launch_rows<32, false>(p, st);
