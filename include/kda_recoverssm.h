@@ -739,8 +739,8 @@ int kda_tree_verify(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v,
 /*
  * kda_draft_accept -- drafted tokens against the target's probabilities, from
  * given random numbers; lossless: the tokens follow the target's
- * distribution.  p_t = target[t], the target's next-token weights after node
- * t; x_t = tokens[t].  Per request, from node a = 0, its last sampled token:
+ * distribution.  p_t = target[t], the target's next-token probabilities after
+ * node t; x_t = tokens[t].  Per request, from node a = 0, its last sampled token:
  *   with draft probabilities (chains; draft[t] = q_t, what x_t was drawn
  *   from): the child t = a + 1 is accepted iff u_a q_t(x_t) < p_a(x_t);
  *   without (drafts taken for sure: trees of likely tokens, or a chain): of
@@ -764,6 +764,11 @@ int kda_tree_verify(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v,
  *   draft weight that is NaN refuses its token, which then has no weight in
  *   the draw; draft weights are not negative.
  *   Uniforms lie in [0, 1).
+ *   Rows of target and draft sum to one, which is not checked: a child is
+ *   accepted by its probability as it stands, while the draw goes by the
+ *   weights' total, so that behind rows of another sum the tokens follow
+ *   neither.  Their distribution is off (in total variation) by what the two
+ *   rows' sums are off by, 2^-8 each at most from rounding to BF16.
  *   Comparisons and sums run at 48 bits or more, so that a token does not
  *   depend on the order of a sum.
  *   target [n_tokens, vocab] and draft (NULL, or the same, with parents NULL)

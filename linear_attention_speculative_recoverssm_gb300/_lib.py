@@ -761,11 +761,11 @@ def kda_draft_accept(target_probs, tokens, accept_uniforms, sample_uniforms, acc
                      query_start_loc=None, null_slot=0, status=None, stream=None,
                      raise_on_error=True):
     """Drafted ``tokens`` [T] against the target's next-token probabilities
-    target_probs [T, vocab] (float32 or bfloat16, rows of any stride), from
-    uniform numbers accept_uniforms [T] (one a node, for its children) and
-    sample_uniforms [B] in [0, 1).  Chains with draft_probs [T, vocab] (what
-    each token was drawn from), or trees (``parents``) and chains of drafts
-    that were taken for sure.  Out, int32: accepted [B] (tokens of the path,
+    target_probs [T, vocab] (float32 or bfloat16, rows of any stride, each
+    summing to one), from uniform numbers accept_uniforms [T] (one a node, for
+    its children) and sample_uniforms [B] in [0, 1).  Chains with draft_probs
+    [T, vocab] (what each token was drawn from; rows as target_probs'), or
+    trees (``parents``) and chains of drafts that were taken for sure.  Out, int32: accepted [B] (tokens of the path,
     the root among them), path [B, 8] (its nodes, -1 behind), next_tokens [B]
     (drawn from the target after the path).  The rules are in
     include/kda_recoverssm.h."""
