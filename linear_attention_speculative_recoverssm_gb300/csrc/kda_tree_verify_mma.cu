@@ -239,7 +239,7 @@ struct TreeMma {
   static constexpr int kThreads = 32 * kWarps;
   // tensor memory: the page, w and y (twice where there is room), P, R (as often)
   static constexpr int kDBufs = NC <= 32 ? 2 : 1;
-  // P: by part of Y, where there is room
+  // P: by the size of the parts' products, where there is room
   static constexpr int kPParts = NC <= 32 ? 3 : 1;
   static constexpr uint32_t kTmP = kTmD + kDBufs * 2 * NC, kTmR = kTmP + kPParts * NC;
   static_assert(kTmR + kDBufs * 3 * NC / 2 <= 512, "tensor memory");
@@ -937,16 +937,19 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
         tc_fence_after();
         // (M = 128 rows: those behind X's are other operands', and P's rows of them
         // nobody reads.)  A product reads its 128 rows of X from shared memory
-        // whatever its N: where tensor memory has room for P by parts of Y, one takes
-        // all parts of Y that go with a part of X.
+        // whatever its N: where tensor memory has room, one takes all parts of Y that
+        // go with part e of X, those with part j to P's (e + j)-th.  Products of one
+        // size are summed there, so that the small ones' sums are not rounded as the
+        // large one's is (all on one, pairs of nodes were off by 51 2^-24).
 #pragma unroll 1
         for (uint32_t e = 0; e < (L::kPParts == 1 ? 6 : 3); ++e) {
           const uint32_t x = x0 + (L::kPParts == 1 ? (kA6 >> 2 * e & 3) : e) * L::kXPart;
           const uint32_t y = y0 + (L::kPParts == 1 ? (kB6 >> 2 * e & 3) * L::kYPart : 0);
           const uint32_t columns = L::kPParts == 1 ? cols : (2 - e) * NC + cols;
+          const uint32_t p_at = tm + L::kTmP + (L::kPParts == 1 ? 0 : e * NC);
 #pragma unroll
           for (int ks = 0; ks < kDim / 16; ++ks)
-            tm_mma_ss(tm + L::kTmP, umma_desc_sw128(x + (ks >> 2) * L::kXBlock + (ks & 3) * 32),
+            tm_mma_ss(p_at, umma_desc_sw128(x + (ks >> 2) * L::kXBlock + (ks & 3) * 32),
                       umma_desc_sw128(y + (ks >> 2) * L::kYBlock + (ks & 3) * 32), tm_idesc(columns),
                       e > 0 || ks > 0, lead);
         }
