@@ -123,7 +123,6 @@ struct AcceptSmem {
   alignas(16) int8_t parent[kTreeNodes];
   int token[kTreeNodes];
   float p[kTreeNodes];
-  uint32_t first_of_token[2];  // nodes whose token no earlier sibling has
   int last, refused;           // the path's last node; the refused child of a chain or -1
   int n_removed;
   int removed[kTreeNodes];  // tokens of the refused children of a tree

@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(TreeMma<NC, BF16>::kThreads, 1)
     };
     bool more = settle(it.start(tasks, bars));
     while (more) {
-      const int n = it.n, cols = (n + 15) & ~15;
+      const int n = it.n;
       const float a = expf(__ldg(p.A_log + it.h));
       const uint16_t *const keys = raw(0), *const queries = raw(1);
       if constexpr (L::kRawBufs > 0) {
