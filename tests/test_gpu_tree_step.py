@@ -271,3 +271,101 @@ def test_select_moves_the_window_of_a_bad_one():
     corr[row, :, 0] = case["node_corr"][t]
     np.testing.assert_array_equal(tt.to_numpy(d["conv_state"]), want)
     np.testing.assert_array_equal(tt.to_numpy(d["corr"]), corr)
+
+
+def loop_over(d):
+    from linear_attention_speculative_recoverssm_gb300 import DeferredRecoverSSM
+    return DeferredRecoverSSM(d["state"], d["state_slots"], d["record_rows"], d["pending"], d["corr"],
+                              d["key_gate"], d["A_log"], d["dt_bias"], Q=8, lower_bound=-5.0,
+                              q_scale=128 ** -0.5, status=d["status"])
+
+
+PER_STEP = ("q", "k", "v", "raw_g", "raw_beta", "parents", "path", "accepted", "x")
+
+
+def one_step(loop, d, raw=False):
+    kw = dict(Q=12)
+    if raw:  # (the rule by the library's call)
+        tt.call_verify(dict(lower_bound=-5.0, q_scale=128 ** -0.5, null_slot=0, Q=12), d)
+    else:
+        loop.verify_tree(d["q"], d["k"], d["v"], d["raw_g"], d["raw_beta"], d["parents"],
+                         d["node_corr"], d["out"], **kw)
+    loop.accept_tree(d["path"], d["accepted"], d["k"], d["raw_g"], d["node_corr"], x=d["x"],
+                     conv_state=d["conv_state"], **kw)
+
+
+def captured_cases():
+    import test_gpu_tree as tg
+    cases = []
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        case = tg.select_case([tt.random_tree(rng, 12) for _ in range(5)], 2, 90 + seed, inert=(1,))
+        if seed % 2:  # (every other step; with a count that a caller made)
+            case["parents"][2 * 12 + 5] = 5
+            case["accepted"][3] = 9
+        case["query_start_loc"] = None
+        cases.append(case)
+    return cases
+
+
+@pytest.mark.parametrize("how", ["graph", "two graphs", "stream"])
+def test_a_captured_step_settles_its_own_requests(how):
+    """A step captured in one graph, or the rule and the acceptance in one each,
+    replayed with good and bad trees in turn, leaves what eager steps leave."""
+    import torch
+    cases = captured_cases()
+    arms = [tt.on_device(cases[0]) for _ in range(2)]
+    eager, other = (loop_over(d) for d in arms)
+    side = torch.cuda.Stream()
+    if how != "stream":
+        spare = tt.on_device(cases[0])
+        one_step(loop_over(spare), spare)  # (all that a first call loads)
+        torch.cuda.synchronize()
+        d, graphs = arms[1], [torch.cuda.CUDAGraph() for _ in range(2 if how == "two graphs" else 1)]
+        with torch.cuda.graph(graphs[0]):
+            if how == "graph":
+                one_step(other, d)
+            else:
+                other.verify_tree(d["q"], d["k"], d["v"], d["raw_g"], d["raw_beta"], d["parents"],
+                                  d["node_corr"], d["out"], Q=12)
+        if how == "two graphs":
+            with torch.cuda.graph(graphs[1]):
+                other.accept_tree(d["path"], d["accepted"], d["k"], d["raw_g"], d["node_corr"],
+                                  x=d["x"], conv_state=d["conv_state"], Q=12)
+    else:
+        other.stream = side
+    for n, case in enumerate(cases):
+        fresh = tt.on_device(case)
+        for d in arms:
+            for name in PER_STEP:
+                d[name].copy_(fresh[name])
+        one_step(eager, arms[0])
+        if how == "stream":
+            side.wait_stream(torch.cuda.current_stream())
+            one_step(other, arms[1])
+            torch.cuda.current_stream().wait_stream(side)
+        else:
+            for graph in graphs:
+                graph.replay()
+        torch.cuda.synchronize()
+        same(*arms, ("state", "corr", "key_gate", "pending", "conv_state", "accepted", "status"))
+        assert int(arms[0]["status"].item()) == (_lib.KDA_ERR_ARG if n % 2 else 0)
+        for d in arms:
+            d["status"].zero_()
+
+
+def test_accept_tree_beside_the_librarys_verify():
+    """Without verify_tree there is nothing that it reported: the paths that fit
+    are taken."""
+    import torch
+    case = captured_cases()[0]
+    arms = [tt.on_device(case) for _ in range(2)]
+    for raw, d in zip((False, True), arms):
+        one_step(loop_over(d), d, raw)
+    torch.cuda.synchronize()
+    same(*arms, ("state", "corr", "key_gate", "pending", "conv_state", "accepted", "status"))
+    taken = case["accepted"].copy()
+    taken[1] = 0
+    got = tt.to_numpy(arms[1]["pending"])
+    assert (got[case["record_rows"]] == np.where(case["state_slots"] > 0, taken,
+                                                 case["pending"][case["record_rows"]])).all()
