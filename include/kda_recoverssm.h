@@ -659,7 +659,9 @@ int kda_recurrent(const kda_bf16 *q, const kda_bf16 *k, const kda_bf16 *v, const
  *    operators that move states take any number of them, kda_draft_accept one
  *    alone, node 0, the last token that was sampled).  A path holds at most
  *    KDA_TREE_MAX_DEPTH tokens.  NULL: every request's nodes are a chain, and
- *    Q is at most that many.
+ *    Q is at most that many.  Where records or convolution windows hold fewer
+ *    tokens, a longer path can be verified and accepted but not kept
+ *    (kda_tree_settle): trees are then no deeper than those.
  *  - A request whose window is bad (see the top) or whose parents are not
  *    such a tree is reported as KDA_ERR_ARG in the status word, and nothing
  *    of it is read or written but what an operator below names.  Rows of the

@@ -13,8 +13,11 @@
 // What bounds it: HBM, for the rows (each read once, but for one tile); a
 // single request's half a dozen loads that depend on one another.  256 chains
 // with drafts, 131072 FP32 weights (268 MB): 58 us, 4.6 TB/s (a copy: 6.7), 44%
-// of the issue slots.  By events around the call 70 us, one request 17, 64 trees
-// of up to 24 nodes, 100003 BF16 weights, 25.
+// of the issue slots.  By events around the call 70 us behind a cache full of
+// written lines, which go back to memory meanwhile, 60 behind one of read lines, 59
+// a pass of eight; one request 17.  64 trees of up to 24 nodes, 100003 BF16 weights:
+// 25 us for 13 MB, which no unit's rate explains: seven rounds of tiles a CTA, each
+// with one tile (32 bytes a lane) on its way.
 //
 // Precision.  The answer is an index, which must not depend on the order of
 // the sums: a row's running sums lie 1e-5 apart and less, where FP32 sums

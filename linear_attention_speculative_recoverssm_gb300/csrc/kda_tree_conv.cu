@@ -4,15 +4,17 @@
 // s_3 the node's own input, s_2 .. s_0 those of its three nearest ancestors,
 // and of the request's window above a root.
 //
-// What bounds it: HBM, 4 bytes a node and channel (one input, one output) and
+// Its floor is HBM's, 4 bytes a node and channel (one input, one output) and
 // the windows' sectors once a request.  A CTA takes a request's nodes, or a
 // run of them, in 512 channels, four a thread.  All inputs are copied to shared
 // memory at once, asynchronously, and a node's four taps read there: window
 // entries and inputs alike, without a branch.
 //
 // 128 trees of up to 33 nodes, 64 heads (326 MB): 84 us, 3.9 TB/s (a copy: 6.7),
-// with 55% of the issue slots and 44% of shared memory's wavefronts; the rows
-// leave room for a third of an SM's warps.  By events around the call 89 us; by
+// with 55% of the issue slots and 44% of shared memory's wavefronts: no unit is
+// at its end.  Four channels of a node take 87 warp instructions, 32 of them
+// addresses and copies, loads and stores of 8 bytes, and the rows leave room for a
+// third of an SM's warps to cover their latencies.  By events around the call 89 us; by
 // loads four nodes ahead in place of the copies 109, two channels a thread 112;
 // loops unrolled further, or the first half of the nodes begun while the rest is
 // on its way, gain nothing.

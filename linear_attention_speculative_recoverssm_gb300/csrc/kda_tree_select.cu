@@ -4,15 +4,17 @@
 //   W <- [W[off + 1], W[off + 2], x[t_0] .. x[t_{m-1}]]
 // (an eager request's window: its last three inputs).
 //
-// What bounds it: HBM, and copies are all there is.  Record CTAs take a
+// Its floor is HBM's, and copies are all there is.  Record CTAs take a
 // request's heads, 8 at a time (a warp a head, 16 bytes a lane); window CTAs
 // take 1024 channels of a request: their window, one piece of memory, goes
 // through shared memory whole, where a thread rewrites the few entries of its
 // four channels, and comes back in 16-byte pieces.
 //
 // 256 requests, 64 heads (285 MB of what has to move, 323 with the entries that
-// are kept): 72 us, 4.0 TB/s (a copy: 6.7), the shared memory's path, where an
-// entry is 2 bytes, busy for 62%.  By events around the call 80 us, by one
+// are kept): 72 us, 4.0 TB/s (a copy: 6.7).  No unit is at its end: HBM is at 57%,
+// the shared memory's path, which windows take twice on their way through registers
+// and where an entry is 2 bytes, at 62%; a window's CTA reads, rewrites and writes it
+// one after the other.  By events around the call 80 us, by one
 // channel a thread 95.
 #include <cuda_runtime.h>
 

@@ -9,8 +9,10 @@
 // anything of a path that records or windows cannot hold: its count as the
 // pending one would replay what an earlier step left in the records.
 //
-// A warp a request, integer work only: two or three loads that depend on one
-// another, and a walk up the tree in shared memory.
+// A warp a request, integer work only.  What bounds it is latency: two or three
+// loads that depend on one another, and walks up the tree in shared memory.  One
+// request to 256 of 64 nodes take 6 us by events around the call, trees and paths
+// at once, or 4096 requests, 8; the launch and the events are some 5 of them.
 #include <cuda_runtime.h>
 
 #include "kda_launch.h"

@@ -291,7 +291,11 @@ extern "C" int kda_tree_verify(
   // of 32 / by whole pages) and on the tensor cores: 4 nodes, 32 items 13 / 15 and
   // 15, 192 items 25 / 19 and 25, 1536 items 130 / 74 and 74; 6 nodes, 32 items 15
   // and 17, 192 items 21 and 25, 512 items 37 and 37, 1536 items 87 and 74; 8 nodes,
-  // 1536 items 95 and 75; 15 nodes, 32 items 23 / 25 and 17.
+  // 1536 items 95 and 75; 15 nodes, 32 items 23 / 25 and 17.  Pages that are only
+  // read, FP32 (and BF16): 6 nodes, 512 items 29 and 27 (27 and 25), 1536 items 64 and
+  // 52 (61 and 45), 8192 items 289 and 199 (267 and 173); 4 nodes, 512 items 23 and 27
+  // (22 and 23), 1536 items 50 and 52 (47 and 44), 8192 items 212 and 199 (195 and
+  // 172; with a replay 328 and 314).
   if (Q > kda::kTrMaxQ || (Q > kda::kTrFewNodes && (long long)B * H > 4LL * sms))
     return kda::launch_tree_mma(p, bf16, sms, st);
   if ((long long)B * H * 4 <= sms)

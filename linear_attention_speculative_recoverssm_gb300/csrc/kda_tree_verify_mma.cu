@@ -37,9 +37,10 @@
 // warp; nodes to X and Y; pages; T and C; R and the outputs; and two warps that
 // issue the products, of X and of R.  Each kind is a chain of latencies (shared
 // memory, the shuffles of a norm, a product's hand-off); one phase after the
-// other by all warps, two CTAs an SM, was slower: 804 against 605 us (128
-// windows of 64 nodes and 64 heads), 111 against 87 (48 of up to 32 nodes, 32
-// heads), 115 against 101 (100 of 24, BF16 pages).
+// other by all warps, two CTAs an SM, was slower when it was tried: 804 against
+// 646 us (128 windows of 64 nodes and 64 heads), 111 against 97 (48 of up to 32
+// nodes, 32 heads), 115 against 113 (100 of 24, BF16 pages).  Later steps took the
+// three to 605, 87 and 101.
 //
 // Those three move 2053, 274 and 243 MB at 3.4, 3.2 and 2.4 TB/s (a copy's rate:
 // 6.7).  What bounds them is not HBM but instructions, their fetch, and the
@@ -47,8 +48,13 @@
 // 24, half of the issue slots, half of the shared memory's wavefronts, a quarter
 // of the tensor pipe's cycles.  The roles' code, all of it in use at once, is
 // more than an SM's instruction cache holds: loops are rolled up wherever their
-// state allows it (BF16 pages, 24 nodes: 115 -> 101 us, the cache's hits from 64
-// to 84% of the requests).
+// state allows it (BF16 pages, 24 nodes: the cache's hits from 64 to 84% of the
+// requests; with the nodes' tensor copies and R ahead of the outputs 113 -> 101 us).
+// At 64 registers a thread 8 to 40 bytes of it are kept in local memory.
+//
+// Small trees cost what their pages do: 1536 items with a replay take 73 to 76 us
+// for 4, 5, 6 and 7 nodes alike (floor 33).  A page has one place in shared memory
+// and one in tensor memory, and the next one waits for both.
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -160,7 +160,8 @@ class DeferredRecoverSSM:
         out BF16 [T, H, 128], raw_beta BF16 [T, H], parents int32 [T]; T =
         B*Q, or packed by query_start_loc [B + 1]), every node from the state
         behind its ancestors.  node_corr FP32 [T, H, 128] takes the nodes'
-        corrections, for ``accept_tree``; the records are not written.  A
+        corrections, for ``accept_tree``; the records are not written.  No path
+        is longer than what the records and convolution windows hold.  A
         request that is reported (a bad tree or window) keeps its pending
         replay, ``accept_tree`` included."""
         replay = {} if self.flushed else dict(pending=self.pending, corr=self.corr,
