@@ -111,8 +111,8 @@ class DeferredRecoverSSM:
         if resumed is not None:
             p = self._plan
             kda_flush_plan(self.state_slots, resumed, self.pending, p["commit_lens"],
-                           p["final_slots"], p["boundary_slots"], p["boundary_lens"], Q=self.Q,
-                           **common)
+                           p["final_slots"], p["boundary_slots"], p["boundary_lens"],
+                           Q=self.corr.shape[2], **common)
             self._commit(p["commit_lens"], p["final_slots"])
         kda_prefill(q, k, v, raw_g, raw_beta, self.A_log, self.dt_bias, self.state_pool, sources,
                     self.state_slots, query_start_loc, out, Q=Q, lower_bound=self.lower_bound,
@@ -204,10 +204,11 @@ class DeferredRecoverSSM:
 
     def flush(self):
         """Fold every pending replay into its checkpoint, in place."""
+        # (a tree's path may fill a record row, beyond a chain's window)
         p = self._plan
         kda_flush_plan(self.state_slots, self.record_rows, self.pending, p["commit_lens"],
                        p["final_slots"], p["boundary_slots"], p["boundary_lens"],
-                       Q=self.Q, null_slot=self.null_slot, status=self.status,
+                       Q=self.corr.shape[2], null_slot=self.null_slot, status=self.status,
                        stream=self.stream)
         self._commit(p["commit_lens"], p["final_slots"], p["boundary_slots"],
                      p["boundary_lens"])

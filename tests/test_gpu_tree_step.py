@@ -369,3 +369,28 @@ def test_accept_tree_beside_the_librarys_verify():
     got = tt.to_numpy(arms[1]["pending"])
     assert (got[case["record_rows"]] == np.where(case["state_slots"] > 0, taken,
                                                  case["pending"][case["record_rows"]])).all()
+
+
+@pytest.mark.parametrize("by", ["flush", "prefill"])
+def test_paths_longer_than_the_chains_windows(by):
+    """Chains of three drafts beside records of eight: all that a tree's path left
+    pending is folded in, as where chains have eight."""
+    import torch
+    arms = [Arm(8, 10), Arm(8, 10)]
+    arms[1].loop.Q = 3
+    deep = [tt.chain(8), tt.chain(8), tt.star(4), tt.chain(6)]
+    left = [a.step(5, deep) for a in arms]
+    same(*left, LEFT + ("count",))
+    assert left[0]["count"].tolist() == [8, 8, 2, 6]
+    for a in arms:
+        if by == "flush":
+            a.loop.flush()
+        else:
+            rng = np.random.default_rng(8)
+            bits = lambda *s: tt.to_torch(synth.to_bf16_bits(rng.standard_normal(s).astype(np.float32)), "cuda")
+            lens = np.array([5, 0, 9, 2])
+            T, qsl = int(lens.sum()), np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+            a.loop.prefill(bits(T, H, 128), bits(T, H, 128), bits(T, H, 128), bits(T, H, 128), bits(T, H),
+                           tt.to_torch(qsl, "cuda"), bits(T, H, 128), Q=9, sources=a.d["slots"])
+        assert int(a.d["status"].item()) == 0
+    same(arms[0].d, arms[1].d, ("state", "pending"))
