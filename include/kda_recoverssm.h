@@ -713,7 +713,7 @@ int kda_tree_conv(const kda_bf16 *x, const kda_bf16 *conv_weight, const kda_bf16
  *   What is held in fewer bits: windows of more than four nodes may form the
  *   products of the state and of pairs of nodes from operands in three BF16
  *   parts (24 bits; a gate path whose decays multiply to less than 2^-110 or
- *   so loses its last part); states, sums, norms, gates and decays are FP32.
+ *   so, or to more than 2^110, loses its last part); states, sums, norms, gates and decays are FP32.
  *   A NaN or an infinity in a node, its gates or a state row reaches that
  *   node's descendants (that row) and no other node.
  *   q, k, v, raw_g, out [n_tokens, H, 128], raw_beta [n_tokens, H] BF16;
